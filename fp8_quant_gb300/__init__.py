@@ -13,6 +13,9 @@ the same names:
   :func:`kv_gather`, :func:`kv_gather_fp8` (the inverse), :func:`kv_inv_scale`,
   :func:`kv_absmax_inv` (scale preparation), :func:`kv_store_fp8_dynamic_tensor`
   (per-tensor scales formed from the batch and the write, in one call).
+* :func:`kv_store_rope` (append with the position rotation applied on the way;
+  16-bit, e4m3fn or 4-bit e2m1 caches), :func:`kv_gather_fp4` (the 4-bit
+  cache's read-back), :func:`kv_attend` (attention over those caches).
 * :func:`kv_error_poll`, :func:`kv_error_reset`, :func:`kv_status_str`.
 
 The tensor-level functions take torch tensors (device memory and streams come
@@ -25,6 +28,7 @@ from __future__ import annotations
 
 import ctypes
 import enum
+import math
 import os
 import threading
 from typing import Optional, Sequence
@@ -37,6 +41,7 @@ __all__ = [
     "kv_gather", "kv_gather_fp8", "kv_inv_scale", "kv_absmax_inv", "kv_error_poll",
     "kv_error_reset", "kv_status_str", "error_record", "load_library", "raw", "STRIDE_FIELDS",
     "fused_fp8_set_kv_buffer", "kv_store_fp8_dynamic_tensor", "DYNAMIC_TENSOR_WORK_BYTES",
+    "kv_store_rope", "kv_gather_fp4", "kv_attend", "ATTEND_WORK_BYTES",
 ]
 
 
@@ -60,6 +65,28 @@ STRIDE_FIELDS = ("k_token", "k_head", "k_dim", "v_token", "v_head", "v_dim",
 
 class _Strides(ctypes.Structure):
     _fields_ = [(f, ctypes.c_int64) for f in STRIDE_FIELDS]
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [("cos_sin", ctypes.c_void_p), ("cos_sin_stride", ctypes.c_int64),
+                ("max_position", ctypes.c_int64), ("positions", ctypes.c_void_p),
+                ("position_dtype", ctypes.c_int32), ("position_stride", ctypes.c_int64),
+                ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("q", ctypes.c_void_p), ("q_out", ctypes.c_void_p),
+                ("num_q_heads", ctypes.c_int32), ("q_token", ctypes.c_int64),
+                ("q_head", ctypes.c_int64), ("qo_token", ctypes.c_int64),
+                ("qo_head", ctypes.c_int64)]
+
+
+class _BlockScales(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p)] + [
+        (f, ctypes.c_int64) for f in ("k_page", "k_slot", "k_head", "v_page", "v_slot", "v_head")]
+
+
+class _AttendStrides(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int64) for f in (
+        "q_token", "q_head", "o_token", "o_head", "kc_page", "kc_slot", "kc_head",
+        "vc_page", "vc_slot", "vc_head")]
 
 
 _lock = threading.Lock()
@@ -115,6 +142,20 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
                                                     ctypes.POINTER(_Strides), I64, I64, I64, I64,
                                                     I32, P, P, P, P, P]
         lib.kv_store_fp8_dynamic_tensor.restype = I32
+        lib.kv_store_rope.argtypes = [P, P, P, P, P, I32, I64, I64, I32, I32, I32,
+                                      ctypes.POINTER(_Strides), I64, I64, I64, I64,
+                                      ctypes.POINTER(_Rope), I32, P, P,
+                                      ctypes.POINTER(_BlockScales), P, P]
+        lib.kv_store_rope.restype = I32
+        lib.kv_gather_fp4.argtypes = [P, P, ctypes.POINTER(_BlockScales), P, P, P, I32, I64, I64,
+                                      I32, I32, I32, ctypes.POINTER(_Strides), I64, I64, I64, I64,
+                                      P, P, P, P]
+        lib.kv_gather_fp4.restype = I32
+        lib.kv_attend.argtypes = [P, P, P, P, P, P, I64, I64, P, P, I32, I64, I32, I32, I32, I32,
+                                  ctypes.POINTER(_AttendStrides), I64, I64, I32, P, P,
+                                  ctypes.POINTER(_BlockScales), ctypes.c_float, I64, I64, P, I64,
+                                  P, P]
+        lib.kv_attend.restype = I32
         lib.kv_store_noalloc.argtypes = [P, P, P, P, P, I32, I64, I64, I32, I32, I32,
                                          ctypes.POINTER(_Strides), I64, I32,
                                          ctypes.POINTER(I64), ctypes.POINTER(I64), P]
@@ -267,6 +308,44 @@ class raw:
         return load_library().kv_absmax_inv(k, v, src_dtype, num_tokens, num_heads, head_dim,
                                             ctypes.byref(st), float(fp8_max), amax, inv, work,
                                             stream)
+
+    @staticmethod
+    def kv_store_rope(k, v, k_cache, v_cache, indices, index_dtype, index_stride, num_tokens,
+                      num_heads, head_dim, src_dtype, strides: Sequence[int], page_size,
+                      kc_page_stride, vc_page_stride, size_limit, rope: Sequence, fmt,
+                      inv_k_scale, inv_v_scale, scales: Optional[Sequence], d_err, stream) -> int:
+        """``rope`` and ``scales``: the fields of kv_rope / kv_block_scales in order."""
+        return load_library().kv_store_rope(
+            k, v, k_cache, v_cache, indices, index_dtype, index_stride, num_tokens, num_heads,
+            head_dim, src_dtype, ctypes.byref(_Strides(*strides)), page_size, kc_page_stride,
+            vc_page_stride, size_limit, None if rope is None else ctypes.byref(_Rope(*rope)), fmt,
+            inv_k_scale, inv_v_scale,
+            None if scales is None else ctypes.byref(_BlockScales(*scales)), d_err, stream)
+
+    @staticmethod
+    def kv_gather_fp4(k_cache, v_cache, scales: Optional[Sequence], k_out, v_out, indices,
+                      index_dtype, index_stride, num_tokens, num_heads, head_dim, out_dtype,
+                      strides: Sequence[int], page_size, kc_page_stride, vc_page_stride,
+                      size_limit, k_scale, v_scale, d_err, stream) -> int:
+        return load_library().kv_gather_fp4(
+            k_cache, v_cache, None if scales is None else ctypes.byref(_BlockScales(*scales)),
+            k_out, v_out, indices, index_dtype, index_stride, num_tokens, num_heads, head_dim,
+            out_dtype, ctypes.byref(_Strides(*strides)), page_size, kc_page_stride,
+            vc_page_stride, size_limit, k_scale, v_scale, d_err, stream)
+
+    @staticmethod
+    def kv_attend(q, out, lse, k_cache, v_cache, page_table, table_stride, table_width, seq_lens,
+                  q_start, num_seqs, num_q_tokens, num_q_heads, num_heads, head_dim, dtype,
+                  strides: Optional[Sequence[int]], page_size, num_pages, fmt, k_scale, v_scale,
+                  scales: Optional[Sequence], sm_scale, window, sinks, work, work_bytes, d_err,
+                  stream) -> int:
+        return load_library().kv_attend(
+            q, out, lse, k_cache, v_cache, page_table, table_stride, table_width, seq_lens,
+            q_start, num_seqs, num_q_tokens, num_q_heads, num_heads, head_dim, dtype,
+            None if strides is None else ctypes.byref(_AttendStrides(*strides)), page_size,
+            num_pages, fmt, k_scale, v_scale,
+            None if scales is None else ctypes.byref(_BlockScales(*scales)), sm_scale, window,
+            sinks, work, work_bytes, d_err, stream)
 
     @staticmethod
     def kv_store_noalloc(k, v, k_cache, v_cache, indices, index_dtype, index_stride,
@@ -701,4 +780,263 @@ def kv_absmax_inv(k, v, *, fp8_max: float = 448.0, num_heads=None, head_dim=None
                              None if work is None else work.data_ptr(),
                              _stream_handle(stream, k.device)),
            "kv_absmax_inv")
+    return out
+
+
+# ---------------------------------------------------------------------------
+# The rotated append, the 4-bit cache and attention
+# ---------------------------------------------------------------------------
+
+CACHE_FORMATS = {None: 0, "e4m3fn": 1, "e2m1": 2}
+ATTEND_WORK_BYTES = 64 << 20  # KV_ATTEND_WORK_BYTES of the C header
+
+
+def _is_bf16(x) -> int:
+    import torch
+    if x.dtype == torch.bfloat16:
+        return 1
+    if x.dtype == torch.float16:
+        return 0
+    raise TypeError("rows must be bf16 or fp16")
+
+
+def _cache_strides(cache, page_size, width, elem_bytes, what):
+    """(page, slot, head, dim) byte strides and the slots and heads of a
+    [slots, H, width] or [pages, page_size, H, width] cache."""
+    if cache.element_size() != elem_bytes:
+        raise TypeError(f"{what} must have {elem_bytes}-byte elements")
+    st = cache.stride()
+    if cache.dim() == 4:
+        pages, ps, H, w = cache.shape
+        if ps != page_size:
+            raise ValueError(f"page_size does not match {what}")
+        slots = pages * ps
+        page, slot, head, dim = st
+    elif cache.dim() == 3:
+        slots, H, w = cache.shape
+        slot, head, dim = st
+        page = slot * page_size
+    else:
+        raise ValueError(f"{what} must be [slots, H, {width}] or [pages, page_size, H, {width}]")
+    if w != width:
+        raise ValueError(f"{what}: rows of {w} elements, {width} expected")
+    return page * elem_bytes, slot * elem_bytes, head * elem_bytes, dim * elem_bytes, slots, H
+
+
+def _cache_pair(k_cache, v_cache, page_size, D, fmt, elem_bytes):
+    width = D // 2 if fmt == "e2m1" else D
+    eb = elem_bytes if fmt is None else 1
+    kc = _cache_strides(k_cache, page_size, width, eb, "k_cache")
+    vc = _cache_strides(v_cache, page_size, width, eb, "v_cache")
+    if kc[4:] != vc[4:]:
+        raise ValueError("k_cache and v_cache differ in slots or heads")
+    return kc, vc
+
+
+def _block_scales(k_scales, v_scales, page_size, D, slots, H):
+    if k_scales is None or v_scales is None:
+        raise ValueError("an e2m1 cache needs k_scales and v_scales")
+    out = []
+    for x, what in ((k_scales, "k_scales"), (v_scales, "v_scales")):
+        page, slot, head, dim, n, h = _cache_strides(x, page_size, D // 16, 1, what)
+        if dim != 1 or (n, h) != (slots, H):
+            raise ValueError(f"{what} must be [slots, H, D / 16] or [pages, page_size, H, D / 16] "
+                             "bytes with contiguous rows, like the cache")
+        out += [page, slot, head]
+    return [k_scales.data_ptr(), v_scales.data_ptr(), *out]
+
+
+def _scalar_ptr(x, what):
+    import torch
+    if x is None:
+        return None
+    if x.dtype != torch.float32 or x.numel() != 1 or x.device.type != "cuda":
+        raise TypeError(f"{what} must be a 1-element fp32 device tensor")
+    return x.data_ptr()
+
+
+def _check_format(fmt):
+    if fmt not in CACHE_FORMATS:
+        raise ValueError(f"fmt must be one of {list(CACHE_FORMATS)}")
+    return CACHE_FORMATS[fmt]
+
+
+def kv_store_rope(k, v, k_cache, v_cache, indices, positions, cos_sin, *, q=None, q_out=None,
+                  page_size: int = 1, interleaved: bool = False, fmt: Optional[str] = None,
+                  inv_k_scale=None, inv_v_scale=None, k_scales=None, v_scales=None,
+                  size_limit: Optional[int] = None, err=None, stream=None):
+    """Append K/V rows to a cache with the position rotation applied on the way.
+
+    ``k``/``v``: bf16 or fp16 [T, H, D]; ``q`` (optional): [T, HQ, D], rotated into ``q_out``
+    (a new tensor if None; may be ``q``), which is returned. Token t goes to slot ``indices[t]``
+    at position ``positions[t]`` (1-D int32 / int64). ``cos_sin``: fp32 [max_position, R], a
+    row's R/2 cosines and then its sines; the first R dims of Q and K are rotated, in pairs
+    (i, i + R/2), or (2i, 2i + 1) when ``interleaved``.
+
+    ``fmt``: None (caches of the rows' dtype), "e4m3fn" (1-byte caches, [..., D]) or "e2m1"
+    (uint8 caches [..., D / 2] with block scales ``k_scales`` / ``v_scales`` [..., D / 16]);
+    caches and scales are [slots, H, ...] or [pages, page_size, H, ...]. ``inv_k_scale`` /
+    ``inv_v_scale``: 1-element fp32 device tensors, the inverse tensor scales (None: 1).
+    Tokens whose slot or position is out of range are skipped and counted in ``err``.
+    """
+    import torch
+    if k.dim() != 3 or k.shape != v.shape or k.dtype != v.dtype:
+        raise ValueError("k and v must be [T, H, D] of one shape and dtype")
+    T, H, D = k.shape
+    bf16 = _is_bf16(k)
+    f = _check_format(fmt)
+    kc, vc = _cache_pair(k_cache, v_cache, page_size, D, fmt, 2)
+    if fmt is None and (k_cache.dtype != k.dtype or v_cache.dtype != k.dtype):
+        raise TypeError("without a format the caches have the rows' dtype")
+    slots = kc[4]
+    if kc[5] != H:
+        raise ValueError(f"caches of {kc[5]} heads, rows of {H}")
+    if indices.dim() != 1 or positions.dim() != 1 or positions.shape[0] != T or indices.shape[0] != T:
+        raise ValueError("indices and positions must hold one entry per row")
+    idt, istride = _index_args(indices)
+    pdt, pstride = _index_args(positions)
+    if cos_sin.dim() != 2 or cos_sin.dtype != torch.float32 or cos_sin.stride(1) != 1:
+        raise TypeError("cos_sin must be fp32 [max_position, R] with contiguous rows")
+    qa = (None, None, 0, 0, 0, 0, 0)
+    if q is not None:
+        if q.dim() != 3 or q.shape[0] != T or q.shape[2] != D or q.dtype != k.dtype or q.stride(2) != 1:
+            raise ValueError("q must be [T, HQ, D] of k's dtype with contiguous dims")
+        if q_out is None:
+            with _on_stream(stream, q.device):
+                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if q_out.shape != q.shape or q_out.dtype != q.dtype or q_out.stride(2) != 1:
+            raise ValueError("q_out must be like q, with contiguous dims")
+        qa = (q.data_ptr(), q_out.data_ptr(), q.shape[1], q.stride(0) * 2, q.stride(1) * 2,
+              q_out.stride(0) * 2, q_out.stride(1) * 2)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if fmt is None and not (inv_k_scale is None and inv_v_scale is None):
+        raise ValueError("caches of the rows' dtype take no scales")
+    sc = _block_scales(k_scales, v_scales, page_size, D, slots, H) if fmt == "e2m1" else None
+    rec = err if err is not None else _default_record(k_cache.device)
+    rope = (cos_sin.data_ptr(), cos_sin.stride(0) if cos_sin.shape[0] > 1 else cos_sin.shape[1],
+            cos_sin.shape[0], positions.data_ptr(), pdt, pstride, cos_sin.shape[1],
+            int(interleaved), *qa)
+    _check(raw.kv_store_rope(
+        k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), indices.data_ptr(),
+        idt, istride, T, H, D, bf16,
+        (k.stride(0) * 2, k.stride(1) * 2, k.stride(2) * 2, v.stride(0) * 2, v.stride(1) * 2,
+         v.stride(2) * 2, kc[1], kc[2], kc[3], vc[1], vc[2], vc[3]),
+        page_size, kc[0], vc[0], slots if size_limit is None else size_limit, rope, f,
+        _scalar_ptr(inv_k_scale, "inv_k_scale"), _scalar_ptr(inv_v_scale, "inv_v_scale"), sc,
+        rec.data_ptr(), _stream_handle(stream, k_cache.device)), "kv_store_rope")
+    return q_out
+
+
+def kv_gather_fp4(k_cache, v_cache, k_scales, v_scales, k_out, v_out, indices, *,
+                  page_size: int = 1, k_scale=None, v_scale=None, size_limit: Optional[int] = None,
+                  err=None, stream=None) -> None:
+    """Dequantising gather of an e2m1 cache (see :func:`kv_store_rope`) into bf16 / fp16 rows:
+    row t of ``k_out`` / ``v_out`` [T, H, D] takes the cache row of ``indices[t]``.
+    ``k_scale`` / ``v_scale``: the forward tensor scales (None: 1)."""
+    if k_out.dim() != 3 or k_out.shape != v_out.shape or k_out.dtype != v_out.dtype:
+        raise ValueError("k_out and v_out must be [T, H, D] of one shape and dtype")
+    T, H, D = k_out.shape
+    kc, vc = _cache_pair(k_cache, v_cache, page_size, D, "e2m1", 1)
+    if kc[5] != H:
+        raise ValueError(f"caches of {kc[5]} heads, rows of {H}")
+    sc = _block_scales(k_scales, v_scales, page_size, D, kc[4], H)
+    idt, istride = _index_args(indices)
+    if indices.shape[0] > T:
+        raise ValueError("fewer output rows than indices")
+    rec = err if err is not None else _default_record(k_cache.device)
+    _check(raw.kv_gather_fp4(
+        k_cache.data_ptr(), v_cache.data_ptr(), sc, k_out.data_ptr(), v_out.data_ptr(),
+        indices.data_ptr(), idt, istride, indices.shape[0], H, D, _is_bf16(k_out),
+        (k_out.stride(0) * 2, k_out.stride(1) * 2, k_out.stride(2) * 2, v_out.stride(0) * 2,
+         v_out.stride(1) * 2, v_out.stride(2) * 2, kc[1], kc[2], kc[3], vc[1], vc[2], vc[3]),
+        page_size, kc[0], vc[0], kc[4] if size_limit is None else size_limit,
+        _scalar_ptr(k_scale, "k_scale"), _scalar_ptr(v_scale, "v_scale"), rec.data_ptr(),
+        _stream_handle(stream, k_cache.device)), "kv_gather_fp4")
+
+
+def _on_stream(stream, device):
+    """The context in which torch allocates for `stream` (None: the current one)."""
+    import contextlib
+    import torch
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+        stream = torch.cuda.ExternalStream(handle, device=device)
+    return torch.cuda.stream(stream)
+
+
+def kv_attend(q, k_cache, v_cache, page_table, seq_lens, *, q_start=None, page_size=None,
+              window: int = 0, sinks: int = 0, sm_scale: Optional[float] = None,
+              fmt: Optional[str] = None, k_scale=None, v_scale=None, k_scales=None, v_scales=None,
+              out=None, lse=None, work=None, err=None, stream=None):
+    """Causal attention of ragged queries over a paged cache; returns ``out``.
+
+    ``q``: bf16 or fp16 [tokens, HQ, D]. Caches as in :func:`kv_store_rope`
+    ([pages, page_size, H, ...], or [slots, H, ...] with ``page_size`` given), HQ a multiple of
+    H. ``page_table``: int32 [B, width] page ids; ``seq_lens``: int32 [B], the cached tokens of
+    each sequence, its queries' own among them; ``q_start``: int32 [B + 1] offsets of each
+    sequence's query rows, its newest tokens (None: one row per sequence).
+
+    A query at position p sees key j <= p, with ``window`` > 0 only j > p - window or
+    j < ``sinks``. ``sm_scale``: of the scores (1 / sqrt(D) if None). ``fmt``, ``k_scales``,
+    ``v_scales``: as in :func:`kv_store_rope`; ``k_scale`` / ``v_scale``: forward tensor scales
+    (1-element fp32 device tensors, None: 1). ``lse``: an fp32 [tokens, HQ] tensor for the
+    logarithms of the rows' sums, or None. ``work``: a device tensor that lets long sequences be
+    split over the GPU (ATTEND_WORK_BYTES is always enough; contents do not matter; calls that
+    share one must not overlap; a new one per call if None). Sequences with a bad length or page
+    id are counted in ``err``.
+    """
+    import torch
+    if q.dim() != 3 or q.stride(2) != 1:
+        raise ValueError("q must be [tokens, HQ, D] with contiguous dims")
+    T, HQ, D = q.shape
+    bf16 = _is_bf16(q)
+    f = _check_format(fmt)
+    if page_size is None:
+        if k_cache.dim() != 4:
+            raise ValueError("page_size is needed with [slots, H, ...] caches")
+        page_size = k_cache.shape[1]
+    kc, vc = _cache_pair(k_cache, v_cache, page_size, D, fmt, 2)
+    if fmt is None and (k_cache.dtype != q.dtype or v_cache.dtype != q.dtype):
+        raise TypeError("without a format the caches have q's dtype")
+    if kc[3] != vc[3] or kc[3] != (2 if fmt is None else 1):
+        raise ValueError("cache dims must be contiguous")
+    slots, H = kc[4:]
+    if HQ % H:
+        raise ValueError(f"{HQ} query heads over {H} KV heads")
+    sc = _block_scales(k_scales, v_scales, page_size, D, slots, H) if fmt == "e2m1" else None
+    if page_table.dim() != 2 or page_table.dtype != torch.int32 or page_table.stride(1) != 1:
+        raise TypeError("page_table must be int32 [B, width] with contiguous rows")
+    B, width = page_table.shape
+    if seq_lens.dtype != torch.int32 or seq_lens.shape != (B,) or (B > 1 and seq_lens.stride(0) != 1):
+        raise TypeError("seq_lens must be a contiguous int32 [B]")
+    if q_start is not None:
+        if q_start.dtype != torch.int32 or q_start.shape != (B + 1,) or q_start.stride(0) != 1:
+            raise TypeError("q_start must be a contiguous int32 [B + 1]")
+    elif T != B:
+        raise ValueError("without q_start there is one query row per sequence")
+    if out is None:
+        with _on_stream(stream, q.device):
+            out = torch.empty((T, HQ, D), dtype=q.dtype, device=q.device)
+    elif out.shape != q.shape or out.dtype != q.dtype or out.stride(2) != 1:
+        raise ValueError("out must be like q, with contiguous dims")
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (T, HQ) or not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous fp32 [tokens, HQ]")
+    if work is None:
+        with _on_stream(stream, q.device):
+            work = torch.empty(ATTEND_WORK_BYTES, dtype=torch.uint8, device=q.device)
+    rec = err if err is not None else _default_record(q.device)
+    _check(raw.kv_attend(
+        q.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
+        k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(),
+        page_table.stride(0) if B > 1 else width, width, seq_lens.data_ptr(),
+        None if q_start is None else q_start.data_ptr(), B, T, HQ, H, D, bf16,
+        (q.stride(0) * 2, q.stride(1) * 2, out.stride(0) * 2, out.stride(1) * 2,
+         *kc[:3], *vc[:3]),
+        page_size, slots // page_size, f, _scalar_ptr(k_scale, "k_scale"),
+        _scalar_ptr(v_scale, "v_scale"), sc, 1.0 / math.sqrt(D) if sm_scale is None else sm_scale,
+        window, sinks, work.data_ptr(), work.numel() * work.element_size(), rec.data_ptr(),
+        _stream_handle(stream, q.device)), "kv_attend")
     return out

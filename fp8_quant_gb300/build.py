@@ -16,7 +16,8 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
-SOURCES = [os.path.join(CSRC, f) for f in ("kvstore.cu", "kv_gather.cu", "kv_scale.cu", "kv_fp8_ex.cu")]
+SOURCES = [os.path.join(CSRC, f) for f in ("kvstore.cu", "kv_gather.cu", "kv_scale.cu", "kv_fp8_ex.cu",
+                                           "kv_rope.cu", "kv_attend.cu")]
 SRC = SOURCES[0]
 HEADER = os.path.join(ROOT, "include", "kvstore.h")
 LIBDIR = os.path.join(HERE, "lib")

@@ -1,0 +1,151 @@
+// Attention over the paged cache (kv_attend): argument checks, the choice of
+// the kernel, and the general kernel.
+//
+//  * kv_attend_rows   any head dim, alignment and stride: one warp per query
+//                     row and head, one key after the other.
+#include <cmath>
+#include <climits>
+
+#include "kv_attend.cuh"
+#include "kv_host.h"
+
+namespace kvimpl {
+namespace {
+
+template <int FMT, int ND>
+__global__ void __launch_bounds__(kThreads) kv_attend_rows(const __grid_constant__ AttendParams p) {
+  grid_handover();
+  const uint64_t nwarps = static_cast<uint64_t>(gridDim.x) * warps_per_cta();
+  const uint64_t units = static_cast<uint64_t>(p.num_q) * static_cast<uint64_t>(p.q_heads);
+  for (uint64_t u = static_cast<uint64_t>(blockIdx.x) * warps_per_cta() + (threadIdx.x >> 5);
+       u < units; u += nwarps) {
+    const int32_t t = static_cast<int32_t>(u / static_cast<uint32_t>(p.q_heads));
+    const int32_t h = static_cast<int32_t>(u - static_cast<uint64_t>(t) * p.q_heads);
+    // the last sequence that begins at or before row t
+    int32_t b = t;
+    if (p.q_start) {
+      int32_t lo = 0, hi = p.num_seqs - 1;
+      while (lo < hi) {
+        const int32_t mid = (lo + hi + 1) >> 1;
+        if (__ldg(p.q_start + mid) <= t) lo = mid; else hi = mid - 1;
+      }
+      b = lo;
+    }
+    const AttendSeq s = attend_seq(p, b, h == 0 && (threadIdx.x & 31u) == 0);
+    if (t < s.q0 || t >= s.q0 + s.nq) continue;
+    attend_row<FMT, ND>(p, b, s.len - s.nq + (t - s.q0), t, h);
+  }
+}
+
+template <int FMT>
+kv_status launch_rows_any(const AttendParams& p, cudaStream_t stream) {
+  const uint64_t units = static_cast<uint64_t>(p.num_q) * static_cast<uint64_t>(p.q_heads);
+  return p.head_dim <= 256 ? launch(kv_attend_rows<FMT, 8>, units, p, stream, 0, 128)
+                           : launch(kv_attend_rows<FMT, 32>, units, p, stream, 0, 128);
+}
+
+FastDiv fast_div(uint32_t d) {
+  FastDiv f{d, 0u, 0u};
+  uint32_t log = 0;
+  while ((uint64_t{1} << log) < d) ++log;  // ceil(log2 d)
+  if ((d & (d - 1u)) == 0u) {
+    f.shift = log;
+    return f;
+  }
+  // ceil(2^(31 + log) / d) fits 32 bits, and its error is below 2^log / 2^31
+  // per unit of x, exact for x < 2^31
+  f.shift = log - 1;
+  f.mul = static_cast<uint32_t>(((uint64_t{1} << (31 + log)) + d - 1) / d);
+  return f;
+}
+
+}  // namespace
+}  // namespace kvimpl
+
+using namespace kvimpl;
+
+extern "C" kv_status kv_attend(const void* q, void* out, float* lse, const void* k_cache,
+                               const void* v_cache, const int32_t* page_table, int64_t table_stride,
+                               int64_t table_width, const int32_t* seq_lens, const int32_t* q_start,
+                               int32_t num_seqs, int64_t num_q_tokens, int32_t num_q_heads,
+                               int32_t num_heads, int32_t head_dim, kv_src_dtype dtype,
+                               const kv_attend_strides* s, int64_t page_size, int64_t num_pages,
+                               kv_cache_format format, const float* k_scale, const float* v_scale,
+                               const kv_block_scales* scales, float sm_scale, int64_t window,
+                               int64_t sinks, void* work, int64_t work_bytes, kv_error_record* d_err,
+                               kv_stream_t stream_) {
+  if (num_seqs < 0 || num_q_tokens < 0) return KV_ERR_INVALID_ARG;
+  if (format != KV_CACHE_SRC && format != KV_CACHE_E4M3FN && format != KV_CACHE_E2M1)
+    return KV_ERR_INVALID_ARG;
+  if (num_seqs == 0 || num_q_tokens == 0) return KV_OK;
+  if (!q || !out || !k_cache || !v_cache || !page_table || !seq_lens || !s || !d_err)
+    return KV_ERR_INVALID_ARG;
+  if (dtype != KV_SRC_F16 && dtype != KV_SRC_BF16) return KV_ERR_INVALID_ARG;
+  if (num_q_heads < 1 || num_heads < 1 || head_dim < 1 || num_q_heads % num_heads != 0 ||
+      page_size < 1 || num_pages < 1 || table_width < 1 || table_stride < table_width ||
+      window < 0 || sinks < 0 || work_bytes < 0 || !std::isfinite(sm_scale))
+    return KV_ERR_INVALID_ARG;
+  if (!q_start && num_q_tokens != num_seqs) return KV_ERR_INVALID_ARG;
+  if (((u64(page_table) | u64(seq_lens) | u64(q_start) | u64(lse) | u64(k_scale) | u64(v_scale)) & 3u) != 0 ||
+      (u64(d_err) & 7u) != 0 || (work && (u64(work) & 255u) != 0))
+    return KV_ERR_INVALID_ARG;
+  if (format == KV_CACHE_E2M1 && (!scales || !scales->k || !scales->v)) return KV_ERR_INVALID_ARG;
+  const uint64_t q_bits = u64(q) | u64(out) | u64(s->q_token) | u64(s->q_head) | u64(s->o_token) | u64(s->o_head);
+  const uint64_t c_bits = u64(k_cache) | u64(v_cache) | u64(s->kc_page) | u64(s->kc_slot) | u64(s->kc_head) |
+                          u64(s->vc_page) | u64(s->vc_slot) | u64(s->vc_head);
+  if ((q_bits & 1u) != 0 || (format == KV_CACHE_SRC && (c_bits & 1u) != 0)) return KV_ERR_UNSUPPORTED;
+  if (head_dim > 1024 || (format == KV_CACHE_E2M1 && head_dim % kFp4Block != 0)) return KV_ERR_UNSUPPORTED;
+  if (num_q_tokens >= INT_MAX || page_size >= INT_MAX || num_pages >= INT_MAX) return KV_ERR_UNSUPPORTED;
+  {
+    const void* in[6] = {q, out, page_table, seq_lens, k_cache, v_cache};
+    bool on_device = true;
+    const kv_status cs = classify_inputs(in, 6, &on_device);
+    if (cs != KV_OK) return cs;
+  }
+
+  AttendParams p = {};
+  p.q = static_cast<const uint8_t*>(q);
+  p.k = static_cast<const uint8_t*>(k_cache);
+  p.v = static_cast<const uint8_t*>(v_cache);
+  p.out = static_cast<uint8_t*>(out);
+  p.lse = lse;
+  p.table = page_table;
+  p.seq_lens = seq_lens;
+  p.q_start = q_start;
+  p.table_stride = table_stride;
+  p.q_token = s->q_token; p.q_head = s->q_head;
+  p.o_token = s->o_token; p.o_head = s->o_head;
+  p.k_page = s->kc_page; p.k_slot = s->kc_slot; p.k_head = s->kc_head;
+  p.v_page = s->vc_page; p.v_slot = s->vc_slot; p.v_head = s->vc_head;
+  if (format == KV_CACHE_E2M1) {
+    p.k_sc = static_cast<const uint8_t*>(scales->k);
+    p.v_sc = static_cast<const uint8_t*>(scales->v);
+    p.ks_page = scales->k_page; p.ks_slot = scales->k_slot; p.ks_head = scales->k_head;
+    p.vs_page = scales->v_page; p.vs_slot = scales->v_slot; p.vs_head = scales->v_head;
+  }
+  if (format != KV_CACHE_SRC) {
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+  }
+  p.page = fast_div(static_cast<uint32_t>(page_size));
+  p.group = fast_div(static_cast<uint32_t>(num_q_heads / num_heads));
+  p.num_pages = static_cast<int32_t>(num_pages);
+  p.num_seqs = num_seqs;
+  p.num_q = static_cast<int32_t>(num_q_tokens);
+  p.q_heads = num_q_heads;
+  p.kv_heads = num_heads;
+  p.head_dim = head_dim;
+  p.max_len = table_width > INT_MAX / page_size ? INT_MAX : static_cast<int32_t>(table_width * page_size);
+  p.window = window;
+  p.sinks = sinks;
+  p.scale_log2 = sm_scale * 1.4426950408889634f;
+  p.bf16 = dtype == KV_SRC_BF16;
+  p.err = d_err;
+  (void)work;
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  switch (format) {
+    case KV_CACHE_SRC: return launch_rows_any<KV_CACHE_SRC>(p, stream);
+    case KV_CACHE_E4M3FN: return launch_rows_any<KV_CACHE_E4M3FN>(p, stream);
+    default: return launch_rows_any<KV_CACHE_E2M1>(p, stream);
+  }
+}

@@ -400,6 +400,187 @@ kv_status kv_store_fp8_dynamic_tensor(const void *k, const void *v, void *k_cach
                                       kv_fp8_format format, float *k_scale, float *v_scale,
                                       uint64_t *work, kv_error_record *d_err, kv_stream_t stream);
 
+/* Formats of a KV cache that is written with the position rotation and read by
+ * attention. */
+typedef enum kv_cache_format {
+    KV_CACHE_SRC = 0,      /* elements of the source type (2 bytes) */
+    KV_CACHE_E4M3FN = 1,   /* one e4m3fn byte per element, an fp32 scale per tensor */
+    KV_CACHE_E2M1 = 2      /* 4 bits per element, an e4m3fn scale per 16 dims, an fp32 scale per tensor */
+} kv_cache_format;
+
+/* The block scales of an e2m1 cache (byte strides).  A head row of head_dim
+ * elements is head_dim / 2 bytes of codes, dim 2j in the low and dim 2j + 1 in
+ * the high half of byte j, and head_dim / 16 e4m3fn bytes; the scale of dims
+ * 16j .. 16j + 15 of (slot s, head h) is the byte at
+ * k + (s / page_size) * k_page + (s % page_size) * k_slot + h * k_head + j
+ * (likewise v).  An element's value is code * block scale * tensor scale. */
+#define KV_FP4_BLOCK 16
+typedef struct kv_block_scales {
+    void *k, *v;
+    int64_t k_page, k_slot, k_head;
+    int64_t v_page, v_slot, v_head;
+} kv_block_scales;
+
+/* The position rotation of kv_store_rope (host struct, read during the call
+ * only). */
+typedef struct kv_rope {
+    const float *cos_sin;       /* device: row p holds cos(a_0 .. a_{R/2-1}), then the sines; R = rotary_dim
+                                 * (NULL when R is 0) */
+    int64_t cos_sin_stride;     /* floats between rows, >= rotary_dim */
+    int64_t max_position;       /* rows of the table; positions must satisfy 0 <= p < max_position */
+    const void *positions;      /* token t's position is positions[t * position_stride] */
+    kv_index_dtype position_dtype;
+    int64_t position_stride;    /* in elements, >= 1 */
+    int32_t rotary_dim;         /* R: even, 0 <= R <= head_dim; dims from R on are not rotated */
+    int32_t interleaved;        /* 0: pairs (i, i + R/2); else pairs (2i, 2i + 1) */
+    const void *q;              /* optional query rows [num_tokens, num_q_heads, head_dim], NULL: none */
+    void *q_out;                /* their rotated form (may be q itself, with q's strides) */
+    int32_t num_q_heads;
+    int64_t q_token, q_head, qo_token, qo_head;  /* byte strides; dims contiguous */
+} kv_rope;
+
+/*
+ * kv_store_rope -- append K and V rows to a paged cache with the position
+ * rotation applied on the way, and rotate the query rows of the same tokens.
+ * The pages write rows that something else has rotated; this call saves that
+ * pass over K and Q.
+ *
+ * For token t with position p, each pair (a, b) of the first rotary_dim dims
+ * of every K and Q head becomes
+ *     a' = fl(fl(a c) - fl(b s)),   b' = fl(fl(b c) + fl(a s)),
+ * c = cos_sin[p][i], s = cos_sin[p][R/2 + i], in fp32 (each operation rounded
+ * to nearest); V and the dims from R on are taken as they are.  Then
+ *   KV_CACHE_SRC     the value is rounded once to the source type (V and
+ *                    unrotated dims keep their bytes; the sign or payload of a
+ *                    NaN that is rotated is not kept);
+ *   KV_CACHE_E4M3FN  the code of fl(x * inv) is written as in kv_store_fp8;
+ *   KV_CACHE_E2M1    y = fl(x * inv); per block of 16 dims
+ *                    S = e4m3fn(fl(max|y| * fl(1/6))) (NaN ignored, saturating
+ *                    at 448), r = fl(1 / S) (0 when S is 0), and the code of
+ *                    fl(y * r): nearest, ties to the even code, saturating at
+ *                    +-6; every NaN is written as +6.
+ * inv is *inv_k_scale / *inv_v_scale (device scalars), or 1 where the pointer
+ * is NULL; KV_CACHE_SRC takes none.  Q is rounded once to the source type.
+ *
+ * Arguments as kv_store_fp8, plus:
+ *   rope     see above.  With q set, q_out is written for every token whose
+ *            position is in range, also where its slot is not.
+ *   format   of the caches; KV_CACHE_E2M1 needs `scales` and head_dim a
+ *            multiple of 16.
+ * A token whose position is out of range writes nothing and is counted in the
+ * error record once, like one whose slot is.
+ * K, V, Q, q_out, the slot ids and the positions may be page-locked host
+ * memory; the caches, scales and the table are device memory.
+ * q_out may be q; it must overlap nothing else.  Dims of Q must be contiguous;
+ * K, V and the caches may have any dim strides, but an e2m1 cache and its
+ * scales have contiguous dims (else KV_ERR_UNSUPPORTED).
+ */
+kv_status kv_store_rope(const void *k, const void *v, void *k_cache, void *v_cache,
+                        const void *indices, kv_index_dtype index_dtype, int64_t index_stride,
+                        int64_t num_tokens, int32_t num_heads, int32_t head_dim,
+                        kv_src_dtype src_dtype, const kv_strides *strides, int64_t page_size,
+                        int64_t kc_page_stride, int64_t vc_page_stride, int64_t size_limit,
+                        const kv_rope *rope, kv_cache_format format, const float *inv_k_scale,
+                        const float *inv_v_scale, const kv_block_scales *scales,
+                        kv_error_record *d_err, kv_stream_t stream);
+
+/*
+ * kv_gather_fp4 -- dequantising gather from e2m1 caches written by
+ * kv_store_rope: row t of k_out / v_out takes fl16(fl(code * S * scale)) of the
+ * cache row of slot indices[t] (code * S is exact in fp32; scale is *k_scale /
+ * *v_scale, forward scales in device memory, or 1 where the pointer is NULL).
+ * A NaN block scale (code 0x7F or 0xFF; never written by kv_store_rope) gives
+ * the canonical NaN 0x7FFF.  Other arguments and errors as kv_gather_fp8;
+ * kc_dim and vc_dim are not used (a row's codes are contiguous), the output's
+ * dims must be (else KV_ERR_UNSUPPORTED).
+ */
+kv_status kv_gather_fp4(const void *k_cache, const void *v_cache, const kv_block_scales *scales,
+                        void *k_out, void *v_out, const void *indices,
+                        kv_index_dtype index_dtype, int64_t index_stride, int64_t num_tokens,
+                        int32_t num_heads, int32_t head_dim, kv_src_dtype out_dtype,
+                        const kv_strides *strides, int64_t page_size, int64_t kc_page_stride,
+                        int64_t vc_page_stride, int64_t size_limit, const float *k_scale,
+                        const float *v_scale, kv_error_record *d_err, kv_stream_t stream);
+
+/* Byte strides of kv_attend.  Element (t, h, d) of q is at q + t * q_token +
+ * h * q_head + d * 2 (likewise out); cache row (page, offset, head) starts at
+ * k_cache + page * kc_page + offset * kc_slot + head * kc_head. */
+typedef struct kv_attend_strides {
+    int64_t q_token, q_head;
+    int64_t o_token, o_head;
+    int64_t kc_page, kc_slot, kc_head;
+    int64_t vc_page, vc_slot, vc_head;
+} kv_attend_strides;
+
+/*
+ * kv_attend -- softmax attention of ragged queries over a paged cache, causal,
+ * with an optional sliding window and a number of first tokens (sinks) that
+ * stay visible.
+ *
+ * Sequence b has seq_lens[b] tokens in the cache, token j at offset
+ * j % page_size of page page_table[b * table_stride + j / page_size], and the
+ * query rows q_start[b] .. q_start[b + 1] - 1 (q_start NULL: row b alone).
+ * They are its newest tokens: query i of n_q stands at position
+ * p = seq_lens[b] - n_q + i, and sees key j when
+ *     0 <= j <= p  and  (window == 0  or  j > p - window  or  j < sinks).
+ * Query head h reads KV head h / (num_q_heads / num_heads):
+ *     s_j = sm_scale * k_scale * sum_d q_d k_jd,
+ *     out = v_scale * sum_j exp(s_j) v_j / sum_j exp(s_j),
+ *     lse = log sum_j exp(s_j)  (natural logarithm),
+ * over the visible keys.  A row that sees no key is 0 with lse -infinity.
+ * Statistics and sums are fp32; 16-bit caches are multiplied in their type,
+ * e4m3fn and e2m1 values (with their block scales, both exact) in fp16 against
+ * queries brought into fp16's range by a power of two per row.
+ *
+ *   q, out      [num_q_tokens, num_q_heads, head_dim] of `dtype`; out must not
+ *               overlap q or the caches.
+ *   lse         NULL, or device floats [num_q_tokens, num_q_heads], contiguous.
+ *   page_table  int32 device array, table_width entries per sequence, rows
+ *               table_stride (>= table_width) entries apart.
+ *   seq_lens    int32 device array [num_seqs].
+ *   q_start     NULL (then num_q_tokens == num_seqs), or int32 device array
+ *               [num_seqs + 1], non-decreasing; values are clamped to
+ *               [0, num_q_tokens], rows outside every range are not written.
+ *   num_pages   pages of the caches.  Keys of a page id outside
+ *               [0, num_pages) are not visible; a sequence length outside
+ *               [0, table_width * page_size] counts as 0.  Either is counted
+ *               in the error record, by sequence (once or more often), and
+ *               never read.
+ *   head_dim    1 .. 1024.  Contiguous dims throughout.  Head dims that are
+ *               multiples of 16 up to 256, with 16-byte aligned bases and
+ *               strides, take the tensor-core kernels; the rest a general one.
+ *   format, k_scale, v_scale, scales
+ *               as kv_gather_fp4 for KV_CACHE_E2M1; forward scales per tensor
+ *               (device scalars, NULL: 1) for KV_CACHE_E4M3FN; none for
+ *               KV_CACHE_SRC (elements of `dtype`).
+ *   work        NULL, or a device workspace of work_bytes (256-byte aligned),
+ *               contents irrelevant.  It lets long sequences be split over the
+ *               GPU and joined; the more room, the finer
+ *               (KV_ATTEND_WORK_BYTES is always enough).  Without it each
+ *               block of query rows of one KV head is one CTA's work.  Calls
+ *               sharing one workspace must not overlap on the GPU.
+ * All pointers are device memory; q, out, the caches, the table and the lengths
+ * are rejected with KV_ERR_INVALID_ARG where CUDA does not know them.  The
+ * result does not depend on the order in which CTAs run; it may differ in rounding with the workspace's size.
+ *
+ * Returns KV_OK once enqueued, KV_ERR_INVALID_ARG for a bad argument (NULL
+ * pointers, sizes < 1, num_heads not dividing num_q_heads, window or sinks
+ * < 0, sm_scale not finite, table_stride < table_width, misaligned scalars or
+ * workspace), KV_ERR_UNSUPPORTED for head_dim > 1024, an e2m1 head_dim that is
+ * no multiple of 16, or odd 2-byte strides.  num_seqs == 0 or
+ * num_q_tokens == 0: KV_OK, nothing launched.
+ */
+#define KV_ATTEND_WORK_BYTES (64ll << 20)
+kv_status kv_attend(const void *q, void *out, float *lse, const void *k_cache,
+                    const void *v_cache, const int32_t *page_table, int64_t table_stride,
+                    int64_t table_width, const int32_t *seq_lens, const int32_t *q_start,
+                    int32_t num_seqs, int64_t num_q_tokens, int32_t num_q_heads,
+                    int32_t num_heads, int32_t head_dim, kv_src_dtype dtype,
+                    const kv_attend_strides *strides, int64_t page_size, int64_t num_pages,
+                    kv_cache_format format, const float *k_scale, const float *v_scale,
+                    const kv_block_scales *scales, float sm_scale, int64_t window, int64_t sinks,
+                    void *work, int64_t work_bytes, kv_error_record *d_err, kv_stream_t stream);
+
 /*
  * kv_store_noalloc -- kv_store for callers that cannot allocate device memory.
  * The pages have no counterpart; this entry point exists for this library's
