@@ -1,13 +1,14 @@
 // Attention over the paged cache (kv_attend): argument checks, the choice of
 // the kernel, and the general kernel.
 //
+//  * kv_attend_split  (kv_attend_split.cuh) head dims that are multiples of 16
+//                     up to 256, 16-byte aligned bases and strides.
 //  * kv_attend_rows   any head dim, alignment and stride: one warp per query
 //                     row and head, one key after the other.
 #include <cmath>
 #include <climits>
 
-#include "kv_attend.cuh"
-#include "kv_host.h"
+#include "kv_attend_split.cuh"
 
 namespace kvimpl {
 namespace {
@@ -135,14 +136,33 @@ extern "C" kv_status kv_attend(const void* q, void* out, float* lse, const void*
   p.q_heads = num_q_heads;
   p.kv_heads = num_heads;
   p.head_dim = head_dim;
-  p.max_len = table_width > INT_MAX / page_size ? INT_MAX : static_cast<int32_t>(table_width * page_size);
+  p.max_len = static_cast<int32_t>(table_width > (int64_t{1} << 30) / page_size ? int64_t{1} << 30 : table_width * page_size);
   p.window = window;
   p.sinks = sinks;
   p.scale_log2 = sm_scale * 1.4426950408889634f;
   p.bf16 = dtype == KV_SRC_BF16;
   p.err = d_err;
-  (void)work;
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  if (head_dim % 16 == 0 && head_dim <= 256 && ((q_bits | c_bits) & 15u) == 0) {
+    SplitParams sp = {};
+    sp.a = p;
+    // query rows of a sequence and KV head, on average: up to 8 take one mma column block, more two
+    const int64_t rows = (num_q_tokens + num_seqs - 1) / num_seqs * p.group.d;
+    const bool wide = rows > 8;
+    // no list of visible keys is longer
+    int64_t keys = p.max_len;
+    if (window > 0 && window < keys && sinks < keys) {
+      const int64_t most = window + sinks + 17;
+      keys = most < keys ? most : keys;
+    }
+    switch (format) {
+      case KV_CACHE_SRC:
+        return p.bf16 ? split_bf16(sp, wide, work, work_bytes, keys, stream)
+                      : split_f16(sp, wide, work, work_bytes, keys, stream);
+      case KV_CACHE_E4M3FN: return split_e4m3(sp, wide, work, work_bytes, keys, stream);
+      default: return split_e2m1(sp, wide, work, work_bytes, keys, stream);
+    }
+  }
   switch (format) {
     case KV_CACHE_SRC: return launch_rows_any<KV_CACHE_SRC>(p, stream);
     case KV_CACHE_E4M3FN: return launch_rows_any<KV_CACHE_E4M3FN>(p, stream);

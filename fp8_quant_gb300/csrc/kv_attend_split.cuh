@@ -1,0 +1,1033 @@
+// Attention for few query rows per sequence (decode, speculative steps): the
+// key axis is split over the GPU and the parts are joined.
+//
+// Bytes bound it: every visible K and V row is read once per KV head and meets
+// the few query rows of that head's group.  So
+//  * a warp takes one KV head and tiles of TW keys.  cp.async brings a tile's K
+//    and V rows from their pages into a ring of NU units of the warp's own
+//    shared memory, two or three units in flight at any time; keys behind the
+//    list's end and head dims behind D are zero-filled, not read.  The warps
+//    of a CTA take the heads of the same keys (their rows lie together) and,
+//    with fewer than eight heads, neighbouring tiles.
+//  * a lane copies exactly the 16-byte pieces that it will multiply, so it
+//    reads its own shared memory back, in order and without conflicts:
+//    S^T = K Q^T has the tile's keys as the 16 rows of mma.m16n8k16, and lane
+//    (g, t) needs row g's dims in any order that Q's registers share;
+//    O^T = V^T P^T has dims as rows, and lane (g, t) needs tokens 2t, 2t+1,
+//    2t+8, 2t+9 of any dims that it writes out in the end.  P^T leaves S^T's
+//    accumulators by movmatrix, and the running maximum, sum and O share one
+//    mapping of query rows to lanes, so no statistic crosses a lane but the
+//    maximum (three shuffles per tile and two rows) and, once, the sum.
+//  * quantised elements become fp16 in registers, exactly: e4m3 and e2m1 codes
+//    by the hardware's conversions, e2m1 blocks times their e4m3 scale (at
+//    most 6 significant bits).  The pair of tokens that V^T wants in one
+//    register is interleaved byte- or nibble-wise before the conversion.
+//    Queries in bf16 are brought to fp16 by a power of two per row that puts
+//    the row's largest element at 2^13 .. 2^14 (elements 2^-38 of it and
+//    smaller lose bits).  The tensor scale and the power go into the softmax's
+//    scale.
+//  * weights multiply 16-bit caches as two 16-bit terms (p = hi + lo), so their
+//    rounding does not add to the output's; the mma pipe has room for the
+//    second product there.  For quantised caches they are fp16 (2^-11).
+//  * every CTA takes an equal, contiguous share of all (sequence, block of
+//    rows, head group, tile) steps, found by a scan over the lengths on the
+//    device, so ragged batches are balanced without the host knowing a length.
+//    A share that begins or ends inside an item leaves its sums in the
+//    workspace, and a second kernel joins them in the order of the keys.
+//  * a row whose sum is 0 or whose output is not finite is done again by
+//    attend_row, which touches its visible keys alone: a NaN value that the
+//    mask hides from a row must not reach it through a weight of 0.
+#pragma once
+
+#include <atomic>
+
+#include "kv_attend.cuh"
+#include "kv_host.h"
+
+namespace kvimpl {
+
+struct SplitParams {
+  AttendParams a;
+  int32_t hw, subs;       // KV heads per CTA; warps per head
+  int32_t hgroups;        // kv_heads / hw
+  int32_t rows;           // query rows per item
+  int32_t tile;           // keys per step of a CTA
+  int32_t split;          // 0: an item is one CTA's
+  int32_t min_steps;      // a share is at least this long
+  int32_t shares;         // CTAs that may take a share
+  float *part_o, *part_ml;  // [2 * shares][hw][rows] x DP and x 2
+  int64_t* meta;          // [num_seqs + 1]: first step of each sequence; steps per share
+};
+
+// An item is (sequence, block of query rows, head group); its steps are its
+// key tiles.  The tile count is the same for all items of a sequence: an upper
+// bound for the union of any block's key lists, and at least one, so that rows
+// without keys are written too.
+struct SplitGeom {
+  int32_t blocks, steps;
+};
+
+__device__ __forceinline__ SplitGeom split_geom(const SplitParams& p, const AttendSeq& s) {
+  SplitGeom r;
+  const uint32_t rows = static_cast<uint32_t>(s.nq) * p.a.group.d;
+  r.blocks = static_cast<int32_t>((rows + p.rows - 1) / static_cast<uint32_t>(p.rows));
+  int64_t keys = s.len;
+  if (p.a.window > 0) {
+    // a block of rows spans at most this many positions
+    const int64_t span = min(static_cast<int64_t>(s.nq),
+                             static_cast<int64_t>((p.rows - 1) / static_cast<int32_t>(p.a.group.d) + 2));
+    const int64_t sinks = min(p.a.sinks, static_cast<int64_t>(s.len));
+    if (p.a.window < keys) keys = min(keys, p.a.window + span + sinks);
+  }
+  r.steps = max(static_cast<int32_t>((keys + p.tile - 1) / p.tile), 1);
+  return r;
+}
+
+__device__ __forceinline__ int64_t seq_units(const SplitParams& p, int32_t b, bool record) {
+  const SplitGeom g = split_geom(p, attend_seq(p.a, b, record));
+  return static_cast<int64_t>(g.blocks) * p.hgroups * (p.split ? g.steps : 1);
+}
+
+// ---------------------------------------------------------------------------
+// Formats: what a lane copies and how it becomes operands.
+// ---------------------------------------------------------------------------
+
+template <int FMT, int DP>
+struct Layout {
+  static constexpr int kBits = FMT == KV_CACHE_SRC ? 16 : FMT == KV_CACHE_E4M3FN ? 8 : 4;
+  static constexpr int kRow = DP * kBits / 8;                     // bytes of a padded row
+  static constexpr int KC = kRow / 4 < 16 ? kRow / 4 : 16;        // K: bytes a lane copies at once (4 lanes a row)
+  static constexpr int KN = kRow / 4 / KC;                        //    and how often
+  static constexpr int VC = kRow / 8 < 16 ? kRow / 8 : 16;        // V: 8 lanes a row
+  static constexpr int VN = kRow / 8 / VC;
+  static constexpr int KD = KC * 8 / kBits;                       // dims of a K piece
+  static constexpr int VD = VC * 8 / kBits;
+  static constexpr int TW = (FMT == KV_CACHE_SRC && DP >= 128) ? 16 : 32;  // keys of a warp's tile
+  static constexpr int MB = TW / 16;
+  static constexpr int kScaleWords = FMT == KV_CACHE_E2M1 ? DP / 64 + 2 : 0;  // words covering a row's scales, and their misalignment
+  static constexpr int kUnit = TW * kRow + TW * kScaleWords * 4;
+};
+
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const uint8_t* src, uint32_t bytes) {
+  if constexpr (BYTES == 16) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+  } else {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(bytes), "n"(BYTES) : "memory");
+  }
+}
+
+__device__ __forceinline__ void commit_async() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+template <int N>
+__device__ __forceinline__ void wait_async() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+template <int BYTES>
+__device__ __forceinline__ void ld_own(uint32_t (&w)[BYTES / 4], uint32_t addr) {
+  if constexpr (BYTES == 16) {
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr) : "memory");
+  } else if constexpr (BYTES == 8) {
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr) : "memory");
+  } else {
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(addr) : "memory");
+  }
+}
+
+__device__ __forceinline__ uint32_t ld_shared_u8(uint32_t addr) {
+  uint32_t r;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(addr) : "memory");
+  return r;
+}
+
+__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
+  uint32_t r;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r) : "r"(addr) : "memory");
+  return r;
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
+  return r;
+}
+
+template <bool kBF16>
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  if constexpr (kBF16) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  } else {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  }
+}
+
+// A K piece of KD dims as KD / 2 packed pairs.  sc: the piece's block scales (e2m1: one or two e4m3 codes).
+template <int FMT, int DP>
+__device__ __forceinline__ void k_pairs(uint32_t (&f)[Layout<FMT, DP>::KD / 2], const uint32_t (&w)[Layout<FMT, DP>::KC / 4],
+                                        uint32_t sc) {
+  using L = Layout<FMT, DP>;
+  if constexpr (FMT == KV_CACHE_SRC) {
+#pragma unroll
+    for (int i = 0; i < L::KC / 4; ++i) f[i] = w[i];
+  } else if constexpr (FMT == KV_CACHE_E4M3FN) {
+#pragma unroll
+    for (int i = 0; i < L::KC / 4; ++i) {
+      f[2 * i] = f16x2_from_e4m3x2(w[i]);
+      f[2 * i + 1] = f16x2_from_e4m3x2(w[i] >> 16);
+    }
+  } else {
+    const uint32_t s2 = f16x2_from_e4m3x2(sc);
+#pragma unroll
+    for (int i = 0; i < L::KC / 4; ++i) {
+      const uint32_t s = __byte_perm(s2, 0u, (i * 8) / kFp4Block == 0 ? 0x1010 : 0x3232);
+      uint32_t x[4];
+      f16x2_from_e2m1x8(w[i], x);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f[4 * i + j] = mul_f16x2(x[j], s);
+    }
+  }
+}
+
+// A V piece of tokens a and b, VD dims each, as VD words (a, b).  sc: e2m1, the tokens' scale codes (a, b)
+// per block of the piece.
+template <int FMT, int DP>
+__device__ __forceinline__ void v_pairs(uint32_t (&f)[Layout<FMT, DP>::VD], const uint32_t (&a)[Layout<FMT, DP>::VC / 4],
+                                        const uint32_t (&b)[Layout<FMT, DP>::VC / 4], const uint32_t (&sc)[2]) {
+  using L = Layout<FMT, DP>;
+  if constexpr (FMT == KV_CACHE_SRC) {
+#pragma unroll
+    for (int i = 0; i < L::VC / 4; ++i) {
+      f[2 * i] = __byte_perm(a[i], b[i], 0x5410);
+      f[2 * i + 1] = __byte_perm(a[i], b[i], 0x7632);
+    }
+  } else if constexpr (FMT == KV_CACHE_E4M3FN) {
+#pragma unroll
+    for (int i = 0; i < L::VC / 4; ++i) {
+      const uint32_t lo = __byte_perm(a[i], b[i], 0x5140), hi = __byte_perm(a[i], b[i], 0x7362);
+      f[4 * i] = f16x2_from_e4m3x2(lo);
+      f[4 * i + 1] = f16x2_from_e4m3x2(lo >> 16);
+      f[4 * i + 2] = f16x2_from_e4m3x2(hi);
+      f[4 * i + 3] = f16x2_from_e4m3x2(hi >> 16);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < L::VC / 4; ++i) {
+      const uint32_t even = (a[i] & 0x0F0F0F0Fu) | ((b[i] << 4) & 0xF0F0F0F0u);
+      const uint32_t odd = ((a[i] >> 4) & 0x0F0F0F0Fu) | (b[i] & 0xF0F0F0F0u);
+      const uint32_t s = f16x2_from_e4m3x2(sc[(i * 8) / kFp4Block]);
+      uint32_t e[4], o[4];
+      f16x2_from_e2m1x8(even, e);
+      f16x2_from_e2m1x8(odd, o);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        f[8 * i + 2 * j] = mul_f16x2(e[j], s);
+        f[8 * i + 2 * j + 1] = mul_f16x2(o[j], s);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The kernel
+// ---------------------------------------------------------------------------
+
+constexpr int kSplitWarps = 8;
+
+// Two CTAs an SM where the accumulators leave room for it.
+template <int DP, int NB>
+constexpr int kSplitCtas = DP * NB <= 128 ? 2 : 1;
+
+// Ring units of a warp: as many (up to 6) as those CTAs can hold in 220 KB.
+template <int FMT, int DP, int NB>
+constexpr int kSplitFit = (220 * 1024 / kSplitCtas<DP, NB> - 2048) / (kSplitWarps * Layout<FMT, DP>::kUnit);
+template <int FMT, int DP, int NB>
+constexpr int kSplitUnits = kSplitFit<FMT, DP, NB> > 6 ? 6 : kSplitFit<FMT, DP, NB>;
+
+// kBF16: the products' type (e4m3 and e2m1 caches: fp16).
+template <int FMT, int DP, int NB, bool kBF16>
+__global__ void __launch_bounds__(32 * kSplitWarps, (kSplitCtas<DP, NB>))
+    kv_attend_split(const __grid_constant__ SplitParams p) {
+  using L = Layout<FMT, DP>;
+  constexpr int NU = kSplitUnits<FMT, DP, NB>;
+  static_assert(NU >= 3, "ring");
+  static_assert(NU * L::kUnit >= NB * 8 * (DP + 2) * 4, "the join of a head's warps reuses the ring");
+  constexpr int TW = L::TW, MB = L::MB;
+  constexpr int QP = DP / 8;               // query pairs of a lane per row block
+  constexpr int OM = L::VN * L::VD / 2;    // O^T products per key block
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int64_t sh_scan[kSplitWarps + 1];
+  __shared__ int64_t sh_first[2];  // the share's first step's sequence, and that sequence's first step
+
+  const AttendParams& a = p.a;
+  const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
+  const uint32_t g = lane >> 2, t = lane & 3u;
+  const int32_t G = static_cast<int32_t>(a.group.d);
+  grid_handover();
+
+  // -- the share of this CTA ------------------------------------------------
+  const int32_t per_thread = (a.num_seqs + static_cast<int32_t>(blockDim.x) - 1) / static_cast<int32_t>(blockDim.x);
+  const int32_t b0 = min(static_cast<int32_t>(threadIdx.x) * per_thread, a.num_seqs);
+  const int32_t b1 = min(b0 + per_thread, a.num_seqs);
+  int64_t mine = 0;
+  for (int32_t b = b0; b < b1; ++b) mine += seq_units(p, b, blockIdx.x == 0);
+  int64_t incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+    if (lane >= static_cast<uint32_t>(o)) incl += v;
+  }
+  if (lane == 31u) sh_scan[warp] = incl;
+  __syncthreads();
+  int64_t excl = incl - mine, total = 0;
+  const uint32_t nwarps = blockDim.x >> 5;
+  for (uint32_t w = 0; w < nwarps; ++w) {
+    if (w < warp) excl += sh_scan[w];
+    total += sh_scan[w];
+  }
+  int64_t per = (total + p.shares - 1) / p.shares;
+  if (p.split && per < p.min_steps) per = p.min_steps;
+  if (per < 1) per = 1;
+  int64_t pos = per * blockIdx.x;
+  const int64_t end = min(total, pos + per);
+  if (pos >= excl && pos < excl + mine) {
+    int64_t base = excl;
+    int32_t b = b0;
+    for (;; ++b) {
+      const int64_t n = seq_units(p, b, false);
+      if (pos < base + n) break;
+      base += n;
+    }
+    sh_first[0] = b;
+    sh_first[1] = base;
+  }
+  if (p.split && blockIdx.x == 0) {  // for the join
+    int64_t base = excl;
+    for (int32_t b = b0; b < b1; ++b) {
+      p.meta[b] = base;
+      base += seq_units(p, b, false);
+    }
+    if (threadIdx.x == 0) p.meta[a.num_seqs] = per;
+  }
+  __syncthreads();
+  if (pos >= end) return;
+  int32_t b = static_cast<int32_t>(sh_first[0]);
+  int64_t base = sh_first[1];
+
+  const int32_t hl = static_cast<int32_t>(warp) % p.hw, sub = static_cast<int32_t>(warp) / p.hw;
+  const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * (NU * L::kUnit);
+  const float kscale = a.scale_log2 * tensor_scale(a.k_scale);
+  const float vscale = tensor_scale(a.v_scale);
+  const uint32_t row_bytes = static_cast<uint32_t>(a.head_dim) * L::kBits / 8;
+
+  while (pos < end && b < a.num_seqs) {
+    const AttendSeq seq = attend_seq(a, b, false);
+    const SplitGeom geom = split_geom(p, seq);
+    const int32_t unit = p.split ? geom.steps : 1;
+    const int64_t local = pos - base;
+    if (local >= static_cast<int64_t>(geom.blocks) * p.hgroups * unit) {
+      base += static_cast<int64_t>(geom.blocks) * p.hgroups * unit;
+      ++b;
+      continue;
+    }
+    const int32_t item = static_cast<int32_t>(local / unit);
+    const int32_t s_in = static_cast<int32_t>(local - static_cast<int64_t>(item) * unit);
+    const int32_t s_out = static_cast<int32_t>(min(static_cast<int64_t>(unit), s_in + (end - pos)));
+    const bool whole = s_out - s_in == unit;
+    const int32_t step0 = p.split ? s_in : 0, step1 = p.split ? s_out : geom.steps;
+    pos += s_out - s_in;
+    const int32_t rb = item / p.hgroups, hg = item - rb * p.hgroups;
+    const int32_t kvh = hg * p.hw + hl;
+    const int32_t row0 = rb * p.rows;
+    const int32_t nrows = min(p.rows, seq.nq * G - row0);
+    const int32_t p_first = seq.len - seq.nq;  // position of the sequence's first query
+    const int32_t q_lo = static_cast<int32_t>(a.group.quot(static_cast<uint32_t>(row0)));
+    const int32_t q_hi = static_cast<int32_t>(a.group.quot(static_cast<uint32_t>(row0 + nrows - 1)));
+    const KeyList keys = visible_keys(a, p_first + q_lo, p_first + q_hi);
+    const bool many_pos = q_lo != q_hi;  // rows at different positions: the list is their union
+
+    // -- queries: lane (g, t) holds the pairs of row g that K's pieces t, t + 4, .. meet -----
+    uint32_t qf[NB][QP];
+    float rs[NB][2];  // softmax scale of rows 2t, 2t + 1
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      const int32_t r = nb * 8 + static_cast<int32_t>(g);
+      const bool ok = r < nrows;
+      const uint32_t qi = a.group.quot(static_cast<uint32_t>(row0 + (ok ? r : 0)));
+      const int32_t h = kvh * G + (row0 + (ok ? r : 0) - static_cast<int32_t>(qi) * G);
+      const uint8_t* src = a.q + (static_cast<int64_t>(seq.q0) + qi) * a.q_token + h * a.q_head;
+      uint32_t amax = 0u;
+#pragma unroll
+      for (int i = 0; i < QP; i += 4) {
+        const int d = (static_cast<int>(t) + 4 * ((2 * i) / L::KD)) * L::KD + (2 * i) % L::KD;
+        uint4 w = make_uint4(0u, 0u, 0u, 0u);
+        if (ok && d < a.head_dim) w = __ldg(reinterpret_cast<const uint4*>(src + 2 * d));
+        qf[nb][i] = w.x; qf[nb][i + 1] = w.y; qf[nb][i + 2] = w.z; qf[nb][i + 3] = w.w;
+      }
+      float inv = 1.0f;
+      if constexpr (FMT != KV_CACHE_SRC) {
+        if (a.bf16) {
+#pragma unroll
+          for (int i = 0; i < QP; ++i) amax = absmax_pair<true>(amax, qf[nb][i]);
+          uint32_t m = __float_as_uint(absmax_pair_value<true>(amax));
+          m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+          m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+          const uint32_t e = m >> 23;  // 2^(140 - e): the largest element to 2^13 .. 2^14
+          const float f = __uint_as_float(min(254u, 267u - e) << 23);
+          inv = __fdiv_rn(1.0f, f);
+#pragma unroll
+          for (int i = 0; i < QP; ++i) {
+            const float2 x = widen2<true>(qf[nb][i]);
+            qf[nb][i] = pack2(x.x * f, x.y * f, false);
+          }
+        }
+      }
+      if (kscale < 0.0f) {  // the running maximum is taken before the scale
+#pragma unroll
+        for (int i = 0; i < QP; ++i) qf[nb][i] ^= 0x80008000u;
+      }
+      float full = fabsf(kscale) * inv;
+      if (full == 0.0f) full = __uint_as_float(1u);  // a scale of 0: hidden scores (-inf) must stay -inf
+      rs[nb][0] = __shfl_sync(0xFFFFFFFFu, full, 8u * t);
+      rs[nb][1] = __shfl_sync(0xFFFFFFFFu, full, 8u * t + 4u);
+    }
+
+    float o[NB][OM][4], m[NB][2], l[NB][2];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+      for (int i = 0; i < OM; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[nb][i][c] = 0.0f;
+      m[nb][0] = m[nb][1] = -INFINITY;
+      l[nb][0] = l[nb][1] = 0.0f;
+    }
+
+    // -- the tiles ----------------------------------------------------------------------
+    const int32_t* table = a.table + static_cast<int64_t>(b) * a.table_stride;
+    const uint8_t* kbase = a.k + kvh * a.k_head;
+    const uint8_t* vbase = a.v + kvh * a.v_head;
+    bool bad = false;  // a page id out of range was met
+    // a lane's key of the tile that is copied next: page id (-1: none) and offset in the page
+    auto lookup = [&](int32_t tile, int32_t* id, uint32_t* off) {
+      const int32_t i = tile * p.tile + sub * TW + static_cast<int32_t>(lane);
+      *id = -1;
+      *off = 0;
+      if (lane < TW && tile < step1 && i < keys.n) {
+        const uint32_t j = static_cast<uint32_t>(keys.key(i));
+        const uint32_t pg = a.page.quot(j);
+        *off = j - pg * a.page.d;
+        *id = __ldg(table + pg);
+      }
+    };
+    auto checked = [&](int32_t id) {
+      if (id >= a.num_pages || id < -1) {
+        bad = true;
+        record_oob(a.err, static_cast<uint64_t>(b));
+        return -1;
+      }
+      return id;
+    };
+    int32_t cur_id, next_id;
+    uint32_t cur_off, next_off;
+    lookup(step0, &next_id, &next_off);
+    int32_t tile_in = step0;  // tile whose units are copied next
+    uint32_t slot_in = 0;     // and the ring slot
+    // K rows of tile `tile_in` (kv 0) or its V rows (kv 1)
+    auto copy_unit = [&](int kv) {
+      if (kv == 0) {
+        // an unused table entry may hold anything; -1 from lookup() is "no key"
+        cur_id = next_id;
+        cur_off = next_off;
+        const bool real = lane < TW && tile_in < step1 && tile_in * p.tile + sub * TW + static_cast<int32_t>(lane) < keys.n;
+        cur_id = real ? (cur_id < 0 || cur_id >= a.num_pages ? checked(cur_id < 0 ? -2 : cur_id) : cur_id) : -1;
+        lookup(tile_in + 1, &next_id, &next_off);
+      }
+      if (tile_in < step1) {
+        const uint32_t unit_at = ring + slot_in * L::kUnit;
+        constexpr int kRows = 2 * MB;  // K rows of a lane: g, g + 8 of each 16
+        if (kv == 0) {
+#pragma unroll
+          for (int r = 0; r < kRows; ++r) {
+            const uint32_t tok = 8u * r + g;
+            const int32_t id = __shfl_sync(0xFFFFFFFFu, cur_id, tok);
+            const uint32_t off = __shfl_sync(0xFFFFFFFFu, cur_off, tok);
+            const uint8_t* src = id < 0 ? kbase : kbase + id * a.k_page + off * a.k_slot;
+            const int32_t have = id < 0 ? 0 : static_cast<int32_t>(row_bytes);
+#pragma unroll
+            for (int i = 0; i < L::KN; ++i) {
+              const int32_t at = static_cast<int32_t>(t + 4 * i) * L::KC;
+              copy_async<L::KC>(unit_at + ((r * L::KN + i) * 32 + lane) * L::KC, have > at ? src + at : kbase,
+                                static_cast<uint32_t>(min(max(have - at, 0), L::KC)));
+            }
+          }
+        } else {
+#pragma unroll
+          for (int r = 0; r < 4 * MB; ++r) {
+            const uint32_t tok = 16u * (r / 4) + 2u * t + (r & 1) + 8u * ((r >> 1) & 1);
+            const int32_t id = __shfl_sync(0xFFFFFFFFu, cur_id, tok);
+            const uint32_t off = __shfl_sync(0xFFFFFFFFu, cur_off, tok);
+            const uint8_t* src = id < 0 ? vbase : vbase + id * a.v_page + off * a.v_slot;
+            const int32_t have = id < 0 ? 0 : static_cast<int32_t>(row_bytes);
+#pragma unroll
+            for (int i = 0; i < L::VN; ++i) {
+              const int32_t at = static_cast<int32_t>(g + 8 * i) * L::VC;
+              copy_async<L::VC>(unit_at + ((r * L::VN + i) * 32 + lane) * L::VC, have > at ? src + at : vbase,
+                                static_cast<uint32_t>(min(max(have - at, 0), L::VC)));
+            }
+          }
+        }
+        if constexpr (FMT == KV_CACHE_E2M1) {
+          // lane = key: the aligned words around its row's scales, and where in them the row begins
+          const uint8_t* sbase = kv == 0 ? a.k_sc + kvh * a.ks_head : a.v_sc + kvh * a.vs_head;
+          const uint8_t* src = cur_id < 0 ? sbase
+                                          : sbase + (kv == 0 ? cur_id * a.ks_page + cur_off * a.ks_slot
+                                                             : cur_id * a.vs_page + cur_off * a.vs_slot);
+          const uint32_t mis = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(src) & 3u);
+          const uint32_t at = unit_at + TW * L::kRow + lane * (L::kScaleWords * 4);
+          const uint32_t need = cur_id < 0 ? 0u : mis + row_bytes / 8;  // a scale per 8 code bytes
+#pragma unroll
+          for (int i = 0; i < L::kScaleWords - 1; ++i)
+            copy_async<4>(at + 4 * i, 4u * i < need ? src - mis + 4 * i : sbase - (reinterpret_cast<uintptr_t>(sbase) & 3u),
+                          4u * i < need ? 4u : 0u);
+          asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + 4 * (L::kScaleWords - 1)), "r"(mis) : "memory");
+        }
+      }
+      commit_async();
+      if (kv == 1) ++tile_in;
+      slot_in = slot_in + 1 == NU ? 0u : slot_in + 1;
+    };
+#pragma unroll
+    for (int i = 0; i < NU - 1; ++i) copy_unit(i & 1);
+
+    uint32_t slot = 0;
+    auto next_slot = [&] { slot = slot + 1 == NU ? 0u : slot + 1; };
+    for (int32_t tile = step0; tile < step1; ++tile) {
+      // S^T = K Q^T
+      wait_async<NU - 2>();
+      __syncwarp();
+      copy_unit((NU - 1) & 1);
+      float s[NB][MB][4];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) s[nb][mb][c] = 0.0f;
+      const uint32_t kat = ring + slot * L::kUnit;
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb) {
+        uint32_t sc[2] = {0u, 0u};
+#pragma unroll
+        for (int i = 0; i < L::KN; ++i) {
+          uint32_t f[2][L::KD / 2];
+#pragma unroll
+          for (int rh = 0; rh < 2; ++rh) {
+            uint32_t w[L::KC / 4];
+            ld_own<L::KC>(w, kat + (((mb * 2 + rh) * L::KN + i) * 32 + lane) * L::KC);
+            if constexpr (FMT == KV_CACHE_E2M1) {
+              const uint32_t srow = kat + TW * L::kRow + (mb * 16 + rh * 8 + g) * (L::kScaleWords * 4);
+              const uint32_t sat = srow + ld_shared_u32(srow + 4 * (L::kScaleWords - 1)) + (t + 4 * i) * (L::KD / kFp4Block);
+              sc[rh] = ld_shared_u8(sat);
+              if constexpr (L::KD > kFp4Block) sc[rh] |= ld_shared_u8(sat + 1) << 8;
+            }
+            k_pairs<FMT, DP>(f[rh], w, sc[rh]);
+          }
+#pragma unroll
+          for (int j = 0; j < L::KD / 4; ++j)
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+              mma16816<kBF16>(s[nb][mb], f[0][2 * j], f[1][2 * j], f[0][2 * j + 1], f[1][2 * j + 1],
+                              qf[nb][i * (L::KD / 2) + 2 * j], qf[nb][i * (L::KD / 2) + 2 * j + 1]);
+        }
+      }
+      next_slot();
+
+      // mask: s[..][0], [1]: key g, rows 2t, 2t + 1; [2], [3]: key g + 8
+      const int32_t first = tile * p.tile + sub * TW;
+      if (many_pos || first + TW > keys.n || __any_sync(0xFFFFFFFFu, bad)) {
+        int32_t pos_of[NB][2];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            pos_of[nb][c] = p_first + static_cast<int32_t>(a.group.quot(static_cast<uint32_t>(row0 + nb * 8 + 2 * t + c)));
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+          for (int rh = 0; rh < 2; ++rh) {
+            const int32_t i = first + mb * 16 + rh * 8 + static_cast<int32_t>(g);
+            bool have = i < keys.n;
+            const int32_t j = have ? keys.key(i) : 0;
+            if (have) {
+              const int32_t id = __ldg(table + a.page.quot(static_cast<uint32_t>(j)));
+              have = id >= 0 && id < a.num_pages;
+            }
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+              for (int c = 0; c < 2; ++c)
+                if (!have || !sees(a, pos_of[nb][c], j)) s[nb][mb][rh * 2 + c] = -INFINITY;
+          }
+      }
+
+      // running maximum and sum
+      uint32_t pt[NB][MB][2], pl[NB][MB][2];
+      bool grew = false;
+      float alpha[NB][2];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float x = s[nb][0][c];
+#pragma unroll
+          for (int mb = 0; mb < MB; ++mb) x = fmaxf(x, fmaxf(s[nb][mb][c], s[nb][mb][2 + c]));
+          x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
+          x = fmaxf(m[nb][c], x * rs[nb][c]);
+          const float ref = x == -INFINITY ? 0.0f : x;
+          grew |= x > m[nb][c];
+          alpha[nb][c] = exp2_fast(m[nb][c] - ref);
+          m[nb][c] = x;
+          float sum = 0.0f;
+#pragma unroll
+          for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+            for (int rh = 0; rh < 2; ++rh) {
+              float& e = s[nb][mb][2 * rh + c];
+              e = exp2_fast(__fmaf_rn(e, rs[nb][c], -ref));
+              sum += e;
+            }
+          l[nb][c] = __fmaf_rn(l[nb][c], alpha[nb][c], sum);
+        }
+      if (__any_sync(0xFFFFFFFFu, grew)) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int i = 0; i < OM; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) o[nb][i][c] *= alpha[nb][c & 1];
+      }
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+          for (int rh = 0; rh < 2; ++rh) {
+            const float x = s[nb][mb][2 * rh], y = s[nb][mb][2 * rh + 1];
+            const uint32_t w = pack2(x, y, kBF16);
+            pt[nb][mb][rh] = transpose8x8(w);
+            if constexpr (FMT == KV_CACHE_SRC) {
+              const float2 r = widen2<kBF16>(w);
+              pl[nb][mb][rh] = transpose8x8(pack2(x - r.x, y - r.y, kBF16));
+            }
+          }
+
+      // O^T += V^T P^T
+      wait_async<NU - 2>();
+      __syncwarp();
+      copy_unit(NU & 1);
+      const uint32_t vat = ring + slot * L::kUnit;
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb) {
+        uint32_t srow[4];
+        if constexpr (FMT == KV_CACHE_E2M1) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const uint32_t tok = 16u * mb + 2u * t + (r & 1) + 8u * (r >> 1);
+            const uint32_t at = vat + TW * L::kRow + tok * (L::kScaleWords * 4);
+            srow[r] = at + ld_shared_u32(at + 4 * (L::kScaleWords - 1));
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < L::VN; ++i) {
+          uint32_t f[2][L::VD];
+#pragma unroll
+          for (int pr = 0; pr < 2; ++pr) {
+            uint32_t wa[L::VC / 4], wb[L::VC / 4], sc[2] = {0u, 0u};
+            ld_own<L::VC>(wa, vat + (((mb * 4 + 2 * pr) * L::VN + i) * 32 + lane) * L::VC);
+            ld_own<L::VC>(wb, vat + (((mb * 4 + 2 * pr + 1) * L::VN + i) * 32 + lane) * L::VC);
+            if constexpr (FMT == KV_CACHE_E2M1) {
+#pragma unroll
+              for (int x = 0; x < (L::VD + kFp4Block - 1) / kFp4Block; ++x) {
+                const uint32_t blk = (g + 8 * i) * L::VD / kFp4Block + x;
+                sc[x] = ld_shared_u8(srow[2 * pr] + blk) | (ld_shared_u8(srow[2 * pr + 1] + blk) << 8);
+              }
+            }
+            v_pairs<FMT, DP>(f[pr], wa, wb, sc);
+          }
+#pragma unroll
+          for (int j = 0; j < L::VD / 2; ++j)
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+              mma16816<kBF16>(o[nb][i * (L::VD / 2) + j], f[0][2 * j], f[0][2 * j + 1], f[1][2 * j], f[1][2 * j + 1],
+                              pt[nb][mb][0], pt[nb][mb][1]);
+              if constexpr (FMT == KV_CACHE_SRC)
+                mma16816<kBF16>(o[nb][i * (L::VD / 2) + j], f[0][2 * j], f[0][2 * j + 1], f[1][2 * j], f[1][2 * j + 1],
+                                pl[nb][mb][0], pl[nb][mb][1]);
+            }
+        }
+      }
+      next_slot();
+    }
+    wait_async<0>();
+
+    // -- the item's end -----------------------------------------------------------------
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float x = l[nb][c];
+        x += __shfl_xor_sync(0xFFFFFFFFu, x, 4);
+        x += __shfl_xor_sync(0xFFFFFFFFu, x, 8);
+        x += __shfl_xor_sync(0xFFFFFFFFu, x, 16);
+        l[nb][c] = x;
+      }
+    if (p.subs > 1) {
+      // the warps of a head join theirs in shared memory: [row][DP + 2] floats each
+      float* own = reinterpret_cast<float*>(smem + warp * (NU * L::kUnit));
+      __syncwarp();
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float* row = own + (nb * 8 + 2 * t + c) * (DP + 2);
+#pragma unroll
+          for (int i = 0; i < OM; ++i) {
+            const int d = (static_cast<int>(g) + 8 * (2 * i / L::VD)) * L::VD + 2 * i % L::VD;
+            row[d] = o[nb][i][c];
+            row[d + 1] = o[nb][i][2 + c];
+          }
+          if (g == 0u) {
+            row[DP] = m[nb][c];
+            row[DP + 1] = l[nb][c];
+          }
+        }
+      __syncthreads();
+      for (int32_t r = sub; r < nrows; r += p.subs) {
+        float mm = -INFINITY;
+        for (int32_t x = 0; x < p.subs; ++x)
+          mm = fmaxf(mm, reinterpret_cast<const float*>(smem + (x * p.hw + hl) * (NU * L::kUnit))[r * (DP + 2) + DP]);
+        const float ref = mm == -INFINITY ? 0.0f : mm;
+        float ll = 0.0f, acc[DP / 32];
+#pragma unroll
+        for (int i = 0; i < DP / 32; ++i) acc[i] = 0.0f;
+        for (int32_t x = 0; x < p.subs; ++x) {
+          const float* row = reinterpret_cast<const float*>(smem + (x * p.hw + hl) * (NU * L::kUnit)) + r * (DP + 2);
+          const float e = exp2_fast(row[DP] - ref);
+          ll = __fmaf_rn(row[DP + 1], e, ll);
+#pragma unroll
+          for (int i = 0; i < DP / 32; ++i) acc[i] = __fmaf_rn(row[lane + 32 * i], e, acc[i]);
+        }
+        if (whole) {
+          const uint32_t qi = a.group.quot(static_cast<uint32_t>(row0 + r));
+          const int32_t tok = seq.q0 + static_cast<int32_t>(qi), h = kvh * G + (row0 + r - static_cast<int32_t>(qi) * G);
+          const float inv = __fdiv_rn(vscale, ll);
+          bool fine = ll > 0.0f;
+#pragma unroll
+          for (int i = 0; i < DP / 32; ++i) fine = fine && fabsf(acc[i] * inv) < INFINITY;
+          if (!__all_sync(0xFFFFFFFFu, fine)) {
+            attend_row<FMT, 8>(a, b, p_first + static_cast<int32_t>(qi), tok, h);
+            continue;
+          }
+          uint16_t* out = reinterpret_cast<uint16_t*>(a.out + tok * a.o_token + h * a.o_head);
+#pragma unroll
+          for (int i = 0; i < DP / 32; ++i)
+            if (static_cast<int32_t>(lane) + 32 * i < a.head_dim) out[lane + 32 * i] = round16(acc[i] * inv, a.bf16);
+          if (a.lse && lane == 0u)
+            a.lse[static_cast<int64_t>(tok) * a.q_heads + h] = (mm + log2f(ll)) * 0.6931471805599453f;
+        } else {
+          const int64_t at = (static_cast<int64_t>(2 * blockIdx.x + (step0 == 0 ? 1 : 0)) * p.hw + hl) * p.rows + r;
+#pragma unroll
+          for (int i = 0; i < DP / 32; ++i) p.part_o[at * DP + lane + 32 * i] = acc[i];
+          if (lane == 0u) *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(mm, ll);
+        }
+      }
+      __syncthreads();
+      continue;
+    }
+    if (!whole) {
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int32_t r = nb * 8 + 2 * static_cast<int32_t>(t) + c;
+          if (r >= nrows) continue;
+          const int64_t at = (static_cast<int64_t>(2 * blockIdx.x + (step0 == 0 ? 1 : 0)) * p.hw + hl) * p.rows + r;
+          float* row = p.part_o + at * DP;
+#pragma unroll
+          for (int i = 0; i < OM; i += 2) {
+            const int d = (static_cast<int>(g) + 8 * (2 * i / L::VD)) * L::VD + 2 * i % L::VD;
+            *reinterpret_cast<float4*>(row + d) = make_float4(o[nb][i][c], o[nb][i][2 + c], o[nb][i + 1][c], o[nb][i + 1][2 + c]);
+          }
+          if (g == 0u) *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(m[nb][c], l[nb][c]);
+        }
+      continue;
+    }
+    uint32_t again = 0u;  // rows to be done once more, a bit each
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int32_t r = nb * 8 + 2 * static_cast<int32_t>(t) + c;
+        if (r < nrows) {
+          const float inv = __fdiv_rn(vscale, l[nb][c]);
+          bool fine = l[nb][c] > 0.0f;
+          const uint32_t qi = a.group.quot(static_cast<uint32_t>(row0 + r));
+          const int32_t tok = seq.q0 + static_cast<int32_t>(qi), h = kvh * G + (row0 + r - static_cast<int32_t>(qi) * G);
+          uint8_t* out = a.out + tok * a.o_token + h * a.o_head;
+#pragma unroll
+          for (int i = 0; i < OM; i += 4) {
+            const int d = (static_cast<int>(g) + 8 * (2 * i / L::VD)) * L::VD + 2 * i % L::VD;
+            uint32_t w[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const float lo = o[nb][i + x][c] * inv, hi = o[nb][i + x][2 + c] * inv;
+              fine = fine && fabsf(lo) < INFINITY && fabsf(hi) < INFINITY;
+              w[x] = pack2(lo, hi, a.bf16);
+            }
+            if (d < a.head_dim) *reinterpret_cast<uint4*>(out + 2 * d) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          if (a.lse && g == 0u)
+            a.lse[static_cast<int64_t>(tok) * a.q_heads + h] = (m[nb][c] + log2f(l[nb][c])) * 0.6931471805599453f;
+          if (!fine) again |= 1u << r;
+        }
+      }
+    again = __reduce_or_sync(0xFFFFFFFFu, again);
+    while (again != 0u) {
+      const int32_t r = __ffs(static_cast<int>(again)) - 1;
+      again &= again - 1u;
+      const uint32_t qi = a.group.quot(static_cast<uint32_t>(row0 + r));
+      attend_row<FMT, 8>(a, b, p_first + static_cast<int32_t>(qi), seq.q0 + static_cast<int32_t>(qi),
+                         kvh * G + (row0 + r - static_cast<int32_t>(qi) * G));
+    }
+  }
+}
+
+// Joins the parts of the items that were split, in the order of their keys:
+// `wpr` warps of the CTA take one output row.
+template <int FMT, int DP>
+__global__ void __launch_bounds__(256) kv_attend_join(const __grid_constant__ SplitParams p, const int32_t wpr) {
+  __shared__ float sh[8][DP + 2];
+  const AttendParams& a = p.a;
+  const uint32_t lane = threadIdx.x & 31u;
+  const int32_t warp = static_cast<int32_t>(threadIdx.x >> 5), part = warp % wpr;
+  const int64_t unit = static_cast<int64_t>(blockIdx.x) * (8 / wpr) + warp / wpr;
+  const int32_t tok = static_cast<int32_t>(unit / a.q_heads), h = static_cast<int32_t>(unit - static_cast<int64_t>(tok) * a.q_heads);
+  grid_handover();
+  int32_t b = tok, c0 = 0, c1 = 0, hl = 0, r = 0, pos = 0;
+  bool joined = false;
+  if (tok < a.num_q) {
+    if (a.q_start) {
+      int32_t lo = 0, hi = a.num_seqs - 1;
+      while (lo < hi) {
+        const int32_t mid = (lo + hi + 1) >> 1;
+        if (__ldg(a.q_start + mid) <= tok) lo = mid; else hi = mid - 1;
+      }
+      b = lo;
+    }
+    const AttendSeq s = attend_seq(a, b, false);
+    if (tok >= s.q0 && tok < s.q0 + s.nq) {
+      const SplitGeom geom = split_geom(p, s);
+      const int32_t G = static_cast<int32_t>(a.group.d), kvh = static_cast<int32_t>(a.group.quot(static_cast<uint32_t>(h)));
+      const int32_t row = (tok - s.q0) * G + (h - kvh * G);
+      const int32_t rb = row / p.rows, hg = kvh / p.hw;
+      hl = kvh - hg * p.hw;
+      r = row - rb * p.rows;
+      pos = s.len - s.nq + (tok - s.q0);
+      const int64_t per = __ldcg(reinterpret_cast<const long long*>(p.meta) + a.num_seqs);
+      const int64_t s0 = __ldcg(reinterpret_cast<const long long*>(p.meta) + b) +
+                         (static_cast<int64_t>(rb) * p.hgroups + hg) * geom.steps;
+      c0 = static_cast<int32_t>(s0 / per);
+      c1 = static_cast<int32_t>((s0 + geom.steps - 1) / per);
+      joined = c0 != c1;
+    }
+  }
+  // all warps of a row agree on `joined`; with one warp a row there is no barrier below
+  float mm = -INFINITY, ll = 0.0f, acc[DP / 32];
+#pragma unroll
+  for (int i = 0; i < DP / 32; ++i) acc[i] = 0.0f;
+  if (joined) {
+    for (int32_t c = c0 + part; c <= c1; c += 4 * wpr) {
+      float2 ml[4];
+      float v[4][DP / 32];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int32_t cc = c + x * wpr;
+        ml[x] = make_float2(-INFINITY, 0.0f);
+#pragma unroll
+        for (int i = 0; i < DP / 32; ++i) v[x][i] = 0.0f;
+        if (cc <= c1) {
+          const int64_t at = (static_cast<int64_t>(2 * cc + (cc == c0 ? 1 : 0)) * p.hw + hl) * p.rows + r;
+          ml[x] = __ldcg(reinterpret_cast<const float2*>(p.part_ml + at * 2));
+#pragma unroll
+          for (int i = 0; i < DP / 32; ++i) v[x][i] = __ldcg(p.part_o + at * DP + lane + 32 * i);
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const float mn = fmaxf(mm, ml[x].x), ref = mn == -INFINITY ? 0.0f : mn;
+        const float ea = exp2_fast(mm - ref), eb = exp2_fast(ml[x].x - ref);
+        mm = mn;
+        ll = __fmaf_rn(ll, ea, ml[x].y * eb);
+#pragma unroll
+        for (int i = 0; i < DP / 32; ++i) acc[i] = __fmaf_rn(acc[i], ea, v[x][i] * eb);
+      }
+    }
+  }
+  if (wpr > 1) {
+#pragma unroll
+    for (int i = 0; i < DP / 32; ++i) sh[warp][lane + 32 * i] = acc[i];
+    if (lane == 0u) {
+      sh[warp][DP] = mm;
+      sh[warp][DP + 1] = ll;
+    }
+    __syncthreads();
+    if (part != 0) return;
+    for (int32_t w = warp + 1; w < warp + wpr; ++w) {
+      const float mw = sh[w][DP], mn = fmaxf(mm, mw), ref = mn == -INFINITY ? 0.0f : mn;
+      const float ea = exp2_fast(mm - ref), eb = exp2_fast(mw - ref);
+      mm = mn;
+      ll = __fmaf_rn(ll, ea, sh[w][DP + 1] * eb);
+#pragma unroll
+      for (int i = 0; i < DP / 32; ++i) acc[i] = __fmaf_rn(acc[i], ea, sh[w][lane + 32 * i] * eb);
+    }
+  }
+  if (!joined) return;
+  const float inv = __fdiv_rn(tensor_scale(a.v_scale), ll);
+  bool fine = ll > 0.0f;
+#pragma unroll
+  for (int i = 0; i < DP / 32; ++i) fine = fine && fabsf(acc[i] * inv) < INFINITY;
+  if (!__all_sync(0xFFFFFFFFu, fine)) {
+    attend_row<FMT, 8>(a, b, pos, tok, h);
+    return;
+  }
+  uint16_t* out = reinterpret_cast<uint16_t*>(a.out + tok * a.o_token + h * a.o_head);
+#pragma unroll
+  for (int i = 0; i < DP / 32; ++i)
+    if (static_cast<int32_t>(lane) + 32 * i < a.head_dim) out[lane + 32 * i] = round16(acc[i] * inv, a.bf16);
+  if (a.lse && lane == 0u)
+    a.lse[static_cast<int64_t>(tok) * a.q_heads + h] = (mm + log2f(ll)) * 0.6931471805599453f;
+}
+
+// ---------------------------------------------------------------------------
+// Host
+// ---------------------------------------------------------------------------
+
+// Raises a kernel's dynamic shared memory limit once per device.
+struct SmemOptIn {
+  std::atomic<uint64_t> done{0};
+  kv_status operator()(const void* kernel, int bytes) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e);
+    const uint64_t bit = dev >= 0 && dev < kMaxDevices ? uint64_t{1} << dev : 0u;
+    if ((done.load(std::memory_order_acquire) & bit) != 0u) return KV_OK;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return cuda_fail(e);
+    done.fetch_or(bit, std::memory_order_release);
+    return KV_OK;
+  }
+};
+
+// Launches the split kernel (and the join) of one format and padded head dim.
+template <int FMT, int DP, int NB, bool kBF16>
+kv_status launch_split(SplitParams p, void* work, int64_t work_bytes, int64_t max_keys, cudaStream_t stream) {
+  using L = Layout<FMT, DP>;
+  constexpr int kSmem = kSplitWarps * kSplitUnits<FMT, DP, NB> * L::kUnit;
+  auto* kernel = kv_attend_split<FMT, DP, NB, kBF16>;
+  const AttendParams& a = p.a;
+  p.rows = 8 * NB;
+  p.hw = 1;
+  for (int h = 2; h <= kSplitWarps; ++h)
+    if (a.kv_heads % h == 0) p.hw = h;
+  p.subs = kSplitWarps / p.hw;
+  p.hgroups = a.kv_heads / p.hw;
+  p.tile = L::TW * p.subs;
+  p.min_steps = 4;
+
+  int sms = 0;
+  kv_status st = current_sm_count(&sms);
+  if (st != KV_OK) return st;
+  static SmemOptIn opt_in;
+  st = opt_in(reinterpret_cast<const void*>(kernel), kSmem);
+  if (st != KV_OK) return st;
+  const int64_t full = static_cast<int64_t>(sms) * kSplitCtas<DP, NB>;
+
+  // An item that cannot be longer than the shortest share is not split, nor is
+  // any where the workspace holds the parts of less than half the GPU.
+  const int64_t meta = (static_cast<int64_t>(a.num_seqs) + 1 + 31) / 32 * 256;
+  const int64_t slot = static_cast<int64_t>(p.hw) * p.rows * (DP + 2) * 4;
+  int64_t shares = full;
+  if (work && work_bytes > meta) {
+    const int64_t fit = (work_bytes - meta) / (2 * slot);
+    shares = fit < full ? fit : full;
+  } else {
+    shares = 0;
+  }
+  p.split = max_keys > static_cast<int64_t>(p.min_steps) * p.tile && 2 * shares >= full;
+  if (p.split) {
+    p.shares = static_cast<int32_t>(shares);
+    p.meta = static_cast<int64_t*>(work);
+    p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(work) + meta);
+    p.part_ml = p.part_o + 2 * shares * p.hw * p.rows * DP;
+  } else {
+    // one share an item: at most this many
+    const int64_t rows = static_cast<int64_t>(a.num_q) * a.group.d;
+    const int64_t items = (rows / p.rows + a.num_seqs) * p.hgroups;
+    p.shares = static_cast<int32_t>(items < 0x7FFFFFFF ? items : 0x7FFFFFFF);
+  }
+
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.shares));
+  cfg.blockDim = dim3(static_cast<unsigned>(32 * p.hw * p.subs));
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t le = cudaLaunchKernelEx(&cfg, kernel, p);
+  if (le != cudaSuccess) return cuda_fail(le);
+  if (!p.split) return KV_OK;
+
+  // few rows: a CTA each, as their parts are many; many rows: a warp each
+  const int64_t rows = static_cast<int64_t>(a.num_q) * a.q_heads;
+  const int32_t wpr = rows < 4ll * sms ? 8 : 1;
+  const int64_t per = 8 / wpr;
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + per - 1) / per));
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  le = cudaLaunchKernelEx(&cfg, kv_attend_join<FMT, DP>, p, wpr);
+  return le == cudaSuccess ? KV_OK : cuda_fail(le);
+}
+
+template <int FMT, bool kBF16>
+kv_status launch_split_fmt(const SplitParams& p, bool wide, void* work, int64_t work_bytes, int64_t max_keys,
+                           cudaStream_t stream) {
+  const int d = p.a.head_dim;
+  if (d <= 64)
+    return wide ? launch_split<FMT, 64, 2, kBF16>(p, work, work_bytes, max_keys, stream)
+                : launch_split<FMT, 64, 1, kBF16>(p, work, work_bytes, max_keys, stream);
+  if (d <= 128)
+    return wide ? launch_split<FMT, 128, 2, kBF16>(p, work, work_bytes, max_keys, stream)
+                : launch_split<FMT, 128, 1, kBF16>(p, work, work_bytes, max_keys, stream);
+  return launch_split<FMT, 256, 1, kBF16>(p, work, work_bytes, max_keys, stream);
+}
+
+// The formats' instantiations, a translation unit each.
+kv_status split_bf16(const SplitParams& p, bool wide, void* work, int64_t work_bytes, int64_t max_keys, cudaStream_t stream);
+kv_status split_f16(const SplitParams& p, bool wide, void* work, int64_t work_bytes, int64_t max_keys, cudaStream_t stream);
+kv_status split_e4m3(const SplitParams& p, bool wide, void* work, int64_t work_bytes, int64_t max_keys, cudaStream_t stream);
+kv_status split_e2m1(const SplitParams& p, bool wide, void* work, int64_t work_bytes, int64_t max_keys, cudaStream_t stream);
+
+}  // namespace kvimpl

@@ -543,7 +543,7 @@ typedef struct kv_attend_strides {
  *               [0, num_q_tokens], rows outside every range are not written.
  *   num_pages   pages of the caches.  Keys of a page id outside
  *               [0, num_pages) are not visible; a sequence length outside
- *               [0, table_width * page_size] counts as 0.  Either is counted
+ *               [0, min(table_width * page_size, 2^30)] counts as 0.  Either is counted
  *               in the error record, by sequence (once or more often), and
  *               never read.
  *   head_dim    1 .. 1024.  Contiguous dims throughout.  Head dims that are

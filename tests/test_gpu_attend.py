@@ -214,6 +214,15 @@ def test_workspace_sizes_and_repeats(batch, fmt):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("sm_scale", [0.0, -0.3, 2.0])
+@pytest.mark.parametrize("batch", ["speculative", "chunks"])
+def test_score_scales(batch, sm_scale, fmt):
+    """Any finite scale: 0 weighs all visible keys alike, a negative one turns the order round."""
+    lens, nqs = BATCHES[batch]
+    run(AttendProblem(lens, nqs, 4, 2, 64, fmt=fmt, window=40, sinks=1, seed=28, scale=0.25), sm_scale=sm_scale)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("nq", [1, 30])
 def test_bad_pages_and_lengths(nq, fmt):
     """Keys of a page id out of range are not visible; a length out of range counts as 0; both are
