@@ -146,6 +146,10 @@ extern "C" kv_status kv_attend(const void* q, void* out, float* lse, const void*
   if (head_dim % 16 == 0 && head_dim <= 256 && ((q_bits | c_bits) & 15u) == 0) {
     SplitParams sp = {};
     sp.a = p;
+    sp.whole_blocks = page_size % 16 == 0;
+    if (format == KV_CACHE_E2M1)
+      sp.sc_aligned = ((u64(scales->k) | u64(scales->v) | u64(scales->k_page) | u64(scales->k_slot) | u64(scales->k_head) |
+                        u64(scales->v_page) | u64(scales->v_slot) | u64(scales->v_head)) & 3u) == 0;
     // query rows of a sequence and KV head, on average: up to 8 take one mma column block, more two
     const int64_t rows = (num_q_tokens + num_seqs - 1) / num_seqs * p.group.d;
     const bool wide = rows > 8;

@@ -51,7 +51,8 @@ struct SplitParams {
   int32_t hw, subs;       // KV heads per CTA; warps per head
   int32_t hgroups;        // kv_heads / hw
   int32_t rows;           // query rows per item
-  int32_t tile;           // keys per step of a CTA
+  int32_t whole_blocks;   // page_size is a multiple of 16: 16 aligned keys share a page
+  int32_t sc_aligned;     // e2m1: every row of block scales begins on a word
   int32_t split;          // 0: an item is one CTA's
   int32_t min_steps;      // a share is at least this long
   int32_t shares;         // CTAs that may take a share
@@ -59,32 +60,53 @@ struct SplitParams {
   int64_t* meta;          // [num_seqs + 1]: first step of each sequence; steps per share
 };
 
-// An item is (sequence, block of query rows, head group); its steps are its
-// key tiles.  The tile count is the same for all items of a sequence: an upper
-// bound for the union of any block's key lists, and at least one, so that rows
-// without keys are written too.
+// An item is (sequence, block of query rows, head group); its steps are the
+// tiles of TW keys, aligned to TW, that hold a key some row of it sees, `subs`
+// at a time.  The step count is the same for all items of a sequence: an upper
+// bound over its blocks, and at least one, so that rows without keys are
+// written too.
 struct SplitGeom {
   int32_t blocks, steps;
 };
 
+template <int TW>
 __device__ __forceinline__ SplitGeom split_geom(const SplitParams& p, const AttendSeq& s) {
   SplitGeom r;
   const uint32_t rows = static_cast<uint32_t>(s.nq) * p.a.group.d;
   r.blocks = static_cast<int32_t>((rows + p.rows - 1) / static_cast<uint32_t>(p.rows));
-  int64_t keys = s.len;
-  if (p.a.window > 0) {
-    // a block of rows spans at most this many positions
-    const int64_t span = min(static_cast<int64_t>(s.nq),
-                             static_cast<int64_t>((p.rows - 1) / static_cast<int32_t>(p.a.group.d) + 2));
-    const int64_t sinks = min(p.a.sinks, static_cast<int64_t>(s.len));
-    if (p.a.window < keys) keys = min(keys, p.a.window + span + sinks);
+  int32_t tiles = (s.len + TW - 1) / TW;
+  if (p.a.window > 0 && p.a.window < s.len) {
+    // a block of rows spans at most `span` positions, and its windows window + span - 1 keys
+    const int32_t span = min(s.nq, (p.rows - 1) / static_cast<int32_t>(p.a.group.d) + 2);
+    const int64_t sinks = (min(p.a.sinks, static_cast<int64_t>(s.len)) + TW - 1) / TW;
+    tiles = static_cast<int32_t>(min(static_cast<int64_t>(tiles), sinks + (p.a.window + span + TW - 3) / TW + 1));
   }
-  r.steps = max(static_cast<int32_t>((keys + p.tile - 1) / p.tile), 1);
+  r.steps = max((tiles + p.subs - 1) / p.subs, 1);
   return r;
 }
 
+// The tiles of a block of rows at positions p_lo .. p_hi: the first `sinks`
+// tiles, then lo, lo + 1, ...; n in all.
+struct TileList {
+  int32_t sinks, lo, n;
+  int32_t lo_key;  // first key of the windows
+  __device__ __forceinline__ int32_t tile(int32_t i) const { return i < sinks ? i : lo + (i - sinks); }
+};
+
+template <int TW>
+__device__ __forceinline__ TileList visible_tiles(const AttendParams& p, int32_t p_lo, int32_t p_hi) {
+  const KeyList k = visible_keys(p, p_lo, p_hi);
+  TileList r;
+  r.lo_key = k.lo;
+  r.lo = k.lo / TW;
+  r.sinks = min((k.sinks + TW - 1) / TW, r.lo);
+  r.n = p_hi < 0 ? 0 : r.sinks + p_hi / TW - r.lo + 1;
+  return r;
+}
+
+template <int TW>
 __device__ __forceinline__ int64_t seq_units(const SplitParams& p, int32_t b, bool record) {
-  const SplitGeom g = split_geom(p, attend_seq(p.a, b, record));
+  const SplitGeom g = split_geom<TW>(p, attend_seq(p.a, b, record));
   return static_cast<int64_t>(g.blocks) * p.hgroups * (p.split ? g.steps : 1);
 }
 
@@ -136,6 +158,12 @@ __device__ __forceinline__ void ld_own(uint32_t (&w)[BYTES / 4], uint32_t addr) 
 __device__ __forceinline__ uint32_t ld_shared_u8(uint32_t addr) {
   uint32_t r;
   asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(addr) : "memory");
+  return r;
+}
+
+__device__ __forceinline__ uint32_t ld_shared_u16(uint32_t addr) {
+  uint16_t r;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(r) : "r"(addr) : "memory");
   return r;
 }
 
@@ -277,7 +305,7 @@ __global__ void __launch_bounds__(32 * kSplitWarps, (kSplitCtas<DP, NB>))
   const int32_t b0 = min(static_cast<int32_t>(threadIdx.x) * per_thread, a.num_seqs);
   const int32_t b1 = min(b0 + per_thread, a.num_seqs);
   int64_t mine = 0;
-  for (int32_t b = b0; b < b1; ++b) mine += seq_units(p, b, blockIdx.x == 0);
+  for (int32_t b = b0; b < b1; ++b) mine += seq_units<L::TW>(p, b, blockIdx.x == 0);
   int64_t incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -301,7 +329,7 @@ __global__ void __launch_bounds__(32 * kSplitWarps, (kSplitCtas<DP, NB>))
     int64_t base = excl;
     int32_t b = b0;
     for (;; ++b) {
-      const int64_t n = seq_units(p, b, false);
+      const int64_t n = seq_units<L::TW>(p, b, false);
       if (pos < base + n) break;
       base += n;
     }
@@ -312,7 +340,7 @@ __global__ void __launch_bounds__(32 * kSplitWarps, (kSplitCtas<DP, NB>))
     int64_t base = excl;
     for (int32_t b = b0; b < b1; ++b) {
       p.meta[b] = base;
-      base += seq_units(p, b, false);
+      base += seq_units<L::TW>(p, b, false);
     }
     if (threadIdx.x == 0) p.meta[a.num_seqs] = per;
   }
@@ -326,10 +354,17 @@ __global__ void __launch_bounds__(32 * kSplitWarps, (kSplitCtas<DP, NB>))
   const float kscale = a.scale_log2 * tensor_scale(a.k_scale);
   const float vscale = tensor_scale(a.v_scale);
   const uint32_t row_bytes = static_cast<uint32_t>(a.head_dim) * L::kBits / 8;
+  // bytes of the lane's i-th K or V piece: less than a whole one behind head_dim
+  auto kbytes = [&](int i) -> uint32_t {
+    return static_cast<uint32_t>(min(max(static_cast<int32_t>(row_bytes) - static_cast<int32_t>(t + 4 * i) * L::KC, 0), L::KC));
+  };
+  auto vbytes = [&](int i) -> uint32_t {
+    return static_cast<uint32_t>(min(max(static_cast<int32_t>(row_bytes) - static_cast<int32_t>(g + 8 * i) * L::VC, 0), L::VC));
+  };
 
   while (pos < end && b < a.num_seqs) {
     const AttendSeq seq = attend_seq(a, b, false);
-    const SplitGeom geom = split_geom(p, seq);
+    const SplitGeom geom = split_geom<TW>(p, seq);
     const int32_t unit = p.split ? geom.steps : 1;
     const int64_t local = pos - base;
     if (local >= static_cast<int64_t>(geom.blocks) * p.hgroups * unit) {
@@ -350,8 +385,8 @@ __global__ void __launch_bounds__(32 * kSplitWarps, (kSplitCtas<DP, NB>))
     const int32_t p_first = seq.len - seq.nq;  // position of the sequence's first query
     const int32_t q_lo = static_cast<int32_t>(a.group.quot(static_cast<uint32_t>(row0)));
     const int32_t q_hi = static_cast<int32_t>(a.group.quot(static_cast<uint32_t>(row0 + nrows - 1)));
-    const KeyList keys = visible_keys(a, p_first + q_lo, p_first + q_hi);
-    const bool many_pos = q_lo != q_hi;  // rows at different positions: the list is their union
+    const int32_t p_lo = p_first + q_lo, p_hi = p_first + q_hi;
+    const TileList list = visible_tiles<TW>(a, p_lo, p_hi);
 
     // -- queries: lane (g, t) holds the pairs of row g that K's pieces t, t + 4, .. meet -----
     uint32_t qf[NB][QP];
@@ -414,58 +449,80 @@ __global__ void __launch_bounds__(32 * kSplitWarps, (kSplitCtas<DP, NB>))
     const int32_t* table = a.table + static_cast<int64_t>(b) * a.table_stride;
     const uint8_t* kbase = a.k + kvh * a.k_head;
     const uint8_t* vbase = a.v + kvh * a.v_head;
+    // where the lane's first K row (g) and V row (2t) of 16 keys begin, less the block's own offset
+    const uint8_t* klane = kbase + g * a.k_slot + t * L::KC;
+    const uint8_t* vlane = vbase + 2 * t * a.v_slot + g * L::VC;
     bool bad = false;  // a page id out of range was met
-    // a lane's key of the tile that is copied next: page id (-1: none) and offset in the page
-    auto lookup = [&](int32_t tile, int32_t* id, uint32_t* off) {
-      const int32_t i = tile * p.tile + sub * TW + static_cast<int32_t>(lane);
+    // a lane's key of step i's tile: page id (-1: no row needs the key) and offset in the page
+    auto lookup = [&](int32_t step, int32_t* id, uint32_t* off) {
+      const int32_t i = step * p.subs + sub;
+      const int32_t j = list.tile(i) * TW + static_cast<int32_t>(lane);
       *id = -1;
       *off = 0;
-      if (lane < TW && tile < step1 && i < keys.n) {
-        const uint32_t j = static_cast<uint32_t>(keys.key(i));
-        const uint32_t pg = a.page.quot(j);
-        *off = j - pg * a.page.d;
-        *id = __ldg(table + pg);
+      if (lane < TW && step < step1 && i < list.n && j <= p_hi && (j >= list.lo_key || j < a.sinks)) {
+        const uint32_t pg = a.page.quot(static_cast<uint32_t>(j));
+        *off = static_cast<uint32_t>(j) - pg * a.page.d;
+        const int32_t x = __ldg(table + pg);
+        *id = x < 0 ? -2 : x;
       }
     };
-    auto checked = [&](int32_t id) {
-      if (id >= a.num_pages || id < -1) {
-        bad = true;
-        record_oob(a.err, static_cast<uint64_t>(b));
-        return -1;
-      }
-      return id;
-    };
-    int32_t cur_id, next_id;
-    uint32_t cur_off, next_off;
+    int32_t cur_id = -1, next_id;
+    uint32_t cur_off = 0, next_off;
+    bool cur_all = false;     // every key of the tile is wanted, and each 16 of them share a page
     lookup(step0, &next_id, &next_off);
-    int32_t tile_in = step0;  // tile whose units are copied next
+    int32_t step_in = step0;  // step whose units are copied next
     uint32_t slot_in = 0;     // and the ring slot
-    // K rows of tile `tile_in` (kv 0) or its V rows (kv 1)
+    // the K rows of step `step_in` (kv 0) or its V rows (kv 1)
     auto copy_unit = [&](int kv) {
       if (kv == 0) {
-        // an unused table entry may hold anything; -1 from lookup() is "no key"
         cur_id = next_id;
         cur_off = next_off;
-        const bool real = lane < TW && tile_in < step1 && tile_in * p.tile + sub * TW + static_cast<int32_t>(lane) < keys.n;
-        cur_id = real ? (cur_id < 0 || cur_id >= a.num_pages ? checked(cur_id < 0 ? -2 : cur_id) : cur_id) : -1;
-        lookup(tile_in + 1, &next_id, &next_off);
+        if (cur_id >= a.num_pages || cur_id == -2) {
+          bad = true;
+          record_oob(a.err, static_cast<uint64_t>(b));
+          cur_id = -1;
+        }
+        cur_all = p.whole_blocks && __all_sync(0xFFFFFFFFu, lane >= TW || cur_id >= 0);
+        lookup(step_in + 1, &next_id, &next_off);
       }
-      if (tile_in < step1) {
+      if (step_in < step1) {
         const uint32_t unit_at = ring + slot_in * L::kUnit;
-        constexpr int kRows = 2 * MB;  // K rows of a lane: g, g + 8 of each 16
-        if (kv == 0) {
+        const uint32_t kat = unit_at + lane * L::KC, vat = unit_at + lane * L::VC;
+        if (cur_all) {
 #pragma unroll
-          for (int r = 0; r < kRows; ++r) {
-            const uint32_t tok = 8u * r + g;
-            const int32_t id = __shfl_sync(0xFFFFFFFFu, cur_id, tok);
-            const uint32_t off = __shfl_sync(0xFFFFFFFFu, cur_off, tok);
-            const uint8_t* src = id < 0 ? kbase : kbase + id * a.k_page + off * a.k_slot;
-            const int32_t have = id < 0 ? 0 : static_cast<int32_t>(row_bytes);
+          for (int mb = 0; mb < MB; ++mb) {
+            const int32_t id = __shfl_sync(0xFFFFFFFFu, cur_id, 16 * mb);
+            const uint32_t off = __shfl_sync(0xFFFFFFFFu, cur_off, 16 * mb);
+            if (kv == 0) {
+              const uint8_t* src = klane + id * a.k_page + off * a.k_slot;
+#pragma unroll
+              for (int rh = 0; rh < 2; ++rh) {
+#pragma unroll
+                for (int i = 0; i < L::KN; ++i)
+                  copy_async<L::KC>(kat + ((2 * mb + rh) * L::KN + i) * 32 * L::KC, src + 4 * i * L::KC, kbytes(i));
+                src += 8 * a.k_slot;
+              }
+            } else {
+              const uint8_t* src = vlane + id * a.v_page + off * a.v_slot;
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+#pragma unroll
+                for (int i = 0; i < L::VN; ++i)
+                  copy_async<L::VC>(vat + ((4 * mb + r) * L::VN + i) * 32 * L::VC, src + 8 * i * L::VC, vbytes(i));
+                src += (r & 1) ? 7 * a.v_slot : a.v_slot;
+              }
+            }
+          }
+        } else if (kv == 0) {
+#pragma unroll
+          for (int r = 0; r < 2 * MB; ++r) {
+            const int32_t id = __shfl_sync(0xFFFFFFFFu, cur_id, 8 * r + g);
+            const uint32_t off = __shfl_sync(0xFFFFFFFFu, cur_off, 8 * r + g);
+            const uint8_t* src = kbase + t * L::KC + (id < 0 ? 0 : id * a.k_page + off * a.k_slot);
 #pragma unroll
             for (int i = 0; i < L::KN; ++i) {
-              const int32_t at = static_cast<int32_t>(t + 4 * i) * L::KC;
-              copy_async<L::KC>(unit_at + ((r * L::KN + i) * 32 + lane) * L::KC, have > at ? src + at : kbase,
-                                static_cast<uint32_t>(min(max(have - at, 0), L::KC)));
+              const uint32_t n = id < 0 ? 0u : kbytes(i);
+              copy_async<L::KC>(kat + (r * L::KN + i) * 32 * L::KC, n ? src + 4 * i * L::KC : kbase, n);
             }
           }
         } else {
@@ -474,34 +531,38 @@ __global__ void __launch_bounds__(32 * kSplitWarps, (kSplitCtas<DP, NB>))
             const uint32_t tok = 16u * (r / 4) + 2u * t + (r & 1) + 8u * ((r >> 1) & 1);
             const int32_t id = __shfl_sync(0xFFFFFFFFu, cur_id, tok);
             const uint32_t off = __shfl_sync(0xFFFFFFFFu, cur_off, tok);
-            const uint8_t* src = id < 0 ? vbase : vbase + id * a.v_page + off * a.v_slot;
-            const int32_t have = id < 0 ? 0 : static_cast<int32_t>(row_bytes);
+            const uint8_t* src = vbase + g * L::VC + (id < 0 ? 0 : id * a.v_page + off * a.v_slot);
 #pragma unroll
             for (int i = 0; i < L::VN; ++i) {
-              const int32_t at = static_cast<int32_t>(g + 8 * i) * L::VC;
-              copy_async<L::VC>(unit_at + ((r * L::VN + i) * 32 + lane) * L::VC, have > at ? src + at : vbase,
-                                static_cast<uint32_t>(min(max(have - at, 0), L::VC)));
+              const uint32_t n = id < 0 ? 0u : vbytes(i);
+              copy_async<L::VC>(vat + (r * L::VN + i) * 32 * L::VC, n ? src + 8 * i * L::VC : vbase, n);
             }
           }
         }
         if constexpr (FMT == KV_CACHE_E2M1) {
           // lane = key: the aligned words around its row's scales, and where in them the row begins
           const uint8_t* sbase = kv == 0 ? a.k_sc + kvh * a.ks_head : a.v_sc + kvh * a.vs_head;
-          const uint8_t* src = cur_id < 0 ? sbase
-                                          : sbase + (kv == 0 ? cur_id * a.ks_page + cur_off * a.ks_slot
-                                                             : cur_id * a.vs_page + cur_off * a.vs_slot);
-          const uint32_t mis = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(src) & 3u);
+          const uint8_t* src = sbase + (cur_id < 0 ? 0
+                                        : kv == 0 ? cur_id * a.ks_page + cur_off * a.ks_slot
+                                                  : cur_id * a.vs_page + cur_off * a.vs_slot);
           const uint32_t at = unit_at + TW * L::kRow + lane * (L::kScaleWords * 4);
-          const uint32_t need = cur_id < 0 ? 0u : mis + row_bytes / 8;  // a scale per 8 code bytes
+          uint32_t need = cur_id < 0 ? 0u : row_bytes / 8;  // a scale per 8 code bytes
+          if (p.sc_aligned) {
 #pragma unroll
-          for (int i = 0; i < L::kScaleWords - 1; ++i)
-            copy_async<4>(at + 4 * i, 4u * i < need ? src - mis + 4 * i : sbase - (reinterpret_cast<uintptr_t>(sbase) & 3u),
-                          4u * i < need ? 4u : 0u);
-          asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + 4 * (L::kScaleWords - 1)), "r"(mis) : "memory");
+            for (int i = 0; i < L::kScaleWords - 2; ++i)
+              if (4u * i < row_bytes / 8) copy_async<4>(at + 4 * i, src + 4 * i, 4u * i < need ? 4u : 0u);
+          } else {
+            const uint32_t mis = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(src) & 3u);
+            need += cur_id < 0 ? 0u : mis;
+#pragma unroll
+            for (int i = 0; i < L::kScaleWords - 1; ++i)
+              copy_async<4>(at + 4 * i, 4u * i < need ? src - mis + 4 * i : src - mis, 4u * i < need ? 4u : 0u);
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + 4 * (L::kScaleWords - 1)), "r"(mis) : "memory");
+          }
         }
       }
       commit_async();
-      if (kv == 1) ++tile_in;
+      if (kv == 1) ++step_in;
       slot_in = slot_in + 1 == NU ? 0u : slot_in + 1;
     };
 #pragma unroll
@@ -509,7 +570,7 @@ __global__ void __launch_bounds__(32 * kSplitWarps, (kSplitCtas<DP, NB>))
 
     uint32_t slot = 0;
     auto next_slot = [&] { slot = slot + 1 == NU ? 0u : slot + 1; };
-    for (int32_t tile = step0; tile < step1; ++tile) {
+    for (int32_t step = step0; step < step1; ++step) {
       // S^T = K Q^T
       wait_async<NU - 2>();
       __syncwarp();
@@ -534,9 +595,14 @@ __global__ void __launch_bounds__(32 * kSplitWarps, (kSplitCtas<DP, NB>))
             ld_own<L::KC>(w, kat + (((mb * 2 + rh) * L::KN + i) * 32 + lane) * L::KC);
             if constexpr (FMT == KV_CACHE_E2M1) {
               const uint32_t srow = kat + TW * L::kRow + (mb * 16 + rh * 8 + g) * (L::kScaleWords * 4);
-              const uint32_t sat = srow + ld_shared_u32(srow + 4 * (L::kScaleWords - 1)) + (t + 4 * i) * (L::KD / kFp4Block);
-              sc[rh] = ld_shared_u8(sat);
-              if constexpr (L::KD > kFp4Block) sc[rh] |= ld_shared_u8(sat + 1) << 8;
+              uint32_t sat = srow + (t + 4 * i) * (L::KD / kFp4Block);
+              if (!p.sc_aligned) sat += ld_shared_u32(srow + 4 * (L::kScaleWords - 1));
+              if (L::KD > kFp4Block && p.sc_aligned) {
+                sc[rh] = ld_shared_u16(sat);
+              } else {
+                sc[rh] = ld_shared_u8(sat);
+                if constexpr (L::KD > kFp4Block) sc[rh] |= ld_shared_u8(sat + 1) << 8;
+              }
             }
             k_pairs<FMT, DP>(f[rh], w, sc[rh]);
           }
@@ -551,8 +617,11 @@ __global__ void __launch_bounds__(32 * kSplitWarps, (kSplitCtas<DP, NB>))
       next_slot();
 
       // mask: s[..][0], [1]: key g, rows 2t, 2t + 1; [2], [3]: key g + 8
-      const int32_t first = tile * p.tile + sub * TW;
-      if (many_pos || first + TW > keys.n || __any_sync(0xFFFFFFFFu, bad)) {
+      const int32_t li = step * p.subs + sub, j0 = list.tile(li) * TW;
+      const bool all_seen = li < list.n && j0 + TW - 1 <= p_lo &&
+                            (a.window == 0 || static_cast<int64_t>(j0) > static_cast<int64_t>(p_hi) - a.window || j0 + TW - 1 < a.sinks);
+      const bool any_bad = __any_sync(0xFFFFFFFFu, bad);
+      if (!all_seen || any_bad) {
         int32_t pos_of[NB][2];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
@@ -563,10 +632,9 @@ __global__ void __launch_bounds__(32 * kSplitWarps, (kSplitCtas<DP, NB>))
         for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
           for (int rh = 0; rh < 2; ++rh) {
-            const int32_t i = first + mb * 16 + rh * 8 + static_cast<int32_t>(g);
-            bool have = i < keys.n;
-            const int32_t j = have ? keys.key(i) : 0;
-            if (have) {
+            const int32_t j = j0 + mb * 16 + rh * 8 + static_cast<int32_t>(g);
+            bool have = li < list.n && j <= p_hi;
+            if (have && any_bad) {
               const int32_t id = __ldg(table + a.page.quot(static_cast<uint32_t>(j)));
               have = id >= 0 && id < a.num_pages;
             }
@@ -644,7 +712,8 @@ __global__ void __launch_bounds__(32 * kSplitWarps, (kSplitCtas<DP, NB>))
           for (int r = 0; r < 4; ++r) {
             const uint32_t tok = 16u * mb + 2u * t + (r & 1) + 8u * (r >> 1);
             const uint32_t at = vat + TW * L::kRow + tok * (L::kScaleWords * 4);
-            srow[r] = at + ld_shared_u32(at + 4 * (L::kScaleWords - 1));
+            srow[r] = at;
+            if (!p.sc_aligned) srow[r] += ld_shared_u32(at + 4 * (L::kScaleWords - 1));
           }
         }
 #pragma unroll
@@ -836,7 +905,7 @@ __global__ void __launch_bounds__(256) kv_attend_join(const __grid_constant__ Sp
     }
     const AttendSeq s = attend_seq(a, b, false);
     if (tok >= s.q0 && tok < s.q0 + s.nq) {
-      const SplitGeom geom = split_geom(p, s);
+      const SplitGeom geom = split_geom<Layout<FMT, DP>::TW>(p, s);
       const int32_t G = static_cast<int32_t>(a.group.d), kvh = static_cast<int32_t>(a.group.quot(static_cast<uint32_t>(h)));
       const int32_t row = (tok - s.q0) * G + (h - kvh * G);
       const int32_t rb = row / p.rows, hg = kvh / p.hw;
@@ -951,7 +1020,6 @@ kv_status launch_split(SplitParams p, void* work, int64_t work_bytes, int64_t ma
     if (a.kv_heads % h == 0) p.hw = h;
   p.subs = kSplitWarps / p.hw;
   p.hgroups = a.kv_heads / p.hw;
-  p.tile = L::TW * p.subs;
   p.min_steps = 4;
 
   int sms = 0;
@@ -973,7 +1041,7 @@ kv_status launch_split(SplitParams p, void* work, int64_t work_bytes, int64_t ma
   } else {
     shares = 0;
   }
-  p.split = max_keys > static_cast<int64_t>(p.min_steps) * p.tile && 2 * shares >= full;
+  p.split = max_keys > static_cast<int64_t>(p.min_steps) * p.subs * L::TW && 2 * shares >= full;
   if (p.split) {
     p.shares = static_cast<int32_t>(shares);
     p.meta = static_cast<int64_t*>(work);
