@@ -96,7 +96,7 @@ extern "C" kv_status kv_attend(const void* q, void* out, float* lse, const void*
                           u64(s->vc_page) | u64(s->vc_slot) | u64(s->vc_head);
   if ((q_bits & 1u) != 0 || (format == KV_CACHE_SRC && (c_bits & 1u) != 0)) return KV_ERR_UNSUPPORTED;
   if (head_dim > 1024 || (format == KV_CACHE_E2M1 && head_dim % kFp4Block != 0)) return KV_ERR_UNSUPPORTED;
-  if (num_q_tokens >= INT_MAX || page_size >= INT_MAX || num_pages >= INT_MAX) return KV_ERR_UNSUPPORTED;
+  if (num_q_tokens >= (1 << 30) || page_size >= INT_MAX || num_pages >= INT_MAX) return KV_ERR_UNSUPPORTED;
   {
     const void* in[6] = {q, out, page_table, seq_lens, k_cache, v_cache};
     bool on_device = true;
@@ -137,19 +137,26 @@ extern "C" kv_status kv_attend(const void* q, void* out, float* lse, const void*
   p.kv_heads = num_heads;
   p.head_dim = head_dim;
   p.max_len = static_cast<int32_t>(table_width > (int64_t{1} << 30) / page_size ? int64_t{1} << 30 : table_width * page_size);
-  p.window = window;
-  p.sinks = sinks;
+  p.window = static_cast<int32_t>(window < (1 << 30) ? window : 1 << 30);
+  p.sinks = static_cast<int32_t>(sinks < (1 << 30) ? sinks : 1 << 30);
   p.scale_log2 = sm_scale * 1.4426950408889634f;
   p.bf16 = dtype == KV_SRC_BF16;
   p.err = d_err;
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
-  if (head_dim % 16 == 0 && head_dim <= 256 && ((q_bits | c_bits) & 15u) == 0) {
+  auto fits = [](int64_t x) { return x > INT_MIN && x < INT_MAX; };
+  bool near = fits(s->kc_page) && fits(s->kc_slot) && fits(s->vc_page) && fits(s->vc_slot);
+  if (format == KV_CACHE_E2M1)
+    near = near && fits(scales->k_page) && fits(scales->k_slot) && fits(scales->v_page) && fits(scales->v_slot);
+  if (head_dim % 16 == 0 && head_dim <= 256 && ((q_bits | c_bits) & 15u) == 0 && near) {
     SplitParams sp = {};
     sp.a = p;
     sp.whole_blocks = page_size % 16 == 0;
-    if (format == KV_CACHE_E2M1)
-      sp.sc_aligned = ((u64(scales->k) | u64(scales->v) | u64(scales->k_page) | u64(scales->k_slot) | u64(scales->k_head) |
-                        u64(scales->v_page) | u64(scales->v_slot) | u64(scales->v_head)) & 3u) == 0;
+    sp.k_page = static_cast<int32_t>(s->kc_page); sp.k_slot = static_cast<int32_t>(s->kc_slot);
+    sp.v_page = static_cast<int32_t>(s->vc_page); sp.v_slot = static_cast<int32_t>(s->vc_slot);
+    if (format == KV_CACHE_E2M1) {
+      sp.ks_page = static_cast<int32_t>(scales->k_page); sp.ks_slot = static_cast<int32_t>(scales->k_slot);
+      sp.vs_page = static_cast<int32_t>(scales->v_page); sp.vs_slot = static_cast<int32_t>(scales->v_slot);
+    }
     // query rows of a sequence and KV head, on average: up to 8 take one mma column block, more two
     const int64_t rows = (num_q_tokens + num_seqs - 1) / num_seqs * p.group.d;
     const bool wide = rows > 8;

@@ -31,7 +31,7 @@ struct AttendParams {
   FastDiv group;               // by the query heads of a KV head
   int32_t num_pages, num_seqs, num_q, q_heads, kv_heads, head_dim;
   int32_t max_len;             // table_width * page_size (at most 2^31 - 1)
-  int64_t window, sinks;       // window 0: none
+  int32_t window, sinks;       // window 0: none; both at most 2^30, as lengths are
   float scale_log2;            // sm_scale * log2(e)
   int32_t bf16;
   kv_error_record* err;
@@ -69,17 +69,15 @@ struct KeyList {
 
 __device__ __forceinline__ KeyList visible_keys(const AttendParams& p, int32_t p_lo, int32_t p_hi) {
   KeyList r;
-  const int64_t lo = p.window > 0 ? static_cast<int64_t>(p_lo) - p.window + 1 : 0;
-  r.lo = lo > 0 ? static_cast<int32_t>(lo) : 0;
-  r.sinks = static_cast<int32_t>(p.sinks < r.lo ? p.sinks : r.lo);
+  r.lo = p.window > 0 ? max(p_lo - p.window + 1, 0) : 0;
+  r.sinks = min(p.sinks, r.lo);
   r.n = p_hi < 0 ? 0 : r.sinks + (p_hi - r.lo + 1);
   return r;
 }
 
 // Whether a query at position pos sees key j (0 <= j).
 __device__ __forceinline__ bool sees(const AttendParams& p, int32_t pos, int32_t j) {
-  return j <= pos && (p.window == 0 || static_cast<int64_t>(j) > static_cast<int64_t>(pos) - p.window ||
-                      j < p.sinks);
+  return j <= pos && (p.window == 0 || j > pos - p.window || j < p.sinks);
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {

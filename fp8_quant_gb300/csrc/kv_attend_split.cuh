@@ -52,7 +52,8 @@ struct SplitParams {
   int32_t hgroups;        // kv_heads / hw
   int32_t rows;           // query rows per item
   int32_t whole_blocks;   // page_size is a multiple of 16: 16 aligned keys share a page
-  int32_t sc_aligned;     // e2m1: every row of block scales begins on a word
+  int32_t k_page, k_slot, v_page, v_slot;      // byte strides, in 32 bits
+  int32_t ks_page, ks_slot, vs_page, vs_slot;  // of the block scales
   int32_t split;          // 0: an item is one CTA's
   int32_t min_steps;      // a share is at least this long
   int32_t shares;         // CTAs that may take a share
@@ -78,8 +79,8 @@ __device__ __forceinline__ SplitGeom split_geom(const SplitParams& p, const Atte
   if (p.a.window > 0 && p.a.window < s.len) {
     // a block of rows spans at most `span` positions, and its windows window + span - 1 keys
     const int32_t span = min(s.nq, (p.rows - 1) / static_cast<int32_t>(p.a.group.d) + 2);
-    const int64_t sinks = (min(p.a.sinks, static_cast<int64_t>(s.len)) + TW - 1) / TW;
-    tiles = static_cast<int32_t>(min(static_cast<int64_t>(tiles), sinks + (p.a.window + span + TW - 3) / TW + 1));
+    const int32_t sinks = (min(p.a.sinks, s.len) + TW - 1) / TW;
+    tiles = min(tiles, sinks + (p.a.window + span + TW - 3) / TW + 1);
   }
   r.steps = max((tiles + p.subs - 1) / p.subs, 1);
   return r;
@@ -126,9 +127,15 @@ struct Layout {
   static constexpr int VD = VC * 8 / kBits;
   static constexpr int TW = (FMT == KV_CACHE_SRC && DP >= 128) ? 16 : 32;  // keys of a warp's tile
   static constexpr int MB = TW / 16;
-  static constexpr int kScaleWords = FMT == KV_CACHE_E2M1 ? DP / 64 + 2 : 0;  // words covering a row's scales, and their misalignment
-  static constexpr int kUnit = TW * kRow + TW * kScaleWords * 4;
+  // e2m1: room for a row's scales: the words around them and a word for where in them they begin;
+  // 16 or 24 bytes spread eight rows over the banks
+  static constexpr int kScaleRow = FMT == KV_CACHE_E2M1 ? (DP <= 128 ? 16 : 24) : 0;
+  static constexpr int kUnit = TW * (kRow + kScaleRow);
 };
+
+// A byte offset in 64 bits from 32-bit factors.
+__device__ __forceinline__ int64_t wide(int32_t n, int32_t stride) { return static_cast<int64_t>(n) * stride; }
+__device__ __forceinline__ int64_t wide(uint32_t n, int32_t stride) { return wide(static_cast<int32_t>(n), stride); }
 
 template <int BYTES>
 __device__ __forceinline__ void copy_async(uint32_t dst, const uint8_t* src, uint32_t bytes) {
@@ -279,8 +286,11 @@ constexpr int kSplitFit = (220 * 1024 / kSplitCtas<DP, NB> - 2048) / (kSplitWarp
 template <int FMT, int DP, int NB>
 constexpr int kSplitUnits = kSplitFit<FMT, DP, NB> > 6 ? 6 : kSplitFit<FMT, DP, NB>;
 
-// kBF16: the products' type (e4m3 and e2m1 caches: fp16).
-template <int FMT, int DP, int NB, bool kBF16>
+// kBF16: the products' type (e4m3 and e2m1 caches: fp16).  kExact: head_dim is
+// DP and a row's block scales begin at a multiple of their size, so that every
+// piece is whole; otherwise pieces behind head_dim are cut or zero, and scales
+// come by the words around them.
+template <int FMT, int DP, int NB, bool kBF16, bool kExact>
 __global__ void __launch_bounds__(32 * kSplitWarps, (kSplitCtas<DP, NB>))
     kv_attend_split(const __grid_constant__ SplitParams p) {
   using L = Layout<FMT, DP>;
@@ -356,9 +366,11 @@ __global__ void __launch_bounds__(32 * kSplitWarps, (kSplitCtas<DP, NB>))
   const uint32_t row_bytes = static_cast<uint32_t>(a.head_dim) * L::kBits / 8;
   // bytes of the lane's i-th K or V piece: less than a whole one behind head_dim
   auto kbytes = [&](int i) -> uint32_t {
+    if (kExact) return L::KC;
     return static_cast<uint32_t>(min(max(static_cast<int32_t>(row_bytes) - static_cast<int32_t>(t + 4 * i) * L::KC, 0), L::KC));
   };
   auto vbytes = [&](int i) -> uint32_t {
+    if (kExact) return L::VC;
     return static_cast<uint32_t>(min(max(static_cast<int32_t>(row_bytes) - static_cast<int32_t>(g + 8 * i) * L::VC, 0), L::VC));
   };
 
@@ -450,8 +462,8 @@ __global__ void __launch_bounds__(32 * kSplitWarps, (kSplitCtas<DP, NB>))
     const uint8_t* kbase = a.k + kvh * a.k_head;
     const uint8_t* vbase = a.v + kvh * a.v_head;
     // where the lane's first K row (g) and V row (2t) of 16 keys begin, less the block's own offset
-    const uint8_t* klane = kbase + g * a.k_slot + t * L::KC;
-    const uint8_t* vlane = vbase + 2 * t * a.v_slot + g * L::VC;
+    const uint8_t* klane = kbase + wide(g, p.k_slot) + t * L::KC;
+    const uint8_t* vlane = vbase + wide(2 * t, p.v_slot) + g * L::VC;
     bool bad = false;  // a page id out of range was met
     // a lane's key of step i's tile: page id (-1: no row needs the key) and offset in the page
     auto lookup = [&](int32_t step, int32_t* id, uint32_t* off) {
@@ -494,22 +506,22 @@ __global__ void __launch_bounds__(32 * kSplitWarps, (kSplitCtas<DP, NB>))
             const int32_t id = __shfl_sync(0xFFFFFFFFu, cur_id, 16 * mb);
             const uint32_t off = __shfl_sync(0xFFFFFFFFu, cur_off, 16 * mb);
             if (kv == 0) {
-              const uint8_t* src = klane + id * a.k_page + off * a.k_slot;
+              const uint8_t* src = klane + wide(id, p.k_page) + wide(off, p.k_slot);
 #pragma unroll
               for (int rh = 0; rh < 2; ++rh) {
 #pragma unroll
                 for (int i = 0; i < L::KN; ++i)
                   copy_async<L::KC>(kat + ((2 * mb + rh) * L::KN + i) * 32 * L::KC, src + 4 * i * L::KC, kbytes(i));
-                src += 8 * a.k_slot;
+                src += 8 * p.k_slot;
               }
             } else {
-              const uint8_t* src = vlane + id * a.v_page + off * a.v_slot;
+              const uint8_t* src = vlane + wide(id, p.v_page) + wide(off, p.v_slot);
 #pragma unroll
               for (int r = 0; r < 4; ++r) {
 #pragma unroll
                 for (int i = 0; i < L::VN; ++i)
                   copy_async<L::VC>(vat + ((4 * mb + r) * L::VN + i) * 32 * L::VC, src + 8 * i * L::VC, vbytes(i));
-                src += (r & 1) ? 7 * a.v_slot : a.v_slot;
+                src += (r & 1) ? 7 * p.v_slot : p.v_slot;
               }
             }
           }
@@ -518,7 +530,7 @@ __global__ void __launch_bounds__(32 * kSplitWarps, (kSplitCtas<DP, NB>))
           for (int r = 0; r < 2 * MB; ++r) {
             const int32_t id = __shfl_sync(0xFFFFFFFFu, cur_id, 8 * r + g);
             const uint32_t off = __shfl_sync(0xFFFFFFFFu, cur_off, 8 * r + g);
-            const uint8_t* src = kbase + t * L::KC + (id < 0 ? 0 : id * a.k_page + off * a.k_slot);
+            const uint8_t* src = kbase + t * L::KC + (id < 0 ? 0 : wide(id, p.k_page) + wide(off, p.k_slot));
 #pragma unroll
             for (int i = 0; i < L::KN; ++i) {
               const uint32_t n = id < 0 ? 0u : kbytes(i);
@@ -531,7 +543,7 @@ __global__ void __launch_bounds__(32 * kSplitWarps, (kSplitCtas<DP, NB>))
             const uint32_t tok = 16u * (r / 4) + 2u * t + (r & 1) + 8u * ((r >> 1) & 1);
             const int32_t id = __shfl_sync(0xFFFFFFFFu, cur_id, tok);
             const uint32_t off = __shfl_sync(0xFFFFFFFFu, cur_off, tok);
-            const uint8_t* src = vbase + g * L::VC + (id < 0 ? 0 : id * a.v_page + off * a.v_slot);
+            const uint8_t* src = vbase + g * L::VC + (id < 0 ? 0 : wide(id, p.v_page) + wide(off, p.v_slot));
 #pragma unroll
             for (int i = 0; i < L::VN; ++i) {
               const uint32_t n = id < 0 ? 0u : vbytes(i);
@@ -543,21 +555,19 @@ __global__ void __launch_bounds__(32 * kSplitWarps, (kSplitCtas<DP, NB>))
           // lane = key: the aligned words around its row's scales, and where in them the row begins
           const uint8_t* sbase = kv == 0 ? a.k_sc + kvh * a.ks_head : a.v_sc + kvh * a.vs_head;
           const uint8_t* src = sbase + (cur_id < 0 ? 0
-                                        : kv == 0 ? cur_id * a.ks_page + cur_off * a.ks_slot
-                                                  : cur_id * a.vs_page + cur_off * a.vs_slot);
-          const uint32_t at = unit_at + TW * L::kRow + lane * (L::kScaleWords * 4);
+                                        : kv == 0 ? wide(cur_id, p.ks_page) + wide(cur_off, p.ks_slot)
+                                                  : wide(cur_id, p.vs_page) + wide(cur_off, p.vs_slot));
+          const uint32_t at = unit_at + TW * L::kRow + lane * L::kScaleRow;
           uint32_t need = cur_id < 0 ? 0u : row_bytes / 8;  // a scale per 8 code bytes
-          if (p.sc_aligned) {
-#pragma unroll
-            for (int i = 0; i < L::kScaleWords - 2; ++i)
-              if (4u * i < row_bytes / 8) copy_async<4>(at + 4 * i, src + 4 * i, 4u * i < need ? 4u : 0u);
+          if constexpr (kExact) {
+            copy_async<DP / 16>(at, src, cur_id < 0 ? 0u : DP / 16);
           } else {
             const uint32_t mis = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(src) & 3u);
             need += cur_id < 0 ? 0u : mis;
 #pragma unroll
-            for (int i = 0; i < L::kScaleWords - 1; ++i)
+            for (int i = 0; i < L::kScaleRow / 4 - 1; ++i)
               copy_async<4>(at + 4 * i, 4u * i < need ? src - mis + 4 * i : src - mis, 4u * i < need ? 4u : 0u);
-            asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + 4 * (L::kScaleWords - 1)), "r"(mis) : "memory");
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + L::kScaleRow - 4), "r"(mis) : "memory");
           }
         }
       }
@@ -594,10 +604,10 @@ __global__ void __launch_bounds__(32 * kSplitWarps, (kSplitCtas<DP, NB>))
             uint32_t w[L::KC / 4];
             ld_own<L::KC>(w, kat + (((mb * 2 + rh) * L::KN + i) * 32 + lane) * L::KC);
             if constexpr (FMT == KV_CACHE_E2M1) {
-              const uint32_t srow = kat + TW * L::kRow + (mb * 16 + rh * 8 + g) * (L::kScaleWords * 4);
+              const uint32_t srow = kat + TW * L::kRow + (mb * 16 + rh * 8 + g) * L::kScaleRow;
               uint32_t sat = srow + (t + 4 * i) * (L::KD / kFp4Block);
-              if (!p.sc_aligned) sat += ld_shared_u32(srow + 4 * (L::kScaleWords - 1));
-              if (L::KD > kFp4Block && p.sc_aligned) {
+              if (!kExact) sat += ld_shared_u32(srow + L::kScaleRow - 4);
+              if (L::KD > kFp4Block && kExact) {
                 sc[rh] = ld_shared_u16(sat);
               } else {
                 sc[rh] = ld_shared_u8(sat);
@@ -619,7 +629,7 @@ __global__ void __launch_bounds__(32 * kSplitWarps, (kSplitCtas<DP, NB>))
       // mask: s[..][0], [1]: key g, rows 2t, 2t + 1; [2], [3]: key g + 8
       const int32_t li = step * p.subs + sub, j0 = list.tile(li) * TW;
       const bool all_seen = li < list.n && j0 + TW - 1 <= p_lo &&
-                            (a.window == 0 || static_cast<int64_t>(j0) > static_cast<int64_t>(p_hi) - a.window || j0 + TW - 1 < a.sinks);
+                            (a.window == 0 || j0 > p_hi - a.window || j0 + TW - 1 < a.sinks);
       const bool any_bad = __any_sync(0xFFFFFFFFu, bad);
       if (!all_seen || any_bad) {
         int32_t pos_of[NB][2];
@@ -711,9 +721,9 @@ __global__ void __launch_bounds__(32 * kSplitWarps, (kSplitCtas<DP, NB>))
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const uint32_t tok = 16u * mb + 2u * t + (r & 1) + 8u * (r >> 1);
-            const uint32_t at = vat + TW * L::kRow + tok * (L::kScaleWords * 4);
+            const uint32_t at = vat + TW * L::kRow + tok * L::kScaleRow;
             srow[r] = at;
-            if (!p.sc_aligned) srow[r] += ld_shared_u32(at + 4 * (L::kScaleWords - 1));
+            if (!kExact) srow[r] += ld_shared_u32(at + L::kScaleRow - 4);
           }
         }
 #pragma unroll
@@ -1008,11 +1018,11 @@ struct SmemOptIn {
 };
 
 // Launches the split kernel (and the join) of one format and padded head dim.
-template <int FMT, int DP, int NB, bool kBF16>
+template <int FMT, int DP, int NB, bool kBF16, bool kExact>
 kv_status launch_split(SplitParams p, void* work, int64_t work_bytes, int64_t max_keys, cudaStream_t stream) {
   using L = Layout<FMT, DP>;
   constexpr int kSmem = kSplitWarps * kSplitUnits<FMT, DP, NB> * L::kUnit;
-  auto* kernel = kv_attend_split<FMT, DP, NB, kBF16>;
+  auto* kernel = kv_attend_split<FMT, DP, NB, kBF16, kExact>;
   const AttendParams& a = p.a;
   p.rows = 8 * NB;
   p.hw = 1;
@@ -1083,13 +1093,20 @@ template <int FMT, bool kBF16>
 kv_status launch_split_fmt(const SplitParams& p, bool wide, void* work, int64_t work_bytes, int64_t max_keys,
                            cudaStream_t stream) {
   const int d = p.a.head_dim;
+  bool exact = d == 64 || d == 128;
+  if (FMT == KV_CACHE_E2M1)
+    exact = exact && ((u64(p.a.k_sc) | u64(p.a.v_sc) | u64(p.a.ks_head) | u64(p.a.vs_head) | u64(int64_t{p.ks_page}) |
+                       u64(int64_t{p.ks_slot}) | u64(int64_t{p.vs_page}) | u64(int64_t{p.vs_slot})) &
+                      static_cast<uint64_t>(d / 16 - 1)) == 0;
+#define KV_SPLIT(DP, NB, EX) launch_split<FMT, DP, NB, kBF16, EX>(p, work, work_bytes, max_keys, stream)
   if (d <= 64)
-    return wide ? launch_split<FMT, 64, 2, kBF16>(p, work, work_bytes, max_keys, stream)
-                : launch_split<FMT, 64, 1, kBF16>(p, work, work_bytes, max_keys, stream);
+    return exact ? (wide ? KV_SPLIT(64, 2, true) : KV_SPLIT(64, 1, true))
+                 : (wide ? KV_SPLIT(64, 2, false) : KV_SPLIT(64, 1, false));
   if (d <= 128)
-    return wide ? launch_split<FMT, 128, 2, kBF16>(p, work, work_bytes, max_keys, stream)
-                : launch_split<FMT, 128, 1, kBF16>(p, work, work_bytes, max_keys, stream);
-  return launch_split<FMT, 256, 1, kBF16>(p, work, work_bytes, max_keys, stream);
+    return exact ? (wide ? KV_SPLIT(128, 2, true) : KV_SPLIT(128, 1, true))
+                 : (wide ? KV_SPLIT(128, 2, false) : KV_SPLIT(128, 1, false));
+  return KV_SPLIT(256, 1, false);
+#undef KV_SPLIT
 }
 
 // The formats' instantiations, a translation unit each.

@@ -548,7 +548,8 @@ typedef struct kv_attend_strides {
  *               never read.
  *   head_dim    1 .. 1024.  Contiguous dims throughout.  Head dims that are
  *               multiples of 16 up to 256, with 16-byte aligned bases and
- *               strides, take the tensor-core kernels; the rest a general one.
+ *               strides and page and slot strides below 2^31 bytes, take the
+ *               tensor-core kernels; the rest a general one.
  *   format, k_scale, v_scale, scales
  *               as kv_gather_fp4 for KV_CACHE_E2M1; forward scales per tensor
  *               (device scalars, NULL: 1) for KV_CACHE_E4M3FN; none for
