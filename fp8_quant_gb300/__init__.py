@@ -789,6 +789,7 @@ def kv_absmax_inv(k, v, *, fp8_max: float = 448.0, num_heads=None, head_dim=None
 
 CACHE_FORMATS = {None: 0, "e4m3fn": 1, "e2m1": 2}
 ATTEND_WORK_BYTES = 64 << 20  # KV_ATTEND_WORK_BYTES of the C header
+ATTEND_HEAD_BYTES = 256       # KV_ATTEND_HEAD_BYTES
 
 
 def _is_bf16(x) -> int:
@@ -984,8 +985,9 @@ def kv_attend(q, k_cache, v_cache, page_table, seq_lens, *, q_start=None, page_s
     ``v_scales``: as in :func:`kv_store_rope`; ``k_scale`` / ``v_scale``: forward tensor scales
     (1-element fp32 device tensors, None: 1). ``lse``: an fp32 [tokens, HQ] tensor for the
     logarithms of the rows' sums, or None. ``work``: a device tensor that lets long sequences be
-    split over the GPU (ATTEND_WORK_BYTES is always enough; contents do not matter; calls that
-    share one must not overlap; a new one per call if None). Sequences with a bad length or page
+    split over the GPU (ATTEND_WORK_BYTES is always enough; its first ATTEND_HEAD_BYTES are zero
+    before its first use, and every call leaves them zero; calls that share one must not overlap; a
+    new one per call if None). Sequences with a bad length or page
     id are counted in ``err``.
     """
     import torch
@@ -1027,6 +1029,7 @@ def kv_attend(q, k_cache, v_cache, page_table, seq_lens, *, q_start=None, page_s
     if work is None:
         with _on_stream(stream, q.device):
             work = torch.empty(ATTEND_WORK_BYTES, dtype=torch.uint8, device=q.device)
+            work[:ATTEND_HEAD_BYTES].zero_()
     rec = err if err is not None else _default_record(q.device)
     _check(raw.kv_attend(
         q.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),

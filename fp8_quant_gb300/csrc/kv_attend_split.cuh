@@ -29,11 +29,15 @@
 //  * weights multiply 16-bit caches as two 16-bit terms (p = hi + lo), so their
 //    rounding does not add to the output's; the mma pipe has room for the
 //    second product there.  For quantised caches they are fp16 (2^-11).
-//  * every CTA takes an equal, contiguous share of all (sequence, block of
-//    rows, head group, tile) steps, found by a scan over the lengths on the
-//    device, so ragged batches are balanced without the host knowing a length.
-//    A share that begins or ends inside an item leaves its sums in the
-//    workspace, and a second kernel joins them in the order of the keys.
+//  * all (sequence, block of rows, head group, tile) steps, counted by a scan
+//    over the lengths on the device, are cut into contiguous shares: one of
+//    80 % of an equal part for each CTA, the rest in shares of half the size and
+//    half again that CTAs take as they become free.  Ragged batches are
+//    balanced without the host knowing a length, and so are the SMs, whose
+//    share of the memory's bandwidth differs by a third (with equal shares the
+//    first SMs ended a 400 us call at 290 us).  A share that begins or ends
+//    inside an item leaves its sums in the workspace, and a second kernel joins
+//    them in the order of the keys, whoever computed them.
 //  * a row whose sum is 0 or whose output is not finite is done again by
 //    attend_row, which touches its visible keys alone: a NaN value that the
 //    mask hides from a row must not reach it through a weight of 0.
@@ -44,7 +48,34 @@
 #include "kv_attend.cuh"
 #include "kv_host.h"
 
+#ifndef KV_ATTEND_L2
+#define KV_ATTEND_L2 ""      // cp.async's L2 prefetch size: "", ".L2::128B" or ".L2::256B"
+#endif
+#ifndef KV_ATTEND_STATIC
+#define KV_ATTEND_STATIC 80  // percent of the steps in the CTAs' first shares
+#endif
+#ifndef KV_ATTEND_MIN_STEPS
+#define KV_ATTEND_MIN_STEPS 4
+#endif
+
 namespace kvimpl {
+
+// The shares: level k holds shares of `size` steps from step `start` on, numbered from `first`.
+struct ShareLevel {
+  int64_t start;
+  int32_t size, first;
+};
+constexpr int kLevels = 6;
+
+// The workspace's head: zero between calls.
+struct SplitWork {
+  unsigned int next;     // the shares that CTAs have taken beyond their first
+  unsigned int pad[63];
+  ShareLevel level[kLevels];
+  int32_t levels, shares;  // in use
+};
+constexpr int64_t kSplitHead = 512;
+static_assert(sizeof(SplitWork) <= kSplitHead, "the workspace's head");
 
 struct SplitParams {
   AttendParams a;
@@ -56,10 +87,43 @@ struct SplitParams {
   int32_t ks_page, ks_slot, vs_page, vs_slot;  // of the block scales
   int32_t split;          // 0: an item is one CTA's
   int32_t min_steps;      // a share is at least this long
-  int32_t shares;         // CTAs that may take a share
-  float *part_o, *part_ml;  // [2 * shares][hw][rows] x DP and x 2
-  int64_t* meta;          // [num_seqs + 1]: first step of each sequence; steps per share
+  int32_t max_shares;     // that the workspace has room for
+  int32_t part_rows;      // rows of an item that can be there
+  SplitWork* head;
+  int64_t* meta;          // [num_seqs]: first step of each sequence
+  float *part_o, *part_ml;  // [2 * max_shares][hw][part_rows] x DP and x 2
 };
+
+// Cuts `total` steps into shares for `ctas` CTAs.
+__device__ __forceinline__ void cut_shares(int64_t total, int32_t ctas, int32_t max_shares, int32_t min_steps,
+                                           SplitWork* w) {
+  int64_t each = (total + ctas - 1) / ctas;
+  if (each < min_steps) each = min_steps;
+  int32_t n = 0, made = 0;
+  int64_t at = 0, size = each;
+  if (each >= 4 * min_steps && max_shares >= 3 * ctas) {
+    size = each * KV_ATTEND_STATIC / 100;
+    while (n < kLevels - 1) {
+      w->level[n++] = ShareLevel{at, static_cast<int32_t>(size), made};
+      at += size * ctas;
+      made += ctas;
+      size = (total - at) / (2 * ctas);
+      if (size < 2 * min_steps || max_shares - made < 3 * ctas) break;
+    }
+    const int64_t room = max_shares - made;
+    size = (total - at + room - 1) / room;
+    if (size < min_steps) size = min_steps;
+  }
+  w->level[n++] = ShareLevel{at, static_cast<int32_t>(size), made};
+  w->levels = n;
+  w->shares = made + static_cast<int32_t>((total - at + size - 1) / size);
+}
+
+__device__ __forceinline__ int32_t share_of(const SplitWork* w, int64_t step) {
+  int32_t k = w->levels - 1;
+  while (k > 0 && w->level[k].start > step) --k;
+  return w->level[k].first + static_cast<int32_t>((step - w->level[k].start) / w->level[k].size);
+}
 
 // An item is (sequence, block of query rows, head group); its steps are the
 // tiles of TW keys, aligned to TW, that hold a key some row of it sees, `subs`
@@ -140,9 +204,9 @@ __device__ __forceinline__ int64_t wide(uint32_t n, int32_t stride) { return wid
 template <int BYTES>
 __device__ __forceinline__ void copy_async(uint32_t dst, const uint8_t* src, uint32_t bytes) {
   if constexpr (BYTES == 16) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+    asm volatile("cp.async.cg.shared.global" KV_ATTEND_L2 " [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
   } else {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(bytes), "n"(BYTES) : "memory");
+    asm volatile("cp.async.ca.shared.global" KV_ATTEND_L2 " [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(bytes), "n"(BYTES) : "memory");
   }
 }
 
@@ -301,8 +365,11 @@ __global__ void __launch_bounds__(32 * kSplitWarps, (kSplitCtas<DP, NB>))
   constexpr int QP = DP / 8;               // query pairs of a lane per row block
   constexpr int OM = L::VN * L::VD / 2;    // O^T products per key block
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int64_t sh_scan[kSplitWarps + 1];
+  __shared__ int64_t sh_scan[kSplitWarps];
+  __shared__ int64_t sh_excl[32 * kSplitWarps + 1];  // first step of each thread's sequences; the total
   __shared__ int64_t sh_first[2];  // the share's first step's sequence, and that sequence's first step
+  __shared__ SplitWork sh_work;
+  __shared__ int32_t sh_next;
 
   const AttendParams& a = p.a;
   const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
@@ -324,40 +391,37 @@ __global__ void __launch_bounds__(32 * kSplitWarps, (kSplitCtas<DP, NB>))
   }
   if (lane == 31u) sh_scan[warp] = incl;
   __syncthreads();
-  int64_t excl = incl - mine, total = 0;
-  const uint32_t nwarps = blockDim.x >> 5;
-  for (uint32_t w = 0; w < nwarps; ++w) {
-    if (w < warp) excl += sh_scan[w];
-    total += sh_scan[w];
-  }
-  int64_t per = (total + p.shares - 1) / p.shares;
-  if (p.split && per < p.min_steps) per = p.min_steps;
-  if (per < 1) per = 1;
-  int64_t pos = per * blockIdx.x;
-  const int64_t end = min(total, pos + per);
-  if (pos >= excl && pos < excl + mine) {
-    int64_t base = excl;
-    int32_t b = b0;
-    for (;; ++b) {
-      const int64_t n = seq_units<L::TW>(p, b, false);
-      if (pos < base + n) break;
-      base += n;
+  {
+    int64_t excl = incl - mine, total = 0;
+    const uint32_t nwarps = blockDim.x >> 5;
+    for (uint32_t w = 0; w < nwarps; ++w) {
+      if (w < warp) excl += sh_scan[w];
+      total += sh_scan[w];
     }
-    sh_first[0] = b;
-    sh_first[1] = base;
-  }
-  if (p.split && blockIdx.x == 0) {  // for the join
-    int64_t base = excl;
-    for (int32_t b = b0; b < b1; ++b) {
-      p.meta[b] = base;
-      base += seq_units<L::TW>(p, b, false);
+    sh_excl[threadIdx.x] = excl;
+    if (threadIdx.x == 0) sh_excl[blockDim.x] = total;
+    if (p.split && blockIdx.x == 0) {  // for the join
+      for (int32_t i = b0; i < b1; ++i) {
+        p.meta[i] = excl;
+        excl += seq_units<L::TW>(p, i, false);
+      }
     }
-    if (threadIdx.x == 0) p.meta[a.num_seqs] = per;
   }
   __syncthreads();
-  if (pos >= end) return;
-  int32_t b = static_cast<int32_t>(sh_first[0]);
-  int64_t base = sh_first[1];
+  if (threadIdx.x == 0) {
+    if (p.split) {
+      cut_shares(sh_excl[blockDim.x], static_cast<int32_t>(gridDim.x), p.max_shares, p.min_steps, &sh_work);
+      if (blockIdx.x == 0) {
+        for (int i = 0; i < sh_work.levels; ++i) p.head->level[i] = sh_work.level[i];
+        p.head->levels = sh_work.levels;
+      }
+    } else {
+      sh_work.level[0] = ShareLevel{0, 1, 0};
+      sh_work.levels = 1;
+      sh_work.shares = static_cast<int32_t>(sh_excl[blockDim.x]);
+    }
+  }
+  __syncthreads();
 
   const int32_t hl = static_cast<int32_t>(warp) % p.hw, sub = static_cast<int32_t>(warp) / p.hw;
   const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * (NU * L::kUnit);
@@ -374,6 +438,25 @@ __global__ void __launch_bounds__(32 * kSplitWarps, (kSplitCtas<DP, NB>))
     return static_cast<uint32_t>(min(max(static_cast<int32_t>(row_bytes) - static_cast<int32_t>(g + 8 * i) * L::VC, 0), L::VC));
   };
 
+  for (int32_t share = static_cast<int32_t>(blockIdx.x); share < sh_work.shares;) {
+    int32_t level = sh_work.levels - 1;
+    while (level > 0 && sh_work.level[level].first > share) --level;
+    int64_t pos = sh_work.level[level].start + static_cast<int64_t>(share - sh_work.level[level].first) * sh_work.level[level].size;
+    const int64_t end = min(sh_excl[blockDim.x], pos + sh_work.level[level].size);
+    if (pos >= sh_excl[threadIdx.x] && pos < sh_excl[threadIdx.x + 1]) {
+      int64_t at = sh_excl[threadIdx.x];
+      int32_t i = static_cast<int32_t>(threadIdx.x) * per_thread;
+      for (; i < a.num_seqs; ++i) {
+        const int64_t n = seq_units<L::TW>(p, i, false);
+        if (pos < at + n) break;
+        at += n;
+      }
+      sh_first[0] = i;
+      sh_first[1] = at;
+    }
+    __syncthreads();
+    int32_t b = static_cast<int32_t>(sh_first[0]);
+    int64_t base = sh_first[1];
   while (pos < end && b < a.num_seqs) {
     const AttendSeq seq = attend_seq(a, b, false);
     const SplitGeom geom = split_geom<TW>(p, seq);
@@ -824,7 +907,7 @@ __global__ void __launch_bounds__(32 * kSplitWarps, (kSplitCtas<DP, NB>))
           if (a.lse && lane == 0u)
             a.lse[static_cast<int64_t>(tok) * a.q_heads + h] = (mm + log2f(ll)) * 0.6931471805599453f;
         } else {
-          const int64_t at = (static_cast<int64_t>(2 * blockIdx.x + (step0 == 0 ? 1 : 0)) * p.hw + hl) * p.rows + r;
+          const int64_t at = (static_cast<int64_t>(2 * share + (step0 == 0 ? 1 : 0)) * p.hw + hl) * p.part_rows + r;
 #pragma unroll
           for (int i = 0; i < DP / 32; ++i) p.part_o[at * DP + lane + 32 * i] = acc[i];
           if (lane == 0u) *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(mm, ll);
@@ -840,7 +923,7 @@ __global__ void __launch_bounds__(32 * kSplitWarps, (kSplitCtas<DP, NB>))
         for (int c = 0; c < 2; ++c) {
           const int32_t r = nb * 8 + 2 * static_cast<int32_t>(t) + c;
           if (r >= nrows) continue;
-          const int64_t at = (static_cast<int64_t>(2 * blockIdx.x + (step0 == 0 ? 1 : 0)) * p.hw + hl) * p.rows + r;
+          const int64_t at = (static_cast<int64_t>(2 * share + (step0 == 0 ? 1 : 0)) * p.hw + hl) * p.part_rows + r;
           float* row = p.part_o + at * DP;
 #pragma unroll
           for (int i = 0; i < OM; i += 2) {
@@ -889,19 +972,28 @@ __global__ void __launch_bounds__(32 * kSplitWarps, (kSplitCtas<DP, NB>))
                          kvh * G + (row0 + r - static_cast<int32_t>(qi) * G));
     }
   }
+    if (!p.split) break;  // as many CTAs as items
+    __syncthreads();      // all warps have read sh_first
+    if (threadIdx.x == 0) sh_next = static_cast<int32_t>(gridDim.x + atomicAdd(&p.head->next, 1u));
+    __syncthreads();
+    share = sh_next;
+  }
 }
+
+constexpr int kJoinWarps = 16;
 
 // Joins the parts of the items that were split, in the order of their keys:
 // `wpr` warps of the CTA take one output row.
 template <int FMT, int DP>
-__global__ void __launch_bounds__(256) kv_attend_join(const __grid_constant__ SplitParams p, const int32_t wpr) {
-  __shared__ float sh[8][DP + 2];
+__global__ void __launch_bounds__(32 * kJoinWarps) kv_attend_join(const __grid_constant__ SplitParams p, const int32_t wpr) {
+  __shared__ float sh[kJoinWarps][DP + 2];
   const AttendParams& a = p.a;
   const uint32_t lane = threadIdx.x & 31u;
   const int32_t warp = static_cast<int32_t>(threadIdx.x >> 5), part = warp % wpr;
-  const int64_t unit = static_cast<int64_t>(blockIdx.x) * (8 / wpr) + warp / wpr;
+  const int64_t unit = static_cast<int64_t>(blockIdx.x) * (kJoinWarps / wpr) + warp / wpr;
   const int32_t tok = static_cast<int32_t>(unit / a.q_heads), h = static_cast<int32_t>(unit - static_cast<int64_t>(tok) * a.q_heads);
   grid_handover();
+  if (blockIdx.x == 0 && threadIdx.x == 0) p.head->next = 0u;
   int32_t b = tok, c0 = 0, c1 = 0, hl = 0, r = 0, pos = 0;
   bool joined = false;
   if (tok < a.num_q) {
@@ -922,11 +1014,9 @@ __global__ void __launch_bounds__(256) kv_attend_join(const __grid_constant__ Sp
       hl = kvh - hg * p.hw;
       r = row - rb * p.rows;
       pos = s.len - s.nq + (tok - s.q0);
-      const int64_t per = __ldcg(reinterpret_cast<const long long*>(p.meta) + a.num_seqs);
-      const int64_t s0 = __ldcg(reinterpret_cast<const long long*>(p.meta) + b) +
-                         (static_cast<int64_t>(rb) * p.hgroups + hg) * geom.steps;
-      c0 = static_cast<int32_t>(s0 / per);
-      c1 = static_cast<int32_t>((s0 + geom.steps - 1) / per);
+      const int64_t s0 = p.meta[b] + (static_cast<int64_t>(rb) * p.hgroups + hg) * geom.steps;
+      c0 = share_of(p.head, s0);
+      c1 = share_of(p.head, s0 + geom.steps - 1);
       joined = c0 != c1;
     }
   }
@@ -945,7 +1035,7 @@ __global__ void __launch_bounds__(256) kv_attend_join(const __grid_constant__ Sp
 #pragma unroll
         for (int i = 0; i < DP / 32; ++i) v[x][i] = 0.0f;
         if (cc <= c1) {
-          const int64_t at = (static_cast<int64_t>(2 * cc + (cc == c0 ? 1 : 0)) * p.hw + hl) * p.rows + r;
+          const int64_t at = (static_cast<int64_t>(2 * cc + (cc == c0 ? 1 : 0)) * p.hw + hl) * p.part_rows + r;
           ml[x] = __ldcg(reinterpret_cast<const float2*>(p.part_ml + at * 2));
 #pragma unroll
           for (int i = 0; i < DP / 32; ++i) v[x][i] = __ldcg(p.part_o + at * DP + lane + 32 * i);
@@ -1030,7 +1120,7 @@ kv_status launch_split(SplitParams p, void* work, int64_t work_bytes, int64_t ma
     if (a.kv_heads % h == 0) p.hw = h;
   p.subs = kSplitWarps / p.hw;
   p.hgroups = a.kv_heads / p.hw;
-  p.min_steps = 4;
+  p.min_steps = KV_ATTEND_MIN_STEPS;
 
   int sms = 0;
   kv_status st = current_sm_count(&sms);
@@ -1042,30 +1132,29 @@ kv_status launch_split(SplitParams p, void* work, int64_t work_bytes, int64_t ma
 
   // An item that cannot be longer than the shortest share is not split, nor is
   // any where the workspace holds the parts of less than half the GPU.
-  const int64_t meta = (static_cast<int64_t>(a.num_seqs) + 1 + 31) / 32 * 256;
-  const int64_t slot = static_cast<int64_t>(p.hw) * p.rows * (DP + 2) * 4;
-  int64_t shares = full;
-  if (work && work_bytes > meta) {
-    const int64_t fit = (work_bytes - meta) / (2 * slot);
-    shares = fit < full ? fit : full;
-  } else {
-    shares = 0;
-  }
-  p.split = max_keys > static_cast<int64_t>(p.min_steps) * p.subs * L::TW && 2 * shares >= full;
+  const int64_t meta = (static_cast<int64_t>(a.num_seqs) + 31) / 32 * 256;
+  p.part_rows = a.q_start || static_cast<int32_t>(a.group.d) > p.rows ? p.rows : static_cast<int32_t>(a.group.d);
+  const int64_t slot = static_cast<int64_t>(p.hw) * p.part_rows * (DP + 2) * 4;
+  int64_t fit = work && work_bytes > kSplitHead + meta ? (work_bytes - kSplitHead - meta) / (2 * slot) : 0;
+  if (fit > kLevels * full) fit = kLevels * full;
+  p.split = max_keys > static_cast<int64_t>(p.min_steps) * p.subs * L::TW && 2 * fit >= full;
+  int64_t grid;
   if (p.split) {
-    p.shares = static_cast<int32_t>(shares);
-    p.meta = static_cast<int64_t*>(work);
-    p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(work) + meta);
-    p.part_ml = p.part_o + 2 * shares * p.hw * p.rows * DP;
+    grid = fit < full ? fit : full;
+    p.max_shares = static_cast<int32_t>(fit);
+    p.head = static_cast<SplitWork*>(work);
+    p.meta = reinterpret_cast<int64_t*>(static_cast<uint8_t*>(work) + kSplitHead);
+    p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(work) + kSplitHead + meta);
+    p.part_ml = p.part_o + 2 * fit * p.hw * p.part_rows * DP;
   } else {
-    // one share an item: at most this many
+    // a CTA an item: at most this many
     const int64_t rows = static_cast<int64_t>(a.num_q) * a.group.d;
     const int64_t items = (rows / p.rows + a.num_seqs) * p.hgroups;
-    p.shares = static_cast<int32_t>(items < 0x7FFFFFFF ? items : 0x7FFFFFFF);
+    grid = items < 0x7FFFFFFF ? items : 0x7FFFFFFF;
   }
 
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.shares));
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(static_cast<unsigned>(32 * p.hw * p.subs));
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = stream;
@@ -1078,12 +1167,13 @@ kv_status launch_split(SplitParams p, void* work, int64_t work_bytes, int64_t ma
   if (le != cudaSuccess) return cuda_fail(le);
   if (!p.split) return KV_OK;
 
-  // few rows: a CTA each, as their parts are many; many rows: a warp each
+  // the fewer the rows, the more parts has each and the more warps take it
   const int64_t rows = static_cast<int64_t>(a.num_q) * a.q_heads;
-  const int32_t wpr = rows < 4ll * sms ? 8 : 1;
-  const int64_t per = 8 / wpr;
+  int32_t wpr = 1;
+  while (wpr < kJoinWarps && rows * wpr < 16ll * sms) wpr *= 2;
+  const int64_t per = kJoinWarps / wpr;
   cfg.gridDim = dim3(static_cast<unsigned>((rows + per - 1) / per));
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.dynamicSmemBytes = 0;
   le = cudaLaunchKernelEx(&cfg, kv_attend_join<FMT, DP>, p, wpr);
   return le == cudaSuccess ? KV_OK : cuda_fail(le);

@@ -554,12 +554,14 @@ typedef struct kv_attend_strides {
  *               as kv_gather_fp4 for KV_CACHE_E2M1; forward scales per tensor
  *               (device scalars, NULL: 1) for KV_CACHE_E4M3FN; none for
  *               KV_CACHE_SRC (elements of `dtype`).
- *   work        NULL, or a device workspace of work_bytes (256-byte aligned),
- *               contents irrelevant.  It lets long sequences be split over the
- *               GPU and joined; the more room, the finer
- *               (KV_ATTEND_WORK_BYTES is always enough).  Without it each
- *               block of query rows of one KV head is one CTA's work.  Calls
- *               sharing one workspace must not overlap on the GPU.
+ *   work        NULL, or a device workspace of work_bytes (256-byte aligned).
+ *               It lets long sequences be split over the GPU and joined; the
+ *               more room, the finer (KV_ATTEND_WORK_BYTES is always enough).
+ *               Without it each block of query rows of one KV head is one
+ *               CTA's work.  Its first KV_ATTEND_HEAD_BYTES are zero before its
+ *               first use, and zero again after every call that completes
+ *               (zero them after a KV_ERR_CUDA); the rest may hold anything.
+ *               Calls sharing one workspace must not overlap on the GPU.
  * All pointers are device memory; q, out, the caches, the table and the lengths
  * are rejected with KV_ERR_INVALID_ARG where CUDA does not know them.  The
  * result does not depend on the order in which CTAs run; it may differ in rounding with the workspace's size.
@@ -572,6 +574,7 @@ typedef struct kv_attend_strides {
  * num_q_tokens == 0: KV_OK, nothing launched.
  */
 #define KV_ATTEND_WORK_BYTES (64ll << 20)
+#define KV_ATTEND_HEAD_BYTES 256
 kv_status kv_attend(const void *q, void *out, float *lse, const void *k_cache,
                     const void *v_cache, const int32_t *page_table, int64_t table_stride,
                     int64_t table_width, const int32_t *seq_lens, const int32_t *q_start,

@@ -190,10 +190,12 @@ def test_workspace_sizes_and_repeats(batch, fmt):
     d = p.tensors(torch.device("cuda"))
     for size in (256, 1 << 16, 1 << 20, kv.ATTEND_WORK_BYTES):
         work = torch.randint(0, 256, (size,), dtype=torch.uint8, device="cuda")
+        work[:kv.ATTEND_HEAD_BYTES] = 0
         a = p.attend(d, work=work)
         p.check(a)
         for _ in range(3):
             assert torch.equal(p.attend(d, work=work).view(torch.int16), a.view(torch.int16))
+        assert not work[:kv.ATTEND_HEAD_BYTES].any()
     T = sum(nqs)
     out = torch.empty_like(a)
     err = kv.error_record()
@@ -250,6 +252,14 @@ def test_bad_pages_and_lengths(nq, fmt):
     p.check(out, lse)
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+def test_many_long_sequences(fmt):
+    """Enough keys that CTAs take several shares and items are cut anywhere."""
+    lens = [9000 - 517 * i for i in range(16)]
+    run(AttendProblem(lens, [1] * 16, 16, 8, 64, fmt=fmt, page=32, seed=29))
+    run(AttendProblem(lens, [3] * 16, 2, 1, 128, fmt=fmt, page=64, window=3000, sinks=40, seed=30))
+
+
 def test_q_start_is_clamped_and_gaps_are_left_alone():
     import torch
     p = AttendProblem([40, 40], [3, 2], 4, 2, 64, seed=25)
@@ -275,7 +285,7 @@ def test_stream_and_graph():
     s.synchronize()
     assert torch.equal(got, ref)
     out = torch.empty_like(ref)
-    work = torch.empty(1 << 22, dtype=torch.uint8, device="cuda")
+    work = torch.zeros(1 << 22, dtype=torch.uint8, device="cuda")
     p.attend(d, out=out, work=work)
     torch.cuda.synchronize()
     g = torch.cuda.CUDAGraph()
