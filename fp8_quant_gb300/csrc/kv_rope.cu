@@ -6,6 +6,17 @@
 // of Q, K and V are read once and written once, with six fp32 operations per
 // rotated pair, so bytes bound it.
 //
+//  * kv_rope_rows   head dims that are multiples of 16 up to 512, contiguous dims
+//                   and 16-byte pieces.  A lane's item is 16 dims of a head as
+//                   two pieces of 8: both halves of eight pairs, so that
+//                   whatever they need is in the lane (an e2m1 block of the
+//                   split-half rotation is two lanes' and takes one shuffle for
+//                   its maximum).  The lanes of a warp are the items of 32 * 16
+//                   / head_dim heads; a warp goes over U such groups of a
+//                   token's Q, K and V heads with all their loads in flight
+//                   before the first store, and since a lane keeps its item
+//                   index, its eight cosines and sines are loaded once for all.
+//                   Row loads do not wait for the slot or the position.
 //  * kv_rope_any    any layout: one warp per (token, head), a lane per rotated
 //                   pair (or unrotated dim, or 16-dim block of an e2m1 row).
 //  * kv_gather_fp4_blocks  one lane per 16-dim block: 8 code bytes and a scale
@@ -163,6 +174,189 @@ __global__ void __launch_bounds__(kThreads) kv_rope_any(const __grid_constant__ 
       }
     }
   }
+}
+
+// 16 bytes that this kernel may overwrite later (q_out may be q): a plain load.
+__device__ __forceinline__ uint4 ld_piece(const uint8_t* p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+  return r;
+}
+
+struct RopeRowParams {
+  RopeParams r;
+  uint32_t iph, hpp;      // items per head; heads per pass
+  uint32_t heads;         // of Q, K and V together
+  uint32_t units;         // per token
+  int narrow;             // slots and pages fit 32 bits
+};
+
+template <int FMT, bool kInter, int U>
+__global__ void __launch_bounds__(kThreads) kv_rope_rows(const __grid_constant__ RopeRowParams p) {
+  const RopeParams& r = p.r;
+  const uint32_t lane = threadIdx.x & 31u;
+  const uint64_t nwarps = static_cast<uint64_t>(gridDim.x) * warps_per_cta();
+  const uint32_t sub = lane / p.iph, item = lane - sub * p.iph;
+  const uint32_t half = r.rotary / 2;
+  const bool turns = item < r.rotary / 16;  // a rotated item (of Q and K)
+  const uint32_t qk = r.q_heads + r.kv_heads;
+  grid_handover();
+  for (uint64_t u = static_cast<uint64_t>(blockIdx.x) * warps_per_cta() + (threadIdx.x >> 5);
+       u < r.num_units; u += nwarps) {
+    const uint64_t tu = u / p.units;
+    const int64_t t = static_cast<int64_t>(tu);
+    const uint32_t first = static_cast<uint32_t>(u - tu * p.units) * U * p.hpp;  // the unit's first head
+    uint4 a[U], b[U];
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const uint32_t hs = first + j * p.hpp + sub;
+      if (sub < p.hpp && hs < p.heads) {
+        const int side = hs < r.q_heads ? 0 : hs < qk ? 1 : 2;
+        const RopeSide& sd = r.side[side];
+        const uint32_t h = hs - (side == 0 ? 0u : side == 1 ? r.q_heads : qk);
+        const uint8_t* src = sd.src + t * sd.src_token + static_cast<int64_t>(h) * sd.src_head;
+        const bool apart = !kInter && turns && side != 2;  // the pieces are half a rotation apart
+        a[j] = ld_piece(src + (apart ? 16u * item : 32u * item));
+        b[j] = ld_piece(src + (apart ? 2u * half + 16u * item : 32u * item + 16u));
+      }
+    }
+    const int64_t slot = load_index(r.indices, t * r.index_stride, r.idx64);
+    const int64_t pos = load_index(r.positions, t * r.position_stride, r.pos64);
+    const bool pos_ok = pos >= 0 && pos < r.max_position;
+    const bool slot_ok = slot >= 0 && slot < r.size_limit;
+    if (first == 0u && lane == 0u && !(pos_ok && slot_ok)) record_oob(r.err, tu);
+    if (!pos_ok) continue;
+    float c[8], s[8];
+    if (turns && first < qk) {
+      const float4* row = reinterpret_cast<const float4*>(r.table + pos * r.table_stride + 8u * item);
+      const float4 c0 = __ldg(row), c1 = __ldg(row + 1), s0 = __ldg(row + half / 4), s1 = __ldg(row + half / 4 + 1);
+      c[0] = c0.x; c[1] = c0.y; c[2] = c0.z; c[3] = c0.w; c[4] = c1.x; c[5] = c1.y; c[6] = c1.z; c[7] = c1.w;
+      s[0] = s0.x; s[1] = s0.y; s[2] = s0.z; s[3] = s0.w; s[4] = s1.x; s[5] = s1.y; s[6] = s1.z; s[7] = s1.w;
+    }
+    int64_t page = 0, off = 0;
+    if (slot_ok) {
+      if (p.narrow) {
+        const uint32_t pg = static_cast<uint32_t>(slot) / static_cast<uint32_t>(r.page_size);
+        page = pg;
+        off = static_cast<uint32_t>(slot) - pg * static_cast<uint32_t>(r.page_size);
+      } else {
+        slot_parts(r, slot, &page, &off);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const uint32_t hs = first + j * p.hpp + sub;
+      const int side = hs < r.q_heads ? 0 : hs < qk ? 1 : 2;
+      const bool live = sub < p.hpp && hs < p.heads && (side == 0 || slot_ok);
+      const RopeSide& sd = r.side[side];
+      const uint32_t h = hs - (side == 0 ? 0u : side == 1 ? r.q_heads : qk);
+      const bool rot = turns && side != 2;
+      uint8_t* dst = side == 0 ? sd.dst + t * sd.dst_slot : sd.dst + page * sd.dst_page + off * sd.dst_slot;
+      dst += static_cast<int64_t>(h) * sd.dst_head;
+      uint32_t w[8] = {a[j].x, a[j].y, a[j].z, a[j].w, b[j].x, b[j].y, b[j].z, b[j].w};
+      const bool plain = FMT == KV_CACHE_SRC || side == 0;  // 16-bit rows
+      if (plain && !rot) {
+        if (live) {
+          *reinterpret_cast<uint4*>(dst + 32u * item) = a[j];
+          *reinterpret_cast<uint4*>(dst + 32u * item + 16u) = b[j];
+        }
+      } else {
+        // x[0 .. 7]: piece a, x[8 .. 15]: piece b, in fp32
+        float x[16];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float2 v = unpack2(w[i], r.bf16);
+          x[2 * i] = v.x;
+          x[2 * i + 1] = v.y;
+        }
+        if (rot) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int i0 = kInter ? 2 * i : i, i1 = kInter ? 2 * i + 1 : i + 8;
+            const float2 y = rotate_pair(x[i0], x[i1], c[i], s[i]);
+            x[i0] = y.x;
+            x[i1] = y.y;
+          }
+        }
+        if (plain) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) w[i] = pack2(x[2 * i], x[2 * i + 1], r.bf16);
+          if (live) {
+            const uint32_t at_a = kInter ? 32u * item : 16u * item;
+            const uint32_t at_b = kInter ? 32u * item + 16u : 2u * half + 16u * item;
+            *reinterpret_cast<uint4*>(dst + at_a) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(dst + at_b) = make_uint4(w[4], w[5], w[6], w[7]);
+          }
+        } else {
+          const bool apart = !kInter && rot;
+          const float inv = sd.inv ? __ldg(sd.inv) : 1.0f;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) x[i] = __fmul_rn(x[i], inv);
+          if constexpr (FMT == KV_CACHE_E4M3FN) {
+            uint32_t o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = e4m3x2(x[4 * i], x[4 * i + 1]) | (e4m3x2(x[4 * i + 2], x[4 * i + 3]) << 16);
+            if (live) {
+              if (apart) {
+                *reinterpret_cast<uint2*>(dst + 8u * item) = make_uint2(o[0], o[1]);
+                *reinterpret_cast<uint2*>(dst + half + 8u * item) = make_uint2(o[2], o[3]);
+              } else {
+                *reinterpret_cast<uint4*>(dst + 16u * item) = make_uint4(o[0], o[1], o[2], o[3]);
+              }
+            }
+          } else {
+            float ma = 0.0f, mb = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              ma = fmaxf(ma, fabsf(x[i]));
+              mb = fmaxf(mb, fabsf(x[8 + i]));
+            }
+            // the other half of each block: the neighbour's where the pieces are apart, else the lane's own
+            const float na = __shfl_xor_sync(0xFFFFFFFFu, ma, 1), nb = __shfl_xor_sync(0xFFFFFFFFu, mb, 1);
+            const float fa = fmaxf(ma, apart ? na : mb), fb = apart ? fmaxf(mb, nb) : fa;
+            float ra, rb;
+            const uint32_t sa = fp4_block_scale(fa, &ra);
+            uint32_t sb = sa;
+            rb = ra;
+            if (apart) sb = fp4_block_scale(fb, &rb);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              x[i] = __fmul_rn(x[i], ra);
+              x[8 + i] = __fmul_rn(x[8 + i], rb);
+            }
+            const uint32_t ca = e2m1x8(x), cb = e2m1x8(x + 8);
+            if (live) {
+              uint8_t* sc = sd.scales + page * sd.sc_page + off * sd.sc_slot + static_cast<int64_t>(h) * sd.sc_head;
+              if (apart) {
+                *reinterpret_cast<uint32_t*>(dst + 4u * item) = ca;
+                *reinterpret_cast<uint32_t*>(dst + half / 2 + 4u * item) = cb;
+                sc[(item & 1u ? half / 16 : 0u) + item / 2] = static_cast<uint8_t>(item & 1u ? sb : sa);
+              } else {
+                *reinterpret_cast<uint2*>(dst + 8u * item) = make_uint2(ca, cb);
+                sc[item] = static_cast<uint8_t>(sa);
+              }
+            }
+          }
+        }
+      }
+    }
+  }
+}
+
+template <int FMT, bool kInter>
+kv_status launch_rope_rows(RopeRowParams& p, int64_t num_tokens, cudaStream_t stream) {
+  // Few tokens: a pass per warp, so that they spread over the SMs (one call
+  // is then one round of loads); else 4 passes' loads in flight per warp.
+  int sms = 0;
+  const kv_status st = current_sm_count(&sms);
+  if (st != KV_OK) return st;
+  const uint32_t passes = (p.heads + p.hpp - 1) / p.hpp;
+  const bool few = static_cast<uint64_t>(num_tokens) * passes < static_cast<uint64_t>(sms) * 16u;
+  p.units = few ? passes : (passes + 3u) / 4u;
+  p.r.num_units = static_cast<uint64_t>(num_tokens) * p.units;
+  return few ? launch(kv_rope_rows<FMT, kInter, 1>, p.r.num_units, p, stream)
+             : launch(kv_rope_rows<FMT, kInter, 4>, p.r.num_units, p, stream);
 }
 
 // ---------------------------------------------------------------------------
@@ -355,6 +549,39 @@ extern "C" kv_status kv_store_rope(const void* k, const void* v, void* k_cache, 
   p.interleaved = rp.interleaved != 0;
   p.err = d_err;
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+
+  // kv_rope_rows: whole items of 16 dims, 16-byte pieces on the 16-bit sides, what an item writes to
+  // a cache aligned to its size, and e2m1 blocks that do not straddle the halves of the rotation
+  const int32_t R = rp.rotary_dim;
+  uint64_t in_bits = u64(k) | u64(v) | u64(s->k_token) | u64(s->k_head) | u64(s->v_token) | u64(s->v_head);
+  if (rp.q) in_bits |= u64(rp.q) | u64(rp.q_out) | u64(rp.q_token) | u64(rp.q_head) | u64(rp.qo_token) | u64(rp.qo_head);
+  if (R > 0) in_bits |= u64(rp.cos_sin) | u64(4 * rp.cos_sin_stride);
+  const uint64_t cache_bits = u64(k_cache) | u64(v_cache) | u64(s->kc_slot) | u64(s->kc_head) | u64(s->vc_slot) |
+                              u64(s->vc_head) | u64(kc_page_stride) | u64(vc_page_stride);
+  const int32_t elem = format == KV_CACHE_SRC ? 2 : 1;
+  const bool rows = head_dim % 16 == 0 && head_dim <= 512 && R % 16 == 0 && (in_bits & 15u) == 0 &&
+                    (cache_bits & (format == KV_CACHE_E2M1 ? 7u : 15u)) == 0 && s->k_dim == 2 && s->v_dim == 2 &&
+                    s->kc_dim == elem && s->vc_dim == elem &&
+                    (format != KV_CACHE_E2M1 || p.interleaved || (R % 32 == 0 && head_dim % 32 == 0));
+  if (rows) {
+    RopeRowParams q = {};
+    q.r = p;
+    q.iph = static_cast<uint32_t>(head_dim / 16);
+    q.hpp = 32u / q.iph;
+    q.heads = p.per_token;
+    q.narrow = size_limit <= INT32_MAX && page_size <= INT32_MAX;
+    switch (format) {
+      case KV_CACHE_SRC:
+        return p.interleaved ? launch_rope_rows<KV_CACHE_SRC, true>(q, num_tokens, stream)
+                             : launch_rope_rows<KV_CACHE_SRC, false>(q, num_tokens, stream);
+      case KV_CACHE_E4M3FN:
+        return p.interleaved ? launch_rope_rows<KV_CACHE_E4M3FN, true>(q, num_tokens, stream)
+                             : launch_rope_rows<KV_CACHE_E4M3FN, false>(q, num_tokens, stream);
+      default:
+        return p.interleaved ? launch_rope_rows<KV_CACHE_E2M1, true>(q, num_tokens, stream)
+                             : launch_rope_rows<KV_CACHE_E2M1, false>(q, num_tokens, stream);
+    }
+  }
   switch (format) {
     case KV_CACHE_SRC: return launch(kv_rope_any<KV_CACHE_SRC>, p.num_units, p, stream);
     case KV_CACHE_E4M3FN: return launch(kv_rope_any<KV_CACHE_E4M3FN>, p.num_units, p, stream);
