@@ -96,6 +96,8 @@ _lib = None
 def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     """Load ``libkvstore.so`` (built by ``fp8_quant_gb300.build``); raises if absent."""
     global _lib
+    if _lib is not None and path is None:
+        return _lib
     with _lock:
         if _lib is not None and path is None:
             return _lib
@@ -407,8 +409,11 @@ def _default_record(device):
 
 
 def _stream_handle(stream, device) -> int:
-    import torch
     if stream is None:
+        import torch
+        if device.index is not None:
+            # the handle without a Stream object around it (2 us less)
+            return torch._C._cuda_getCurrentRawStream(device.index)
         stream = torch.cuda.current_stream(device)
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -792,11 +797,11 @@ ATTEND_WORK_BYTES = 64 << 20  # KV_ATTEND_WORK_BYTES of the C header
 ATTEND_HEAD_BYTES = 256       # KV_ATTEND_HEAD_BYTES
 
 
-def _is_bf16(x) -> int:
+def _is_bf16(dtype) -> int:
     import torch
-    if x.dtype == torch.bfloat16:
+    if dtype is torch.bfloat16:
         return 1
-    if x.dtype == torch.float16:
+    if dtype is torch.float16:
         return 0
     raise TypeError("rows must be bf16 or fp16")
 
@@ -804,29 +809,35 @@ def _is_bf16(x) -> int:
 def _cache_strides(cache, page_size, width, elem_bytes, what):
     """(page, slot, head, dim) byte strides and the slots and heads of a
     [slots, H, width] or [pages, page_size, H, width] cache."""
-    if cache.element_size() != elem_bytes:
+    e = cache.element_size()
+    if e != elem_bytes:
         raise TypeError(f"{what} must have {elem_bytes}-byte elements")
-    st = cache.stride()
-    if cache.dim() == 4:
-        pages, ps, H, w = cache.shape
+    shape = cache.shape
+    if len(shape) == 4:
+        pages, ps, H, w = shape
         if ps != page_size:
             raise ValueError(f"page_size does not match {what}")
+        page, slot, head, dim = cache.stride()
         slots = pages * ps
-        page, slot, head, dim = st
-    elif cache.dim() == 3:
-        slots, H, w = cache.shape
-        slot, head, dim = st
+    elif len(shape) == 3:
+        slots, H, w = shape
+        slot, head, dim = cache.stride()
         page = slot * page_size
     else:
         raise ValueError(f"{what} must be [slots, H, {width}] or [pages, page_size, H, {width}]")
     if w != width:
         raise ValueError(f"{what}: rows of {w} elements, {width} expected")
-    return page * elem_bytes, slot * elem_bytes, head * elem_bytes, dim * elem_bytes, slots, H
+    return page * e, slot * e, head * e, dim * e, slots, H
 
 
-def _cache_pair(k_cache, v_cache, page_size, D, fmt, elem_bytes):
-    width = D // 2 if fmt == "e2m1" else D
-    eb = elem_bytes if fmt is None else 1
+def _cache_pair(k_cache, v_cache, page_size, D, fmt, dtype):
+    """The strides of both caches of format ``fmt`` (None: of ``dtype``)."""
+    if fmt is None:
+        if k_cache.dtype is not dtype or v_cache.dtype is not dtype:
+            raise TypeError("without a format the caches have the rows' dtype")
+        width, eb = D, 2
+    else:
+        width, eb = (D // 2 if fmt == "e2m1" else D), 1
     kc = _cache_strides(k_cache, page_size, width, eb, "k_cache")
     vc = _cache_strides(v_cache, page_size, width, eb, "v_cache")
     if kc[4:] != vc[4:]:
@@ -837,21 +848,21 @@ def _cache_pair(k_cache, v_cache, page_size, D, fmt, elem_bytes):
 def _block_scales(k_scales, v_scales, page_size, D, slots, H):
     if k_scales is None or v_scales is None:
         raise ValueError("an e2m1 cache needs k_scales and v_scales")
-    out = []
+    out = [k_scales.data_ptr(), v_scales.data_ptr()]
     for x, what in ((k_scales, "k_scales"), (v_scales, "v_scales")):
         page, slot, head, dim, n, h = _cache_strides(x, page_size, D // 16, 1, what)
-        if dim != 1 or (n, h) != (slots, H):
+        if dim != 1 or n != slots or h != H:
             raise ValueError(f"{what} must be [slots, H, D / 16] or [pages, page_size, H, D / 16] "
                              "bytes with contiguous rows, like the cache")
-        out += [page, slot, head]
-    return [k_scales.data_ptr(), v_scales.data_ptr(), *out]
+        out += (page, slot, head)
+    return out
 
 
 def _scalar_ptr(x, what):
-    import torch
     if x is None:
         return None
-    if x.dtype != torch.float32 or x.numel() != 1 or x.device.type != "cuda":
+    import torch
+    if x.dtype is not torch.float32 or x.numel() != 1 or not x.is_cuda:
         raise TypeError(f"{what} must be a 1-element fp32 device tensor")
     return x.data_ptr()
 
@@ -881,51 +892,57 @@ def kv_store_rope(k, v, k_cache, v_cache, indices, positions, cos_sin, *, q=None
     Tokens whose slot or position is out of range are skipped and counted in ``err``.
     """
     import torch
-    if k.dim() != 3 or k.shape != v.shape or k.dtype != v.dtype:
+    shape, dtype = k.shape, k.dtype
+    if len(shape) != 3 or shape != v.shape or dtype is not v.dtype:
         raise ValueError("k and v must be [T, H, D] of one shape and dtype")
-    T, H, D = k.shape
-    bf16 = _is_bf16(k)
+    T, H, D = shape
+    bf16 = _is_bf16(dtype)
     f = _check_format(fmt)
-    kc, vc = _cache_pair(k_cache, v_cache, page_size, D, fmt, 2)
-    if fmt is None and (k_cache.dtype != k.dtype or v_cache.dtype != k.dtype):
-        raise TypeError("without a format the caches have the rows' dtype")
-    slots = kc[4]
+    kc, vc = _cache_pair(k_cache, v_cache, page_size, D, fmt, dtype)
     if kc[5] != H:
         raise ValueError(f"caches of {kc[5]} heads, rows of {H}")
-    if indices.dim() != 1 or positions.dim() != 1 or positions.shape[0] != T or indices.shape[0] != T:
+    if indices.shape != (T,) or positions.shape != (T,):
         raise ValueError("indices and positions must hold one entry per row")
     idt, istride = _index_args(indices)
     pdt, pstride = _index_args(positions)
-    if cos_sin.dim() != 2 or cos_sin.dtype != torch.float32 or cos_sin.stride(1) != 1:
+    rows, rot = cos_sin.shape if cos_sin.dim() == 2 else (0, -1)
+    tstride, tdim = cos_sin.stride() if rot >= 0 else (0, 0)
+    if tdim != 1 or cos_sin.dtype is not torch.float32:
         raise TypeError("cos_sin must be fp32 [max_position, R] with contiguous rows")
-    qa = (None, None, 0, 0, 0, 0, 0)
     if q is not None:
-        if q.dim() != 3 or q.shape[0] != T or q.shape[2] != D or q.dtype != k.dtype or q.stride(2) != 1:
+        qshape = q.shape
+        qst = q.stride()
+        if len(qshape) != 3 or qshape[0] != T or qshape[2] != D or q.dtype is not dtype or qst[2] != 1:
             raise ValueError("q must be [T, HQ, D] of k's dtype with contiguous dims")
         if q_out is None:
             with _on_stream(stream, q.device):
-                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        if q_out.shape != q.shape or q_out.dtype != q.dtype or q_out.stride(2) != 1:
+                q_out = torch.empty(qshape, dtype=dtype, device=q.device)
+        ost = q_out.stride()
+        if q_out.shape != qshape or q_out.dtype is not dtype or ost[2] != 1:
             raise ValueError("q_out must be like q, with contiguous dims")
-        qa = (q.data_ptr(), q_out.data_ptr(), q.shape[1], q.stride(0) * 2, q.stride(1) * 2,
-              q_out.stride(0) * 2, q_out.stride(1) * 2)
+        qa = (q.data_ptr(), q_out.data_ptr(), qshape[1], qst[0] * 2, qst[1] * 2, ost[0] * 2, ost[1] * 2)
     elif q_out is not None:
         raise ValueError("q_out without q")
+    else:
+        qa = (None, None, 0, 0, 0, 0, 0)
     if fmt is None and not (inv_k_scale is None and inv_v_scale is None):
         raise ValueError("caches of the rows' dtype take no scales")
-    sc = _block_scales(k_scales, v_scales, page_size, D, slots, H) if fmt == "e2m1" else None
-    rec = err if err is not None else _default_record(k_cache.device)
-    rope = (cos_sin.data_ptr(), cos_sin.stride(0) if cos_sin.shape[0] > 1 else cos_sin.shape[1],
-            cos_sin.shape[0], positions.data_ptr(), pdt, pstride, cos_sin.shape[1],
-            int(interleaved), *qa)
-    _check(raw.kv_store_rope(
+    sc = _block_scales(k_scales, v_scales, page_size, D, kc[4], H) if fmt == "e2m1" else None
+    k0, k1, k2 = k.stride()
+    v0, v1, v2 = v.stride()
+    device = k_cache.device
+    rec = err if err is not None else _default_record(device)
+    rc = raw.kv_store_rope(
         k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), indices.data_ptr(),
         idt, istride, T, H, D, bf16,
-        (k.stride(0) * 2, k.stride(1) * 2, k.stride(2) * 2, v.stride(0) * 2, v.stride(1) * 2,
-         v.stride(2) * 2, kc[1], kc[2], kc[3], vc[1], vc[2], vc[3]),
-        page_size, kc[0], vc[0], slots if size_limit is None else size_limit, rope, f,
-        _scalar_ptr(inv_k_scale, "inv_k_scale"), _scalar_ptr(inv_v_scale, "inv_v_scale"), sc,
-        rec.data_ptr(), _stream_handle(stream, k_cache.device)), "kv_store_rope")
+        (k0 * 2, k1 * 2, k2 * 2, v0 * 2, v1 * 2, v2 * 2, kc[1], kc[2], kc[3], vc[1], vc[2], vc[3]),
+        page_size, kc[0], vc[0], kc[4] if size_limit is None else size_limit,
+        (cos_sin.data_ptr(), tstride if rows > 1 else rot, rows, positions.data_ptr(), pdt, pstride,
+         rot, 1 if interleaved else 0, *qa),
+        f, _scalar_ptr(inv_k_scale, "inv_k_scale"), _scalar_ptr(inv_v_scale, "inv_v_scale"), sc,
+        rec.data_ptr(), _stream_handle(stream, device))
+    if rc:
+        _check(rc, "kv_store_rope")
     return q_out
 
 
@@ -935,25 +952,31 @@ def kv_gather_fp4(k_cache, v_cache, k_scales, v_scales, k_out, v_out, indices, *
     """Dequantising gather of an e2m1 cache (see :func:`kv_store_rope`) into bf16 / fp16 rows:
     row t of ``k_out`` / ``v_out`` [T, H, D] takes the cache row of ``indices[t]``.
     ``k_scale`` / ``v_scale``: the forward tensor scales (None: 1)."""
-    if k_out.dim() != 3 or k_out.shape != v_out.shape or k_out.dtype != v_out.dtype:
+    shape = k_out.shape
+    if len(shape) != 3 or shape != v_out.shape or k_out.dtype is not v_out.dtype:
         raise ValueError("k_out and v_out must be [T, H, D] of one shape and dtype")
-    T, H, D = k_out.shape
-    kc, vc = _cache_pair(k_cache, v_cache, page_size, D, "e2m1", 1)
+    T, H, D = shape
+    kc, vc = _cache_pair(k_cache, v_cache, page_size, D, "e2m1", None)
     if kc[5] != H:
         raise ValueError(f"caches of {kc[5]} heads, rows of {H}")
     sc = _block_scales(k_scales, v_scales, page_size, D, kc[4], H)
     idt, istride = _index_args(indices)
-    if indices.shape[0] > T:
+    n = indices.shape[0]
+    if n > T:
         raise ValueError("fewer output rows than indices")
-    rec = err if err is not None else _default_record(k_cache.device)
-    _check(raw.kv_gather_fp4(
+    k0, k1, k2 = k_out.stride()
+    v0, v1, v2 = v_out.stride()
+    device = k_cache.device
+    rec = err if err is not None else _default_record(device)
+    rc = raw.kv_gather_fp4(
         k_cache.data_ptr(), v_cache.data_ptr(), sc, k_out.data_ptr(), v_out.data_ptr(),
-        indices.data_ptr(), idt, istride, indices.shape[0], H, D, _is_bf16(k_out),
-        (k_out.stride(0) * 2, k_out.stride(1) * 2, k_out.stride(2) * 2, v_out.stride(0) * 2,
-         v_out.stride(1) * 2, v_out.stride(2) * 2, kc[1], kc[2], kc[3], vc[1], vc[2], vc[3]),
+        indices.data_ptr(), idt, istride, n, H, D, _is_bf16(k_out.dtype),
+        (k0 * 2, k1 * 2, k2 * 2, v0 * 2, v1 * 2, v2 * 2, kc[1], kc[2], kc[3], vc[1], vc[2], vc[3]),
         page_size, kc[0], vc[0], kc[4] if size_limit is None else size_limit,
         _scalar_ptr(k_scale, "k_scale"), _scalar_ptr(v_scale, "v_scale"), rec.data_ptr(),
-        _stream_handle(stream, k_cache.device)), "kv_gather_fp4")
+        _stream_handle(stream, device))
+    if rc:
+        _check(rc, "kv_gather_fp4")
 
 
 def _on_stream(stream, device):
@@ -991,55 +1014,58 @@ def kv_attend(q, k_cache, v_cache, page_table, seq_lens, *, q_start=None, page_s
     id are counted in ``err``.
     """
     import torch
-    if q.dim() != 3 or q.stride(2) != 1:
+    shape, dtype, qst = q.shape, q.dtype, q.stride()
+    if len(shape) != 3 or qst[2] != 1:
         raise ValueError("q must be [tokens, HQ, D] with contiguous dims")
-    T, HQ, D = q.shape
-    bf16 = _is_bf16(q)
+    T, HQ, D = shape
+    bf16 = _is_bf16(dtype)
     f = _check_format(fmt)
     if page_size is None:
         if k_cache.dim() != 4:
             raise ValueError("page_size is needed with [slots, H, ...] caches")
         page_size = k_cache.shape[1]
-    kc, vc = _cache_pair(k_cache, v_cache, page_size, D, fmt, 2)
-    if fmt is None and (k_cache.dtype != q.dtype or v_cache.dtype != q.dtype):
-        raise TypeError("without a format the caches have q's dtype")
+    kc, vc = _cache_pair(k_cache, v_cache, page_size, D, fmt, dtype)
     if kc[3] != vc[3] or kc[3] != (2 if fmt is None else 1):
         raise ValueError("cache dims must be contiguous")
-    slots, H = kc[4:]
+    slots, H = kc[4], kc[5]
     if HQ % H:
         raise ValueError(f"{HQ} query heads over {H} KV heads")
     sc = _block_scales(k_scales, v_scales, page_size, D, slots, H) if fmt == "e2m1" else None
-    if page_table.dim() != 2 or page_table.dtype != torch.int32 or page_table.stride(1) != 1:
+    tst = page_table.stride()
+    if len(tst) != 2 or page_table.dtype is not torch.int32 or tst[1] != 1:
         raise TypeError("page_table must be int32 [B, width] with contiguous rows")
     B, width = page_table.shape
-    if seq_lens.dtype != torch.int32 or seq_lens.shape != (B,) or (B > 1 and seq_lens.stride(0) != 1):
+    if seq_lens.dtype is not torch.int32 or seq_lens.shape != (B,) or (B > 1 and seq_lens.stride(0) != 1):
         raise TypeError("seq_lens must be a contiguous int32 [B]")
     if q_start is not None:
-        if q_start.dtype != torch.int32 or q_start.shape != (B + 1,) or q_start.stride(0) != 1:
+        if q_start.dtype is not torch.int32 or q_start.shape != (B + 1,) or q_start.stride(0) != 1:
             raise TypeError("q_start must be a contiguous int32 [B + 1]")
     elif T != B:
         raise ValueError("without q_start there is one query row per sequence")
+    device = q.device
     if out is None:
-        with _on_stream(stream, q.device):
-            out = torch.empty((T, HQ, D), dtype=q.dtype, device=q.device)
-    elif out.shape != q.shape or out.dtype != q.dtype or out.stride(2) != 1:
+        with _on_stream(stream, device):
+            out = torch.empty(shape, dtype=dtype, device=device)
+    ost = out.stride()
+    if out.shape != shape or out.dtype is not dtype or ost[2] != 1:
         raise ValueError("out must be like q, with contiguous dims")
-    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (T, HQ) or not lse.is_contiguous()):
+    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (T, HQ) or not lse.is_contiguous()):
         raise ValueError("lse must be a contiguous fp32 [tokens, HQ]")
     if work is None:
-        with _on_stream(stream, q.device):
-            work = torch.empty(ATTEND_WORK_BYTES, dtype=torch.uint8, device=q.device)
+        with _on_stream(stream, device):
+            work = torch.empty(ATTEND_WORK_BYTES, dtype=torch.uint8, device=device)
             work[:ATTEND_HEAD_BYTES].zero_()
-    rec = err if err is not None else _default_record(q.device)
-    _check(raw.kv_attend(
+    rec = err if err is not None else _default_record(device)
+    rc = raw.kv_attend(
         q.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
         k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(),
-        page_table.stride(0) if B > 1 else width, width, seq_lens.data_ptr(),
+        tst[0] if B > 1 else width, width, seq_lens.data_ptr(),
         None if q_start is None else q_start.data_ptr(), B, T, HQ, H, D, bf16,
-        (q.stride(0) * 2, q.stride(1) * 2, out.stride(0) * 2, out.stride(1) * 2,
-         *kc[:3], *vc[:3]),
+        (qst[0] * 2, qst[1] * 2, ost[0] * 2, ost[1] * 2, kc[0], kc[1], kc[2], vc[0], vc[1], vc[2]),
         page_size, slots // page_size, f, _scalar_ptr(k_scale, "k_scale"),
         _scalar_ptr(v_scale, "v_scale"), sc, 1.0 / math.sqrt(D) if sm_scale is None else sm_scale,
         window, sinks, work.data_ptr(), work.numel() * work.element_size(), rec.data_ptr(),
-        _stream_handle(stream, q.device)), "kv_attend")
+        _stream_handle(stream, device))
+    if rc:
+        _check(rc, "kv_attend")
     return out

@@ -19,7 +19,8 @@ CSRC = os.path.join(HERE, "csrc")
 SOURCES = [os.path.join(CSRC, f) for f in ("kvstore.cu", "kv_gather.cu", "kv_scale.cu", "kv_fp8_ex.cu",
                                            "kv_rope.cu", "kv_attend.cu", "kv_attend_split_bf16.cu",
                                            "kv_attend_split_f16.cu", "kv_attend_split_e4m3.cu",
-                                           "kv_attend_split_e2m1.cu")]
+                                           "kv_attend_split_e2m1.cu", "kv_attend_tile_src.cu",
+                                           "kv_attend_tile_quant.cu")]
 SRC = SOURCES[0]
 HEADER = os.path.join(ROOT, "include", "kvstore.h")
 LIBDIR = os.path.join(HERE, "lib")

@@ -1,6 +1,8 @@
 // Attention over the paged cache (kv_attend): argument checks, the choice of
 // the kernel, and the general kernel.
 //
+//  * kv_attend_tile   (kv_attend_tile.cuh) many query rows per sequence: head
+//                     dims that are multiples of 16 up to 128, aligned as below.
 //  * kv_attend_split  (kv_attend_split.cuh) head dims that are multiples of 16
 //                     up to 256, 16-byte aligned bases and strides.
 //  * kv_attend_rows   any head dim, alignment and stride: one warp per query
@@ -8,7 +10,7 @@
 #include <cmath>
 #include <climits>
 
-#include "kv_attend_split.cuh"
+#include "kv_attend_tile.cuh"
 
 namespace kvimpl {
 namespace {
@@ -148,6 +150,20 @@ extern "C" kv_status kv_attend(const void* q, void* out, float* lse, const void*
   if (format == KV_CACHE_E2M1)
     near = near && fits(scales->k_page) && fits(scales->k_slot) && fits(scales->v_page) && fits(scales->v_slot);
   if (head_dim % 16 == 0 && head_dim <= 256 && ((q_bits | c_bits) & 15u) == 0 && near) {
+    const int64_t per_seq = (num_q_tokens + num_seqs - 1) / num_seqs * p.group.d;
+    if (head_dim <= 128 && p.group.d <= 128 && per_seq >= 32) {
+      TileParams tp = {};
+      tp.a = p;
+      tp.k_page = static_cast<int32_t>(s->kc_page); tp.k_slot = static_cast<int32_t>(s->kc_slot);
+      tp.v_page = static_cast<int32_t>(s->vc_page); tp.v_slot = static_cast<int32_t>(s->vc_slot);
+      if (format == KV_CACHE_E2M1) {
+        tp.ks_page = static_cast<int32_t>(scales->k_page); tp.ks_slot = static_cast<int32_t>(scales->k_slot);
+        tp.vs_page = static_cast<int32_t>(scales->v_page); tp.vs_slot = static_cast<int32_t>(scales->v_slot);
+      }
+      tp.qpt = kTileRows / static_cast<int32_t>(p.group.d);
+      tp.blocks = p.num_q / (2 * tp.qpt) + num_seqs;
+      return format == KV_CACHE_SRC ? tile_src(tp, stream) : tile_quant(tp, format, stream);
+    }
     SplitParams sp = {};
     sp.a = p;
     sp.whole_blocks = page_size % 16 == 0;

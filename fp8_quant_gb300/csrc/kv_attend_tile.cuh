@@ -1,0 +1,708 @@
+// Attention for many query rows per sequence (prefill): tiles of 128 query
+// rows against tiles of 128 keys on the tensor cores (tcgen05).
+//
+// Products bound it: 4 * head_dim operations a query row and visible key.  A
+// CTA takes one KV head and up to two tiles of query rows, a row being a
+// (query, head of the group) pair, so that a group's heads share K and V and a
+// window's edge costs few keys.
+//
+//   warps 0-3, 4-7  the softmax of tile 0 and of tile 1, a thread a row: S from
+//                   TMEM, running maximum and sum in registers, P back over S
+//                   as 16-bit, O rescaled in TMEM.  A maximum that grew by less
+//                   than 2^8 is kept, as the weights then stay below 2^8: O is
+//                   seldom touched.
+//   warp  8         issues the products: S_t = Q_t K^T (both operands in shared
+//                   memory), O_t += P_t V (P in TMEM, V as it lies: keys as
+//                   rows, head dims contiguous).  While one tile's softmax runs
+//                   the other tile's products do.
+//   warps 9-11      bring K and V from their pages into a ring of shared memory,
+//                   16 bytes a lane, in the 128-byte swizzle that the products
+//                   read; 16-bit rows go there by cp.async, quantised ones by
+//                   cp.async into a staging ring of the lane's own and from there
+//                   as fp16 (exact; see kv_attend_split.cuh).
+//
+// TMEM (512 columns): S_0/P_0, S_1/P_1 (128 each), O_0, O_1 (head_dim each).
+// The products of one CTA run in the order of their issue, so S_t of the next
+// keys may overwrite P_t behind O_t's product without a wait between.
+//
+// Every wait has a limit (kSpin); a CTA whose wait ran out counts its sequence
+// in the error record, lets its copies and products end and leaves.
+#pragma once
+
+#include "kv_attend_split.cuh"
+
+namespace kvimpl {
+
+struct TileParams {
+  AttendParams a;
+  int32_t k_page, k_slot, v_page, v_slot;      // byte strides, in 32 bits
+  int32_t ks_page, ks_slot, vs_page, vs_slot;  // of the block scales
+  int32_t qpt;     // queries of a tile: 128 / group
+  int32_t blocks;  // query blocks of the launch (an upper bound)
+};
+
+constexpr int kTileRows = 128, kTileKeys = 128;
+constexpr int kTileThreads = 384;
+constexpr int kCopyThreads = 96;
+constexpr uint32_t kSpin = 1u << 24;  // tries of a wait: far beyond any that ends
+
+template <int FMT, int DP>
+struct TileSmem {
+  static constexpr bool kQuant = FMT != KV_CACHE_SRC;
+  static constexpr int kUnits = kQuant ? 3 : 4;              // ring units: a K or a V tile in 16 bits
+  static constexpr int kUnit = kTileKeys * DP * 2;
+  static constexpr int kQ = kTileRows * DP * 2;
+  static constexpr int kItems = kQuant ? kTileKeys * DP / 16 : kTileKeys * DP / 8;  // a lane's pieces: 16 or 8 dims
+  static constexpr int kPer = (kItems + kCopyThreads - 1) / kCopyThreads;
+  static constexpr int kRawItem = FMT == KV_CACHE_E4M3FN ? 16 : FMT == KV_CACHE_E2M1 ? 12 : 0;
+  static constexpr int kRawUnits = kQuant ? 3 : 0;
+  static constexpr int kRaw = kPer * kCopyThreads * kRawItem;
+  static constexpr int kOffRing = 2 * kQ;
+  static constexpr int kOffRaw = kOffRing + kUnits * kUnit;
+  static constexpr int kOffRows = kOffRaw + kRawUnits * kRaw;   // [4][128]: page << 32 | offset of a tile's keys, -1: not wanted
+  static constexpr int kOffBad = kOffRows + 4 * kTileKeys * 8;  // [8][4] words: a tile's keys on bad pages
+  static constexpr int kOffBars = kOffBad + 8 * 16;
+  static constexpr int kBars = 2 * kUnits + 9;
+  static constexpr int kTotal = kOffBars + kBars * 8 + 1024;    // the base is aligned to 1,024
+};
+
+// -- mbarriers, tcgen05 -----------------------------------------------------------------------
+
+__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\t"
+               "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+               "selp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  return ok != 0u;
+}
+
+// False when the wait ran out here or anywhere in the CTA.
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* failed) {
+  for (uint32_t i = 0; i < kSpin; ++i) {
+    if (bar_try(bar, parity)) return true;
+    if ((i & 1023u) == 1023u && *failed != 0) return false;
+  }
+  *failed = 1;
+  return false;
+}
+
+__device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// D (TMEM) = or += A (shared memory) B (shared memory)
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+               "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+               ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u) : "memory");
+}
+
+// D (TMEM) = or += A (TMEM) B (shared memory)
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+               "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+               ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u) : "memory");
+}
+
+#define KV_R4(r, i) "=r"((r)[i]), "=r"((r)[(i) + 1]), "=r"((r)[(i) + 2]), "=r"((r)[(i) + 3])
+#define KV_R16(r, i) KV_R4(r, i), KV_R4(r, (i) + 4), KV_R4(r, (i) + 8), KV_R4(r, (i) + 12)
+#define KV_S4(r, i) "r"((r)[i]), "r"((r)[(i) + 1]), "r"((r)[(i) + 2]), "r"((r)[(i) + 3])
+#define KV_S16(r, i) KV_S4(r, i), KV_S4(r, (i) + 4), KV_S4(r, (i) + 8), KV_S4(r, (i) + 12)
+
+// Columns of the warp's 32 lanes: a lane's row, a register a column.  The wait
+// is part of the statement: nothing may touch the registers before it.
+__device__ __forceinline__ void tc_ld32(uint32_t (&r)[32], uint32_t addr) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+               "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+               "tcgen05.wait::ld.sync.aligned;"
+               : KV_R16(r, 0), KV_R16(r, 16) : "r"(addr) : "memory");
+}
+
+__device__ __forceinline__ void tc_ld128(uint32_t (&r)[128], uint32_t addr) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x128.b32 "
+               "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63, %64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, %75, %76, %77, %78, %79, %80, %81, %82, %83, %84, %85, %86, %87, %88, %89, %90, %91, %92, %93, %94, %95, %96, %97, %98, %99, %100, %101, %102, %103, %104, %105, %106, %107, %108, %109, %110, %111, %112, %113, %114, %115, %116, %117, %118, %119, %120, %121, %122, %123, %124, %125, %126, %127}, [%128];\n\t"
+               "tcgen05.wait::ld.sync.aligned;"
+               : KV_R16(r, 0), KV_R16(r, 16), KV_R16(r, 32), KV_R16(r, 48), KV_R16(r, 64), KV_R16(r, 80), KV_R16(r, 96), KV_R16(r, 112)
+               : "r"(addr) : "memory");
+}
+
+__device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t (&r)[32]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+               "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};"
+               ::KV_S16(r, 0), KV_S16(r, 16), "r"(addr) : "memory");
+}
+
+#undef KV_R4
+#undef KV_R16
+#undef KV_S4
+#undef KV_S16
+
+// Descriptor of an operand in shared memory, 128-byte swizzle: rows of 128 bytes, groups of eight
+// rows 1,024 bytes apart.  `lead`: bytes from one 64-element column block to the next, where the
+// contiguous dimension is not the summed one (V); unused otherwise.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead) {
+  return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(lead >> 4) << 16) |
+         (static_cast<uint64_t>(1024u >> 4) << 32) | (uint64_t{1} << 46) | (uint64_t{2} << 61);
+}
+
+// kind::f16 instruction descriptor: fp32 accumulator, A and B bf16 or f16, B's contiguous dimension.
+__device__ __forceinline__ uint32_t instr_desc(bool bf16, bool b_rows_summed, int n) {
+  return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((b_rows_summed ? 1u : 0u) << 16) |
+         (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(kTileRows >> 4) << 24);
+}
+
+// Byte of 16-byte piece `piece` of row `row` in a tile of `rows` rows.
+__device__ __forceinline__ uint32_t swizzled(uint32_t row, uint32_t piece, uint32_t rows) {
+  return (piece >> 3) * (rows * 128u) + row * 128u + (((piece & 7u) ^ (row & 7u)) << 4);
+}
+
+__device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+template <int FMT, int DP, bool kBF16>
+__global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_constant__ TileParams p) {
+  using S = TileSmem<FMT, DP>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  __shared__ int32_t sh_item[2];   // the CTA's sequence and query block
+  __shared__ uint32_t sh_tmem;
+  __shared__ volatile int sh_failed;
+
+  const AttendParams& a = p.a;
+  const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31u;
+  const uint32_t smem = (static_cast<uint32_t>(__cvta_generic_to_shared(smem_raw)) + 1023u) & ~1023u;
+  uint8_t* const smem_ptr = smem_raw + (smem - static_cast<uint32_t>(__cvta_generic_to_shared(smem_raw)));
+  const int32_t G = static_cast<int32_t>(a.group.d);
+  grid_handover();
+
+  // -- which sequence, which queries --------------------------------------------------------
+  const int32_t kvh = static_cast<int32_t>(blockIdx.x % static_cast<uint32_t>(a.kv_heads));
+  const int32_t want = static_cast<int32_t>(blockIdx.x / static_cast<uint32_t>(a.kv_heads));
+  if (warp == 0) {
+    int32_t before = 0, found = -1, block = 0;
+    for (int32_t b0 = 0; b0 < a.num_seqs && found < 0; b0 += 32) {
+      const int32_t b = b0 + static_cast<int32_t>(lane);
+      int32_t n = 0;
+      if (b < a.num_seqs) n = (attend_seq(a, b, blockIdx.x == 0).nq + 2 * p.qpt - 1) / (2 * p.qpt);
+      int32_t incl = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int32_t v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+        if (lane >= static_cast<uint32_t>(o)) incl += v;
+      }
+      const int32_t at = before + incl - n;
+      const uint32_t hit = __ballot_sync(0xFFFFFFFFu, want >= at && want < at + n);
+      if (hit != 0u) {
+        const int src = __ffs(static_cast<int>(hit)) - 1;
+        found = b0 + src;
+        // the last queries, which see the most keys, first
+        block = __shfl_sync(0xFFFFFFFFu, n - 1 - (want - at), src);
+      }
+      before += __shfl_sync(0xFFFFFFFFu, incl, 31);
+    }
+    if (blockIdx.x == 0 && found >= 0)  // lengths out of range are recorded behind it too
+      for (int32_t b = (found / 32 + 1) * 32 + static_cast<int32_t>(lane); b < a.num_seqs; b += 32) attend_seq(a, b, true);
+    if (lane == 0u) {
+      sh_item[0] = found;
+      sh_item[1] = block;
+      sh_failed = 0;
+    }
+  }
+  __syncthreads();
+  const int32_t b = sh_item[0];
+  if (b < 0) return;
+  const AttendSeq seq = attend_seq(a, b, false);
+  const int32_t q_first = sh_item[1] * 2 * p.qpt;            // the block's first query in its sequence
+  const int32_t nq = min(2 * p.qpt, seq.nq - q_first);       // and their number
+  const int32_t tiles = nq > p.qpt ? 2 : 1;
+  const int32_t p_first = seq.len - seq.nq + q_first;        // position of the first
+  const TileList list = visible_tiles<kTileKeys>(a, p_first, p_first + nq - 1);
+  const int32_t p_hi = p_first + nq - 1;
+
+  const uint32_t ring = smem + S::kOffRing;
+  const uint32_t bars = smem + S::kOffBars;
+  const uint32_t full = bars, empty = bars + 8 * S::kUnits;
+  const uint32_t q_full = empty + 8 * S::kUnits, s_full = q_full + 16, p_full = s_full + 16, o_full = p_full + 16, rows_full = o_full + 16;
+  if (warp == 8) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+        static_cast<uint32_t>(__cvta_generic_to_shared(&sh_tmem))) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (tid == 0) {
+    for (int i = 0; i < S::kUnits; ++i) {
+      bar_init(full + 8 * i, kCopyThreads);
+      bar_init(empty + 8 * i, 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      bar_init(q_full + 8 * t, kTileRows);
+      bar_init(s_full + 8 * t, 1);
+      bar_init(p_full + 8 * t, kTileRows);
+      bar_init(o_full + 8 * t, 1);
+    }
+    bar_init(rows_full, kCopyThreads);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  uint32_t* const bad_words = reinterpret_cast<uint32_t*>(smem_ptr + S::kOffBad);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh_tmem;
+  volatile int* const failed = &sh_failed;
+
+  if (warp < 8) {
+    // ======================================================================================
+    // softmax of tile t: a thread a row
+    // ======================================================================================
+    const int32_t t = static_cast<int32_t>(warp >> 2);
+    const int32_t r = static_cast<int32_t>(tid & 127u);
+    if (t < tiles) {
+      const int32_t qi = static_cast<int32_t>(a.group.quot(static_cast<uint32_t>(r)));
+      const int32_t q_in = t * p.qpt + qi;              // query in the block
+      const bool mine = qi < p.qpt && q_in < nq;
+      const int32_t h = kvh * G + (r - qi * G);
+      const int32_t tok = seq.q0 + q_first + q_in;
+      const int32_t pos = mine ? p_first + q_in : -1;
+      // positions of the tile's rows
+      const int32_t t_lo = p_first + t * p.qpt, t_hi = min(p_first + t * p.qpt + p.qpt - 1, p_hi);
+      float scale = a.scale_log2 * tensor_scale(a.k_scale);
+      {
+        const uint8_t* src = a.q + static_cast<int64_t>(tok) * a.q_token + static_cast<int64_t>(h) * a.q_head;
+        uint4 w[DP / 8];
+#pragma unroll
+        for (int i = 0; i < DP / 8; ++i) {
+          w[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (mine && 8 * i < a.head_dim) w[i] = __ldg(reinterpret_cast<const uint4*>(src) + i);
+        }
+        if constexpr (FMT != KV_CACHE_SRC) {
+          if (a.bf16) {  // into fp16's range: the row's largest element to 2^13 .. 2^14
+            uint32_t m = 0u;
+#pragma unroll
+            for (int i = 0; i < DP / 8; ++i)
+              m = absmax_pair<true>(absmax_pair<true>(absmax_pair<true>(absmax_pair<true>(m, w[i].x), w[i].y), w[i].z), w[i].w);
+            const uint32_t e = __float_as_uint(absmax_pair_value<true>(m)) >> 23;
+            const float f = __uint_as_float(min(254u, 267u - e) << 23);
+            scale *= __fdiv_rn(1.0f, f);
+            auto shift = [&](uint32_t x) {
+              const float2 v = widen2<true>(x);
+              return pack2(v.x * f, v.y * f, false);
+            };
+#pragma unroll
+            for (int i = 0; i < DP / 8; ++i) w[i] = make_uint4(shift(w[i].x), shift(w[i].y), shift(w[i].z), shift(w[i].w));
+          }
+        }
+        const uint32_t flip = scale < 0.0f ? 0x80008000u : 0u;  // the maximum is taken before the scale
+        const uint32_t dst = smem + t * S::kQ;
+#pragma unroll
+        for (int i = 0; i < DP / 8; ++i)
+          st_shared16(dst + swizzled(static_cast<uint32_t>(r), i, kTileRows), w[i].x ^ flip, w[i].y ^ flip, w[i].z ^ flip, w[i].w ^ flip);
+        scale = fabsf(scale);
+        if (scale == 0.0f) scale = __uint_as_float(1u);  // hidden scores (-inf) must stay -inf
+        fence_async_shared();
+        bar_arrive(q_full + 8 * t);
+      }
+      const uint32_t lanes = (warp & 3u) << 21;  // the warp's 32 lanes of TMEM
+      const uint32_t s_at = tmem + lanes + t * 128, o_at = tmem + lanes + 256 + t * DP;
+      float m = -INFINITY, l = 0.0f;   // m: of scaled scores, as last used
+      bool ok = true;
+      for (int32_t j = 0; j < list.n; ++j) {
+        ok = bar_wait(s_full + 8 * t, j & 1, failed);
+        if (!__all_sync(0xFFFFFFFFu, ok)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t sw[kTileKeys];
+        tc_ld128(sw, s_at);
+        float s[kTileKeys];
+#pragma unroll
+        for (int i = 0; i < kTileKeys; ++i) s[i] = __uint_as_float(sw[i]);
+        // mask
+        const int32_t j0 = list.tile(j) * kTileKeys;
+        const uint32_t* bw = bad_words + 4 * (j & 7);
+        const bool none_bad = (bw[0] | bw[1] | bw[2] | bw[3]) == 0u;
+        if (!(none_bad && j0 + kTileKeys - 1 <= t_lo && (a.window == 0 || j0 > t_hi - a.window || j0 + kTileKeys - 1 < a.sinks))) {
+          // keys up to pos, and of those the window's or the sinks'
+          auto upto = [](int32_t n) {  // n low bits set
+            return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u;
+          };
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int32_t k0 = j0 + 32 * c;
+            uint32_t see = upto(pos - k0 + 1);
+            if (a.window > 0) see &= ~upto(pos - a.window - k0 + 1) | upto(a.sinks - k0);
+            see &= ~bw[c];
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if ((see & (1u << i)) == 0u) s[32 * c + i] = -INFINITY;
+          }
+        }
+        float x = s[0];
+#pragma unroll
+        for (int i = 1; i < kTileKeys; ++i) x = fmaxf(x, s[i]);
+        x *= scale;
+        // a maximum that grew little is kept (the weights stay below 2^8)
+        const bool grow = x > m + 8.0f || (m == -INFINITY && x > m);
+        if (__any_sync(0xFFFFFFFFu, grow)) {
+          const float mn = grow ? x : m;
+          const float alpha = exp2_fast(m - (mn == -INFINITY ? 0.0f : mn));
+          m = mn;
+          if (j > 0) {
+            const float f = grow ? alpha : 1.0f;
+            l *= f;
+#pragma unroll
+            for (int c = 0; c < DP / 32; ++c) {
+              uint32_t w[32];
+              tc_ld32(w, o_at + 32 * c);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * f);
+              tc_st32(o_at + 32 * c, w);
+            }
+          }
+        }
+        const float ref = m == -INFINITY ? 0.0f : m;
+        float sum0 = 0.0f, sum1 = 0.0f;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t w[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float e0 = exp2_fast(__fmaf_rn(s[64 * c + 2 * i], scale, -ref));
+            const float e1 = exp2_fast(__fmaf_rn(s[64 * c + 2 * i + 1], scale, -ref));
+            sum0 += e0;
+            sum1 += e1;
+            w[i] = pack2(e0, e1, kBF16);
+          }
+          tc_st32(s_at + 32 * c, w);
+        }
+        l += sum0 + sum1;
+        tc_wait_st();
+        tc_fence_before();
+        bar_arrive(p_full + 8 * t);
+      }
+      // -- out ------------------------------------------------------------------------------
+      const float inv = __fdiv_rn(tensor_scale(a.v_scale), l);
+      bool fine = l > 0.0f;
+      if (list.n > 0 && ok) {
+        ok = bar_wait(o_full + 8 * t, 0, failed);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        tc_fence_after();
+      }
+      if (ok) {
+        uint8_t* out = a.out + static_cast<int64_t>(tok) * a.o_token + static_cast<int64_t>(h) * a.o_head;
+        if (list.n > 0) {
+#pragma unroll
+          for (int c = 0; c < DP / 32; ++c) {
+            uint32_t w[32];
+            tc_ld32(w, o_at + 32 * c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t o[4];
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                const float lo = __uint_as_float(w[8 * i + 2 * x]) * inv, hi = __uint_as_float(w[8 * i + 2 * x + 1]) * inv;
+                fine = fine && fabsf(lo) < INFINITY && fabsf(hi) < INFINITY;
+                o[x] = pack2(lo, hi, a.bf16);
+              }
+              if (mine && 32 * c + 8 * i < a.head_dim)
+                *reinterpret_cast<uint4*>(out + 2 * (32 * c + 8 * i)) = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+          }
+          if (mine && a.lse)
+            a.lse[static_cast<int64_t>(tok) * a.q_heads + h] = (m + log2f(l)) * 0.6931471805599453f;
+        }
+        uint32_t again = __ballot_sync(0xFFFFFFFFu, mine && !fine);
+        while (again != 0u) {
+          const int src = __ffs(static_cast<int>(again)) - 1;
+          again &= again - 1u;
+          attend_row<FMT, 8>(a, b, __shfl_sync(0xFFFFFFFFu, pos, src), __shfl_sync(0xFFFFFFFFu, tok, src),
+                             __shfl_sync(0xFFFFFFFFu, h, src));
+        }
+      }
+    }
+  } else if (warp == 8) {
+    // ======================================================================================
+    // the products
+    // ======================================================================================
+    const uint32_t qk_desc = instr_desc(kBF16, false, kTileKeys), pv_desc = instr_desc(kBF16, true, DP);
+    auto slot_of = [](int32_t u) { return static_cast<uint32_t>(u) % S::kUnits; };
+    auto round_of = [](int32_t u) { return (static_cast<uint32_t>(u) / S::kUnits) & 1u; };
+    bool ok = true;
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+      if (ok) ok = __all_sync(0xFFFFFFFFu, bar_wait(bar, parity, failed));
+      if (ok) tc_fence_after();
+    };
+    auto scores = [&](int32_t t, int32_t j) {  // S_t = Q_t K_j^T
+      if (ok && lane == 0u) {
+        const uint32_t q = smem + t * S::kQ, k = ring + slot_of(2 * j) * S::kUnit;
+#pragma unroll
+        for (int i = 0; i < DP / 16; ++i) {
+          const uint32_t at = (i / 4) * (kTileRows * 128) + (i % 4) * 32;
+          tc_mma_ss(tmem + t * 128, smem_desc(q + at, 16), smem_desc(k + at, 16), qk_desc, i > 0);
+        }
+        tc_commit(s_full + 8 * t);
+        if (t == tiles - 1) tc_commit(empty + 8 * slot_of(2 * j));
+      }
+      __syncwarp();
+    };
+    for (int32_t t = 0; t < tiles && list.n > 0; ++t) {
+      wait(q_full + 8 * t, 0);
+      if (t == 0) wait(full + 8 * slot_of(0), round_of(0));
+      scores(t, 0);
+    }
+    for (int32_t j = 0; j < list.n && ok; ++j) {
+      for (int32_t t = 0; t < tiles; ++t) {
+        if (t == 0) wait(full + 8 * slot_of(2 * j + 1), round_of(2 * j + 1));
+        wait(p_full + 8 * t, j & 1);
+        if (ok && lane == 0u) {  // O_t += P_t V_j
+          const uint32_t v = ring + slot_of(2 * j + 1) * S::kUnit;
+#pragma unroll
+          for (int i = 0; i < kTileKeys / 16; ++i)
+            tc_mma_ts(tmem + 256 + t * DP, tmem + t * 128 + i * 8, smem_desc(v + i * 2048, kTileKeys * 128), pv_desc, j > 0 || i > 0);
+          if (t == tiles - 1) tc_commit(empty + 8 * slot_of(2 * j + 1));
+          if (j == list.n - 1) tc_commit(o_full + 8 * t);
+        }
+        __syncwarp();
+        if (j + 1 < list.n) {
+          if (t == 0) wait(full + 8 * slot_of(2 * j + 2), round_of(2 * j + 2));
+          scores(t, j + 1);
+        }
+      }
+    }
+    if (!ok && lane == 0u) {  // products still in flight read shared memory and write TMEM: let them end
+      tc_commit(o_full);
+      for (uint32_t i = 0; i < kSpin && !bar_try(o_full, 0); ++i) {}
+    }
+    __syncwarp();
+  } else {
+    // ======================================================================================
+    // K and V into the ring
+    // ======================================================================================
+    const int32_t c = static_cast<int32_t>(tid) - (kTileThreads - kCopyThreads);
+    int64_t* const rows = reinterpret_cast<int64_t*>(smem_ptr + S::kOffRows);
+    const int32_t* table = a.table + static_cast<int64_t>(b) * a.table_stride;
+    const uint32_t row_bytes = static_cast<uint32_t>(a.head_dim) * (FMT == KV_CACHE_SRC ? 16 : FMT == KV_CACHE_E4M3FN ? 8 : 4) / 8;
+    const int32_t units = 2 * list.n;
+    bool ok = true;
+    // page id and offset of key c (and c + 96) of a tile: id -1: not wanted
+    int32_t id[2];
+    uint32_t off[2];
+    auto look = [&](int32_t j) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int32_t key = c + kCopyThreads * x;
+        id[x] = -1;
+        off[x] = 0u;
+        if (key < kTileKeys && j < list.n) {
+          const int32_t k = list.tile(j) * kTileKeys + key;
+          if (k <= p_hi && (k >= list.lo_key || k < a.sinks)) {
+            const uint32_t pg = a.page.quot(static_cast<uint32_t>(k));
+            off[x] = static_cast<uint32_t>(k) - pg * a.page.d;
+            const int32_t v = __ldg(table + pg);
+            id[x] = v < 0 ? -2 : v;
+          }
+        }
+      }
+    };
+    // The keys of tile j for all lanes of the three warps.  Four buffers: a lane may still read tile
+    // j - 2 (the scales of its staged pieces), and none is more than one tile ahead of another.
+    auto publish = [&](int32_t j) {
+      if (j >= list.n || !ok) return;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int32_t key = c + kCopyThreads * x;
+        const bool is_bad = id[x] == -2 || id[x] >= a.num_pages;
+        const uint32_t bits = __ballot_sync(0xFFFFFFFFu, is_bad);
+        if (is_bad) {
+          record_oob(a.err, static_cast<uint64_t>(b));
+          id[x] = -1;
+        }
+        if (key < kTileKeys) {
+          if (lane == 0u) bad_words[4 * (j & 7) + (key >> 5)] = bits;
+          rows[(j & 3) * kTileKeys + key] = id[x] < 0 ? -1 : (static_cast<int64_t>(id[x]) << 32) | off[x];
+        }
+      }
+      bar_arrive(rows_full);
+      ok = __all_sync(0xFFFFFFFFu, bar_wait(rows_full, j & 1, failed));
+    };
+    constexpr int kPieces = TileSmem<FMT, DP>::kQuant ? DP / 16 : DP / 8;  // of a row
+    const uint32_t raw = smem + S::kOffRaw;
+    auto issue = [&](int32_t u) {
+      if (u < units) {
+        const int32_t j = u >> 1, kv = u & 1;
+        const int64_t* rw = rows + (j & 3) * kTileKeys;
+        const uint8_t* base = kv ? a.v + kvh * a.v_head : a.k + kvh * a.k_head;
+        const int32_t page = kv ? p.v_page : p.k_page, slot = kv ? p.v_slot : p.k_slot;
+#pragma unroll 4
+        for (int i = 0; i < S::kPer; ++i) {
+          const int32_t n = i * kCopyThreads + c;
+          if (S::kItems % kCopyThreads != 0 && n >= S::kItems) break;
+          const uint32_t key = static_cast<uint32_t>(n) / kPieces, piece = static_cast<uint32_t>(n) % kPieces;
+          const int64_t at = rw[key];
+          const int32_t pg = static_cast<int32_t>(at >> 32), of = static_cast<int32_t>(at);
+          const uint8_t* src = base + wide(pg, page) + wide(of, slot);
+          if constexpr (FMT == KV_CACHE_SRC) {
+            const bool have = at >= 0 && piece * 16 < row_bytes;
+            copy_async<16>(ring + (static_cast<uint32_t>(u) % S::kUnits) * S::kUnit + swizzled(key, piece, kTileKeys),
+                           have ? src + piece * 16 : base, have ? 16u : 0u);
+          } else {
+            constexpr uint32_t kCode = FMT == KV_CACHE_E4M3FN ? 16 : 8;
+            const bool have = at >= 0 && piece * kCode < row_bytes;
+            const uint32_t dst = raw + (static_cast<uint32_t>(u) % S::kRawUnits) * S::kRaw + static_cast<uint32_t>(n) * kCode;
+            copy_async<kCode>(dst, have ? src + piece * kCode : base, have ? kCode : 0u);
+            if constexpr (FMT == KV_CACHE_E2M1) {
+              const uint8_t* sb = kv ? a.v_sc + kvh * a.vs_head : a.k_sc + kvh * a.ks_head;
+              const uint8_t* ss = sb + (have ? wide(pg, kv ? p.vs_page : p.ks_page) + wide(of, kv ? p.vs_slot : p.ks_slot) + piece : 0);
+              // the word around the scale's byte
+              const uint32_t mis = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(ss) & 3u);
+              copy_async<4>(raw + (static_cast<uint32_t>(u) % S::kRawUnits) * S::kRaw + S::kPer * kCopyThreads * 8 + static_cast<uint32_t>(n) * 4,
+                            ss - mis, have ? 4u : 0u);
+            }
+          }
+        }
+      }
+      commit_async();
+    };
+    if constexpr (FMT == KV_CACHE_SRC) {
+      look(0);
+      publish(0);
+      look(1);
+      for (int32_t u = 0; u < units && ok; ++u) {
+        const uint32_t slot = static_cast<uint32_t>(u) % S::kUnits, round = static_cast<uint32_t>(u) / S::kUnits;
+        if (round > 0) ok = bar_wait(empty + 8 * slot, (round - 1) & 1u, failed);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
+        issue(u);
+        if (u > 0) {  // the unit before has landed
+          wait_async<1>();
+          fence_async_shared();
+          bar_arrive(full + 8 * (static_cast<uint32_t>(u - 1) % S::kUnits));
+        }
+        if (u & 1) {
+          publish((u >> 1) + 1);
+          look((u >> 1) + 2);
+        }
+      }
+      wait_async<0>();
+      if (ok && units > 0) {
+        fence_async_shared();
+        bar_arrive(full + 8 * (static_cast<uint32_t>(units - 1) % S::kUnits));
+      }
+    } else {
+      look(0);
+      publish(0);
+      look(1);
+      auto issue_next = [&](int32_t u) {  // publishes the next tile behind its V
+        issue(u);
+        if (u & 1) {
+          publish((u >> 1) + 1);
+          look((u >> 1) + 2);
+        }
+      };
+      issue_next(0);
+      issue_next(1);
+      for (int32_t u = 0; u < units && ok; ++u) {
+        issue_next(u + 2);   // into the staging slot that unit u - 1 left
+        wait_async<2>();     // unit u has landed
+        const uint32_t slot = static_cast<uint32_t>(u) % S::kUnits, round = static_cast<uint32_t>(u) / S::kUnits;
+        if (round > 0) ok = bar_wait(empty + 8 * slot, (round - 1) & 1u, failed);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
+        const uint32_t from = raw + (static_cast<uint32_t>(u) % S::kRawUnits) * S::kRaw;
+        const uint8_t* sb = (u & 1) ? a.v_sc + kvh * a.vs_head : a.k_sc + kvh * a.ks_head;
+        (void)sb;
+#pragma unroll 2
+        for (int i = 0; i < S::kPer; ++i) {
+          const int32_t n = i * kCopyThreads + c;
+          if (S::kItems % kCopyThreads != 0 && n >= S::kItems) break;
+          const uint32_t key = static_cast<uint32_t>(n) / kPieces, piece = static_cast<uint32_t>(n) % kPieces;
+          uint32_t f[8];
+          if constexpr (FMT == KV_CACHE_E4M3FN) {
+            uint32_t w[4];
+            ld_own<16>(w, from + static_cast<uint32_t>(n) * 16);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              f[2 * x] = f16x2_from_e4m3x2(w[x]);
+              f[2 * x + 1] = f16x2_from_e4m3x2(w[x] >> 16);
+            }
+          } else {
+            uint32_t w[2];
+            ld_own<8>(w, from + static_cast<uint32_t>(n) * 8);
+            const uint32_t word = ld_shared_u32(from + S::kPer * kCopyThreads * 8 + static_cast<uint32_t>(n) * 4);
+            // where the scale's byte is in its word: as issue() found it
+            const int64_t at = rows[((u >> 1) & 3) * kTileKeys + key];
+            const uint32_t mis = at < 0 ? 0u : static_cast<uint32_t>(
+                reinterpret_cast<uintptr_t>(sb + wide(static_cast<int32_t>(at >> 32), (u & 1) ? p.vs_page : p.ks_page) +
+                                            wide(static_cast<int32_t>(at), (u & 1) ? p.vs_slot : p.ks_slot) + piece) & 3u);
+            const uint32_t sc = (word >> (8 * mis)) & 0xFFu;
+            const uint32_t s2 = f16x2_from_e4m3x2(sc * 0x0101u);
+            f16x2_from_e2m1x8(w[0], f);
+            f16x2_from_e2m1x8(w[1], f + 4);
+#pragma unroll
+            for (int x = 0; x < 8; ++x) f[x] = mul_f16x2(f[x], s2);
+          }
+          const uint32_t dst = ring + slot * S::kUnit;
+          st_shared16(dst + swizzled(key, 2 * piece, kTileKeys), f[0], f[1], f[2], f[3]);
+          st_shared16(dst + swizzled(key, 2 * piece + 1, kTileKeys), f[4], f[5], f[6], f[7]);
+        }
+        fence_async_shared();
+        bar_arrive(full + 8 * slot);
+      }
+      wait_async<0>();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (tid == 0 && *failed != 0) record_oob(a.err, static_cast<uint64_t>(b));
+  if (warp == 8) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host
+// ---------------------------------------------------------------------------
+
+template <int FMT, int DP, bool kBF16>
+kv_status launch_tile(TileParams p, cudaStream_t stream) {
+  auto* kernel = kv_attend_tile<FMT, DP, kBF16>;
+  constexpr int kSmem = TileSmem<FMT, DP>::kTotal;
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+  static SmemOptIn opt_in;
+  const kv_status st = opt_in(reinterpret_cast<const void*>(kernel), kSmem);
+  if (st != KV_OK) return st;
+  const int64_t grid = static_cast<int64_t>(p.blocks) * p.a.kv_heads;
+  if (grid > 0x7FFFFFFF) return KV_ERR_UNSUPPORTED;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(kTileThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
+  return e == cudaSuccess ? KV_OK : cuda_fail(e);
+}
+
+// The instantiations: 16-bit caches, and quantised ones.
+kv_status tile_src(const TileParams& p, cudaStream_t stream);
+kv_status tile_quant(const TileParams& p, kv_cache_format format, cudaStream_t stream);
+
+}  // namespace kvimpl
