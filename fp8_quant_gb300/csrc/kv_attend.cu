@@ -162,7 +162,15 @@ extern "C" kv_status kv_attend(const void* q, void* out, float* lse, const void*
       }
       tp.qpt = kTileRows / static_cast<int32_t>(p.group.d);
       tp.blocks = p.num_q / (2 * tp.qpt) + num_seqs;
-      return format == KV_CACHE_SRC ? tile_src(tp, stream) : tile_quant(tp, format, stream);
+      if (format != KV_CACHE_SRC) return tile_quant(tp, format, stream);
+      // TMA: a tile is whole pages, or part of one
+      if (page_size >= 8 && (page_size <= kTileKeys ? kTileKeys % page_size == 0 : page_size % kTileKeys == 0)) {
+        const int box = page_size < kTileKeys ? static_cast<int>(page_size) : kTileKeys;
+        if (tile_map(&tp.k_map, k_cache, p.bf16, head_dim, num_heads, page_size, num_pages, s->kc_head, s->kc_slot, s->kc_page, box) &&
+            tile_map(&tp.v_map, v_cache, p.bf16, head_dim, num_heads, page_size, num_pages, s->vc_head, s->vc_slot, s->vc_page, box))
+          tp.box = box;
+      }
+      return tile_src(tp, stream);
     }
     SplitParams sp = {};
     sp.a = p;

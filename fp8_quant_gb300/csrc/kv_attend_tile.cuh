@@ -15,11 +15,17 @@
 //                   memory), O_t += P_t V (P in TMEM, V as it lies: keys as
 //                   rows, head dims contiguous).  While one tile's softmax runs
 //                   the other tile's products do.
-//   warps 9-11      bring K and V from their pages into a ring of shared memory,
-//                   16 bytes a lane, in the 128-byte swizzle that the products
-//                   read; 16-bit rows go there by cp.async, quantised ones by
-//                   cp.async into a staging ring of the lane's own and from there
-//                   as fp16 (exact; see kv_attend_split.cuh).
+//   warps 9-15      bring K and V from their pages into a ring of shared memory,
+//                   in the 128-byte swizzle that the products read.  16-bit
+//                   tiles whose keys all exist go by TMA, a box for each page
+//                   and 64 dims, where pages divide or are divided by 128 keys;
+//                   others by cp.async, 16 bytes a lane, with zeros for keys that
+//                   no row needs.  Quantised rows go through registers, two units
+//                   ahead, and become fp16 on the way (exact; see
+//                   kv_attend_split.cuh).
+//
+// Registers: 512 threads are launched with 128 each; the softmax warps take 184
+// (a row's 128 scores stay in registers), the others leave 72.
 //
 // TMEM (512 columns): S_0/P_0, S_1/P_1 (128 each), O_0, O_1 (head_dim each).
 // The products of one CTA run in the order of their issue, so S_t of the next
@@ -28,6 +34,8 @@
 // Every wait has a limit (kSpin); a CTA whose wait ran out counts its sequence
 // in the error record, lets its copies and products end and leaves.
 #pragma once
+
+#include <cuda.h>  // CUtensorMap
 
 #include "kv_attend_split.cuh"
 
@@ -39,27 +47,29 @@ struct TileParams {
   int32_t ks_page, ks_slot, vs_page, vs_slot;  // of the block scales
   int32_t qpt;     // queries of a tile: 128 / group
   int32_t blocks;  // query blocks of the launch (an upper bound)
+  int32_t box;     // keys of a TMA box (a page, or 128 of one); 0: no TMA
+  CUtensorMap k_map, v_map;
 };
 
 constexpr int kTileRows = 128, kTileKeys = 128;
-constexpr int kTileThreads = 384;
-constexpr int kCopyThreads = 96;
+constexpr int kTileThreads = 512;
+constexpr int kCopyThreads = 224;
+constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;
+static_assert(256 * kSoftmaxRegs + 256 * kOtherRegs <= 65536, "the registers of the launch");
 constexpr uint32_t kSpin = 1u << 24;  // tries of a wait: far beyond any that ends
 
 template <int FMT, int DP>
 struct TileSmem {
-  static constexpr bool kQuant = FMT != KV_CACHE_SRC;
-  static constexpr int kUnits = kQuant ? 3 : 4;              // ring units: a K or a V tile in 16 bits
+  static constexpr int kUnits = 4;  // ring units: a K or a V tile in 16 bits
   static constexpr int kUnit = kTileKeys * DP * 2;
   static constexpr int kQ = kTileRows * DP * 2;
-  static constexpr int kItems = kQuant ? kTileKeys * DP / 16 : kTileKeys * DP / 8;  // a lane's pieces: 16 or 8 dims
-  static constexpr int kPer = (kItems + kCopyThreads - 1) / kCopyThreads;
-  static constexpr int kRawItem = FMT == KV_CACHE_E4M3FN ? 16 : FMT == KV_CACHE_E2M1 ? 12 : 0;
-  static constexpr int kRawUnits = kQuant ? 3 : 0;
-  static constexpr int kRaw = kPer * kCopyThreads * kRawItem;
+  // a lane's pieces of a unit: 8 dims (16-bit) or 16 (quantised) of every kStep-th key
+  static constexpr int kPieces = FMT == KV_CACHE_SRC ? DP / 8 : DP / 16;
+  static constexpr int kStep = kCopyThreads / kPieces;
+  static_assert(kCopyThreads % kPieces == 0, "a lane keeps its piece of the rows");
+  static constexpr int kPer = (kTileKeys + kStep - 1) / kStep;
   static constexpr int kOffRing = 2 * kQ;
-  static constexpr int kOffRaw = kOffRing + kUnits * kUnit;
-  static constexpr int kOffRows = kOffRaw + kRawUnits * kRaw;   // [4][128]: page << 32 | offset of a tile's keys, -1: not wanted
+  static constexpr int kOffRows = kOffRing + kUnits * kUnit;    // [4][128]: page << 32 | offset of a tile's keys, -1: not wanted
   static constexpr int kOffBad = kOffRows + 4 * kTileKeys * 8;  // [8][4] words: a tile's keys on bad pages
   static constexpr int kOffBars = kOffBad + 8 * 16;
   static constexpr int kBars = 2 * kUnits + 9;
@@ -74,6 +84,18 @@ __device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
 
 __device__ __forceinline__ void bar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// Arrives and expects `bytes` more of this phase by TMA.
+__device__ __forceinline__ void bar_arrive_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
+// A box of 64 dims x `box` keys of one head and page.
+__device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t dim, int32_t head,
+                                         int32_t key, int32_t page) {
+  asm volatile("cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];"
+               ::"r"(dst), "l"(map), "r"(bar), "r"(dim), "r"(head), "r"(key), "r"(page) : "memory");
 }
 
 __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
@@ -132,12 +154,11 @@ __device__ __forceinline__ void tc_ld32(uint32_t (&r)[32], uint32_t addr) {
                : KV_R16(r, 0), KV_R16(r, 16) : "r"(addr) : "memory");
 }
 
-__device__ __forceinline__ void tc_ld128(uint32_t (&r)[128], uint32_t addr) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x128.b32 "
-               "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63, %64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, %75, %76, %77, %78, %79, %80, %81, %82, %83, %84, %85, %86, %87, %88, %89, %90, %91, %92, %93, %94, %95, %96, %97, %98, %99, %100, %101, %102, %103, %104, %105, %106, %107, %108, %109, %110, %111, %112, %113, %114, %115, %116, %117, %118, %119, %120, %121, %122, %123, %124, %125, %126, %127}, [%128];\n\t"
+__device__ __forceinline__ void tc_ld64(uint32_t* r, uint32_t addr) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x64.b32 "
+               "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];\n\t"
                "tcgen05.wait::ld.sync.aligned;"
-               : KV_R16(r, 0), KV_R16(r, 16), KV_R16(r, 32), KV_R16(r, 48), KV_R16(r, 64), KV_R16(r, 80), KV_R16(r, 96), KV_R16(r, 112)
-               : "r"(addr) : "memory");
+               : KV_R16(r, 0), KV_R16(r, 16), KV_R16(r, 32), KV_R16(r, 48) : "r"(addr) : "memory");
 }
 
 __device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t (&r)[32]) {
@@ -263,7 +284,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
   const uint32_t tmem = sh_tmem;
   volatile int* const failed = &sh_failed;
 
+  // (all warps of a warpgroup execute the same one)
+  if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
   if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     // ======================================================================================
     // softmax of tile t: a thread a row
     // ======================================================================================
@@ -326,7 +350,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
         }
         tc_fence_after();
         uint32_t sw[kTileKeys];
-        tc_ld128(sw, s_at);
+        tc_ld64(sw, s_at);
+        tc_ld64(sw + 64, s_at + 64);
         float s[kTileKeys];
 #pragma unroll
         for (int i = 0; i < kTileKeys; ++i) s[i] = __uint_as_float(sw[i]);
@@ -495,173 +520,200 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
     int64_t* const rows = reinterpret_cast<int64_t*>(smem_ptr + S::kOffRows);
     const int32_t* table = a.table + static_cast<int64_t>(b) * a.table_stride;
     const uint32_t row_bytes = static_cast<uint32_t>(a.head_dim) * (FMT == KV_CACHE_SRC ? 16 : FMT == KV_CACHE_E4M3FN ? 8 : 4) / 8;
-    const int32_t units = 2 * list.n;
+    const uint8_t* const kbase = a.k + kvh * a.k_head;
+    const uint8_t* const vbase = a.v + kvh * a.v_head;
+    const uint32_t piece = static_cast<uint32_t>(c) % S::kPieces, key0 = static_cast<uint32_t>(c) / S::kPieces;
     bool ok = true;
-    // page id and offset of key c (and c + 96) of a tile: id -1: not wanted
-    int32_t id[2];
-    uint32_t off[2];
+    uint32_t published = 0u;
+    // page id and offset of key c of a tile (the first four of the warps); id -1: not wanted
+    int32_t id = -1;
+    uint32_t off = 0u;
     auto look = [&](int32_t j) {
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int32_t key = c + kCopyThreads * x;
-        id[x] = -1;
-        off[x] = 0u;
-        if (key < kTileKeys && j < list.n) {
-          const int32_t k = list.tile(j) * kTileKeys + key;
-          if (k <= p_hi && (k >= list.lo_key || k < a.sinks)) {
-            const uint32_t pg = a.page.quot(static_cast<uint32_t>(k));
-            off[x] = static_cast<uint32_t>(k) - pg * a.page.d;
-            const int32_t v = __ldg(table + pg);
-            id[x] = v < 0 ? -2 : v;
-          }
+      id = -1;
+      if (c < kTileKeys && j < list.n) {
+        const int32_t k = list.tile(j) * kTileKeys + c;
+        if (k <= p_hi && (k >= list.lo_key || k < a.sinks)) {
+          const uint32_t pg = a.page.quot(static_cast<uint32_t>(k));
+          off = static_cast<uint32_t>(k) - pg * a.page.d;
+          const int32_t v = __ldg(table + pg);
+          id = v < 0 ? -2 : v;
         }
       }
     };
-    // The keys of tile j for all lanes of the three warps.  Four buffers: a lane may still read tile
-    // j - 2 (the scales of its staged pieces), and none is more than one tile ahead of another.
+    // The keys of tile j for all lanes.  Four buffers: no lane is more than a tile ahead of another.
     auto publish = [&](int32_t j) {
       if (j >= list.n || !ok) return;
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int32_t key = c + kCopyThreads * x;
-        const bool is_bad = id[x] == -2 || id[x] >= a.num_pages;
+      if (c < kTileKeys) {
+        const bool is_bad = id == -2 || id >= a.num_pages;
         const uint32_t bits = __ballot_sync(0xFFFFFFFFu, is_bad);
-        if (is_bad) {
-          record_oob(a.err, static_cast<uint64_t>(b));
-          id[x] = -1;
-        }
-        if (key < kTileKeys) {
-          if (lane == 0u) bad_words[4 * (j & 7) + (key >> 5)] = bits;
-          rows[(j & 3) * kTileKeys + key] = id[x] < 0 ? -1 : (static_cast<int64_t>(id[x]) << 32) | off[x];
-        }
+        if (is_bad) record_oob(a.err, static_cast<uint64_t>(b));
+        if (lane == 0u) bad_words[4 * (j & 7) + (c >> 5)] = bits;
+        rows[(j & 3) * kTileKeys + c] = id < 0 || is_bad ? -1 : (static_cast<int64_t>(id) << 32) | off;
       }
       bar_arrive(rows_full);
-      ok = __all_sync(0xFFFFFFFFu, bar_wait(rows_full, j & 1, failed));
+      ok = __all_sync(0xFFFFFFFFu, bar_wait(rows_full, published & 1u, failed));
+      ++published;
     };
-    constexpr int kPieces = TileSmem<FMT, DP>::kQuant ? DP / 16 : DP / 8;  // of a row
-    const uint32_t raw = smem + S::kOffRaw;
-    auto issue = [&](int32_t u) {
-      if (u < units) {
-        const int32_t j = u >> 1, kv = u & 1;
-        const int64_t* rw = rows + (j & 3) * kTileKeys;
-        const uint8_t* base = kv ? a.v + kvh * a.v_head : a.k + kvh * a.k_head;
-        const int32_t page = kv ? p.v_page : p.k_page, slot = kv ? p.v_slot : p.k_slot;
-#pragma unroll 4
+    auto wait_empty = [&](int32_t u) {
+      const uint32_t round = static_cast<uint32_t>(u) / S::kUnits;
+      if (ok && round > 0) ok = __all_sync(0xFFFFFFFFu, bar_wait(empty + 8 * (static_cast<uint32_t>(u) % S::kUnits), (round - 1) & 1u, failed));
+    };
+    if constexpr (FMT == KV_CACHE_SRC) {
+      auto copy_unit = [&](int32_t u) {  // by cp.async, from the published rows
+        const int64_t* rw = rows + ((u >> 1) & 3) * kTileKeys;
+        const uint8_t* base = (u & 1) ? vbase : kbase;
+        const int32_t page = (u & 1) ? p.v_page : p.k_page, slot = (u & 1) ? p.v_slot : p.k_slot;
+        const uint32_t unit = ring + (static_cast<uint32_t>(u) % S::kUnits) * S::kUnit;
+#pragma unroll
         for (int i = 0; i < S::kPer; ++i) {
-          const int32_t n = i * kCopyThreads + c;
-          if (S::kItems % kCopyThreads != 0 && n >= S::kItems) break;
-          const uint32_t key = static_cast<uint32_t>(n) / kPieces, piece = static_cast<uint32_t>(n) % kPieces;
+          const uint32_t key = key0 + i * S::kStep;
+          if (kTileKeys % S::kStep != 0 && key >= kTileKeys) break;
           const int64_t at = rw[key];
-          const int32_t pg = static_cast<int32_t>(at >> 32), of = static_cast<int32_t>(at);
-          const uint8_t* src = base + wide(pg, page) + wide(of, slot);
-          if constexpr (FMT == KV_CACHE_SRC) {
-            const bool have = at >= 0 && piece * 16 < row_bytes;
-            copy_async<16>(ring + (static_cast<uint32_t>(u) % S::kUnits) * S::kUnit + swizzled(key, piece, kTileKeys),
-                           have ? src + piece * 16 : base, have ? 16u : 0u);
-          } else {
-            constexpr uint32_t kCode = FMT == KV_CACHE_E4M3FN ? 16 : 8;
-            const bool have = at >= 0 && piece * kCode < row_bytes;
-            const uint32_t dst = raw + (static_cast<uint32_t>(u) % S::kRawUnits) * S::kRaw + static_cast<uint32_t>(n) * kCode;
-            copy_async<kCode>(dst, have ? src + piece * kCode : base, have ? kCode : 0u);
-            if constexpr (FMT == KV_CACHE_E2M1) {
-              const uint8_t* sb = kv ? a.v_sc + kvh * a.vs_head : a.k_sc + kvh * a.ks_head;
-              const uint8_t* ss = sb + (have ? wide(pg, kv ? p.vs_page : p.ks_page) + wide(of, kv ? p.vs_slot : p.ks_slot) + piece : 0);
-              // the word around the scale's byte
-              const uint32_t mis = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(ss) & 3u);
-              copy_async<4>(raw + (static_cast<uint32_t>(u) % S::kRawUnits) * S::kRaw + S::kPer * kCopyThreads * 8 + static_cast<uint32_t>(n) * 4,
-                            ss - mis, have ? 4u : 0u);
+          const bool have = at >= 0 && piece * 16 < row_bytes;
+          const uint8_t* src = base + (have ? wide(static_cast<int32_t>(at >> 32), page) + wide(static_cast<int32_t>(at), slot) + piece * 16 : 0);
+          copy_async<16>(unit + swizzled(key, piece, kTileKeys), src, have ? 16u : 0u);
+        }
+      };
+      // TMA: lane i of warp 9 takes the tile's i-th page; every warp knows whether all are there
+      const int32_t boxes = p.box > 0 ? kTileKeys / p.box : 0;
+      auto first_page = [&](int32_t j) -> int32_t {
+        if (j >= list.n || static_cast<int32_t>(lane) >= boxes) return 0;
+        const int32_t k = list.tile(j) * kTileKeys + static_cast<int32_t>(lane) * p.box;
+        return k < seq.len ? __ldg(table + a.page.quot(static_cast<uint32_t>(k))) : -1;
+      };
+      int32_t next = first_page(0);
+      for (int32_t j = 0; j < list.n && ok; ++j) {
+        const int32_t j0 = list.tile(j) * kTileKeys;
+        const int32_t mine = next;
+        next = first_page(j + 1);
+        const bool whole = boxes > 0 && j0 + kTileKeys <= seq.len &&
+                           __all_sync(0xFFFFFFFFu, mine >= 0 && mine < a.num_pages);
+        if (whole) {
+          if (warp == 9 && lane < 4u) bad_words[4 * (j & 7) + lane] = 0u;
+          __syncwarp();
+          for (int kv = 0; kv < 2; ++kv) {
+            const int32_t u = 2 * j + kv;
+            wait_empty(u);
+            if (!ok) break;
+            const uint32_t slot = static_cast<uint32_t>(u) % S::kUnits, bar = full + 8 * slot;
+            if (c == 0) bar_arrive_expect(bar, S::kUnit); else bar_arrive(bar);
+            __syncwarp();
+            if (warp == 9 && static_cast<int32_t>(lane) < boxes) {
+              const uint32_t k = static_cast<uint32_t>(j0) + lane * static_cast<uint32_t>(p.box);
+              const int32_t key = static_cast<int32_t>(k - a.page.quot(k) * a.page.d);
+#pragma unroll
+              for (int x = 0; x < DP / 64; ++x)
+                tma_rows(ring + slot * S::kUnit + x * (kTileKeys * 128) + lane * static_cast<uint32_t>(p.box) * 128u,
+                         kv ? &p.v_map : &p.k_map, bar, 64 * x, kvh, key, mine);
             }
+          }
+        } else {
+          look(j);
+          publish(j);
+          for (int kv = 0; kv < 2; ++kv) {
+            const int32_t u = 2 * j + kv;
+            wait_empty(u);
+            if (!ok) break;
+            copy_unit(u);
+            commit_async();
+          }
+          if (ok) {
+            wait_async<1>();
+            fence_async_shared();
+            bar_arrive(full + 8 * (static_cast<uint32_t>(2 * j) % S::kUnits));
+          }
+          wait_async<0>();
+          if (ok) {
+            fence_async_shared();
+            bar_arrive(full + 8 * (static_cast<uint32_t>(2 * j + 1) % S::kUnits));
           }
         }
       }
-      commit_async();
-    };
-    if constexpr (FMT == KV_CACHE_SRC) {
-      look(0);
-      publish(0);
-      look(1);
-      for (int32_t u = 0; u < units && ok; ++u) {
-        const uint32_t slot = static_cast<uint32_t>(u) % S::kUnits, round = static_cast<uint32_t>(u) / S::kUnits;
-        if (round > 0) ok = bar_wait(empty + 8 * slot, (round - 1) & 1u, failed);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) break;
-        issue(u);
-        if (u > 0) {  // the unit before has landed
-          wait_async<1>();
-          fence_async_shared();
-          bar_arrive(full + 8 * (static_cast<uint32_t>(u - 1) % S::kUnits));
-        }
-        if (u & 1) {
-          publish((u >> 1) + 1);
-          look((u >> 1) + 2);
-        }
-      }
-      wait_async<0>();
-      if (ok && units > 0) {
-        fence_async_shared();
-        bar_arrive(full + 8 * (static_cast<uint32_t>(units - 1) % S::kUnits));
+      if (!ok) {
+        // boxes in flight write shared memory: let them end before the CTA does
+        for (int i = 0; i < S::kUnits; ++i)
+          for (uint32_t n = 0; n < 4096u && !bar_try(full + 8 * i, 0) && !bar_try(full + 8 * i, 1); ++n) {}
       }
     } else {
-      look(0);
-      publish(0);
-      look(1);
-      auto issue_next = [&](int32_t u) {  // publishes the next tile behind its V
-        issue(u);
-        if (u & 1) {
-          publish((u >> 1) + 1);
-          look((u >> 1) + 2);
+      // the raw pieces of a unit in registers: codes (and, e2m1, their block's scale)
+      constexpr int kWords = FMT == KV_CACHE_E4M3FN ? 4 : 2;
+      struct Raw {
+        uint32_t w[S::kPer][kWords];
+        uint32_t sc[FMT == KV_CACHE_E2M1 ? S::kPer : 1];
+      };
+      auto load = [&](int32_t u, Raw& r) {
+        const int64_t* rw = rows + ((u >> 1) & 3) * kTileKeys;
+        const uint8_t* base = (u & 1) ? vbase : kbase;
+        const int32_t page = (u & 1) ? p.v_page : p.k_page, slot = (u & 1) ? p.v_slot : p.k_slot;
+#pragma unroll
+        for (int i = 0; i < S::kPer; ++i) {
+          const uint32_t key = key0 + i * S::kStep;
+#pragma unroll
+          for (int x = 0; x < kWords; ++x) r.w[i][x] = 0u;
+          if (FMT == KV_CACHE_E2M1) r.sc[FMT == KV_CACHE_E2M1 ? i : 0] = 0u;
+          if (u >= 2 * list.n || (kTileKeys % S::kStep != 0 && key >= kTileKeys)) continue;
+          const int64_t at = rw[key];
+          if (at < 0 || piece * (4 * kWords) >= row_bytes) continue;
+          const int32_t pg = static_cast<int32_t>(at >> 32), of = static_cast<int32_t>(at);
+          const uint8_t* src = base + wide(pg, page) + wide(of, slot) + piece * (4 * kWords);
+          if constexpr (FMT == KV_CACHE_E4M3FN) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4*>(src));
+            r.w[i][0] = v.x; r.w[i][1] = v.y; r.w[i][2] = v.z; r.w[i][3] = v.w;
+          } else {
+            const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
+            r.w[i][0] = v.x; r.w[i][1] = v.y;
+            const uint8_t* ss = (u & 1) ? a.v_sc + kvh * a.vs_head + wide(pg, p.vs_page) + wide(of, p.vs_slot)
+                                        : a.k_sc + kvh * a.ks_head + wide(pg, p.ks_page) + wide(of, p.ks_slot);
+            r.sc[i] = __ldg(ss + piece);
+          }
         }
       };
-      issue_next(0);
-      issue_next(1);
-      for (int32_t u = 0; u < units && ok; ++u) {
-        issue_next(u + 2);   // into the staging slot that unit u - 1 left
-        wait_async<2>();     // unit u has landed
-        const uint32_t slot = static_cast<uint32_t>(u) % S::kUnits, round = static_cast<uint32_t>(u) / S::kUnits;
-        if (round > 0) ok = bar_wait(empty + 8 * slot, (round - 1) & 1u, failed);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) break;
-        const uint32_t from = raw + (static_cast<uint32_t>(u) % S::kRawUnits) * S::kRaw;
-        const uint8_t* sb = (u & 1) ? a.v_sc + kvh * a.vs_head : a.k_sc + kvh * a.ks_head;
-        (void)sb;
-#pragma unroll 2
+      auto store = [&](int32_t u, const Raw& r) {
+        const uint32_t unit = ring + (static_cast<uint32_t>(u) % S::kUnits) * S::kUnit;
+#pragma unroll
         for (int i = 0; i < S::kPer; ++i) {
-          const int32_t n = i * kCopyThreads + c;
-          if (S::kItems % kCopyThreads != 0 && n >= S::kItems) break;
-          const uint32_t key = static_cast<uint32_t>(n) / kPieces, piece = static_cast<uint32_t>(n) % kPieces;
+          const uint32_t key = key0 + i * S::kStep;
+          if (kTileKeys % S::kStep != 0 && key >= kTileKeys) break;
           uint32_t f[8];
           if constexpr (FMT == KV_CACHE_E4M3FN) {
-            uint32_t w[4];
-            ld_own<16>(w, from + static_cast<uint32_t>(n) * 16);
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-              f[2 * x] = f16x2_from_e4m3x2(w[x]);
-              f[2 * x + 1] = f16x2_from_e4m3x2(w[x] >> 16);
+              f[2 * x] = f16x2_from_e4m3x2(r.w[i][x]);
+              f[2 * x + 1] = f16x2_from_e4m3x2(r.w[i][x] >> 16);
             }
           } else {
-            uint32_t w[2];
-            ld_own<8>(w, from + static_cast<uint32_t>(n) * 8);
-            const uint32_t word = ld_shared_u32(from + S::kPer * kCopyThreads * 8 + static_cast<uint32_t>(n) * 4);
-            // where the scale's byte is in its word: as issue() found it
-            const int64_t at = rows[((u >> 1) & 3) * kTileKeys + key];
-            const uint32_t mis = at < 0 ? 0u : static_cast<uint32_t>(
-                reinterpret_cast<uintptr_t>(sb + wide(static_cast<int32_t>(at >> 32), (u & 1) ? p.vs_page : p.ks_page) +
-                                            wide(static_cast<int32_t>(at), (u & 1) ? p.vs_slot : p.ks_slot) + piece) & 3u);
-            const uint32_t sc = (word >> (8 * mis)) & 0xFFu;
-            const uint32_t s2 = f16x2_from_e4m3x2(sc * 0x0101u);
-            f16x2_from_e2m1x8(w[0], f);
-            f16x2_from_e2m1x8(w[1], f + 4);
+            const uint32_t s2 = f16x2_from_e4m3x2(r.sc[i] * 0x0101u);
+            f16x2_from_e2m1x8(r.w[i][0], f);
+            f16x2_from_e2m1x8(r.w[i][1], f + 4);
 #pragma unroll
             for (int x = 0; x < 8; ++x) f[x] = mul_f16x2(f[x], s2);
           }
-          const uint32_t dst = ring + slot * S::kUnit;
-          st_shared16(dst + swizzled(key, 2 * piece, kTileKeys), f[0], f[1], f[2], f[3]);
-          st_shared16(dst + swizzled(key, 2 * piece + 1, kTileKeys), f[4], f[5], f[6], f[7]);
+          st_shared16(unit + swizzled(key, 2 * piece, kTileKeys), f[0], f[1], f[2], f[3]);
+          st_shared16(unit + swizzled(key, 2 * piece + 1, kTileKeys), f[4], f[5], f[6], f[7]);
         }
         fence_async_shared();
-        bar_arrive(full + 8 * slot);
+        bar_arrive(full + 8 * (static_cast<uint32_t>(u) % S::kUnits));
+      };
+      Raw kr, vr;
+      look(0);
+      publish(0);
+      look(1);
+      if (ok) {
+        load(0, kr);
+        load(1, vr);
       }
-      wait_async<0>();
+      for (int32_t j = 0; j < list.n && ok; ++j) {
+        publish(j + 1);
+        look(j + 2);
+        wait_empty(2 * j);
+        if (!ok) break;
+        store(2 * j, kr);
+        load(2 * j + 2, kr);
+        wait_empty(2 * j + 1);
+        if (!ok) break;
+        store(2 * j + 1, vr);
+        load(2 * j + 3, vr);
+      }
     }
   }
   tc_fence_before();
@@ -700,6 +752,11 @@ kv_status launch_tile(TileParams p, cudaStream_t stream) {
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
   return e == cudaSuccess ? KV_OK : cuda_fail(e);
 }
+
+// The tensor map of a 16-bit cache for boxes of 64 dims x `box` keys of one head and page; false where
+// there is none (a stride that TMA does not take).
+bool tile_map(CUtensorMap* map, const void* cache, bool bf16, int head_dim, int heads, int64_t page_size, int64_t pages,
+              int64_t head_stride, int64_t slot_stride, int64_t page_stride, int box);
 
 // The instantiations: 16-bit caches, and quantised ones.
 kv_status tile_src(const TileParams& p, cudaStream_t stream);
