@@ -122,21 +122,24 @@ __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence:
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// The products and their commits: executed by a whole, converged warp, issued by
+// one lane of it, so that descriptors and addresses stay in uniform registers.
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xFFFFFFFF;\n\t"
+               "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar) : "memory");
 }
 
 // D (TMEM) = or += A (shared memory) B (shared memory)
 __device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-               "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+  asm volatile("{\n\t.reg .pred e, p;\n\telect.sync _|e, 0xFFFFFFFF;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+               "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
                ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u) : "memory");
 }
 
 // D (TMEM) = or += A (TMEM) B (shared memory)
 __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-               "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+  asm volatile("{\n\t.reg .pred e, p;\n\telect.sync _|e, 0xFFFFFFFF;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+               "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
                ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u) : "memory");
 }
 
@@ -193,6 +196,24 @@ __device__ __forceinline__ uint32_t swizzled(uint32_t row, uint32_t piece, uint3
 
 __device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+// x * s + t and x + y for both lanes, in one instruction each.
+__device__ __forceinline__ float2 fma2(float2 x, float s, float t) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %4};\n\tmov.b64 c, {%5, %5};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(r.x), "=f"(r.y) : "f"(x.x), "f"(x.y), "f"(s), "f"(t));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 x, float2 y) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(r.x), "=f"(r.y) : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+  return r;
 }
 
 template <int FMT, int DP, bool kBF16>
@@ -375,9 +396,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
               if ((see & (1u << i)) == 0u) s[32 * c + i] = -INFINITY;
           }
         }
-        float x = s[0];
+        float xs[8];
 #pragma unroll
-        for (int i = 1; i < kTileKeys; ++i) x = fmaxf(x, s[i]);
+        for (int i = 0; i < 8; ++i) xs[i] = fmaxf(s[i], s[i + 8]);
+#pragma unroll
+        for (int i = 16; i < kTileKeys; i += 16)
+#pragma unroll
+          for (int y = 0; y < 8; ++y) xs[y] = fmaxf(xs[y], fmaxf(s[i + y], s[i + 8 + y]));
+        float x = fmaxf(fmaxf(fmaxf(xs[0], xs[1]), fmaxf(xs[2], xs[3])), fmaxf(fmaxf(xs[4], xs[5]), fmaxf(xs[6], xs[7])));
         x *= scale;
         // a maximum that grew little is kept (the weights stay below 2^8)
         const bool grow = x > m + 8.0f || (m == -INFINITY && x > m);
@@ -399,21 +425,24 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
           }
         }
         const float ref = m == -INFINITY ? 0.0f : m;
-        float sum0 = 0.0f, sum1 = 0.0f;
+        // pairs of weights: one packed product and sum for both
+        float2 sum[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) sum[y] = make_float2(0.0f, 0.0f);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           uint32_t w[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            const float e0 = exp2_fast(__fmaf_rn(s[64 * c + 2 * i], scale, -ref));
-            const float e1 = exp2_fast(__fmaf_rn(s[64 * c + 2 * i + 1], scale, -ref));
-            sum0 += e0;
-            sum1 += e1;
-            w[i] = pack2(e0, e1, kBF16);
+            const float2 z = fma2(make_float2(s[64 * c + 2 * i], s[64 * c + 2 * i + 1]), scale, -ref);
+            const float2 e = make_float2(exp2_fast(z.x), exp2_fast(z.y));
+            sum[i & 3] = add2(sum[i & 3], e);
+            w[i] = pack2(e.x, e.y, kBF16);
           }
           tc_st32(s_at + 32 * c, w);
         }
-        l += sum0 + sum1;
+        sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+        l += sum[0].x + sum[0].y;
         tc_wait_st();
         tc_fence_before();
         bar_arrive(p_full + 8 * t);
@@ -470,18 +499,18 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
       if (ok) ok = __all_sync(0xFFFFFFFFu, bar_wait(bar, parity, failed));
       if (ok) tc_fence_after();
     };
+    // descriptors of the operands' first pieces; the others are constant steps (in 16 bytes) away
+    const uint64_t q_desc = smem_desc(smem, 16), k_desc = smem_desc(ring, 16), v_desc = smem_desc(ring, kTileKeys * 128);
     auto scores = [&](int32_t t, int32_t j) {  // S_t = Q_t K_j^T
-      if (ok && lane == 0u) {
-        const uint32_t q = smem + t * S::kQ, k = ring + slot_of(2 * j) * S::kUnit;
+      if (!ok) return;
+      const uint64_t q = q_desc + static_cast<uint32_t>(t) * (S::kQ >> 4), k = k_desc + slot_of(2 * j) * (S::kUnit >> 4);
 #pragma unroll
-        for (int i = 0; i < DP / 16; ++i) {
-          const uint32_t at = (i / 4) * (kTileRows * 128) + (i % 4) * 32;
-          tc_mma_ss(tmem + t * 128, smem_desc(q + at, 16), smem_desc(k + at, 16), qk_desc, i > 0);
-        }
-        tc_commit(s_full + 8 * t);
-        if (t == tiles - 1) tc_commit(empty + 8 * slot_of(2 * j));
+      for (int i = 0; i < DP / 16; ++i) {
+        const uint32_t at = ((i / 4) * (kTileRows * 128) + (i % 4) * 32) >> 4;
+        tc_mma_ss(tmem + t * 128, q + at, k + at, qk_desc, i > 0);
       }
-      __syncwarp();
+      tc_commit(s_full + 8 * t);
+      if (t == tiles - 1) tc_commit(empty + 8 * slot_of(2 * j));
     };
     for (int32_t t = 0; t < tiles && list.n > 0; ++t) {
       wait(q_full + 8 * t, 0);
@@ -492,22 +521,21 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
       for (int32_t t = 0; t < tiles; ++t) {
         if (t == 0) wait(full + 8 * slot_of(2 * j + 1), round_of(2 * j + 1));
         wait(p_full + 8 * t, j & 1);
-        if (ok && lane == 0u) {  // O_t += P_t V_j
-          const uint32_t v = ring + slot_of(2 * j + 1) * S::kUnit;
+        if (ok) {  // O_t += P_t V_j
+          const uint64_t v = v_desc + slot_of(2 * j + 1) * (S::kUnit >> 4);
 #pragma unroll
           for (int i = 0; i < kTileKeys / 16; ++i)
-            tc_mma_ts(tmem + 256 + t * DP, tmem + t * 128 + i * 8, smem_desc(v + i * 2048, kTileKeys * 128), pv_desc, j > 0 || i > 0);
+            tc_mma_ts(tmem + 256 + t * DP, tmem + t * 128 + i * 8, v + i * (2048 >> 4), pv_desc, j > 0 || i > 0);
           if (t == tiles - 1) tc_commit(empty + 8 * slot_of(2 * j + 1));
           if (j == list.n - 1) tc_commit(o_full + 8 * t);
         }
-        __syncwarp();
         if (j + 1 < list.n) {
           if (t == 0) wait(full + 8 * slot_of(2 * j + 2), round_of(2 * j + 2));
           scores(t, j + 1);
         }
       }
     }
-    if (!ok && lane == 0u) {  // products still in flight read shared memory and write TMEM: let them end
+    if (!ok) {  // products still in flight read shared memory and write TMEM: let them end
       tc_commit(o_full);
       for (uint32_t i = 0; i < kSpin && !bar_try(o_full, 0); ++i) {}
     }
