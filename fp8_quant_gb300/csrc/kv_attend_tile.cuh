@@ -31,8 +31,12 @@
 // The products of one CTA run in the order of their issue, so S_t of the next
 // keys may overwrite P_t behind O_t's product without a wait between.
 //
-// Every wait has a limit (kSpin); a CTA whose wait ran out counts its sequence
-// in the error record, lets its copies and products end and leaves.
+// A CTA stays and takes item after item (one CTA an SM): the copies run ahead
+// into the next item's keys and its queries are loaded while the last one's
+// softmax ends and its rows are written.
+//
+// Every wait has a limit (kSpin); a CTA whose wait ran out counts that in the
+// error record, lets its copies and products end and leaves.
 #pragma once
 
 #include <cuda.h>  // CUtensorMap
@@ -54,7 +58,7 @@ struct TileParams {
 constexpr int kTileRows = 128, kTileKeys = 128;
 constexpr int kTileThreads = 512;
 constexpr int kCopyThreads = 224;
-constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;
+constexpr int kSoftmaxRegs = 176, kOtherRegs = 80;
 static_assert(256 * kSoftmaxRegs + 256 * kOtherRegs <= 65536, "the registers of the launch");
 constexpr uint32_t kSpin = 1u << 24;  // tries of a wait: far beyond any that ends
 
@@ -69,10 +73,8 @@ struct TileSmem {
   static_assert(kCopyThreads % kPieces == 0, "a lane keeps its piece of the rows");
   static constexpr int kPer = (kTileKeys + kStep - 1) / kStep;
   static constexpr int kOffRing = 2 * kQ;
-  static constexpr int kOffRows = kOffRing + kUnits * kUnit;    // [4][128]: page << 32 | offset of a tile's keys, -1: not wanted
-  static constexpr int kOffBad = kOffRows + 4 * kTileKeys * 8;  // [8][4] words: a tile's keys on bad pages
-  static constexpr int kOffBars = kOffBad + 8 * 16;
-  static constexpr int kBars = 2 * kUnits + 9;
+  static constexpr int kOffBars = kOffRing + kUnits * kUnit;
+  static constexpr int kBars = 2 * kUnits + 11;
   static constexpr int kTotal = kOffBars + kBars * 8 + 1024;    // the base is aligned to 1,024
 };
 
@@ -216,69 +218,69 @@ __device__ __forceinline__ float2 add2(float2 x, float2 y) {
   return r;
 }
 
+// One item: a block of up to 2 * qpt queries of a sequence, for one KV head.
+struct TileItem {
+  int32_t b, kvh, tiles;
+  AttendSeq seq;
+  int32_t q_first, nq;   // the block's first query in its sequence, and their number
+  int32_t p_first, p_hi; // positions of the first and the last
+  TileList list;
+};
+
+// The CTA's item of a round, by a whole warp; false behind the last.  Blocks of
+// a sequence come with the last queries, which see the most keys, first, and
+// every second round runs the other way, so that CTAs get long and short ones.
+__device__ __forceinline__ bool tile_item(const TileParams& p, int32_t round, TileItem* it) {
+  const AttendParams& a = p.a;
+  const uint32_t lane = threadIdx.x & 31u;
+  const int64_t n = static_cast<int64_t>(round) * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+  if (n >= static_cast<int64_t>(p.blocks) * a.kv_heads) return false;
+  const int32_t want = static_cast<int32_t>(n / a.kv_heads);
+  it->kvh = static_cast<int32_t>(n - static_cast<int64_t>(want) * a.kv_heads);
+  int32_t before = 0;
+  for (int32_t b0 = 0; b0 < a.num_seqs; b0 += 32) {
+    const int32_t b = b0 + static_cast<int32_t>(lane);
+    const int32_t k = b < a.num_seqs ? (attend_seq(a, b, false).nq + 2 * p.qpt - 1) / (2 * p.qpt) : 0;
+    int32_t incl = k;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      if (lane >= static_cast<uint32_t>(o)) incl += v;
+    }
+    const int32_t at = before + incl - k;
+    const uint32_t hit = __ballot_sync(0xFFFFFFFFu, want >= at && want < at + k);
+    if (hit != 0u) {
+      const int src = __ffs(static_cast<int>(hit)) - 1;
+      it->b = b0 + src;
+      it->q_first = __shfl_sync(0xFFFFFFFFu, k - 1 - (want - at), src) * 2 * p.qpt;
+      it->seq = attend_seq(a, it->b, false);
+      it->nq = min(2 * p.qpt, it->seq.nq - it->q_first);
+      it->tiles = it->nq > p.qpt ? 2 : 1;
+      it->p_first = it->seq.len - it->seq.nq + it->q_first;
+      it->p_hi = it->p_first + it->nq - 1;
+      it->list = visible_tiles<kTileKeys>(a, it->p_first, it->p_hi);
+      return true;
+    }
+    before += __shfl_sync(0xFFFFFFFFu, incl, 31);
+  }
+  return false;
+}
+
 template <int FMT, int DP, bool kBF16>
 __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_constant__ TileParams p) {
   using S = TileSmem<FMT, DP>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  __shared__ int32_t sh_item[2];   // the CTA's sequence and query block
   __shared__ uint32_t sh_tmem;
-  __shared__ volatile int sh_failed;
+  __shared__ volatile int sh_failed;  // a wait ran out
+  __shared__ volatile int sh_bad;     // a page id out of range was met: the CTA's rows are done again
 
   const AttendParams& a = p.a;
   const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31u;
   const uint32_t smem = (static_cast<uint32_t>(__cvta_generic_to_shared(smem_raw)) + 1023u) & ~1023u;
-  uint8_t* const smem_ptr = smem_raw + (smem - static_cast<uint32_t>(__cvta_generic_to_shared(smem_raw)));
   const int32_t G = static_cast<int32_t>(a.group.d);
-  grid_handover();
-
-  // -- which sequence, which queries --------------------------------------------------------
-  const int32_t kvh = static_cast<int32_t>(blockIdx.x % static_cast<uint32_t>(a.kv_heads));
-  const int32_t want = static_cast<int32_t>(blockIdx.x / static_cast<uint32_t>(a.kv_heads));
-  if (warp == 0) {
-    int32_t before = 0, found = -1, block = 0;
-    for (int32_t b0 = 0; b0 < a.num_seqs && found < 0; b0 += 32) {
-      const int32_t b = b0 + static_cast<int32_t>(lane);
-      int32_t n = 0;
-      if (b < a.num_seqs) n = (attend_seq(a, b, blockIdx.x == 0).nq + 2 * p.qpt - 1) / (2 * p.qpt);
-      int32_t incl = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int32_t v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-        if (lane >= static_cast<uint32_t>(o)) incl += v;
-      }
-      const int32_t at = before + incl - n;
-      const uint32_t hit = __ballot_sync(0xFFFFFFFFu, want >= at && want < at + n);
-      if (hit != 0u) {
-        const int src = __ffs(static_cast<int>(hit)) - 1;
-        found = b0 + src;
-        // the last queries, which see the most keys, first
-        block = __shfl_sync(0xFFFFFFFFu, n - 1 - (want - at), src);
-      }
-      before += __shfl_sync(0xFFFFFFFFu, incl, 31);
-    }
-    if (blockIdx.x == 0 && found >= 0)  // lengths out of range are recorded behind it too
-      for (int32_t b = (found / 32 + 1) * 32 + static_cast<int32_t>(lane); b < a.num_seqs; b += 32) attend_seq(a, b, true);
-    if (lane == 0u) {
-      sh_item[0] = found;
-      sh_item[1] = block;
-      sh_failed = 0;
-    }
-  }
-  __syncthreads();
-  const int32_t b = sh_item[0];
-  if (b < 0) return;
-  const AttendSeq seq = attend_seq(a, b, false);
-  const int32_t q_first = sh_item[1] * 2 * p.qpt;            // the block's first query in its sequence
-  const int32_t nq = min(2 * p.qpt, seq.nq - q_first);       // and their number
-  const int32_t tiles = nq > p.qpt ? 2 : 1;
-  const int32_t p_first = seq.len - seq.nq + q_first;        // position of the first
-  const TileList list = visible_tiles<kTileKeys>(a, p_first, p_first + nq - 1);
-  const int32_t p_hi = p_first + nq - 1;
-
   const uint32_t ring = smem + S::kOffRing;
-  const uint32_t bars = smem + S::kOffBars;
-  const uint32_t full = bars, empty = bars + 8 * S::kUnits;
-  const uint32_t q_full = empty + 8 * S::kUnits, s_full = q_full + 16, p_full = s_full + 16, o_full = p_full + 16, rows_full = o_full + 16;
+  const uint32_t full = smem + S::kOffBars, empty = full + 8 * S::kUnits;
+  const uint32_t q_full = empty + 8 * S::kUnits, s_full = q_full + 16, p_full = s_full + 16, o_full = p_full + 32, done = o_full + 16;
   if (warp == 8) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
         static_cast<uint32_t>(__cvta_generic_to_shared(&sh_tmem))) : "memory");
@@ -292,18 +294,24 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
     for (int t = 0; t < 2; ++t) {
       bar_init(q_full + 8 * t, kTileRows);
       bar_init(s_full + 8 * t, 1);
-      bar_init(p_full + 8 * t, kTileRows);
+      bar_init(p_full + 16 * t, kTileRows);
+      bar_init(p_full + 16 * t + 8, kTileRows);
       bar_init(o_full + 8 * t, 1);
     }
-    bar_init(rows_full, kCopyThreads);
+    bar_init(done, 1);
+    sh_failed = 0;
+    sh_bad = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  uint32_t* const bad_words = reinterpret_cast<uint32_t*>(smem_ptr + S::kOffBad);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh_tmem;
   volatile int* const failed = &sh_failed;
+  grid_handover();
+  if (blockIdx.x == 0 && warp == 15)  // lengths out of range, once
+    for (int32_t b = static_cast<int32_t>(lane); b < a.num_seqs; b += 32) attend_seq(a, b, true);
+  __syncwarp();
 
   // (all warps of a warpgroup execute the same one)
   if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
@@ -314,61 +322,69 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
     // ======================================================================================
     const int32_t t = static_cast<int32_t>(warp >> 2);
     const int32_t r = static_cast<int32_t>(tid & 127u);
-    if (t < tiles) {
-      const int32_t qi = static_cast<int32_t>(a.group.quot(static_cast<uint32_t>(r)));
-      const int32_t q_in = t * p.qpt + qi;              // query in the block
-      const bool mine = qi < p.qpt && q_in < nq;
-      const int32_t h = kvh * G + (r - qi * G);
-      const int32_t tok = seq.q0 + q_first + q_in;
-      const int32_t pos = mine ? p_first + q_in : -1;
-      // positions of the tile's rows
-      const int32_t t_lo = p_first + t * p.qpt, t_hi = min(p_first + t * p.qpt + p.qpt - 1, p_hi);
-      float scale = a.scale_log2 * tensor_scale(a.k_scale);
-      {
-        const uint8_t* src = a.q + static_cast<int64_t>(tok) * a.q_token + static_cast<int64_t>(h) * a.q_head;
-        uint4 w[DP / 8];
+    const int32_t qi = static_cast<int32_t>(a.group.quot(static_cast<uint32_t>(r)));
+    const int32_t gh = r - qi * G, q_in = t * p.qpt + qi;  // head in the group, query in the block
+    const float vscale = tensor_scale(a.v_scale);
+    const float full_scale = a.scale_log2 * tensor_scale(a.k_scale);
+    const uint32_t flip = full_scale < 0.0f ? 0x80008000u : 0u;  // the maximum is taken before the scale
+    const uint32_t lanes = (warp & 3u) << 21;  // the warp's 32 lanes of TMEM
+    const uint32_t s_at = tmem + lanes + t * 128, o_at = tmem + lanes + 256 + t * DP;
+    TileItem it;
+    bool ok = true, have = tile_item(p, 0, &it);
+    uint4 qw[DP / 8];
+    auto row_live = [&](const TileItem& x) { return t < x.tiles && qi < p.qpt && q_in < x.nq; };
+    auto load_q = [&](const TileItem& x) {
+      const bool mine = row_live(x);
+      const uint8_t* src = a.q + static_cast<int64_t>(x.seq.q0 + x.q_first + q_in) * a.q_token +
+                           static_cast<int64_t>(x.kvh * G + gh) * a.q_head;
 #pragma unroll
-        for (int i = 0; i < DP / 8; ++i) {
-          w[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (mine && 8 * i < a.head_dim) w[i] = __ldg(reinterpret_cast<const uint4*>(src) + i);
-        }
+      for (int i = 0; i < DP / 8; ++i) {
+        qw[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (mine && 8 * i < a.head_dim) qw[i] = __ldg(reinterpret_cast<const uint4*>(src) + i);
+      }
+    };
+    if (have) load_q(it);
+    uint32_t waits = 0u, items = 0u;  // phases of s_full and p_full, and of q_full and o_full, that went by
+    for (int32_t round = 0; have && ok;) {
+      const bool mine = row_live(it);
+      const int32_t pos = mine ? it.p_first + q_in : -1;
+      const int32_t tok = it.seq.q0 + it.q_first + q_in, h = it.kvh * G + gh;
+      const bool live = t < it.tiles && it.list.n > 0;
+      float scale = full_scale;
+      float m = -INFINITY, l = 0.0f;   // m: of scaled scores, as last used
+      if (live) {
         if constexpr (FMT != KV_CACHE_SRC) {
           if (a.bf16) {  // into fp16's range: the row's largest element to 2^13 .. 2^14
-            uint32_t m = 0u;
+            uint32_t x = 0u;
 #pragma unroll
             for (int i = 0; i < DP / 8; ++i)
-              m = absmax_pair<true>(absmax_pair<true>(absmax_pair<true>(absmax_pair<true>(m, w[i].x), w[i].y), w[i].z), w[i].w);
-            const uint32_t e = __float_as_uint(absmax_pair_value<true>(m)) >> 23;
+              x = absmax_pair<true>(absmax_pair<true>(absmax_pair<true>(absmax_pair<true>(x, qw[i].x), qw[i].y), qw[i].z), qw[i].w);
+            const uint32_t e = __float_as_uint(absmax_pair_value<true>(x)) >> 23;
             const float f = __uint_as_float(min(254u, 267u - e) << 23);
             scale *= __fdiv_rn(1.0f, f);
-            auto shift = [&](uint32_t x) {
-              const float2 v = widen2<true>(x);
+            auto shift = [&](uint32_t y) {
+              const float2 v = widen2<true>(y);
               return pack2(v.x * f, v.y * f, false);
             };
 #pragma unroll
-            for (int i = 0; i < DP / 8; ++i) w[i] = make_uint4(shift(w[i].x), shift(w[i].y), shift(w[i].z), shift(w[i].w));
+            for (int i = 0; i < DP / 8; ++i) qw[i] = make_uint4(shift(qw[i].x), shift(qw[i].y), shift(qw[i].z), shift(qw[i].w));
           }
         }
-        const uint32_t flip = scale < 0.0f ? 0x80008000u : 0u;  // the maximum is taken before the scale
+        // the products that read this tile's queries before have ended: their scores were waited for
         const uint32_t dst = smem + t * S::kQ;
 #pragma unroll
         for (int i = 0; i < DP / 8; ++i)
-          st_shared16(dst + swizzled(static_cast<uint32_t>(r), i, kTileRows), w[i].x ^ flip, w[i].y ^ flip, w[i].z ^ flip, w[i].w ^ flip);
+          st_shared16(dst + swizzled(static_cast<uint32_t>(r), i, kTileRows), qw[i].x ^ flip, qw[i].y ^ flip, qw[i].z ^ flip, qw[i].w ^ flip);
         scale = fabsf(scale);
         if (scale == 0.0f) scale = __uint_as_float(1u);  // hidden scores (-inf) must stay -inf
         fence_async_shared();
         bar_arrive(q_full + 8 * t);
       }
-      const uint32_t lanes = (warp & 3u) << 21;  // the warp's 32 lanes of TMEM
-      const uint32_t s_at = tmem + lanes + t * 128, o_at = tmem + lanes + 256 + t * DP;
-      float m = -INFINITY, l = 0.0f;   // m: of scaled scores, as last used
-      bool ok = true;
-      for (int32_t j = 0; j < list.n; ++j) {
-        ok = bar_wait(s_full + 8 * t, j & 1, failed);
-        if (!__all_sync(0xFFFFFFFFu, ok)) {
-          ok = false;
-          break;
-        }
+      // positions of the tile's rows
+      const int32_t t_lo = it.p_first + t * p.qpt, t_hi = min(t_lo + p.qpt - 1, it.p_hi);
+      for (int32_t j = 0; live && j < it.list.n; ++j) {
+        ok = __all_sync(0xFFFFFFFFu, bar_wait(s_full + 8 * t, waits & 1u, failed));
+        if (!ok) break;
         tc_fence_after();
         uint32_t sw[kTileKeys];
         tc_ld64(sw, s_at);
@@ -377,10 +393,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
 #pragma unroll
         for (int i = 0; i < kTileKeys; ++i) s[i] = __uint_as_float(sw[i]);
         // mask
-        const int32_t j0 = list.tile(j) * kTileKeys;
-        const uint32_t* bw = bad_words + 4 * (j & 7);
-        const bool none_bad = (bw[0] | bw[1] | bw[2] | bw[3]) == 0u;
-        if (!(none_bad && j0 + kTileKeys - 1 <= t_lo && (a.window == 0 || j0 > t_hi - a.window || j0 + kTileKeys - 1 < a.sinks))) {
+        const int32_t j0 = it.list.tile(j) * kTileKeys;
+        if (!(j0 + kTileKeys - 1 <= t_lo && (a.window == 0 || j0 > t_hi - a.window || j0 + kTileKeys - 1 < a.sinks))) {
           // keys up to pos, and of those the window's or the sinks'
           auto upto = [](int32_t n) {  // n low bits set
             return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u;
@@ -390,7 +404,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
             const int32_t k0 = j0 + 32 * c;
             uint32_t see = upto(pos - k0 + 1);
             if (a.window > 0) see &= ~upto(pos - a.window - k0 + 1) | upto(a.sinks - k0);
-            see &= ~bw[c];
 #pragma unroll
             for (int i = 0; i < 32; ++i)
               if ((see & (1u << i)) == 0u) s[32 * c + i] = -INFINITY;
@@ -409,10 +422,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
         const bool grow = x > m + 8.0f || (m == -INFINITY && x > m);
         if (__any_sync(0xFFFFFFFFu, grow)) {
           const float mn = grow ? x : m;
-          const float alpha = exp2_fast(m - (mn == -INFINITY ? 0.0f : mn));
+          const float f = grow ? exp2_fast(m - (mn == -INFINITY ? 0.0f : mn)) : 1.0f;
           m = mn;
           if (j > 0) {
-            const float f = grow ? alpha : 1.0f;
             l *= f;
 #pragma unroll
             for (int c = 0; c < DP / 32; ++c) {
@@ -425,7 +437,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
           }
         }
         const float ref = m == -INFINITY ? 0.0f : m;
-        // pairs of weights: one packed product and sum for both
+        // pairs of weights: one packed product and sum for both; the first half's product starts early
         float2 sum[4];
 #pragma unroll
         for (int y = 0; y < 4; ++y) sum[y] = make_float2(0.0f, 0.0f);
@@ -440,24 +452,27 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
             w[i] = pack2(e.x, e.y, kBF16);
           }
           tc_st32(s_at + 32 * c, w);
+          tc_wait_st();
+          tc_fence_before();
+          bar_arrive(p_full + 16 * t + 8 * c);
         }
         sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
         l += sum[0].x + sum[0].y;
-        tc_wait_st();
-        tc_fence_before();
-        bar_arrive(p_full + 8 * t);
+        ++waits;
       }
-      // -- out ------------------------------------------------------------------------------
-      const float inv = __fdiv_rn(tensor_scale(a.v_scale), l);
-      bool fine = l > 0.0f;
-      if (list.n > 0 && ok) {
-        ok = bar_wait(o_full + 8 * t, 0, failed);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        tc_fence_after();
-      }
-      if (ok) {
-        uint8_t* out = a.out + static_cast<int64_t>(tok) * a.o_token + static_cast<int64_t>(h) * a.o_head;
-        if (list.n > 0) {
+      if (!ok) break;
+      // -- out, with the next item's queries on their way ---------------------------------------
+      TileItem next;
+      have = tile_item(p, ++round, &next);
+      if (t < it.tiles) {
+        bool fine = l > 0.0f;
+        if (live) {
+          ok = __all_sync(0xFFFFFFFFu, bar_wait(o_full + 8 * t, items & 1u, failed));
+          if (!ok) break;
+          ++items;
+          tc_fence_after();
+          const float inv = __fdiv_rn(vscale, l);
+          uint8_t* out = a.out + static_cast<int64_t>(tok) * a.o_token + static_cast<int64_t>(h) * a.o_head;
 #pragma unroll
           for (int c = 0; c < DP / 32; ++c) {
             uint32_t w[32];
@@ -478,22 +493,22 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
           if (mine && a.lse)
             a.lse[static_cast<int64_t>(tok) * a.q_heads + h] = (m + log2f(l)) * 0.6931471805599453f;
         }
-        uint32_t again = __ballot_sync(0xFFFFFFFFu, mine && !fine);
+        uint32_t again = __ballot_sync(0xFFFFFFFFu, mine && (!fine || sh_bad != 0));
         while (again != 0u) {
           const int src = __ffs(static_cast<int>(again)) - 1;
           again &= again - 1u;
-          attend_row<FMT, 8>(a, b, __shfl_sync(0xFFFFFFFFu, pos, src), __shfl_sync(0xFFFFFFFFu, tok, src),
+          attend_row<FMT, 8>(a, it.b, __shfl_sync(0xFFFFFFFFu, pos, src), __shfl_sync(0xFFFFFFFFu, tok, src),
                              __shfl_sync(0xFFFFFFFFu, h, src));
         }
       }
+      it = next;
+      if (have) load_q(it);
     }
   } else if (warp == 8) {
     // ======================================================================================
     // the products
     // ======================================================================================
     const uint32_t qk_desc = instr_desc(kBF16, false, kTileKeys), pv_desc = instr_desc(kBF16, true, DP);
-    auto slot_of = [](int32_t u) { return static_cast<uint32_t>(u) % S::kUnits; };
-    auto round_of = [](int32_t u) { return (static_cast<uint32_t>(u) / S::kUnits) & 1u; };
     bool ok = true;
     auto wait = [&](uint32_t bar, uint32_t parity) {
       if (ok) ok = __all_sync(0xFFFFFFFFu, bar_wait(bar, parity, failed));
@@ -501,43 +516,60 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
     };
     // descriptors of the operands' first pieces; the others are constant steps (in 16 bytes) away
     const uint64_t q_desc = smem_desc(smem, 16), k_desc = smem_desc(ring, 16), v_desc = smem_desc(ring, kTileKeys * 128);
-    auto scores = [&](int32_t t, int32_t j) {  // S_t = Q_t K_j^T
-      if (!ok) return;
-      const uint64_t q = q_desc + static_cast<uint32_t>(t) * (S::kQ >> 4), k = k_desc + slot_of(2 * j) * (S::kUnit >> 4);
+    uint32_t unit = 0u;                              // ring units that went by
+    uint32_t items0 = 0u, items1 = 0u, done0 = 0u, done1 = 0u;  // of each tile: items and products P V
+    TileItem it;
+    for (int32_t round = 0; ok && tile_item(p, round, &it); ++round) {
+      const int32_t n = it.list.n, tiles = it.tiles;
+      if (n == 0) continue;
+      auto wait_unit = [&](uint32_t u) { wait(full + 8 * (u % S::kUnits), (u / S::kUnits) & 1u); };
+      auto scores = [&](int32_t t, uint32_t u) {  // S_t = Q_t K^T, K in unit u
+        if (!ok) return;
+        const uint64_t q = q_desc + static_cast<uint32_t>(t) * (S::kQ >> 4), k = k_desc + (u % S::kUnits) * (S::kUnit >> 4);
 #pragma unroll
-      for (int i = 0; i < DP / 16; ++i) {
-        const uint32_t at = ((i / 4) * (kTileRows * 128) + (i % 4) * 32) >> 4;
-        tc_mma_ss(tmem + t * 128, q + at, k + at, qk_desc, i > 0);
-      }
-      tc_commit(s_full + 8 * t);
-      if (t == tiles - 1) tc_commit(empty + 8 * slot_of(2 * j));
-    };
-    for (int32_t t = 0; t < tiles && list.n > 0; ++t) {
-      wait(q_full + 8 * t, 0);
-      if (t == 0) wait(full + 8 * slot_of(0), round_of(0));
-      scores(t, 0);
-    }
-    for (int32_t j = 0; j < list.n && ok; ++j) {
+        for (int i = 0; i < DP / 16; ++i) {
+          const uint32_t at = ((i / 4) * (kTileRows * 128) + (i % 4) * 32) >> 4;
+          tc_mma_ss(tmem + t * 128, q + at, k + at, qk_desc, i > 0);
+        }
+        tc_commit(s_full + 8 * t);
+        if (t == tiles - 1) tc_commit(empty + 8 * (u % S::kUnits));
+      };
       for (int32_t t = 0; t < tiles; ++t) {
-        if (t == 0) wait(full + 8 * slot_of(2 * j + 1), round_of(2 * j + 1));
-        wait(p_full + 8 * t, j & 1);
-        if (ok) {  // O_t += P_t V_j
-          const uint64_t v = v_desc + slot_of(2 * j + 1) * (S::kUnit >> 4);
+        wait(q_full + 8 * t, (t ? items1 : items0) & 1u);
+        if (t == 0) wait_unit(unit);
+        scores(t, unit);
+      }
+      for (int32_t j = 0; j < n && ok; ++j) {
+        const uint32_t u = unit + 2 * j;
+        for (int32_t t = 0; t < tiles; ++t) {
+          const uint32_t parity = (t ? done1 : done0) & 1u;
+          if (t == 0) wait_unit(u + 1);
+          const uint64_t v = v_desc + ((u + 1) % S::kUnits) * (S::kUnit >> 4);
 #pragma unroll
-          for (int i = 0; i < kTileKeys / 16; ++i)
-            tc_mma_ts(tmem + 256 + t * DP, tmem + t * 128 + i * 8, v + i * (2048 >> 4), pv_desc, j > 0 || i > 0);
-          if (t == tiles - 1) tc_commit(empty + 8 * slot_of(2 * j + 1));
-          if (j == list.n - 1) tc_commit(o_full + 8 * t);
-        }
-        if (j + 1 < list.n) {
-          if (t == 0) wait(full + 8 * slot_of(2 * j + 2), round_of(2 * j + 2));
-          scores(t, j + 1);
+          for (int half = 0; half < 2; ++half) {  // O_t += P_t V
+            wait(p_full + 16 * t + 8 * half, parity);
+            if (!ok) break;
+#pragma unroll
+            for (int i = half * (kTileKeys / 32); i < (half + 1) * (kTileKeys / 32); ++i)
+              tc_mma_ts(tmem + 256 + t * DP, tmem + t * 128 + i * 8, v + i * (2048 >> 4), pv_desc, j > 0 || i > 0);
+          }
+          if (!ok) break;
+          if (t == tiles - 1) tc_commit(empty + 8 * ((u + 1) % S::kUnits));
+          if (j == n - 1) tc_commit(o_full + 8 * t);
+          if (t) ++done1; else ++done0;
+          if (j + 1 < n) {
+            if (t == 0) wait_unit(u + 2);
+            scores(t, u + 2);
+          }
         }
       }
+      unit += 2 * n;
+      ++items0;
+      if (tiles > 1) ++items1;
     }
     if (!ok) {  // products still in flight read shared memory and write TMEM: let them end
-      tc_commit(o_full);
-      for (uint32_t i = 0; i < kSpin && !bar_try(o_full, 0); ++i) {}
+      tc_commit(done);
+      for (uint32_t i = 0; i < kSpin && !bar_try(done, 0); ++i) {}
     }
     __syncwarp();
   } else {
@@ -545,123 +577,109 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
     // K and V into the ring
     // ======================================================================================
     const int32_t c = static_cast<int32_t>(tid) - (kTileThreads - kCopyThreads);
-    int64_t* const rows = reinterpret_cast<int64_t*>(smem_ptr + S::kOffRows);
-    const int32_t* table = a.table + static_cast<int64_t>(b) * a.table_stride;
     const uint32_t row_bytes = static_cast<uint32_t>(a.head_dim) * (FMT == KV_CACHE_SRC ? 16 : FMT == KV_CACHE_E4M3FN ? 8 : 4) / 8;
-    const uint8_t* const kbase = a.k + kvh * a.k_head;
-    const uint8_t* const vbase = a.v + kvh * a.v_head;
     const uint32_t piece = static_cast<uint32_t>(c) % S::kPieces, key0 = static_cast<uint32_t>(c) / S::kPieces;
     bool ok = true;
-    uint32_t published = 0u;
-    // page id and offset of key c of a tile (the first four of the warps); id -1: not wanted
-    int32_t id = -1;
-    uint32_t off = 0u;
-    auto look = [&](int32_t j) {
-      id = -1;
-      if (c < kTileKeys && j < list.n) {
-        const int32_t k = list.tile(j) * kTileKeys + c;
-        if (k <= p_hi && (k >= list.lo_key || k < a.sinks)) {
-          const uint32_t pg = a.page.quot(static_cast<uint32_t>(k));
-          off = static_cast<uint32_t>(k) - pg * a.page.d;
-          const int32_t v = __ldg(table + pg);
-          id = v < 0 ? -2 : v;
-        }
+    uint32_t unit = 0u;  // ring units that went by
+    auto wait_empty = [&](uint32_t u) {
+      if (ok && u >= S::kUnits) ok = __all_sync(0xFFFFFFFFu, bar_wait(empty + 8 * (u % S::kUnits), (u / S::kUnits - 1) & 1u, failed));
+    };
+    // The page of the lane's i-th key of a tile; -1: no row needs it (or, counted, a bad one).
+    auto page_of = [&](const TileItem& it, int32_t j, int i) -> int32_t {
+      const uint32_t key = key0 + i * S::kStep;
+      if ((kTileKeys % S::kStep != 0 && key >= kTileKeys) || j >= it.list.n) return -1;
+      const int32_t k = it.list.tile(j) * kTileKeys + static_cast<int32_t>(key);
+      if (k > it.p_hi || (k < it.list.lo_key && k >= a.sinks)) return -1;
+      const int32_t id = __ldg(a.table + static_cast<int64_t>(it.b) * a.table_stride + a.page.quot(static_cast<uint32_t>(k)));
+      return id < 0 ? -2 : id;
+    };
+    auto checked = [&](const TileItem& it, int32_t id) -> int32_t {
+      if (id >= a.num_pages || id < -1) {
+        sh_bad = 1;
+        record_oob(a.err, static_cast<uint64_t>(it.b));
+        return -1;
       }
+      return id;
     };
-    // The keys of tile j for all lanes.  Four buffers: no lane is more than a tile ahead of another.
-    auto publish = [&](int32_t j) {
-      if (j >= list.n || !ok) return;
-      if (c < kTileKeys) {
-        const bool is_bad = id == -2 || id >= a.num_pages;
-        const uint32_t bits = __ballot_sync(0xFFFFFFFFu, is_bad);
-        if (is_bad) record_oob(a.err, static_cast<uint64_t>(b));
-        if (lane == 0u) bad_words[4 * (j & 7) + (c >> 5)] = bits;
-        rows[(j & 3) * kTileKeys + c] = id < 0 || is_bad ? -1 : (static_cast<int64_t>(id) << 32) | off;
-      }
-      bar_arrive(rows_full);
-      ok = __all_sync(0xFFFFFFFFu, bar_wait(rows_full, published & 1u, failed));
-      ++published;
+    auto offset_of = [&](const TileItem& it, int32_t j, int i) -> int32_t {  // in its page
+      const uint32_t k = static_cast<uint32_t>(it.list.tile(j) * kTileKeys) + key0 + i * S::kStep;
+      return static_cast<int32_t>(k - a.page.quot(k) * a.page.d);
     };
-    auto wait_empty = [&](int32_t u) {
-      const uint32_t round = static_cast<uint32_t>(u) / S::kUnits;
-      if (ok && round > 0) ok = __all_sync(0xFFFFFFFFu, bar_wait(empty + 8 * (static_cast<uint32_t>(u) % S::kUnits), (round - 1) & 1u, failed));
-    };
+    TileItem it;
     if constexpr (FMT == KV_CACHE_SRC) {
-      auto copy_unit = [&](int32_t u) {  // by cp.async, from the published rows
-        const int64_t* rw = rows + ((u >> 1) & 3) * kTileKeys;
-        const uint8_t* base = (u & 1) ? vbase : kbase;
-        const int32_t page = (u & 1) ? p.v_page : p.k_page, slot = (u & 1) ? p.v_slot : p.k_slot;
-        const uint32_t unit = ring + (static_cast<uint32_t>(u) % S::kUnits) * S::kUnit;
-#pragma unroll
-        for (int i = 0; i < S::kPer; ++i) {
-          const uint32_t key = key0 + i * S::kStep;
-          if (kTileKeys % S::kStep != 0 && key >= kTileKeys) break;
-          const int64_t at = rw[key];
-          const bool have = at >= 0 && piece * 16 < row_bytes;
-          const uint8_t* src = base + (have ? wide(static_cast<int32_t>(at >> 32), page) + wide(static_cast<int32_t>(at), slot) + piece * 16 : 0);
-          copy_async<16>(unit + swizzled(key, piece, kTileKeys), src, have ? 16u : 0u);
-        }
-      };
       // TMA: lane i of warp 9 takes the tile's i-th page; every warp knows whether all are there
       const int32_t boxes = p.box > 0 ? kTileKeys / p.box : 0;
-      auto first_page = [&](int32_t j) -> int32_t {
-        if (j >= list.n || static_cast<int32_t>(lane) >= boxes) return 0;
-        const int32_t k = list.tile(j) * kTileKeys + static_cast<int32_t>(lane) * p.box;
-        return k < seq.len ? __ldg(table + a.page.quot(static_cast<uint32_t>(k))) : -1;
-      };
-      int32_t next = first_page(0);
-      for (int32_t j = 0; j < list.n && ok; ++j) {
-        const int32_t j0 = list.tile(j) * kTileKeys;
-        const int32_t mine = next;
-        next = first_page(j + 1);
-        const bool whole = boxes > 0 && j0 + kTileKeys <= seq.len &&
-                           __all_sync(0xFFFFFFFFu, mine >= 0 && mine < a.num_pages);
-        if (whole) {
-          if (warp == 9 && lane < 4u) bad_words[4 * (j & 7) + lane] = 0u;
-          __syncwarp();
-          for (int kv = 0; kv < 2; ++kv) {
-            const int32_t u = 2 * j + kv;
-            wait_empty(u);
-            if (!ok) break;
-            const uint32_t slot = static_cast<uint32_t>(u) % S::kUnits, bar = full + 8 * slot;
-            if (c == 0) bar_arrive_expect(bar, S::kUnit); else bar_arrive(bar);
-            __syncwarp();
-            if (warp == 9 && static_cast<int32_t>(lane) < boxes) {
-              const uint32_t k = static_cast<uint32_t>(j0) + lane * static_cast<uint32_t>(p.box);
-              const int32_t key = static_cast<int32_t>(k - a.page.quot(k) * a.page.d);
+      for (int32_t round = 0; ok && tile_item(p, round, &it); ++round) {
+        const int32_t* table = a.table + static_cast<int64_t>(it.b) * a.table_stride;
+        const uint8_t* const kbase = a.k + it.kvh * a.k_head;
+        const uint8_t* const vbase = a.v + it.kvh * a.v_head;
+        auto first_page = [&](int32_t j) -> int32_t {
+          if (j >= it.list.n || static_cast<int32_t>(lane) >= boxes) return 0;
+          const int32_t k = it.list.tile(j) * kTileKeys + static_cast<int32_t>(lane) * p.box;
+          return k < it.seq.len ? __ldg(table + a.page.quot(static_cast<uint32_t>(k))) : -1;
+        };
+        int32_t next = first_page(0);
+        for (int32_t j = 0; j < it.list.n && ok; ++j, unit += 2) {
+          const int32_t j0 = it.list.tile(j) * kTileKeys;
+          const int32_t mine = next;
+          next = first_page(j + 1);
+          const bool whole = boxes > 0 && j0 + kTileKeys <= it.seq.len &&
+                             __all_sync(0xFFFFFFFFu, mine >= 0 && mine < a.num_pages);
+          if (whole) {
 #pragma unroll
-              for (int x = 0; x < DP / 64; ++x)
-                tma_rows(ring + slot * S::kUnit + x * (kTileKeys * 128) + lane * static_cast<uint32_t>(p.box) * 128u,
-                         kv ? &p.v_map : &p.k_map, bar, 64 * x, kvh, key, mine);
+            for (int kv = 0; kv < 2; ++kv) {
+              wait_empty(unit + kv);
+              if (!ok) break;
+              const uint32_t slot = (unit + kv) % S::kUnits, bar = full + 8 * slot;
+              if (c == 0) bar_arrive_expect(bar, S::kUnit); else bar_arrive(bar);
+              __syncwarp();
+              if (warp == 9 && static_cast<int32_t>(lane) < boxes) {
+                const uint32_t k = static_cast<uint32_t>(j0) + lane * static_cast<uint32_t>(p.box);
+                const int32_t key = static_cast<int32_t>(k - a.page.quot(k) * a.page.d);
+#pragma unroll
+                for (int x = 0; x < DP / 64; ++x)
+                  tma_rows(ring + slot * S::kUnit + x * (kTileKeys * 128) + lane * static_cast<uint32_t>(p.box) * 128u,
+                           kv ? &p.v_map : &p.k_map, bar, 64 * x, it.kvh, key, mine);
+              }
             }
-          }
-        } else {
-          look(j);
-          publish(j);
-          for (int kv = 0; kv < 2; ++kv) {
-            const int32_t u = 2 * j + kv;
-            wait_empty(u);
-            if (!ok) break;
-            copy_unit(u);
-            commit_async();
-          }
-          if (ok) {
-            wait_async<1>();
-            fence_async_shared();
-            bar_arrive(full + 8 * (static_cast<uint32_t>(2 * j) % S::kUnits));
-          }
-          wait_async<0>();
-          if (ok) {
-            fence_async_shared();
-            bar_arrive(full + 8 * (static_cast<uint32_t>(2 * j + 1) % S::kUnits));
+          } else {
+            int32_t id[S::kPer];
+#pragma unroll
+            for (int i = 0; i < S::kPer; ++i) id[i] = page_of(it, j, i);
+#pragma unroll
+            for (int i = 0; i < S::kPer; ++i) id[i] = checked(it, id[i]);
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+              wait_empty(unit + kv);
+              if (!ok) break;
+              const uint8_t* base = kv ? vbase : kbase;
+              const uint32_t at = ring + ((unit + kv) % S::kUnits) * S::kUnit;
+#pragma unroll
+              for (int i = 0; i < S::kPer; ++i) {
+                const uint32_t key = key0 + i * S::kStep;
+                if (kTileKeys % S::kStep != 0 && key >= kTileKeys) break;
+                const bool want = id[i] >= 0 && piece * 16 < row_bytes;
+                const uint8_t* src = base + (want ? wide(id[i], kv ? p.v_page : p.k_page) +
+                                                        wide(offset_of(it, j, i), kv ? p.v_slot : p.k_slot) + piece * 16 : 0);
+                copy_async<16>(at + swizzled(key, piece, kTileKeys), src, want ? 16u : 0u);
+              }
+              commit_async();
+            }
+            if (ok) {
+              wait_async<1>();
+              fence_async_shared();
+              bar_arrive(full + 8 * (unit % S::kUnits));
+            }
+            wait_async<0>();
+            if (ok) {
+              fence_async_shared();
+              bar_arrive(full + 8 * ((unit + 1) % S::kUnits));
+            }
           }
         }
       }
-      if (!ok) {
-        // boxes in flight write shared memory: let them end before the CTA does
-        for (int i = 0; i < S::kUnits; ++i)
-          for (uint32_t n = 0; n < 4096u && !bar_try(full + 8 * i, 0) && !bar_try(full + 8 * i, 1); ++n) {}
-      }
+      if (!ok)  // boxes in flight write shared memory: let them land before the CTA leaves it
+        for (int i = 0; i < 1000; ++i) __nanosleep(1000);
     } else {
       // the raw pieces of a unit in registers: codes (and, e2m1, their block's scale)
       constexpr int kWords = FMT == KV_CACHE_E4M3FN ? 4 : 2;
@@ -669,35 +687,29 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
         uint32_t w[S::kPer][kWords];
         uint32_t sc[FMT == KV_CACHE_E2M1 ? S::kPer : 1];
       };
-      auto load = [&](int32_t u, Raw& r) {
-        const int64_t* rw = rows + ((u >> 1) & 3) * kTileKeys;
-        const uint8_t* base = (u & 1) ? vbase : kbase;
-        const int32_t page = (u & 1) ? p.v_page : p.k_page, slot = (u & 1) ? p.v_slot : p.k_slot;
+      // codes of keys that are not wanted, and behind head_dim, become 0
+      auto load = [&](const TileItem& it, int32_t j, int kv, const int32_t (&id)[S::kPer], Raw& r) {
+        const uint8_t* base = kv ? a.v + it.kvh * a.v_head : a.k + it.kvh * a.k_head;
+        const uint8_t* sb = kv ? a.v_sc + it.kvh * a.vs_head : a.k_sc + it.kvh * a.ks_head;
 #pragma unroll
         for (int i = 0; i < S::kPer; ++i) {
-          const uint32_t key = key0 + i * S::kStep;
-#pragma unroll
-          for (int x = 0; x < kWords; ++x) r.w[i][x] = 0u;
-          if (FMT == KV_CACHE_E2M1) r.sc[FMT == KV_CACHE_E2M1 ? i : 0] = 0u;
-          if (u >= 2 * list.n || (kTileKeys % S::kStep != 0 && key >= kTileKeys)) continue;
-          const int64_t at = rw[key];
-          if (at < 0 || piece * (4 * kWords) >= row_bytes) continue;
-          const int32_t pg = static_cast<int32_t>(at >> 32), of = static_cast<int32_t>(at);
-          const uint8_t* src = base + wide(pg, page) + wide(of, slot) + piece * (4 * kWords);
+          const bool want = id[i] >= 0 && piece * (4 * kWords) < row_bytes;
+          const int32_t pg = want ? id[i] : 0, of = want ? offset_of(it, j, i) : 0;
+          const uint32_t at = want ? piece : 0u;
+          const uint8_t* src = base + wide(pg, kv ? p.v_page : p.k_page) + wide(of, kv ? p.v_slot : p.k_slot) + at * (4 * kWords);
           if constexpr (FMT == KV_CACHE_E4M3FN) {
             const uint4 v = __ldg(reinterpret_cast<const uint4*>(src));
-            r.w[i][0] = v.x; r.w[i][1] = v.y; r.w[i][2] = v.z; r.w[i][3] = v.w;
+            r.w[i][0] = want ? v.x : 0u; r.w[i][1] = want ? v.y : 0u; r.w[i][2] = want ? v.z : 0u; r.w[i][3] = want ? v.w : 0u;
           } else {
             const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
             r.w[i][0] = v.x; r.w[i][1] = v.y;
-            const uint8_t* ss = (u & 1) ? a.v_sc + kvh * a.vs_head + wide(pg, p.vs_page) + wide(of, p.vs_slot)
-                                        : a.k_sc + kvh * a.ks_head + wide(pg, p.ks_page) + wide(of, p.ks_slot);
-            r.sc[i] = __ldg(ss + piece);
+            const uint32_t sc = __ldg(sb + wide(pg, kv ? p.vs_page : p.ks_page) + wide(of, kv ? p.vs_slot : p.ks_slot) + at);
+            r.sc[i] = want ? sc : 0u;
           }
         }
       };
-      auto store = [&](int32_t u, const Raw& r) {
-        const uint32_t unit = ring + (static_cast<uint32_t>(u) % S::kUnits) * S::kUnit;
+      auto store = [&](uint32_t u, const Raw& r) {
+        const uint32_t at = ring + (u % S::kUnits) * S::kUnit;
 #pragma unroll
         for (int i = 0; i < S::kPer; ++i) {
           const uint32_t key = key0 + i * S::kStep;
@@ -716,37 +728,70 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
 #pragma unroll
             for (int x = 0; x < 8; ++x) f[x] = mul_f16x2(f[x], s2);
           }
-          st_shared16(unit + swizzled(key, 2 * piece, kTileKeys), f[0], f[1], f[2], f[3]);
-          st_shared16(unit + swizzled(key, 2 * piece + 1, kTileKeys), f[4], f[5], f[6], f[7]);
+          // lanes of the second 64 dims store their halves in the other order: eight lanes meet all banks
+          const uint32_t first = (piece >> 2) & 1u;
+          st_shared16(at + swizzled(key, 2 * piece + first, kTileKeys), first ? f[4] : f[0], first ? f[5] : f[1], first ? f[6] : f[2],
+                      first ? f[7] : f[3]);
+          st_shared16(at + swizzled(key, 2 * piece + 1 - first, kTileKeys), first ? f[0] : f[4], first ? f[1] : f[5], first ? f[2] : f[6],
+                      first ? f[3] : f[7]);
         }
         fence_async_shared();
-        bar_arrive(full + 8 * (static_cast<uint32_t>(u) % S::kUnits));
+        bar_arrive(full + 8 * (u % S::kUnits));
       };
+      // two cursors: pages are looked up a tile before codes are loaded, codes a tile before they are stored
       Raw kr, vr;
-      look(0);
-      publish(0);
-      look(1);
-      if (ok) {
-        load(0, kr);
-        load(1, vr);
+      int32_t id[S::kPer];
+      TileItem nx;
+      int32_t nx_round = 0, nx_j = 0;
+      bool nx_have = tile_item(p, 0, &nx);
+      auto skip_empty = [&] {
+        while (nx_have && nx_j >= nx.list.n) {
+          nx_j = 0;
+          nx_have = tile_item(p, ++nx_round, &nx);
+        }
+      };
+      auto look = [&] {
+#pragma unroll
+        for (int i = 0; i < S::kPer; ++i) id[i] = nx_have ? page_of(nx, nx_j, i) : -1;
+      };
+      auto check = [&] {
+#pragma unroll
+        for (int i = 0; i < S::kPer; ++i) id[i] = checked(nx, id[i]);
+      };
+      skip_empty();
+      look();
+      check();
+      bool more = nx_have;
+      if (more) {
+        load(nx, nx_j, 0, id, kr);
+        load(nx, nx_j, 1, id, vr);
+        ++nx_j;
+        skip_empty();
+        look();
       }
-      for (int32_t j = 0; j < list.n && ok; ++j) {
-        publish(j + 1);
-        look(j + 2);
-        wait_empty(2 * j);
+      while (more && ok) {
+        more = nx_have;
+        check();
+        wait_empty(unit);
         if (!ok) break;
-        store(2 * j, kr);
-        load(2 * j + 2, kr);
-        wait_empty(2 * j + 1);
+        store(unit, kr);
+        if (more) load(nx, nx_j, 0, id, kr);
+        wait_empty(unit + 1);
         if (!ok) break;
-        store(2 * j + 1, vr);
-        load(2 * j + 3, vr);
+        store(unit + 1, vr);
+        if (more) {
+          load(nx, nx_j, 1, id, vr);
+          ++nx_j;
+          skip_empty();
+          look();
+        }
+        unit += 2;
       }
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (tid == 0 && *failed != 0) record_oob(a.err, static_cast<uint64_t>(b));
+  if (tid == 0 && *failed != 0) record_oob(a.err, 0u);
   if (warp == 8) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
@@ -765,8 +810,11 @@ kv_status launch_tile(TileParams p, cudaStream_t stream) {
   static SmemOptIn opt_in;
   const kv_status st = opt_in(reinterpret_cast<const void*>(kernel), kSmem);
   if (st != KV_OK) return st;
-  const int64_t grid = static_cast<int64_t>(p.blocks) * p.a.kv_heads;
-  if (grid > 0x7FFFFFFF) return KV_ERR_UNSUPPORTED;
+  int sms = 0;
+  const kv_status sc = current_sm_count(&sms);
+  if (sc != KV_OK) return sc;
+  const int64_t items = static_cast<int64_t>(p.blocks) * p.a.kv_heads;
+  const int64_t grid = items < sms ? items : sms;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(kTileThreads);
