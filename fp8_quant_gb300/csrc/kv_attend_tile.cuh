@@ -584,22 +584,31 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
     auto wait_empty = [&](uint32_t u) {
       if (ok && u >= S::kUnits) ok = __all_sync(0xFFFFFFFFu, bar_wait(empty + 8 * (u % S::kUnits), (u / S::kUnits - 1) & 1u, failed));
     };
-    // The page of the lane's i-th key of a tile; -1: no row needs it (or, counted, a bad one).
-    auto page_of = [&](const TileItem& it, int32_t j, int i) -> int32_t {
-      const uint32_t key = key0 + i * S::kStep;
-      if ((kTileKeys % S::kStep != 0 && key >= kTileKeys) || j >= it.list.n) return -1;
-      const int32_t k = it.list.tile(j) * kTileKeys + static_cast<int32_t>(key);
-      if (k > it.p_hi || (k < it.list.lo_key && k >= a.sinks)) return -1;
-      const int32_t id = __ldg(a.table + static_cast<int64_t>(it.b) * a.table_stride + a.page.quot(static_cast<uint32_t>(k)));
-      return id < 0 ? -2 : id;
-    };
-    auto checked = [&](const TileItem& it, int32_t id) -> int32_t {
-      if (id >= a.num_pages || id < -1) {
-        sh_bad = 1;
-        record_oob(a.err, static_cast<uint64_t>(it.b));
-        return -1;
+    // Which of the lane's keys of a tile a row needs, a bit each, and their pages.  What is loaded
+    // is not looked at before it is used, a tile later: a select behind a load would wait for it.
+    auto pages_of = [&](const TileItem& it, int32_t j, int32_t (&id)[S::kPer]) -> uint32_t {
+      uint32_t want = 0u;
+      const int32_t* table = a.table + static_cast<int64_t>(it.b) * a.table_stride;
+#pragma unroll
+      for (int i = 0; i < S::kPer; ++i) {
+        const uint32_t key = key0 + i * S::kStep;
+        const int32_t k = it.list.tile(j) * kTileKeys + static_cast<int32_t>(key);
+        const bool w = (kTileKeys % S::kStep == 0 || key < kTileKeys) && k <= it.p_hi && (k >= it.list.lo_key || k < a.sinks);
+        want |= (w ? 1u : 0u) << i;
+        if (w) id[i] = __ldg(table + a.page.quot(static_cast<uint32_t>(k)));
       }
-      return id;
+      return want;
+    };
+    // The bits of keys on pages that exist; the others are counted.
+    auto checked = [&](const TileItem& it, uint32_t want, const int32_t (&id)[S::kPer]) -> uint32_t {
+#pragma unroll
+      for (int i = 0; i < S::kPer; ++i)
+        if ((want >> i & 1u) != 0u && (id[i] < 0 || id[i] >= a.num_pages)) {
+          sh_bad = 1;
+          record_oob(a.err, static_cast<uint64_t>(it.b));
+          want &= ~(1u << i);
+        }
+      return want;
     };
     auto offset_of = [&](const TileItem& it, int32_t j, int i) -> int32_t {  // in its page
       const uint32_t k = static_cast<uint32_t>(it.list.tile(j) * kTileKeys) + key0 + i * S::kStep;
@@ -644,10 +653,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
             }
           } else {
             int32_t id[S::kPer];
-#pragma unroll
-            for (int i = 0; i < S::kPer; ++i) id[i] = page_of(it, j, i);
-#pragma unroll
-            for (int i = 0; i < S::kPer; ++i) id[i] = checked(it, id[i]);
+            const uint32_t want = checked(it, pages_of(it, j, id), id);
 #pragma unroll
             for (int kv = 0; kv < 2; ++kv) {
               wait_empty(unit + kv);
@@ -658,10 +664,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
               for (int i = 0; i < S::kPer; ++i) {
                 const uint32_t key = key0 + i * S::kStep;
                 if (kTileKeys % S::kStep != 0 && key >= kTileKeys) break;
-                const bool want = id[i] >= 0 && piece * 16 < row_bytes;
-                const uint8_t* src = base + (want ? wide(id[i], kv ? p.v_page : p.k_page) +
+                const bool w = (want >> i & 1u) != 0u && piece * 16 < row_bytes;
+                const uint8_t* src = base + (w ? wide(id[i], kv ? p.v_page : p.k_page) +
                                                         wide(offset_of(it, j, i), kv ? p.v_slot : p.k_slot) + piece * 16 : 0);
-                copy_async<16>(at + swizzled(key, piece, kTileKeys), src, want ? 16u : 0u);
+                copy_async<16>(at + swizzled(key, piece, kTileKeys), src, w ? 16u : 0u);
               }
               commit_async();
             }
@@ -686,25 +692,25 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
       struct Raw {
         uint32_t w[S::kPer][kWords];
         uint32_t sc[FMT == KV_CACHE_E2M1 ? S::kPer : 1];
+        uint32_t want;  // bits of the pieces that count: the others become 0
       };
-      // codes of keys that are not wanted, and behind head_dim, become 0
-      auto load = [&](const TileItem& it, int32_t j, int kv, const int32_t (&id)[S::kPer], Raw& r) {
+      auto load = [&](const TileItem& it, int32_t j, int kv, uint32_t want, const int32_t (&id)[S::kPer], Raw& r) {
         const uint8_t* base = kv ? a.v + it.kvh * a.v_head : a.k + it.kvh * a.k_head;
         const uint8_t* sb = kv ? a.v_sc + it.kvh * a.vs_head : a.k_sc + it.kvh * a.ks_head;
+        if (piece * (4 * kWords) >= row_bytes) want = 0u;
+        r.want = want;
 #pragma unroll
         for (int i = 0; i < S::kPer; ++i) {
-          const bool want = id[i] >= 0 && piece * (4 * kWords) < row_bytes;
-          const int32_t pg = want ? id[i] : 0, of = want ? offset_of(it, j, i) : 0;
-          const uint32_t at = want ? piece : 0u;
-          const uint8_t* src = base + wide(pg, kv ? p.v_page : p.k_page) + wide(of, kv ? p.v_slot : p.k_slot) + at * (4 * kWords);
+          if ((want >> i & 1u) == 0u) continue;
+          const int32_t of = offset_of(it, j, i);
+          const uint8_t* src = base + wide(id[i], kv ? p.v_page : p.k_page) + wide(of, kv ? p.v_slot : p.k_slot) + piece * (4 * kWords);
           if constexpr (FMT == KV_CACHE_E4M3FN) {
             const uint4 v = __ldg(reinterpret_cast<const uint4*>(src));
-            r.w[i][0] = want ? v.x : 0u; r.w[i][1] = want ? v.y : 0u; r.w[i][2] = want ? v.z : 0u; r.w[i][3] = want ? v.w : 0u;
+            r.w[i][0] = v.x; r.w[i][1] = v.y; r.w[i][2] = v.z; r.w[i][3] = v.w;
           } else {
             const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
             r.w[i][0] = v.x; r.w[i][1] = v.y;
-            const uint32_t sc = __ldg(sb + wide(pg, kv ? p.vs_page : p.ks_page) + wide(of, kv ? p.vs_slot : p.ks_slot) + at);
-            r.sc[i] = want ? sc : 0u;
+            r.sc[i] = __ldg(sb + wide(id[i], kv ? p.vs_page : p.ks_page) + wide(of, kv ? p.vs_slot : p.ks_slot) + piece);
           }
         }
       };
@@ -714,15 +720,17 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
         for (int i = 0; i < S::kPer; ++i) {
           const uint32_t key = key0 + i * S::kStep;
           if (kTileKeys % S::kStep != 0 && key >= kTileKeys) break;
+          const bool w = (r.want >> i & 1u) != 0u;
           uint32_t f[8];
           if constexpr (FMT == KV_CACHE_E4M3FN) {
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-              f[2 * x] = f16x2_from_e4m3x2(r.w[i][x]);
-              f[2 * x + 1] = f16x2_from_e4m3x2(r.w[i][x] >> 16);
+              const uint32_t v = w ? r.w[i][x] : 0u;
+              f[2 * x] = f16x2_from_e4m3x2(v);
+              f[2 * x + 1] = f16x2_from_e4m3x2(v >> 16);
             }
           } else {
-            const uint32_t s2 = f16x2_from_e4m3x2(r.sc[i] * 0x0101u);
+            const uint32_t s2 = f16x2_from_e4m3x2(w ? r.sc[i] * 0x0101u : 0u);  // e2m1 codes are finite
             f16x2_from_e2m1x8(r.w[i][0], f);
             f16x2_from_e2m1x8(r.w[i][1], f + 4);
 #pragma unroll
@@ -750,37 +758,33 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
           nx_have = tile_item(p, ++nx_round, &nx);
         }
       };
-      auto look = [&] {
-#pragma unroll
-        for (int i = 0; i < S::kPer; ++i) id[i] = nx_have ? page_of(nx, nx_j, i) : -1;
-      };
-      auto check = [&] {
-#pragma unroll
-        for (int i = 0; i < S::kPer; ++i) id[i] = checked(nx, id[i]);
-      };
+      uint32_t want = 0u;
+      auto look = [&] { want = nx_have ? pages_of(nx, nx_j, id) : 0u; };
       skip_empty();
       look();
-      check();
+      want = checked(nx, want, id);
       bool more = nx_have;
       if (more) {
-        load(nx, nx_j, 0, id, kr);
-        load(nx, nx_j, 1, id, vr);
+        load(nx, nx_j, 0, want, id, kr);
+        load(nx, nx_j, 1, want, id, vr);
         ++nx_j;
         skip_empty();
         look();
       }
       while (more && ok) {
         more = nx_have;
-        check();
         wait_empty(unit);
         if (!ok) break;
         store(unit, kr);
-        if (more) load(nx, nx_j, 0, id, kr);
+        if (more) {
+          want = checked(nx, want, id);
+          load(nx, nx_j, 0, want, id, kr);
+        }
         wait_empty(unit + 1);
         if (!ok) break;
         store(unit + 1, vr);
         if (more) {
-          load(nx, nx_j, 1, id, vr);
+          load(nx, nx_j, 1, want, id, vr);
           ++nx_j;
           skip_empty();
           look();
