@@ -578,14 +578,18 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
     // ======================================================================================
     const int32_t c = static_cast<int32_t>(tid) - (kTileThreads - kCopyThreads);
     const uint32_t row_bytes = static_cast<uint32_t>(a.head_dim) * (FMT == KV_CACHE_SRC ? 16 : FMT == KV_CACHE_E4M3FN ? 8 : 4) / 8;
-    const uint32_t piece = static_cast<uint32_t>(c) % S::kPieces, key0 = static_cast<uint32_t>(c) / S::kPieces;
+    // Quantised rows of 128 dims: the lanes of the second 64 take the other key of a pair, so that the
+    // eight lanes whose stores go together meet all banks.
+    const uint32_t piece = static_cast<uint32_t>(c) % S::kPieces;
+    const uint32_t key0 = static_cast<uint32_t>(c) / S::kPieces ^ (FMT != KV_CACHE_SRC && DP == 128 ? piece >> 2 : 0u);
     bool ok = true;
     uint32_t unit = 0u;  // ring units that went by
     auto wait_empty = [&](uint32_t u) {
       if (ok && u >= S::kUnits) ok = __all_sync(0xFFFFFFFFu, bar_wait(empty + 8 * (u % S::kUnits), (u / S::kUnits - 1) & 1u, failed));
     };
     // Which of the lane's keys of a tile a row needs, a bit each, and their pages.  What is loaded
-    // is not looked at before it is used, a tile later: a select behind a load would wait for it.
+    // is not looked at before it is used, a tile later (a select behind a load would wait for it),
+    // and nothing branches: keys that are not needed read the last needed one's entry.
     auto pages_of = [&](const TileItem& it, int32_t j, int32_t (&id)[S::kPer]) -> uint32_t {
       uint32_t want = 0u;
       const int32_t* table = a.table + static_cast<int64_t>(it.b) * a.table_stride;
@@ -595,20 +599,22 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
         const int32_t k = it.list.tile(j) * kTileKeys + static_cast<int32_t>(key);
         const bool w = (kTileKeys % S::kStep == 0 || key < kTileKeys) && k <= it.p_hi && (k >= it.list.lo_key || k < a.sinks);
         want |= (w ? 1u : 0u) << i;
-        if (w) id[i] = __ldg(table + a.page.quot(static_cast<uint32_t>(k)));
+        id[i] = __ldg(table + a.page.quot(static_cast<uint32_t>(min(k, it.p_hi))));
       }
       return want;
     };
     // The bits of keys on pages that exist; the others are counted.
     auto checked = [&](const TileItem& it, uint32_t want, const int32_t (&id)[S::kPer]) -> uint32_t {
+      uint32_t bad = 0u;
 #pragma unroll
       for (int i = 0; i < S::kPer; ++i)
-        if ((want >> i & 1u) != 0u && (id[i] < 0 || id[i] >= a.num_pages)) {
-          sh_bad = 1;
-          record_oob(a.err, static_cast<uint64_t>(it.b));
-          want &= ~(1u << i);
-        }
-      return want;
+        bad |= (static_cast<uint32_t>(id[i]) >= static_cast<uint32_t>(a.num_pages) ? 1u : 0u) << i;
+      bad &= want;
+      if (bad != 0u) {
+        sh_bad = 1;
+        record_oob(a.err, static_cast<uint64_t>(it.b));
+      }
+      return want & ~bad;
     };
     auto offset_of = [&](const TileItem& it, int32_t j, int i) -> int32_t {  // in its page
       const uint32_t k = static_cast<uint32_t>(it.list.tile(j) * kTileKeys) + key0 + i * S::kStep;
@@ -699,18 +705,19 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
         const uint8_t* sb = kv ? a.v_sc + it.kvh * a.vs_head : a.k_sc + it.kvh * a.ks_head;
         if (piece * (4 * kWords) >= row_bytes) want = 0u;
         r.want = want;
+        const uint32_t mine = want != 0u ? piece : 0u;
 #pragma unroll
         for (int i = 0; i < S::kPer; ++i) {
-          if ((want >> i & 1u) == 0u) continue;
-          const int32_t of = offset_of(it, j, i);
-          const uint8_t* src = base + wide(id[i], kv ? p.v_page : p.k_page) + wide(of, kv ? p.v_slot : p.k_slot) + piece * (4 * kWords);
+          const bool w = (want >> i & 1u) != 0u;  // else the first row of the cache, to be dropped
+          const int32_t pg = w ? id[i] : 0, of = w ? offset_of(it, j, i) : 0;
+          const uint8_t* src = base + wide(pg, kv ? p.v_page : p.k_page) + wide(of, kv ? p.v_slot : p.k_slot) + mine * (4 * kWords);
           if constexpr (FMT == KV_CACHE_E4M3FN) {
             const uint4 v = __ldg(reinterpret_cast<const uint4*>(src));
             r.w[i][0] = v.x; r.w[i][1] = v.y; r.w[i][2] = v.z; r.w[i][3] = v.w;
           } else {
             const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
             r.w[i][0] = v.x; r.w[i][1] = v.y;
-            r.sc[i] = __ldg(sb + wide(id[i], kv ? p.vs_page : p.ks_page) + wide(of, kv ? p.vs_slot : p.ks_slot) + piece);
+            r.sc[i] = __ldg(sb + wide(pg, kv ? p.vs_page : p.ks_page) + wide(of, kv ? p.vs_slot : p.ks_slot) + mine);
           }
         }
       };
@@ -736,12 +743,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
 #pragma unroll
             for (int x = 0; x < 8; ++x) f[x] = mul_f16x2(f[x], s2);
           }
-          // lanes of the second 64 dims store their halves in the other order: eight lanes meet all banks
-          const uint32_t first = (piece >> 2) & 1u;
-          st_shared16(at + swizzled(key, 2 * piece + first, kTileKeys), first ? f[4] : f[0], first ? f[5] : f[1], first ? f[6] : f[2],
-                      first ? f[7] : f[3]);
-          st_shared16(at + swizzled(key, 2 * piece + 1 - first, kTileKeys), first ? f[0] : f[4], first ? f[1] : f[5], first ? f[2] : f[6],
-                      first ? f[3] : f[7]);
+          st_shared16(at + swizzled(key, 2 * piece, kTileKeys), f[0], f[1], f[2], f[3]);
+          st_shared16(at + swizzled(key, 2 * piece + 1, kTileKeys), f[4], f[5], f[6], f[7]);
         }
         fence_async_shared();
         bar_arrive(full + 8 * (u % S::kUnits));
