@@ -16,11 +16,11 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
-SOURCES = [os.path.join(CSRC, f) for f in ("kvstore.cu", "kv_gather.cu", "kv_scale.cu", "kv_fp8_ex.cu",
-                                           "kv_rope.cu", "kv_attend.cu", "kv_attend_split_bf16.cu",
-                                           "kv_attend_split_f16.cu", "kv_attend_split_e4m3.cu",
-                                           "kv_attend_split_e2m1.cu", "kv_attend_tile_src.cu",
-                                           "kv_attend_tile_quant.cu")]
+SOURCES = [os.path.join(CSRC, f + ".cu") for f in (
+    "kvstore", "kv_gather", "kv_scale", "kv_fp8_ex", "kv_rope", "kv_async", "kv_attend",
+    "kv_attend_split_bf16", "kv_attend_split_f16", "kv_attend_split_e4m3", "kv_attend_split_e2m1",
+    "kv_attend_stream_bf16", "kv_attend_stream_f16", "kv_attend_stream_e4m3", "kv_attend_stream_e2m1",
+    "kv_attend_tile_src", "kv_attend_tile_quant")]
 SRC = SOURCES[0]
 HEADER = os.path.join(ROOT, "include", "kvstore.h")
 LIBDIR = os.path.join(HERE, "lib")

@@ -3,14 +3,21 @@
 //
 //  * kv_attend_tile   (kv_attend_tile.cuh) many query rows per sequence: head
 //                     dims that are multiples of 16 up to 128, aligned as below.
-//  * kv_attend_split  (kv_attend_split.cuh) head dims that are multiples of 16
+//  * kv_attend_stream (kv_attend_stream.cuh) few query rows over much cache, in
+//                     layouts that TMA takes.
+//  * kv_attend_split  (kv_attend_split.cuh) the rest of head dims that are multiples of 16
 //                     up to 256, 16-byte aligned bases and strides.
 //  * kv_attend_rows   any head dim, alignment and stride: one warp per query
 //                     row and head, one key after the other.
 #include <cmath>
 #include <climits>
 
+#include "kv_attend_stream.cuh"
 #include "kv_attend_tile.cuh"
+
+#ifndef KV_STREAM_MIN_BYTES
+#define KV_STREAM_MIN_BYTES (32ll << 20)  // cache bytes from which on kv_attend_stream is faster
+#endif
 
 namespace kvimpl {
 namespace {
@@ -166,8 +173,10 @@ extern "C" kv_status kv_attend(const void* q, void* out, float* lse, const void*
       // TMA: a tile is whole pages, or part of one
       if (page_size >= 8 && (page_size <= kTileKeys ? kTileKeys % page_size == 0 : page_size % kTileKeys == 0)) {
         const int box = page_size < kTileKeys ? static_cast<int>(page_size) : kTileKeys;
-        if (tile_map(&tp.k_map, k_cache, p.bf16, head_dim, num_heads, page_size, num_pages, s->kc_head, s->kc_slot, s->kc_page, box) &&
-            tile_map(&tp.v_map, v_cache, p.bf16, head_dim, num_heads, page_size, num_pages, s->vc_head, s->vc_slot, s->vc_page, box))
+        if (cache_map(&tp.k_map, k_cache, 2, p.bf16, head_dim, page_size, num_heads, num_pages, s->kc_slot, s->kc_head, s->kc_page, 64,
+                      box, 1, true) &&
+            cache_map(&tp.v_map, v_cache, 2, p.bf16, head_dim, page_size, num_heads, num_pages, s->vc_slot, s->vc_head, s->vc_page, 64,
+                      box, 1, true))
           tp.box = box;
       }
       return tile_src(tp, stream);
@@ -189,6 +198,41 @@ extern "C" kv_status kv_attend(const void* q, void* out, float* lse, const void*
     if (window > 0 && window < keys && sinks < keys) {
       const int64_t most = window + sinks + 17;
       keys = most < keys ? most : keys;
+    }
+    // kv_attend_stream: boxes of 16 or of a tile's keys within a page, e2m1 scales of a CTA's heads in
+    // one run of whole 16 bytes, and enough cache to be worth the maps and the deep ring
+    const int bits = format == KV_CACHE_SRC ? 16 : format == KV_CACHE_E4M3FN ? 8 : 4;
+    const int64_t row = static_cast<int64_t>(head_dim) * bits / 8;
+    if (head_dim <= 128 && page_size % 16 == 0 && num_seqs * keys * num_heads * row * 2 >= KV_STREAM_MIN_BYTES &&
+        (format != KV_CACHE_E2M1 || head_dim % 32 == 0)) {
+      StreamParams tp = {};
+      tp.s = sp;
+      const int tile = format == KV_CACHE_SRC && head_dim > 64 ? 16 : 32;
+      tp.box = page_size % tile == 0 ? tile : 16;
+      int hw = 1;
+      for (int h = 2; h <= kSplitWarps; ++h)
+        if (num_heads % h == 0) hw = h;
+      const int padded = (head_dim <= 64 ? 64 : 128) * bits / 8, width = padded < 128 ? padded : 128;
+      const int ds = head_dim / 16;
+      bool fit = cache_map(&tp.k_map, k_cache, 1, false, row, page_size, num_heads, num_pages, s->kc_slot, s->kc_head, s->kc_page,
+                           width, tp.box, hw, true) &&
+                 cache_map(&tp.v_map, v_cache, 1, false, row, page_size, num_heads, num_pages, s->vc_slot, s->vc_head, s->vc_page,
+                           width, tp.box, hw, true);
+      if (fit && format == KV_CACHE_E2M1)
+        fit = (num_heads == 1 || (scales->k_head == ds && scales->v_head == ds)) &&
+              cache_map(&tp.ks_map, scales->k, 1, false, num_heads * ds, page_size, 1, num_pages, scales->k_slot, 16, scales->k_page,
+                        hw * ds, tp.box, 1, false) &&
+              cache_map(&tp.vs_map, scales->v, 1, false, num_heads * ds, page_size, 1, num_pages, scales->v_slot, 16, scales->v_page,
+                        hw * ds, tp.box, 1, false);
+      if (fit) {
+        switch (format) {
+          case KV_CACHE_SRC:
+            return p.bf16 ? stream_bf16(tp, wide, work, work_bytes, keys, stream)
+                          : stream_f16(tp, wide, work, work_bytes, keys, stream);
+          case KV_CACHE_E4M3FN: return stream_e4m3(tp, wide, work, work_bytes, keys, stream);
+          default: return stream_e2m1(tp, wide, work, work_bytes, keys, stream);
+        }
+      }
     }
     switch (format) {
       case KV_CACHE_SRC:

@@ -335,6 +335,223 @@ __device__ __forceinline__ void v_pairs(uint32_t (&f)[Layout<FMT, DP>::VD], cons
 }
 
 // ---------------------------------------------------------------------------
+// A warp's share of the work on one block of query rows: lane (g, t) is lane 4 g + t.
+// ---------------------------------------------------------------------------
+
+// The queries as the products' second operand: lane (g, t) holds row g of each eight; pair i of it
+// are dims dim_of(i), dim_of(i) + 1 (four pairs at a time are eight dims in a row).  rs: the
+// softmax scale (log2) of rows 2t, 2t + 1.
+template <int FMT, int DP, int NB, typename DimOf>
+__device__ __forceinline__ void load_queries(const AttendParams& a, const AttendSeq& seq, int32_t kvh, int32_t row0, int32_t nrows,
+                                             float kscale, DimOf dim_of, uint32_t (&qf)[NB][DP / 8], float (&rs)[NB][2]) {
+  constexpr int QP = DP / 8;
+  const uint32_t lane = threadIdx.x & 31u, g = lane >> 2, t = lane & 3u;
+  const int32_t G = static_cast<int32_t>(a.group.d);
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    const int32_t r = nb * 8 + static_cast<int32_t>(g);
+    const bool ok = r < nrows;
+    const uint32_t qi = a.group.quot(static_cast<uint32_t>(row0 + (ok ? r : 0)));
+    const int32_t h = kvh * G + (row0 + (ok ? r : 0) - static_cast<int32_t>(qi) * G);
+    const uint8_t* src = a.q + (static_cast<int64_t>(seq.q0) + qi) * a.q_token + h * a.q_head;
+#pragma unroll
+    for (int i = 0; i < QP; i += 4) {
+      const int d = dim_of(i);
+      uint4 w = make_uint4(0u, 0u, 0u, 0u);
+      if (ok && d < a.head_dim) w = __ldg(reinterpret_cast<const uint4*>(src + 2 * d));
+      qf[nb][i] = w.x; qf[nb][i + 1] = w.y; qf[nb][i + 2] = w.z; qf[nb][i + 3] = w.w;
+    }
+    float inv = 1.0f;
+    if constexpr (FMT != KV_CACHE_SRC) {
+      if (a.bf16) {
+        uint32_t amax = 0u;
+#pragma unroll
+        for (int i = 0; i < QP; ++i) amax = absmax_pair<true>(amax, qf[nb][i]);
+        uint32_t m = __float_as_uint(absmax_pair_value<true>(amax));
+        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+        const uint32_t e = m >> 23;  // 2^(140 - e): the largest element to 2^13 .. 2^14
+        const float f = __uint_as_float(min(254u, 267u - e) << 23);
+        inv = __fdiv_rn(1.0f, f);
+#pragma unroll
+        for (int i = 0; i < QP; ++i) {
+          const float2 x = widen2<true>(qf[nb][i]);
+          qf[nb][i] = pack2(x.x * f, x.y * f, false);
+        }
+      }
+    }
+    if (kscale < 0.0f) {  // the running maximum is taken before the scale
+#pragma unroll
+      for (int i = 0; i < QP; ++i) qf[nb][i] ^= 0x80008000u;
+    }
+    float full = fabsf(kscale) * inv;
+    if (full == 0.0f) full = __uint_as_float(1u);  // a scale of 0: hidden scores (-inf) must stay -inf
+    rs[nb][0] = __shfl_sync(0xFFFFFFFFu, full, 8u * t);
+    rs[nb][1] = __shfl_sync(0xFFFFFFFFu, full, 8u * t + 4u);
+  }
+}
+
+// Scores s[..][0], [1] are those of key g of each 16 and rows 2t, 2t + 1, [2], [3] of key g + 8.
+// Those of keys (from j0 on, up to key_hi) that their row does not see become -inf; pages: some
+// page id was out of range, so look each key's up.
+template <int NB, int MB>
+__device__ __forceinline__ void hide_scores(const AttendParams& a, const int32_t* table, int32_t j0, int32_t key_hi, bool pages,
+                                            int32_t p_first, int32_t row0, float (&s)[NB][MB][4]) {
+  const uint32_t lane = threadIdx.x & 31u, g = lane >> 2, t = lane & 3u;
+  int32_t pos_of[NB][2];
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+      pos_of[nb][c] = p_first + static_cast<int32_t>(a.group.quot(static_cast<uint32_t>(row0 + nb * 8 + 2 * t + c)));
+#pragma unroll
+  for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+    for (int rh = 0; rh < 2; ++rh) {
+      const int32_t j = j0 + mb * 16 + rh * 8 + static_cast<int32_t>(g);
+      bool have = j <= key_hi;
+      if (have && pages) {
+        const int32_t id = __ldg(table + a.page.quot(static_cast<uint32_t>(j)));
+        have = id >= 0 && id < a.num_pages;
+      }
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          if (!have || !sees(a, pos_of[nb][c], j)) s[nb][mb][rh * 2 + c] = -INFINITY;
+    }
+}
+
+// Running maximum and sum of rows 2t, 2t + 1; the weights, transposed to the second operand of
+// O^T = V^T P^T (pt; pl: what their rounding left, 16-bit caches).
+template <int FMT, int NB, int MB, int OM, bool kBF16>
+__device__ __forceinline__ void softmax_step(float (&s)[NB][MB][4], const float (&rs)[NB][2], float (&m)[NB][2], float (&l)[NB][2],
+                                             float (&o)[NB][OM][4], uint32_t (&pt)[NB][MB][2], uint32_t (&pl)[NB][MB][2]) {
+  bool grew = false;
+  float alpha[NB][2];
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      float x = s[nb][0][c];
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb) x = fmaxf(x, fmaxf(s[nb][mb][c], s[nb][mb][2 + c]));
+      x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
+      x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
+      x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
+      x = fmaxf(m[nb][c], x * rs[nb][c]);
+      const float ref = x == -INFINITY ? 0.0f : x;
+      grew |= x > m[nb][c];
+      alpha[nb][c] = exp2_fast(m[nb][c] - ref);
+      m[nb][c] = x;
+      float sum = 0.0f;
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+        for (int rh = 0; rh < 2; ++rh) {
+          float& e = s[nb][mb][2 * rh + c];
+          e = exp2_fast(__fmaf_rn(e, rs[nb][c], -ref));
+          sum += e;
+        }
+      l[nb][c] = __fmaf_rn(l[nb][c], alpha[nb][c], sum);
+    }
+  if (__any_sync(0xFFFFFFFFu, grew)) {
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int i = 0; i < OM; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[nb][i][c] *= alpha[nb][c & 1];
+  }
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+      for (int rh = 0; rh < 2; ++rh) {
+        const float x = s[nb][mb][2 * rh], y = s[nb][mb][2 * rh + 1];
+        const uint32_t w = pack2(x, y, kBF16);
+        pt[nb][mb][rh] = transpose8x8(w);
+        if constexpr (FMT == KV_CACHE_SRC) {
+          const float2 r = widen2<kBF16>(w);
+          pl[nb][mb][rh] = transpose8x8(pack2(x - r.x, y - r.y, kBF16));
+        }
+      }
+}
+
+// Dim of the lane's i-th O^T product (rows g are even dims of its pieces, rows g + 8 the odd ones).
+template <int FMT, int DP>
+__device__ __forceinline__ int out_dim(int i) {
+  using L = Layout<FMT, DP>;
+  return (static_cast<int>((threadIdx.x & 31u) >> 2) + 8 * (2 * i / L::VD)) * L::VD + 2 * i % L::VD;
+}
+
+// The rows of an item that one warp has whole.
+template <int FMT, int DP, int NB, int OM>
+__device__ __forceinline__ void write_rows(const AttendParams& a, int32_t b, const AttendSeq& seq, int32_t kvh, int32_t row0, int32_t nrows,
+                                           float vscale, const float (&o)[NB][OM][4], const float (&m)[NB][2], const float (&l)[NB][2]) {
+  const uint32_t lane = threadIdx.x & 31u, g = lane >> 2, t = lane & 3u;
+  const int32_t G = static_cast<int32_t>(a.group.d);
+  uint32_t again = 0u;  // rows to be done once more, a bit each
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int32_t r = nb * 8 + 2 * static_cast<int32_t>(t) + c;
+      if (r < nrows) {
+        const float inv = __fdiv_rn(vscale, l[nb][c]);
+        bool fine = l[nb][c] > 0.0f;
+        const uint32_t qi = a.group.quot(static_cast<uint32_t>(row0 + r));
+        const int32_t tok = seq.q0 + static_cast<int32_t>(qi), h = kvh * G + (row0 + r - static_cast<int32_t>(qi) * G);
+        uint8_t* out = a.out + tok * a.o_token + h * a.o_head;
+#pragma unroll
+        for (int i = 0; i < OM; i += 4) {
+          const int d = out_dim<FMT, DP>(i);
+          uint32_t w[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const float lo = o[nb][i + x][c] * inv, hi = o[nb][i + x][2 + c] * inv;
+            fine = fine && fabsf(lo) < INFINITY && fabsf(hi) < INFINITY;
+            w[x] = pack2(lo, hi, a.bf16);
+          }
+          if (d < a.head_dim) *reinterpret_cast<uint4*>(out + 2 * d) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        if (a.lse && g == 0u)
+          a.lse[static_cast<int64_t>(tok) * a.q_heads + h] = (m[nb][c] + log2f(l[nb][c])) * 0.6931471805599453f;
+        if (!fine) again |= 1u << r;
+      }
+    }
+  again = __reduce_or_sync(0xFFFFFFFFu, again);
+  while (again != 0u) {
+    const int32_t r = __ffs(static_cast<int>(again)) - 1;
+    again &= again - 1u;
+    const uint32_t qi = a.group.quot(static_cast<uint32_t>(row0 + r));
+    attend_row<FMT, 8>(a, b, seq.len - seq.nq + static_cast<int32_t>(qi), seq.q0 + static_cast<int32_t>(qi),
+                       kvh * G + (row0 + r - static_cast<int32_t>(qi) * G));
+  }
+}
+
+// The sums of a part of an item, from row `at` of the workspace on.
+template <int FMT, int DP, int NB, int OM>
+__device__ __forceinline__ void write_part(const SplitParams& p, int64_t at, int32_t nrows, const float (&o)[NB][OM][4],
+                                           const float (&m)[NB][2], const float (&l)[NB][2]) {
+  const uint32_t lane = threadIdx.x & 31u, g = lane >> 2, t = lane & 3u;
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int32_t r = nb * 8 + 2 * static_cast<int32_t>(t) + c;
+      if (r >= nrows) continue;
+      float* row = p.part_o + (at + r) * DP;
+#pragma unroll
+      for (int i = 0; i < OM; i += 2)
+        *reinterpret_cast<float4*>(row + out_dim<FMT, DP>(i)) =
+            make_float4(o[nb][i][c], o[nb][i][2 + c], o[nb][i + 1][c], o[nb][i + 1][2 + c]);
+      if (g == 0u) *reinterpret_cast<float2*>(p.part_ml + (at + r) * 2) = make_float2(m[nb][c], l[nb][c]);
+    }
+}
+
+// ---------------------------------------------------------------------------
 // The kernel
 // ---------------------------------------------------------------------------
 
@@ -486,48 +703,8 @@ __global__ void __launch_bounds__(32 * kSplitWarps, (kSplitCtas<DP, NB>))
     // -- queries: lane (g, t) holds the pairs of row g that K's pieces t, t + 4, .. meet -----
     uint32_t qf[NB][QP];
     float rs[NB][2];  // softmax scale of rows 2t, 2t + 1
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      const int32_t r = nb * 8 + static_cast<int32_t>(g);
-      const bool ok = r < nrows;
-      const uint32_t qi = a.group.quot(static_cast<uint32_t>(row0 + (ok ? r : 0)));
-      const int32_t h = kvh * G + (row0 + (ok ? r : 0) - static_cast<int32_t>(qi) * G);
-      const uint8_t* src = a.q + (static_cast<int64_t>(seq.q0) + qi) * a.q_token + h * a.q_head;
-      uint32_t amax = 0u;
-#pragma unroll
-      for (int i = 0; i < QP; i += 4) {
-        const int d = (static_cast<int>(t) + 4 * ((2 * i) / L::KD)) * L::KD + (2 * i) % L::KD;
-        uint4 w = make_uint4(0u, 0u, 0u, 0u);
-        if (ok && d < a.head_dim) w = __ldg(reinterpret_cast<const uint4*>(src + 2 * d));
-        qf[nb][i] = w.x; qf[nb][i + 1] = w.y; qf[nb][i + 2] = w.z; qf[nb][i + 3] = w.w;
-      }
-      float inv = 1.0f;
-      if constexpr (FMT != KV_CACHE_SRC) {
-        if (a.bf16) {
-#pragma unroll
-          for (int i = 0; i < QP; ++i) amax = absmax_pair<true>(amax, qf[nb][i]);
-          uint32_t m = __float_as_uint(absmax_pair_value<true>(amax));
-          m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-          m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-          const uint32_t e = m >> 23;  // 2^(140 - e): the largest element to 2^13 .. 2^14
-          const float f = __uint_as_float(min(254u, 267u - e) << 23);
-          inv = __fdiv_rn(1.0f, f);
-#pragma unroll
-          for (int i = 0; i < QP; ++i) {
-            const float2 x = widen2<true>(qf[nb][i]);
-            qf[nb][i] = pack2(x.x * f, x.y * f, false);
-          }
-        }
-      }
-      if (kscale < 0.0f) {  // the running maximum is taken before the scale
-#pragma unroll
-        for (int i = 0; i < QP; ++i) qf[nb][i] ^= 0x80008000u;
-      }
-      float full = fabsf(kscale) * inv;
-      if (full == 0.0f) full = __uint_as_float(1u);  // a scale of 0: hidden scores (-inf) must stay -inf
-      rs[nb][0] = __shfl_sync(0xFFFFFFFFu, full, 8u * t);
-      rs[nb][1] = __shfl_sync(0xFFFFFFFFu, full, 8u * t + 4u);
-    }
+    load_queries<FMT, DP, NB>(a, seq, kvh, row0, nrows, kscale,
+                              [&](int i) { return (static_cast<int>(t) + 4 * ((2 * i) / L::KD)) * L::KD + (2 * i) % L::KD; }, qf, rs);
 
     float o[NB][OM][4], m[NB][2], l[NB][2];
 #pragma unroll
@@ -715,82 +892,12 @@ __global__ void __launch_bounds__(32 * kSplitWarps, (kSplitCtas<DP, NB>))
                             (a.window == 0 || j0 > p_hi - a.window || j0 + TW - 1 < a.sinks);
       const bool any_bad = __any_sync(0xFFFFFFFFu, bad);
       if (!all_seen || any_bad) {
-        int32_t pos_of[NB][2];
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-          for (int c = 0; c < 2; ++c)
-            pos_of[nb][c] = p_first + static_cast<int32_t>(a.group.quot(static_cast<uint32_t>(row0 + nb * 8 + 2 * t + c)));
-#pragma unroll
-        for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-          for (int rh = 0; rh < 2; ++rh) {
-            const int32_t j = j0 + mb * 16 + rh * 8 + static_cast<int32_t>(g);
-            bool have = li < list.n && j <= p_hi;
-            if (have && any_bad) {
-              const int32_t id = __ldg(table + a.page.quot(static_cast<uint32_t>(j)));
-              have = id >= 0 && id < a.num_pages;
-            }
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-              for (int c = 0; c < 2; ++c)
-                if (!have || !sees(a, pos_of[nb][c], j)) s[nb][mb][rh * 2 + c] = -INFINITY;
-          }
+        hide_scores<NB, MB>(a, table, j0, li < list.n ? p_hi : -1, any_bad, p_first, row0, s);
       }
 
       // running maximum and sum
       uint32_t pt[NB][MB][2], pl[NB][MB][2];
-      bool grew = false;
-      float alpha[NB][2];
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float x = s[nb][0][c];
-#pragma unroll
-          for (int mb = 0; mb < MB; ++mb) x = fmaxf(x, fmaxf(s[nb][mb][c], s[nb][mb][2 + c]));
-          x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
-          x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
-          x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
-          x = fmaxf(m[nb][c], x * rs[nb][c]);
-          const float ref = x == -INFINITY ? 0.0f : x;
-          grew |= x > m[nb][c];
-          alpha[nb][c] = exp2_fast(m[nb][c] - ref);
-          m[nb][c] = x;
-          float sum = 0.0f;
-#pragma unroll
-          for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-            for (int rh = 0; rh < 2; ++rh) {
-              float& e = s[nb][mb][2 * rh + c];
-              e = exp2_fast(__fmaf_rn(e, rs[nb][c], -ref));
-              sum += e;
-            }
-          l[nb][c] = __fmaf_rn(l[nb][c], alpha[nb][c], sum);
-        }
-      if (__any_sync(0xFFFFFFFFu, grew)) {
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-          for (int i = 0; i < OM; ++i)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) o[nb][i][c] *= alpha[nb][c & 1];
-      }
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-          for (int rh = 0; rh < 2; ++rh) {
-            const float x = s[nb][mb][2 * rh], y = s[nb][mb][2 * rh + 1];
-            const uint32_t w = pack2(x, y, kBF16);
-            pt[nb][mb][rh] = transpose8x8(w);
-            if constexpr (FMT == KV_CACHE_SRC) {
-              const float2 r = widen2<kBF16>(w);
-              pl[nb][mb][rh] = transpose8x8(pack2(x - r.x, y - r.y, kBF16));
-            }
-          }
+      softmax_step<FMT, NB, MB, OM, kBF16>(s, rs, m, l, o, pt, pl);
 
       // O^T += V^T P^T
       wait_async<NU - 2>();
@@ -916,60 +1023,10 @@ __global__ void __launch_bounds__(32 * kSplitWarps, (kSplitCtas<DP, NB>))
       __syncthreads();
       continue;
     }
-    if (!whole) {
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int32_t r = nb * 8 + 2 * static_cast<int32_t>(t) + c;
-          if (r >= nrows) continue;
-          const int64_t at = (static_cast<int64_t>(2 * share + (step0 == 0 ? 1 : 0)) * p.hw + hl) * p.part_rows + r;
-          float* row = p.part_o + at * DP;
-#pragma unroll
-          for (int i = 0; i < OM; i += 2) {
-            const int d = (static_cast<int>(g) + 8 * (2 * i / L::VD)) * L::VD + 2 * i % L::VD;
-            *reinterpret_cast<float4*>(row + d) = make_float4(o[nb][i][c], o[nb][i][2 + c], o[nb][i + 1][c], o[nb][i + 1][2 + c]);
-          }
-          if (g == 0u) *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(m[nb][c], l[nb][c]);
-        }
-      continue;
-    }
-    uint32_t again = 0u;  // rows to be done once more, a bit each
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int32_t r = nb * 8 + 2 * static_cast<int32_t>(t) + c;
-        if (r < nrows) {
-          const float inv = __fdiv_rn(vscale, l[nb][c]);
-          bool fine = l[nb][c] > 0.0f;
-          const uint32_t qi = a.group.quot(static_cast<uint32_t>(row0 + r));
-          const int32_t tok = seq.q0 + static_cast<int32_t>(qi), h = kvh * G + (row0 + r - static_cast<int32_t>(qi) * G);
-          uint8_t* out = a.out + tok * a.o_token + h * a.o_head;
-#pragma unroll
-          for (int i = 0; i < OM; i += 4) {
-            const int d = (static_cast<int>(g) + 8 * (2 * i / L::VD)) * L::VD + 2 * i % L::VD;
-            uint32_t w[4];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const float lo = o[nb][i + x][c] * inv, hi = o[nb][i + x][2 + c] * inv;
-              fine = fine && fabsf(lo) < INFINITY && fabsf(hi) < INFINITY;
-              w[x] = pack2(lo, hi, a.bf16);
-            }
-            if (d < a.head_dim) *reinterpret_cast<uint4*>(out + 2 * d) = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-          if (a.lse && g == 0u)
-            a.lse[static_cast<int64_t>(tok) * a.q_heads + h] = (m[nb][c] + log2f(l[nb][c])) * 0.6931471805599453f;
-          if (!fine) again |= 1u << r;
-        }
-      }
-    again = __reduce_or_sync(0xFFFFFFFFu, again);
-    while (again != 0u) {
-      const int32_t r = __ffs(static_cast<int>(again)) - 1;
-      again &= again - 1u;
-      const uint32_t qi = a.group.quot(static_cast<uint32_t>(row0 + r));
-      attend_row<FMT, 8>(a, b, p_first + static_cast<int32_t>(qi), seq.q0 + static_cast<int32_t>(qi),
-                         kvh * G + (row0 + r - static_cast<int32_t>(qi) * G));
+    if (whole) {
+      write_rows<FMT, DP, NB>(a, b, seq, kvh, row0, nrows, vscale, o, m, l);
+    } else {
+      write_part<FMT, DP, NB>(p, (static_cast<int64_t>(2 * share + (step0 == 0 ? 1 : 0)) * p.hw + hl) * p.part_rows, nrows, o, m, l);
     }
   }
     if (!p.split) break;  // as many CTAs as items
@@ -1107,29 +1164,35 @@ struct SmemOptIn {
   }
 };
 
-// Launches the split kernel (and the join) of one format and padded head dim.
-template <int FMT, int DP, int NB, bool kBF16, bool kExact>
-kv_status launch_split(SplitParams p, void* work, int64_t work_bytes, int64_t max_keys, cudaStream_t stream) {
-  using L = Layout<FMT, DP>;
-  constexpr int kSmem = kSplitWarps * kSplitUnits<FMT, DP, NB> * L::kUnit;
-  auto* kernel = kv_attend_split<FMT, DP, NB, kBF16, kExact>;
+// A launch that may overlap its predecessor's end (programmatic dependent launch).
+template <typename... P, typename... A>
+kv_status launch_chained(void (*kernel)(P...), int64_t grid, int threads, int smem, cudaStream_t stream, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  return e == cudaSuccess ? KV_OK : cuda_fail(e);
+}
+
+// Heads and warps of a CTA, and the workspace; returns the CTAs to launch, at most `full` where items
+// are split.
+template <int DP>
+int64_t set_up_split(SplitParams& p, int rows, int tile, int64_t full, void* work, int64_t work_bytes, int64_t max_keys) {
   const AttendParams& a = p.a;
-  p.rows = 8 * NB;
+  p.rows = rows;
   p.hw = 1;
   for (int h = 2; h <= kSplitWarps; ++h)
     if (a.kv_heads % h == 0) p.hw = h;
   p.subs = kSplitWarps / p.hw;
   p.hgroups = a.kv_heads / p.hw;
   p.min_steps = KV_ATTEND_MIN_STEPS;
-
-  int sms = 0;
-  kv_status st = current_sm_count(&sms);
-  if (st != KV_OK) return st;
-  static SmemOptIn opt_in;
-  st = opt_in(reinterpret_cast<const void*>(kernel), kSmem);
-  if (st != KV_OK) return st;
-  const int64_t full = static_cast<int64_t>(sms) * kSplitCtas<DP, NB>;
-
   // An item that cannot be longer than the shortest share is not split, nor is
   // any where the workspace holds the parts of less than half the GPU.
   const int64_t meta = (static_cast<int64_t>(a.num_seqs) + 31) / 32 * 256;
@@ -1137,46 +1200,46 @@ kv_status launch_split(SplitParams p, void* work, int64_t work_bytes, int64_t ma
   const int64_t slot = static_cast<int64_t>(p.hw) * p.part_rows * (DP + 2) * 4;
   int64_t fit = work && work_bytes > kSplitHead + meta ? (work_bytes - kSplitHead - meta) / (2 * slot) : 0;
   if (fit > kLevels * full) fit = kLevels * full;
-  p.split = max_keys > static_cast<int64_t>(p.min_steps) * p.subs * L::TW && 2 * fit >= full;
-  int64_t grid;
+  p.split = max_keys > static_cast<int64_t>(p.min_steps) * p.subs * tile && 2 * fit >= full;
   if (p.split) {
-    grid = fit < full ? fit : full;
     p.max_shares = static_cast<int32_t>(fit);
     p.head = static_cast<SplitWork*>(work);
     p.meta = reinterpret_cast<int64_t*>(static_cast<uint8_t*>(work) + kSplitHead);
     p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(work) + kSplitHead + meta);
     p.part_ml = p.part_o + 2 * fit * p.hw * p.part_rows * DP;
-  } else {
-    // a CTA an item: at most this many
-    const int64_t rows = static_cast<int64_t>(a.num_q) * a.group.d;
-    const int64_t items = (rows / p.rows + a.num_seqs) * p.hgroups;
-    grid = items < 0x7FFFFFFF ? items : 0x7FFFFFFF;
+    return fit < full ? fit : full;
   }
+  // a CTA an item: at most this many
+  const int64_t items = (static_cast<int64_t>(a.num_q) * a.group.d / p.rows + a.num_seqs) * p.hgroups;
+  return items < 0x7FFFFFFF ? items : 0x7FFFFFFF;
+}
 
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(static_cast<unsigned>(32 * p.hw * p.subs));
-  cfg.dynamicSmemBytes = kSmem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cudaError_t le = cudaLaunchKernelEx(&cfg, kernel, p);
-  if (le != cudaSuccess) return cuda_fail(le);
-  if (!p.split) return KV_OK;
-
-  // the fewer the rows, the more parts has each and the more warps take it
-  const int64_t rows = static_cast<int64_t>(a.num_q) * a.q_heads;
+// The fewer the rows, the more parts has each and the more warps take it.
+template <int FMT, int DP>
+kv_status launch_join(const SplitParams& p, int sms, cudaStream_t stream) {
+  const int64_t rows = static_cast<int64_t>(p.a.num_q) * p.a.q_heads;
   int32_t wpr = 1;
   while (wpr < kJoinWarps && rows * wpr < 16ll * sms) wpr *= 2;
   const int64_t per = kJoinWarps / wpr;
-  cfg.gridDim = dim3(static_cast<unsigned>((rows + per - 1) / per));
-  cfg.blockDim = dim3(32 * kJoinWarps);
-  cfg.dynamicSmemBytes = 0;
-  le = cudaLaunchKernelEx(&cfg, kv_attend_join<FMT, DP>, p, wpr);
-  return le == cudaSuccess ? KV_OK : cuda_fail(le);
+  return launch_chained(kv_attend_join<FMT, DP>, (rows + per - 1) / per, 32 * kJoinWarps, 0, stream, p, wpr);
+}
+
+// Launches the split kernel (and the join) of one format and padded head dim.
+template <int FMT, int DP, int NB, bool kBF16, bool kExact>
+kv_status launch_split(SplitParams p, void* work, int64_t work_bytes, int64_t max_keys, cudaStream_t stream) {
+  using L = Layout<FMT, DP>;
+  constexpr int kSmem = kSplitWarps * kSplitUnits<FMT, DP, NB> * L::kUnit;
+  auto* kernel = kv_attend_split<FMT, DP, NB, kBF16, kExact>;
+  int sms = 0;
+  kv_status st = current_sm_count(&sms);
+  if (st != KV_OK) return st;
+  static SmemOptIn opt_in;
+  st = opt_in(reinterpret_cast<const void*>(kernel), kSmem);
+  if (st != KV_OK) return st;
+  const int64_t grid = set_up_split<DP>(p, 8 * NB, L::TW, static_cast<int64_t>(sms) * kSplitCtas<DP, NB>, work, work_bytes, max_keys);
+  st = launch_chained(kernel, grid, 32 * p.hw * p.subs, kSmem, stream, p);
+  if (st != KV_OK || !p.split) return st;
+  return launch_join<FMT, DP>(p, sms, stream);
 }
 
 template <int FMT, bool kBF16>

@@ -39,8 +39,7 @@
 // error record, lets its copies and products end and leaves.
 #pragma once
 
-#include <cuda.h>  // CUtensorMap
-
+#include "kv_async.cuh"
 #include "kv_attend_split.cuh"
 
 namespace kvimpl {
@@ -60,7 +59,6 @@ constexpr int kTileThreads = 512;
 constexpr int kCopyThreads = 224;
 constexpr int kSoftmaxRegs = 176, kOtherRegs = 80;
 static_assert(256 * kSoftmaxRegs + 256 * kOtherRegs <= 65536, "the registers of the launch");
-constexpr uint32_t kSpin = 1u << 24;  // tries of a wait: far beyond any that ends
 
 template <int FMT, int DP>
 struct TileSmem {
@@ -78,48 +76,8 @@ struct TileSmem {
   static constexpr int kTotal = kOffBars + kBars * 8 + 1024;    // the base is aligned to 1,024
 };
 
-// -- mbarriers, tcgen05 -----------------------------------------------------------------------
+// -- tcgen05 ----------------------------------------------------------------------------------
 
-__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
-
-__device__ __forceinline__ void bar_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-// Arrives and expects `bytes` more of this phase by TMA.
-__device__ __forceinline__ void bar_arrive_expect(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-}
-
-// A box of 64 dims x `box` keys of one head and page.
-__device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t dim, int32_t head,
-                                         int32_t key, int32_t page) {
-  asm volatile("cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];"
-               ::"r"(dst), "l"(map), "r"(bar), "r"(dim), "r"(head), "r"(key), "r"(page) : "memory");
-}
-
-__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile("{\n\t.reg .pred p;\n\t"
-               "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-               "selp.u32 %0, 1, 0, p;\n\t}"
-               : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-  return ok != 0u;
-}
-
-// False when the wait ran out here or anywhere in the CTA.
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* failed) {
-  for (uint32_t i = 0; i < kSpin; ++i) {
-    if (bar_try(bar, parity)) return true;
-    if ((i & 1023u) == 1023u && *failed != 0) return false;
-  }
-  *failed = 1;
-  return false;
-}
-
-__device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -653,8 +611,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
                 const int32_t key = static_cast<int32_t>(k - a.page.quot(k) * a.page.d);
 #pragma unroll
                 for (int x = 0; x < DP / 64; ++x)
-                  tma_rows(ring + slot * S::kUnit + x * (kTileKeys * 128) + lane * static_cast<uint32_t>(p.box) * 128u,
-                           kv ? &p.v_map : &p.k_map, bar, 64 * x, it.kvh, key, mine);
+                  tma_box(ring + slot * S::kUnit + x * (kTileKeys * 128) + lane * static_cast<uint32_t>(p.box) * 128u,
+                           kv ? &p.v_map : &p.k_map, bar, 64 * x, key, it.kvh, mine);
               }
             }
           } else {
@@ -822,24 +780,8 @@ kv_status launch_tile(TileParams p, cudaStream_t stream) {
   if (sc != KV_OK) return sc;
   const int64_t items = static_cast<int64_t>(p.blocks) * p.a.kv_heads;
   const int64_t grid = items < sms ? items : sms;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(kTileThreads);
-  cfg.dynamicSmemBytes = kSmem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
-  return e == cudaSuccess ? KV_OK : cuda_fail(e);
+  return launch_chained(kernel, grid, kTileThreads, kSmem, stream, p);
 }
-
-// The tensor map of a 16-bit cache for boxes of 64 dims x `box` keys of one head and page; false where
-// there is none (a stride that TMA does not take).
-bool tile_map(CUtensorMap* map, const void* cache, bool bf16, int head_dim, int heads, int64_t page_size, int64_t pages,
-              int64_t head_stride, int64_t slot_stride, int64_t page_stride, int box);
 
 // The instantiations: 16-bit caches, and quantised ones.
 kv_status tile_src(const TileParams& p, cudaStream_t stream);
