@@ -209,28 +209,34 @@ extern "C" kv_status kv_attend(const void* q, void* out, float* lse, const void*
       tp.s = sp;
       const int tile = format == KV_CACHE_SRC && head_dim > 64 ? 16 : 32;
       tp.box = page_size % tile == 0 ? tile : 16;
-      int hw = 1;
-      for (int h = 2; h <= kSplitWarps; ++h)
-        if (num_heads % h == 0) hw = h;
-      const int padded = (head_dim <= 64 ? 64 : 128) * bits / 8, width = padded < 128 ? padded : 128;
-      const int ds = head_dim / 16;
-      bool fit = cache_map(&tp.k_map, k_cache, 1, false, row, page_size, num_heads, num_pages, s->kc_slot, s->kc_head, s->kc_page,
-                           width, tp.box, hw, true) &&
-                 cache_map(&tp.v_map, v_cache, 1, false, row, page_size, num_heads, num_pages, s->vc_slot, s->vc_head, s->vc_page,
-                           width, tp.box, hw, true);
-      if (fit && format == KV_CACHE_E2M1)
-        fit = (num_heads == 1 || (scales->k_head == ds && scales->v_head == ds)) &&
-              cache_map(&tp.ks_map, scales->k, 1, false, num_heads * ds, page_size, 1, num_pages, scales->k_slot, 16, scales->k_page,
-                        hw * ds, tp.box, 1, false) &&
-              cache_map(&tp.vs_map, scales->v, 1, false, num_heads * ds, page_size, 1, num_pages, scales->v_slot, 16, scales->v_page,
-                        hw * ds, tp.box, 1, false);
+      const int hw = heads_of_cta(num_heads, kSplitWarps);
+      const int padded = (head_dim <= 64 ? 64 : 128) * bits / 8, ds = head_dim / 16;
+      // short rows of neighbouring heads as rows of 128 bytes
+      const int per_row = padded < 128 ? 128 / padded : 1;
+      const bool pack = per_row > 1 && row == padded && hw % per_row == 0 && s->kc_head == row && s->vc_head == row;
+      const int width = pack || padded > 128 ? 128 : padded;
+      auto map = [&](CUtensorMap* m, const void* base, int64_t slot, int64_t head, int64_t page) {
+        return pack ? cache_map(m, base, 1, false, 128, page_size, num_heads / per_row, num_pages, slot, 128, page, 128, tp.box, hw / per_row, true)
+                    : cache_map(m, base, 1, false, row, page_size, num_heads, num_pages, slot, head, page, width, tp.box, hw, true);
+      };
+      bool fit = map(&tp.k_map, k_cache, s->kc_slot, s->kc_head, s->kc_page) && map(&tp.v_map, v_cache, s->vc_slot, s->vc_head, s->vc_page);
+      if (fit && format == KV_CACHE_E2M1) {
+        const kv_block_scales& b = *scales;
+        const int64_t run = static_cast<int64_t>(num_heads) * ds;
+        fit = num_heads == 1 || (b.k_head == ds && b.v_head == ds);
+        tp.flat_scales = fit && hw == num_heads && b.k_slot == run && b.v_slot == run && (tp.box * run) % 16 == 0 &&
+                         ((u64(b.k) | u64(b.v) | u64(b.k_page) | u64(b.v_page) | u64(16 * run)) & 15u) == 0;
+        if (fit && !tp.flat_scales)
+          fit = cache_map(&tp.ks_map, b.k, 1, false, run, page_size, 1, num_pages, b.k_slot, 16, b.k_page, hw * ds, tp.box, 1, false) &&
+                cache_map(&tp.vs_map, b.v, 1, false, run, page_size, 1, num_pages, b.v_slot, 16, b.v_page, hw * ds, tp.box, 1, false);
+      }
       if (fit) {
         switch (format) {
           case KV_CACHE_SRC:
-            return p.bf16 ? stream_bf16(tp, wide, work, work_bytes, keys, stream)
-                          : stream_f16(tp, wide, work, work_bytes, keys, stream);
-          case KV_CACHE_E4M3FN: return stream_e4m3(tp, wide, work, work_bytes, keys, stream);
-          default: return stream_e2m1(tp, wide, work, work_bytes, keys, stream);
+            return p.bf16 ? stream_bf16(tp, wide, pack, work, work_bytes, keys, stream)
+                          : stream_f16(tp, wide, pack, work, work_bytes, keys, stream);
+          case KV_CACHE_E4M3FN: return stream_e4m3(tp, wide, pack, work, work_bytes, keys, stream);
+          default: return stream_e2m1(tp, wide, pack, work, work_bytes, keys, stream);
         }
       }
     }

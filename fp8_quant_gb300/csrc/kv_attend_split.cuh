@@ -268,69 +268,107 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
   }
 }
 
-// A K piece of KD dims as KD / 2 packed pairs.  sc: the piece's block scales (e2m1: one or two e4m3 codes).
-template <int FMT, int DP>
-__device__ __forceinline__ void k_pairs(uint32_t (&f)[Layout<FMT, DP>::KD / 2], const uint32_t (&w)[Layout<FMT, DP>::KC / 4],
-                                        uint32_t sc) {
-  using L = Layout<FMT, DP>;
+// Pieces are converted a word at a time, so that few operands are live.  A word holds kWord dims.
+template <int FMT>
+constexpr int kWord = FMT == KV_CACHE_SRC ? 2 : FMT == KV_CACHE_E4M3FN ? 4 : 8;
+
+// A K word as kWord / 2 packed pairs.  s2: its block's scale in both halves (e2m1).
+template <int FMT>
+__device__ __forceinline__ void k_word(uint32_t (&f)[kWord<FMT> / 2], uint32_t w, uint32_t s2) {
   if constexpr (FMT == KV_CACHE_SRC) {
-#pragma unroll
-    for (int i = 0; i < L::KC / 4; ++i) f[i] = w[i];
+    f[0] = w;
   } else if constexpr (FMT == KV_CACHE_E4M3FN) {
-#pragma unroll
-    for (int i = 0; i < L::KC / 4; ++i) {
-      f[2 * i] = f16x2_from_e4m3x2(w[i]);
-      f[2 * i + 1] = f16x2_from_e4m3x2(w[i] >> 16);
-    }
+    f[0] = f16x2_from_e4m3x2(w);
+    f[1] = f16x2_from_e4m3x2(w >> 16);
   } else {
-    const uint32_t s2 = f16x2_from_e4m3x2(sc);
+    f16x2_from_e2m1x8(w, f);
 #pragma unroll
-    for (int i = 0; i < L::KC / 4; ++i) {
-      const uint32_t s = __byte_perm(s2, 0u, (i * 8) / kFp4Block == 0 ? 0x1010 : 0x3232);
-      uint32_t x[4];
-      f16x2_from_e2m1x8(w[i], x);
+    for (int j = 0; j < 4; ++j) f[j] = mul_f16x2(f[j], s2);
+  }
+}
+
+// A V word of tokens a and b as kWord words (a, b).  s2: the tokens' block scales (e2m1).
+template <int FMT>
+__device__ __forceinline__ void v_word(uint32_t (&f)[kWord<FMT>], uint32_t a, uint32_t b, uint32_t s2) {
+  if constexpr (FMT == KV_CACHE_SRC) {
+    f[0] = __byte_perm(a, b, 0x5410);
+    f[1] = __byte_perm(a, b, 0x7632);
+  } else if constexpr (FMT == KV_CACHE_E4M3FN) {
+    const uint32_t lo = __byte_perm(a, b, 0x5140), hi = __byte_perm(a, b, 0x7362);
+    f[0] = f16x2_from_e4m3x2(lo);
+    f[1] = f16x2_from_e4m3x2(lo >> 16);
+    f[2] = f16x2_from_e4m3x2(hi);
+    f[3] = f16x2_from_e4m3x2(hi >> 16);
+  } else {
+    const uint32_t even = (a & 0x0F0F0F0Fu) | ((b << 4) & 0xF0F0F0F0u);
+    const uint32_t odd = ((a >> 4) & 0x0F0F0F0Fu) | (b & 0xF0F0F0F0u);
+    uint32_t e[4], o[4];
+    f16x2_from_e2m1x8(even, e);
+    f16x2_from_e2m1x8(odd, o);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) f[4 * i + j] = mul_f16x2(x[j], s);
+    for (int j = 0; j < 4; ++j) {
+      f[2 * j] = mul_f16x2(e[j], s2);
+      f[2 * j + 1] = mul_f16x2(o[j], s2);
     }
   }
 }
 
-// A V piece of tokens a and b, VD dims each, as VD words (a, b).  sc: e2m1, the tokens' scale codes (a, b)
-// per block of the piece.
-template <int FMT, int DP>
-__device__ __forceinline__ void v_pairs(uint32_t (&f)[Layout<FMT, DP>::VD], const uint32_t (&a)[Layout<FMT, DP>::VC / 4],
-                                        const uint32_t (&b)[Layout<FMT, DP>::VC / 4], const uint32_t (&sc)[2]) {
-  using L = Layout<FMT, DP>;
+// S^T += K Q^T for one piece of rows g (w[0]) and g + 8 (w[1]): KD / 4 products a block of queries,
+// whose pairs for it begin at qf[..][first].  sc: the rows' block scale codes (e2m1).
+template <int FMT, int DP, int NB, bool kBF16>
+__device__ __forceinline__ void k_products(float (&s)[NB][4], const uint32_t (&w)[2][Layout<FMT, DP>::KC / 4], const uint32_t (&sc)[2],
+                                           const uint32_t (&qf)[NB][DP / 8], int first) {
+  constexpr int kWords = Layout<FMT, DP>::KC / 4;
   if constexpr (FMT == KV_CACHE_SRC) {
 #pragma unroll
-    for (int i = 0; i < L::VC / 4; ++i) {
-      f[2 * i] = __byte_perm(a[i], b[i], 0x5410);
-      f[2 * i + 1] = __byte_perm(a[i], b[i], 0x7632);
-    }
-  } else if constexpr (FMT == KV_CACHE_E4M3FN) {
+    for (int i = 0; i < kWords; i += 2)
 #pragma unroll
-    for (int i = 0; i < L::VC / 4; ++i) {
-      const uint32_t lo = __byte_perm(a[i], b[i], 0x5140), hi = __byte_perm(a[i], b[i], 0x7362);
-      f[4 * i] = f16x2_from_e4m3x2(lo);
-      f[4 * i + 1] = f16x2_from_e4m3x2(lo >> 16);
-      f[4 * i + 2] = f16x2_from_e4m3x2(hi);
-      f[4 * i + 3] = f16x2_from_e4m3x2(hi >> 16);
-    }
+      for (int nb = 0; nb < NB; ++nb)
+        mma16816<kBF16>(s[nb], w[0][i], w[1][i], w[0][i + 1], w[1][i + 1], qf[nb][first + i], qf[nb][first + i + 1]);
   } else {
-#pragma unroll
-    for (int i = 0; i < L::VC / 4; ++i) {
-      const uint32_t even = (a[i] & 0x0F0F0F0Fu) | ((b[i] << 4) & 0xF0F0F0F0u);
-      const uint32_t odd = ((a[i] >> 4) & 0x0F0F0F0Fu) | (b[i] & 0xF0F0F0F0u);
-      const uint32_t s = f16x2_from_e4m3x2(sc[(i * 8) / kFp4Block]);
-      uint32_t e[4], o[4];
-      f16x2_from_e2m1x8(even, e);
-      f16x2_from_e2m1x8(odd, o);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        f[8 * i + 2 * j] = mul_f16x2(e[j], s);
-        f[8 * i + 2 * j + 1] = mul_f16x2(o[j], s);
-      }
+    uint32_t two[2] = {0u, 0u};
+    if constexpr (FMT == KV_CACHE_E2M1) {
+      two[0] = f16x2_from_e4m3x2(sc[0]);
+      two[1] = f16x2_from_e4m3x2(sc[1]);
     }
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      uint32_t f[2][kWord<FMT> / 2];
+#pragma unroll
+      for (int rh = 0; rh < 2; ++rh)
+        k_word<FMT>(f[rh], w[rh][i], __byte_perm(two[rh], 0u, i * 8 / kFp4Block == 0 ? 0x1010 : 0x3232));
+#pragma unroll
+      for (int j = 0; j < kWord<FMT> / 2; j += 2)
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+          mma16816<kBF16>(s[nb], f[0][j], f[1][j], f[0][j + 1], f[1][j + 1], qf[nb][first + i * (kWord<FMT> / 2) + j],
+                          qf[nb][first + i * (kWord<FMT> / 2) + j + 1]);
+    }
+  }
+}
+
+// O^T += V^T P^T for one piece of tokens 2t, 2t + 1 (w[0], w[1]), 2t + 8, 2t + 9 (w[2], w[3]): VD / 2
+// products a block of queries, from o[..][first] on.  sc: the scale codes of the first and of the
+// second two tokens, a byte each, per block of the piece (e2m1).
+template <int FMT, int DP, int NB, bool kBF16, int OM>
+__device__ __forceinline__ void v_products(float (&o)[NB][OM][4], const uint32_t (&w)[4][Layout<FMT, DP>::VC / 4],
+                                           const uint32_t (&sc)[2][2], const uint32_t (&pt)[NB][2], const uint32_t (&pl)[NB][2], int first) {
+  constexpr int kWords = Layout<FMT, DP>::VC / 4;
+#pragma unroll
+  for (int i = 0; i < kWords; ++i) {
+    uint32_t f[2][kWord<FMT>];
+#pragma unroll
+    for (int pr = 0; pr < 2; ++pr)
+      v_word<FMT>(f[pr], w[2 * pr][i], w[2 * pr + 1][i], FMT == KV_CACHE_E2M1 ? f16x2_from_e4m3x2(sc[pr][i * 8 / kFp4Block]) : 0u);
+#pragma unroll
+    for (int j = 0; j < kWord<FMT> / 2; ++j)
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        float (&acc)[4] = o[nb][first + i * (kWord<FMT> / 2) + j];
+        mma16816<kBF16>(acc, f[0][2 * j], f[0][2 * j + 1], f[1][2 * j], f[1][2 * j + 1], pt[nb][0], pt[nb][1]);
+        if constexpr (FMT == KV_CACHE_SRC)
+          mma16816<kBF16>(acc, f[0][2 * j], f[0][2 * j + 1], f[1][2 * j], f[1][2 * j + 1], pl[nb][0], pl[nb][1]);
+      }
   }
 }
 
@@ -391,13 +429,13 @@ __device__ __forceinline__ void load_queries(const AttendParams& a, const Attend
   }
 }
 
-// Scores s[..][0], [1] are those of key g of each 16 and rows 2t, 2t + 1, [2], [3] of key g + 8.
+// Scores s[..][0], [1] are those of key `key` of each 16 and rows 2t, 2t + 1, [2], [3] of key + 8.
 // Those of keys (from j0 on, up to key_hi) that their row does not see become -inf; pages: some
 // page id was out of range, so look each key's up.
 template <int NB, int MB>
 __device__ __forceinline__ void hide_scores(const AttendParams& a, const int32_t* table, int32_t j0, int32_t key_hi, bool pages,
-                                            int32_t p_first, int32_t row0, float (&s)[NB][MB][4]) {
-  const uint32_t lane = threadIdx.x & 31u, g = lane >> 2, t = lane & 3u;
+                                            int32_t p_first, int32_t row0, uint32_t key, float (&s)[MB][NB][4]) {
+  const uint32_t t = threadIdx.x & 3u;
   int32_t pos_of[NB][2];
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb)
@@ -408,7 +446,7 @@ __device__ __forceinline__ void hide_scores(const AttendParams& a, const int32_t
   for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
     for (int rh = 0; rh < 2; ++rh) {
-      const int32_t j = j0 + mb * 16 + rh * 8 + static_cast<int32_t>(g);
+      const int32_t j = j0 + mb * 16 + rh * 8 + static_cast<int32_t>(key);
       bool have = j <= key_hi;
       if (have && pages) {
         const int32_t id = __ldg(table + a.page.quot(static_cast<uint32_t>(j)));
@@ -418,24 +456,24 @@ __device__ __forceinline__ void hide_scores(const AttendParams& a, const int32_t
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int c = 0; c < 2; ++c)
-          if (!have || !sees(a, pos_of[nb][c], j)) s[nb][mb][rh * 2 + c] = -INFINITY;
+          if (!have || !sees(a, pos_of[nb][c], j)) s[mb][nb][rh * 2 + c] = -INFINITY;
     }
 }
 
 // Running maximum and sum of rows 2t, 2t + 1; the weights, transposed to the second operand of
 // O^T = V^T P^T (pt; pl: what their rounding left, 16-bit caches).
 template <int FMT, int NB, int MB, int OM, bool kBF16>
-__device__ __forceinline__ void softmax_step(float (&s)[NB][MB][4], const float (&rs)[NB][2], float (&m)[NB][2], float (&l)[NB][2],
-                                             float (&o)[NB][OM][4], uint32_t (&pt)[NB][MB][2], uint32_t (&pl)[NB][MB][2]) {
+__device__ __forceinline__ void softmax_step(float (&s)[MB][NB][4], const float (&rs)[NB][2], float (&m)[NB][2], float (&l)[NB][2],
+                                             float (&o)[NB][OM][4], uint32_t (&pt)[MB][NB][2], uint32_t (&pl)[MB][NB][2]) {
   bool grew = false;
   float alpha[NB][2];
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      float x = s[nb][0][c];
+      float x = s[0][nb][c];
 #pragma unroll
-      for (int mb = 0; mb < MB; ++mb) x = fmaxf(x, fmaxf(s[nb][mb][c], s[nb][mb][2 + c]));
+      for (int mb = 0; mb < MB; ++mb) x = fmaxf(x, fmaxf(s[mb][nb][c], s[mb][nb][2 + c]));
       x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
       x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
       x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
@@ -449,7 +487,7 @@ __device__ __forceinline__ void softmax_step(float (&s)[NB][MB][4], const float 
       for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
         for (int rh = 0; rh < 2; ++rh) {
-          float& e = s[nb][mb][2 * rh + c];
+          float& e = s[mb][nb][2 * rh + c];
           e = exp2_fast(__fmaf_rn(e, rs[nb][c], -ref));
           sum += e;
         }
@@ -469,12 +507,12 @@ __device__ __forceinline__ void softmax_step(float (&s)[NB][MB][4], const float 
     for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
       for (int rh = 0; rh < 2; ++rh) {
-        const float x = s[nb][mb][2 * rh], y = s[nb][mb][2 * rh + 1];
+        const float x = s[mb][nb][2 * rh], y = s[mb][nb][2 * rh + 1];
         const uint32_t w = pack2(x, y, kBF16);
-        pt[nb][mb][rh] = transpose8x8(w);
+        pt[mb][nb][rh] = transpose8x8(w);
         if constexpr (FMT == KV_CACHE_SRC) {
           const float2 r = widen2<kBF16>(w);
-          pl[nb][mb][rh] = transpose8x8(pack2(x - r.x, y - r.y, kBF16));
+          pl[mb][nb][rh] = transpose8x8(pack2(x - r.x, y - r.y, kBF16));
         }
       }
 }
@@ -845,24 +883,22 @@ __global__ void __launch_bounds__(32 * kSplitWarps, (kSplitCtas<DP, NB>))
       wait_async<NU - 2>();
       __syncwarp();
       copy_unit((NU - 1) & 1);
-      float s[NB][MB][4];
+      float s[MB][NB][4];
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) s[nb][mb][c] = 0.0f;
+          for (int c = 0; c < 4; ++c) s[mb][nb][c] = 0.0f;
       const uint32_t kat = ring + slot * L::kUnit;
 #pragma unroll
       for (int mb = 0; mb < MB; ++mb) {
-        uint32_t sc[2] = {0u, 0u};
 #pragma unroll
         for (int i = 0; i < L::KN; ++i) {
-          uint32_t f[2][L::KD / 2];
+          uint32_t w[2][L::KC / 4], sc[2] = {0u, 0u};
 #pragma unroll
           for (int rh = 0; rh < 2; ++rh) {
-            uint32_t w[L::KC / 4];
-            ld_own<L::KC>(w, kat + (((mb * 2 + rh) * L::KN + i) * 32 + lane) * L::KC);
+            ld_own<L::KC>(w[rh], kat + (((mb * 2 + rh) * L::KN + i) * 32 + lane) * L::KC);
             if constexpr (FMT == KV_CACHE_E2M1) {
               const uint32_t srow = kat + TW * L::kRow + (mb * 16 + rh * 8 + g) * L::kScaleRow;
               uint32_t sat = srow + (t + 4 * i) * (L::KD / kFp4Block);
@@ -874,14 +910,8 @@ __global__ void __launch_bounds__(32 * kSplitWarps, (kSplitCtas<DP, NB>))
                 if constexpr (L::KD > kFp4Block) sc[rh] |= ld_shared_u8(sat + 1) << 8;
               }
             }
-            k_pairs<FMT, DP>(f[rh], w, sc[rh]);
           }
-#pragma unroll
-          for (int j = 0; j < L::KD / 4; ++j)
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-              mma16816<kBF16>(s[nb][mb], f[0][2 * j], f[1][2 * j], f[0][2 * j + 1], f[1][2 * j + 1],
-                              qf[nb][i * (L::KD / 2) + 2 * j], qf[nb][i * (L::KD / 2) + 2 * j + 1]);
+          k_products<FMT, DP, NB, kBF16>(s[mb], w, sc, qf, i * (L::KD / 2));
         }
       }
       next_slot();
@@ -892,11 +922,11 @@ __global__ void __launch_bounds__(32 * kSplitWarps, (kSplitCtas<DP, NB>))
                             (a.window == 0 || j0 > p_hi - a.window || j0 + TW - 1 < a.sinks);
       const bool any_bad = __any_sync(0xFFFFFFFFu, bad);
       if (!all_seen || any_bad) {
-        hide_scores<NB, MB>(a, table, j0, li < list.n ? p_hi : -1, any_bad, p_first, row0, s);
+        hide_scores<NB, MB>(a, table, j0, li < list.n ? p_hi : -1, any_bad, p_first, row0, g, s);
       }
 
       // running maximum and sum
-      uint32_t pt[NB][MB][2], pl[NB][MB][2];
+      uint32_t pt[MB][NB][2], pl[MB][NB][2];
       softmax_step<FMT, NB, MB, OM, kBF16>(s, rs, m, l, o, pt, pl);
 
       // O^T += V^T P^T
@@ -918,31 +948,17 @@ __global__ void __launch_bounds__(32 * kSplitWarps, (kSplitCtas<DP, NB>))
         }
 #pragma unroll
         for (int i = 0; i < L::VN; ++i) {
-          uint32_t f[2][L::VD];
+          uint32_t w[4][L::VC / 4], sc[2][2] = {{0u, 0u}, {0u, 0u}};
 #pragma unroll
-          for (int pr = 0; pr < 2; ++pr) {
-            uint32_t wa[L::VC / 4], wb[L::VC / 4], sc[2] = {0u, 0u};
-            ld_own<L::VC>(wa, vat + (((mb * 4 + 2 * pr) * L::VN + i) * 32 + lane) * L::VC);
-            ld_own<L::VC>(wb, vat + (((mb * 4 + 2 * pr + 1) * L::VN + i) * 32 + lane) * L::VC);
+          for (int x = 0; x < 4; ++x) {
+            ld_own<L::VC>(w[x], vat + (((mb * 4 + x) * L::VN + i) * 32 + lane) * L::VC);
             if constexpr (FMT == KV_CACHE_E2M1) {
 #pragma unroll
-              for (int x = 0; x < (L::VD + kFp4Block - 1) / kFp4Block; ++x) {
-                const uint32_t blk = (g + 8 * i) * L::VD / kFp4Block + x;
-                sc[x] = ld_shared_u8(srow[2 * pr] + blk) | (ld_shared_u8(srow[2 * pr + 1] + blk) << 8);
-              }
+              for (int y = 0; y < (L::VD + kFp4Block - 1) / kFp4Block; ++y)
+                sc[x >> 1][y] |= ld_shared_u8(srow[x] + (g + 8 * i) * L::VD / kFp4Block + y) << (8 * (x & 1));
             }
-            v_pairs<FMT, DP>(f[pr], wa, wb, sc);
           }
-#pragma unroll
-          for (int j = 0; j < L::VD / 2; ++j)
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-              mma16816<kBF16>(o[nb][i * (L::VD / 2) + j], f[0][2 * j], f[0][2 * j + 1], f[1][2 * j], f[1][2 * j + 1],
-                              pt[nb][mb][0], pt[nb][mb][1]);
-              if constexpr (FMT == KV_CACHE_SRC)
-                mma16816<kBF16>(o[nb][i * (L::VD / 2) + j], f[0][2 * j], f[0][2 * j + 1], f[1][2 * j], f[1][2 * j + 1],
-                                pl[nb][mb][0], pl[nb][mb][1]);
-            }
+          v_products<FMT, DP, NB, kBF16>(o, w, sc, pt[mb], pl[mb], i * (L::VD / 2));
         }
       }
       next_slot();
@@ -1181,16 +1197,22 @@ kv_status launch_chained(void (*kernel)(P...), int64_t grid, int threads, int sm
   return e == cudaSuccess ? KV_OK : cuda_fail(e);
 }
 
+// The KV heads that a CTA with room for `most` takes: the most that divide them.
+inline int heads_of_cta(int kv_heads, int most) {
+  int n = 1;
+  for (int h = 2; h <= most; ++h)
+    if (kv_heads % h == 0) n = h;
+  return n;
+}
+
 // Heads and warps of a CTA, and the workspace; returns the CTAs to launch, at most `full` where items
 // are split.
 template <int DP>
-int64_t set_up_split(SplitParams& p, int rows, int tile, int64_t full, void* work, int64_t work_bytes, int64_t max_keys) {
+int64_t set_up_split(SplitParams& p, int heads, int rows, int tile, int64_t full, void* work, int64_t work_bytes, int64_t max_keys) {
   const AttendParams& a = p.a;
   p.rows = rows;
-  p.hw = 1;
-  for (int h = 2; h <= kSplitWarps; ++h)
-    if (a.kv_heads % h == 0) p.hw = h;
-  p.subs = kSplitWarps / p.hw;
+  p.hw = heads_of_cta(a.kv_heads, heads);
+  p.subs = heads / p.hw;
   p.hgroups = a.kv_heads / p.hw;
   p.min_steps = KV_ATTEND_MIN_STEPS;
   // An item that cannot be longer than the shortest share is not split, nor is
@@ -1236,7 +1258,7 @@ kv_status launch_split(SplitParams p, void* work, int64_t work_bytes, int64_t ma
   static SmemOptIn opt_in;
   st = opt_in(reinterpret_cast<const void*>(kernel), kSmem);
   if (st != KV_OK) return st;
-  const int64_t grid = set_up_split<DP>(p, 8 * NB, L::TW, static_cast<int64_t>(sms) * kSplitCtas<DP, NB>, work, work_bytes, max_keys);
+  const int64_t grid = set_up_split<DP>(p, kSplitWarps, 8 * NB, L::TW, static_cast<int64_t>(sms) * kSplitCtas<DP, NB>, work, work_bytes, max_keys);
   st = launch_chained(kernel, grid, 32 * p.hw * p.subs, kSmem, stream, p);
   if (st != KV_OK || !p.split) return st;
   return launch_join<FMT, DP>(p, sms, stream);

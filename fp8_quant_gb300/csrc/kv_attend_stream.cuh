@@ -24,28 +24,39 @@
 
 namespace kvimpl {
 
-constexpr int kStreamRegs = 208, kStreamCopyRegs = 88;  // of 168 at launch
-static_assert(256 * kStreamRegs + 128 * kStreamCopyRegs <= 384 * 168, "the registers of the launch");
+// A run of bytes (both ends and the length multiples of 16).
+__device__ __forceinline__ void copy_run(uint32_t dst, const uint8_t* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+               ::"r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
+}
 
 struct StreamParams {
   SplitParams s;
   int32_t box;   // keys of a TMA box: TW, or 16
+  int32_t flat_scales;  // e2m1: the scales of neighbouring keys and all heads are one run of bytes
   CUtensorMap k_map, v_map, ks_map, vs_map;
 };
 
-template <int FMT, int DP, int NB>
+// kPack: rows shorter than 128 bytes whose heads lie side by side are fetched two or four heads at a
+// time, as 128-byte rows: TMA takes about three cycles a row whatever its length (64-byte rows
+// alone held the 4-bit cache to 3.8 TB/s).
+template <int FMT, int DP, int NB, bool kPack>
 struct StreamLayout {
   using L = Layout<FMT, DP>;
-  static constexpr int kWarps = kSplitWarps;                     // that multiply
+  static constexpr int kHeads = kSplitWarps;                     // heads, or tiles of fewer, of a CTA: a warp each
+  static constexpr int kWarps = kHeads;
   static constexpr int kThreads = 32 * (kWarps + 4);             // and a warpgroup of which one warp copies
-  static constexpr int W = L::kRow < 128 ? L::kRow : 128;        // bytes of a row in one box
-  static constexpr int kSpans = L::kRow / W;
-  static constexpr int kCodes = kSplitWarps * L::TW * L::kRow;
-  static constexpr int kUnit = kCodes + (FMT == KV_CACHE_E2M1 ? kSplitWarps * L::TW * (DP / 16) : 0);
+  static constexpr int kLaunchRegs = 168, kRegs = 208, kCopyRegs = 88;
+  static_assert(32 * kWarps * kRegs + 128 * kCopyRegs <= kThreads * kLaunchRegs, "the registers of the launch");
+  static constexpr int kPerRow = kPack ? 128 / L::kRow : 1;      // heads of a row of a box
+  static constexpr int W = kPack || L::kRow > 128 ? 128 : L::kRow;  // its bytes
+  static constexpr int kSpans = L::kRow > 128 ? L::kRow / 128 : 1;  // boxes of a head's row
+  static constexpr int kCodes = kHeads * L::TW * L::kRow;
+  static constexpr int kUnit = kCodes + (FMT == KV_CACHE_E2M1 ? (kHeads * L::TW * (DP / 16) + 1023) / 1024 * 1024 : 0);
   static constexpr int kFrag = (NB * (L::VN * L::VD / 2) * 4 + 4 * NB) * 128;  // a warp's sums and statistics
-  static constexpr int kJoin = kWarps / 2 * kFrag;                // half of them write, half read
-  static constexpr int kFit = (226 * 1024 - 2048 - kJoin) / kUnit;
-  static constexpr int kUnits = kFit > 8 ? 8 : kFit;
+  static constexpr int kJoin = kWarps / 2 * kFrag;                // at most half of them write at a time
+  static constexpr int kFit = (219 * 1024 - 3072 - kJoin) / kUnit;      // 8 KB are left to the static part
+  static constexpr int kUnits = kFit > 20 ? 20 : kFit;
   static constexpr int kOffJoin = kUnits * kUnit;
   static constexpr int kOffBars = kOffJoin + kJoin;
   static constexpr int kOffDesc = kOffBars + (2 * kUnits + 1) * 8 + 8;
@@ -61,11 +72,11 @@ struct StreamStep {
 // of an item's steps in a share: the first, the last; the share has all of them, or the item's first; no more steps
 constexpr int kFirst = 1, kLast = 2, kWhole = 4, kBegins = 8, kStop = 16;
 
-template <int FMT, int DP, int NB, bool kBF16>
-__global__ void __launch_bounds__(StreamLayout<FMT, DP, NB>::kThreads, 1)
+template <int FMT, int DP, int NB, bool kBF16, bool kPack>
+__global__ void __launch_bounds__(StreamLayout<FMT, DP, NB, kPack>::kThreads, 1)
     kv_attend_stream(const __grid_constant__ StreamParams sp) {
   using L = Layout<FMT, DP>;
-  using S = StreamLayout<FMT, DP, NB>;
+  using S = StreamLayout<FMT, DP, NB, kPack>;
   constexpr int TW = L::TW, MB = L::MB, W = S::W, QP = DP / 8, OM = L::VN * L::VD / 2;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ int64_t sh_scan[S::kThreads / 32];
@@ -140,7 +151,7 @@ __global__ void __launch_bounds__(StreamLayout<FMT, DP, NB>::kThreads, 1)
   const int32_t G = static_cast<int32_t>(a.group.d);
 
   // (all warps of a warpgroup execute the same one)
-  if (warp >= S::kWarps) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kStreamCopyRegs));
+  if (warp >= S::kWarps) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kCopyRegs));
   if (warp == S::kWarps) {
     // ======================================================================================
     // the copies
@@ -148,7 +159,7 @@ __global__ void __launch_bounds__(StreamLayout<FMT, DP, NB>::kThreads, 1)
     const int32_t nbox = TW / sp.box;                  // boxes of a tile
     const int32_t sub = static_cast<int32_t>(lane) / nbox, part = static_cast<int32_t>(lane) - sub * nbox;
     const bool mine = sub < p.subs;                    // the lane has a box of every step
-    const uint32_t box_bytes = static_cast<uint32_t>(sp.box) * p.hw * W;  // of one span
+    const uint32_t box_bytes = static_cast<uint32_t>(sp.box * p.hw / S::kPerRow) * W;
     const uint32_t sc_bytes = FMT == KV_CACHE_E2M1 ? static_cast<uint32_t>(sp.box * p.hw * (a.head_dim / 16)) : 0u;
     const uint32_t at_codes = static_cast<uint32_t>(sub) * (p.hw * TW * L::kRow) + static_cast<uint32_t>(part) * S::kSpans * box_bytes;
     const uint32_t at_scales = S::kCodes + static_cast<uint32_t>(sub * nbox + part) * sc_bytes;
@@ -237,9 +248,14 @@ __global__ void __launch_bounds__(StreamLayout<FMT, DP, NB>::kThreads, 1)
             if (has) {
 #pragma unroll
               for (int x = 0; x < S::kSpans; ++x)
-                tma_box(at + at_codes + x * box_bytes, kv ? &sp.v_map : &sp.k_map, bar, x * W, static_cast<int32_t>(in_page), hg * p.hw, page);
-              if constexpr (FMT == KV_CACHE_E2M1)
-                tma_box(at + at_scales, kv ? &sp.vs_map : &sp.ks_map, bar, hg * p.hw * (a.head_dim / 16), static_cast<int32_t>(in_page), 0, page);
+                tma_box(at + at_codes + x * box_bytes, kv ? &sp.v_map : &sp.k_map, bar, x * W, static_cast<int32_t>(in_page), hg * p.hw / S::kPerRow, page);
+              if constexpr (FMT == KV_CACHE_E2M1) {
+                if (sp.flat_scales)
+                  copy_run(at + at_scales, (kv ? a.v_sc : a.k_sc) + (page == a.num_pages ? 0 : wide(page, kv ? p.vs_page : p.ks_page) +
+                                               wide(in_page, kv ? p.vs_slot : p.ks_slot)), sc_bytes, bar);
+                else
+                  tma_box(at + at_scales, kv ? &sp.vs_map : &sp.ks_map, bar, hg * p.hw * (a.head_dim / 16), static_cast<int32_t>(in_page), 0, page);
+              }
             }
           }
           if (!ok) break;
@@ -259,17 +275,21 @@ __global__ void __launch_bounds__(StreamLayout<FMT, DP, NB>::kThreads, 1)
     // ======================================================================================
     // the products
     // ======================================================================================
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kStreamRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kRegs));
     const uint32_t g = lane >> 2, t = lane & 3u;
     const bool used = static_cast<int32_t>(warp) < p.hw * p.subs;
     const int32_t hl = static_cast<int32_t>(warp) % p.hw, sub = static_cast<int32_t>(warp) / p.hw;
+    // Row g of a product is key gk of its eight: lanes that read together then meet rows of both
+    // parities and of both halves of the swizzle.
+    const uint32_t gk = g ^ ((g & 1u) << 2);
+    const uint32_t in_row = static_cast<uint32_t>(hl % S::kPerRow) * (L::kRow / 16);  // the head's first 16 bytes of a packed row
     const float kscale = a.scale_log2 * tensor_scale(a.k_scale);
     const float vscale = tensor_scale(a.v_scale);
     const uint32_t ds = static_cast<uint32_t>(a.head_dim) / 16;
     // where the warp's rows are in a unit
-    const uint32_t head_at = static_cast<uint32_t>(sub) * (p.hw * TW * L::kRow) + static_cast<uint32_t>(hl * sp.box) * W;
-    const uint32_t mb_step = sp.box == 16 ? static_cast<uint32_t>(S::kSpans * p.hw) * 16u * W : 16u * W;
-    const uint32_t span_step = static_cast<uint32_t>(p.hw * sp.box) * W;
+    const uint32_t head_at = static_cast<uint32_t>(sub) * (p.hw * TW * L::kRow) + static_cast<uint32_t>(hl / S::kPerRow * sp.box) * W;
+    const uint32_t span_step = static_cast<uint32_t>(p.hw / S::kPerRow * sp.box) * W;
+    const uint32_t mb_step = sp.box == 16 ? S::kSpans * span_step : 16u * W;
     const uint32_t sc_row = static_cast<uint32_t>(p.hw) * ds;
     const uint32_t sc_at = S::kCodes + static_cast<uint32_t>(sub * TW) * sc_row + static_cast<uint32_t>(hl) * ds;
     float* const frag = reinterpret_cast<float*>(smem_ptr + S::kOffJoin);
@@ -309,7 +329,7 @@ __global__ void __launch_bounds__(StreamLayout<FMT, DP, NB>::kThreads, 1)
         load_queries<FMT, DP, NB>(a, seq, kvh, row0, nrows, kscale,
                                   [&](int i) {
                                     const int pc = 2 * i / L::KD, rem = 2 * i % L::KD;
-                                    return W == 128 ? ((pc >> 1) * 8 + 2 * static_cast<int>(t) + (pc & 1)) * L::KD + rem
+                                    return L::kRow >= 128 ? ((pc >> 1) * 8 + 2 * static_cast<int>(t) + (pc & 1)) * L::KD + rem
                                                     : static_cast<int>(t) * L::KD + rem;
                                   }, qf, rs);
 #pragma unroll
@@ -325,48 +345,44 @@ __global__ void __launch_bounds__(StreamLayout<FMT, DP, NB>::kThreads, 1)
       const int32_t share = d.share;
       const int32_t li = step * p.subs + sub, j0 = list.tile(li) * TW;
       const bool work = used && li < list.n;
-      uint32_t pt[NB][MB][2], pl[NB][MB][2];
+      uint32_t pt[MB][NB][2], pl[MB][NB][2];
       if (work) {
         // S^T = K Q^T
-        float s[NB][MB][4];
+        float s[MB][NB][4];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
           for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) s[nb][mb][c] = 0.0f;
-        const uint32_t kat = ring + ks * S::kUnit + head_at + g * W;
-        const uint32_t scat = ring + ks * S::kUnit + sc_at + g * sc_row;
+            for (int c = 0; c < 4; ++c) s[mb][nb][c] = 0.0f;
+        const uint32_t kat = ring + ks * S::kUnit + head_at + gk * W;
+        const uint32_t scat = ring + ks * S::kUnit + sc_at + gk * sc_row;
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb) {
 #pragma unroll
           for (int i = 0; i < L::KN; ++i) {
             // rows g and g + 8 share a swizzle
-            const uint32_t piece = W == 128 ? ((2u * t + (i & 1)) ^ g) << 4 : W == 64 ? (t ^ ((g >> 1) & 3u)) << 4 : t * L::KC;
-            uint32_t f[2][L::KD / 2];
+            const uint32_t piece = L::kRow >= 128 ? ((2u * t + (i & 1)) ^ gk) << 4
+                                   : kPack        ? (((in_row + t * L::KC / 16) ^ gk) << 4) + t * L::KC % 16
+                                   : W == 64      ? (t ^ ((gk >> 1) & 3u)) << 4
+                                                  : t * L::KC;
+            uint32_t w[2][L::KC / 4], sc[2] = {0u, 0u};
 #pragma unroll
             for (int rh = 0; rh < 2; ++rh) {
-              uint32_t w[L::KC / 4], sc = 0u;
-              ld_own<L::KC>(w, kat + mb * mb_step + (W == 128 ? i >> 1 : 0) * span_step + rh * 8 * W + piece);
+              ld_own<L::KC>(w[rh], kat + mb * mb_step + (L::kRow >= 128 ? i >> 1 : 0) * span_step + rh * 8 * W + piece);
               if constexpr (FMT == KV_CACHE_E2M1) {
-                const uint32_t at = scat + (mb * 16 + rh * 8) * sc_row + (W == 128 ? 2u * t + i : t) * (L::KD / kFp4Block);
-                sc = L::KD > kFp4Block ? ld_shared_u16(at) : ld_shared_u8(at);
+                const uint32_t at = scat + (mb * 16 + rh * 8) * sc_row + (L::kRow >= 128 ? 2u * t + i : t) * (L::KD / kFp4Block);
+                sc[rh] = L::KD > kFp4Block ? ld_shared_u16(at) : ld_shared_u8(at);
               }
-              k_pairs<FMT, DP>(f[rh], w, sc);
             }
-#pragma unroll
-            for (int j = 0; j < L::KD / 4; ++j)
-#pragma unroll
-              for (int nb = 0; nb < NB; ++nb)
-                mma16816<kBF16>(s[nb][mb], f[0][2 * j], f[1][2 * j], f[0][2 * j + 1], f[1][2 * j + 1],
-                                qf[nb][i * (L::KD / 2) + 2 * j], qf[nb][i * (L::KD / 2) + 2 * j + 1]);
+            k_products<FMT, DP, NB, kBF16>(s[mb], w, sc, qf, i * (L::KD / 2));
           }
         }
         __syncwarp();
         if (lane == 0u) bar_arrive(empty + 8 * ks);
         const bool bad = sh_bad != 0;
         if (bad || !(j0 + TW - 1 <= p_lo && (a.window == 0 || j0 > p_hi - a.window || j0 + TW - 1 < a.sinks)))
-          hide_scores<NB, MB>(a, a.table + static_cast<int64_t>(b) * a.table_stride, j0, p_hi, bad, seq.len - seq.nq, row0, s);
+          hide_scores<NB, MB>(a, a.table + static_cast<int64_t>(b) * a.table_stride, j0, p_hi, bad, seq.len - seq.nq, row0, gk, s);
         softmax_step<FMT, NB, MB, OM, kBF16>(s, rs, m, l, o, pt, pl);
       } else {
         __syncwarp();
@@ -388,7 +404,10 @@ __global__ void __launch_bounds__(StreamLayout<FMT, DP, NB>::kThreads, 1)
               const uint32_t at = vat + static_cast<uint32_t>(r >> 4) * mb_step + static_cast<uint32_t>(r & 15) * W;
 #pragma unroll
               for (int x = 0; x < S::kSpans; ++x)
-                if (lane < W / 16) asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at + x * span_step + lane * 16u), "r"(0u) : "memory");
+                if (lane < (kPack ? L::kRow : W) / 16) {
+                  const uint32_t c = kPack ? (in_row + lane) ^ (static_cast<uint32_t>(r) & 7u) : lane;
+                  asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at + x * span_step + c * 16u), "r"(0u) : "memory");
+                }
             }
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before TMA fills the unit again
@@ -398,33 +417,22 @@ __global__ void __launch_bounds__(StreamLayout<FMT, DP, NB>::kThreads, 1)
         for (int mb = 0; mb < MB; ++mb) {
 #pragma unroll
           for (int i = 0; i < L::VN; ++i) {
-            uint32_t f[2][L::VD];
+            uint32_t w[4][L::VC / 4], sc[2][2] = {{0u, 0u}, {0u, 0u}};
 #pragma unroll
-            for (int pr = 0; pr < 2; ++pr) {
-              uint32_t w2[2][L::VC / 4], sc[2] = {0u, 0u};
-#pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                const uint32_t r = 2u * t + x;  // row 8 * pr + r of the 16
-                const uint32_t piece = W == 128 ? (g ^ r) << 4 : W == 64 ? (((g >> 1) ^ t) << 4) + (g & 1u) * 8u : g * L::VC;
-                ld_own<L::VC>(w2[x], vat + mb * mb_step + i * span_step + (8u * pr + r) * W + piece);
-                if constexpr (FMT == KV_CACHE_E2M1) {
-                  const uint32_t at = unit_at + sc_at + (mb * 16 + 8u * pr + r) * sc_row + (g + 8 * i) * L::VD / kFp4Block;
-                  sc[0] |= ld_shared_u8(at) << (8 * x);
-                  if constexpr (L::VD > kFp4Block) sc[1] |= ld_shared_u8(at + 1) << (8 * x);
-                }
+            for (int x = 0; x < 4; ++x) {
+              const uint32_t r = (x & 1) ? (2u * t + 1u) ^ 4u : 2u * t, row = 8u * (x >> 1) + r;
+              const uint32_t piece = L::kRow >= 128 ? (g ^ r) << 4
+                                     : kPack        ? (((in_row + g * L::VC / 16) ^ r) << 4) + g * L::VC % 16
+                                     : W == 64      ? (((g >> 1) ^ ((r >> 1) & 3u)) << 4) + (g & 1u) * 8u
+                                                    : g * L::VC;
+              ld_own<L::VC>(w[x], vat + mb * mb_step + i * span_step + row * W + piece);
+              if constexpr (FMT == KV_CACHE_E2M1) {
+                const uint32_t at = unit_at + sc_at + (mb * 16 + row) * sc_row + (g + 8 * i) * L::VD / kFp4Block;
+                sc[x >> 1][0] |= ld_shared_u8(at) << (8 * (x & 1));
+                if constexpr (L::VD > kFp4Block) sc[x >> 1][1] |= ld_shared_u8(at + 1) << (8 * (x & 1));
               }
-              v_pairs<FMT, DP>(f[pr], w2[0], w2[1], sc);
             }
-#pragma unroll
-            for (int j = 0; j < L::VD / 2; ++j)
-#pragma unroll
-              for (int nb = 0; nb < NB; ++nb) {
-                mma16816<kBF16>(o[nb][i * (L::VD / 2) + j], f[0][2 * j], f[0][2 * j + 1], f[1][2 * j], f[1][2 * j + 1],
-                                pt[nb][mb][0], pt[nb][mb][1]);
-                if constexpr (FMT == KV_CACHE_SRC)
-                  mma16816<kBF16>(o[nb][i * (L::VD / 2) + j], f[0][2 * j], f[0][2 * j + 1], f[1][2 * j], f[1][2 * j + 1],
-                                  pl[nb][mb][0], pl[nb][mb][1]);
-              }
+            v_products<FMT, DP, NB, kBF16>(o, w, sc, pt[mb], pl[mb], i * (L::VD / 2));
           }
         }
       }
@@ -443,9 +451,10 @@ __global__ void __launch_bounds__(StreamLayout<FMT, DP, NB>::kThreads, 1)
           x += __shfl_xor_sync(0xFFFFFFFFu, x, 16);
           l[nb][c] = x;
         }
-      for (int32_t half = p.subs / 2; half > 0; half >>= 1) {
-        float* const at = frag + ((sub & (half - 1)) * p.hw + hl) * (S::kFrag / 4) + lane;  // a float a lane
-        if (used && sub >= half && sub < 2 * half) {
+      for (int32_t many = p.subs; many > 1; many = (many + 1) / 2) {
+        const int32_t half = (many + 1) / 2;  // subs half .. many - 1 hand theirs to 0 .. many - half - 1
+        float* const at = frag + ((sub >= half ? sub - half : sub) * p.hw + hl) * (S::kFrag / 4) + lane;  // a float a lane
+        if (used && sub >= half && sub < many) {
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
@@ -460,7 +469,7 @@ __global__ void __launch_bounds__(StreamLayout<FMT, DP, NB>::kThreads, 1)
           }
         }
         join_wait();
-        if (used && sub < half) {
+        if (used && sub < many - half) {
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -496,12 +505,12 @@ __global__ void __launch_bounds__(StreamLayout<FMT, DP, NB>::kThreads, 1)
 // Host
 // ---------------------------------------------------------------------------
 
-// Launches the kernel of one format and padded head dim (p.s as set_up_split() left it, one CTA an SM).
-template <int FMT, int DP, int NB, bool kBF16>
+// Launches the kernel of one format and padded head dim.
+template <int FMT, int DP, int NB, bool kBF16, bool kPack>
 kv_status launch_stream(StreamParams sp, void* work, int64_t work_bytes, int64_t max_keys, cudaStream_t stream) {
   using L = Layout<FMT, DP>;
-  using S = StreamLayout<FMT, DP, NB>;
-  auto* kernel = kv_attend_stream<FMT, DP, NB, kBF16>;
+  using S = StreamLayout<FMT, DP, NB, kPack>;
+  auto* kernel = kv_attend_stream<FMT, DP, NB, kBF16, kPack>;
   static_assert(S::kTotal <= 227 * 1024 - 8 * 1024, "shared memory, with the static part");
   int sms = 0;
   kv_status st = current_sm_count(&sms);
@@ -509,26 +518,36 @@ kv_status launch_stream(StreamParams sp, void* work, int64_t work_bytes, int64_t
   static SmemOptIn opt_in;
   st = opt_in(reinterpret_cast<const void*>(kernel), S::kTotal);
   if (st != KV_OK) return st;
-  int64_t grid = set_up_split<DP>(sp.s, 8 * NB, L::TW, sms, work, work_bytes, max_keys);
+  int64_t grid = set_up_split<DP>(sp.s, S::kHeads, 8 * NB, L::TW, sms, work, work_bytes, max_keys);
   if (!sp.s.split && grid > sms) grid = sms;  // CTAs go on to further items by themselves
   const kv_status ls = launch_chained(kernel, grid, S::kThreads, S::kTotal, stream, sp);
   if (ls != KV_OK || !sp.s.split) return ls;
   return launch_join<FMT, DP>(sp.s, sms, stream);
 }
 
+template <int FMT, int DP, bool kBF16>
+kv_status launch_stream_dim(const StreamParams& sp, bool wide, bool pack, void* work, int64_t work_bytes, int64_t max_keys,
+                            cudaStream_t stream) {
+  if constexpr (Layout<FMT, DP>::kRow < 128) {
+    if (pack)
+      return wide ? launch_stream<FMT, DP, 2, kBF16, true>(sp, work, work_bytes, max_keys, stream)
+                  : launch_stream<FMT, DP, 1, kBF16, true>(sp, work, work_bytes, max_keys, stream);
+  }
+  return wide ? launch_stream<FMT, DP, 2, kBF16, false>(sp, work, work_bytes, max_keys, stream)
+              : launch_stream<FMT, DP, 1, kBF16, false>(sp, work, work_bytes, max_keys, stream);
+}
+
 template <int FMT, bool kBF16>
-kv_status launch_stream_fmt(const StreamParams& sp, bool wide, void* work, int64_t work_bytes, int64_t max_keys, cudaStream_t stream) {
-  if (sp.s.a.head_dim <= 64)
-    return wide ? launch_stream<FMT, 64, 2, kBF16>(sp, work, work_bytes, max_keys, stream)
-                : launch_stream<FMT, 64, 1, kBF16>(sp, work, work_bytes, max_keys, stream);
-  return wide ? launch_stream<FMT, 128, 2, kBF16>(sp, work, work_bytes, max_keys, stream)
-              : launch_stream<FMT, 128, 1, kBF16>(sp, work, work_bytes, max_keys, stream);
+kv_status launch_stream_fmt(const StreamParams& sp, bool wide, bool pack, void* work, int64_t work_bytes, int64_t max_keys,
+                            cudaStream_t stream) {
+  return sp.s.a.head_dim <= 64 ? launch_stream_dim<FMT, 64, kBF16>(sp, wide, pack, work, work_bytes, max_keys, stream)
+                               : launch_stream_dim<FMT, 128, kBF16>(sp, wide, pack, work, work_bytes, max_keys, stream);
 }
 
 // The formats' instantiations, a translation unit each.
-kv_status stream_bf16(const StreamParams& p, bool wide, void* work, int64_t work_bytes, int64_t max_keys, cudaStream_t stream);
-kv_status stream_f16(const StreamParams& p, bool wide, void* work, int64_t work_bytes, int64_t max_keys, cudaStream_t stream);
-kv_status stream_e4m3(const StreamParams& p, bool wide, void* work, int64_t work_bytes, int64_t max_keys, cudaStream_t stream);
-kv_status stream_e2m1(const StreamParams& p, bool wide, void* work, int64_t work_bytes, int64_t max_keys, cudaStream_t stream);
+kv_status stream_bf16(const StreamParams& p, bool wide, bool pack, void* work, int64_t work_bytes, int64_t max_keys, cudaStream_t stream);
+kv_status stream_f16(const StreamParams& p, bool wide, bool pack, void* work, int64_t work_bytes, int64_t max_keys, cudaStream_t stream);
+kv_status stream_e4m3(const StreamParams& p, bool wide, bool pack, void* work, int64_t work_bytes, int64_t max_keys, cudaStream_t stream);
+kv_status stream_e2m1(const StreamParams& p, bool wide, bool pack, void* work, int64_t work_bytes, int64_t max_keys, cudaStream_t stream);
 
 }  // namespace kvimpl
