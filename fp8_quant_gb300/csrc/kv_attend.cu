@@ -207,8 +207,9 @@ extern "C" kv_status kv_attend(const void* q, void* out, float* lse, const void*
         (format != KV_CACHE_E2M1 || head_dim % 32 == 0)) {
       StreamParams tp = {};
       tp.s = sp;
-      const int tile = format == KV_CACHE_SRC && head_dim > 64 ? 16 : 32;
-      tp.box = page_size % tile == 0 ? tile : 16;
+      const int tile = format == KV_CACHE_SRC && head_dim > 64 ? 16 : format == KV_CACHE_E2M1 ? KV_STREAM_FP4_TILE : 32;
+      tp.box = tile;
+      while (page_size % tp.box != 0) tp.box /= 2;
       const int hw = heads_of_cta(num_heads, kSplitWarps);
       const int padded = (head_dim <= 64 ? 64 : 128) * bits / 8, ds = head_dim / 16;
       // short rows of neighbouring heads as rows of 128 bytes

@@ -313,36 +313,43 @@ __device__ __forceinline__ void v_word(uint32_t (&f)[kWord<FMT>], uint32_t a, ui
   }
 }
 
-// S^T += K Q^T for one piece of rows g (w[0]) and g + 8 (w[1]): KD / 4 products a block of queries,
-// whose pairs for it begin at qf[..][first].  sc: the rows' block scale codes (e2m1).
-template <int FMT, int DP, int NB, bool kBF16>
-__device__ __forceinline__ void k_products(float (&s)[NB][4], const uint32_t (&w)[2][Layout<FMT, DP>::KC / 4], const uint32_t (&sc)[2],
-                                           const uint32_t (&qf)[NB][DP / 8], int first) {
+// S^T += K Q^T for one piece of rows g (w[..][0]) and g + 8 (w[..][1]) of each 16 keys: KD / 4 products
+// a block of queries, whose pairs for it begin at qf[..][first].  sc: the rows' block scale codes
+// (e2m1).  The 16s take turns: a product waits for the one before it in the same sums.
+template <int FMT, int DP, int NB, bool kBF16, int MB>
+__device__ __forceinline__ void k_products(float (&s)[MB][NB][4], const uint32_t (&w)[MB][2][Layout<FMT, DP>::KC / 4],
+                                           const uint32_t (&sc)[MB][2], const uint32_t (&qf)[NB][DP / 8], int first) {
   constexpr int kWords = Layout<FMT, DP>::KC / 4;
   if constexpr (FMT == KV_CACHE_SRC) {
 #pragma unroll
     for (int i = 0; i < kWords; i += 2)
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-        mma16816<kBF16>(s[nb], w[0][i], w[1][i], w[0][i + 1], w[1][i + 1], qf[nb][first + i], qf[nb][first + i + 1]);
+      for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+          mma16816<kBF16>(s[mb][nb], w[mb][0][i], w[mb][1][i], w[mb][0][i + 1], w[mb][1][i + 1], qf[nb][first + i], qf[nb][first + i + 1]);
   } else {
-    uint32_t two[2] = {0u, 0u};
-    if constexpr (FMT == KV_CACHE_E2M1) {
-      two[0] = f16x2_from_e4m3x2(sc[0]);
-      two[1] = f16x2_from_e4m3x2(sc[1]);
-    }
+    uint32_t two[MB][2];
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+      for (int rh = 0; rh < 2; ++rh) two[mb][rh] = FMT == KV_CACHE_E2M1 ? f16x2_from_e4m3x2(sc[mb][rh]) : 0u;
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {
-      uint32_t f[2][kWord<FMT> / 2];
+      uint32_t f[MB][2][kWord<FMT> / 2];
 #pragma unroll
-      for (int rh = 0; rh < 2; ++rh)
-        k_word<FMT>(f[rh], w[rh][i], __byte_perm(two[rh], 0u, i * 8 / kFp4Block == 0 ? 0x1010 : 0x3232));
+      for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+        for (int rh = 0; rh < 2; ++rh)
+          k_word<FMT>(f[mb][rh], w[mb][rh][i], __byte_perm(two[mb][rh], 0u, i * 8 / kFp4Block == 0 ? 0x1010 : 0x3232));
 #pragma unroll
       for (int j = 0; j < kWord<FMT> / 2; j += 2)
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-          mma16816<kBF16>(s[nb], f[0][j], f[1][j], f[0][j + 1], f[1][j + 1], qf[nb][first + i * (kWord<FMT> / 2) + j],
-                          qf[nb][first + i * (kWord<FMT> / 2) + j + 1]);
+        for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+            mma16816<kBF16>(s[mb][nb], f[mb][0][j], f[mb][1][j], f[mb][0][j + 1], f[mb][1][j + 1],
+                            qf[nb][first + i * (kWord<FMT> / 2) + j], qf[nb][first + i * (kWord<FMT> / 2) + j + 1]);
     }
   }
 }
@@ -892,27 +899,27 @@ __global__ void __launch_bounds__(32 * kSplitWarps, (kSplitCtas<DP, NB>))
           for (int c = 0; c < 4; ++c) s[mb][nb][c] = 0.0f;
       const uint32_t kat = ring + slot * L::kUnit;
 #pragma unroll
-      for (int mb = 0; mb < MB; ++mb) {
+      for (int i = 0; i < L::KN; ++i) {
+        uint32_t w[MB][2][L::KC / 4], sc[MB][2];
 #pragma unroll
-        for (int i = 0; i < L::KN; ++i) {
-          uint32_t w[2][L::KC / 4], sc[2] = {0u, 0u};
+        for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
           for (int rh = 0; rh < 2; ++rh) {
-            ld_own<L::KC>(w[rh], kat + (((mb * 2 + rh) * L::KN + i) * 32 + lane) * L::KC);
+            ld_own<L::KC>(w[mb][rh], kat + (((mb * 2 + rh) * L::KN + i) * 32 + lane) * L::KC);
+            sc[mb][rh] = 0u;
             if constexpr (FMT == KV_CACHE_E2M1) {
               const uint32_t srow = kat + TW * L::kRow + (mb * 16 + rh * 8 + g) * L::kScaleRow;
               uint32_t sat = srow + (t + 4 * i) * (L::KD / kFp4Block);
               if (!kExact) sat += ld_shared_u32(srow + L::kScaleRow - 4);
               if (L::KD > kFp4Block && kExact) {
-                sc[rh] = ld_shared_u16(sat);
+                sc[mb][rh] = ld_shared_u16(sat);
               } else {
-                sc[rh] = ld_shared_u8(sat);
-                if constexpr (L::KD > kFp4Block) sc[rh] |= ld_shared_u8(sat + 1) << 8;
+                sc[mb][rh] = ld_shared_u8(sat);
+                if constexpr (L::KD > kFp4Block) sc[mb][rh] |= ld_shared_u8(sat + 1) << 8;
               }
             }
           }
-          k_products<FMT, DP, NB, kBF16>(s[mb], w, sc, qf, i * (L::KD / 2));
-        }
+        k_products<FMT, DP, NB, kBF16>(s, w, sc, qf, i * (L::KD / 2));
       }
       next_slot();
 
@@ -1057,7 +1064,7 @@ constexpr int kJoinWarps = 16;
 
 // Joins the parts of the items that were split, in the order of their keys:
 // `wpr` warps of the CTA take one output row.
-template <int FMT, int DP>
+template <int FMT, int DP, int TW>
 __global__ void __launch_bounds__(32 * kJoinWarps) kv_attend_join(const __grid_constant__ SplitParams p, const int32_t wpr) {
   __shared__ float sh[kJoinWarps][DP + 2];
   const AttendParams& a = p.a;
@@ -1080,7 +1087,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) kv_attend_join(const __grid_c
     }
     const AttendSeq s = attend_seq(a, b, false);
     if (tok >= s.q0 && tok < s.q0 + s.nq) {
-      const SplitGeom geom = split_geom<Layout<FMT, DP>::TW>(p, s);
+      const SplitGeom geom = split_geom<TW>(p, s);
       const int32_t G = static_cast<int32_t>(a.group.d), kvh = static_cast<int32_t>(a.group.quot(static_cast<uint32_t>(h)));
       const int32_t row = (tok - s.q0) * G + (h - kvh * G);
       const int32_t rb = row / p.rows, hg = kvh / p.hw;
@@ -1237,13 +1244,13 @@ int64_t set_up_split(SplitParams& p, int heads, int rows, int tile, int64_t full
 }
 
 // The fewer the rows, the more parts has each and the more warps take it.
-template <int FMT, int DP>
+template <int FMT, int DP, int TW>
 kv_status launch_join(const SplitParams& p, int sms, cudaStream_t stream) {
   const int64_t rows = static_cast<int64_t>(p.a.num_q) * p.a.q_heads;
   int32_t wpr = 1;
   while (wpr < kJoinWarps && rows * wpr < 16ll * sms) wpr *= 2;
   const int64_t per = kJoinWarps / wpr;
-  return launch_chained(kv_attend_join<FMT, DP>, (rows + per - 1) / per, 32 * kJoinWarps, 0, stream, p, wpr);
+  return launch_chained(kv_attend_join<FMT, DP, TW>, (rows + per - 1) / per, 32 * kJoinWarps, 0, stream, p, wpr);
 }
 
 // Launches the split kernel (and the join) of one format and padded head dim.
@@ -1261,7 +1268,7 @@ kv_status launch_split(SplitParams p, void* work, int64_t work_bytes, int64_t ma
   const int64_t grid = set_up_split<DP>(p, kSplitWarps, 8 * NB, L::TW, static_cast<int64_t>(sms) * kSplitCtas<DP, NB>, work, work_bytes, max_keys);
   st = launch_chained(kernel, grid, 32 * p.hw * p.subs, kSmem, stream, p);
   if (st != KV_OK || !p.split) return st;
-  return launch_join<FMT, DP>(p, sms, stream);
+  return launch_join<FMT, DP, L::TW>(p, sms, stream);
 }
 
 template <int FMT, bool kBF16>

@@ -22,6 +22,10 @@
 #include "kv_async.cuh"
 #include "kv_attend_split.cuh"
 
+#ifndef KV_STREAM_FP4_TILE
+#define KV_STREAM_FP4_TILE 64
+#endif
+
 namespace kvimpl {
 
 // A run of bytes (both ends and the length multiples of 16).
@@ -32,7 +36,7 @@ __device__ __forceinline__ void copy_run(uint32_t dst, const uint8_t* src, uint3
 
 struct StreamParams {
   SplitParams s;
-  int32_t box;   // keys of a TMA box: TW, or 16
+  int32_t box;   // keys of a TMA box: a tile's, or 32 or 16 of them
   int32_t flat_scales;  // e2m1: the scales of neighbouring keys and all heads are one run of bytes
   CUtensorMap k_map, v_map, ks_map, vs_map;
 };
@@ -43,6 +47,8 @@ struct StreamParams {
 template <int FMT, int DP, int NB, bool kPack>
 struct StreamLayout {
   using L = Layout<FMT, DP>;
+  // Keys of a tile: 64 4-bit ones, whose softmax would cost as much as their products otherwise.
+  static constexpr int TW = FMT == KV_CACHE_E2M1 ? KV_STREAM_FP4_TILE : L::TW;
   static constexpr int kHeads = kSplitWarps;                     // heads, or tiles of fewer, of a CTA: a warp each
   static constexpr int kWarps = kHeads;
   static constexpr int kThreads = 32 * (kWarps + 4);             // and a warpgroup of which one warp copies
@@ -51,8 +57,8 @@ struct StreamLayout {
   static constexpr int kPerRow = kPack ? 128 / L::kRow : 1;      // heads of a row of a box
   static constexpr int W = kPack || L::kRow > 128 ? 128 : L::kRow;  // its bytes
   static constexpr int kSpans = L::kRow > 128 ? L::kRow / 128 : 1;  // boxes of a head's row
-  static constexpr int kCodes = kHeads * L::TW * L::kRow;
-  static constexpr int kUnit = kCodes + (FMT == KV_CACHE_E2M1 ? (kHeads * L::TW * (DP / 16) + 1023) / 1024 * 1024 : 0);
+  static constexpr int kCodes = kHeads * TW * L::kRow;
+  static constexpr int kUnit = kCodes + (FMT == KV_CACHE_E2M1 ? (kHeads * TW * (DP / 16) + 1023) / 1024 * 1024 : 0);
   static constexpr int kFrag = (NB * (L::VN * L::VD / 2) * 4 + 4 * NB) * 128;  // a warp's sums and statistics
   static constexpr int kJoin = kWarps / 2 * kFrag;                // at most half of them write at a time
   static constexpr int kFit = (219 * 1024 - 3072 - kJoin) / kUnit;      // 8 KB are left to the static part
@@ -77,7 +83,7 @@ __global__ void __launch_bounds__(StreamLayout<FMT, DP, NB, kPack>::kThreads, 1)
     kv_attend_stream(const __grid_constant__ StreamParams sp) {
   using L = Layout<FMT, DP>;
   using S = StreamLayout<FMT, DP, NB, kPack>;
-  constexpr int TW = L::TW, MB = L::MB, W = S::W, QP = DP / 8, OM = L::VN * L::VD / 2;
+  constexpr int TW = S::TW, MB = TW / 16, W = S::W, QP = DP / 8, OM = L::VN * L::VD / 2;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ int64_t sh_scan[S::kThreads / 32];
   __shared__ int64_t sh_excl[S::kThreads + 1];  // first step of each thread's sequences; the total
@@ -289,7 +295,12 @@ __global__ void __launch_bounds__(StreamLayout<FMT, DP, NB, kPack>::kThreads, 1)
     // where the warp's rows are in a unit
     const uint32_t head_at = static_cast<uint32_t>(sub) * (p.hw * TW * L::kRow) + static_cast<uint32_t>(hl / S::kPerRow * sp.box) * W;
     const uint32_t span_step = static_cast<uint32_t>(p.hw / S::kPerRow * sp.box) * W;
-    const uint32_t mb_step = sp.box == 16 ? S::kSpans * span_step : 16u * W;
+    // where 16 keys begin: boxes of a tile lie one behind the other
+    const uint32_t box_step = S::kSpans * span_step;
+    const int per_box = sp.box / 16;  // 1, 2 or 4
+    auto mb_at = [&](int mb) -> uint32_t {
+      return per_box == 1 ? mb * box_step : per_box == 2 ? (mb >> 1) * box_step + (mb & 1) * 16u * W : mb * 16u * W;
+    };
     const uint32_t sc_row = static_cast<uint32_t>(p.hw) * ds;
     const uint32_t sc_at = S::kCodes + static_cast<uint32_t>(sub * TW) * sc_row + static_cast<uint32_t>(hl) * ds;
     float* const frag = reinterpret_cast<float*>(smem_ptr + S::kOffJoin);
@@ -358,25 +369,25 @@ __global__ void __launch_bounds__(StreamLayout<FMT, DP, NB, kPack>::kThreads, 1)
         const uint32_t kat = ring + ks * S::kUnit + head_at + gk * W;
         const uint32_t scat = ring + ks * S::kUnit + sc_at + gk * sc_row;
 #pragma unroll
-        for (int mb = 0; mb < MB; ++mb) {
+        for (int i = 0; i < L::KN; ++i) {
+          // rows gk and gk + 8 share a swizzle
+          const uint32_t piece = L::kRow >= 128 ? ((2u * t + (i & 1)) ^ gk) << 4
+                                 : kPack        ? (((in_row + t * L::KC / 16) ^ gk) << 4) + t * L::KC % 16
+                                 : W == 64      ? (t ^ ((gk >> 1) & 3u)) << 4
+                                                : t * L::KC;
+          uint32_t w[MB][2][L::KC / 4], sc[MB][2];
 #pragma unroll
-          for (int i = 0; i < L::KN; ++i) {
-            // rows g and g + 8 share a swizzle
-            const uint32_t piece = L::kRow >= 128 ? ((2u * t + (i & 1)) ^ gk) << 4
-                                   : kPack        ? (((in_row + t * L::KC / 16) ^ gk) << 4) + t * L::KC % 16
-                                   : W == 64      ? (t ^ ((gk >> 1) & 3u)) << 4
-                                                  : t * L::KC;
-            uint32_t w[2][L::KC / 4], sc[2] = {0u, 0u};
+          for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
             for (int rh = 0; rh < 2; ++rh) {
-              ld_own<L::KC>(w[rh], kat + mb * mb_step + (L::kRow >= 128 ? i >> 1 : 0) * span_step + rh * 8 * W + piece);
+              ld_own<L::KC>(w[mb][rh], kat + mb_at(mb) + (L::kRow >= 128 ? i >> 1 : 0) * span_step + rh * 8 * W + piece);
+              sc[mb][rh] = 0u;
               if constexpr (FMT == KV_CACHE_E2M1) {
                 const uint32_t at = scat + (mb * 16 + rh * 8) * sc_row + (L::kRow >= 128 ? 2u * t + i : t) * (L::KD / kFp4Block);
-                sc[rh] = L::KD > kFp4Block ? ld_shared_u16(at) : ld_shared_u8(at);
+                sc[mb][rh] = L::KD > kFp4Block ? ld_shared_u16(at) : ld_shared_u8(at);
               }
             }
-            k_products<FMT, DP, NB, kBF16>(s[mb], w, sc, qf, i * (L::KD / 2));
-          }
+          k_products<FMT, DP, NB, kBF16>(s, w, sc, qf, i * (L::KD / 2));
         }
         __syncwarp();
         if (lane == 0u) bar_arrive(empty + 8 * ks);
@@ -401,7 +412,7 @@ __global__ void __launch_bounds__(StreamLayout<FMT, DP, NB, kPack>::kThreads, 1)
               for (uint32_t x = lane; x < ds; x += 32u)
                 asm volatile("st.shared.u8 [%0], %1;" ::"r"(unit_at + sc_at + static_cast<uint32_t>(r) * sc_row + x), "h"(static_cast<uint16_t>(0)) : "memory");
             } else {
-              const uint32_t at = vat + static_cast<uint32_t>(r >> 4) * mb_step + static_cast<uint32_t>(r & 15) * W;
+              const uint32_t at = vat + mb_at(r >> 4) + static_cast<uint32_t>(r & 15) * W;
 #pragma unroll
               for (int x = 0; x < S::kSpans; ++x)
                 if (lane < (kPack ? L::kRow : W) / 16) {
@@ -425,7 +436,7 @@ __global__ void __launch_bounds__(StreamLayout<FMT, DP, NB, kPack>::kThreads, 1)
                                      : kPack        ? (((in_row + g * L::VC / 16) ^ r) << 4) + g * L::VC % 16
                                      : W == 64      ? (((g >> 1) ^ ((r >> 1) & 3u)) << 4) + (g & 1u) * 8u
                                                     : g * L::VC;
-              ld_own<L::VC>(w[x], vat + mb * mb_step + i * span_step + row * W + piece);
+              ld_own<L::VC>(w[x], vat + mb_at(mb) + i * span_step + row * W + piece);
               if constexpr (FMT == KV_CACHE_E2M1) {
                 const uint32_t at = unit_at + sc_at + (mb * 16 + row) * sc_row + (g + 8 * i) * L::VD / kFp4Block;
                 sc[x >> 1][0] |= ld_shared_u8(at) << (8 * (x & 1));
@@ -508,7 +519,6 @@ __global__ void __launch_bounds__(StreamLayout<FMT, DP, NB, kPack>::kThreads, 1)
 // Launches the kernel of one format and padded head dim.
 template <int FMT, int DP, int NB, bool kBF16, bool kPack>
 kv_status launch_stream(StreamParams sp, void* work, int64_t work_bytes, int64_t max_keys, cudaStream_t stream) {
-  using L = Layout<FMT, DP>;
   using S = StreamLayout<FMT, DP, NB, kPack>;
   auto* kernel = kv_attend_stream<FMT, DP, NB, kBF16, kPack>;
   static_assert(S::kTotal <= 227 * 1024 - 8 * 1024, "shared memory, with the static part");
@@ -518,11 +528,11 @@ kv_status launch_stream(StreamParams sp, void* work, int64_t work_bytes, int64_t
   static SmemOptIn opt_in;
   st = opt_in(reinterpret_cast<const void*>(kernel), S::kTotal);
   if (st != KV_OK) return st;
-  int64_t grid = set_up_split<DP>(sp.s, S::kHeads, 8 * NB, L::TW, sms, work, work_bytes, max_keys);
+  int64_t grid = set_up_split<DP>(sp.s, S::kHeads, 8 * NB, S::TW, sms, work, work_bytes, max_keys);
   if (!sp.s.split && grid > sms) grid = sms;  // CTAs go on to further items by themselves
   const kv_status ls = launch_chained(kernel, grid, S::kThreads, S::kTotal, stream, sp);
   if (ls != KV_OK || !sp.s.split) return ls;
-  return launch_join<FMT, DP>(sp.s, sms, stream);
+  return launch_join<FMT, DP, S::TW>(sp.s, sms, stream);
 }
 
 template <int FMT, int DP, bool kBF16>
