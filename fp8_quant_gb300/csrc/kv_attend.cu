@@ -9,6 +9,7 @@
 //                     up to 256, 16-byte aligned bases and strides.
 //  * kv_attend_rows   any head dim, alignment and stride: one warp per query
 //                     row and head, one key after the other.
+#include <algorithm>
 #include <cmath>
 #include <climits>
 
@@ -52,6 +53,32 @@ kv_status launch_rows_any(const AttendParams& p, cudaStream_t stream) {
   const uint64_t units = static_cast<uint64_t>(p.num_q) * static_cast<uint64_t>(p.q_heads);
   return p.head_dim <= 256 ? launch(kv_attend_rows<FMT, 8>, units, p, stream, 0, 128)
                            : launch(kv_attend_rows<FMT, 32>, units, p, stream, 0, 128);
+}
+
+// Whether kv_attend_tile is the faster for `rows` query rows per sequence and KV
+// head and `keys` visible keys (upper bounds: the host knows no length).  Both
+// times in us, fitted to calls of 1 to 64 sequences, 512 to 65,536 keys, 1 to 1,024 rows:
+//  * a CTA of the tile kernel takes 128 keys (up to 256 rows) in 1.4 (16-bit rows
+//    of 128 dims), 2.8 (e2m1) or 1.25 - 1.7 us (64 dims), bound by its own
+//    latencies, in items / SMs rounds; all together read at most 5.3 TB/s;
+//  * the others read the cache once per 8 or 16 rows, at 6 TB/s, or 21 (128
+//    dims) and 32 (64 dims) keys and heads a ns for e2m1, and take 16 us more
+//    (two launches, the scan of the lengths, the join).
+// E.g. 8 sequences x 4,096 keys, 32 over 8 heads of 128, 16-bit: tile 52, the
+// others 41 us at 16 rows, 52 against 65 at 32; 64 sequences x 512 keys, e2m1:
+// 61 against 39 us at 16 rows, 62 against 107 at 64.
+bool tiles_pay(const AttendParams& p, kv_cache_format format, int64_t rows, int64_t keys) {
+  int sms = 0;
+  if (current_sm_count(&sms) != KV_OK) return false;
+  const bool small = p.head_dim <= 64, fp4 = format == KV_CACHE_E2M1;
+  const double heads = static_cast<double>(p.num_seqs) * p.kv_heads, n = static_cast<double>(keys);
+  const double bytes = heads * n * 2.0 * p.head_dim * (fp4 ? 0.5625 : format == KV_CACHE_E4M3FN ? 1.0 : 2.0);
+  const double step = (fp4 ? (small ? 1.7 : 2.8) : format == KV_CACHE_E4M3FN ? (small ? 1.5 : 2.2) : (small ? 1.25 : 1.4)) *
+                      (rows > 128 ? 1.15 : 1.0);
+  const double blocks = rows <= 8 ? 1.0 : std::ceil(rows / 16.0), row_tiles = std::ceil(rows / 256.0);
+  const double tile = std::max(4.0 + std::ceil(heads * row_tiles / sms) * (3.0 + std::ceil(n / kTileKeys) * step),
+                               row_tiles * bytes / 5.3e6);
+  return tile < 16.0 + blocks * (fp4 ? heads * n / (small ? 32e3 : 21e3) : bytes / 6e6);
 }
 
 FastDiv fast_div(uint32_t d) {
@@ -158,7 +185,13 @@ extern "C" kv_status kv_attend(const void* q, void* out, float* lse, const void*
     near = near && fits(scales->k_page) && fits(scales->k_slot) && fits(scales->v_page) && fits(scales->v_slot);
   if (head_dim % 16 == 0 && head_dim <= 256 && ((q_bits | c_bits) & 15u) == 0 && near) {
     const int64_t per_seq = (num_q_tokens + num_seqs - 1) / num_seqs * p.group.d;
-    if (head_dim <= 128 && p.group.d <= 128 && per_seq >= 32) {
+    // no list of visible keys is longer
+    int64_t keys = p.max_len;
+    if (window > 0 && window < keys && sinks < keys) {
+      const int64_t most = window + sinks + (num_q_tokens + num_seqs - 1) / num_seqs + 16;
+      keys = most < keys ? most : keys;
+    }
+    if (head_dim <= 128 && p.group.d <= 128 && tiles_pay(p, format, per_seq, keys)) {
       TileParams tp = {};
       tp.a = p;
       tp.k_page = static_cast<int32_t>(s->kc_page); tp.k_slot = static_cast<int32_t>(s->kc_slot);
@@ -190,15 +223,7 @@ extern "C" kv_status kv_attend(const void* q, void* out, float* lse, const void*
       sp.ks_page = static_cast<int32_t>(scales->k_page); sp.ks_slot = static_cast<int32_t>(scales->k_slot);
       sp.vs_page = static_cast<int32_t>(scales->v_page); sp.vs_slot = static_cast<int32_t>(scales->v_slot);
     }
-    // query rows of a sequence and KV head, on average: up to 8 take one mma column block, more two
-    const int64_t rows = (num_q_tokens + num_seqs - 1) / num_seqs * p.group.d;
-    const bool wide = rows > 8;
-    // no list of visible keys is longer
-    int64_t keys = p.max_len;
-    if (window > 0 && window < keys && sinks < keys) {
-      const int64_t most = window + sinks + 17;
-      keys = most < keys ? most : keys;
-    }
+    const bool wide = per_seq > 8;  // up to 8 rows of a sequence and head take one block of mma columns, more two
     // kv_attend_stream: boxes of 16 or of a tile's keys within a page, e2m1 scales of a CTA's heads in
     // one run of whole 16 bytes, and enough cache to be worth the maps and the deep ring
     const int bits = format == KV_CACHE_SRC ? 16 : format == KV_CACHE_E4M3FN ? 8 : 4;

@@ -640,50 +640,54 @@ __global__ void __launch_bounds__(32 * kSplitWarps, (kSplitCtas<DP, NB>))
   grid_handover();
 
   // -- the share of this CTA ------------------------------------------------
+  // one row a sequence and no splits: item n is head group n % hgroups of sequence n / hgroups
+  const bool direct = !p.split && a.q_start == nullptr && static_cast<int32_t>(a.group.d) <= p.rows;
   const int32_t per_thread = (a.num_seqs + static_cast<int32_t>(blockDim.x) - 1) / static_cast<int32_t>(blockDim.x);
-  const int32_t b0 = min(static_cast<int32_t>(threadIdx.x) * per_thread, a.num_seqs);
-  const int32_t b1 = min(b0 + per_thread, a.num_seqs);
-  int64_t mine = 0;
-  for (int32_t b = b0; b < b1; ++b) mine += seq_units<L::TW>(p, b, blockIdx.x == 0);
-  int64_t incl = mine;
+  if (!direct) {
+    const int32_t b0 = min(static_cast<int32_t>(threadIdx.x) * per_thread, a.num_seqs);
+    const int32_t b1 = min(b0 + per_thread, a.num_seqs);
+    int64_t mine = 0;
+    for (int32_t b = b0; b < b1; ++b) mine += seq_units<L::TW>(p, b, blockIdx.x == 0);
+    int64_t incl = mine;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-    if (lane >= static_cast<uint32_t>(o)) incl += v;
-  }
-  if (lane == 31u) sh_scan[warp] = incl;
-  __syncthreads();
-  {
-    int64_t excl = incl - mine, total = 0;
-    const uint32_t nwarps = blockDim.x >> 5;
-    for (uint32_t w = 0; w < nwarps; ++w) {
-      if (w < warp) excl += sh_scan[w];
-      total += sh_scan[w];
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      if (lane >= static_cast<uint32_t>(o)) incl += v;
     }
-    sh_excl[threadIdx.x] = excl;
-    if (threadIdx.x == 0) sh_excl[blockDim.x] = total;
-    if (p.split && blockIdx.x == 0) {  // for the join
-      for (int32_t i = b0; i < b1; ++i) {
-        p.meta[i] = excl;
-        excl += seq_units<L::TW>(p, i, false);
+    if (lane == 31u) sh_scan[warp] = incl;
+    __syncthreads();
+    {
+      int64_t excl = incl - mine, total = 0;
+      const uint32_t nwarps = blockDim.x >> 5;
+      for (uint32_t w = 0; w < nwarps; ++w) {
+        if (w < warp) excl += sh_scan[w];
+        total += sh_scan[w];
+      }
+      sh_excl[threadIdx.x] = excl;
+      if (threadIdx.x == 0) sh_excl[blockDim.x] = total;
+      if (p.split && blockIdx.x == 0) {  // for the join
+        for (int32_t i = b0; i < b1; ++i) {
+          p.meta[i] = excl;
+          excl += seq_units<L::TW>(p, i, false);
+        }
       }
     }
-  }
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    if (p.split) {
-      cut_shares(sh_excl[blockDim.x], static_cast<int32_t>(gridDim.x), p.max_shares, p.min_steps, &sh_work);
-      if (blockIdx.x == 0) {
-        for (int i = 0; i < sh_work.levels; ++i) p.head->level[i] = sh_work.level[i];
-        p.head->levels = sh_work.levels;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      if (p.split) {
+        cut_shares(sh_excl[blockDim.x], static_cast<int32_t>(gridDim.x), p.max_shares, p.min_steps, &sh_work);
+        if (blockIdx.x == 0) {
+          for (int i = 0; i < sh_work.levels; ++i) p.head->level[i] = sh_work.level[i];
+          p.head->levels = sh_work.levels;
+        }
+      } else {
+        sh_work.level[0] = ShareLevel{0, 1, 0};
+        sh_work.levels = 1;
+        sh_work.shares = static_cast<int32_t>(sh_excl[blockDim.x]);
       }
-    } else {
-      sh_work.level[0] = ShareLevel{0, 1, 0};
-      sh_work.levels = 1;
-      sh_work.shares = static_cast<int32_t>(sh_excl[blockDim.x]);
     }
+    __syncthreads();
   }
-  __syncthreads();
 
   const int32_t hl = static_cast<int32_t>(warp) % p.hw, sub = static_cast<int32_t>(warp) / p.hw;
   const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * (NU * L::kUnit);
@@ -700,27 +704,34 @@ __global__ void __launch_bounds__(32 * kSplitWarps, (kSplitCtas<DP, NB>))
     return static_cast<uint32_t>(min(max(static_cast<int32_t>(row_bytes) - static_cast<int32_t>(g + 8 * i) * L::VC, 0), L::VC));
   };
 
-  for (int32_t share = static_cast<int32_t>(blockIdx.x); share < sh_work.shares;) {
-    int32_t level = sh_work.levels - 1;
-    while (level > 0 && sh_work.level[level].first > share) --level;
-    int64_t pos = sh_work.level[level].start + static_cast<int64_t>(share - sh_work.level[level].first) * sh_work.level[level].size;
-    const int64_t end = min(sh_excl[blockDim.x], pos + sh_work.level[level].size);
-    if (pos >= sh_excl[threadIdx.x] && pos < sh_excl[threadIdx.x + 1]) {
-      int64_t at = sh_excl[threadIdx.x];
-      int32_t i = static_cast<int32_t>(threadIdx.x) * per_thread;
-      for (; i < a.num_seqs; ++i) {
-        const int64_t n = seq_units<L::TW>(p, i, false);
-        if (pos < at + n) break;
-        at += n;
+  for (int32_t share = static_cast<int32_t>(blockIdx.x); direct || share < sh_work.shares;) {
+    int64_t pos = share, end = share + 1, base = 0;
+    int32_t b = 0;
+    if (direct) {
+      b = share / p.hgroups;
+      base = static_cast<int64_t>(b) * p.hgroups;
+    } else {
+      int32_t level = sh_work.levels - 1;
+      while (level > 0 && sh_work.level[level].first > share) --level;
+      pos = sh_work.level[level].start + static_cast<int64_t>(share - sh_work.level[level].first) * sh_work.level[level].size;
+      end = min(sh_excl[blockDim.x], pos + sh_work.level[level].size);
+      if (pos >= sh_excl[threadIdx.x] && pos < sh_excl[threadIdx.x + 1]) {
+        int64_t at = sh_excl[threadIdx.x];
+        int32_t i = static_cast<int32_t>(threadIdx.x) * per_thread;
+        for (; i < a.num_seqs; ++i) {
+          const int64_t n = seq_units<L::TW>(p, i, false);
+          if (pos < at + n) break;
+          at += n;
+        }
+        sh_first[0] = i;
+        sh_first[1] = at;
       }
-      sh_first[0] = i;
-      sh_first[1] = at;
+      __syncthreads();
+      b = static_cast<int32_t>(sh_first[0]);
+      base = sh_first[1];
     }
-    __syncthreads();
-    int32_t b = static_cast<int32_t>(sh_first[0]);
-    int64_t base = sh_first[1];
   while (pos < end && b < a.num_seqs) {
-    const AttendSeq seq = attend_seq(a, b, false);
+    const AttendSeq seq = attend_seq(a, b, direct && threadIdx.x == 0 && share == b * p.hgroups);
     const SplitGeom geom = split_geom<TW>(p, seq);
     const int32_t unit = p.split ? geom.steps : 1;
     const int64_t local = pos - base;
@@ -744,12 +755,6 @@ __global__ void __launch_bounds__(32 * kSplitWarps, (kSplitCtas<DP, NB>))
     const int32_t q_hi = static_cast<int32_t>(a.group.quot(static_cast<uint32_t>(row0 + nrows - 1)));
     const int32_t p_lo = p_first + q_lo, p_hi = p_first + q_hi;
     const TileList list = visible_tiles<TW>(a, p_lo, p_hi);
-
-    // -- queries: lane (g, t) holds the pairs of row g that K's pieces t, t + 4, .. meet -----
-    uint32_t qf[NB][QP];
-    float rs[NB][2];  // softmax scale of rows 2t, 2t + 1
-    load_queries<FMT, DP, NB>(a, seq, kvh, row0, nrows, kscale,
-                              [&](int i) { return (static_cast<int>(t) + 4 * ((2 * i) / L::KD)) * L::KD + (2 * i) % L::KD; }, qf, rs);
 
     float o[NB][OM][4], m[NB][2], l[NB][2];
 #pragma unroll
@@ -882,6 +887,12 @@ __global__ void __launch_bounds__(32 * kSplitWarps, (kSplitCtas<DP, NB>))
     };
 #pragma unroll
     for (int i = 0; i < NU - 1; ++i) copy_unit(i & 1);
+
+    // -- queries: lane (g, t) holds the pairs of row g that K's pieces t, t + 4, .. meet -----
+    uint32_t qf[NB][QP];
+    float rs[NB][2];  // softmax scale of rows 2t, 2t + 1
+    load_queries<FMT, DP, NB>(a, seq, kvh, row0, nrows, kscale,
+                              [&](int i) { return (static_cast<int>(t) + 4 * ((2 * i) / L::KD)) * L::KD + (2 * i) % L::KD; }, qf, rs);
 
     uint32_t slot = 0;
     auto next_slot = [&] { slot = slot + 1 == NU ? 0u : slot + 1; };
@@ -1238,6 +1249,8 @@ int64_t set_up_split(SplitParams& p, int heads, int rows, int tile, int64_t full
     p.part_ml = p.part_o + 2 * fit * p.hw * p.part_rows * DP;
     return fit < full ? fit : full;
   }
+  if (!a.q_start && static_cast<int32_t>(a.group.d) <= p.rows)  // one row a sequence: the kernel's direct items
+    return static_cast<int64_t>(a.num_seqs) * p.hgroups;
   // a CTA an item: at most this many
   const int64_t items = (static_cast<int64_t>(a.num_q) * a.group.d / p.rows + a.num_seqs) * p.hgroups;
   return items < 0x7FFFFFFF ? items : 0x7FFFFFFF;

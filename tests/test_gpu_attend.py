@@ -188,7 +188,7 @@ def test_workspace_sizes_and_repeats(batch, fmt):
     lens, nqs = BATCHES[batch]
     p = AttendProblem(lens, nqs, 8, 2, 128, fmt=fmt, seed=23)
     d = p.tensors(torch.device("cuda"))
-    for size in (256, 1 << 16, 1 << 20, kv.ATTEND_WORK_BYTES):
+    for size in (256, 1 << 16, 1 << 20, 6 << 20, kv.ATTEND_WORK_BYTES):
         work = torch.randint(0, 256, (size,), dtype=torch.uint8, device="cuda")
         work[:kv.ATTEND_HEAD_BYTES] = 0
         a = p.attend(d, work=work)
