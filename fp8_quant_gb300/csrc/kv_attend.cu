@@ -203,9 +203,11 @@ extern "C" kv_status kv_attend(const void* q, void* out, float* lse, const void*
       tp.qpt = kTileRows / static_cast<int32_t>(p.group.d);
       tp.blocks = p.num_q / (2 * tp.qpt) + num_seqs;
       if (format != KV_CACHE_SRC) return tile_quant(tp, format, stream);
-      // TMA: a tile is whole pages, or part of one
-      if (page_size >= 8 && (page_size <= kTileKeys ? kTileKeys % page_size == 0 : page_size % kTileKeys == 0)) {
-        const int box = page_size < kTileKeys ? static_cast<int>(page_size) : kTileKeys;
+      // TMA: a tile is whole pages or part of one; behind a window's lower edge, and with other pages, 16 keys are
+      auto divides = [&](int64_t keys) { return page_size <= keys ? keys % page_size == 0 : page_size % keys == 0; };
+      const int64_t granule = window == 0 && divides(kTileKeys) ? kTileKeys : 16;
+      if (page_size >= 8 && divides(granule)) {
+        const int box = static_cast<int>(page_size < granule ? page_size : granule);
         if (cache_map(&tp.k_map, k_cache, 2, p.bf16, head_dim, page_size, num_heads, num_pages, s->kc_slot, s->kc_head, s->kc_page, 64,
                       box, 1, true) &&
             cache_map(&tp.v_map, v_cache, 2, p.bf16, head_dim, page_size, num_heads, num_pages, s->vc_slot, s->vc_head, s->vc_page, 64,

@@ -50,7 +50,7 @@ struct TileParams {
   int32_t ks_page, ks_slot, vs_page, vs_slot;  // of the block scales
   int32_t qpt;     // queries of a tile: 128 / group
   int32_t blocks;  // query blocks of the launch (an upper bound)
-  int32_t box;     // keys of a TMA box (a page, or 128 of one); 0: no TMA
+  int32_t box;     // keys of a TMA box (a page, 128 of one, or 16); 0: no TMA
   CUtensorMap k_map, v_map;
 };
 
@@ -71,8 +71,9 @@ struct TileSmem {
   static_assert(kCopyThreads % kPieces == 0, "a lane keeps its piece of the rows");
   static constexpr int kPer = (kTileKeys + kStep - 1) / kStep;
   static constexpr int kOffRing = 2 * kQ;
-  static constexpr int kOffBars = kOffRing + kUnits * kUnit;
-  static constexpr int kBars = 2 * kUnits + 11;
+  static constexpr int kOffOut = kOffRing + kUnits * kUnit;  // 32 rows of 64 dims for each softmax warp
+  static constexpr int kOffBars = kOffOut + 8 * 4096;
+  static constexpr int kBars = 2 * kUnits + 15;
   static constexpr int kTotal = kOffBars + kBars * 8 + 1024;    // the base is aligned to 1,024
 };
 
@@ -130,6 +131,19 @@ __device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t (&r)[32]) 
                ::KV_S16(r, 0), KV_S16(r, 16), "r"(addr) : "memory");
 }
 
+__device__ __forceinline__ void tc_ld16(uint32_t (&r)[16], uint32_t addr) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+               "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+               "tcgen05.wait::ld.sync.aligned;"
+               : KV_R16(r, 0) : "r"(addr) : "memory");
+}
+
+__device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+               "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};"
+               ::KV_S16(r, 0), "r"(addr) : "memory");
+}
+
 #undef KV_R4
 #undef KV_R16
 #undef KV_S4
@@ -158,6 +172,12 @@ __device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t x, uint32_t 
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
+__device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
 // x * s + t and x + y for both lanes, in one instruction each.
 __device__ __forceinline__ float2 fma2(float2 x, float s, float t) {
   float2 r;
@@ -176,13 +196,37 @@ __device__ __forceinline__ float2 add2(float2 x, float2 y) {
   return r;
 }
 
+// The keys that a block of queries sees between them, in tiles of kTileKeys: the
+// first ones (sinks), filled up to a multiple of 16, and behind them the others
+// from a multiple of 16 on, so that a window's edges cost few keys beside it
+// (4 sinks and a window of 1,024 are 9 tiles for 64 queries, at tiles of whole
+// 128s 10.5 on average).  Place v of the list is key(v).
+struct TileKeys {
+  int32_t n;       // tiles
+  int32_t lo_key;  // first key of the windows
+  int32_t lead, shift;
+  __device__ __forceinline__ int32_t key(int32_t v) const { return v + (v >= lead ? shift : 0); }
+};
+
+__device__ __forceinline__ TileKeys tile_keys(const AttendParams& a, int32_t p_lo, int32_t p_hi) {
+  const KeyList k = visible_keys(a, p_lo, p_hi);
+  TileKeys r;
+  r.lo_key = k.lo;
+  const int32_t lo = k.lo & ~15;
+  r.lead = min((k.sinks + 15) & ~15, lo);
+  r.shift = lo - r.lead;
+  r.n = p_hi < 0 ? 0 : (p_hi + 1 - r.shift + kTileKeys - 1) / kTileKeys;
+  return r;
+}
+
 // One item: a block of up to 2 * qpt queries of a sequence, for one KV head.
 struct TileItem {
   int32_t b, kvh, tiles;
   AttendSeq seq;
   int32_t q_first, nq;   // the block's first query in its sequence, and their number
   int32_t p_first, p_hi; // positions of the first and the last
-  TileList list;
+  TileKeys list;
+  int32_t have;
 };
 
 // The CTA's item of a round, by a whole warp; false behind the last.  Blocks of
@@ -191,6 +235,7 @@ struct TileItem {
 __device__ __forceinline__ bool tile_item(const TileParams& p, int32_t round, TileItem* it) {
   const AttendParams& a = p.a;
   const uint32_t lane = threadIdx.x & 31u;
+  it->have = 0;
   const int64_t n = static_cast<int64_t>(round) * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
   if (n >= static_cast<int64_t>(p.blocks) * a.kv_heads) return false;
   const int32_t want = static_cast<int32_t>(n / a.kv_heads);
@@ -216,7 +261,8 @@ __device__ __forceinline__ bool tile_item(const TileParams& p, int32_t round, Ti
       it->tiles = it->nq > p.qpt ? 2 : 1;
       it->p_first = it->seq.len - it->seq.nq + it->q_first;
       it->p_hi = it->p_first + it->nq - 1;
-      it->list = visible_tiles<kTileKeys>(a, it->p_first, it->p_hi);
+      it->list = tile_keys(a, it->p_first, it->p_hi);
+      it->have = 1;
       return true;
     }
     before += __shfl_sync(0xFFFFFFFFu, incl, 31);
@@ -231,6 +277,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
   __shared__ uint32_t sh_tmem;
   __shared__ volatile int sh_failed;  // a wait ran out
   __shared__ volatile int sh_bad;     // a page id out of range was met: the CTA's rows are done again
+  __shared__ TileItem sh_item[2];     // the item of an odd and of an even round, for the softmax warps
 
   const AttendParams& a = p.a;
   const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31u;
@@ -238,7 +285,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
   const int32_t G = static_cast<int32_t>(a.group.d);
   const uint32_t ring = smem + S::kOffRing;
   const uint32_t full = smem + S::kOffBars, empty = full + 8 * S::kUnits;
-  const uint32_t q_full = empty + 8 * S::kUnits, s_full = q_full + 16, p_full = s_full + 16, o_full = p_full + 32, done = o_full + 16;
+  const uint32_t q_full = empty + 8 * S::kUnits, s_full = q_full + 16, p_full = s_full + 16, o_full = p_full + 32, item_full = o_full + 16,
+                 item_empty = item_full + 16, done = item_empty + 16;
   if (warp == 8) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
         static_cast<uint32_t>(__cvta_generic_to_shared(&sh_tmem))) : "memory");
@@ -255,6 +303,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
       bar_init(p_full + 16 * t, kTileRows);
       bar_init(p_full + 16 * t + 8, kTileRows);
       bar_init(o_full + 8 * t, 1);
+      bar_init(item_full + 8 * t, 1);
+      bar_init(item_empty + 8 * t, 8);
     }
     bar_init(done, 1);
     sh_failed = 0;
@@ -287,57 +337,81 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
     const uint32_t flip = full_scale < 0.0f ? 0x80008000u : 0u;  // the maximum is taken before the scale
     const uint32_t lanes = (warp & 3u) << 21;  // the warp's 32 lanes of TMEM
     const uint32_t s_at = tmem + lanes + t * 128, o_at = tmem + lanes + 256 + t * DP;
-    TileItem it;
-    bool ok = true, have = tile_item(p, 0, &it);
-    uint4 qw[DP / 8];
+    bool ok = true;
+    auto take_item = [&](int32_t round, TileItem* x) {
+      ok = __all_sync(0xFFFFFFFFu, bar_wait(item_full + 8 * (round & 1), static_cast<uint32_t>(round >> 1) & 1u, failed));
+      if (!ok) return;
+      *x = sh_item[round & 1];
+      __syncwarp();
+      if (lane == 0u) bar_arrive(item_empty + 8 * (round & 1));
+    };
     auto row_live = [&](const TileItem& x) { return t < x.tiles && qi < p.qpt && q_in < x.nq; };
+    // A warp's queries: kQL lanes a row, 16 bytes each, so that a load meets few lines of 128 bytes.
+    // Lane l's i-th piece is piece l % kQL of row row0 + i * (32 / kQL) + l / kQL.
+    constexpr int kQL = DP / 8, kQR = 32 / kQL;
+    const int32_t row0 = (static_cast<int32_t>(warp) & 3) * 32, q_row = static_cast<int32_t>(lane) / kQL, q_piece = static_cast<int32_t>(lane) % kQL;
+    uint4 qw[kQL];
     auto load_q = [&](const TileItem& x) {
-      const bool mine = row_live(x);
-      const uint8_t* src = a.q + static_cast<int64_t>(x.seq.q0 + x.q_first + q_in) * a.q_token +
-                           static_cast<int64_t>(x.kvh * G + gh) * a.q_head;
+      const uint8_t* src = a.q + static_cast<int64_t>(x.seq.q0 + x.q_first + t * p.qpt) * a.q_token +
+                           static_cast<int64_t>(x.kvh * G) * a.q_head + 16 * q_piece;
 #pragma unroll
-      for (int i = 0; i < DP / 8; ++i) {
+      for (int i = 0; i < kQL; ++i) {
+        const int32_t row = row0 + i * kQR + q_row, y = static_cast<int32_t>(a.group.quot(static_cast<uint32_t>(row)));
         qw[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (mine && 8 * i < a.head_dim) qw[i] = __ldg(reinterpret_cast<const uint4*>(src) + i);
+        if (t < x.tiles && y < p.qpt && t * p.qpt + y < x.nq && 8 * q_piece < a.head_dim)
+          qw[i] = __ldg(reinterpret_cast<const uint4*>(src + y * a.q_token + (row - y * G) * a.q_head));
       }
     };
-    if (have) load_q(it);
+    // Queries to shared memory; the products that read this tile's queries before have ended, as
+    // their scores were waited for.  Returns the row's factor of the scores.
+    auto put_q = [&](const TileItem& x) {
+      float scale = full_scale;
+      if constexpr (FMT != KV_CACHE_SRC) {
+        if (a.bf16) {  // into fp16's range: the row's largest element to 2^13 .. 2^14
+#pragma unroll
+          for (int i = 0; i < kQL; ++i) {
+            uint32_t y = absmax_pair<true>(absmax_pair<true>(absmax_pair<true>(absmax_pair<true>(0u, qw[i].x), qw[i].y), qw[i].z), qw[i].w);
+#pragma unroll
+            for (int o = 1; o < kQL; o <<= 1) y = absmax_pair<true>(y, __shfl_xor_sync(0xFFFFFFFFu, y, o));
+            const uint32_t e = __float_as_uint(absmax_pair_value<true>(y)) >> 23;
+            const float f = __uint_as_float(min(254u, 267u - e) << 23);
+            auto shift = [&](uint32_t z) {
+              const float2 v = widen2<true>(z);
+              return pack2(v.x * f, v.y * f, false);
+            };
+            qw[i] = make_uint4(shift(qw[i].x), shift(qw[i].y), shift(qw[i].z), shift(qw[i].w));
+            const float mine = __shfl_sync(0xFFFFFFFFu, f, (static_cast<int>(lane) % kQR) * kQL);
+            if (static_cast<int>(lane) / kQR == i) scale = full_scale * __fdiv_rn(1.0f, mine);
+          }
+        }
+      }
+      if (t < x.tiles && x.list.n > 0) {
+        const uint32_t dst = smem + t * S::kQ;
+#pragma unroll
+        for (int i = 0; i < kQL; ++i)
+          st_shared16(dst + swizzled(static_cast<uint32_t>(row0 + i * kQR + q_row), q_piece, kTileRows),
+                      qw[i].x ^ flip, qw[i].y ^ flip, qw[i].z ^ flip, qw[i].w ^ flip);
+        fence_async_shared();
+        bar_arrive(q_full + 8 * t);
+      }
+      scale = fabsf(scale);
+      return scale == 0.0f ? __uint_as_float(1u) : scale;  // hidden scores (-inf) must stay -inf
+    };
+    float scale = full_scale;
+    TileItem it;
+    it.have = 0;
+    take_item(0, &it);
+    if (ok && it.have) {
+      load_q(it);
+      scale = put_q(it);
+    }
     uint32_t waits = 0u, items = 0u;  // phases of s_full and p_full, and of q_full and o_full, that went by
-    for (int32_t round = 0; have && ok;) {
+    for (int32_t round = 0; ok && it.have;) {
       const bool mine = row_live(it);
       const int32_t pos = mine ? it.p_first + q_in : -1;
       const int32_t tok = it.seq.q0 + it.q_first + q_in, h = it.kvh * G + gh;
       const bool live = t < it.tiles && it.list.n > 0;
-      float scale = full_scale;
       float m = -INFINITY, l = 0.0f;   // m: of scaled scores, as last used
-      if (live) {
-        if constexpr (FMT != KV_CACHE_SRC) {
-          if (a.bf16) {  // into fp16's range: the row's largest element to 2^13 .. 2^14
-            uint32_t x = 0u;
-#pragma unroll
-            for (int i = 0; i < DP / 8; ++i)
-              x = absmax_pair<true>(absmax_pair<true>(absmax_pair<true>(absmax_pair<true>(x, qw[i].x), qw[i].y), qw[i].z), qw[i].w);
-            const uint32_t e = __float_as_uint(absmax_pair_value<true>(x)) >> 23;
-            const float f = __uint_as_float(min(254u, 267u - e) << 23);
-            scale *= __fdiv_rn(1.0f, f);
-            auto shift = [&](uint32_t y) {
-              const float2 v = widen2<true>(y);
-              return pack2(v.x * f, v.y * f, false);
-            };
-#pragma unroll
-            for (int i = 0; i < DP / 8; ++i) qw[i] = make_uint4(shift(qw[i].x), shift(qw[i].y), shift(qw[i].z), shift(qw[i].w));
-          }
-        }
-        // the products that read this tile's queries before have ended: their scores were waited for
-        const uint32_t dst = smem + t * S::kQ;
-#pragma unroll
-        for (int i = 0; i < DP / 8; ++i)
-          st_shared16(dst + swizzled(static_cast<uint32_t>(r), i, kTileRows), qw[i].x ^ flip, qw[i].y ^ flip, qw[i].z ^ flip, qw[i].w ^ flip);
-        scale = fabsf(scale);
-        if (scale == 0.0f) scale = __uint_as_float(1u);  // hidden scores (-inf) must stay -inf
-        fence_async_shared();
-        bar_arrive(q_full + 8 * t);
-      }
       // positions of the tile's rows
       const int32_t t_lo = it.p_first + t * p.qpt, t_hi = min(t_lo + p.qpt - 1, it.p_hi);
       for (int32_t j = 0; live && j < it.list.n; ++j) {
@@ -351,17 +425,20 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
 #pragma unroll
         for (int i = 0; i < kTileKeys; ++i) s[i] = __uint_as_float(sw[i]);
         // mask
-        const int32_t j0 = it.list.tile(j) * kTileKeys;
-        if (!(j0 + kTileKeys - 1 <= t_lo && (a.window == 0 || j0 > t_hi - a.window || j0 + kTileKeys - 1 < a.sinks))) {
+        const int32_t v0 = j * kTileKeys, v1 = v0 + kTileKeys - 1;
+        if (!(it.list.key(v1) <= t_lo && (a.window == 0 || v1 < a.sinks || (v0 >= it.list.lead && it.list.key(v0) > t_hi - a.window)))) {
           // keys up to pos, and of those the window's or the sinks'
           auto upto = [](int32_t n) {  // n low bits set
             return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u;
           };
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int32_t k0 = j0 + 32 * c;
+          auto seen = [&](int32_t k0) {  // of 16 keys from k0
             uint32_t see = upto(pos - k0 + 1);
             if (a.window > 0) see &= ~upto(pos - a.window - k0 + 1) | upto(a.sinks - k0);
+            return see & 0xFFFFu;
+          };
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t see = seen(it.list.key(v0 + 32 * c)) | seen(it.list.key(v0 + 32 * c + 16)) << 16;
 #pragma unroll
             for (int i = 0; i < 32; ++i)
               if ((see & (1u << i)) == 0u) s[32 * c + i] = -INFINITY;
@@ -384,13 +461,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
           m = mn;
           if (j > 0) {
             l *= f;
+#pragma unroll 1
+            for (int c = 0; c < DP / 16; ++c) {  // (few registers: the scores are in them too)
+              uint32_t w[16];
+              tc_ld16(w, o_at + 16 * c);
 #pragma unroll
-            for (int c = 0; c < DP / 32; ++c) {
-              uint32_t w[32];
-              tc_ld32(w, o_at + 32 * c);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * f);
-              tc_st32(o_at + 32 * c, w);
+              for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * f);
+              tc_st16(o_at + 16 * c, w);
             }
           }
         }
@@ -419,9 +496,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
         ++waits;
       }
       if (!ok) break;
-      // -- out, with the next item's queries on their way ---------------------------------------
+      // -- the next item's queries, so that its scores are there when this one's rows are written ---
       TileItem next;
-      have = tile_item(p, ++round, &next);
+      take_item(++round, &next);
+      if (!ok) break;
+      if (next.have) {
+        load_q(next);
+        scale = put_q(next);
+      }
       if (t < it.tiles) {
         bool fine = l > 0.0f;
         if (live) {
@@ -430,23 +512,38 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
           ++items;
           tc_fence_after();
           const float inv = __fdiv_rn(vscale, l);
-          uint8_t* out = a.out + static_cast<int64_t>(tok) * a.o_token + static_cast<int64_t>(h) * a.o_head;
+          // 64 dims at a time through shared memory, so that eight lanes write 128 bytes of a row
+          const uint32_t stage = smem + S::kOffOut + warp * 4096u;
+          uint8_t* const out = a.out + static_cast<int64_t>(it.seq.q0 + it.q_first + t * p.qpt) * a.o_token +
+                               static_cast<int64_t>(it.kvh * G) * a.o_head + 16 * (lane & 7u);
 #pragma unroll
-          for (int c = 0; c < DP / 32; ++c) {
-            uint32_t w[32];
-            tc_ld32(w, o_at + 32 * c);
+          for (int c = 0; c < DP / 64; ++c) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint32_t o[4];
+            for (int half = 0; half < 2; ++half) {
+              uint32_t w[32];
+              tc_ld32(w, o_at + 64 * c + 32 * half);
 #pragma unroll
-              for (int x = 0; x < 4; ++x) {
-                const float lo = __uint_as_float(w[8 * i + 2 * x]) * inv, hi = __uint_as_float(w[8 * i + 2 * x + 1]) * inv;
-                fine = fine && fabsf(lo) < INFINITY && fabsf(hi) < INFINITY;
-                o[x] = pack2(lo, hi, a.bf16);
+              for (int i = 0; i < 4; ++i) {
+                uint32_t o[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                  const float lo = __uint_as_float(w[8 * i + 2 * x]) * inv, hi = __uint_as_float(w[8 * i + 2 * x + 1]) * inv;
+                  fine = fine && fabsf(lo) < INFINITY && fabsf(hi) < INFINITY;
+                  o[x] = pack2(lo, hi, a.bf16);
+                }
+                st_shared16(stage + swizzled(lane, 4 * half + i, 32), o[0], o[1], o[2], o[3]);
               }
-              if (mine && 32 * c + 8 * i < a.head_dim)
-                *reinterpret_cast<uint4*>(out + 2 * (32 * c + 8 * i)) = make_uint4(o[0], o[1], o[2], o[3]);
             }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const uint32_t row = 4 * i + (lane >> 3);
+              const int32_t rr = row0 + static_cast<int32_t>(row), y = static_cast<int32_t>(a.group.quot(static_cast<uint32_t>(rr)));
+              const uint4 v = ld_shared16(stage + swizzled(row, lane & 7u, 32));
+              if (y < p.qpt && t * p.qpt + y < it.nq && static_cast<int32_t>(64 * c + 8 * (lane & 7u)) < a.head_dim)
+                *reinterpret_cast<uint4*>(out + y * a.o_token + (rr - y * G) * a.o_head + 128 * c) = v;
+            }
+            __syncwarp();
           }
           if (mine && a.lse)
             a.lse[static_cast<int64_t>(tok) * a.q_heads + h] = (m + log2f(l)) * 0.6931471805599453f;
@@ -460,7 +557,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
         }
       }
       it = next;
-      if (have) load_q(it);
     }
   } else if (warp == 8) {
     // ======================================================================================
@@ -476,10 +572,25 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
     const uint64_t q_desc = smem_desc(smem, 16), k_desc = smem_desc(ring, 16), v_desc = smem_desc(ring, kTileKeys * 128);
     uint32_t unit = 0u;                              // ring units that went by
     uint32_t items0 = 0u, items1 = 0u, done0 = 0u, done1 = 0u;  // of each tile: items and products P V
-    TileItem it;
-    for (int32_t round = 0; ok && tile_item(p, round, &it); ++round) {
+    // the items, a round ahead of their use, for this warp and the softmax warps
+    auto publish = [&](int32_t round, TileItem* x) {
+      tile_item(p, round, x);
+      if (round >= 2) wait(item_empty + 8 * (round & 1), static_cast<uint32_t>((round >> 1) - 1) & 1u);
+      if (!ok) return;
+      if (lane == 0u) {
+        sh_item[round & 1] = *x;
+        bar_arrive(item_full + 8 * (round & 1));
+      }
+      __syncwarp();
+    };
+    TileItem it, next;
+    publish(0, &it);
+    for (int32_t round = 0; ok && it.have; ++round, it = next) {
       const int32_t n = it.list.n, tiles = it.tiles;
-      if (n == 0) continue;
+      if (n == 0) {
+        publish(round + 1, &next);
+        continue;
+      }
       auto wait_unit = [&](uint32_t u) { wait(full + 8 * (u % S::kUnits), (u / S::kUnits) & 1u); };
       auto scores = [&](int32_t t, uint32_t u) {  // S_t = Q_t K^T, K in unit u
         if (!ok) return;
@@ -497,6 +608,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
         if (t == 0) wait_unit(unit);
         scores(t, unit);
       }
+      if (ok) publish(round + 1, &next);
       for (int32_t j = 0; j < n && ok; ++j) {
         const uint32_t u = unit + 2 * j;
         for (int32_t t = 0; t < tiles; ++t) {
@@ -554,7 +666,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
 #pragma unroll
       for (int i = 0; i < S::kPer; ++i) {
         const uint32_t key = key0 + i * S::kStep;
-        const int32_t k = it.list.tile(j) * kTileKeys + static_cast<int32_t>(key);
+        const int32_t k = it.list.key(j * kTileKeys + static_cast<int32_t>(key));
         const bool w = (kTileKeys % S::kStep == 0 || key < kTileKeys) && k <= it.p_hi && (k >= it.list.lo_key || k < a.sinks);
         want |= (w ? 1u : 0u) << i;
         id[i] = __ldg(table + a.page.quot(static_cast<uint32_t>(min(k, it.p_hi))));
@@ -575,7 +687,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
       return want & ~bad;
     };
     auto offset_of = [&](const TileItem& it, int32_t j, int i) -> int32_t {  // in its page
-      const uint32_t k = static_cast<uint32_t>(it.list.tile(j) * kTileKeys) + key0 + i * S::kStep;
+      const uint32_t k = static_cast<uint32_t>(it.list.key(j * kTileKeys + static_cast<int32_t>(key0) + i * S::kStep));
       return static_cast<int32_t>(k - a.page.quot(k) * a.page.d);
     };
     TileItem it;
@@ -588,15 +700,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
         const uint8_t* const vbase = a.v + it.kvh * a.v_head;
         auto first_page = [&](int32_t j) -> int32_t {
           if (j >= it.list.n || static_cast<int32_t>(lane) >= boxes) return 0;
-          const int32_t k = it.list.tile(j) * kTileKeys + static_cast<int32_t>(lane) * p.box;
+          const int32_t k = it.list.key(j * kTileKeys + static_cast<int32_t>(lane) * p.box);
           return k < it.seq.len ? __ldg(table + a.page.quot(static_cast<uint32_t>(k))) : -1;
         };
         int32_t next = first_page(0);
         for (int32_t j = 0; j < it.list.n && ok; ++j, unit += 2) {
-          const int32_t j0 = it.list.tile(j) * kTileKeys;
           const int32_t mine = next;
           next = first_page(j + 1);
-          const bool whole = boxes > 0 && j0 + kTileKeys <= it.seq.len &&
+          const bool whole = boxes > 0 && it.list.key(j * kTileKeys + kTileKeys - 1) < it.seq.len &&
                              __all_sync(0xFFFFFFFFu, mine >= 0 && mine < a.num_pages);
           if (whole) {
 #pragma unroll
@@ -607,7 +718,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
               if (c == 0) bar_arrive_expect(bar, S::kUnit); else bar_arrive(bar);
               __syncwarp();
               if (warp == 9 && static_cast<int32_t>(lane) < boxes) {
-                const uint32_t k = static_cast<uint32_t>(j0) + lane * static_cast<uint32_t>(p.box);
+                const uint32_t k = static_cast<uint32_t>(it.list.key(j * kTileKeys + static_cast<int32_t>(lane) * p.box));
                 const int32_t key = static_cast<int32_t>(k - a.page.quot(k) * a.page.d);
 #pragma unroll
                 for (int x = 0; x < DP / 64; ++x)
