@@ -199,6 +199,9 @@ extern "C" kv_status kv_attend(const void* q, void* out, float* lse, const void*
       if (format == KV_CACHE_E2M1) {
         tp.ks_page = static_cast<int32_t>(scales->k_page); tp.ks_slot = static_cast<int32_t>(scales->k_slot);
         tp.vs_page = static_cast<int32_t>(scales->v_page); tp.vs_slot = static_cast<int32_t>(scales->v_slot);
+        const uint64_t bits = u64(scales->k) | u64(scales->v) | u64(scales->k_page) | u64(scales->v_page) | u64(scales->k_slot) |
+                              u64(scales->v_slot) | u64(scales->k_head) | u64(scales->v_head);
+        tp.scale_word = (bits & 7u) == 0 && head_dim == 128 ? 8 : (bits & 3u) == 0 && head_dim % 64 == 0 ? 4 : 1;
       }
       tp.qpt = kTileRows / static_cast<int32_t>(p.group.d);
       tp.blocks = p.num_q / (2 * tp.qpt) + num_seqs;

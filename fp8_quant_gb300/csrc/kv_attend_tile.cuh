@@ -20,9 +20,9 @@
 //                   tiles whose keys all exist go by TMA, a box for each page
 //                   and 64 dims, where pages divide or are divided by 128 keys;
 //                   others by cp.async, 16 bytes a lane, with zeros for keys that
-//                   no row needs.  Quantised rows go through registers, two units
-//                   ahead, and become fp16 on the way (exact; see
-//                   kv_attend_split.cuh).
+//                   no row needs.  Quantised rows are copied as they are by
+//                   warp 15 (cp.async, a tile ahead) and become fp16 on their
+//                   way into the ring (exact; see kv_attend_split.cuh) by 9-14.
 //
 // Registers: 512 threads are launched with 128 each; the softmax warps take 184
 // (a row's 128 scores stay in registers), the others leave 72.
@@ -48,6 +48,7 @@ struct TileParams {
   AttendParams a;
   int32_t k_page, k_slot, v_page, v_slot;      // byte strides, in 32 bits
   int32_t ks_page, ks_slot, vs_page, vs_slot;  // of the block scales
+  int32_t scale_word;  // bytes of them that may be copied at once: 8, 4 or 1
   int32_t qpt;     // queries of a tile: 128 / group
   int32_t blocks;  // query blocks of the launch (an upper bound)
   int32_t box;     // keys of a TMA box (a page, 128 of one, or 16); 0: no TMA
@@ -62,18 +63,25 @@ static_assert(256 * kSoftmaxRegs + 256 * kOtherRegs <= 65536, "the registers of 
 
 template <int FMT, int DP>
 struct TileSmem {
-  static constexpr int kUnits = 4;  // ring units: a K or a V tile in 16 bits
+  // Ring units, a K or a V tile in 16 bits: quantised caches take three, as a tile of their K and one
+  // of their V wait in front of the ring.
+  static constexpr int kUnits = FMT == KV_CACHE_SRC ? 4 : 3;
   static constexpr int kUnit = kTileKeys * DP * 2;
   static constexpr int kQ = kTileRows * DP * 2;
   // a lane's pieces of a unit: 8 dims (16-bit) or 16 (quantised) of every kStep-th key
+  static constexpr int kFillers = FMT == KV_CACHE_SRC ? kCopyThreads : kCopyThreads - 32;
   static constexpr int kPieces = FMT == KV_CACHE_SRC ? DP / 8 : DP / 16;
-  static constexpr int kStep = kCopyThreads / kPieces;
-  static_assert(kCopyThreads % kPieces == 0, "a lane keeps its piece of the rows");
+  static constexpr int kStep = kFillers / kPieces;
+  static_assert(kFillers % kPieces == 0, "a lane keeps its piece of the rows");
+  static constexpr int kRaw = FMT == KV_CACHE_SRC ? 0 : FMT == KV_CACHE_E4M3FN ? DP : DP / 2;  // bytes of a quantised row
+  static constexpr int kRawScales = FMT == KV_CACHE_E2M1 ? 8 : 0;
   static constexpr int kPer = (kTileKeys + kStep - 1) / kStep;
   static constexpr int kOffRing = 2 * kQ;
   static constexpr int kOffOut = kOffRing + kUnits * kUnit;  // 32 rows of 64 dims for each softmax warp
-  static constexpr int kOffBars = kOffOut + 8 * 4096;
-  static constexpr int kBars = 2 * kUnits + 15;
+  static constexpr int kOffRaw = kOffOut + 8 * 4096;         // a K and a V tile as they lie in the cache
+  static constexpr int kRawTile = kTileKeys * (kRaw + kRawScales);
+  static constexpr int kOffBars = kOffRaw + 2 * kRawTile;
+  static constexpr int kBars = 2 * kUnits + 19;
   static constexpr int kTotal = kOffBars + kBars * 8 + 1024;    // the base is aligned to 1,024
 };
 
@@ -286,7 +294,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
   const uint32_t ring = smem + S::kOffRing;
   const uint32_t full = smem + S::kOffBars, empty = full + 8 * S::kUnits;
   const uint32_t q_full = empty + 8 * S::kUnits, s_full = q_full + 16, p_full = s_full + 16, o_full = p_full + 32, item_full = o_full + 16,
-                 item_empty = item_full + 16, done = item_empty + 16;
+                 item_empty = item_full + 16, raw_full = item_empty + 16, raw_empty = raw_full + 16, done = raw_empty + 16;
   if (warp == 8) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
         static_cast<uint32_t>(__cvta_generic_to_shared(&sh_tmem))) : "memory");
@@ -294,7 +302,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
   }
   if (tid == 0) {
     for (int i = 0; i < S::kUnits; ++i) {
-      bar_init(full + 8 * i, kCopyThreads);
+      bar_init(full + 8 * i, S::kFillers);
       bar_init(empty + 8 * i, 1);
     }
     for (int t = 0; t < 2; ++t) {
@@ -305,6 +313,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
       bar_init(o_full + 8 * t, 1);
       bar_init(item_full + 8 * t, 1);
       bar_init(item_empty + 8 * t, 8);
+      bar_init(raw_full + 8 * t, 32);
+      bar_init(raw_empty + 8 * t, S::kFillers / 32);
     }
     bar_init(done, 1);
     sh_failed = 0;
@@ -761,107 +771,162 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
       }
       if (!ok)  // boxes in flight write shared memory: let them land before the CTA leaves it
         for (int i = 0; i < 1000; ++i) __nanosleep(1000);
-    } else {
-      // the raw pieces of a unit in registers: codes (and, e2m1, their block's scale)
-      constexpr int kWords = FMT == KV_CACHE_E4M3FN ? 4 : 2;
-      struct Raw {
-        uint32_t w[S::kPer][kWords];
-        uint32_t sc[FMT == KV_CACHE_E2M1 ? S::kPer : 1];
-        uint32_t want;  // bits of the pieces that count: the others become 0
-      };
-      auto load = [&](const TileItem& it, int32_t j, int kv, uint32_t want, const int32_t (&id)[S::kPer], Raw& r) {
-        const uint8_t* base = kv ? a.v + it.kvh * a.v_head : a.k + it.kvh * a.k_head;
-        const uint8_t* sb = kv ? a.v_sc + it.kvh * a.vs_head : a.k_sc + it.kvh * a.ks_head;
-        if (piece * (4 * kWords) >= row_bytes) want = 0u;
-        r.want = want;
-        const uint32_t mine = want != 0u ? piece : 0u;
-#pragma unroll
-        for (int i = 0; i < S::kPer; ++i) {
-          const bool w = (want >> i & 1u) != 0u;  // else the first row of the cache, to be dropped
-          const int32_t pg = w ? id[i] : 0, of = w ? offset_of(it, j, i) : 0;
-          const uint8_t* src = base + wide(pg, kv ? p.v_page : p.k_page) + wide(of, kv ? p.v_slot : p.k_slot) + mine * (4 * kWords);
-          if constexpr (FMT == KV_CACHE_E4M3FN) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4*>(src));
-            r.w[i][0] = v.x; r.w[i][1] = v.y; r.w[i][2] = v.z; r.w[i][3] = v.w;
-          } else {
-            const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
-            r.w[i][0] = v.x; r.w[i][1] = v.y;
-            r.sc[i] = __ldg(sb + wide(pg, kv ? p.vs_page : p.ks_page) + wide(of, kv ? p.vs_slot : p.ks_slot) + mine);
-          }
-        }
-      };
-      auto store = [&](uint32_t u, const Raw& r) {
-        const uint32_t at = ring + (u % S::kUnits) * S::kUnit;
-#pragma unroll
-        for (int i = 0; i < S::kPer; ++i) {
-          const uint32_t key = key0 + i * S::kStep;
-          if (kTileKeys % S::kStep != 0 && key >= kTileKeys) break;
-          const bool w = (r.want >> i & 1u) != 0u;
-          uint32_t f[8];
-          if constexpr (FMT == KV_CACHE_E4M3FN) {
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const uint32_t v = w ? r.w[i][x] : 0u;
-              f[2 * x] = f16x2_from_e4m3x2(v);
-              f[2 * x + 1] = f16x2_from_e4m3x2(v >> 16);
-            }
-          } else {
-            const uint32_t s2 = f16x2_from_e4m3x2(w ? r.sc[i] * 0x0101u : 0u);  // e2m1 codes are finite
-            f16x2_from_e2m1x8(r.w[i][0], f);
-            f16x2_from_e2m1x8(r.w[i][1], f + 4);
-#pragma unroll
-            for (int x = 0; x < 8; ++x) f[x] = mul_f16x2(f[x], s2);
-          }
-          st_shared16(at + swizzled(key, 2 * piece, kTileKeys), f[0], f[1], f[2], f[3]);
-          st_shared16(at + swizzled(key, 2 * piece + 1, kTileKeys), f[4], f[5], f[6], f[7]);
-        }
-        fence_async_shared();
-        bar_arrive(full + 8 * (u % S::kUnits));
-      };
-      // two cursors: pages are looked up a tile before codes are loaded, codes a tile before they are stored
-      Raw kr, vr;
-      int32_t id[S::kPer];
-      TileItem nx;
-      int32_t nx_round = 0, nx_j = 0;
-      bool nx_have = tile_item(p, 0, &nx);
+    } else if (warp == 15) {
+      // ====================================================================================
+      // quantised rows as they lie into shared memory: lane l looks up keys l, l + 32, ..
+      // ====================================================================================
+      constexpr int kKeys = kTileKeys / 32, kChunks = S::kRaw / 16, kRows = 32 / kChunks;
+      int32_t round = 0, j = 0;
+      bool have = tile_item(p, 0, &it);
       auto skip_empty = [&] {
-        while (nx_have && nx_j >= nx.list.n) {
-          nx_j = 0;
-          nx_have = tile_item(p, ++nx_round, &nx);
+        while (have && j >= it.list.n) {
+          j = 0;
+          have = tile_item(p, ++round, &it);
         }
       };
-      uint32_t want = 0u;
-      auto look = [&] { want = nx_have ? pages_of(nx, nx_j, id) : 0u; };
+      int32_t id[kKeys];
+      auto look = [&] {  // the pages of the cursor's tile; not looked at before a tile later
+        const int32_t* table = a.table + static_cast<int64_t>(it.b) * a.table_stride;
+#pragma unroll
+        for (int i = 0; i < kKeys; ++i)
+          id[i] = __ldg(table + a.page.quot(static_cast<uint32_t>(min(it.list.key(j * kTileKeys + 32 * i + static_cast<int32_t>(lane)), it.p_hi))));
+      };
       skip_empty();
-      look();
-      want = checked(nx, want, id);
-      bool more = nx_have;
-      if (more) {
-        load(nx, nx_j, 0, want, id, kr);
-        load(nx, nx_j, 1, want, id, vr);
-        ++nx_j;
+      if (have) look();
+      for (uint32_t tile = 0u; have; ++tile) {
+        // page and slot of the lane's keys; page -1: a key that no row needs
+        int32_t pg[kKeys], of[kKeys];
+        uint32_t bad = 0u;
+#pragma unroll
+        for (int i = 0; i < kKeys; ++i) {
+          const int32_t k = it.list.key(j * kTileKeys + 32 * i + static_cast<int32_t>(lane));
+          const bool want = k <= it.p_hi && (k >= it.list.lo_key || k < a.sinks);
+          const bool page = static_cast<uint32_t>(id[i]) < static_cast<uint32_t>(a.num_pages);
+          if (want && !page) bad = 1u;
+          pg[i] = want && page ? id[i] : -1;
+          of[i] = k - static_cast<int32_t>(a.page.quot(static_cast<uint32_t>(k)) * a.page.d);
+        }
+        if (bad != 0u) {
+          sh_bad = 1;
+          record_oob(a.err, static_cast<uint64_t>(it.b));
+        }
+        __syncwarp();
+        const int32_t kvh = it.kvh;
+        ++j;
         skip_empty();
-        look();
+        if (have) look();
+#pragma unroll 1
+        for (int kv = 0; kv < 2; ++kv) {
+          if (tile > 0u) ok = __all_sync(0xFFFFFFFFu, bar_wait(raw_empty + 8 * kv, (tile - 1u) & 1u, failed));
+          if (!ok) break;
+          const uint32_t at = smem + S::kOffRaw + static_cast<uint32_t>(kv) * S::kRawTile;
+          const uint8_t* const base = kv ? a.v + kvh * a.v_head : a.k + kvh * a.k_head;
+          const int32_t page = kv ? p.v_page : p.k_page, slot = kv ? p.v_slot : p.k_slot;
+          // kChunks lanes a row, so that a copy meets few lines
+          const uint32_t chunk = lane % kChunks;
+          const int32_t bytes = min(max(static_cast<int32_t>(row_bytes) - 16 * static_cast<int32_t>(chunk), 0), 16);
+#pragma unroll
+          for (int i = 0; i < kKeys; ++i) {
+            const int64_t off = pg[i] < 0 ? -1 : wide(pg[i], page) + wide(of[i], slot);
+#pragma unroll
+            for (int y = 0; y < 32 / kRows; ++y) {
+              const int64_t o = __shfl_sync(0xFFFFFFFFu, off, y * kRows + lane / kChunks);
+              const uint32_t key = 32 * i + y * kRows + lane / kChunks;
+              const bool w = o != -1 && bytes > 0;
+              copy_async<16>(at + key * S::kRaw + chunk * 16, base + (w ? o + 16 * chunk : 0), w ? static_cast<uint32_t>(bytes) : 0u);
+            }
+          }
+          bool plain = false;
+          if constexpr (FMT == KV_CACHE_E2M1) {
+            const uint8_t* const sb = kv ? a.v_sc + kvh * a.vs_head : a.k_sc + kvh * a.ks_head;
+            const int32_t sp = kv ? p.vs_page : p.ks_page, ss = kv ? p.vs_slot : p.ks_slot;
+            const int32_t ds = a.head_dim / 16;
+            plain = p.scale_word == 1;
+#pragma unroll
+            for (int i = 0; i < kKeys; ++i) {
+              const bool w = pg[i] >= 0;
+              const uint8_t* src = sb + (w ? wide(pg[i], sp) + wide(of[i], ss) : 0);
+              const uint32_t dst = at + kTileKeys * S::kRaw + (32 * i + lane) * 8;
+              if (p.scale_word == 8) {
+                copy_async<8>(dst, src, w ? 8u : 0u);
+              } else if (p.scale_word == 4) {
+                copy_async<4>(dst, src, w ? 4u : 0u);
+                copy_async<4>(dst + 4, w && ds > 4 ? src + 4 : src, w && ds > 4 ? static_cast<uint32_t>(min(ds - 4, 4)) : 0u);
+              } else {
+                uint32_t lo = 0u, hi = 0u;
+                for (int32_t x = 0; x < ds && w; ++x) {
+                  const uint32_t v = __ldg(src + x);
+                  if (x < 4) lo |= v << (8 * x); else hi |= v << (8 * x - 32);
+                }
+                asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(dst), "r"(lo), "r"(hi) : "memory");
+              }
+            }
+          }
+          if (plain) {
+            wait_all_async();
+            bar_arrive(raw_full + 8 * kv);
+          } else {
+            bar_arrive_copies(raw_full + 8 * kv);
+          }
+        }
+        if (!ok) break;
       }
-      while (more && ok) {
-        more = nx_have;
-        wait_empty(unit);
-        if (!ok) break;
-        store(unit, kr);
-        if (more) {
-          want = checked(nx, want, id);
-          load(nx, nx_j, 0, want, id, kr);
+      wait_all_async();  // copies in flight write shared memory
+    } else {
+      // ====================================================================================
+      // and from there, as fp16, into the ring
+      // ====================================================================================
+      constexpr int kWords = FMT == KV_CACHE_E4M3FN ? 4 : 2;
+      uint32_t tile = 0u;
+      for (int32_t round = 0; ok && tile_item(p, round, &it); ++round) {
+        for (int32_t j = 0; j < it.list.n && ok; ++j, ++tile) {
+#pragma unroll 1
+          for (int kv = 0; kv < 2 && ok; ++kv, ++unit) {
+            const uint32_t from = smem + S::kOffRaw + static_cast<uint32_t>(kv) * S::kRawTile;
+            uint32_t w[S::kPer][kWords], sc[FMT == KV_CACHE_E2M1 ? S::kPer : 1];
+            ok = __all_sync(0xFFFFFFFFu, bar_wait(raw_full + 8 * kv, tile & 1u, failed));
+            if (!ok) break;
+#pragma unroll
+            for (int i = 0; i < S::kPer; ++i) {
+              const uint32_t key = min(key0 + i * S::kStep, static_cast<uint32_t>(kTileKeys - 1));
+              if constexpr (FMT == KV_CACHE_E4M3FN) {
+                const uint4 v = ld_shared16(from + key * S::kRaw + piece * 16);
+                w[i][0] = v.x; w[i][1] = v.y; w[i][2] = v.z; w[i][3] = v.w;
+              } else {
+                asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[i][0]), "=r"(w[i][1]) : "r"(from + key * S::kRaw + piece * 8) : "memory");
+                asm volatile("ld.shared.u8 %0, [%1];" : "=r"(sc[i]) : "r"(from + kTileKeys * S::kRaw + key * 8 + piece) : "memory");
+              }
+            }
+            __syncwarp();
+            if (lane == 0u) bar_arrive(raw_empty + 8 * kv);
+            wait_empty(unit);
+            if (!ok) break;
+            const uint32_t at = ring + (unit % S::kUnits) * S::kUnit;
+#pragma unroll
+            for (int i = 0; i < S::kPer; ++i) {
+              const uint32_t key = key0 + i * S::kStep;
+              if (kTileKeys % S::kStep != 0 && key >= kTileKeys) break;
+              uint32_t f[8];
+              if constexpr (FMT == KV_CACHE_E4M3FN) {
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                  f[2 * x] = f16x2_from_e4m3x2(w[i][x]);
+                  f[2 * x + 1] = f16x2_from_e4m3x2(w[i][x] >> 16);
+                }
+              } else {
+                const uint32_t s2 = f16x2_from_e4m3x2(sc[i] * 0x0101u);  // e2m1 codes are finite
+                f16x2_from_e2m1x8(w[i][0], f);
+                f16x2_from_e2m1x8(w[i][1], f + 4);
+#pragma unroll
+                for (int x = 0; x < 8; ++x) f[x] = mul_f16x2(f[x], s2);
+              }
+              st_shared16(at + swizzled(key, 2 * piece, kTileKeys), f[0], f[1], f[2], f[3]);
+              st_shared16(at + swizzled(key, 2 * piece + 1, kTileKeys), f[4], f[5], f[6], f[7]);
+            }
+            fence_async_shared();
+            bar_arrive(full + 8 * (unit % S::kUnits));
+          }
         }
-        wait_empty(unit + 1);
-        if (!ok) break;
-        store(unit + 1, vr);
-        if (more) {
-          load(nx, nx_j, 1, want, id, vr);
-          ++nx_j;
-          skip_empty();
-          look();
-        }
-        unit += 2;
       }
     }
   }
