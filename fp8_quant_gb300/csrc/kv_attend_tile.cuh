@@ -21,8 +21,9 @@
 //                   and 64 dims, where pages divide or are divided by 128 keys;
 //                   others by cp.async, 16 bytes a lane, with zeros for keys that
 //                   no row needs.  Quantised rows are copied as they are by
-//                   warp 15 (cp.async, a tile ahead) and become fp16 on their
-//                   way into the ring (exact; see kv_attend_split.cuh) by 9-14.
+//                   warps 14 (V) and 15 (K) with cp.async, a tile ahead, and
+//                   become fp16 on their way into the ring (exact; see
+//                   kv_attend_split.cuh) by 9-13.
 //
 // Registers: 512 threads are launched with 128 each; the softmax warps take 184
 // (a row's 128 scores stay in registers), the others leave 72.
@@ -69,7 +70,7 @@ struct TileSmem {
   static constexpr int kUnit = kTileKeys * DP * 2;
   static constexpr int kQ = kTileRows * DP * 2;
   // a lane's pieces of a unit: 8 dims (16-bit) or 16 (quantised) of every kStep-th key
-  static constexpr int kFillers = FMT == KV_CACHE_SRC ? kCopyThreads : kCopyThreads - 32;
+  static constexpr int kFillers = FMT == KV_CACHE_SRC ? kCopyThreads : kCopyThreads - 64;
   static constexpr int kPieces = FMT == KV_CACHE_SRC ? DP / 8 : DP / 16;
   static constexpr int kStep = kFillers / kPieces;
   static_assert(kFillers % kPieces == 0, "a lane keeps its piece of the rows");
@@ -771,10 +772,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
       }
       if (!ok)  // boxes in flight write shared memory: let them land before the CTA leaves it
         for (int i = 0; i < 1000; ++i) __nanosleep(1000);
-    } else if (warp == 15) {
+    } else if (warp >= 14) {
       // ====================================================================================
       // quantised rows as they lie into shared memory: lane l looks up keys l, l + 32, ..
       // ====================================================================================
+      const int32_t kv = warp == 15 ? 0 : 1;
+      const uint32_t at = smem + S::kOffRaw + static_cast<uint32_t>(kv) * S::kRawTile;
+      const int32_t page_stride = kv ? p.v_page : p.k_page, slot_stride = kv ? p.v_slot : p.k_slot;
       constexpr int kKeys = kTileKeys / 32, kChunks = S::kRaw / 16, kRows = 32 / kChunks;
       int32_t round = 0, j = 0;
       bool have = tile_item(p, 0, &it);
@@ -808,68 +812,62 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
         }
         if (bad != 0u) {
           sh_bad = 1;
-          record_oob(a.err, static_cast<uint64_t>(it.b));
+          if (kv == 0) record_oob(a.err, static_cast<uint64_t>(it.b));
         }
         __syncwarp();
         const int32_t kvh = it.kvh;
         ++j;
         skip_empty();
         if (have) look();
-#pragma unroll 1
-        for (int kv = 0; kv < 2; ++kv) {
-          if (tile > 0u) ok = __all_sync(0xFFFFFFFFu, bar_wait(raw_empty + 8 * kv, (tile - 1u) & 1u, failed));
-          if (!ok) break;
-          const uint32_t at = smem + S::kOffRaw + static_cast<uint32_t>(kv) * S::kRawTile;
-          const uint8_t* const base = kv ? a.v + kvh * a.v_head : a.k + kvh * a.k_head;
-          const int32_t page = kv ? p.v_page : p.k_page, slot = kv ? p.v_slot : p.k_slot;
-          // kChunks lanes a row, so that a copy meets few lines
-          const uint32_t chunk = lane % kChunks;
-          const int32_t bytes = min(max(static_cast<int32_t>(row_bytes) - 16 * static_cast<int32_t>(chunk), 0), 16);
+        if (tile > 0u) ok = __all_sync(0xFFFFFFFFu, bar_wait(raw_empty + 8 * kv, (tile - 1u) & 1u, failed));
+        if (!ok) break;
+        const uint8_t* const base = kv ? a.v + kvh * a.v_head : a.k + kvh * a.k_head;
+        // kChunks lanes a row, so that a copy meets few lines
+        const uint32_t chunk = lane % kChunks;
+        const int32_t bytes = min(max(static_cast<int32_t>(row_bytes) - 16 * static_cast<int32_t>(chunk), 0), 16);
 #pragma unroll
-          for (int i = 0; i < kKeys; ++i) {
-            const int64_t off = pg[i] < 0 ? -1 : wide(pg[i], page) + wide(of[i], slot);
+        for (int i = 0; i < kKeys; ++i) {
+          const int64_t off = pg[i] < 0 ? -1 : wide(pg[i], page_stride) + wide(of[i], slot_stride);
 #pragma unroll
-            for (int y = 0; y < 32 / kRows; ++y) {
-              const int64_t o = __shfl_sync(0xFFFFFFFFu, off, y * kRows + lane / kChunks);
-              const uint32_t key = 32 * i + y * kRows + lane / kChunks;
-              const bool w = o != -1 && bytes > 0;
-              copy_async<16>(at + key * S::kRaw + chunk * 16, base + (w ? o + 16 * chunk : 0), w ? static_cast<uint32_t>(bytes) : 0u);
-            }
-          }
-          bool plain = false;
-          if constexpr (FMT == KV_CACHE_E2M1) {
-            const uint8_t* const sb = kv ? a.v_sc + kvh * a.vs_head : a.k_sc + kvh * a.ks_head;
-            const int32_t sp = kv ? p.vs_page : p.ks_page, ss = kv ? p.vs_slot : p.ks_slot;
-            const int32_t ds = a.head_dim / 16;
-            plain = p.scale_word == 1;
-#pragma unroll
-            for (int i = 0; i < kKeys; ++i) {
-              const bool w = pg[i] >= 0;
-              const uint8_t* src = sb + (w ? wide(pg[i], sp) + wide(of[i], ss) : 0);
-              const uint32_t dst = at + kTileKeys * S::kRaw + (32 * i + lane) * 8;
-              if (p.scale_word == 8) {
-                copy_async<8>(dst, src, w ? 8u : 0u);
-              } else if (p.scale_word == 4) {
-                copy_async<4>(dst, src, w ? 4u : 0u);
-                copy_async<4>(dst + 4, w && ds > 4 ? src + 4 : src, w && ds > 4 ? static_cast<uint32_t>(min(ds - 4, 4)) : 0u);
-              } else {
-                uint32_t lo = 0u, hi = 0u;
-                for (int32_t x = 0; x < ds && w; ++x) {
-                  const uint32_t v = __ldg(src + x);
-                  if (x < 4) lo |= v << (8 * x); else hi |= v << (8 * x - 32);
-                }
-                asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(dst), "r"(lo), "r"(hi) : "memory");
-              }
-            }
-          }
-          if (plain) {
-            wait_all_async();
-            bar_arrive(raw_full + 8 * kv);
-          } else {
-            bar_arrive_copies(raw_full + 8 * kv);
+          for (int y = 0; y < 32 / kRows; ++y) {
+            const int64_t o = __shfl_sync(0xFFFFFFFFu, off, y * kRows + lane / kChunks);
+            const uint32_t key = 32 * i + y * kRows + lane / kChunks;
+            const bool w = o != -1 && bytes > 0;
+            copy_async<16>(at + key * S::kRaw + chunk * 16, base + (w ? o + 16 * chunk : 0), w ? static_cast<uint32_t>(bytes) : 0u);
           }
         }
-        if (!ok) break;
+        bool plain = false;
+        if constexpr (FMT == KV_CACHE_E2M1) {
+          const uint8_t* const sb = kv ? a.v_sc + kvh * a.vs_head : a.k_sc + kvh * a.ks_head;
+          const int32_t sp = kv ? p.vs_page : p.ks_page, ss = kv ? p.vs_slot : p.ks_slot;
+          const int32_t ds = a.head_dim / 16;
+          plain = p.scale_word == 1;
+#pragma unroll
+          for (int i = 0; i < kKeys; ++i) {
+            const bool w = pg[i] >= 0;
+            const uint8_t* src = sb + (w ? wide(pg[i], sp) + wide(of[i], ss) : 0);
+            const uint32_t dst = at + kTileKeys * S::kRaw + (32 * i + lane) * 8;
+            if (p.scale_word == 8) {
+              copy_async<8>(dst, src, w ? 8u : 0u);
+            } else if (p.scale_word == 4) {
+              copy_async<4>(dst, src, w ? 4u : 0u);
+              copy_async<4>(dst + 4, w && ds > 4 ? src + 4 : src, w && ds > 4 ? static_cast<uint32_t>(min(ds - 4, 4)) : 0u);
+            } else {
+              uint32_t lo = 0u, hi = 0u;
+              for (int32_t x = 0; x < ds && w; ++x) {
+                const uint32_t v = __ldg(src + x);
+                if (x < 4) lo |= v << (8 * x); else hi |= v << (8 * x - 32);
+              }
+              asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(dst), "r"(lo), "r"(hi) : "memory");
+            }
+          }
+        }
+        if (plain) {
+          wait_all_async();
+          bar_arrive(raw_full + 8 * kv);
+        } else {
+          bar_arrive_copies(raw_full + 8 * kv);
+        }
       }
       wait_all_async();  // copies in flight write shared memory
     } else {
