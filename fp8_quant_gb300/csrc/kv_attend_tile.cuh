@@ -25,8 +25,8 @@
 //                   become fp16 on their way into the ring (exact; see
 //                   kv_attend_split.cuh) by 9-13.
 //
-// Registers: 512 threads are launched with 128 each; the softmax warps take 184
-// (a row's 128 scores stay in registers), the others leave 72.
+// Registers: 512 threads are launched with 128 each; the softmax warps take 176
+// or 184 (a row's 128 scores stay in registers), the others leave 80 or 72.
 //
 // TMEM (512 columns): S_0/P_0, S_1/P_1 (128 each), O_0, O_1 (head_dim each).
 // The products of one CTA run in the order of their issue, so S_t of the next
@@ -59,8 +59,6 @@ struct TileParams {
 constexpr int kTileRows = 128, kTileKeys = 128;
 constexpr int kTileThreads = 512;
 constexpr int kCopyThreads = 224;
-constexpr int kSoftmaxRegs = 176, kOtherRegs = 80;
-static_assert(256 * kSoftmaxRegs + 256 * kOtherRegs <= 65536, "the registers of the launch");
 
 template <int FMT, int DP>
 struct TileSmem {
@@ -70,6 +68,9 @@ struct TileSmem {
   static constexpr int kUnit = kTileKeys * DP * 2;
   static constexpr int kQ = kTileRows * DP * 2;
   // a lane's pieces of a unit: 8 dims (16-bit) or 16 (quantised) of every kStep-th key
+  // 256 threads of each, of the 65,536 registers of the launch
+  static constexpr int kSoftmaxRegs = FMT == KV_CACHE_SRC ? 176 : 184, kOtherRegs = FMT == KV_CACHE_SRC ? 80 : 72;
+  static_assert(256 * (kSoftmaxRegs + kOtherRegs) <= 65536, "the registers of the launch");
   static constexpr int kFillers = FMT == KV_CACHE_SRC ? kCopyThreads : kCopyThreads - 64;
   static constexpr int kPieces = FMT == KV_CACHE_SRC ? DP / 8 : DP / 16;
   static constexpr int kStep = kFillers / kPieces;
@@ -82,7 +83,7 @@ struct TileSmem {
   static constexpr int kOffRaw = kOffOut + 8 * 4096;         // a K and a V tile as they lie in the cache
   static constexpr int kRawTile = kTileKeys * (kRaw + kRawScales);
   static constexpr int kOffBars = kOffRaw + 2 * kRawTile;
-  static constexpr int kBars = 2 * kUnits + 19;
+  static constexpr int kBars = 2 * kUnits + 17;
   static constexpr int kTotal = kOffBars + kBars * 8 + 1024;    // the base is aligned to 1,024
 };
 
@@ -294,7 +295,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
   const int32_t G = static_cast<int32_t>(a.group.d);
   const uint32_t ring = smem + S::kOffRing;
   const uint32_t full = smem + S::kOffBars, empty = full + 8 * S::kUnits;
-  const uint32_t q_full = empty + 8 * S::kUnits, s_full = q_full + 16, p_full = s_full + 16, o_full = p_full + 32, item_full = o_full + 16,
+  const uint32_t q_full = empty + 8 * S::kUnits, s_full = q_full + 16, p_full = s_full + 16, o_full = p_full + 16, item_full = o_full + 16,
                  item_empty = item_full + 16, raw_full = item_empty + 16, raw_empty = raw_full + 16, done = raw_empty + 16;
   if (warp == 8) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
@@ -309,8 +310,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
     for (int t = 0; t < 2; ++t) {
       bar_init(q_full + 8 * t, kTileRows);
       bar_init(s_full + 8 * t, 1);
-      bar_init(p_full + 16 * t, kTileRows);
-      bar_init(p_full + 16 * t + 8, kTileRows);
+      bar_init(p_full + 8 * t, kTileRows);
       bar_init(o_full + 8 * t, 1);
       bar_init(item_full + 8 * t, 1);
       bar_init(item_empty + 8 * t, 8);
@@ -333,9 +333,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
   __syncwarp();
 
   // (all warps of a warpgroup execute the same one)
-  if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+  if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kOtherRegs));
   if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kSoftmaxRegs));
     // ======================================================================================
     // softmax of tile t: a thread a row
     // ======================================================================================
@@ -379,6 +379,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
       float scale = full_scale;
       if constexpr (FMT != KV_CACHE_SRC) {
         if (a.bf16) {  // into fp16's range: the row's largest element to 2^13 .. 2^14
+          float row_f = 1.0f;
 #pragma unroll
           for (int i = 0; i < kQL; ++i) {
             uint32_t y = absmax_pair<true>(absmax_pair<true>(absmax_pair<true>(absmax_pair<true>(0u, qw[i].x), qw[i].y), qw[i].z), qw[i].w);
@@ -392,8 +393,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
             };
             qw[i] = make_uint4(shift(qw[i].x), shift(qw[i].y), shift(qw[i].z), shift(qw[i].w));
             const float mine = __shfl_sync(0xFFFFFFFFu, f, (static_cast<int>(lane) % kQR) * kQL);
-            if (static_cast<int>(lane) / kQR == i) scale = full_scale * __fdiv_rn(1.0f, mine);
+            if (static_cast<int>(lane) / kQR == i) row_f = mine;
           }
+          scale *= __fdiv_rn(1.0f, row_f);
         }
       }
       if (t < x.tiles && x.list.n > 0) {
@@ -483,7 +485,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
           }
         }
         const float ref = m == -INFINITY ? 0.0f : m;
-        // pairs of weights: one packed product and sum for both; the first half's product starts early
+        // pairs of weights: one packed product and sum for both
         float2 sum[4];
 #pragma unroll
         for (int y = 0; y < 4; ++y) sum[y] = make_float2(0.0f, 0.0f);
@@ -498,10 +500,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
             w[i] = pack2(e.x, e.y, kBF16);
           }
           tc_st32(s_at + 32 * c, w);
-          tc_wait_st();
-          tc_fence_before();
-          bar_arrive(p_full + 16 * t + 8 * c);
         }
+        tc_wait_st();
+        tc_fence_before();
+        bar_arrive(p_full + 8 * t);
         sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
         l += sum[0].x + sum[0].y;
         ++waits;
@@ -624,22 +626,20 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
         const uint32_t u = unit + 2 * j;
         for (int32_t t = 0; t < tiles; ++t) {
           const uint32_t parity = (t ? done1 : done0) & 1u;
-          if (t == 0) wait_unit(u + 1);
-          const uint64_t v = v_desc + ((u + 1) % S::kUnits) * (S::kUnit >> 4);
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {  // O_t += P_t V
-            wait(p_full + 16 * t + 8 * half, parity);
-            if (!ok) break;
-#pragma unroll
-            for (int i = half * (kTileKeys / 32); i < (half + 1) * (kTileKeys / 32); ++i)
-              tc_mma_ts(tmem + 256 + t * DP, tmem + t * 128 + i * 8, v + i * (2048 >> 4), pv_desc, j > 0 || i > 0);
+          if (t == 0) {  // both before P, so that its two products follow each other
+            wait_unit(u + 1);
+            if (j + 1 < n) wait_unit(u + 2);
           }
+          const uint64_t v = v_desc + ((u + 1) % S::kUnits) * (S::kUnit >> 4);
+          wait(p_full + 8 * t, parity);
           if (!ok) break;
+#pragma unroll
+          for (int i = 0; i < kTileKeys / 16; ++i)  // O_t += P_t V
+            tc_mma_ts(tmem + 256 + t * DP, tmem + t * 128 + i * 8, v + i * (2048 >> 4), pv_desc, j > 0 || i > 0);
           if (t == tiles - 1) tc_commit(empty + 8 * ((u + 1) % S::kUnits));
           if (j == n - 1) tc_commit(o_full + 8 * t);
           if (t) ++done1; else ++done0;
           if (j + 1 < n) {
-            if (t == 0) wait_unit(u + 2);
             scores(t, u + 2);
           }
         }
