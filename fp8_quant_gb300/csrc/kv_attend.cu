@@ -59,26 +59,32 @@ kv_status launch_rows_any(const AttendParams& p, cudaStream_t stream) {
 // head and `keys` visible keys (upper bounds: the host knows no length).  Both
 // times in us, fitted to calls of 1 to 64 sequences, 512 to 65,536 keys, 1 to 1,024 rows:
 //  * a CTA of the tile kernel takes 128 keys (up to 256 rows) in 1.4 (16-bit rows
-//    of 128 dims), 2.8 (e2m1) or 1.25 - 1.7 us (64 dims), bound by its own
-//    latencies, in items / SMs rounds; all together read at most 5.3 TB/s;
-//  * the others read the cache once per 8 or 16 rows, at 6 TB/s, or 21 (128
-//    dims) and 32 (64 dims) keys and heads a ns for e2m1, and take 16 us more
-//    (two launches, the scan of the lengths, the join).
+//    of 128 dims), 1.5 (quantised ones) or 1.2 - 1.35 us (64 dims), bound by its
+//    own latencies, in items / SMs rounds with 3 us of their own (6 where 128 dims
+//    are converted; half as much again, and tiles 1.3 times as long, with all SMs
+//    at it); all together read at most 5.3 TB/s;
+//  * the others read the cache once per 8 or 16 rows, at 6 TB/s, or 25 (8 rows)
+//    and 17 (16) quantised keys and heads of 128 dims a ns, 36 and 27 of 64; and
+//    take 11 us more (two launches, the scan of the lengths, the join), 16 when
+//    the warps of a CTA have eight heads to do.
 // E.g. 8 sequences x 4,096 keys, 32 over 8 heads of 128, 16-bit: tile 52, the
 // others 41 us at 16 rows, 52 against 65 at 32; 64 sequences x 512 keys, e2m1:
-// 61 against 39 us at 16 rows, 62 against 107 at 64.
+// 72 against 38 us at 16 rows, 77 against 108 at 64.
 bool tiles_pay(const AttendParams& p, kv_cache_format format, int64_t rows, int64_t keys) {
   int sms = 0;
   if (current_sm_count(&sms) != KV_OK) return false;
-  const bool small = p.head_dim <= 64, fp4 = format == KV_CACHE_E2M1;
+  const bool small = p.head_dim <= 64, quant = format != KV_CACHE_SRC, fp4 = format == KV_CACHE_E2M1;
   const double heads = static_cast<double>(p.num_seqs) * p.kv_heads, n = static_cast<double>(keys);
-  const double bytes = heads * n * 2.0 * p.head_dim * (fp4 ? 0.5625 : format == KV_CACHE_E4M3FN ? 1.0 : 2.0);
-  const double step = (fp4 ? (small ? 1.7 : 2.8) : format == KV_CACHE_E4M3FN ? (small ? 1.5 : 2.2) : (small ? 1.25 : 1.4)) *
-                      (rows > 128 ? 1.15 : 1.0);
-  const double blocks = rows <= 8 ? 1.0 : std::ceil(rows / 16.0), row_tiles = std::ceil(rows / 256.0);
-  const double tile = std::max(4.0 + std::ceil(heads * row_tiles / sms) * (3.0 + std::ceil(n / kTileKeys) * step),
-                               row_tiles * bytes / 5.3e6);
-  return tile < 16.0 + blocks * (fp4 ? heads * n / (small ? 32e3 : 21e3) : bytes / 6e6);
+  const double bytes = heads * n * 2.0 * p.head_dim * (fp4 ? 0.5625 : quant ? 1.0 : 2.0);
+  const double row_tiles = std::ceil(rows / 256.0), items = heads * row_tiles;
+  const double load = quant && items >= sms ? 1.3 : 1.0;
+  const double step = (quant ? (small ? (fp4 ? 1.35 : 1.2) : 1.5) : (small ? 1.25 : 1.4)) * (rows > 128 ? 1.1 : 1.0) * load;
+  const double start = quant && !small ? (load > 1.0 ? 9.0 : 6.0) : 3.0;
+  const double tile = std::max(4.0 + std::ceil(items / sms) * (start + std::ceil(n / kTileKeys) * step), row_tiles * bytes / 5.3e6);
+  const bool narrow = rows <= 8;
+  const double blocks = narrow ? 1.0 : std::ceil(rows / 16.0);
+  const double pass = std::max(bytes / 6e6, quant ? heads * n / (small ? (narrow ? 36e3 : 27e3) : (narrow ? 25e3 : 17e3)) : 0.0);
+  return tile < 11.0 + 0.625 * heads_of_cta(p.kv_heads, kSplitWarps) + blocks * pass;
 }
 
 FastDiv fast_div(uint32_t d) {

@@ -62,8 +62,8 @@ constexpr int kCopyThreads = 224;
 
 template <int FMT, int DP>
 struct TileSmem {
-  // Ring units, a K or a V tile in 16 bits: quantised caches take three, as a tile of their K and one
-  // of their V wait in front of the ring.
+  // Ring units, a K or a V tile in 16 bits: quantised caches take three, as raw tiles wait in front of
+  // the ring: as many as there is room for.
   static constexpr int kUnits = FMT == KV_CACHE_SRC ? 4 : 3;
   static constexpr int kUnit = kTileKeys * DP * 2;
   static constexpr int kQ = kTileRows * DP * 2;
@@ -79,11 +79,13 @@ struct TileSmem {
   static constexpr int kRawScales = FMT == KV_CACHE_E2M1 ? 8 : 0;
   static constexpr int kPer = (kTileKeys + kStep - 1) / kStep;
   static constexpr int kOffRing = 2 * kQ;
-  static constexpr int kOffOut = kOffRing + kUnits * kUnit;  // 32 rows of 64 dims for each softmax warp
-  static constexpr int kOffRaw = kOffOut + 8 * 4096;         // a K and a V tile as they lie in the cache
+  static constexpr int kOutDims = FMT == KV_CACHE_SRC ? 64 : 32;  // of 32 rows for each softmax warp
+  static constexpr int kOffOut = kOffRing + kUnits * kUnit;
+  static constexpr int kOffRaw = kOffOut + 8 * 64 * kOutDims;  // K and V tiles in turn, as they lie in the cache
+  static constexpr int kRaws = FMT == KV_CACHE_SRC ? 0 : FMT == KV_CACHE_E4M3FN ? 3 : 4;
   static constexpr int kRawTile = kTileKeys * (kRaw + kRawScales);
-  static constexpr int kOffBars = kOffRaw + 2 * kRawTile;
-  static constexpr int kBars = 2 * kUnits + 17;
+  static constexpr int kOffBars = kOffRaw + kRaws * kRawTile;
+  static constexpr int kBars = 2 * kUnits + 21;
   static constexpr int kTotal = kOffBars + kBars * 8 + 1024;    // the base is aligned to 1,024
 };
 
@@ -296,7 +298,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
   const uint32_t ring = smem + S::kOffRing;
   const uint32_t full = smem + S::kOffBars, empty = full + 8 * S::kUnits;
   const uint32_t q_full = empty + 8 * S::kUnits, s_full = q_full + 16, p_full = s_full + 16, o_full = p_full + 16, item_full = o_full + 16,
-                 item_empty = item_full + 16, raw_full = item_empty + 16, raw_empty = raw_full + 16, done = raw_empty + 16;
+                 item_empty = item_full + 16, raw_full = item_empty + 16, raw_empty = raw_full + 32, done = raw_empty + 32;
   if (warp == 8) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
         static_cast<uint32_t>(__cvta_generic_to_shared(&sh_tmem))) : "memory");
@@ -314,8 +316,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
       bar_init(o_full + 8 * t, 1);
       bar_init(item_full + 8 * t, 1);
       bar_init(item_empty + 8 * t, 8);
-      bar_init(raw_full + 8 * t, 32);
-      bar_init(raw_empty + 8 * t, S::kFillers / 32);
+    }
+    for (int i = 0; i < S::kRaws; ++i) {
+      bar_init(raw_full + 8 * i, 32);
+      bar_init(raw_empty + 8 * i, S::kFillers / 32);
     }
     bar_init(done, 1);
     sh_failed = 0;
@@ -525,16 +529,20 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
           ++items;
           tc_fence_after();
           const float inv = __fdiv_rn(vscale, l);
-          // 64 dims at a time through shared memory, so that eight lanes write 128 bytes of a row
-          const uint32_t stage = smem + S::kOffOut + warp * 4096u;
+          // kOutDims dims at a time through shared memory, so that neighbouring lanes write one row
+          constexpr int kOL = S::kOutDims / 8, kOR = 32 / kOL;  // lanes a row, rows at once
+          const uint32_t stage = smem + S::kOffOut + warp * (64u * S::kOutDims);
+          auto staged = [&](uint32_t row, uint32_t piece) {
+            return stage + row * (2u * S::kOutDims) + ((piece ^ (kOL == 8 ? row & 7u : row >> 1 & 3u)) << 4);
+          };
           uint8_t* const out = a.out + static_cast<int64_t>(it.seq.q0 + it.q_first + t * p.qpt) * a.o_token +
-                               static_cast<int64_t>(it.kvh * G) * a.o_head + 16 * (lane & 7u);
+                               static_cast<int64_t>(it.kvh * G) * a.o_head + 16 * (lane % kOL);
 #pragma unroll
-          for (int c = 0; c < DP / 64; ++c) {
+          for (int c = 0; c < DP / S::kOutDims; ++c) {
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
+            for (int half = 0; half < S::kOutDims / 32; ++half) {
               uint32_t w[32];
-              tc_ld32(w, o_at + 64 * c + 32 * half);
+              tc_ld32(w, o_at + S::kOutDims * c + 32 * half);
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 uint32_t o[4];
@@ -544,17 +552,17 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
                   fine = fine && fabsf(lo) < INFINITY && fabsf(hi) < INFINITY;
                   o[x] = pack2(lo, hi, a.bf16);
                 }
-                st_shared16(stage + swizzled(lane, 4 * half + i, 32), o[0], o[1], o[2], o[3]);
+                st_shared16(staged(lane, 4 * half + i), o[0], o[1], o[2], o[3]);
               }
             }
             __syncwarp();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const uint32_t row = 4 * i + (lane >> 3);
+            for (int i = 0; i < 32 / kOR; ++i) {
+              const uint32_t row = kOR * i + lane / kOL;
               const int32_t rr = row0 + static_cast<int32_t>(row), y = static_cast<int32_t>(a.group.quot(static_cast<uint32_t>(rr)));
-              const uint4 v = ld_shared16(stage + swizzled(row, lane & 7u, 32));
-              if (y < p.qpt && t * p.qpt + y < it.nq && static_cast<int32_t>(64 * c + 8 * (lane & 7u)) < a.head_dim)
-                *reinterpret_cast<uint4*>(out + y * a.o_token + (rr - y * G) * a.o_head + 128 * c) = v;
+              const uint4 v = ld_shared16(staged(row, lane % kOL));
+              if (y < p.qpt && t * p.qpt + y < it.nq && static_cast<int32_t>(S::kOutDims * c + 8 * (lane % kOL)) < a.head_dim)
+                *reinterpret_cast<uint4*>(out + y * a.o_token + (rr - y * G) * a.o_head + 2 * S::kOutDims * c) = v;
             }
             __syncwarp();
           }
@@ -777,7 +785,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
       // quantised rows as they lie into shared memory: lane l looks up keys l, l + 32, ..
       // ====================================================================================
       const int32_t kv = warp == 15 ? 0 : 1;
-      const uint32_t at = smem + S::kOffRaw + static_cast<uint32_t>(kv) * S::kRawTile;
       const int32_t page_stride = kv ? p.v_page : p.k_page, slot_stride = kv ? p.v_slot : p.k_slot;
       constexpr int kKeys = kTileKeys / 32, kChunks = S::kRaw / 16, kRows = 32 / kChunks;
       int32_t round = 0, j = 0;
@@ -819,8 +826,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
         ++j;
         skip_empty();
         if (have) look();
-        if (tile > 0u) ok = __all_sync(0xFFFFFFFFu, bar_wait(raw_empty + 8 * kv, (tile - 1u) & 1u, failed));
+        const uint32_t u = 2u * tile + static_cast<uint32_t>(kv), raw = u % S::kRaws;
+        if (u >= S::kRaws) ok = __all_sync(0xFFFFFFFFu, bar_wait(raw_empty + 8 * raw, (u / S::kRaws - 1u) & 1u, failed));
         if (!ok) break;
+        const uint32_t at = smem + S::kOffRaw + raw * S::kRawTile;
         const uint8_t* const base = kv ? a.v + kvh * a.v_head : a.k + kvh * a.k_head;
         // kChunks lanes a row, so that a copy meets few lines
         const uint32_t chunk = lane % kChunks;
@@ -864,9 +873,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
         }
         if (plain) {
           wait_all_async();
-          bar_arrive(raw_full + 8 * kv);
+          bar_arrive(raw_full + 8 * raw);
         } else {
-          bar_arrive_copies(raw_full + 8 * kv);
+          bar_arrive_copies(raw_full + 8 * raw);
         }
       }
       wait_all_async();  // copies in flight write shared memory
@@ -875,55 +884,52 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
       // and from there, as fp16, into the ring
       // ====================================================================================
       constexpr int kWords = FMT == KV_CACHE_E4M3FN ? 4 : 2;
-      uint32_t tile = 0u;
       for (int32_t round = 0; ok && tile_item(p, round, &it); ++round) {
-        for (int32_t j = 0; j < it.list.n && ok; ++j, ++tile) {
 #pragma unroll 1
-          for (int kv = 0; kv < 2 && ok; ++kv, ++unit) {
-            const uint32_t from = smem + S::kOffRaw + static_cast<uint32_t>(kv) * S::kRawTile;
-            uint32_t w[S::kPer][kWords], sc[FMT == KV_CACHE_E2M1 ? S::kPer : 1];
-            ok = __all_sync(0xFFFFFFFFu, bar_wait(raw_full + 8 * kv, tile & 1u, failed));
-            if (!ok) break;
+        for (int32_t left = 2 * it.list.n; left > 0 && ok; --left, ++unit) {
+          const uint32_t raw = unit % S::kRaws, from = smem + S::kOffRaw + raw * S::kRawTile;
+          uint32_t w[S::kPer][kWords], sc[FMT == KV_CACHE_E2M1 ? S::kPer : 1];
+          ok = __all_sync(0xFFFFFFFFu, bar_wait(raw_full + 8 * raw, (unit / S::kRaws) & 1u, failed));
+          if (!ok) break;
 #pragma unroll
-            for (int i = 0; i < S::kPer; ++i) {
-              const uint32_t key = min(key0 + i * S::kStep, static_cast<uint32_t>(kTileKeys - 1));
-              if constexpr (FMT == KV_CACHE_E4M3FN) {
-                const uint4 v = ld_shared16(from + key * S::kRaw + piece * 16);
-                w[i][0] = v.x; w[i][1] = v.y; w[i][2] = v.z; w[i][3] = v.w;
-              } else {
-                asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[i][0]), "=r"(w[i][1]) : "r"(from + key * S::kRaw + piece * 8) : "memory");
-                asm volatile("ld.shared.u8 %0, [%1];" : "=r"(sc[i]) : "r"(from + kTileKeys * S::kRaw + key * 8 + piece) : "memory");
-              }
+          for (int i = 0; i < S::kPer; ++i) {
+            const uint32_t key = min(key0 + i * S::kStep, static_cast<uint32_t>(kTileKeys - 1));
+            if constexpr (FMT == KV_CACHE_E4M3FN) {
+              const uint4 v = ld_shared16(from + key * S::kRaw + piece * 16);
+              w[i][0] = v.x; w[i][1] = v.y; w[i][2] = v.z; w[i][3] = v.w;
+            } else {
+              asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[i][0]), "=r"(w[i][1]) : "r"(from + key * S::kRaw + piece * 8) : "memory");
+              asm volatile("ld.shared.u8 %0, [%1];" : "=r"(sc[i]) : "r"(from + kTileKeys * S::kRaw + key * 8 + piece) : "memory");
             }
-            __syncwarp();
-            if (lane == 0u) bar_arrive(raw_empty + 8 * kv);
-            wait_empty(unit);
-            if (!ok) break;
-            const uint32_t at = ring + (unit % S::kUnits) * S::kUnit;
-#pragma unroll
-            for (int i = 0; i < S::kPer; ++i) {
-              const uint32_t key = key0 + i * S::kStep;
-              if (kTileKeys % S::kStep != 0 && key >= kTileKeys) break;
-              uint32_t f[8];
-              if constexpr (FMT == KV_CACHE_E4M3FN) {
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                  f[2 * x] = f16x2_from_e4m3x2(w[i][x]);
-                  f[2 * x + 1] = f16x2_from_e4m3x2(w[i][x] >> 16);
-                }
-              } else {
-                const uint32_t s2 = f16x2_from_e4m3x2(sc[i] * 0x0101u);  // e2m1 codes are finite
-                f16x2_from_e2m1x8(w[i][0], f);
-                f16x2_from_e2m1x8(w[i][1], f + 4);
-#pragma unroll
-                for (int x = 0; x < 8; ++x) f[x] = mul_f16x2(f[x], s2);
-              }
-              st_shared16(at + swizzled(key, 2 * piece, kTileKeys), f[0], f[1], f[2], f[3]);
-              st_shared16(at + swizzled(key, 2 * piece + 1, kTileKeys), f[4], f[5], f[6], f[7]);
-            }
-            fence_async_shared();
-            bar_arrive(full + 8 * (unit % S::kUnits));
           }
+          __syncwarp();
+          if (lane == 0u) bar_arrive(raw_empty + 8 * raw);
+          wait_empty(unit);
+          if (!ok) break;
+          const uint32_t at = ring + (unit % S::kUnits) * S::kUnit;
+#pragma unroll
+          for (int i = 0; i < S::kPer; ++i) {
+            const uint32_t key = key0 + i * S::kStep;
+            if (kTileKeys % S::kStep != 0 && key >= kTileKeys) break;
+            uint32_t f[8];
+            if constexpr (FMT == KV_CACHE_E4M3FN) {
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                f[2 * x] = f16x2_from_e4m3x2(w[i][x]);
+                f[2 * x + 1] = f16x2_from_e4m3x2(w[i][x] >> 16);
+              }
+            } else {
+              const uint32_t s2 = f16x2_from_e4m3x2(sc[i] * 0x0101u);  // e2m1 codes are finite
+              f16x2_from_e2m1x8(w[i][0], f);
+              f16x2_from_e2m1x8(w[i][1], f + 4);
+#pragma unroll
+              for (int x = 0; x < 8; ++x) f[x] = mul_f16x2(f[x], s2);
+            }
+            st_shared16(at + swizzled(key, 2 * piece, kTileKeys), f[0], f[1], f[2], f[3]);
+            st_shared16(at + swizzled(key, 2 * piece + 1, kTileKeys), f[4], f[5], f[6], f[7]);
+          }
+          fence_async_shared();
+          bar_arrive(full + 8 * (unit % S::kUnits));
         }
       }
     }
