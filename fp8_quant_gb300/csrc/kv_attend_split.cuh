@@ -48,17 +48,13 @@
 #include "kv_attend.cuh"
 #include "kv_host.h"
 
-#ifndef KV_ATTEND_L2
-#define KV_ATTEND_L2 ""      // cp.async's L2 prefetch size: "", ".L2::128B" or ".L2::256B"
-#endif
-#ifndef KV_ATTEND_STATIC
-#define KV_ATTEND_STATIC 80  // percent of the steps in the CTAs' first shares
-#endif
-#ifndef KV_ATTEND_MIN_STEPS
-#define KV_ATTEND_MIN_STEPS 4
-#endif
-
 namespace kvimpl {
+
+constexpr int kFirstShares = 80;  // percent of the steps in the CTAs' first shares
+// Steps of a share at least; kLastSteps where a CTA has eight times as many to do: each share of
+// an item is a part to be written and joined (windows of 4,096 in 128 sequences: 317 us at 12
+// steps, 332 at 4; one sequence of 1,000 keys, one share a CTA: 26 us at 16, 17.5 at 4).
+constexpr int kMinSteps = 4, kLastSteps = 12;
 
 // The shares: level k holds shares of `size` steps from step `start` on, numbered from `first`.
 struct ShareLevel {
@@ -99,10 +95,11 @@ __device__ __forceinline__ void cut_shares(int64_t total, int32_t ctas, int32_t 
                                            SplitWork* w) {
   int64_t each = (total + ctas - 1) / ctas;
   if (each < min_steps) each = min_steps;
+  min_steps = static_cast<int32_t>(max(static_cast<int64_t>(min_steps), min(each / 8, static_cast<int64_t>(kLastSteps))));
   int32_t n = 0, made = 0;
   int64_t at = 0, size = each;
   if (each >= 4 * min_steps && max_shares >= 3 * ctas) {
-    size = each * KV_ATTEND_STATIC / 100;
+    size = each * kFirstShares / 100;
     while (n < kLevels - 1) {
       w->level[n++] = ShareLevel{at, static_cast<int32_t>(size), made};
       at += size * ctas;
@@ -204,9 +201,9 @@ __device__ __forceinline__ int64_t wide(uint32_t n, int32_t stride) { return wid
 template <int BYTES>
 __device__ __forceinline__ void copy_async(uint32_t dst, const uint8_t* src, uint32_t bytes) {
   if constexpr (BYTES == 16) {
-    asm volatile("cp.async.cg.shared.global" KV_ATTEND_L2 " [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
   } else {
-    asm volatile("cp.async.ca.shared.global" KV_ATTEND_L2 " [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(bytes), "n"(BYTES) : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(bytes), "n"(BYTES) : "memory");
   }
 }
 
@@ -1232,7 +1229,7 @@ int64_t set_up_split(SplitParams& p, int heads, int rows, int tile, int64_t full
   p.hw = heads_of_cta(a.kv_heads, heads);
   p.subs = heads / p.hw;
   p.hgroups = a.kv_heads / p.hw;
-  p.min_steps = KV_ATTEND_MIN_STEPS;
+  p.min_steps = kMinSteps;
   // An item that cannot be longer than the shortest share is not split, nor is
   // any where the workspace holds the parts of less than half the GPU.
   const int64_t meta = (static_cast<int64_t>(a.num_seqs) + 31) / 32 * 256;

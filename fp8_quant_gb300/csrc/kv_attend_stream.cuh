@@ -22,10 +22,6 @@
 #include "kv_async.cuh"
 #include "kv_attend_split.cuh"
 
-#ifndef KV_STREAM_FP4_TILE
-#define KV_STREAM_FP4_TILE 64
-#endif
-
 namespace kvimpl {
 
 // A run of bytes (both ends and the length multiples of 16).
@@ -34,6 +30,10 @@ __device__ __forceinline__ void copy_run(uint32_t dst, const uint8_t* src, uint3
                ::"r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
 }
 
+// Keys of a tile of a 4-bit cache, whose softmax would cost as much as their products otherwise
+// (64 sequences of 24,000 keys: 427 us at 64, 480 at 32).
+constexpr int kStreamFp4Tile = 64;
+
 struct StreamParams {
   SplitParams s;
   int32_t box;   // keys of a TMA box: a tile's, or 32 or 16 of them
@@ -41,21 +41,16 @@ struct StreamParams {
   CUtensorMap k_map, v_map, ks_map, vs_map;
 };
 
-// kPack: rows shorter than 128 bytes whose heads lie side by side are fetched two or four heads at a
-// time, as 128-byte rows: TMA takes about three cycles a row whatever its length (64-byte rows
-// alone held the 4-bit cache to 3.8 TB/s).
-template <int FMT, int DP, int NB, bool kPack>
+template <int FMT, int DP, int NB>
 struct StreamLayout {
   using L = Layout<FMT, DP>;
-  // Keys of a tile: 64 4-bit ones, whose softmax would cost as much as their products otherwise.
-  static constexpr int TW = FMT == KV_CACHE_E2M1 ? KV_STREAM_FP4_TILE : L::TW;
+  static constexpr int TW = FMT == KV_CACHE_E2M1 ? kStreamFp4Tile : L::TW;
   static constexpr int kHeads = kSplitWarps;                     // heads, or tiles of fewer, of a CTA: a warp each
   static constexpr int kWarps = kHeads;
   static constexpr int kThreads = 32 * (kWarps + 4);             // and a warpgroup of which one warp copies
   static constexpr int kLaunchRegs = 168, kRegs = 208, kCopyRegs = 88;
   static_assert(32 * kWarps * kRegs + 128 * kCopyRegs <= kThreads * kLaunchRegs, "the registers of the launch");
-  static constexpr int kPerRow = kPack ? 128 / L::kRow : 1;      // heads of a row of a box
-  static constexpr int W = kPack || L::kRow > 128 ? 128 : L::kRow;  // its bytes
+  static constexpr int W = L::kRow > 128 ? 128 : L::kRow;        // bytes of a row of a box
   static constexpr int kSpans = L::kRow > 128 ? L::kRow / 128 : 1;  // boxes of a head's row
   static constexpr int kCodes = kHeads * TW * L::kRow;
   static constexpr int kUnit = kCodes + (FMT == KV_CACHE_E2M1 ? (kHeads * TW * (DP / 16) + 1023) / 1024 * 1024 : 0);
@@ -78,11 +73,11 @@ struct StreamStep {
 // of an item's steps in a share: the first, the last; the share has all of them, or the item's first; no more steps
 constexpr int kFirst = 1, kLast = 2, kWhole = 4, kBegins = 8, kStop = 16;
 
-template <int FMT, int DP, int NB, bool kBF16, bool kPack>
-__global__ void __launch_bounds__(StreamLayout<FMT, DP, NB, kPack>::kThreads, 1)
+template <int FMT, int DP, int NB, bool kBF16>
+__global__ void __launch_bounds__(StreamLayout<FMT, DP, NB>::kThreads, 1)
     kv_attend_stream(const __grid_constant__ StreamParams sp) {
   using L = Layout<FMT, DP>;
-  using S = StreamLayout<FMT, DP, NB, kPack>;
+  using S = StreamLayout<FMT, DP, NB>;
   constexpr int TW = S::TW, MB = TW / 16, W = S::W, QP = DP / 8, OM = L::VN * L::VD / 2;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ int64_t sh_scan[S::kThreads / 32];
@@ -165,7 +160,7 @@ __global__ void __launch_bounds__(StreamLayout<FMT, DP, NB, kPack>::kThreads, 1)
     const int32_t nbox = TW / sp.box;                  // boxes of a tile
     const int32_t sub = static_cast<int32_t>(lane) / nbox, part = static_cast<int32_t>(lane) - sub * nbox;
     const bool mine = sub < p.subs;                    // the lane has a box of every step
-    const uint32_t box_bytes = static_cast<uint32_t>(sp.box * p.hw / S::kPerRow) * W;
+    const uint32_t box_bytes = static_cast<uint32_t>(sp.box * p.hw) * W;
     const uint32_t sc_bytes = FMT == KV_CACHE_E2M1 ? static_cast<uint32_t>(sp.box * p.hw * (a.head_dim / 16)) : 0u;
     const uint32_t at_codes = static_cast<uint32_t>(sub) * (p.hw * TW * L::kRow) + static_cast<uint32_t>(part) * S::kSpans * box_bytes;
     const uint32_t at_scales = S::kCodes + static_cast<uint32_t>(sub * nbox + part) * sc_bytes;
@@ -254,7 +249,7 @@ __global__ void __launch_bounds__(StreamLayout<FMT, DP, NB, kPack>::kThreads, 1)
             if (has) {
 #pragma unroll
               for (int x = 0; x < S::kSpans; ++x)
-                tma_box(at + at_codes + x * box_bytes, kv ? &sp.v_map : &sp.k_map, bar, x * W, static_cast<int32_t>(in_page), hg * p.hw / S::kPerRow, page);
+                tma_box(at + at_codes + x * box_bytes, kv ? &sp.v_map : &sp.k_map, bar, x * W, static_cast<int32_t>(in_page), hg * p.hw, page);
               if constexpr (FMT == KV_CACHE_E2M1) {
                 if (sp.flat_scales)
                   copy_run(at + at_scales, (kv ? a.v_sc : a.k_sc) + (page == a.num_pages ? 0 : wide(page, kv ? p.vs_page : p.ks_page) +
@@ -288,13 +283,12 @@ __global__ void __launch_bounds__(StreamLayout<FMT, DP, NB, kPack>::kThreads, 1)
     // Row g of a product is key gk of its eight: lanes that read together then meet rows of both
     // parities and of both halves of the swizzle.
     const uint32_t gk = g ^ ((g & 1u) << 2);
-    const uint32_t in_row = static_cast<uint32_t>(hl % S::kPerRow) * (L::kRow / 16);  // the head's first 16 bytes of a packed row
     const float kscale = a.scale_log2 * tensor_scale(a.k_scale);
     const float vscale = tensor_scale(a.v_scale);
     const uint32_t ds = static_cast<uint32_t>(a.head_dim) / 16;
     // where the warp's rows are in a unit
-    const uint32_t head_at = static_cast<uint32_t>(sub) * (p.hw * TW * L::kRow) + static_cast<uint32_t>(hl / S::kPerRow * sp.box) * W;
-    const uint32_t span_step = static_cast<uint32_t>(p.hw / S::kPerRow * sp.box) * W;
+    const uint32_t head_at = static_cast<uint32_t>(sub) * (p.hw * TW * L::kRow) + static_cast<uint32_t>(hl * sp.box) * W;
+    const uint32_t span_step = static_cast<uint32_t>(p.hw * sp.box) * W;
     // where 16 keys begin: boxes of a tile lie one behind the other
     const uint32_t box_step = S::kSpans * span_step;
     const int per_box = sp.box / 16;  // 1, 2 or 4
@@ -372,7 +366,6 @@ __global__ void __launch_bounds__(StreamLayout<FMT, DP, NB, kPack>::kThreads, 1)
         for (int i = 0; i < L::KN; ++i) {
           // rows gk and gk + 8 share a swizzle
           const uint32_t piece = L::kRow >= 128 ? ((2u * t + (i & 1)) ^ gk) << 4
-                                 : kPack        ? (((in_row + t * L::KC / 16) ^ gk) << 4) + t * L::KC % 16
                                  : W == 64      ? (t ^ ((gk >> 1) & 3u)) << 4
                                                 : t * L::KC;
           uint32_t w[MB][2][L::KC / 4], sc[MB][2];
@@ -415,9 +408,8 @@ __global__ void __launch_bounds__(StreamLayout<FMT, DP, NB, kPack>::kThreads, 1)
               const uint32_t at = vat + mb_at(r >> 4) + static_cast<uint32_t>(r & 15) * W;
 #pragma unroll
               for (int x = 0; x < S::kSpans; ++x)
-                if (lane < (kPack ? L::kRow : W) / 16) {
-                  const uint32_t c = kPack ? (in_row + lane) ^ (static_cast<uint32_t>(r) & 7u) : lane;
-                  asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at + x * span_step + c * 16u), "r"(0u) : "memory");
+                if (lane < W / 16) {
+                  asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at + x * span_step + lane * 16u), "r"(0u) : "memory");
                 }
             }
           }
@@ -433,7 +425,6 @@ __global__ void __launch_bounds__(StreamLayout<FMT, DP, NB, kPack>::kThreads, 1)
             for (int x = 0; x < 4; ++x) {
               const uint32_t r = (x & 1) ? (2u * t + 1u) ^ 4u : 2u * t, row = 8u * (x >> 1) + r;
               const uint32_t piece = L::kRow >= 128 ? (g ^ r) << 4
-                                     : kPack        ? (((in_row + g * L::VC / 16) ^ r) << 4) + g * L::VC % 16
                                      : W == 64      ? (((g >> 1) ^ ((r >> 1) & 3u)) << 4) + (g & 1u) * 8u
                                                     : g * L::VC;
               ld_own<L::VC>(w[x], vat + mb_at(mb) + i * span_step + row * W + piece);
@@ -517,10 +508,10 @@ __global__ void __launch_bounds__(StreamLayout<FMT, DP, NB, kPack>::kThreads, 1)
 // ---------------------------------------------------------------------------
 
 // Launches the kernel of one format and padded head dim.
-template <int FMT, int DP, int NB, bool kBF16, bool kPack>
+template <int FMT, int DP, int NB, bool kBF16>
 kv_status launch_stream(StreamParams sp, void* work, int64_t work_bytes, int64_t max_keys, cudaStream_t stream) {
-  using S = StreamLayout<FMT, DP, NB, kPack>;
-  auto* kernel = kv_attend_stream<FMT, DP, NB, kBF16, kPack>;
+  using S = StreamLayout<FMT, DP, NB>;
+  auto* kernel = kv_attend_stream<FMT, DP, NB, kBF16>;
   static_assert(S::kTotal <= 227 * 1024 - 8 * 1024, "shared memory, with the static part");
   int sms = 0;
   kv_status st = current_sm_count(&sms);
@@ -536,28 +527,23 @@ kv_status launch_stream(StreamParams sp, void* work, int64_t work_bytes, int64_t
 }
 
 template <int FMT, int DP, bool kBF16>
-kv_status launch_stream_dim(const StreamParams& sp, bool wide, bool pack, void* work, int64_t work_bytes, int64_t max_keys,
+kv_status launch_stream_dim(const StreamParams& sp, bool wide, void* work, int64_t work_bytes, int64_t max_keys,
                             cudaStream_t stream) {
-  if constexpr (Layout<FMT, DP>::kRow < 128) {
-    if (pack)
-      return wide ? launch_stream<FMT, DP, 2, kBF16, true>(sp, work, work_bytes, max_keys, stream)
-                  : launch_stream<FMT, DP, 1, kBF16, true>(sp, work, work_bytes, max_keys, stream);
-  }
-  return wide ? launch_stream<FMT, DP, 2, kBF16, false>(sp, work, work_bytes, max_keys, stream)
-              : launch_stream<FMT, DP, 1, kBF16, false>(sp, work, work_bytes, max_keys, stream);
+  return wide ? launch_stream<FMT, DP, 2, kBF16>(sp, work, work_bytes, max_keys, stream)
+              : launch_stream<FMT, DP, 1, kBF16>(sp, work, work_bytes, max_keys, stream);
 }
 
 template <int FMT, bool kBF16>
-kv_status launch_stream_fmt(const StreamParams& sp, bool wide, bool pack, void* work, int64_t work_bytes, int64_t max_keys,
+kv_status launch_stream_fmt(const StreamParams& sp, bool wide, void* work, int64_t work_bytes, int64_t max_keys,
                             cudaStream_t stream) {
-  return sp.s.a.head_dim <= 64 ? launch_stream_dim<FMT, 64, kBF16>(sp, wide, pack, work, work_bytes, max_keys, stream)
-                               : launch_stream_dim<FMT, 128, kBF16>(sp, wide, pack, work, work_bytes, max_keys, stream);
+  return sp.s.a.head_dim <= 64 ? launch_stream_dim<FMT, 64, kBF16>(sp, wide, work, work_bytes, max_keys, stream)
+                               : launch_stream_dim<FMT, 128, kBF16>(sp, wide, work, work_bytes, max_keys, stream);
 }
 
 // The formats' instantiations, a translation unit each.
-kv_status stream_bf16(const StreamParams& p, bool wide, bool pack, void* work, int64_t work_bytes, int64_t max_keys, cudaStream_t stream);
-kv_status stream_f16(const StreamParams& p, bool wide, bool pack, void* work, int64_t work_bytes, int64_t max_keys, cudaStream_t stream);
-kv_status stream_e4m3(const StreamParams& p, bool wide, bool pack, void* work, int64_t work_bytes, int64_t max_keys, cudaStream_t stream);
-kv_status stream_e2m1(const StreamParams& p, bool wide, bool pack, void* work, int64_t work_bytes, int64_t max_keys, cudaStream_t stream);
+kv_status stream_bf16(const StreamParams& p, bool wide, void* work, int64_t work_bytes, int64_t max_keys, cudaStream_t stream);
+kv_status stream_f16(const StreamParams& p, bool wide, void* work, int64_t work_bytes, int64_t max_keys, cudaStream_t stream);
+kv_status stream_e4m3(const StreamParams& p, bool wide, void* work, int64_t work_bytes, int64_t max_keys, cudaStream_t stream);
+kv_status stream_e2m1(const StreamParams& p, bool wide, void* work, int64_t work_bytes, int64_t max_keys, cudaStream_t stream);
 
 }  // namespace kvimpl
