@@ -500,7 +500,8 @@ __device__ __forceinline__ void softmax_step(float (&s)[MB][NB][4], const float 
         }
       l[nb][c] = __fmaf_rn(l[nb][c], alpha[nb][c], sum);
     }
-  if (__any_sync(0xFFFFFFFFu, grew)) {
+  // (e2m1: without the branch the compiler mixes this with the next products' loads and conversions)
+  if (FMT == KV_CACHE_E2M1 || __any_sync(0xFFFFFFFFu, grew)) {
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll

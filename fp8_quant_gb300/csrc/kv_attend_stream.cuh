@@ -19,9 +19,9 @@
 // Every wait has a limit; a CTA whose wait ran out counts that and leaves.
 //
 // Measured on one GB300 (one query a sequence, 32 over 8 heads of 128): 128
-// windows of 4,096 16-bit keys 314 us, 6.8 TB/s; 32 sequences of 16,000 - 32,768
-// e4m3fn keys 246 us, 6.5 TB/s (100 and 96 % of a copy's rate); 64 such sequences of
-// 4-bit keys 422 us, 4.3 TB/s, and one of 131,071 keys 49 us.  The 4-bit ones are
+// windows of 4,096 16-bit keys 317 us, 6.7 TB/s; 32 sequences of 16,000 - 32,768
+// e4m3fn keys 248 us, 6.4 TB/s (99 and 95 % of a copy's rate); 64 such sequences of
+// 4-bit keys 419 us, 4.3 TB/s, and one of 131,071 keys 48 us.  The 4-bit ones are
 // bound by the eight warps' conversions and products, not by memory; 12 or 16
 // warps with fewer registers each took 670 us and more.
 #pragma once
@@ -394,6 +394,10 @@ __global__ void __launch_bounds__(StreamLayout<FMT, DP, NB>::kThreads, 1)
         const bool bad = sh_bad != 0;
         if (bad || !(j0 + TW - 1 <= p_lo && (a.window == 0 || j0 > p_hi - a.window || j0 + TW - 1 < a.sinks)))
           hide_scores<NB, MB>(a, a.table + static_cast<int64_t>(b) * a.table_stride, j0, p_hi, bad, seq.len - seq.nq, row0, gk, s);
+        if constexpr (FMT == KV_CACHE_E2M1) {  // before the softmax, for one stretch of code without a wait
+          ok = __all_sync(0xFFFFFFFFu, bar_wait(full + 8 * vs, ((2u * n + 1u) / S::kUnits) & 1u, failed));
+          if (!ok) break;
+        }
         softmax_step<FMT, NB, MB, OM, kBF16>(s, rs, m, l, o, pt, pl);
       } else {
         __syncwarp();
@@ -401,7 +405,8 @@ __global__ void __launch_bounds__(StreamLayout<FMT, DP, NB>::kThreads, 1)
       }
 
       // O^T += V^T P^T
-      ok = __all_sync(0xFFFFFFFFu, bar_wait(full + 8 * vs, ((2u * n + 1u) / S::kUnits) & 1u, failed));
+      if (FMT != KV_CACHE_E2M1 || !work)
+        ok = __all_sync(0xFFFFFFFFu, bar_wait(full + 8 * vs, ((2u * n + 1u) / S::kUnits) & 1u, failed));
       if (!ok) break;
       if (work) {
         const uint32_t unit_at = ring + vs * S::kUnit, vat = unit_at + head_at;

@@ -37,9 +37,9 @@
 // softmax ends and its rows are written.
 //
 // Measured on one GB300 (32 over 8 heads of 128): one causal prompt of 8,192
-// fp16 tokens 410 us, 1.34 PFLOP/s; prompts of 2,500 and 4,095 bf16 tokens in windows
+// fp16 tokens 416 us, 1.32 PFLOP/s; prompts of 2,500 and 4,095 bf16 tokens in windows
 // of 1,024 137 us, 0.81 PFLOP/s; chunks of 400 - 1,000 fp16 tokens over windows of
-// 4,096 4-bit keys 150 us, 0.95 PFLOP/s.  What bounds it is the chain of one tile:
+// 4,096 4-bit keys 148 us, 0.96 PFLOP/s.  What bounds it is the chain of one tile:
 // S's product, maximum and weights (0.9 us of a row's 128 scores in one thread), P V, next
 // product: 2.0 us a pair of tiles and 128 keys against 1.1 of products.  Handing the weights
 // over in two or three parts, or loading S while its first half's maximum is taken, gained
