@@ -17,13 +17,17 @@
 //                   the other tile's products do.
 //   warps 9-15      bring K and V from their pages into a ring of shared memory,
 //                   in the 128-byte swizzle that the products read.  16-bit
-//                   tiles whose keys all exist go by TMA, a box for each page
-//                   and 64 dims, where pages divide or are divided by 128 keys;
-//                   others by cp.async, 16 bytes a lane, with zeros for keys that
-//                   no row needs.  Quantised rows are copied as they are by
-//                   warps 14 (V) and 15 (K) with cp.async, a tile ahead, and
-//                   become fp16 on their way into the ring (exact; see
-//                   kv_attend_split.cuh) by 9-13.
+//                   tiles whose keys all exist go by TMA, a box for each 64 dims
+//                   and page, or 16 keys of one (windows, and pages that 128 keys
+//                   are no multiple of); others by cp.async, 16 bytes a lane, with
+//                   zeros for keys that no row needs.  Quantised rows are copied
+//                   as they are by warps 14 (V) and 15 (K) with cp.async, up to
+//                   two tiles ahead, and become fp16 on their way into the ring
+//                   (exact; see kv_attend_split.cuh) by 9-13.
+//
+// Weights are rounded once to 16 bits, as the product's operand: 2^-9 (bf16) or
+// 2^-12 of each at most, which is what the output's own rounding is; their sum
+// is of the unrounded ones in fp32.
 //
 // Registers: 512 threads are launched with 128 each; the softmax warps take 176
 // or 184 (a row's 128 scores stay in registers), the others leave 80 or 72.
