@@ -823,7 +823,7 @@ __global__ void __launch_bounds__(32 * kSplitWarps, (kSplitCtas<DP, NB>))
 #pragma unroll
                 for (int i = 0; i < L::KN; ++i)
                   copy_async<L::KC>(kat + ((2 * mb + rh) * L::KN + i) * 32 * L::KC, src + 4 * i * L::KC, kbytes(i));
-                src += 8 * p.k_slot;
+                src += wide(8, p.k_slot);
               }
             } else {
               const uint8_t* src = vlane + wide(id, p.v_page) + wide(off, p.v_slot);
@@ -832,7 +832,7 @@ __global__ void __launch_bounds__(32 * kSplitWarps, (kSplitCtas<DP, NB>))
 #pragma unroll
                 for (int i = 0; i < L::VN; ++i)
                   copy_async<L::VC>(vat + ((4 * mb + r) * L::VN + i) * 32 * L::VC, src + 8 * i * L::VC, vbytes(i));
-                src += (r & 1) ? 7 * p.v_slot : p.v_slot;
+                src += wide((r & 1) ? 7 : 1, p.v_slot);
               }
             }
           }
