@@ -217,6 +217,7 @@ __global__ void __launch_bounds__(kThreads) kv_rope_rows(const __grid_constant__
 #pragma unroll
     for (int j = 0; j < U; ++j) {
       const uint32_t hs = first + j * p.hpp + sub;
+      a[j] = b[j] = make_uint4(0u, 0u, 0u, 0u);
       if (sub < p.hpp && hs < p.heads) {
         const int side = hs < r.q_heads ? 0 : hs < qk ? 1 : 2;
         const RopeSide& sd = r.side[side];
@@ -262,14 +263,14 @@ __global__ void __launch_bounds__(kThreads) kv_rope_rows(const __grid_constant__
       dst += static_cast<int64_t>(h) * sd.dst_head;
       uint32_t w[8] = {a[j].x, a[j].y, a[j].z, a[j].w, b[j].x, b[j].y, b[j].z, b[j].w};
       const bool plain = FMT == KV_CACHE_SRC || side == 0;  // 16-bit rows
+      // x[0 .. 7]: piece a, x[8 .. 15]: piece b, in fp32 (0 where they are copied)
+      float x[16] = {};
       if (plain && !rot) {
         if (live) {
           *reinterpret_cast<uint4*>(dst + 32u * item) = a[j];
           *reinterpret_cast<uint4*>(dst + 32u * item + 16u) = b[j];
         }
       } else {
-        // x[0 .. 7]: piece a, x[8 .. 15]: piece b, in fp32
-        float x[16];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float2 v = unpack2(w[i], r.bf16);
@@ -295,11 +296,11 @@ __global__ void __launch_bounds__(kThreads) kv_rope_rows(const __grid_constant__
             *reinterpret_cast<uint4*>(dst + at_b) = make_uint4(w[4], w[5], w[6], w[7]);
           }
         } else {
-          const bool apart = !kInter && rot;
           const float inv = sd.inv ? __ldg(sd.inv) : 1.0f;
 #pragma unroll
           for (int i = 0; i < 16; ++i) x[i] = __fmul_rn(x[i], inv);
           if constexpr (FMT == KV_CACHE_E4M3FN) {
+            const bool apart = !kInter && rot;
             uint32_t o[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[i] = e4m3x2(x[4 * i], x[4 * i + 1]) | (e4m3x2(x[4 * i + 2], x[4 * i + 3]) << 16);
@@ -311,37 +312,50 @@ __global__ void __launch_bounds__(kThreads) kv_rope_rows(const __grid_constant__
                 *reinterpret_cast<uint4*>(dst + 16u * item) = make_uint4(o[0], o[1], o[2], o[3]);
               }
             }
-          } else {
-            float ma = 0.0f, mb = 0.0f;
+          }
+        }
+      }
+      if constexpr (FMT == KV_CACHE_E2M1) {
+        // the lanes of a 16-bit row come here too, with nothing to write: the shuffles name every lane
+        const bool apart = !kInter && rot;
+        float ma = 0.0f, mb = 0.0f;
+        if (!plain) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              ma = fmaxf(ma, fabsf(x[i]));
-              mb = fmaxf(mb, fabsf(x[8 + i]));
-            }
-            // the other half of each block: the neighbour's where the pieces are apart, else the lane's own
-            const float na = __shfl_xor_sync(0xFFFFFFFFu, ma, 1), nb = __shfl_xor_sync(0xFFFFFFFFu, mb, 1);
-            const float fa = fmaxf(ma, apart ? na : mb), fb = apart ? fmaxf(mb, nb) : fa;
-            float ra, rb;
-            const uint32_t sa = fp4_block_scale(fa, &ra);
-            uint32_t sb = sa;
-            rb = ra;
-            if (apart) sb = fp4_block_scale(fb, &rb);
+          for (int i = 0; i < 8; ++i) {
+            ma = fmaxf(ma, fabsf(x[i]));
+            mb = fmaxf(mb, fabsf(x[8 + i]));
+          }
+        }
+        // the other half of each block: the neighbour's where the pieces are apart, else the lane's own
+        float fa = fmaxf(ma, mb), fb = fa;
+        if constexpr (!kInter) {
+          const float na = __shfl_xor_sync(0xFFFFFFFFu, ma, 1), nb = __shfl_xor_sync(0xFFFFFFFFu, mb, 1);
+          if (apart) {
+            fa = fmaxf(ma, na);
+            fb = fmaxf(mb, nb);
+          }
+        }
+        if (!plain) {
+          float ra, rb;
+          const uint32_t sa = fp4_block_scale(fa, &ra);
+          uint32_t sb = sa;
+          rb = ra;
+          if (apart) sb = fp4_block_scale(fb, &rb);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              x[i] = __fmul_rn(x[i], ra);
-              x[8 + i] = __fmul_rn(x[8 + i], rb);
-            }
-            const uint32_t ca = e2m1x8(x), cb = e2m1x8(x + 8);
-            if (live) {
-              uint8_t* sc = sd.scales + page * sd.sc_page + off * sd.sc_slot + static_cast<int64_t>(h) * sd.sc_head;
-              if (apart) {
-                *reinterpret_cast<uint32_t*>(dst + 4u * item) = ca;
-                *reinterpret_cast<uint32_t*>(dst + half / 2 + 4u * item) = cb;
-                sc[(item & 1u ? half / 16 : 0u) + item / 2] = static_cast<uint8_t>(item & 1u ? sb : sa);
-              } else {
-                *reinterpret_cast<uint2*>(dst + 8u * item) = make_uint2(ca, cb);
-                sc[item] = static_cast<uint8_t>(sa);
-              }
+          for (int i = 0; i < 8; ++i) {
+            x[i] = __fmul_rn(x[i], ra);
+            x[8 + i] = __fmul_rn(x[8 + i], rb);
+          }
+          const uint32_t ca = e2m1x8(x), cb = e2m1x8(x + 8);
+          if (live) {
+            uint8_t* sc = sd.scales + page * sd.sc_page + off * sd.sc_slot + static_cast<int64_t>(h) * sd.sc_head;
+            if (apart) {
+              *reinterpret_cast<uint32_t*>(dst + 4u * item) = ca;
+              *reinterpret_cast<uint32_t*>(dst + half / 2 + 4u * item) = cb;
+              sc[(item & 1u ? half / 16 : 0u) + item / 2] = static_cast<uint8_t>(item & 1u ? sb : sa);
+            } else {
+              *reinterpret_cast<uint2*>(dst + 8u * item) = make_uint2(ca, cb);
+              sc[item] = static_cast<uint8_t>(sa);
             }
           }
         }
