@@ -705,6 +705,13 @@ __global__ void __launch_bounds__(32 * kSplitWarps, (kSplitCtas<DP, NB>))
     return static_cast<uint32_t>(min(max(static_cast<int32_t>(row_bytes) - static_cast<int32_t>(g + 8 * i) * L::VC, 0), L::VC));
   };
 
+  // The scale code of a row's block. Blocks behind head_dim have none (their codes are 0; the bytes there,
+  // in the copied words, are another head's or key's, and may be NaN).
+  auto scale_of = [&](uint32_t block, uint32_t at) -> uint32_t {
+    const uint32_t x = ld_shared_u8(at);
+    return kExact || block < row_bytes / (kFp4Block / 2) ? x : 0u;
+  };
+
   for (int32_t share = static_cast<int32_t>(blockIdx.x); direct || share < sh_work.shares;) {
     int64_t pos = share, end = share + 1, base = 0;
     int32_t b = 0;
@@ -921,13 +928,14 @@ __global__ void __launch_bounds__(32 * kSplitWarps, (kSplitCtas<DP, NB>))
             sc[mb][rh] = 0u;
             if constexpr (FMT == KV_CACHE_E2M1) {
               const uint32_t srow = kat + TW * L::kRow + (mb * 16 + rh * 8 + g) * L::kScaleRow;
-              uint32_t sat = srow + (t + 4 * i) * (L::KD / kFp4Block);
+              const uint32_t block = (t + 4 * i) * (L::KD / kFp4Block);
+              uint32_t sat = srow + block;
               if (!kExact) sat += ld_shared_u32(srow + L::kScaleRow - 4);
               if (L::KD > kFp4Block && kExact) {
                 sc[mb][rh] = ld_shared_u16(sat);
               } else {
-                sc[mb][rh] = ld_shared_u8(sat);
-                if constexpr (L::KD > kFp4Block) sc[mb][rh] |= ld_shared_u8(sat + 1) << 8;
+                sc[mb][rh] = scale_of(block, sat);
+                if constexpr (L::KD > kFp4Block) sc[mb][rh] |= scale_of(block + 1, sat + 1) << 8;
               }
             }
           }
@@ -973,8 +981,10 @@ __global__ void __launch_bounds__(32 * kSplitWarps, (kSplitCtas<DP, NB>))
             ld_own<L::VC>(w[x], vat + (((mb * 4 + x) * L::VN + i) * 32 + lane) * L::VC);
             if constexpr (FMT == KV_CACHE_E2M1) {
 #pragma unroll
-              for (int y = 0; y < (L::VD + kFp4Block - 1) / kFp4Block; ++y)
-                sc[x >> 1][y] |= ld_shared_u8(srow[x] + (g + 8 * i) * L::VD / kFp4Block + y) << (8 * (x & 1));
+              for (int y = 0; y < (L::VD + kFp4Block - 1) / kFp4Block; ++y) {
+                const uint32_t block = (g + 8 * i) * L::VD / kFp4Block + y;
+                sc[x >> 1][y] |= scale_of(block, srow[x] + block) << (8 * (x & 1));
+              }
             }
           }
           v_products<FMT, DP, NB, kBF16>(o, w, sc, pt[mb], pl[mb], i * (L::VD / 2));

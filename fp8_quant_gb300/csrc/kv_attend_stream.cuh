@@ -80,7 +80,9 @@ struct StreamStep {
 // of an item's steps in a share: the first, the last; the share has all of them, or the item's first; no more steps
 constexpr int kFirst = 1, kLast = 2, kWhole = 4, kBegins = 8, kStop = 16;
 
-template <int FMT, int DP, int NB, bool kBF16>
+// kDimsFit (4-bit caches): head_dim is DP, so that every piece of a lane has its block scales (fp4_decode
+// 420 us; 456 with the other form's selection).
+template <int FMT, int DP, int NB, bool kBF16, bool kDimsFit>
 __global__ void __launch_bounds__(StreamLayout<FMT, DP, NB>::kThreads, 1)
     kv_attend_stream(const __grid_constant__ StreamParams sp) {
   using L = Layout<FMT, DP>;
@@ -304,6 +306,12 @@ __global__ void __launch_bounds__(StreamLayout<FMT, DP, NB>::kThreads, 1)
     };
     const uint32_t sc_row = static_cast<uint32_t>(p.hw) * ds;
     const uint32_t sc_at = S::kCodes + static_cast<uint32_t>(sub * TW) * sc_row + static_cast<uint32_t>(hl) * ds;
+    // The lane's block scales of a K and of a V row: where they are, and which bits count. A piece behind
+    // head_dim has none (its codes are 0; the next bytes are another head's or key's, and may be NaN).
+    const uint32_t k_block = t * (L::KD / kFp4Block), v_block = g * L::VD / kFp4Block;
+    const uint32_t k_sc = kDimsFit || k_block < ds ? k_block : 0u, k_bits = kDimsFit || k_block < ds ? 0xFFFFu : 0u;
+    const uint32_t v_sc = kDimsFit || v_block < ds ? v_block : 0u, v_bits = kDimsFit || v_block < ds ? 0xFFu : 0u;
+    static_assert(FMT != KV_CACHE_E2M1 || (L::KN == 1 && L::VN == 1 && L::VD <= kFp4Block), "a lane has one piece of a 4-bit row");
     float* const frag = reinterpret_cast<float*>(smem_ptr + S::kOffJoin);
 
     uint32_t qf[NB][QP];
@@ -383,8 +391,8 @@ __global__ void __launch_bounds__(StreamLayout<FMT, DP, NB>::kThreads, 1)
               ld_own<L::KC>(w[mb][rh], kat + mb_at(mb) + (L::kRow >= 128 ? i >> 1 : 0) * span_step + rh * 8 * W + piece);
               sc[mb][rh] = 0u;
               if constexpr (FMT == KV_CACHE_E2M1) {
-                const uint32_t at = scat + (mb * 16 + rh * 8) * sc_row + (L::kRow >= 128 ? 2u * t + i : t) * (L::KD / kFp4Block);
-                sc[mb][rh] = L::KD > kFp4Block ? ld_shared_u16(at) : ld_shared_u8(at);
+                const uint32_t at = scat + (mb * 16 + rh * 8) * sc_row + k_sc;
+                sc[mb][rh] = (L::KD > kFp4Block ? ld_shared_u16(at) : ld_shared_u8(at)) & k_bits;
               }
             }
           k_products<FMT, DP, NB, kBF16>(s, w, sc, qf, i * (L::KD / 2));
@@ -441,9 +449,8 @@ __global__ void __launch_bounds__(StreamLayout<FMT, DP, NB>::kThreads, 1)
                                                     : g * L::VC;
               ld_own<L::VC>(w[x], vat + mb_at(mb) + i * span_step + row * W + piece);
               if constexpr (FMT == KV_CACHE_E2M1) {
-                const uint32_t at = unit_at + sc_at + (mb * 16 + row) * sc_row + (g + 8 * i) * L::VD / kFp4Block;
-                sc[x >> 1][0] |= ld_shared_u8(at) << (8 * (x & 1));
-                if constexpr (L::VD > kFp4Block) sc[x >> 1][1] |= ld_shared_u8(at + 1) << (8 * (x & 1));
+                const uint32_t at = unit_at + sc_at + (mb * 16 + row) * sc_row + v_sc;
+                sc[x >> 1][0] |= (ld_shared_u8(at) & v_bits) << (8 * (x & 1));
               }
             }
             v_products<FMT, DP, NB, kBF16>(o, w, sc, pt[mb], pl[mb], i * (L::VD / 2));
@@ -520,10 +527,10 @@ __global__ void __launch_bounds__(StreamLayout<FMT, DP, NB>::kThreads, 1)
 // ---------------------------------------------------------------------------
 
 // Launches the kernel of one format and padded head dim.
-template <int FMT, int DP, int NB, bool kBF16>
+template <int FMT, int DP, int NB, bool kBF16, bool kDimsFit>
 kv_status launch_stream(StreamParams sp, void* work, int64_t work_bytes, int64_t max_keys, cudaStream_t stream) {
   using S = StreamLayout<FMT, DP, NB>;
-  auto* kernel = kv_attend_stream<FMT, DP, NB, kBF16>;
+  auto* kernel = kv_attend_stream<FMT, DP, NB, kBF16, kDimsFit>;
   static_assert(S::kTotal <= 227 * 1024 - 8 * 1024, "shared memory, with the static part");
   int sms = 0;
   kv_status st = current_sm_count(&sms);
@@ -541,8 +548,13 @@ kv_status launch_stream(StreamParams sp, void* work, int64_t work_bytes, int64_t
 template <int FMT, int DP, bool kBF16>
 kv_status launch_stream_dim(const StreamParams& sp, bool wide, void* work, int64_t work_bytes, int64_t max_keys,
                             cudaStream_t stream) {
-  return wide ? launch_stream<FMT, DP, 2, kBF16>(sp, work, work_bytes, max_keys, stream)
-              : launch_stream<FMT, DP, 1, kBF16>(sp, work, work_bytes, max_keys, stream);
+  if constexpr (FMT == KV_CACHE_E2M1) {
+    if (sp.s.a.head_dim != DP)
+      return wide ? launch_stream<FMT, DP, 2, kBF16, false>(sp, work, work_bytes, max_keys, stream)
+                  : launch_stream<FMT, DP, 1, kBF16, false>(sp, work, work_bytes, max_keys, stream);
+  }
+  return wide ? launch_stream<FMT, DP, 2, kBF16, true>(sp, work, work_bytes, max_keys, stream)
+              : launch_stream<FMT, DP, 1, kBF16, true>(sp, work, work_bytes, max_keys, stream);
 }
 
 template <int FMT, bool kBF16>

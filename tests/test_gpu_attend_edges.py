@@ -47,3 +47,23 @@ def test_slot_strides_beyond_28_bits(wide, nq, fmt):
         at += pages * H * W * eb
     assert at <= SLOT
     p.check(p.attend(d))
+
+
+@pytest.mark.parametrize("wide,nq", [(False, 1), (True, 1), (True, 3), (False, 40)])
+@pytest.mark.parametrize("D,H", [(32, 8), (96, 8), (96, 16), (80, 4), (112, 2), (48, 2), (160, 4)])
+def test_block_scales_next_to_a_row(D, H, wide, nq):
+    """NaN scales of another head or of a slot that no row sees leave every other row's bits as they are."""
+    p = AttendProblem([333, 64, 50, 1], [nq, 1, nq, 1], 2 * H, H, D, fmt="e2m1", page=32, seed=52)
+    d = tensors(p, wide)
+    want = p.attend(d)
+    p.check(want)
+    used = torch.from_numpy(p.used).cuda()[..., None, None]
+    clean = dict(d, ks=torch.where(used, d["ks"], 0), vs=torch.where(used, d["vs"], 0))
+    assert torch.equal(p.attend(clean).view(torch.int16), want.view(torch.int16))
+    dirty = dict(d, ks=d["ks"].clone(), vs=d["vs"].clone())
+    for n in ("ks", "vs"):
+        dirty[n][:, :, 1] = 0x7F
+    got = p.attend(dirty)
+    others = [h for h in range(2 * H) if h // 2 != 1]
+    assert torch.equal(got[:, others].view(torch.int16), want[:, others].view(torch.int16))
+    assert got[:, 2:4].isnan().all()
