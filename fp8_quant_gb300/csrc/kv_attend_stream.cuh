@@ -13,8 +13,10 @@
 //    the swizzle of TMA; the lanes' pieces of a row are chosen so that the eight (or
 //    sixteen) lanes that read together meet all banks: K pieces 2t and 2t + 1
 //    of a 128-byte row for lane (g, t), V piece g of rows 2t.
-//  * keys behind a sequence's end are not hidden from TMA: their scores are
-//    masked and their V rows (e2m1: scales) are zeroed in shared memory, by the warp
+//  * boxes in which no row sees a key (beside the sinks, before a window, behind
+//    the last query) are not copied, nor are their pages looked up; other keys behind a
+//    sequence's end are not hidden from TMA.  The scores of both are masked and
+//    their V rows (e2m1: scales) are zeroed in shared memory, by the warp
 //    that is about to use them.  Pages out of range are fetched as zeros.
 // Every wait has a limit; a CTA whose wait ran out counts that and leaves.
 //
@@ -217,11 +219,12 @@ __global__ void __launch_bounds__(StreamLayout<FMT, DP, NB>::kThreads, 1)
         const int32_t p_hi = p_first + static_cast<int32_t>(a.group.quot(static_cast<uint32_t>(row0 + nrows - 1)));
         const TileList list = visible_tiles<TW>(a, p_lo, p_hi);
         const int32_t* table = a.table + static_cast<int64_t>(b) * a.table_stride;
-        auto key_of = [&](int32_t step) -> int32_t {  // first key of the lane's box; -1: none
+        // First key of the lane's box; -1: none, or none that a row sees (its page may be gone).
+        auto key_of = [&](int32_t step) -> int32_t {
           const int32_t li = step * p.subs + sub;
           if (!mine || step >= step1 || li >= list.n) return -1;
           const int32_t k = list.tile(li) * TW + part * sp.box;
-          return k < seq.len ? k : -1;
+          return k > p_hi || (k >= a.sinks && k + sp.box <= list.lo_key) ? -1 : k;
         };
         int32_t key = key_of(step0);
         int32_t id = key >= 0 ? __ldg(table + a.page.quot(static_cast<uint32_t>(key))) : 0;
@@ -418,9 +421,10 @@ __global__ void __launch_bounds__(StreamLayout<FMT, DP, NB>::kThreads, 1)
       if (!ok) break;
       if (work) {
         const uint32_t unit_at = ring + vs * S::kUnit, vat = unit_at + head_at;
-        if (j0 + TW > seq.len) {
-          // rows behind the sequence's end may hold anything: a weight of 0 must not meet a NaN
-          for (int32_t r = seq.len - j0; r < TW; ++r) {
+        // Rows behind the sequence's end and in boxes that were not copied may hold anything, and a weight of 0
+        // must not meet a NaN: rows r0 .. r1 - 1 of the tile are cleared.
+        auto clear = [&](int32_t r0, int32_t r1) {
+          for (int32_t r = r0; r < r1; ++r) {
             if constexpr (FMT == KV_CACHE_E2M1) {
               for (uint32_t x = lane; x < ds; x += 32u)
                 asm volatile("st.shared.u8 [%0], %1;" ::"r"(unit_at + sc_at + static_cast<uint32_t>(r) * sc_row + x), "h"(static_cast<uint16_t>(0)) : "memory");
@@ -433,6 +437,13 @@ __global__ void __launch_bounds__(StreamLayout<FMT, DP, NB>::kThreads, 1)
                 }
             }
           }
+        };
+        const int32_t in_box = sp.box - 1;  // boxes are 16, 32 or 64 keys
+        const int32_t there = min(seq.len, (p_hi | in_box) + 1);                               // keys from here on are not,
+        const int32_t gap0 = (a.sinks + in_box) & ~in_box, gap1 = list.lo_key & ~in_box;       // nor those between these two
+        if (j0 + TW > there || (gap0 < gap1 && j0 < gap1 && j0 + TW > gap0)) {
+          clear(max(there - j0, 0), TW);
+          clear(max(gap0 - j0, 0), min(gap1 - j0, TW));
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before TMA fills the unit again
           __syncwarp();
         }

@@ -67,3 +67,45 @@ def test_block_scales_next_to_a_row(D, H, wide, nq):
     others = [h for h in range(2 * H) if h // 2 != 1]
     assert torch.equal(got[:, others].view(torch.int16), want[:, others].view(torch.int16))
     assert got[:, 2:4].isnan().all()
+
+
+def check_without_unseen_pages(p, wide):
+    """A window's freed pages: no count in the record, and the bits of a whole table. They hold NaN, too."""
+    d = tensors(p, wide)
+    err = torch.zeros(2, dtype=torch.int64, device="cuda")
+    want = p.attend(d, err=err)
+    table, gone = d["table"].clone(), 0
+    bare = {n: d[n].clone() for n in ("kc", "vc", "ks", "vs") if n in d}
+    for b, n in enumerate(p.lens):
+        seen = p.visible(b).any(0)
+        for i in range(-(-n // p.page)):
+            if not seen[i * p.page:(i + 1) * p.page].any():
+                table[b, i] = -1
+                gone += 1
+                for x in bare.values():
+                    x[p.table[b, i]] = float("nan") if x.dtype.is_floating_point else 0x7F
+    assert gone > 3
+    p.check(want)
+    got = p.attend(dict(d, table=table), err=err)
+    assert torch.equal(got.view(torch.int16), want.view(torch.int16))
+    assert not err.any()
+    assert torch.equal(p.attend(dict(d, **bare), err=err).view(torch.int16), want.view(torch.int16))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("page,window,sinks", [(16, 100, 4), (16, 40, 20), (32, 300, 1), (16, 64, 0), (64, 65, 70), (8, 33, 3)])
+@pytest.mark.parametrize("nq", [1, 3, 40])
+def test_pages_that_no_row_sees_may_be_gone(nq, page, window, sinks, D, fmt):
+    check_without_unseen_pages(AttendProblem([1000, 333, 64, 450], [nq, 1, 2, nq], 8, 4, D, fmt=fmt, page=page, window=window,
+                                             sinks=sinks, seed=53), False)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("page,window,sinks", [(16, 1040, 4), (16, 1041, 20), (32, 1100, 1), (48, 1077, 0), (64, 1030, 70)])
+@pytest.mark.parametrize("B,H,nq", [(64, 1, 1), (20, 8, 3)])
+def test_pages_of_long_windows_may_be_gone(B, H, nq, page, window, sinks, fmt):
+    """Windows of 8 MB and more together, of few rows each, as the TMA-fed kernels take them."""
+    lens = [1500 - 19 * (i % 23) for i in range(B)]
+    p = AttendProblem(lens, [nq, 1] * (B // 2), 2 * H if H == 1 else H, H, 128, fmt=fmt, page=page, window=window, sinks=sinks, seed=54)
+    check_without_unseen_pages(p, True)
