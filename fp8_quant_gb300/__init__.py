@@ -51,6 +51,7 @@ class KVStatus(enum.IntEnum):
     ERR_UNSUPPORTED = 2
     ERR_CUDA = 3
     ERR_INDEX_OOB = 4
+    ERR_WAIT = 5
 
 
 class KVError(RuntimeError):
@@ -543,12 +544,14 @@ def kv_store_fp8(k, v, k_cache, v_cache, indices, *, page_size: int = 1,
 
 
 def kv_error_poll(err=None, stream=None, device=None):
-    """Synchronise, read and clear an error record: (status, oob_count, first_bad_token)."""
+    """Synchronise, read and clear an error record: (status, oob_count, first_bad_token).
+
+    ``KVStatus.ERR_WAIT``: a kernel of :func:`kv_attend` gave up a wait; its outputs are not to be used."""
     import torch
     if err is None:
         err = _default_record(device or torch.device("cuda", torch.cuda.current_device()))
     rc, n, first = raw.kv_error_poll(err.data_ptr(), _stream_handle(stream, err.device))
-    if rc not in (KVStatus.OK, KVStatus.ERR_INDEX_OOB):
+    if rc not in (KVStatus.OK, KVStatus.ERR_INDEX_OOB, KVStatus.ERR_WAIT):
         raise KVError(rc, "kv_error_poll")
     return KVStatus(rc), n, first
 
@@ -1009,9 +1012,10 @@ def kv_attend(q, k_cache, v_cache, page_table, seq_lens, *, q_start=None, page_s
     (1-element fp32 device tensors, None: 1). ``lse``: an fp32 [tokens, HQ] tensor for the
     logarithms of the rows' sums, or None. ``work``: a device tensor that lets long sequences be
     split over the GPU (ATTEND_WORK_BYTES is always enough; its first ATTEND_HEAD_BYTES are zero
-    before its first use, and every call leaves them zero; calls that share one must not overlap; a
-    new one per call if None). Sequences with a bad length or page
-    id are counted in ``err``.
+    before its first use, and every call that completes leaves them zero; calls that share one must
+    not overlap; a new one per call if None). Sequences with a bad length or page id are counted in
+    ``err``; a kernel that gave up a wait sets it to ``KVStatus.ERR_WAIT`` (see :func:`kv_error_poll`),
+    and the outputs are not to be used.
     """
     import torch
     shape, dtype, qst = q.shape, q.dtype, q.stride()

@@ -66,10 +66,11 @@ struct ShareLevel {
 };
 constexpr int kLevels = 6;
 
-// The workspace's head: zero between calls.
+// The workspace's head: zero between calls that complete.
 struct SplitWork {
   unsigned int next;     // the shares that CTAs have taken beyond their first
-  unsigned int pad[63];
+  unsigned int gave_up;  // a CTA left before its shares were done (not reset here)
+  unsigned int pad[62];
   ShareLevel level[kLevels];
   int32_t levels, shares;  // in use
 };
@@ -1097,7 +1098,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) kv_attend_join(const __grid_c
   grid_handover();
   if (blockIdx.x == 0 && threadIdx.x == 0) p.head->next = 0u;
   int32_t b = tok, c0 = 0, c1 = 0, hl = 0, r = 0, pos = 0;
-  bool joined = false;
+  bool joined = false, lost = false;
   if (tok < a.num_q) {
     if (a.q_start) {
       int32_t lo = 0, hi = a.num_seqs - 1;
@@ -1120,6 +1121,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) kv_attend_join(const __grid_c
       c0 = share_of(p.head, s0);
       c1 = share_of(p.head, s0 + geom.steps - 1);
       joined = c0 != c1;
+      lost = p.head->gave_up != 0u;
     }
   }
   // all warps of a row agree on `joined`; with one warp a row there is no barrier below
@@ -1172,6 +1174,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) kv_attend_join(const __grid_c
       for (int i = 0; i < DP / 32; ++i) acc[i] = __fmaf_rn(acc[i], ea, sh[w][lane + 32 * i] * eb);
     }
   }
+  uint16_t* out = reinterpret_cast<uint16_t*>(a.out + tok * a.o_token + h * a.o_head);
+  if (lost) {  // parts are missing, or whole rows: NaN, whatever was computed
+    for (int32_t d = static_cast<int32_t>(lane); d < a.head_dim; d += 32) out[d] = 0x7FFFu;
+    if (a.lse && lane == 0u) a.lse[static_cast<int64_t>(tok) * a.q_heads + h] = __uint_as_float(0x7FFFFFFFu);
+    return;
+  }
   if (!joined) return;
   const float inv = __fdiv_rn(tensor_scale(a.v_scale), ll);
   bool fine = ll > 0.0f;
@@ -1181,7 +1189,6 @@ __global__ void __launch_bounds__(32 * kJoinWarps) kv_attend_join(const __grid_c
     attend_row<FMT, 8>(a, b, pos, tok, h);
     return;
   }
-  uint16_t* out = reinterpret_cast<uint16_t*>(a.out + tok * a.o_token + h * a.o_head);
 #pragma unroll
   for (int i = 0; i < DP / 32; ++i)
     if (static_cast<int32_t>(lane) + 32 * i < a.head_dim) out[lane + 32 * i] = round16(acc[i] * inv, a.bf16);

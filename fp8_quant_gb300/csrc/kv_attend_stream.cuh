@@ -18,7 +18,7 @@
 //    sequence's end are not hidden from TMA.  The scores of both are masked and
 //    their V rows (e2m1: scales) are zeroed in shared memory, by the warp
 //    that is about to use them.  Pages out of range are fetched as zeros.
-// Every wait has a limit; a CTA whose wait ran out counts that and leaves.
+// Every wait has a limit; a CTA whose wait ran out records that, for the join too, and leaves.
 //
 // Measured on one GB300 (one query a sequence, 32 over 8 heads of 128): 128
 // windows of 4,096 16-bit keys 317 us, 6.7 TB/s; 32 sequences of 16,000 - 32,768
@@ -530,7 +530,10 @@ __global__ void __launch_bounds__(StreamLayout<FMT, DP, NB>::kThreads, 1)
     }
   }
   __syncthreads();
-  if (tid == 0 && *failed != 0) record_oob(a.err, 0u);
+  if (tid == 0 && *failed != 0) {
+    record_wait(a.err);
+    if (p.split) p.head->gave_up = 1u;
+  }
 }
 
 // ---------------------------------------------------------------------------

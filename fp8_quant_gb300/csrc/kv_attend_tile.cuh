@@ -51,7 +51,7 @@
 // against 399 us); the next queries by the copying warps cost 5 % in windows.  Items of equal
 // length leave CTAs idle in the last round: 5.5 rounds of windows take 6.
 //
-// Every wait has a limit (kSpin); a CTA whose wait ran out counts that in the
+// Every wait has a limit (kSpin); a CTA whose wait ran out records that in the
 // error record, lets its copies and products end and leaves.
 #pragma once
 
@@ -951,7 +951,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
   }
   tc_fence_before();
   __syncthreads();
-  if (tid == 0 && *failed != 0) record_oob(a.err, 0u);
+  if (tid == 0 && *failed != 0) record_wait(a.err);
   if (warp == 8) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");

@@ -217,6 +217,11 @@ __device__ __forceinline__ void record_oob(kv_error_record* err, uint64_t t) {
             static_cast<unsigned long long>(~t));
 }
 
+// A wait of the running kernel ran out: its call's outputs are not to be used.
+__device__ __forceinline__ void record_wait(kv_error_record* err) {
+  atomicOr(reinterpret_cast<unsigned long long*>(&err->oob_count), static_cast<unsigned long long>(KV_ERROR_WAIT_BIT));
+}
+
 // Unit u -> (token, K|V, segment, part).
 struct UnitShape {
   uint64_t num_units;        // num_tokens * units_per_token

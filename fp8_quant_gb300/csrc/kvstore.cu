@@ -921,10 +921,12 @@ extern "C" kv_status kv_error_poll(kv_error_record* d_err, kv_stream_t stream_, 
   if (e != cudaSuccess) return cuda_fail(e);
   e = cudaStreamSynchronize(stream);
   if (e != cudaSuccess) return cuda_fail(e);
+  const bool gave_up = (h.oob_count & KV_ERROR_WAIT_BIT) != 0;
+  h.oob_count &= ~KV_ERROR_WAIT_BIT;
   if (oob_count) *oob_count = static_cast<int64_t>(h.oob_count);
   if (first_bad_token)
     *first_bad_token = h.oob_count ? static_cast<int64_t>(~h.first_bad_key) : int64_t{-1};
-  return h.oob_count ? KV_ERR_INDEX_OOB : KV_OK;
+  return gave_up ? KV_ERR_WAIT : h.oob_count ? KV_ERR_INDEX_OOB : KV_OK;
 }
 
 namespace kvimpl {
@@ -999,6 +1001,7 @@ extern "C" const char* kv_status_str(kv_status status) {
     case KV_ERR_UNSUPPORTED: return "KV_ERR_UNSUPPORTED";
     case KV_ERR_CUDA: return "KV_ERR_CUDA";
     case KV_ERR_INDEX_OOB: return "KV_ERR_INDEX_OOB";
+    case KV_ERR_WAIT: return "KV_ERR_WAIT";
   }
   return "KV_STATUS_UNKNOWN";
 }

@@ -162,7 +162,7 @@ def generate(prompts=(1, 77, 300, 1023), steps=8, q_heads=32, kv_heads=8, dim=12
         outs.append(step().clone())
     status, bad, _ = kv.kv_error_poll(layer.err)
     if status != kv.KVStatus.OK or bad:
-        raise RuntimeError(f"{bad} tokens or sequences out of range")
+        raise RuntimeError(f"{kv.kv_status_str(status)}: {bad} tokens or sequences out of range")
     return layer, step, outs, rows
 
 

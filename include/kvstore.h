@@ -69,7 +69,8 @@ typedef enum kv_status {
     KV_ERR_INVALID_ARG = 1,  /* bad argument found on the host; nothing was launched */
     KV_ERR_UNSUPPORTED = 2,  /* legal request this library does not implement; nothing launched */
     KV_ERR_CUDA = 3,         /* a CUDA runtime call failed; see kv_last_cuda_error() */
-    KV_ERR_INDEX_OOB = 4     /* kv_error_poll: at least one token had an out-of-range slot */
+    KV_ERR_INDEX_OOB = 4,    /* kv_error_poll: at least one token had an out-of-range slot */
+    KV_ERR_WAIT = 5          /* kv_error_poll: a kernel gave up a wait; outputs of its call are not to be used */
 } kv_status;
 
 typedef enum kv_index_dtype { KV_INDEX_I32 = 0, KV_INDEX_I64 = 1 } kv_index_dtype;
@@ -92,8 +93,10 @@ typedef struct kv_strides {
  * zero-initialised before first use, e.g. with cudaMemsetAsync or
  * kv_error_reset).  Kernels only add to it; kv_error_poll reads and clears it.
  * Calls that share one record on different streams share its counts. */
+#define KV_ERROR_WAIT_BIT (1ull << 63)
 typedef struct kv_error_record {
-    uint64_t oob_count;      /* tokens skipped because their slot was out of range */
+    uint64_t oob_count;      /* tokens skipped because their slot was out of range; KV_ERROR_WAIT_BIT
+                              * beside them when a kernel of kv_attend gave up a wait */
     uint64_t first_bad_key;  /* bitwise NOT of the lowest skipped token; 0 if none */
 } kv_error_record;
 
@@ -560,8 +563,12 @@ typedef struct kv_attend_strides {
  *               Without it each block of query rows of one KV head is one
  *               CTA's work.  Its first KV_ATTEND_HEAD_BYTES are zero before its
  *               first use, and zero again after every call that completes
- *               (zero them after a KV_ERR_CUDA); the rest may hold anything.
+ *               (zero them after a KV_ERR_CUDA or KV_ERR_WAIT); the rest may
+ *               hold anything.
  *               Calls sharing one workspace must not overlap on the GPU.
+ * Waits inside the kernels have a limit, far beyond any that ends.  A CTA whose
+ * wait ran out leaves rows unwritten, and kv_error_poll returns KV_ERR_WAIT; a
+ * call that splits sequences gives NaN for all its rows then.
  * All pointers are device memory; q, out, the caches, the table and the lengths
  * are rejected with KV_ERR_INVALID_ARG where CUDA does not know them.  The
  * result does not depend on the order in which CTAs run; it may differ in rounding with the workspace's size.
@@ -637,7 +644,8 @@ kv_status kv_store_noalloc(const void *k, const void *v, void *k_cache, void *v_
  * (The pages trap inside the kernel on a bad slot; this library reports it
  * here instead.)  Writes the number of skipped tokens and the lowest skipped
  * token (-1 if none) to the optional host outputs.  Returns KV_OK when no
- * token was skipped, KV_ERR_INDEX_OOB when one was, KV_ERR_INVALID_ARG for a
+ * token was skipped, KV_ERR_INDEX_OOB when one was, KV_ERR_WAIT when a kernel
+ * gave up a wait (whether or not one was), KV_ERR_INVALID_ARG for a
  * NULL or misaligned record, KV_ERR_CUDA if a CUDA call failed (including an
  * earlier asynchronous error surfaced by the synchronisation).
  * Not capturable in a CUDA graph (it synchronises).

@@ -1,0 +1,48 @@
+"""What a caller learns of a wait that ran out in an attention kernel, and that none does while a CTA is at work."""
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from attncheck import AttendProblem
+
+pytestmark = pytest.mark.gpu
+
+FMTS = (None, "e4m3fn", "e2m1")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    import __graft_entry__
+    __graft_entry__.build()
+    yield
+
+
+@pytest.mark.parametrize("skipped", [0, 3])
+def test_the_record_tells_a_wait_from_an_index(skipped):
+    import fp8_quant_gb300 as kv
+    err = kv.error_record()
+    err[0] = skipped - 2 ** 63
+    err[1] = ~5 if skipped else 0
+    assert kv.kv_error_poll(err) == (kv.KVStatus.ERR_WAIT, skipped, 5 if skipped else -1)
+    assert kv.kv_error_poll(err) == (kv.KVStatus.OK, 0, -1)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("long", [False, True])
+def test_a_split_call_that_lost_a_part_gives_nan(long, fmt):
+    """The mark that a CTA leaves in the workspace's head, set beforehand: no row is made of parts that may be missing."""
+    import fp8_quant_gb300 as kv
+    p = AttendProblem([3000, 70], [1, 2], 8, 2, 128, fmt=fmt, seed=61)
+    d = p.tensors(torch.device("cuda"))
+    if long:    # a table row long enough for the TMA-fed kernels
+        t = d["table"]
+        d["table"] = torch.full((2, 60000 // p.page), -1, dtype=torch.int32, device="cuda")
+        d["table"][:, :t.shape[1]] = t
+    work = torch.zeros(kv.ATTEND_WORK_BYTES, dtype=torch.uint8, device="cuda")
+    lse = torch.zeros(3, 8, device="cuda")
+    p.check(p.attend(d, work=work, lse=lse), lse)
+    work.view(torch.int32)[1] = 1
+    assert p.attend(d, work=work, lse=lse).isnan().all() and lse.isnan().all()
+    work[:kv.ATTEND_HEAD_BYTES] = 0
+    p.check(p.attend(d, work=work, lse=lse), lse)
