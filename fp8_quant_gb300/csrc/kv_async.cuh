@@ -8,7 +8,9 @@
 
 namespace kvimpl {
 
-constexpr uint32_t kSpin = 1u << 24;  // tries of a wait: far beyond any that ends
+// Tries of a wait, of 2 us and more each: 2 to 4 s, where no warp's work between two barriers takes a
+// millisecond but attend_row's, for which waits stand still (WaitState).
+constexpr uint32_t kSpin = 1u << 20;
 
 __device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
@@ -46,13 +48,25 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
   return ok != 0u;
 }
 
+// A CTA's waits, in shared memory.
+struct WaitState {
+  int failed;  // a wait ran out
+  int held;    // warps at work that may take any time (a row's keys one by one): tries are not counted meanwhile
+
+  __device__ __forceinline__ bool ran_out() const { return *const_cast<const volatile int*>(&failed) != 0; }
+  __device__ __forceinline__ void hold(int more) { atomicAdd(&held, more); }
+};
+
 // False when the wait ran out here or anywhere in the CTA.
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* failed) {
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, WaitState* state) {
   for (uint32_t i = 0; i < kSpin; ++i) {
     if (bar_try(bar, parity)) return true;
-    if ((i & 1023u) == 1023u && *failed != 0) return false;
+    if ((i & 1023u) == 1023u) {
+      if (state->ran_out()) return false;
+      if (*const_cast<volatile int*>(&state->held) != 0) i = 0;
+    }
   }
-  *failed = 1;
+  *const_cast<volatile int*>(&state->failed) = 1;
   return false;
 }
 

@@ -48,6 +48,7 @@
 
 #include <atomic>
 
+#include "kv_async.cuh"
 #include "kv_attend.cuh"
 #include "kv_host.h"
 
@@ -536,7 +537,8 @@ __device__ __forceinline__ int out_dim(int i) {
 // The rows of an item that one warp has whole.
 template <int FMT, int DP, int NB, int OM>
 __device__ __forceinline__ void write_rows(const AttendParams& a, int32_t b, const AttendSeq& seq, int32_t kvh, int32_t row0, int32_t nrows,
-                                           float vscale, const float (&o)[NB][OM][4], const float (&m)[NB][2], const float (&l)[NB][2]) {
+                                           float vscale, const float (&o)[NB][OM][4], const float (&m)[NB][2], const float (&l)[NB][2],
+                                           WaitState* waits = nullptr) {
   const uint32_t lane = threadIdx.x & 31u, g = lane >> 2, t = lane & 3u;
   const int32_t G = static_cast<int32_t>(a.group.d);
   uint32_t again = 0u;  // rows to be done once more, a bit each
@@ -569,6 +571,8 @@ __device__ __forceinline__ void write_rows(const AttendParams& a, int32_t b, con
       }
     }
   again = __reduce_or_sync(0xFFFFFFFFu, again);
+  const bool hold = waits != nullptr && again != 0u && lane == 0u;
+  if (hold) waits->hold(1);
   while (again != 0u) {
     const int32_t r = __ffs(static_cast<int>(again)) - 1;
     again &= again - 1u;
@@ -576,6 +580,7 @@ __device__ __forceinline__ void write_rows(const AttendParams& a, int32_t b, con
     attend_row<FMT, 8>(a, b, seq.len - seq.nq + static_cast<int32_t>(qi), seq.q0 + static_cast<int32_t>(qi),
                        kvh * G + (row0 + r - static_cast<int32_t>(qi) * G));
   }
+  if (hold) waits->hold(-1);
 }
 
 // The sums of a part of an item, from row `at` of the workspace on.

@@ -94,7 +94,8 @@ __global__ void __launch_bounds__(StreamLayout<FMT, DP, NB>::kThreads, 1)
   __shared__ int64_t sh_scan[S::kThreads / 32];
   __shared__ int64_t sh_excl[S::kThreads + 1];  // first step of each thread's sequences; the total
   __shared__ SplitWork sh_work;
-  __shared__ volatile int sh_failed, sh_bad;
+  __shared__ WaitState sh_waits;
+  __shared__ volatile int sh_bad;
 
   const SplitParams& p = sp.s;
   const AttendParams& a = p.a;
@@ -110,7 +111,7 @@ __global__ void __launch_bounds__(StreamLayout<FMT, DP, NB>::kThreads, 1)
       bar_init(empty + 8 * i, S::kWarps);
     }
     bar_init(join_bar, S::kWarps);
-    sh_failed = 0;
+    sh_waits = WaitState{0, 0};
     sh_bad = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -159,7 +160,7 @@ __global__ void __launch_bounds__(StreamLayout<FMT, DP, NB>::kThreads, 1)
     }
   }
   __syncthreads();
-  volatile int* const failed = &sh_failed;
+  WaitState* const waits = &sh_waits;
   const int32_t G = static_cast<int32_t>(a.group.d);
 
   // (all warps of a warpgroup execute the same one)
@@ -178,7 +179,7 @@ __global__ void __launch_bounds__(StreamLayout<FMT, DP, NB>::kThreads, 1)
     uint32_t unit = 0u;
     bool ok = true;
     auto wait_empty = [&](uint32_t u) {
-      if (ok && u >= S::kUnits) ok = __all_sync(0xFFFFFFFFu, bar_wait(empty + 8 * (u % S::kUnits), (u / S::kUnits - 1) & 1u, failed));
+      if (ok && u >= S::kUnits) ok = __all_sync(0xFFFFFFFFu, bar_wait(empty + 8 * (u % S::kUnits), (u / S::kUnits - 1) & 1u, waits));
     };
     const int32_t shares = sh_work.shares;
     int32_t share = static_cast<int32_t>(blockIdx.x);
@@ -327,12 +328,12 @@ __global__ void __launch_bounds__(StreamLayout<FMT, DP, NB>::kThreads, 1)
     auto join_wait = [&] {
       __syncwarp();
       if (lane == 0u) bar_arrive(join_bar);
-      if (ok) ok = __all_sync(0xFFFFFFFFu, bar_wait(join_bar, joins & 1u, failed));
+      if (ok) ok = __all_sync(0xFFFFFFFFu, bar_wait(join_bar, joins & 1u, waits));
       ++joins;
     };
     for (uint32_t n = 0u; ok; ++n) {
       const uint32_t ks = (2u * n) % S::kUnits, vs = (2u * n + 1u) % S::kUnits;
-      ok = __all_sync(0xFFFFFFFFu, bar_wait(full + 8 * ks, ((2u * n) / S::kUnits) & 1u, failed));
+      ok = __all_sync(0xFFFFFFFFu, bar_wait(full + 8 * ks, ((2u * n) / S::kUnits) & 1u, waits));
       if (!ok) break;
       const volatile StreamStep& d = steps[ks];
       const int32_t flags = d.flags, step = d.step;
@@ -406,7 +407,7 @@ __global__ void __launch_bounds__(StreamLayout<FMT, DP, NB>::kThreads, 1)
         if (bad || !(j0 + TW - 1 <= p_lo && (a.window == 0 || j0 > p_hi - a.window || j0 + TW - 1 < a.sinks)))
           hide_scores<NB, MB>(a, a.table + static_cast<int64_t>(b) * a.table_stride, j0, p_hi, bad, seq.len - seq.nq, row0, gk, s);
         if constexpr (FMT == KV_CACHE_E2M1) {  // before the softmax, for one stretch of code without a wait
-          ok = __all_sync(0xFFFFFFFFu, bar_wait(full + 8 * vs, ((2u * n + 1u) / S::kUnits) & 1u, failed));
+          ok = __all_sync(0xFFFFFFFFu, bar_wait(full + 8 * vs, ((2u * n + 1u) / S::kUnits) & 1u, waits));
           if (!ok) break;
         }
         softmax_step<FMT, NB, MB, OM, kBF16>(s, rs, m, l, o, pt, pl);
@@ -417,7 +418,7 @@ __global__ void __launch_bounds__(StreamLayout<FMT, DP, NB>::kThreads, 1)
 
       // O^T += V^T P^T
       if (FMT != KV_CACHE_E2M1 || !work)
-        ok = __all_sync(0xFFFFFFFFu, bar_wait(full + 8 * vs, ((2u * n + 1u) / S::kUnits) & 1u, failed));
+        ok = __all_sync(0xFFFFFFFFu, bar_wait(full + 8 * vs, ((2u * n + 1u) / S::kUnits) & 1u, waits));
       if (!ok) break;
       if (work) {
         const uint32_t unit_at = ring + vs * S::kUnit, vat = unit_at + head_at;
@@ -521,7 +522,7 @@ __global__ void __launch_bounds__(StreamLayout<FMT, DP, NB>::kThreads, 1)
       }
       if (ok && used && sub == 0) {
         if ((flags & kWhole) != 0) {
-          write_rows<FMT, DP, NB>(a, b, seq, kvh, row0, nrows, vscale, o, m, l);
+          write_rows<FMT, DP, NB>(a, b, seq, kvh, row0, nrows, vscale, o, m, l, waits);
         } else {
           // a part that begins its item is the second of its share, one that does not the first
           write_part<FMT, DP, NB>(p, (static_cast<int64_t>(2 * share + ((flags & kBegins) != 0 ? 1 : 0)) * p.hw + hl) * p.part_rows, nrows, o, m, l);
@@ -530,7 +531,7 @@ __global__ void __launch_bounds__(StreamLayout<FMT, DP, NB>::kThreads, 1)
     }
   }
   __syncthreads();
-  if (tid == 0 && *failed != 0) {
+  if (tid == 0 && waits->ran_out()) {
     record_wait(a.err);
     if (p.split) p.head->gave_up = 1u;
   }

@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
   using S = TileSmem<FMT, DP>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ uint32_t sh_tmem;
-  __shared__ volatile int sh_failed;  // a wait ran out
+  __shared__ WaitState sh_waits;
   __shared__ volatile int sh_bad;     // a page id out of range was met: the CTA's rows are done again
   __shared__ TileItem sh_item[2];     // the item of an odd and of an even round, for the softmax warps
 
@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
       bar_init(raw_empty + 8 * i, S::kFillers / 32);
     }
     bar_init(done, 1);
-    sh_failed = 0;
+    sh_waits = WaitState{0, 0};
     sh_bad = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh_tmem;
-  volatile int* const failed = &sh_failed;
+  WaitState* const state = &sh_waits;
   grid_handover();
   if (blockIdx.x == 0 && warp == 15)  // lengths out of range, once
     for (int32_t b = static_cast<int32_t>(lane); b < a.num_seqs; b += 32) attend_seq(a, b, true);
@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
     const uint32_t s_at = tmem + lanes + t * 128, o_at = tmem + lanes + 256 + t * DP;
     bool ok = true;
     auto take_item = [&](int32_t round, TileItem* x) {
-      ok = __all_sync(0xFFFFFFFFu, bar_wait(item_full + 8 * (round & 1), static_cast<uint32_t>(round >> 1) & 1u, failed));
+      ok = __all_sync(0xFFFFFFFFu, bar_wait(item_full + 8 * (round & 1), static_cast<uint32_t>(round >> 1) & 1u, state));
       if (!ok) return;
       *x = sh_item[round & 1];
       __syncwarp();
@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
       // positions of the tile's rows
       const int32_t t_lo = it.p_first + t * p.qpt, t_hi = min(t_lo + p.qpt - 1, it.p_hi);
       for (int32_t j = 0; live && j < it.list.n; ++j) {
-        ok = __all_sync(0xFFFFFFFFu, bar_wait(s_full + 8 * t, waits & 1u, failed));
+        ok = __all_sync(0xFFFFFFFFu, bar_wait(s_full + 8 * t, waits & 1u, state));
         if (!ok) break;
         tc_fence_after();
         uint32_t sw[kTileKeys];
@@ -539,7 +539,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
       if (t < it.tiles) {
         bool fine = l > 0.0f;
         if (live) {
-          ok = __all_sync(0xFFFFFFFFu, bar_wait(o_full + 8 * t, items & 1u, failed));
+          ok = __all_sync(0xFFFFFFFFu, bar_wait(o_full + 8 * t, items & 1u, state));
           if (!ok) break;
           ++items;
           tc_fence_after();
@@ -585,12 +585,15 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
             a.lse[static_cast<int64_t>(tok) * a.q_heads + h] = (m + log2f(l)) * 0.6931471805599453f;
         }
         uint32_t again = __ballot_sync(0xFFFFFFFFu, mine && (!fine || sh_bad != 0));
+        const bool hold = again != 0u && lane == 0u;
+        if (hold) state->hold(1);
         while (again != 0u) {
           const int src = __ffs(static_cast<int>(again)) - 1;
           again &= again - 1u;
           attend_row<FMT, 8>(a, it.b, __shfl_sync(0xFFFFFFFFu, pos, src), __shfl_sync(0xFFFFFFFFu, tok, src),
                              __shfl_sync(0xFFFFFFFFu, h, src));
         }
+        if (hold) state->hold(-1);
       }
       it = next;
     }
@@ -601,7 +604,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
     const uint32_t qk_desc = instr_desc(kBF16, false, kTileKeys), pv_desc = instr_desc(kBF16, true, DP);
     bool ok = true;
     auto wait = [&](uint32_t bar, uint32_t parity) {
-      if (ok) ok = __all_sync(0xFFFFFFFFu, bar_wait(bar, parity, failed));
+      if (ok) ok = __all_sync(0xFFFFFFFFu, bar_wait(bar, parity, state));
       if (ok) tc_fence_after();
     };
     // descriptors of the operands' first pieces; the others are constant steps (in 16 bytes) away
@@ -689,7 +692,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
     bool ok = true;
     uint32_t unit = 0u;  // ring units that went by
     auto wait_empty = [&](uint32_t u) {
-      if (ok && u >= S::kUnits) ok = __all_sync(0xFFFFFFFFu, bar_wait(empty + 8 * (u % S::kUnits), (u / S::kUnits - 1) & 1u, failed));
+      if (ok && u >= S::kUnits) ok = __all_sync(0xFFFFFFFFu, bar_wait(empty + 8 * (u % S::kUnits), (u / S::kUnits - 1) & 1u, state));
     };
     // Which of the lane's keys of a tile a row needs, a bit each, and their pages.  What is loaded
     // is not looked at before it is used, a tile later (a select behind a load would wait for it),
@@ -842,7 +845,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
         skip_empty();
         if (have) look();
         const uint32_t u = 2u * tile + static_cast<uint32_t>(kv), raw = u % S::kRaws;
-        if (u >= S::kRaws) ok = __all_sync(0xFFFFFFFFu, bar_wait(raw_empty + 8 * raw, (u / S::kRaws - 1u) & 1u, failed));
+        if (u >= S::kRaws) ok = __all_sync(0xFFFFFFFFu, bar_wait(raw_empty + 8 * raw, (u / S::kRaws - 1u) & 1u, state));
         if (!ok) break;
         const uint32_t at = smem + S::kOffRaw + raw * S::kRawTile;
         const uint8_t* const base = kv ? a.v + kvh * a.v_head : a.k + kvh * a.k_head;
@@ -904,7 +907,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
         for (int32_t left = 2 * it.list.n; left > 0 && ok; --left, ++unit) {
           const uint32_t raw = unit % S::kRaws, from = smem + S::kOffRaw + raw * S::kRawTile;
           uint32_t w[S::kPer][kWords], sc[FMT == KV_CACHE_E2M1 ? S::kPer : 1];
-          ok = __all_sync(0xFFFFFFFFu, bar_wait(raw_full + 8 * raw, (unit / S::kRaws) & 1u, failed));
+          ok = __all_sync(0xFFFFFFFFu, bar_wait(raw_full + 8 * raw, (unit / S::kRaws) & 1u, state));
           if (!ok) break;
 #pragma unroll
           for (int i = 0; i < S::kPer; ++i) {
@@ -951,7 +954,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
   }
   tc_fence_before();
   __syncthreads();
-  if (tid == 0 && *failed != 0) record_wait(a.err);
+  if (tid == 0 && state->ran_out()) record_wait(a.err);
   if (warp == 8) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");

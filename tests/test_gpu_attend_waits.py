@@ -46,3 +46,25 @@ def test_a_split_call_that_lost_a_part_gives_nan(long, fmt):
     assert p.attend(d, work=work, lse=lse).isnan().all() and lse.isnan().all()
     work[:kv.ATTEND_HEAD_BYTES] = 0
     p.check(p.attend(d, work=work, lse=lse), lse)
+
+
+def test_no_wait_runs_out_while_rows_are_done_again():
+    """A NaN that every row sees has them done key by key, for seconds here: longer than any wait may last,
+    and the CTA's next item waits all that time. (Which CTA has two items: as many blocks as SMs and more.)"""
+    import numpy as np
+    import fp8_quant_gb300 as kv
+    lens = [64] * 200
+    lens[120] = 200_000
+    p = AttendProblem(lens, [40] * 200, 4, 1, 128, fmt="e4m3fn", page=64, seed=62)
+    p.value[1][p.table[120, 0], 0] = np.nan
+    p.cache[1][p.table[120, 0], 0] = 0x7F
+    d = p.tensors(torch.device("cuda"))
+    err = kv.error_record()
+    out = torch.full_like(d["q"], 7.0)
+    start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    start.record()
+    p.attend(d, out=out, err=err)
+    end.record()
+    assert kv.kv_error_poll(err) == (kv.KVStatus.OK, 0, -1)
+    p.check(out)
+    assert start.elapsed_time(end) > 2300      # it did take longer than a wait may
