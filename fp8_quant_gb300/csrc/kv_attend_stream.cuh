@@ -79,8 +79,9 @@ struct StreamStep {
   int32_t b, item, step, flags;
   int32_t share, pad[3];
 };
-// of an item's steps in a share: the first, the last; the share has all of them, or the item's first; no more steps
-constexpr int kFirst = 1, kLast = 2, kWhole = 4, kBegins = 8, kStop = 16;
+// of an item's steps in a share: the first, the last; the share has all of them, or the item's first; no more
+// steps; a page id of the step's is out of range
+constexpr int kFirst = 1, kLast = 2, kWhole = 4, kBegins = 8, kStop = 16, kBadPage = 32;
 
 // kDimsFit (4-bit caches): head_dim is DP, so that every piece of a lane has its block scales (fp4_decode
 // 420 us; 456 with the other form's selection).
@@ -95,7 +96,6 @@ __global__ void __launch_bounds__(StreamLayout<FMT, DP, NB>::kThreads, 1)
   __shared__ int64_t sh_excl[S::kThreads + 1];  // first step of each thread's sequences; the total
   __shared__ SplitWork sh_work;
   __shared__ WaitState sh_waits;
-  __shared__ volatile int sh_bad;
 
   const SplitParams& p = sp.s;
   const AttendParams& a = p.a;
@@ -112,7 +112,6 @@ __global__ void __launch_bounds__(StreamLayout<FMT, DP, NB>::kThreads, 1)
     }
     bar_init(join_bar, S::kWarps);
     sh_waits = WaitState{0, 0};
-    sh_bad = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   grid_handover();
@@ -233,15 +232,15 @@ __global__ void __launch_bounds__(StreamLayout<FMT, DP, NB>::kThreads, 1)
           const bool has = key >= 0;
           const uint32_t boxes = static_cast<uint32_t>(__popc(__ballot_sync(0xFFFFFFFFu, has)));
           int32_t page = id;
-          if (has && (id < 0 || id >= a.num_pages)) {
+          const bool bad = has && (id < 0 || id >= a.num_pages);
+          if (bad) {
             page = a.num_pages;  // outside the map: zeros
-            sh_bad = 1;
             record_oob(a.err, static_cast<uint64_t>(b));
           }
+          const bool any_bad = __any_sync(0xFFFFFFFFu, bad);
           const uint32_t in_page = has ? static_cast<uint32_t>(key) - a.page.quot(static_cast<uint32_t>(key)) * a.page.d : 0u;
           key = key_of(step + 1);
           id = key >= 0 ? __ldg(table + a.page.quot(static_cast<uint32_t>(key))) : 0;
-          __syncwarp();  // sh_bad before the arrival
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {
             const uint32_t u = unit + kv, slot = u % S::kUnits, bar = full + 8 * slot, at = ring + slot * S::kUnit;
@@ -253,7 +252,7 @@ __global__ void __launch_bounds__(StreamLayout<FMT, DP, NB>::kThreads, 1)
                 d.b = b;
                 d.item = item;
                 d.step = step;
-                d.flags = (step == step0 ? kFirst : 0) | (step == step1 - 1 ? kLast : 0) | (s_out - s_in == unit_steps ? kWhole : 0) | (step0 == 0 ? kBegins : 0);
+                d.flags = (step == step0 ? kFirst : 0) | (step == step1 - 1 ? kLast : 0) | (s_out - s_in == unit_steps ? kWhole : 0) | (step0 == 0 ? kBegins : 0) | (any_bad ? kBadPage : 0);
                 d.share = share;
               }
               bar_arrive_expect(bar, boxes * (S::kSpans * box_bytes + sc_bytes));
@@ -403,7 +402,7 @@ __global__ void __launch_bounds__(StreamLayout<FMT, DP, NB>::kThreads, 1)
         }
         __syncwarp();
         if (lane == 0u) bar_arrive(empty + 8 * ks);
-        const bool bad = sh_bad != 0;
+        const bool bad = (flags & kBadPage) != 0;
         if (bad || !(j0 + TW - 1 <= p_lo && (a.window == 0 || j0 > p_hi - a.window || j0 + TW - 1 < a.sinks)))
           hide_scores<NB, MB>(a, a.table + static_cast<int64_t>(b) * a.table_stride, j0, p_hi, bad, seq.len - seq.nq, row0, gk, s);
         if constexpr (FMT == KV_CACHE_E2M1) {  // before the softmax, for one stretch of code without a wait

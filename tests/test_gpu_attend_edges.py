@@ -109,3 +109,27 @@ def test_pages_of_long_windows_may_be_gone(B, H, nq, page, window, sinks, fmt):
     lens = [1500 - 19 * (i % 23) for i in range(B)]
     p = AttendProblem(lens, [nq, 1] * (B // 2), 2 * H if H == 1 else H, H, 128, fmt=fmt, page=page, window=window, sinks=sinks, seed=54)
     check_without_unseen_pages(p, True)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("B,nq,wide", [(200, 40, False), (200, 1, True)])
+def test_a_bad_page_is_its_own_sequences_matter(B, nq, wide, fmt):
+    """Sequences without a bad page keep their bits, whatever a CTA met before them; the others' keys there are hidden."""
+    import numpy as np
+    import fp8_quant_gb300 as kv
+    p = AttendProblem([64 + i % 3 for i in range(B)], [nq] * B, 4, 1, 128, fmt=fmt, page=16, seed=55)
+    d = tensors(p, wide)
+    want = p.attend(d)
+    bad = list(range(0, B, 3)) + list(range(104, 152))      # first items of CTAs that have two, among them
+    table = d["table"].clone()
+    table[bad, 1] = -1
+    err = kv.error_record()
+    got = p.attend(dict(d, table=table), err=err)
+    status, n, first = kv.kv_error_poll(err)
+    assert status == kv.KVStatus.ERR_INDEX_OOB and n >= len(set(bad)) and first == 0
+    good = [i for i in range(B) if i not in bad]
+    assert torch.equal(got.view(B, nq, 4, 128)[good].view(torch.int16), want.view(B, nq, 4, 128)[good].view(torch.int16))
+    see = p.visible
+    hide = lambda n: (np.arange(n) < 16) | (np.arange(n) >= 32)   # noqa: E731
+    p.visible = lambda b: see(b) & hide(p.lens[b]) if b in bad else see(b)
+    p.check(got)
