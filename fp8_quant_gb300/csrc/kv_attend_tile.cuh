@@ -592,6 +592,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
         uint32_t again = __ballot_sync(0xFFFFFFFFu, mine && (!fine || bad));
         const bool hold = again != 0u && lane == 0u;
         if (hold) state->hold(1);
+        __syncwarp();  // other lanes write these rows and their sums now (a vote orders no memory)
         while (again != 0u) {
           const int src = __ffs(static_cast<int>(again)) - 1;
           again &= again - 1u;

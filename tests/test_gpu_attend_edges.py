@@ -133,3 +133,25 @@ def test_a_bad_page_is_its_own_sequences_matter(B, nq, wide, fmt):
     hide = lambda n: (np.arange(n) < 16) | (np.arange(n) >= 32)   # noqa: E731
     p.visible = lambda b: see(b) & hide(p.lens[b]) if b in bad else see(b)
     p.check(got)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("nq,wide", [(1, False), (3, True), (40, False)])
+def test_rows_done_again_are_written_last(nq, wide, fmt):
+    """Rows that a hidden NaN touched: their second result and its lse stay, call after call."""
+    p = AttendProblem([500, 333, 64], [nq] * 3, 8, 2, 64, fmt=fmt, page=16, window=70, sinks=2, seed=56)
+    d = tensors(p, wide)
+    for b, n in enumerate(p.lens):      # the window's page holds hidden keys in front of it, NaN now
+        j = n - nq - 70
+        if j > 2:
+            at = p.table[b, j // 16], j % 16
+            x = d["vc"] if fmt is None else d["ks"] if fmt == "e2m1" else d["vc"]
+            x[at] = float("nan") if fmt is None else 0x7F
+    first = lse = None
+    for i in range(10):
+        out, l = torch.full_like(d["q"], 7.0), torch.full((3 * nq, 8), 7.0, device="cuda")
+        p.attend(d, out=out, lse=l)
+        if i == 0:
+            p.check(out, l)
+            first, lse = out, l
+        assert torch.equal(out.view(torch.int16), first.view(torch.int16)) and torch.equal(l, lse)
