@@ -571,9 +571,10 @@ __device__ __forceinline__ void write_rows(const AttendParams& a, int32_t b, con
       }
     }
   again = __reduce_or_sync(0xFFFFFFFFu, again);
-  const bool hold = waits != nullptr && again != 0u && lane == 0u;
+  if (again == 0u) return;
+  const bool hold = waits != nullptr && lane == 0u;
   if (hold) waits->hold(1);
-  __syncwarp();  // other lanes write these rows now (a reduction or vote orders no memory)
+  __syncwarp();  // other lanes write these rows now (a reduction orders no memory)
   while (again != 0u) {
     const int32_t r = __ffs(static_cast<int>(again)) - 1;
     again &= again - 1u;

@@ -246,6 +246,19 @@ __device__ __forceinline__ TileKeys tile_keys(const AttendParams& a, int32_t p_l
   return r;
 }
 
+// Whether a page id of the keys that some row needs is out of range; by a whole warp, once the CTA has met one.
+__device__ __noinline__ inline bool bad_pages(const AttendParams& a, int32_t b, TileKeys list, int32_t p_hi) {
+  const int32_t* table = a.table + static_cast<int64_t>(b) * a.table_stride;
+  bool bad = false;
+  for (int32_t v = static_cast<int32_t>(threadIdx.x & 31u); v < list.n * kTileKeys; v += 32) {
+    const int32_t k = list.key(v);
+    if (k > p_hi || (k < list.lo_key && k >= a.sinks)) continue;
+    const int32_t id = __ldg(table + a.page.quot(static_cast<uint32_t>(k)));
+    bad |= id < 0 || id >= a.num_pages;
+  }
+  return __any_sync(0xFFFFFFFFu, bad);
+}
+
 // One item: a block of up to 2 * qpt queries of a sequence, for one KV head.
 struct TileItem {
   int32_t b, kvh, tiles;
@@ -303,10 +316,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ uint32_t sh_tmem;
   __shared__ WaitState sh_waits;
-  // Items with keys are counted; bit (count % 32): the item has a page id out of range, and its rows are done
-  // again. The copies are a few items ahead of the rows' end at most (a ring's units), so the bit of 16 items
-  // on is free when they begin one.
-  __shared__ uint32_t sh_bad;
+  __shared__ volatile int sh_bad;     // a page id out of range was met, in this item or an earlier or later one
   __shared__ TileItem sh_item[2];     // the item of an odd and of an even round, for the softmax warps
 
   const AttendParams& a = p.a;
@@ -441,7 +451,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
       scale = put_q(it);
     }
     uint32_t waits = 0u, items = 0u;  // phases of s_full and p_full, and of q_full and o_full, that went by
-    uint32_t filled = 0u;             // items with keys that went by
     for (int32_t round = 0; ok && it.have;) {
       const bool mine = row_live(it);
       const int32_t pos = mine ? it.p_first + q_in : -1;
@@ -585,14 +594,15 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
             }
             __syncwarp();
           }
-          if (mine && a.lse)
-            a.lse[static_cast<int64_t>(tok) * a.q_heads + h] = (m + log2f(l)) * 0.6931471805599453f;
         }
-        const bool bad = it.list.n > 0 && (*const_cast<volatile uint32_t*>(&sh_bad) >> (filled & 31u) & 1u) != 0u;
-        uint32_t again = __ballot_sync(0xFFFFFFFFu, mine && (!fine || bad));
+        // rows of an item with a page id out of range are done again: zeros stood for its keys
+        const bool bad = __any_sync(0xFFFFFFFFu, sh_bad != 0) && bad_pages(a, it.b, it.list, it.p_hi);
+        const bool done = mine && fine && !bad;
+        if (done && a.lse)  // (a row without keys is not fine)
+          a.lse[static_cast<int64_t>(tok) * a.q_heads + h] = (m + log2f(l)) * 0.6931471805599453f;
+        uint32_t again = __ballot_sync(0xFFFFFFFFu, mine && !done);
         const bool hold = again != 0u && lane == 0u;
         if (hold) state->hold(1);
-        __syncwarp();  // other lanes write these rows and their sums now (a vote orders no memory)
         while (again != 0u) {
           const int src = __ffs(static_cast<int>(again)) - 1;
           again &= again - 1u;
@@ -601,7 +611,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
         }
         if (hold) state->hold(-1);
       }
-      if (it.list.n > 0) ++filled;
       it = next;
     }
   } else if (warp == 8) {
@@ -718,20 +727,17 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
       return want;
     };
     // The bits of keys on pages that exist; the others are counted.
-    auto checked = [&](const TileItem& it, uint32_t filled, uint32_t want, const int32_t (&id)[S::kPer]) -> uint32_t {
+    auto checked = [&](const TileItem& it, uint32_t want, const int32_t (&id)[S::kPer]) -> uint32_t {
       uint32_t bad = 0u;
 #pragma unroll
       for (int i = 0; i < S::kPer; ++i)
         bad |= (static_cast<uint32_t>(id[i]) >= static_cast<uint32_t>(a.num_pages) ? 1u : 0u) << i;
       bad &= want;
       if (bad != 0u) {
-        atomicOr(&sh_bad, 1u << (filled & 31u));
+        sh_bad = 1;
         record_oob(a.err, static_cast<uint64_t>(it.b));
       }
       return want & ~bad;
-    };
-    auto begin_item = [&](uint32_t filled) {  // by one warp
-      if (lane == 0u) atomicAnd(&sh_bad, ~(1u << ((filled + 16u) & 31u)));
     };
     auto offset_of = [&](const TileItem& it, int32_t j, int i) -> int32_t {  // in its page
       const uint32_t k = static_cast<uint32_t>(it.list.key(j * kTileKeys + static_cast<int32_t>(key0) + i * S::kStep));
@@ -741,9 +747,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
     if constexpr (FMT == KV_CACHE_SRC) {
       // TMA: lane i of warp 9 takes the tile's i-th page; every warp knows whether all are there
       const int32_t boxes = p.box > 0 ? kTileKeys / p.box : 0;
-      uint32_t filled = 0u;  // items with keys that went by
       for (int32_t round = 0; ok && tile_item(p, round, &it); ++round) {
-        if (it.list.n > 0 && warp == 9) begin_item(filled);
         const int32_t* table = a.table + static_cast<int64_t>(it.b) * a.table_stride;
         const uint8_t* const kbase = a.k + it.kvh * a.k_head;
         const uint8_t* const vbase = a.v + it.kvh * a.v_head;
@@ -777,7 +781,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
             }
           } else {
             int32_t id[S::kPer];
-            const uint32_t want = checked(it, filled, pages_of(it, j, id), id);
+            const uint32_t want = checked(it, pages_of(it, j, id), id);
 #pragma unroll
             for (int kv = 0; kv < 2; ++kv) {
               wait_empty(unit + kv);
@@ -807,7 +811,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
             }
           }
         }
-        if (it.list.n > 0) ++filled;
       }
       if (!ok)  // boxes in flight write shared memory: let them land before the CTA leaves it
         for (int i = 0; i < 1000; ++i) __nanosleep(1000);
@@ -819,11 +822,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
       const int32_t page_stride = kv ? p.v_page : p.k_page, slot_stride = kv ? p.v_slot : p.k_slot;
       constexpr int kKeys = kTileKeys / 32, kChunks = S::kRaw / 16, kRows = 32 / kChunks;
       int32_t round = 0, j = 0;
-      uint32_t filled = 0u;  // items with keys that went by
       bool have = tile_item(p, 0, &it);
       auto skip_empty = [&] {
         while (have && j >= it.list.n) {
-          if (it.list.n > 0) ++filled;
           j = 0;
           have = tile_item(p, ++round, &it);
         }
@@ -851,12 +852,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
           of[i] = k - static_cast<int32_t>(a.page.quot(static_cast<uint32_t>(k)) * a.page.d);
         }
         if (bad != 0u) {
-          atomicOr(&sh_bad, 1u << (filled & 31u));
+          sh_bad = 1;
           if (kv == 0) record_oob(a.err, static_cast<uint64_t>(it.b));
         }
         __syncwarp();
         const int32_t kvh = it.kvh;
-        if (j == 0 && kv == 0) begin_item(filled);
         ++j;
         skip_empty();
         if (have) look();
