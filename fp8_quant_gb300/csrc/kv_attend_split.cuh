@@ -28,7 +28,9 @@
 //    scale.
 //  * weights multiply 16-bit caches as two 16-bit terms (p = hi + lo), so their
 //    rounding does not add to the output's; the mma pipe has room for the
-//    second product there.  For quantised caches they are fp16 (2^-11).
+//    second product there.  For quantised caches they are fp16 (2^-11).  fp16
+//    weights are 2^15 of the largest, not 1, so that they keep their bits down to
+//    2^-29 of it and end at 2^-40, not 2^-25: many small ones beside a strong key add up.
 //  * all (sequence, block of rows, head group, tile) steps, counted by a scan
 //    over the lengths on the device, are cut into contiguous shares: one of
 //    80 % of an equal part for each CTA, the rest in shares of half the size and
@@ -469,7 +471,11 @@ __device__ __forceinline__ void hide_scores(const AttendParams& a, const int32_t
     }
 }
 
-// Running maximum and sum of rows 2t, 2t + 1; the weights, transposed to the second operand of
+// The running maximum is kept less this power, so the largest weight is 2 to it.
+template <bool kBF16>
+constexpr float kRoom = kBF16 ? 0.0f : 15.0f;
+
+// Running maximum (less kRoom) and sum of rows 2t, 2t + 1; the weights, transposed to the second operand of
 // O^T = V^T P^T (pt; pl: what their rounding left, 16-bit caches).
 template <int FMT, int NB, int MB, int OM, bool kBF16>
 __device__ __forceinline__ void softmax_step(float (&s)[MB][NB][4], const float (&rs)[NB][2], float (&m)[NB][2], float (&l)[NB][2],
@@ -486,7 +492,7 @@ __device__ __forceinline__ void softmax_step(float (&s)[MB][NB][4], const float 
       x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
       x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
       x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
-      x = fmaxf(m[nb][c], x * rs[nb][c]);
+      x = fmaxf(m[nb][c], __fmaf_rn(x, rs[nb][c], -kRoom<kBF16>));
       const float ref = x == -INFINITY ? 0.0f : x;
       grew |= x > m[nb][c];
       alpha[nb][c] = exp2_fast(m[nb][c] - ref);

@@ -9,8 +9,8 @@
 //   warps 0-3, 4-7  the softmax of tile 0 and of tile 1, a thread a row: S from
 //                   TMEM, running maximum and sum in registers, P back over S
 //                   as 16-bit, O rescaled in TMEM.  A maximum that grew by less
-//                   than 2^8 is kept, as the weights then stay below 2^8: O is
-//                   seldom touched.
+//                   than 2^8 is kept, as the weights then stay below 2^8 (fp16: 2^15,
+//                   so that small ones keep their bits): O is seldom touched.
 //   warp  8         issues the products: S_t = Q_t K^T (both operands in shared
 //                   memory), O_t += P_t V (P in TMEM, V as it lies: keys as
 //                   rows, head dims contiguous).  While one tile's softmax runs
@@ -456,7 +456,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
       const int32_t pos = mine ? it.p_first + q_in : -1;
       const int32_t tok = it.seq.q0 + it.q_first + q_in, h = it.kvh * G + gh;
       const bool live = t < it.tiles && it.list.n > 0;
-      float m = -INFINITY, l = 0.0f;   // m: of scaled scores, as last used
+      // the maximum of scaled scores, as last used and less kSmall: weights begin at 2 to that
+      constexpr float kSmall = kBF16 ? 0.0f : 7.0f;
+      float m = -INFINITY, l = 0.0f;
       // positions of the tile's rows
       const int32_t t_lo = it.p_first + t * p.qpt, t_hi = min(t_lo + p.qpt - 1, it.p_hi);
       for (int32_t j = 0; live && j < it.list.n; ++j) {
@@ -497,8 +499,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
 #pragma unroll
           for (int y = 0; y < 8; ++y) xs[y] = fmaxf(xs[y], fmaxf(s[i + y], s[i + 8 + y]));
         float x = fmaxf(fmaxf(fmaxf(xs[0], xs[1]), fmaxf(xs[2], xs[3])), fmaxf(fmaxf(xs[4], xs[5]), fmaxf(xs[6], xs[7])));
-        x *= scale;
-        // a maximum that grew little is kept (the weights stay below 2^8)
+        x = __fmaf_rn(x, scale, -kSmall);
+        // a maximum that grew little is kept (the weights stay below 2^(kSmall + 8))
         const bool grow = x > m + 8.0f || (m == -INFINITY && x > m);
         if (__any_sync(0xFFFFFFFFu, grow)) {
           const float mn = grow ? x : m;
