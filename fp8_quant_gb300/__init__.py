@@ -1059,6 +1059,8 @@ def kv_attend(q, k_cache, v_cache, page_table, seq_lens, *, q_start=None, page_s
         with _on_stream(stream, device):
             work = torch.empty(ATTEND_WORK_BYTES, dtype=torch.uint8, device=device)
             work[:ATTEND_HEAD_BYTES].zero_()
+    elif not work.is_contiguous():
+        raise ValueError("work must be contiguous")
     rec = err if err is not None else _default_record(device)
     rc = raw.kv_attend(
         q.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),

@@ -140,9 +140,19 @@ extern "C" kv_status kv_attend(const void* q, void* out, float* lse, const void*
   if (head_dim > 1024 || (format == KV_CACHE_E2M1 && head_dim % kFp4Block != 0)) return KV_ERR_UNSUPPORTED;
   if (num_q_tokens >= (1 << 30) || page_size >= INT_MAX || num_pages >= INT_MAX) return KV_ERR_UNSUPPORTED;
   {
-    const void* in[6] = {q, out, page_table, seq_lens, k_cache, v_cache};
+    const void* in[14] = {q, out, page_table, seq_lens, k_cache, v_cache, d_err};
+    int n = 7;
+    if (lse) in[n++] = lse;
+    if (q_start) in[n++] = q_start;
+    if (work && work_bytes > 0) in[n++] = work;
+    if (format == KV_CACHE_E2M1) {
+      in[n++] = scales->k;
+      in[n++] = scales->v;
+    }
+    if (format != KV_CACHE_SRC && k_scale) in[n++] = k_scale;
+    if (format != KV_CACHE_SRC && v_scale) in[n++] = v_scale;
     bool on_device = true;
-    const kv_status cs = classify_inputs(in, 6, &on_device);
+    const kv_status cs = classify_inputs(in, n, &on_device);
     if (cs != KV_OK) return cs;
   }
 

@@ -519,9 +519,21 @@ extern "C" kv_status kv_store_rope(const void* k, const void* v, void* k_cache, 
   }
   if (num_tokens > (int64_t{1} << 40)) return KV_ERR_UNSUPPORTED;
   {
-    const void* in[6] = {k, v, indices, rp.positions, rp.q, rp.q_out};
+    const void* in[14] = {k, v, indices, rp.positions, k_cache, v_cache, d_err};
+    int n = 7;
+    if (rp.q) {
+      in[n++] = rp.q;
+      in[n++] = rp.q_out;
+    }
+    if (rp.rotary_dim > 0) in[n++] = rp.cos_sin;
+    if (format == KV_CACHE_E2M1) {
+      in[n++] = scales->k;
+      in[n++] = scales->v;
+    }
+    if (format != KV_CACHE_SRC && inv_k_scale) in[n++] = inv_k_scale;
+    if (format != KV_CACHE_SRC && inv_v_scale) in[n++] = inv_v_scale;
     bool on_device = true;
-    const kv_status cs = classify_inputs(in, rp.q ? 6 : 4, &on_device);
+    const kv_status cs = classify_inputs(in, n, &on_device);
     if (cs != KV_OK) return cs;
   }
 
@@ -633,9 +645,12 @@ extern "C" kv_status kv_gather_fp4(const void* k_cache, const void* v_cache,
   const uint64_t per_token = 2ull * static_cast<uint64_t>(num_heads) * static_cast<uint64_t>(head_dim / kFp4Block);
   if (num_tokens > (int64_t{1} << 40) || per_token >= (1ull << 31)) return KV_ERR_UNSUPPORTED;
   {
-    const void* in[3] = {k_out, v_out, indices};
+    const void* in[10] = {k_out, v_out, indices, k_cache, v_cache, scales->k, scales->v, d_err};
+    int n = 8;
+    if (k_scale) in[n++] = k_scale;
+    if (v_scale) in[n++] = v_scale;
     bool on_device = true;
-    const kv_status cs = classify_inputs(in, 3, &on_device);
+    const kv_status cs = classify_inputs(in, n, &on_device);
     if (cs != KV_OK) return cs;
   }
   Fp4GatherParams p = {};

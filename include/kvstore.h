@@ -473,7 +473,8 @@ typedef struct kv_rope {
  * A token whose position is out of range writes nothing and is counted in the
  * error record once, like one whose slot is.
  * K, V, Q, q_out, the slot ids and the positions may be page-locked host
- * memory; the caches, scales and the table are device memory.
+ * memory; the caches, scales, the table and the record are device memory.  Any
+ * that CUDA does not know is rejected with KV_ERR_INVALID_ARG.
  * q_out may be q; it must overlap nothing else.  Dims of Q must be contiguous;
  * K, V and the caches may have any dim strides, but an e2m1 cache and its
  * scales have contiguous dims (else KV_ERR_UNSUPPORTED).
@@ -569,9 +570,9 @@ typedef struct kv_attend_strides {
  * Waits inside the kernels have a limit, far beyond any that ends.  A CTA whose
  * wait ran out leaves rows unwritten, and kv_error_poll returns KV_ERR_WAIT; a
  * call that splits sequences gives NaN for all its rows then.
- * All pointers are device memory; q, out, the caches, the table and the lengths
- * are rejected with KV_ERR_INVALID_ARG where CUDA does not know them.  The
- * result does not depend on the order in which CTAs run; it may differ in rounding with the workspace's size.
+ * All pointers are device memory, and rejected with KV_ERR_INVALID_ARG where
+ * CUDA does not know them.  The result does not depend on the order in which
+ * CTAs run; it may differ in rounding with the workspace's size.
  *
  * Returns KV_OK once enqueued, KV_ERR_INVALID_ARG for a bad argument (NULL
  * pointers, sizes < 1, num_heads not dividing num_q_heads, window or sinks

@@ -14,3 +14,12 @@ def lib():
 
 def test_status_of_a_wait():
     assert kv.kv_status_str(5) == "KV_ERR_WAIT" and kv.KVStatus(5).name == "ERR_WAIT"
+
+
+def test_a_workspace_is_contiguous(monkeypatch):
+    import torch
+    monkeypatch.setattr(kv.raw, "kv_attend", lambda *a: pytest.fail("called"))
+    q, kc = (torch.zeros(s, dtype=torch.bfloat16) for s in ((2, 8, 64), (4, 16, 2, 64)))
+    with pytest.raises(ValueError, match="contiguous"):
+        kv.kv_attend(q, kc, kc, torch.zeros(2, 3, dtype=torch.int32), torch.zeros(2, dtype=torch.int32),
+                     work=torch.zeros(4096, dtype=torch.uint8)[::2], err=torch.zeros(2, dtype=torch.int64))
