@@ -883,10 +883,10 @@ def kv_store_rope(k, v, k_cache, v_cache, indices, positions, cos_sin, *, q=None
     """Append K/V rows to a cache with the position rotation applied on the way.
 
     ``k``/``v``: bf16 or fp16 [T, H, D]; ``q`` (optional): [T, HQ, D], rotated into ``q_out``
-    (a new tensor if None; may be ``q``), which is returned. Token t goes to slot ``indices[t]``
-    at position ``positions[t]`` (1-D int32 / int64). ``cos_sin``: fp32 [max_position, R], a
-    row's R/2 cosines and then its sines; the first R dims of Q and K are rotated, in pairs
-    (i, i + R/2), or (2i, 2i + 1) when ``interleaved``.
+    (a new tensor on the caches' device if None; may be ``q``), which is returned. Token t goes
+    to slot ``indices[t]`` at position ``positions[t]`` (1-D int32 / int64). ``cos_sin``: fp32
+    [max_position, R], a row's R/2 cosines and then its sines; the first R dims of Q and K are
+    rotated, in pairs (i, i + R/2), or (2i, 2i + 1) when ``interleaved``.
 
     ``fmt``: None (caches of the rows' dtype), "e4m3fn" (1-byte caches, [..., D]) or "e2m1"
     (uint8 caches [..., D / 2] with block scales ``k_scales`` / ``v_scales`` [..., D / 16]);
@@ -918,8 +918,8 @@ def kv_store_rope(k, v, k_cache, v_cache, indices, positions, cos_sin, *, q=None
         if len(qshape) != 3 or qshape[0] != T or qshape[2] != D or q.dtype is not dtype or qst[2] != 1:
             raise ValueError("q must be [T, HQ, D] of k's dtype with contiguous dims")
         if q_out is None:
-            with _on_stream(stream, q.device):
-                q_out = torch.empty(qshape, dtype=dtype, device=q.device)
+            with _on_stream(stream, k_cache.device):  # (q itself may be page-locked host memory)
+                q_out = torch.empty(qshape, dtype=dtype, device=k_cache.device)
         ost = q_out.stride()
         if q_out.shape != qshape or q_out.dtype is not dtype or ost[2] != 1:
             raise ValueError("q_out must be like q, with contiguous dims")

@@ -23,3 +23,15 @@ def test_a_workspace_is_contiguous(monkeypatch):
     with pytest.raises(ValueError, match="contiguous"):
         kv.kv_attend(q, kc, kc, torch.zeros(2, 3, dtype=torch.int32), torch.zeros(2, dtype=torch.int32),
                      work=torch.zeros(4096, dtype=torch.uint8)[::2], err=torch.zeros(2, dtype=torch.int64))
+
+
+def test_rotated_queries_belong_to_the_caches_device(monkeypatch):
+    """Queries may be page-locked host memory; a result on the host beside them would be refused."""
+    import torch
+    monkeypatch.setattr(kv.raw, "kv_store_rope", lambda *a: 0)
+    monkeypatch.setattr(kv, "_stream_handle", lambda stream, device: 0)
+    q, k = torch.zeros(3, 8, 64, dtype=torch.bfloat16), torch.zeros(3, 2, 64, dtype=torch.bfloat16)
+    cache = torch.zeros(16, 2, 64, dtype=torch.bfloat16, device="meta")
+    out = kv.kv_store_rope(k, k, cache, cache, torch.arange(3), torch.arange(3), torch.zeros(9, 64), q=q,
+                           err=torch.zeros(2, dtype=torch.int64))
+    assert out.device == cache.device and out.shape == q.shape

@@ -26,3 +26,18 @@ def _lib():
 @pytest.mark.parametrize("T", [1, 700])
 def test_rows_of_all_kinds_in_a_warp(T, HQ, H, D, R, interleaved, fmt):
     run(T, HQ, H, D, R, "bf16", fmt, interleaved=interleaved, seed=9)
+
+
+def test_pinned_queries_without_an_output():
+    import torch
+    import fp8_quant_gb300 as kv
+    from attncheck import rope_table
+    T, HQ, H, D = 30, 4, 2, 64
+    q, k, v = (torch.randn(T, h, D).to(torch.bfloat16) for h in (HQ, H, H))
+    tab, pos = torch.from_numpy(rope_table(64, 64)).cuda(), torch.arange(T, device="cuda")
+    got = []
+    for put in (lambda x: x.cuda(), lambda x: x.pin_memory()):
+        kc, vc = (torch.zeros(32, H, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        got.append(kv.kv_store_rope(put(k), put(v), kc, vc, pos, pos, tab, q=put(q)))
+        torch.cuda.synchronize()
+    assert got[1].is_cuda and torch.equal(*got)
