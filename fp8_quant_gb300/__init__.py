@@ -815,6 +815,8 @@ def _cache_strides(cache, page_size, width, elem_bytes, what):
     e = cache.element_size()
     if e != elem_bytes:
         raise TypeError(f"{what} must have {elem_bytes}-byte elements")
+    if page_size < 1:
+        raise ValueError("page_size must be at least 1")
     shape = cache.shape
     if len(shape) == 4:
         pages, ps, H, w = shape
@@ -1032,7 +1034,7 @@ def kv_attend(q, k_cache, v_cache, page_table, seq_lens, *, q_start=None, page_s
     if kc[3] != vc[3] or kc[3] != (2 if fmt is None else 1):
         raise ValueError("cache dims must be contiguous")
     slots, H = kc[4], kc[5]
-    if HQ % H:
+    if H < 1 or HQ % H:
         raise ValueError(f"{HQ} query heads over {H} KV heads")
     sc = _block_scales(k_scales, v_scales, page_size, D, slots, H) if fmt == "e2m1" else None
     tst = page_table.stride()

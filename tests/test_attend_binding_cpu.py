@@ -35,3 +35,13 @@ def test_rotated_queries_belong_to_the_caches_device(monkeypatch):
     out = kv.kv_store_rope(k, k, cache, cache, torch.arange(3), torch.arange(3), torch.zeros(9, 64), q=q,
                            err=torch.zeros(2, dtype=torch.int64))
     assert out.device == cache.device and out.shape == q.shape
+
+
+@pytest.mark.parametrize("shape,page_size", [((64, 2, 64), 0), ((64, 2, 64), -16), ((4, 0, 2, 64), None), ((64, 0, 64), 16)])
+def test_empty_pages_and_caches_are_refused(shape, page_size, monkeypatch):
+    import torch
+    monkeypatch.setattr(kv.raw, "kv_attend", lambda *a: pytest.fail("called"))
+    q, kc = torch.zeros(2, 8, 64, dtype=torch.bfloat16), torch.zeros(shape, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        kv.kv_attend(q, kc, kc, torch.zeros(2, 3, dtype=torch.int32), torch.zeros(2, dtype=torch.int32), page_size=page_size,
+                     work=torch.zeros(256, dtype=torch.uint8), err=torch.zeros(2, dtype=torch.int64))
