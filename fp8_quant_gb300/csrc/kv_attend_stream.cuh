@@ -177,8 +177,12 @@ __global__ void __launch_bounds__(StreamLayout<FMT, DP, NB>::kThreads, 1)
     const uint32_t at_scales = S::kCodes + static_cast<uint32_t>(sub * nbox + part) * sc_bytes;
     uint32_t unit = 0u;
     bool ok = true;
+    // Ends with a fence between proxies: the products' loads are generic accesses, still under way for all that
+    // an arrival tells TMA, which writes past them. (Without it units were overwritten under a warp
+    // that was late while the others stored their sums.)
     auto wait_empty = [&](uint32_t u) {
       if (ok && u >= S::kUnits) ok = __all_sync(0xFFFFFFFFu, bar_wait(empty + 8 * (u % S::kUnits), (u / S::kUnits - 1) & 1u, waits));
+      fence_async_shared();
     };
     const int32_t shares = sh_work.shares;
     int32_t share = static_cast<int32_t>(blockIdx.x);

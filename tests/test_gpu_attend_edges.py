@@ -155,3 +155,33 @@ def test_rows_done_again_are_written_last(nq, wide, fmt):
             p.check(out, l)
             first, lse = out, l
         assert torch.equal(out.view(torch.int16), first.view(torch.int16)) and torch.equal(l, lse)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("B,nq,n,page", [(48, 4, 3000, 64), (48, 4, 3000, 32), (96, 2, 1500, 16), (64, 1, 4000, 64)])
+def test_long_calls_repeat_themselves(B, nq, n, page, fmt):
+    """Enough shares that the copies run into the next one while a warp still multiplies: the same bits thirty times."""
+    import fp8_quant_gb300 as kv
+    HQ, H, D, dev = 32, 8, 128, "cuda"
+    g = torch.Generator(device=dev).manual_seed(57)
+    lens = torch.tensor([n - 11 * i for i in range(B)], dtype=torch.int32, device=dev)
+    need = -(-n // page)
+    pages = B * need
+    table = torch.randperm(pages, generator=g, device=dev).to(torch.int32).view(B, need)
+    a = dict(fmt=fmt, q_start=torch.arange(0, B * nq + 1, nq, dtype=torch.int32, device=dev))
+    if fmt is None:
+        kc, vc = (torch.randn(pages, page, H, D, generator=g, device=dev, dtype=torch.bfloat16) for _ in range(2))
+    else:
+        width = D // 2 if fmt == "e2m1" else D
+        kc, vc = (torch.randint(0, 256, (pages, page, H, width), generator=g, device=dev, dtype=torch.uint8) for _ in range(2))
+        if fmt == "e4m3fn":
+            kc, vc = (x & 0xB7 for x in (kc, vc))          # finite, at most 1.875
+        else:
+            a["k_scales"], a["v_scales"] = (torch.randint(0x28, 0x30, (pages, page, H, D // 16), generator=g, device=dev,
+                                                          dtype=torch.uint8) for _ in range(2))
+    q = torch.randn(B * nq, HQ, D, generator=g, device=dev, dtype=torch.bfloat16)
+    work = torch.zeros(kv.ATTEND_WORK_BYTES, dtype=torch.uint8, device=dev)
+    first = kv.kv_attend(q, kc, vc, table, lens, work=work, **a)
+    assert first.isfinite().all()
+    for _ in range(30):
+        assert torch.equal(kv.kv_attend(q, kc, vc, table, lens, work=work, **a).view(torch.int16), first.view(torch.int16))
