@@ -68,3 +68,15 @@ def test_no_wait_runs_out_while_rows_are_done_again():
     assert kv.kv_error_poll(err) == (kv.KVStatus.OK, 0, -1)
     p.check(out)
     assert start.elapsed_time(end) > 2300      # it did take longer than a wait may
+
+
+def test_a_wait_that_nothing_ends_runs_out(tmp_path):
+    """The kernels' wait, on a barrier of its own: false for every warp, the record's bit beside its count, a live context."""
+    import os
+    import subprocess
+    from fp8_quant_gb300 import build
+    exe = str(tmp_path / "wait_limit")
+    src = os.path.join(os.path.dirname(os.path.abspath(__file__)), "c", "wait_limit.cu")
+    subprocess.check_call([build.nvcc(), *build.NVCC_FLAGS, "-I", os.path.join(build.ROOT, "include"), "-I", build.CSRC, "-o", exe, src])
+    got = subprocess.run([exe], capture_output=True, text=True, timeout=120)
+    assert got.returncode == 0 and got.stdout.split() == ["no", "error", "1", "0", "0", "1", "3"], got.stdout + got.stderr
