@@ -1011,7 +1011,9 @@ def kv_attend(q, k_cache, v_cache, page_table, seq_lens, *, q_start=None, page_s
     A query at position p sees key j <= p, with ``window`` > 0 only j > p - window or
     j < ``sinks``. ``sm_scale``: of the scores (1 / sqrt(D) if None). ``fmt``, ``k_scales``,
     ``v_scales``: as in :func:`kv_store_rope`; ``k_scale`` / ``v_scale``: forward tensor scales
-    (1-element fp32 device tensors, None: 1). ``lse``: an fp32 [tokens, HQ] tensor for the
+    (1-element fp32 device tensors, None: 1). The same call gives the same bits; the rounding of
+    a sequence's rows may differ with the others in the call, as the kernel is chosen for all
+    (see the C header). ``lse``: an fp32 [tokens, HQ] tensor for the
     logarithms of the rows' sums, or None. ``work``: a device tensor that lets long sequences be
     split over the GPU (ATTEND_WORK_BYTES is always enough; its first ATTEND_HEAD_BYTES are zero
     before its first use, and every call that completes leaves them zero; calls that share one must

@@ -28,9 +28,9 @@
 //    scale.
 //  * weights multiply 16-bit caches as two 16-bit terms (p = hi + lo), so their
 //    rounding does not add to the output's; the mma pipe has room for the
-//    second product there.  For quantised caches they are fp16 (2^-11).  fp16
-//    weights are 2^15 of the largest, not 1, so that they keep their bits down to
-//    2^-29 of it and end at 2^-40, not 2^-25: many small ones beside a strong key add up.
+//    second product there.  For quantised caches they are fp16 (2^-12 of each).
+//    fp16 weights begin at 2^15 instead of 1, so that they keep their bits down to 2^-29
+//    of the largest and end at 2^-40, not at 2^-14 and 2^-25: many small ones add up.
 //  * all (sequence, block of rows, head group, tile) steps, counted by a scan
 //    over the lengths on the device, are cut into contiguous shares: one of
 //    80 % of an equal part for each CTA, the rest in shares of half the size and
@@ -41,8 +41,8 @@
 //    inside an item leaves its sums in the workspace, and a second kernel joins
 //    them in the order of the keys, whoever computed them.
 //    Two launches and their scans are what a short call costs: one query over
-//    1,000 16-bit keys, 32 over 8 heads of 128, 17.5 us; 16 sequences of 40 - 130
-//    tokens, unsplit, 12 us; 48 windows of 4,096 in pages of 20 keys, 781 MB, 163 us, 4.8 TB/s.
+//    1,000 16-bit keys, 32 over 8 heads of 128, 16 us; 16 sequences of 40 - 130
+//    tokens, unsplit, 11 us; 48 windows of 4,096 in pages of 20 keys, 781 MB, 160 us, 4.9 TB/s.
 //  * a row whose sum is 0 or whose output is not finite is done again by
 //    attend_row, which touches its visible keys alone: a NaN value that the
 //    mask hides from a row must not reach it through a weight of 0.

@@ -18,12 +18,14 @@
 //    sequence's end are not hidden from TMA.  The scores of both are masked and
 //    their V rows (e2m1: scales) are zeroed in shared memory, by the warp
 //    that is about to use them.  Pages out of range are fetched as zeros.
+//  * the products' loads and TMA's writes are accesses of different proxies: the copy
+//    warp puts a fence between an empty unit's last arrival and its next box.
 // Every wait has a limit; a CTA whose wait ran out records that, for the join too, and leaves.
 //
 // Measured on one GB300 (one query a sequence, 32 over 8 heads of 128): 128
 // windows of 4,096 16-bit keys 317 us, 6.7 TB/s; 32 sequences of 16,000 - 32,768
-// e4m3fn keys 248 us, 6.4 TB/s (99 and 95 % of a copy's rate); 64 such sequences of
-// 4-bit keys 419 us, 4.3 TB/s, and one of 131,071 keys 48 us.  The 4-bit ones are
+// e4m3fn keys 249 us, 6.4 TB/s (99 and 95 % of a copy's rate), with four queries each
+// 321 us; 64 such sequences of 4-bit keys 409 us, 4.4 TB/s, and one of 131,071 keys 48 us.  The 4-bit ones are
 // bound by the eight warps' conversions and products, not by memory; 12 or 16
 // warps with fewer registers each took 670 us and more.
 #pragma once
@@ -83,8 +85,8 @@ struct StreamStep {
 // steps; a page id of the step's is out of range
 constexpr int kFirst = 1, kLast = 2, kWhole = 4, kBegins = 8, kStop = 16, kBadPage = 32;
 
-// kDimsFit (4-bit caches): head_dim is DP, so that every piece of a lane has its block scales (fp4_decode
-// 420 us; 456 with the other form's selection).
+// kDimsFit (4-bit caches): head_dim is DP, so that every piece of a lane has its block scales (64
+// sequences of 16,000 - 32,768 keys 420 us; 456 with the other form's selection).
 template <int FMT, int DP, int NB, bool kBF16, bool kDimsFit>
 __global__ void __launch_bounds__(StreamLayout<FMT, DP, NB>::kThreads, 1)
     kv_attend_stream(const __grid_constant__ StreamParams sp) {

@@ -21,9 +21,9 @@
 //                   and page, or 16 keys of one (windows, and pages that 128 keys
 //                   are no multiple of); others by cp.async, 16 bytes a lane, with
 //                   zeros for keys that no row needs.  Quantised rows are copied
-//                   as they are by warps 14 (V) and 15 (K) with cp.async, up to
-//                   two tiles ahead, and become fp16 on their way into the ring
-//                   (exact; see kv_attend_split.cuh) by 9-13.
+//                   as they are by warps 14 (V) and 15 (K) with cp.async, three
+//                   (e4m3fn) or four K and V tiles ahead, and become fp16 on their way
+//                   into the ring (exact; see kv_attend_split.cuh) by 9-13.
 //
 // Weights are rounded once to 16 bits, as the product's operand: 2^-9 (bf16) or
 // 2^-12 of each at most, which is what the output's own rounding is; their sum
@@ -41,9 +41,9 @@
 // softmax ends and its rows are written.
 //
 // Measured on one GB300 (32 over 8 heads of 128): one causal prompt of 8,192
-// fp16 tokens 416 us, 1.32 PFLOP/s; prompts of 2,500 and 4,095 bf16 tokens in windows
-// of 1,024 137 us, 0.81 PFLOP/s; chunks of 400 - 1,000 fp16 tokens over windows of
-// 4,096 4-bit keys 148 us, 0.96 PFLOP/s.  What bounds it is the chain of one tile:
+// fp16 tokens 420 us, 1.31 PFLOP/s, and over e4m3fn keys (bf16 queries) 468 us; prompts of
+// 2,500 and 4,095 bf16 tokens in windows of 1,024 136 us, 0.82 PFLOP/s; chunks of 400 - 1,000
+// fp16 tokens over windows of 4,096 4-bit keys 150 us, 0.94 PFLOP/s.  What bounds it is the chain of one tile:
 // S's product, maximum and weights (0.9 us of a row's 128 scores in one thread), P V, next
 // product: 2.0 us a pair of tiles and 128 keys against 1.1 of products.  Handing the weights
 // over in two or three parts, or loading S while its first half's maximum is taken, gained

@@ -11,7 +11,7 @@
 //                   two pieces of 8: both halves of eight pairs, so that
 //                   whatever they need is in the lane (an e2m1 block of the
 //                   split-half rotation is two lanes' and takes one shuffle for
-//                   its maximum).  The lanes of a warp are the items of 32 * 16
+//                   its maximum, which all lanes execute).  The lanes of a warp are the items of 32 * 16
 //                   / head_dim heads; a warp goes over U such groups of a
 //                   token's Q, K and V heads with all their loads in flight
 //                   before the first store, and since a lane keeps its item
@@ -23,10 +23,11 @@
 //                   in, 32 bytes out.
 //
 // Measured on one GB300 (32 query and 8 KV heads of 128, q in and out):
-// 32,768 fp16 tokens into a 16-bit cache, 822 MB, 147 us, 5.6 TB/s, 83 % of a
-// copy's rate (the table's rows of scattered positions come on top of the counted bytes);
-// 8,191 bf16 tokens into the 4-bit cache 44 us; their gather 12.7 us; 256 tokens
-// into an e4m3fn cache 5.4 us and one token 3.9 us, launch and three dependent loads.
+// 32,768 fp16 tokens into a 16-bit cache, 822 MB, 145 us, 5.7 TB/s, 84 % of a
+// copy's rate (the table's rows of scattered positions come on top of the counted bytes),
+// and bf16 ones into an e4m3fn cache 149 us; 8,191 bf16 tokens into the 4-bit cache 42 us; their
+// gather 11.8 us; 256 tokens into an e4m3fn cache 4.1 us and one token 2.1 us (calls
+// captured one behind the other), launch and three dependent loads.
 #include <cmath>
 
 #include "kv_fp4.cuh"

@@ -477,7 +477,8 @@ typedef struct kv_rope {
  * that CUDA does not know is rejected with KV_ERR_INVALID_ARG.
  * q_out may be q; it must overlap nothing else.  Dims of Q must be contiguous;
  * K, V and the caches may have any dim strides, but an e2m1 cache and its
- * scales have contiguous dims (else KV_ERR_UNSUPPORTED).
+ * scales have contiguous dims (else KV_ERR_UNSUPPORTED).  Of tokens that share a
+ * slot, an e2m1 block's codes and its scale may be different ones'.
  */
 kv_status kv_store_rope(const void *k, const void *v, void *k_cache, void *v_cache,
                         const void *indices, kv_index_dtype index_dtype, int64_t index_stride,
@@ -534,7 +535,12 @@ typedef struct kv_attend_strides {
  * over the visible keys.  A row that sees no key is 0 with lse -infinity.
  * Statistics and sums are fp32; 16-bit caches are multiplied in their type,
  * e4m3fn and e2m1 values (with their block scales, both exact) in fp16 against
- * queries brought into fp16's range by a power of two per row.
+ * queries brought into fp16's range by a power of two per row.  The weights
+ * exp(s_j) meet the values as 16-bit operands (fp16, or bf16 for a bf16 cache):
+ * rounded once in the kernel for many query rows and for quantised caches, as
+ * two terms (no loss beside the output's rounding) for few rows over a 16-bit
+ * cache, and kept in fp32 by the general kernel.  One rounding adds up to
+ * 2^-9 (bf16) or 2^-12 (fp16) of sum p_j |v_j| / sum p_j to the output's error.
  *
  *   q, out      [num_q_tokens, num_q_heads, head_dim] of `dtype`; out must not
  *               overlap q or the caches.
@@ -572,7 +578,10 @@ typedef struct kv_attend_strides {
  * call that splits sequences gives NaN for all its rows then.
  * All pointers are device memory, and rejected with KV_ERR_INVALID_ARG where
  * CUDA does not know them.  The result does not depend on the order in which
- * CTAs run; it may differ in rounding with the workspace's size.
+ * CTAs run, so the same call gives the same bits.  It may differ in rounding
+ * with the workspace's size, and with what else the call holds: the kernel, and
+ * with it how weights are rounded and where sums are split, is chosen once for the
+ * call, from num_seqs, num_q_tokens, table_width and window.
  *
  * Returns KV_OK once enqueued, KV_ERR_INVALID_ARG for a bad argument (NULL
  * pointers, sizes < 1, num_heads not dividing num_q_heads, window or sinks
