@@ -9,7 +9,7 @@
 namespace kvimpl {
 
 // Tries of a wait, of 2 us and more each: 2 to 4 s, where no warp's work between two barriers takes a
-// millisecond but attend_row's, for which waits stand still (WaitState).
+// millisecond but on rows done key by key and page tables gone through, for which waits stand still (WaitState).
 constexpr uint32_t kSpin = 1u << 20;
 
 __device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {

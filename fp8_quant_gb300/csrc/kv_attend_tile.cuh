@@ -247,7 +247,8 @@ __device__ __forceinline__ TileKeys tile_keys(const AttendParams& a, int32_t p_l
 }
 
 // Whether a page id of the keys that some row needs is out of range; by a whole warp, once the CTA has met one.
-__device__ __noinline__ inline bool bad_pages(const AttendParams& a, int32_t b, TileKeys list, int32_t p_hi) {
+__device__ __noinline__ inline bool bad_pages(const AttendParams& a, int32_t b, TileKeys list, int32_t p_hi, WaitState* state) {
+  if ((threadIdx.x & 31u) == 0u) state->hold(1);
   const int32_t* table = a.table + static_cast<int64_t>(b) * a.table_stride;
   bool bad = false;
   for (int32_t v = static_cast<int32_t>(threadIdx.x & 31u); v < list.n * kTileKeys; v += 32) {
@@ -256,7 +257,9 @@ __device__ __noinline__ inline bool bad_pages(const AttendParams& a, int32_t b, 
     const int32_t id = __ldg(table + a.page.quot(static_cast<uint32_t>(k)));
     bad |= id < 0 || id >= a.num_pages;
   }
-  return __any_sync(0xFFFFFFFFu, bad);
+  bad = __any_sync(0xFFFFFFFFu, bad);
+  if ((threadIdx.x & 31u) == 0u) state->hold(-1);
+  return bad;
 }
 
 // One item: a block of up to 2 * qpt queries of a sequence, for one KV head.
@@ -598,7 +601,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
           }
         }
         // rows of an item with a page id out of range are done again: zeros stood for its keys
-        const bool bad = __any_sync(0xFFFFFFFFu, sh_bad != 0) && bad_pages(a, it.b, it.list, it.p_hi);
+        const bool bad = __any_sync(0xFFFFFFFFu, sh_bad != 0) && bad_pages(a, it.b, it.list, it.p_hi, state);
         const bool done = mine && fine && !bad;
         if (done && a.lse)  // (a row without keys is not fine)
           a.lse[static_cast<int64_t>(tok) * a.q_heads + h] = (m + log2f(l)) * 0.6931471805599453f;
