@@ -316,6 +316,7 @@ __device__ __forceinline__ bool tile_item(const TileParams& p, int32_t round, Ti
 template <int FMT, int DP, bool kBF16>
 __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_constant__ TileParams p) {
   using S = TileSmem<FMT, DP>;
+  constexpr bool kApart = FMT == KV_CACHE_SRC;  // of the waits
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ uint32_t sh_tmem;
   __shared__ WaitState sh_waits;
@@ -385,7 +386,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
     const uint32_t s_at = tmem + lanes + t * 128, o_at = tmem + lanes + 256 + t * DP;
     bool ok = true;
     auto take_item = [&](int32_t round, TileItem* x) {
-      ok = __all_sync(0xFFFFFFFFu, bar_wait(item_full + 8 * (round & 1), static_cast<uint32_t>(round >> 1) & 1u, state));
+      ok = __all_sync(0xFFFFFFFFu, bar_wait<kApart>(item_full + 8 * (round & 1), static_cast<uint32_t>(round >> 1) & 1u, state));
       if (!ok) return;
       *x = sh_item[round & 1];
       __syncwarp();
@@ -465,7 +466,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
       // positions of the tile's rows
       const int32_t t_lo = it.p_first + t * p.qpt, t_hi = min(t_lo + p.qpt - 1, it.p_hi);
       for (int32_t j = 0; live && j < it.list.n; ++j) {
-        ok = __all_sync(0xFFFFFFFFu, bar_wait(s_full + 8 * t, waits & 1u, state));
+        ok = __all_sync(0xFFFFFFFFu, bar_wait<kApart>(s_full + 8 * t, waits & 1u, state));
         if (!ok) break;
         tc_fence_after();
         uint32_t sw[kTileKeys];
@@ -557,7 +558,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
       if (t < it.tiles) {
         bool fine = l > 0.0f;
         if (live) {
-          ok = __all_sync(0xFFFFFFFFu, bar_wait(o_full + 8 * t, items & 1u, state));
+          ok = __all_sync(0xFFFFFFFFu, bar_wait<kApart>(o_full + 8 * t, items & 1u, state));
           if (!ok) break;
           ++items;
           tc_fence_after();
@@ -625,7 +626,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
     const uint32_t qk_desc = instr_desc(kBF16, false, kTileKeys), pv_desc = instr_desc(kBF16, true, DP);
     bool ok = true;
     auto wait = [&](uint32_t bar, uint32_t parity) {
-      if (ok) ok = __all_sync(0xFFFFFFFFu, bar_wait(bar, parity, state));
+      if (ok) ok = __all_sync(0xFFFFFFFFu, bar_wait<kApart>(bar, parity, state));
       if (ok) tc_fence_after();
     };
     // descriptors of the operands' first pieces; the others are constant steps (in 16 bytes) away
@@ -713,7 +714,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
     bool ok = true;
     uint32_t unit = 0u;  // ring units that went by
     auto wait_empty = [&](uint32_t u) {
-      if (ok && u >= S::kUnits) ok = __all_sync(0xFFFFFFFFu, bar_wait(empty + 8 * (u % S::kUnits), (u / S::kUnits - 1) & 1u, state));
+      if (ok && u >= S::kUnits) ok = __all_sync(0xFFFFFFFFu, bar_wait<kApart>(empty + 8 * (u % S::kUnits), (u / S::kUnits - 1) & 1u, state));
     };
     // Which of the lane's keys of a tile a row needs, a bit each, and their pages.  What is loaded
     // is not looked at before it is used, a tile later (a select behind a load would wait for it),
@@ -866,7 +867,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
         skip_empty();
         if (have) look();
         const uint32_t u = 2u * tile + static_cast<uint32_t>(kv), raw = u % S::kRaws;
-        if (u >= S::kRaws) ok = __all_sync(0xFFFFFFFFu, bar_wait(raw_empty + 8 * raw, (u / S::kRaws - 1u) & 1u, state));
+        if (u >= S::kRaws) ok = __all_sync(0xFFFFFFFFu, bar_wait<kApart>(raw_empty + 8 * raw, (u / S::kRaws - 1u) & 1u, state));
         if (!ok) break;
         const uint32_t at = smem + S::kOffRaw + raw * S::kRawTile;
         const uint8_t* const base = kv ? a.v + kvh * a.v_head : a.k + kvh * a.k_head;
@@ -928,7 +929,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) kv_attend_tile(const __grid_c
         for (int32_t left = 2 * it.list.n; left > 0 && ok; --left, ++unit) {
           const uint32_t raw = unit % S::kRaws, from = smem + S::kOffRaw + raw * S::kRawTile;
           uint32_t w[S::kPer][kWords], sc[FMT == KV_CACHE_E2M1 ? S::kPer : 1];
-          ok = __all_sync(0xFFFFFFFFu, bar_wait(raw_full + 8 * raw, (unit / S::kRaws) & 1u, state));
+          ok = __all_sync(0xFFFFFFFFu, bar_wait<kApart>(raw_full + 8 * raw, (unit / S::kRaws) & 1u, state));
           if (!ok) break;
 #pragma unroll
           for (int i = 0; i < S::kPer; ++i) {
