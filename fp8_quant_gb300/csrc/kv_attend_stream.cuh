@@ -24,8 +24,8 @@
 //
 // Measured on one GB300 (one query a sequence, 32 over 8 heads of 128): 128
 // windows of 4,096 16-bit keys 317 us, 6.7 TB/s; 32 sequences of 16,000 - 32,768
-// e4m3fn keys 249 us, 6.4 TB/s (99 and 95 % of a copy's rate), with four queries each
-// 321 us; 64 such sequences of 4-bit keys 409 us, 4.4 TB/s, and one of 131,071 keys 48 us.  The 4-bit ones are
+// e4m3fn keys 248 us, 6.4 TB/s (99 and 95 % of a copy's rate), with four queries each
+// 312 us; 64 such sequences of 4-bit keys 401 us, 4.5 TB/s, and one of 131,071 keys 48 us.  The 4-bit ones are
 // bound by the eight warps' conversions and products, not by memory; 12 or 16
 // warps with fewer registers each took 670 us and more.
 #pragma once

@@ -41,8 +41,8 @@
 // softmax ends and its rows are written.
 //
 // Measured on one GB300 (32 over 8 heads of 128): one causal prompt of 8,192
-// fp16 tokens 420 us, 1.31 PFLOP/s, and over e4m3fn keys (bf16 queries) 468 us; prompts of
-// 2,500 and 4,095 bf16 tokens in windows of 1,024 136 us, 0.82 PFLOP/s; chunks of 400 - 1,000
+// fp16 tokens 415 us, 1.32 PFLOP/s, and over e4m3fn keys (bf16 queries) 472 us; prompts of
+// 2,500 and 4,095 bf16 tokens in windows of 1,024 133 us, 0.83 PFLOP/s; chunks of 400 - 1,000
 // fp16 tokens over windows of 4,096 4-bit keys 150 us, 0.94 PFLOP/s.  What bounds it is the chain of one tile:
 // S's product, maximum and weights (0.9 us of a row's 128 scores in one thread), P V, next
 // product: 2.0 us a pair of tiles and 128 keys against 1.1 of products.  Handing the weights
