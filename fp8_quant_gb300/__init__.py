@@ -16,6 +16,9 @@ the same names:
 * :func:`kv_store_rope` (append with the position rotation applied on the way;
   16-bit, e4m3fn or 4-bit e2m1 caches), :func:`kv_gather_fp4` (the 4-bit
   cache's read-back), :func:`kv_attend` (attention over those caches).
+* :func:`kv_store_latent`, :func:`kv_gather_latent`, :func:`kv_attend_latent` (a cache
+  of latent rows, which all query heads share as keys and values: its append, its
+  read-back and attention over it; 16-bit or e4m3fn rows).
 * :func:`kv_error_poll`, :func:`kv_error_reset`, :func:`kv_status_str`.
 
 The tensor-level functions take torch tensors (device memory and streams come
@@ -42,6 +45,7 @@ __all__ = [
     "kv_error_reset", "kv_status_str", "error_record", "load_library", "raw", "STRIDE_FIELDS",
     "fused_fp8_set_kv_buffer", "kv_store_fp8_dynamic_tensor", "DYNAMIC_TENSOR_WORK_BYTES",
     "kv_store_rope", "kv_gather_fp4", "kv_attend", "ATTEND_WORK_BYTES",
+    "kv_store_latent", "kv_gather_latent", "kv_attend_latent",
 ]
 
 
@@ -88,6 +92,16 @@ class _AttendStrides(ctypes.Structure):
     _fields_ = [(f, ctypes.c_int64) for f in (
         "q_token", "q_head", "o_token", "o_head", "kc_page", "kc_slot", "kc_head",
         "vc_page", "vc_slot", "vc_head")]
+
+
+class _LatentStrides(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int64) for f in (
+        "c_token", "r_token", "cache_page", "cache_slot", "scale_slot")]
+
+
+class _AttendLatentStrides(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int64) for f in (
+        "q_token", "q_head", "o_token", "o_head", "cache_page", "cache_slot", "scale_slot")]
 
 
 _lock = threading.Lock()
@@ -159,6 +173,17 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
                                   ctypes.POINTER(_BlockScales), ctypes.c_float, I64, I64, P, I64,
                                   P, P]
         lib.kv_attend.restype = I32
+        lib.kv_store_latent.argtypes = [P, P, P, P, I32, I64, I64, I32, I32, I32,
+                                        ctypes.POINTER(_LatentStrides), I64, I64, P, ctypes.c_float,
+                                        ctypes.POINTER(_Rope), I32, P, P, P]
+        lib.kv_store_latent.restype = I32
+        lib.kv_gather_latent.argtypes = [P, P, P, P, I32, I64, I64, I32, I32,
+                                         ctypes.POINTER(_LatentStrides), I64, I64, I32, P, P]
+        lib.kv_gather_latent.restype = I32
+        lib.kv_attend_latent.argtypes = [P, P, P, P, P, P, I64, I64, P, P, I32, I64, I32, I32, I32,
+                                         I32, ctypes.POINTER(_AttendLatentStrides), I64, I64, I32,
+                                         ctypes.c_float, P, I64, P, P]
+        lib.kv_attend_latent.restype = I32
         lib.kv_store_noalloc.argtypes = [P, P, P, P, P, I32, I64, I64, I32, I32, I32,
                                          ctypes.POINTER(_Strides), I64, I32,
                                          ctypes.POINTER(I64), ctypes.POINTER(I64), P]
@@ -349,6 +374,38 @@ class raw:
             num_pages, fmt, k_scale, v_scale,
             None if scales is None else ctypes.byref(_BlockScales(*scales)), sm_scale, window,
             sinks, work, work_bytes, d_err, stream)
+
+    @staticmethod
+    def kv_store_latent(c, r, cache, indices, index_dtype, index_stride, num_tokens, latent_dim,
+                        rope_dim, src_dtype, strides: Optional[Sequence[int]], page_size,
+                        size_limit, weight, eps, rope: Optional[Sequence], fmt, scales, d_err,
+                        stream) -> int:
+        """``strides`` and ``rope``: the fields of kv_latent_strides / kv_rope in order."""
+        return load_library().kv_store_latent(
+            c, r, cache, indices, index_dtype, index_stride, num_tokens, latent_dim, rope_dim,
+            src_dtype, None if strides is None else ctypes.byref(_LatentStrides(*strides)), page_size,
+            size_limit, weight, eps, None if rope is None else ctypes.byref(_Rope(*rope)), fmt, scales,
+            d_err, stream)
+
+    @staticmethod
+    def kv_gather_latent(cache, scales, out, indices, index_dtype, index_stride, num_tokens,
+                         row_dim, out_dtype, strides: Optional[Sequence[int]], page_size,
+                         size_limit, fmt, d_err, stream) -> int:
+        return load_library().kv_gather_latent(
+            cache, scales, out, indices, index_dtype, index_stride, num_tokens, row_dim, out_dtype,
+            None if strides is None else ctypes.byref(_LatentStrides(*strides)), page_size, size_limit,
+            fmt, d_err, stream)
+
+    @staticmethod
+    def kv_attend_latent(q, out, lse, cache, scales, page_table, table_stride, table_width, seq_lens,
+                         q_start, num_seqs, num_q_tokens, num_q_heads, row_dim, latent_dim, dtype,
+                         strides: Optional[Sequence[int]], page_size, num_pages, fmt, sm_scale, work,
+                         work_bytes, d_err, stream) -> int:
+        return load_library().kv_attend_latent(
+            q, out, lse, cache, scales, page_table, table_stride, table_width, seq_lens, q_start,
+            num_seqs, num_q_tokens, num_q_heads, row_dim, latent_dim, dtype,
+            None if strides is None else ctypes.byref(_AttendLatentStrides(*strides)), page_size,
+            num_pages, fmt, sm_scale, work, work_bytes, d_err, stream)
 
     @staticmethod
     def kv_store_noalloc(k, v, k_cache, v_cache, indices, index_dtype, index_stride,
@@ -1078,4 +1135,208 @@ def kv_attend(q, k_cache, v_cache, page_table, seq_lens, *, q_start=None, page_s
         _stream_handle(stream, device))
     if rc:
         _check(rc, "kv_attend")
+    return out
+
+
+# ---------------------------------------------------------------------------
+# A cache of latent rows
+# ---------------------------------------------------------------------------
+
+LATENT_FORMATS = {None: 0, "e4m3fn": 1}
+
+
+def _latent_cache(cache, page_size, fmt, dtype):
+    """(page, slot) byte strides, slots and row dims of a [slots, 1, D] or [pages, page_size, 1, D]
+    cache of format ``fmt`` (None: of ``dtype``)."""
+    if fmt not in LATENT_FORMATS:
+        raise ValueError(f"fmt must be one of {list(LATENT_FORMATS)}")
+    if fmt is None and cache.dtype is not dtype:
+        raise TypeError("without a format the cache has the rows' dtype")
+    D = cache.shape[-1] if cache.dim() else 0
+    page, slot, _, dim, slots, H = _cache_strides(cache, page_size, D, 1 if fmt else 2, "cache")
+    if H != 1 or (dim != cache.element_size() and D > 1):
+        raise ValueError("a latent cache has one head, with contiguous dims")
+    return page, slot, slots, D
+
+
+def _latent_scales(scales, fmt, slots):
+    """(pointer, floats between slots) of the per-slot scales: [slots] or [slots, 1]."""
+    if fmt is None:
+        if scales is not None:
+            raise ValueError("caches of the rows' dtype take no scales")
+        return None, 1
+    import torch
+    if scales is None or scales.dtype is not torch.float32:
+        raise TypeError("an e4m3fn cache needs fp32 scales")
+    if tuple(scales.shape) not in ((slots,), (slots, 1)):
+        raise ValueError("scales must be [slots] or [slots, 1]")
+    return scales.data_ptr(), scales.stride(0) if slots > 1 else 1
+
+
+def kv_store_latent(c, r, cache, indices, positions=None, cos_sin=None, *, weight=None, eps: float = 1e-6,
+                    q=None, q_out=None, page_size: int = 1, interleaved: bool = False,
+                    fmt: Optional[str] = None, scales=None, size_limit: Optional[int] = None, err=None,
+                    stream=None):
+    """Form the latent rows of new tokens and write them to a cache of latent rows.
+
+    ``c``: bf16 or fp16 [T, L], the latent dims; ``r``: [T, R] of the same dtype, the rotary dims
+    (None: R = 0; both may be columns of one projection). With ``weight`` [L] the latent dims are
+    divided by their root mean square (of which ``eps`` is added to the square) and multiplied by
+    it. The first ``cos_sin.shape[1]`` rotary dims are rotated by ``positions[t]`` as in
+    :func:`kv_store_rope`. ``q`` (optional): the rotary dims of the tokens' queries, [T, HQ, R],
+    rotated into ``q_out`` (a new tensor on the cache's device if None; may be ``q``, or the rotary
+    columns of whole query rows), which is returned.
+
+    ``cache``: [slots, 1, L + R] or [pages, page_size, 1, L + R] with any slot and page strides.
+    ``fmt``: None (the rows' dtype) or "e4m3fn" (1-byte elements; ``scales``: fp32 [slots] or
+    [slots, 1], which takes each row's largest magnitude / 448). Tokens whose slot or position is
+    out of range are skipped and counted in ``err``.
+    """
+    import torch
+    dtype = c.dtype
+    bf16 = _is_bf16(dtype)
+    if c.dim() != 2 or (c.shape[1] > 1 and c.stride(1) != 1):
+        raise ValueError("c must be [T, L] with contiguous dims")
+    T, L = c.shape
+    if r is None:
+        R = 0
+        if q is not None or positions is not None or cos_sin is not None:
+            raise ValueError("positions, cos_sin and q belong to rotary dims (r)")
+    else:
+        if r.dim() != 2 or r.shape[0] != T or r.dtype is not dtype or (r.shape[1] > 1 and r.stride(1) != 1):
+            raise ValueError("r must be [T, R] of c's dtype with contiguous dims")
+        R = r.shape[1]
+        if positions is None or cos_sin is None:
+            raise ValueError("rotary dims need positions and cos_sin")
+    page, slot, slots, D = _latent_cache(cache, page_size, fmt, dtype)
+    if D != L + R:
+        raise ValueError(f"cache rows of {D} dims, {L} + {R} expected")
+    if indices.shape != (T,):
+        raise ValueError("indices must hold one entry per row")
+    idt, istride = _index_args(indices)
+    if weight is not None and (weight.dtype is not dtype or tuple(weight.shape) != (L,) or not weight.is_contiguous()):
+        raise ValueError("weight must be a contiguous [L] of c's dtype")
+    sc, sc_slot = _latent_scales(scales, fmt, slots)
+    device = cache.device
+    rope = None
+    if R:
+        if positions.shape != (T,):
+            raise ValueError("positions must hold one entry per row")
+        pdt, pstride = _index_args(positions)
+        rows, rot = cos_sin.shape if cos_sin.dim() == 2 else (0, -1)
+        tstride, tdim = cos_sin.stride() if rot >= 0 else (0, 0)
+        if (tdim != 1 and rot > 1) or rot < 0 or cos_sin.dtype is not torch.float32:
+            raise TypeError("cos_sin must be fp32 [max_position, R] with contiguous rows")
+        qa = (None, None, 0, 0, 0, 0, 0)
+        if q is not None:
+            if q.dim() != 3 or q.shape[0] != T or q.shape[2] != R or q.dtype is not dtype or (R > 1 and q.stride(2) != 1):
+                raise ValueError("q must be [T, HQ, R] of c's dtype with contiguous dims")
+            if q_out is None:
+                with _on_stream(stream, device):  # (q itself may be page-locked host memory)
+                    q_out = torch.empty(q.shape, dtype=dtype, device=device)
+            if q_out.shape != q.shape or q_out.dtype is not dtype or (R > 1 and q_out.stride(2) != 1):
+                raise ValueError("q_out must be like q, with contiguous dims")
+            if q.shape[1]:
+                qa = (q.data_ptr(), q_out.data_ptr(), q.shape[1], q.stride(0) * 2, q.stride(1) * 2,
+                      q_out.stride(0) * 2, q_out.stride(1) * 2)
+        rope = (cos_sin.data_ptr(), tstride if rows > 1 else rot, rows, positions.data_ptr(), pdt, pstride, rot,
+                1 if interleaved else 0, *qa)
+    if q is None and q_out is not None:
+        raise ValueError("q_out without q")
+    rec = err if err is not None else _default_record(device)
+    rc = raw.kv_store_latent(
+        c.data_ptr(), r.data_ptr() if R else None, cache.data_ptr(), indices.data_ptr(), idt, istride, T, L, R, bf16,
+        (c.stride(0) * 2, r.stride(0) * 2 if R else 0, page, slot, sc_slot), page_size,
+        slots if size_limit is None else size_limit, None if weight is None else weight.data_ptr(), eps, rope,
+        LATENT_FORMATS[fmt], sc, rec.data_ptr(), _stream_handle(stream, device))
+    if rc:
+        _check(rc, "kv_store_latent")
+    return q_out
+
+
+def kv_gather_latent(cache, out, indices, *, page_size: int = 1, fmt: Optional[str] = None, scales=None,
+                     size_limit: Optional[int] = None, err=None, stream=None) -> None:
+    """Rows of a cache of latent rows (see :func:`kv_store_latent`) back: row t of ``out`` [T, L + R],
+    bf16 or fp16, takes the row of ``indices[t]``, dequantised for "e4m3fn"."""
+    if out.dim() != 2 or (out.shape[1] > 1 and out.stride(1) != 1):
+        raise ValueError("out must be [T, L + R] with contiguous dims")
+    bf16 = _is_bf16(out.dtype)
+    page, slot, slots, D = _latent_cache(cache, page_size, fmt, out.dtype)
+    if out.shape[1] != D:
+        raise ValueError(f"cache rows of {D} dims, output rows of {out.shape[1]}")
+    idt, istride = _index_args(indices)
+    n = indices.shape[0]
+    if n > out.shape[0]:
+        raise ValueError("fewer output rows than indices")
+    sc, sc_slot = _latent_scales(scales, fmt, slots)
+    rec = err if err is not None else _default_record(cache.device)
+    rc = raw.kv_gather_latent(cache.data_ptr(), sc, out.data_ptr(), indices.data_ptr(), idt, istride, n, D, bf16,
+                              (out.stride(0) * 2, 0, page, slot, sc_slot), page_size,
+                              slots if size_limit is None else size_limit, LATENT_FORMATS[fmt], rec.data_ptr(),
+                              _stream_handle(stream, cache.device))
+    if rc:
+        _check(rc, "kv_gather_latent")
+
+
+def kv_attend_latent(q, cache, page_table, seq_lens, *, latent_dim: int, q_start=None, page_size=None,
+                     sm_scale: Optional[float] = None, fmt: Optional[str] = None, scales=None, out=None, lse=None,
+                     work=None, err=None, stream=None):
+    """Causal attention of ragged queries over a paged cache of latent rows; returns ``out``.
+
+    ``q``: bf16 or fp16 [tokens, HQ, D], D the cache rows' dims; ``out``: [tokens, HQ, latent_dim].
+    Every head reads the same rows, whose first ``latent_dim`` dims are the values. ``cache``, ``fmt``
+    and ``scales`` as in :func:`kv_store_latent` (``page_size`` is needed with a [slots, 1, D] cache);
+    ``page_table``, ``seq_lens``, ``q_start``, ``lse``, ``work`` and ``err`` as in :func:`kv_attend`.
+    ``sm_scale``: of the scores (1 / sqrt(D) if None).
+    """
+    import torch
+    dtype = q.dtype
+    bf16 = _is_bf16(dtype)
+    if q.dim() != 3 or (q.shape[2] > 1 and q.stride(2) != 1):
+        raise ValueError("q must be [tokens, HQ, D] with contiguous dims")
+    T, HQ, D = q.shape
+    if page_size is None:
+        if cache.dim() != 4:
+            raise ValueError("page_size is needed with [slots, 1, D] caches")
+        page_size = cache.shape[1]
+    page, slot, slots, Dc = _latent_cache(cache, page_size, fmt, dtype)
+    if Dc != D or not 1 <= latent_dim <= D:
+        raise ValueError(f"queries of {D} dims, cache rows of {Dc}, {latent_dim} of them values")
+    sc, sc_slot = _latent_scales(scales, fmt, slots)
+    tst = page_table.stride()
+    if len(tst) != 2 or page_table.dtype is not torch.int32 or tst[1] != 1:
+        raise TypeError("page_table must be int32 [B, width] with contiguous rows")
+    B, width = page_table.shape
+    if seq_lens.dtype is not torch.int32 or seq_lens.shape != (B,) or (B > 1 and seq_lens.stride(0) != 1):
+        raise TypeError("seq_lens must be a contiguous int32 [B]")
+    if q_start is not None:
+        if q_start.dtype is not torch.int32 or q_start.shape != (B + 1,) or q_start.stride(0) != 1:
+            raise TypeError("q_start must be a contiguous int32 [B + 1]")
+    elif T != B:
+        raise ValueError("without q_start there is one query row per sequence")
+    device = q.device
+    shape = (T, HQ, latent_dim)
+    if out is None:
+        with _on_stream(stream, device):
+            out = torch.empty(shape, dtype=dtype, device=device)
+    if tuple(out.shape) != shape or out.dtype is not dtype or (latent_dim > 1 and out.stride(2) != 1):
+        raise ValueError("out must be [tokens, HQ, latent_dim] of q's dtype, with contiguous dims")
+    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (T, HQ) or not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous fp32 [tokens, HQ]")
+    if work is None:
+        with _on_stream(stream, device):
+            work = torch.empty(ATTEND_WORK_BYTES, dtype=torch.uint8, device=device)
+            work[:ATTEND_HEAD_BYTES].zero_()
+    elif not work.is_contiguous():
+        raise ValueError("work must be contiguous")
+    rec = err if err is not None else _default_record(device)
+    rc = raw.kv_attend_latent(
+        q.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(), cache.data_ptr(), sc,
+        page_table.data_ptr(), tst[0] if B > 1 else width, width, seq_lens.data_ptr(),
+        None if q_start is None else q_start.data_ptr(), B, T, HQ, D, latent_dim, bf16,
+        (q.stride(0) * 2, q.stride(1) * 2, out.stride(0) * 2, out.stride(1) * 2, page, slot, sc_slot), page_size,
+        slots // page_size, LATENT_FORMATS[fmt], 1.0 / math.sqrt(D) if sm_scale is None else sm_scale, work.data_ptr(),
+        work.numel() * work.element_size(), rec.data_ptr(), _stream_handle(stream, device))
+    if rc:
+        _check(rc, "kv_attend_latent")
     return out

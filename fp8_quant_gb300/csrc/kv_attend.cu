@@ -87,21 +87,6 @@ bool tiles_pay(const AttendParams& p, kv_cache_format format, int64_t rows, int6
   return tile < 11.0 + 0.625 * heads_of_cta(p.kv_heads, kSplitWarps) + blocks * pass;
 }
 
-FastDiv fast_div(uint32_t d) {
-  FastDiv f{d, 0u, 0u};
-  uint32_t log = 0;
-  while ((uint64_t{1} << log) < d) ++log;  // ceil(log2 d)
-  if ((d & (d - 1u)) == 0u) {
-    f.shift = log;
-    return f;
-  }
-  // ceil(2^(31 + log) / d) fits 32 bits, and its error is below 2^log / 2^31
-  // per unit of x, exact for x < 2^31
-  f.shift = log - 1;
-  f.mul = static_cast<uint32_t>(((uint64_t{1} << (31 + log)) + d - 1) / d);
-  return f;
-}
-
 }  // namespace
 }  // namespace kvimpl
 

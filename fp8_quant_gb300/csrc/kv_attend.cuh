@@ -16,6 +16,21 @@ struct FastDiv {
   }
 };
 
+inline FastDiv fast_div(uint32_t d) {
+  FastDiv f{d, 0u, 0u};
+  uint32_t log = 0;
+  while ((uint64_t{1} << log) < d) ++log;  // ceil(log2 d)
+  if ((d & (d - 1u)) == 0u) {
+    f.shift = log;
+    return f;
+  }
+  // ceil(2^(31 + log) / d) fits 32 bits, and its error is below 2^log / 2^31
+  // per unit of x, exact for x < 2^31
+  f.shift = log - 1;
+  f.mul = static_cast<uint32_t>(((uint64_t{1} << (31 + log)) + d - 1) / d);
+  return f;
+}
+
 struct AttendParams {
   const uint8_t *q, *k, *v;
   uint8_t* out;

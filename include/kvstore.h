@@ -603,6 +603,117 @@ kv_status kv_attend(const void *q, void *out, float *lse, const void *k_cache,
                     void *work, int64_t work_bytes, kv_error_record *d_err, kv_stream_t stream);
 
 /*
+ * A cache of latent rows: one row per token for all query heads, latent_dim
+ * dims that attention takes as key and as value, and behind them rope_dim
+ * rotated dims that it takes as key only.  The library's 1 x 576 rows (config
+ * "odd") are 512 + 64 such dims.  A row lies at
+ *     cache + (s / page_size) * cache_page + (s % page_size) * cache_slot
+ * for slot s, dims contiguous: KV_CACHE_SRC elements of the source type, or
+ * KV_CACHE_E4M3FN bytes with one fp32 scale per slot, scales[s * scale_slot]
+ * (a row's value is code * scale).
+ */
+typedef struct kv_latent_strides {
+    int64_t c_token, r_token;        /* bytes between tokens' latent and rotary inputs (dims contiguous) */
+    int64_t cache_page, cache_slot;  /* bytes */
+    int64_t scale_slot;              /* floats, >= 1 (KV_CACHE_E4M3FN) */
+} kv_latent_strides;
+
+/*
+ * kv_store_latent -- form the latent rows of new tokens and write them to the
+ * cache; rotate the rotary dims of the tokens' queries.
+ *
+ * For token t:
+ *   n = c_t, or with `weight`:  n = fl(fl(c_t * g) * weight),
+ *       g = 1 / sqrt(mean(c_t^2) + eps), the mean over the latent dims;
+ *   r' = r_t rotated as kv_store_rope does with `rope` (its first rotary_dim
+ *       dims, by the token's position);
+ *   KV_CACHE_SRC     every element of [n | r'] rounded once to the source type
+ *                    (elements that neither step touches keep their bytes);
+ *   KV_CACHE_E4M3FN  m = max |[n | r']| (NaN ignored), scale = fl(m / 448),
+ *                    codes e4m3fn(fl(x * fl(448 / m))), saturating; scale and
+ *                    factor are 1 where m is 0.
+ * All in fp32; the mean is a sum of fp32 squares (its relative error is below
+ * 2^-18 for up to 1,024 dims).
+ * rope->q (optional): rotary dims of the queries, [num_tokens, num_q_heads,
+ * rope_dim], rotated into rope->q_out, whose token and head strides may be those
+ * of whole query rows.
+ *
+ *   c, r         [num_tokens, latent_dim] and [num_tokens, rope_dim] of
+ *                src_dtype; r and rope may be NULL when rope_dim is 0.
+ *   weight       NULL, or latent_dim elements of src_dtype.  eps >= 0.
+ *   rope         as in kv_store_rope; rotary_dim <= rope_dim.
+ * Tokens whose slot or position is out of range: as in kv_store_rope.  Memory
+ * kinds as there; weight and scales are device memory.  q_out may be q.
+ * latent_dim >= 1, rope_dim >= 0, both together at most 1,024 (else
+ * KV_ERR_UNSUPPORTED).  Of tokens that share a slot, codes and scale may be different ones'.
+ */
+kv_status kv_store_latent(const void *c, const void *r, void *cache, const void *indices,
+                          kv_index_dtype index_dtype, int64_t index_stride, int64_t num_tokens,
+                          int32_t latent_dim, int32_t rope_dim, kv_src_dtype src_dtype,
+                          const kv_latent_strides *strides, int64_t page_size, int64_t size_limit,
+                          const void *weight, float eps, const kv_rope *rope,
+                          kv_cache_format format, float *scales, kv_error_record *d_err,
+                          kv_stream_t stream);
+
+/*
+ * kv_gather_latent -- cache rows back: row t of out takes the row_dim dims of
+ * slot indices[t], the bytes as they are (KV_CACHE_SRC) or fl16(fl(code *
+ * scale)).  strides->c_token is out's token stride; r_token is not used.  An
+ * out-of-range slot leaves its row untouched and is counted.  `out` and the
+ * slot ids may be page-locked host memory.
+ */
+kv_status kv_gather_latent(const void *cache, const float *scales, void *out, const void *indices,
+                           kv_index_dtype index_dtype, int64_t index_stride, int64_t num_tokens,
+                           int32_t row_dim, kv_src_dtype out_dtype, const kv_latent_strides *strides,
+                           int64_t page_size, int64_t size_limit, kv_cache_format format,
+                           kv_error_record *d_err, kv_stream_t stream);
+
+/* Byte strides of kv_attend_latent, and floats between slots' scales. */
+typedef struct kv_attend_latent_strides {
+    int64_t q_token, q_head;
+    int64_t o_token, o_head;
+    int64_t cache_page, cache_slot;
+    int64_t scale_slot;
+} kv_attend_latent_strides;
+
+/*
+ * kv_attend_latent -- causal attention of ragged queries over a paged cache of
+ * latent rows.
+ *
+ * Sequences, queries, pages and positions are kv_attend's.  Every query head
+ * reads the same rows k_j of row_dim dims, whose first latent_dim are the
+ * values:
+ *     s_j = sm_scale * sum_{d < row_dim} q_d k_jd,
+ *     out = sum_j exp(s_j) k_j[0 .. latent_dim) / sum_j exp(s_j),
+ * over keys j <= the query's position; lse as in kv_attend.  A row that sees no
+ * key is 0 with lse -infinity.
+ * Statistics and sums are fp32.  16-bit rows are multiplied in their type, e4m3fn
+ * codes in fp16 (exact) against queries brought into fp16's range by a power of
+ * two per row; a row's scale multiplies its score and its weight in fp32.  The
+ * weights meet the values as 16-bit operands (fp16, or bf16 for a bf16 cache),
+ * rounded once: up to 2^-9 (bf16) or 2^-12 (fp16) of sum p_j |k_j| / sum p_j
+ * beside the output's own rounding.  fp16 weights begin at 2^7 and end at 2^-24.
+ *
+ *   q            [num_q_tokens, num_q_heads, row_dim] of `dtype`.
+ *   out          [num_q_tokens, num_q_heads, latent_dim]; must not overlap q or the cache.
+ *   row_dim      1 .. 1024; latent_dim 1 .. row_dim.  Multiples of 16 (row_dim,
+ *                up to 576) and 8 (latent_dim, up to 512) with 16-byte aligned
+ *                bases and strides take the tensor-core kernel; the rest a general one.
+ *   format       KV_CACHE_SRC or KV_CACHE_E4M3FN (with scales).
+ *   work         as in kv_attend (KV_ATTEND_WORK_BYTES is always enough).
+ * Page tables, lengths, q_start, waits, errors, determinism and the workspace's
+ * head are as in kv_attend.
+ */
+kv_status kv_attend_latent(const void *q, void *out, float *lse, const void *cache,
+                           const float *scales, const int32_t *page_table, int64_t table_stride,
+                           int64_t table_width, const int32_t *seq_lens, const int32_t *q_start,
+                           int32_t num_seqs, int64_t num_q_tokens, int32_t num_q_heads,
+                           int32_t row_dim, int32_t latent_dim, kv_src_dtype dtype,
+                           const kv_attend_latent_strides *strides, int64_t page_size,
+                           int64_t num_pages, kv_cache_format format, float sm_scale, void *work,
+                           int64_t work_bytes, kv_error_record *d_err, kv_stream_t stream);
+
+/*
  * kv_store_noalloc -- kv_store for callers that cannot allocate device memory.
  * The pages have no counterpart; this entry point exists for this library's
  * users only.
