@@ -20,7 +20,8 @@ SOURCES = [os.path.join(CSRC, f + ".cu") for f in (
     "kvstore", "kv_gather", "kv_scale", "kv_fp8_ex", "kv_rope", "kv_async", "kv_attend",
     "kv_attend_split_bf16", "kv_attend_split_f16", "kv_attend_split_e4m3", "kv_attend_split_e2m1",
     "kv_attend_stream_bf16", "kv_attend_stream_f16", "kv_attend_stream_e4m3", "kv_attend_stream_e2m1",
-    "kv_attend_tile_src", "kv_attend_tile_quant", "kv_latent", "kv_attend_latent")]
+    "kv_attend_tile_src", "kv_attend_tile_quant", "kv_latent", "kv_attend_latent", "kv_attend_latent_src",
+    "kv_attend_latent_e4m3")]
 SRC = SOURCES[0]
 HEADER = os.path.join(ROOT, "include", "kvstore.h")
 LIBDIR = os.path.join(HERE, "lib")

@@ -1,12 +1,14 @@
 // Attention over a paged cache of latent rows (kv_attend_latent): argument
 // checks, the choice of the kernel, and the general kernel.
 //
+//  * kv_attend_latent_tile  (kv_attend_latent_tile.cuh) row dims that are multiples of 16 up to 576, latent
+//                           dims multiples of 8 up to 512, 16-byte aligned bases and strides.
 //  * kv_latent_attend_rows  any dims, alignment and stride: one warp per query row
 //                           and head, one key after the other.
 #include <cmath>
 #include <climits>
 
-#include "kv_attend_latent.cuh"
+#include "kv_attend_latent_tile.cuh"
 
 namespace kvimpl {
 namespace {
@@ -32,7 +34,7 @@ __global__ void __launch_bounds__(kThreads) kv_latent_attend_rows(const __grid_c
     }
     const AttendSeq s = attend_seq(a, b, h == 0 && (threadIdx.x & 31u) == 0);
     if (t < s.q0 || t >= s.q0 + s.nq) continue;
-    attend_latent_row<FMT, ND>(p, b, s.len - s.nq + (t - s.q0), t, h);
+    attend_latent_row<FMT, ND>(p, b, s.len - s.nq + (t - s.q0), t, h, 0, p.latent);
   }
 }
 
@@ -115,5 +117,25 @@ extern "C" kv_status kv_attend_latent(const void* q, void* out, float* lse, cons
   p.scale_slot = s->scale_slot;
   p.latent = latent_dim;
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  auto fits = [](int64_t x) { return x > INT_MIN && x < INT_MAX; };
+  if (row_dim % 16 == 0 && row_dim <= 64 * kLatMaxChunks && latent_dim % 8 == 0 && latent_dim <= 512 && ((q_bits | c_bits) & 15u) == 0 &&
+      fits(s->cache_page) && fits(s->cache_slot)) {
+    LatentTileParams tp = {};
+    tp.l = p;
+    tp.page_stride = static_cast<int32_t>(s->cache_page);
+    tp.slot_stride = static_cast<int32_t>(s->cache_slot);
+    tp.chunks = (row_dim + 63) / 64;
+    tp.ksteps = row_dim / 16;
+    tp.blocks = (latent_dim + 127) / 128;
+    const int64_t rows = (num_q_tokens + num_seqs - 1) / num_seqs * num_q_heads;
+    const bool few = rows <= 32;
+    if (fp8) return latent_tile_e4m3(tp, few, work, work_bytes, a.max_len, stream);
+    // TMA: the longest runs of 8 to 64 keys that pages are cut into
+    int box = kLatKeys;
+    while (page_size % box != 0) box /= 2;
+    if (box >= 8 && cache_map(&tp.map, cache, 2, a.bf16, row_dim, page_size, 1, num_pages, s->cache_slot, 0, s->cache_page, 64, box, 1, true))
+      tp.box = box;
+    return latent_tile_src(tp, few, work, work_bytes, a.max_len, stream);
+  }
   return fp8 ? launch_rows_any<KV_CACHE_E4M3FN>(p, stream) : launch_rows_any<KV_CACHE_SRC>(p, stream);
 }

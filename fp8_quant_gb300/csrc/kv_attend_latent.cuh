@@ -21,12 +21,12 @@ __device__ __forceinline__ float row_scale(const LatentParams& p, int32_t id, ui
 }
 
 // One query row by one warp, any layout: lane l owns dims l, l + 32, ... (ND of them). Reads the
-// visible keys one by one and nothing else.
+// visible keys one by one and nothing else. Writes output dims d0 .. d1 - 1, and the lse with dim 0.
 template <int FMT, int ND>
-__device__ __noinline__ void attend_latent_row(const LatentParams& lp, int32_t b, int32_t pos, int32_t t, int32_t h) {
+__device__ __noinline__ void attend_latent_row(const LatentParams& lp, int32_t b, int32_t pos, int32_t t, int32_t h, int32_t d0, int32_t d1) {
   const AttendParams& p = lp.a;
   const uint32_t lane = threadIdx.x & 31u;
-  const uint32_t D = static_cast<uint32_t>(p.head_dim), L = static_cast<uint32_t>(lp.latent);
+  const uint32_t D = static_cast<uint32_t>(p.head_dim);
   const uint8_t* q = p.q + t * p.q_token + h * p.q_head;
   float qv[ND], o[ND];
 #pragma unroll
@@ -72,9 +72,9 @@ __device__ __noinline__ void attend_latent_row(const LatentParams& lp, int32_t b
 #pragma unroll
   for (int x = 0; x < ND; ++x) {
     const uint32_t d = lane + 32u * x;
-    if (d < L) out[d] = round16(o[x] * inv, p.bf16);
+    if (d >= static_cast<uint32_t>(d0) && d < static_cast<uint32_t>(d1)) out[d] = round16(o[x] * inv, p.bf16);
   }
-  if (p.lse && lane == 0)
+  if (p.lse && lane == 0 && d0 == 0)
     p.lse[static_cast<int64_t>(t) * p.q_heads + h] = any ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
