@@ -130,7 +130,7 @@ extern "C" kv_status kv_attend_latent(const void* q, void* out, float* lse, cons
     const int64_t rows = (num_q_tokens + num_seqs - 1) / num_seqs * num_q_heads;
     const bool few = rows <= 32;
     if (fp8) return latent_tile_e4m3(tp, few, work, work_bytes, a.max_len, stream);
-    // TMA: the longest runs of 8 to 64 keys that pages are cut into
+    // TMA: the longest runs of 8 to 32 keys that pages are cut into
     int box = kLatKeys;
     while (page_size % box != 0) box /= 2;
     if (box >= 8 && cache_map(&tp.map, cache, 2, a.bf16, row_dim, page_size, 1, num_pages, s->cache_slot, 0, s->cache_page, 64, box, 1, true))

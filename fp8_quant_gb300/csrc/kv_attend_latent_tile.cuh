@@ -46,11 +46,10 @@
 
 namespace kvimpl {
 
-constexpr int kLatKeys = 64;        // keys of a tile
-constexpr int kLatChunk = 8192;     // bytes of 64 keys x 64 dims of 16 bits
+constexpr int kLatKeys = 32;        // keys of a tile
+constexpr int kLatChunk = kLatKeys * 128;  // bytes of its keys x 64 dims of 16 bits
 constexpr int kLatMaxChunks = 9;    // row dims up to 576
-constexpr int kLatMaxStages = 4;
-constexpr int kLatPairs = 5;        // chunks are given back in pairs
+constexpr int kLatMaxStages = 8;
 
 struct LatentTileParams {
   LatentParams l;
@@ -87,19 +86,20 @@ struct LatentSeg {
 template <int NR>
 struct LatentSmem {  // behind the stages
   static constexpr int kP = NR * 128;
-  static constexpr int kBars = 64;
+  static constexpr int kBars = 32;
   static constexpr int kSeg = 2;
   static __host__ __device__ constexpr int q_bytes(int chunks) { return chunks * NR * 128; }
   // offsets behind Q and P
   static constexpr int kOffBars = 0, kOffSegs = kOffBars + kBars * 8, kOffAlpha = kOffSegs + kSeg * 64,
                        kOffInv = kOffAlpha + 2 * NR * 4, kOffQf = kOffInv + NR * 4, kOffPlace = kOffQf + NR * 4,
-                       kOffMisc = kOffPlace + kLatKeys * 8, kOffValid = kOffMisc + 64, kOffScale = kOffValid + kLatMaxStages * 8;
+                       kOffMisc = kOffPlace + kLatKeys * 8, kOffValid = kOffMisc + 64, kOffScale = kOffValid + kLatMaxStages * 4;
   static __host__ __device__ constexpr int total(int chunks, int stages) {
     return stages * (chunks * kLatChunk + kLatKeys * 4) + q_bytes(chunks) + kP + kOffScale;
   }
 };
 static_assert(sizeof(LatentSeg) <= 64, "segments");
-static_assert(LatentSmem<64>::total(kLatMaxChunks, 2) <= 227 * 1024, "two stages of the widest rows fit");
+static_assert(LatentSmem<64>::total(kLatMaxChunks, 4) <= 227 * 1024, "four stages of the widest rows fit");
+static_assert(2 * kLatMaxStages + 13 <= LatentSmem<64>::kBars, "barriers");
 
 // Rows of the sequence's queries in blocks of NR, and tiles of each (an upper bound, at least one).
 struct LatentGeom {
@@ -141,18 +141,27 @@ __device__ __forceinline__ int32_t latent_cut(int64_t total, int32_t ctas, int32
   return 2;
 }
 
-// 16 lanes x 64 columns over the warp: thread (g, t) = (lane / 4, lane % 4) gets columns 8 i + 2 t, + 1 of
+// 16 lanes x 32 columns over the warp: thread (g, t) = (lane / 4, lane % 4) gets columns 8 i + 2 t, + 1 of
 // rows g (r[4 i], r[4 i + 1]) and g + 8 (r[4 i + 2], r[4 i + 3]).
-__device__ __forceinline__ void tc_ld_rows(float (&s)[32], uint32_t addr) {
-  uint32_t r[32];
-#define KV_R4(i) "=r"(r[i]), "=r"(r[(i) + 1]), "=r"(r[(i) + 2]), "=r"(r[(i) + 3])
-  asm volatile("tcgen05.ld.sync.aligned.16x256b.x8.b32 "
-               "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+__device__ __forceinline__ void tc_ld_rows(float (&s)[16], uint32_t addr) {
+  uint32_t r[16];
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+               "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
                "tcgen05.wait::ld.sync.aligned;"
-               : KV_R4(0), KV_R4(4), KV_R4(8), KV_R4(12), KV_R4(16), KV_R4(20), KV_R4(24), KV_R4(28) : "r"(addr) : "memory");
-#undef KV_R4
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+                 "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]) : "r"(addr) : "memory");
 #pragma unroll
-  for (int i = 0; i < 32; ++i) s[i] = __uint_as_float(r[i]);
+  for (int i = 0; i < 16; ++i) s[i] = __uint_as_float(r[i]);
+}
+
+// bar_try without a pause.
+__device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\t"
+               "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+               "selp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  return ok != 0u;
 }
 
 __device__ __forceinline__ float lg2_fast(float x) {
@@ -184,17 +193,16 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
   const uint32_t p_at = q_at + static_cast<uint32_t>(S::q_bytes(p.chunks));
   const uint32_t small = p_at + S::kP;
   uint8_t* const small_ptr = smem_raw + (small - ring);
-  const uint32_t nbars = static_cast<uint32_t>(p.stages * p.chunks);
-  const uint32_t full = small + S::kOffBars, empty = full + 8 * nbars, q_full = empty + 8 * kLatPairs * static_cast<uint32_t>(p.stages),
-                 s_full = q_full + 8, p_full = s_full + 16, pv_done = p_full + 8, seg_full = pv_done + 8, seg_empty = seg_full + 16,
-                 done = seg_empty + 16, load_bar = done + 8;
+  const uint32_t full = small + S::kOffBars, empty = full + 8 * kLatMaxStages, q_full = empty + 8 * kLatMaxStages, s_full = q_full + 8,
+                 p_full = s_full + 16, pv_done = p_full + 16, seg_full = pv_done + 16, seg_empty = seg_full + 16, done = seg_empty + 16,
+                 load_bar = done + 8;
   LatentSeg* const segs = reinterpret_cast<LatentSeg*>(small_ptr + S::kOffSegs);
   float* const sh_alpha = reinterpret_cast<float*>(small_ptr + S::kOffAlpha);   // [2][NR]
   float* const sh_inv = reinterpret_cast<float*>(small_ptr + S::kOffInv);
   float* const sh_qf = reinterpret_cast<float*>(small_ptr + S::kOffQf);
   int64_t* const sh_place = reinterpret_cast<int64_t*>(small_ptr + S::kOffPlace);
-  float* const sh_scale = reinterpret_cast<float*>(small_ptr + S::kOffScale);   // [stages][64]
-  uint64_t* const sh_valid = reinterpret_cast<uint64_t*>(small_ptr + S::kOffValid);
+  float* const sh_scale = reinterpret_cast<float*>(small_ptr + S::kOffScale);   // [stages][kLatKeys]
+  uint32_t* const sh_valid = reinterpret_cast<uint32_t*>(small_ptr + S::kOffValid);  // of a stage's keys, a bit each
   WaitState* const state = reinterpret_cast<WaitState*>(small_ptr + S::kOffMisc);
   uint32_t* const sh_tmem = reinterpret_cast<uint32_t*>(small_ptr + S::kOffMisc + 16);
   unsigned long long* const sh_bad = reinterpret_cast<unsigned long long*>(small_ptr + S::kOffMisc + 24);
@@ -206,14 +214,15 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   if (tid == 0) {
-    for (uint32_t i = 0; i < nbars; ++i) bar_init(full + 8 * i, 1);
-    for (int i = 0; i < kLatPairs * p.stages; ++i) bar_init(empty + 8 * i, 1);
+    for (int i = 0; i < p.stages; ++i) {
+      bar_init(full + 8 * i, 1);
+      bar_init(empty + 8 * i, 1);
+    }
     bar_init(q_full, 128);
-    bar_init(s_full, 1);
-    bar_init(s_full + 8, 1);
-    bar_init(p_full, 128);
-    bar_init(pv_done, 1);
     for (int i = 0; i < 2; ++i) {
+      bar_init(s_full + 8 * i, 1);
+      bar_init(p_full + 8 * i, 128);
+      bar_init(pv_done + 8 * i, 1);
       bar_init(seg_full + 8 * i, 1);
       bar_init(seg_empty + 8 * i, 5 + kLoaders);
     }
@@ -239,7 +248,7 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
     if (lane == 0u) bar_arrive(seg_empty + 8 * (k & 1u));
     return s->stop == 0;
   };
-  const uint32_t tm_s = tmem + 4 * NR;  // S, two buffers of 64 columns, behind O^T
+  const uint32_t tm_s = tmem + 4 * NR;  // S, two buffers of kLatKeys columns, behind O^T
 
   if (warp < 4) {
     // ======================================================================================
@@ -326,46 +335,45 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
       }
       for (int32_t j = seg.t0; j < seg.t1; ++j, ++T) {
         ok = ok && __all_sync(0xFFFFFFFFu, bar_wait(s_full + 8 * (T & 1u), (T >> 1) & 1u, state) &&
-                                               bar_wait(full + 8 * (stage * static_cast<uint32_t>(p.chunks)), phase, state));
+                                               bar_wait(full + 8 * stage, phase, state));
         tc_fence_after();
-        float s[32], kf[16], alpha[2] = {1.0f, 1.0f};  // scores, their keys' scales, factors of the rows' sums
+        float s[16], kf[8], alpha[2] = {1.0f, 1.0f};  // scores, their keys' scales, factors of the rows' sums
         bool grew = false;
         if (has_rows && ok) {
-          tc_ld_rows(s, tm_s + 64u * (T & 1u) + lanes);
+          tc_ld_rows(s, tm_s + kLatKeys * (T & 1u) + lanes);
           if constexpr (FMT != KV_CACHE_SRC) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < 4; ++i) {
               const float2 f = *reinterpret_cast<const float2*>(sh_scale + stage * kLatKeys + 8 * i + 2 * t);
               kf[2 * i] = f.x;
               kf[2 * i + 1] = f.y;
             }
 #pragma unroll
-            for (int i = 0; i < 32; ++i) s[i] *= kf[2 * (i / 4) + (i & 1)] * rs[(i >> 1) & 1];
+            for (int i = 0; i < 16; ++i) s[i] *= kf[2 * (i / 4) + (i & 1)] * rs[(i >> 1) & 1];
           }
-          const uint64_t valid = sh_valid[stage];
-          if (j * kLatKeys + kLatKeys - 1 > p_lo || valid != ~0ull) {
+          const uint32_t valid = sh_valid[stage];
+          if (j * kLatKeys + kLatKeys - 1 > p_lo || valid != ~0u) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               const int32_t n = pos[c] - j * kLatKeys + 1;  // the first n keys
-              const uint64_t see = (n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1ull) & valid;
-              const uint32_t lo = static_cast<uint32_t>(see >> (2 * t)), hi = static_cast<uint32_t>(see >> (32 + 2 * t));
+              const uint32_t see = ((n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u) & valid) >> (2 * t);
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
+              for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int x = 0; x < 2; ++x)
-                  if ((((i < 4 ? lo : hi) >> (8 * (i & 3) + x)) & 1u) == 0u) s[4 * i + 2 * c + x] = -INFINITY;
+                  if ((see >> (8 * i + x) & 1u) == 0u) s[4 * i + 2 * c + x] = -INFINITY;
             }
           }
-          float lv[16];
+          float lv[8];
           if constexpr (FMT != KV_CACHE_SRC) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) lv[i] = fmaxf(lg2_fast(fabsf(kf[i])), -100.0f);
+            for (int i = 0; i < 8; ++i) lv[i] = fmaxf(lg2_fast(fabsf(kf[i])), -100.0f);
           }
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             float x[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
               for (int y = 0; y < 2; ++y) x[y] = fmaxf(x[y], FMT == KV_CACHE_SRC ? s[4 * i + 2 * c + y] : s[4 * i + 2 * c + y] + lv[2 * i + y]);
             float top = fmaxf(x[0], x[1]);
@@ -390,14 +398,14 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
           ok = false;
           break;
         }
-        uint32_t pw[16];
+        uint32_t pw[8];
         if (has_rows) {
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             const float ref = m[c] == -INFINITY ? 0.0f : m[c];
             float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < 4; ++i) {
               float2 z = make_float2(s[4 * i + 2 * c], s[4 * i + 2 * c + 1]);
               if constexpr (FMT == KV_CACHE_SRC) z = fma2(z, rs[c], -ref); else z = add2(z, make_float2(-ref, -ref));
               float2 e = make_float2(exp2_fast(z.x), exp2_fast(z.y));
@@ -412,9 +420,10 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
             l[c] = __fmaf_rn(l[c], alpha[c], sum[0].x + sum[0].y);
           }
         }
-        if (T > 0u)  // P V of the last tile has read P and written O^T
-          ok = __all_sync(0xFFFFFFFFu, bar_wait(pv_done, (T - 1u) & 1u, state));
-        if (rescale && ok) {
+        if (T > 1u)  // P V of the last tile but one has read its P
+          ok = __all_sync(0xFFFFFFFFu, bar_wait(pv_done + 8 * (T & 1u), ((T >> 1) - 1u) & 1u, state));
+        if (rescale && ok) {  // and that of the last one has written O^T
+          ok = __all_sync(0xFFFFFFFFu, bar_wait(pv_done + 8 * ((T - 1u) & 1u), ((T - 1u) >> 1) & 1u, state));
           tc_fence_after();
           const float* f = sh_alpha + (T & 1u) * NR;
           for (int32_t b = 0; b < p.blocks; ++b)
@@ -433,13 +442,13 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
           for (int c = 0; c < 2; ++c) {
             const uint32_t r = static_cast<uint32_t>(r0 + 8 * c);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              asm volatile("st.shared.u32 [%0], %1;" ::"r"(p_at + r * 128u + ((i ^ (r & 7u)) << 4) + 4u * t), "r"(pw[2 * i + c]) : "memory");
+            for (int i = 0; i < 4; ++i)  // tiles take turns in the halves of P's rows
+              asm volatile("st.shared.u32 [%0], %1;" ::"r"(p_at + r * 128u + (((i + 4u * (T & 1u)) ^ (r & 7u)) << 4) + 4u * t), "r"(pw[2 * i + c]) : "memory");
           }
         }
         fence_async_shared();
         tc_fence_before();
-        bar_arrive(p_full);
+        bar_arrive(p_full + 8 * (T & 1u));
         if (++stage == static_cast<uint32_t>(p.stages)) {
           stage = 0u;
           phase ^= 1u;
@@ -458,7 +467,7 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
         if (has_rows && t == 0u) sh_inv[r0 + 8 * c] = l[c] < INFINITY ? __fdiv_rn(1.0f, l[c]) : NAN;
       }
       if (live) {
-        ok = __all_sync(0xFFFFFFFFu, bar_wait(pv_done, (T - 1u) & 1u, state));
+        ok = __all_sync(0xFFFFFFFFu, bar_wait(pv_done + 8 * ((T - 1u) & 1u), ((T - 1u) >> 1) & 1u, state));
         tc_fence_after();
       }
       if (any_of_softmax(!ok)) break;
@@ -544,54 +553,83 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
     // ======================================================================================
     // the products
     // ======================================================================================
-    const uint32_t qk_desc = (1u << 4) | (kBF16 ? 1u << 7 | 1u << 10 : 0u) | ((64u >> 3) << 17) | ((64u >> 4) << 24);
+    const uint32_t qk_desc = (1u << 4) | (kBF16 ? 1u << 7 | 1u << 10 : 0u) | ((static_cast<uint32_t>(kLatKeys) >> 3) << 17) | ((64u >> 4) << 24);
     const uint32_t pv_desc = (1u << 4) | (kBF16 ? 1u << 7 | 1u << 10 : 0u) | (1u << 15) | ((static_cast<uint32_t>(NR) >> 3) << 17) | ((128u >> 4) << 24);
     auto wait = [&](uint32_t bar, uint32_t parity) {
       if (ok) ok = __all_sync(0xFFFFFFFFu, bar_wait(bar, parity, state));
-      if (ok) tc_fence_after();
+      tc_fence_after();
     };
-    const uint64_t q_desc = smem_desc(q_at, 16), k_desc = smem_desc(ring, 16), v_desc = smem_desc(ring, kLatChunk), p_desc = smem_desc(p_at, 16);
-    const int32_t pairs = (p.chunks + 1) / 2;
+    // Descriptors and addresses have to stay in uniform registers: a reduction's result is in one, loops end by the
+    // parameters alone, and products stand in straight lines. (Of the 36 + 8 products of a tile of 576 / 512 dims each takes
+    // 25 to 48 clocks to run; with descriptors in any register 70 to 140 to issue.)
+    auto same = [](uint32_t x) { return __reduce_or_sync(0xFFFFFFFFu, x); };
+    const uint32_t ring0 = same(ring), o_at = same(tmem), s_at = same(tm_s), free0 = same(empty);
+    const uint64_t q_desc = smem_desc(same(q_at), 16), p_desc = smem_desc(same(p_at), 16);
     uint32_t k = 0u, T = 0u, items = 0u, stage = 0u, phase = 0u;
     LatentSeg seg;
     // O^T += V^T P^T over tile T - 1, in stage s
     auto values = [&](uint32_t s, bool first) {
-      wait(p_full, (T - 1u) & 1u);
-      if (!ok) return;
-      const uint64_t v = v_desc + s * (stage_bytes >> 4);
-      for (int32_t b = 0; b < p.blocks; ++b) {
+      const uint32_t at = same(ring0 + s * stage_bytes), free_at = same(free0 + 8 * s), old = same(first ? 0u : 1u), odd = same((T - 1u) & 1u);
+      wait(p_full + 8 * odd, ((T - 1u) >> 1) & 1u);
+      const uint64_t v = smem_desc(at, kLatChunk), pd = p_desc + 4 * odd;
+      auto block = [&](int32_t b) {
 #pragma unroll
         for (int i = 0; i < kLatKeys / 16; ++i)
-          tc_mma_ss(tmem + b * NR, v + b * (2 * kLatChunk >> 4) + i * (2048 >> 4), p_desc + i * 2, pv_desc, !first || i > 0);
-        tc_commit(empty + 8 * (s * kLatPairs + b));
+          tc_mma_ss(o_at + b * NR, v + (b * (2 * kLatChunk >> 4) + i * (2048 >> 4)), pd + i * 2, pv_desc, i > 0 || old != 0u);
+      };
+      if (p.blocks == 4) {
+        block(0); block(1); block(2); block(3);
+      } else {
+#pragma unroll 1
+        for (int32_t b = 0; b < p.blocks; ++b) block(b);
       }
-      tc_commit(pv_done);
+      tc_commit(free_at);
+      tc_commit(pv_done + 8 * odd);
+    };
+    // Whether tile T - 1's weights are there before the next tile (its barrier `next`).
+    auto values_first = [&](uint32_t next, uint32_t parity) {
+      for (uint32_t i = 0; i < kSpin; ++i) {
+        if (__any_sync(0xFFFFFFFFu, bar_test(next, parity))) return false;
+        if (__any_sync(0xFFFFFFFFu, bar_test(p_full + 8 * ((T - 1u) & 1u), ((T - 1u) >> 1) & 1u))) return true;
+        if ((i & 1023u) == 1023u && state->ran_out()) break;
+      }
+      return true;  // (the wait to come runs out)
     };
     while (take(k++, &seg)) {
-      const int32_t n = seg.t1 - seg.t0;
+      const int32_t n = static_cast<int32_t>(same(static_cast<uint32_t>(seg.t1 - seg.t0)));
       if (n <= 0) continue;
       wait(q_full, items++ & 1u);
       uint32_t last = 0u;
+      bool valued = true;  // P V of the tile before has been issued
       for (int32_t j = 0; j < n && ok; ++j) {
-        for (int32_t c = 0; c < p.chunks && ok; ++c) {
-          wait(full + 8 * (stage * static_cast<uint32_t>(p.chunks) + c), phase);
-          if (!ok) break;
-          const uint64_t q = q_desc + c * (NR * 128 >> 4), kd = k_desc + stage * (stage_bytes >> 4) + c * (kLatChunk >> 4);
-          const int32_t steps = min(4, p.ksteps - 4 * c);
-          for (int32_t i = 0; i < steps; ++i) tc_mma_ss(tm_s + 64u * (T & 1u), q + 2 * i, kd + 2 * i, qk_desc, c > 0 || i > 0);
+        const uint32_t at = same(ring0 + stage * stage_bytes), d = same(s_at + kLatKeys * (T & 1u));
+        const uint64_t kd = smem_desc(at, 16);
+        wait(full + 8 * stage, phase);
+        auto step = [&](int k16, bool acc) {
+          tc_mma_ss(d, q_desc + ((k16 / 4) * (NR * 128 >> 4) + (k16 % 4) * 2), kd + ((k16 / 4) * (kLatChunk >> 4) + (k16 % 4) * 2), qk_desc, acc);
+        };
+#pragma unroll
+        for (int g = 0; g < kLatMaxChunks * 4; g += 12) {
+          if (p.ksteps >= g + 12) {
+#pragma unroll
+            for (int i = 0; i < 12; ++i) step(g + i, g + i > 0);
+          } else {
+#pragma unroll 1
+            for (int32_t i = g; i < p.ksteps; ++i) step(i, i > 0);
+          }
         }
-        if (!ok) break;
         tc_commit(s_full + 8 * (T & 1u));
-        for (int32_t b = p.blocks; b < pairs; ++b) tc_commit(empty + 8 * (stage * kLatPairs + b));  // not values
-        if (j > 0) values(last, j == 1);
+        if (!valued) values(last, j == 1);
         last = stage;
         ++T;
         if (++stage == static_cast<uint32_t>(p.stages)) {
           stage = 0u;
           phase ^= 1u;
         }
+        // P V of this tile, or S of the next before it: whichever can go first.
+        valued = j + 1 == n || values_first(full + 8 * stage, phase);
+        if (valued && ok) values(last, j == 0);
       }
-      if (ok) values(last, n == 1);
       if (!ok) break;
     }
     if (!ok) {  // products still in flight read shared memory and write TMEM: let them end
@@ -714,13 +752,11 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
     // ======================================================================================
     constexpr uint32_t kN = 32u * kLoaders;
     const uint32_t lt = tid - 6u * 32u;  // of the loaders
-    const int32_t pairs = (p.chunks + 1) / 2;
     uint32_t k = 0u, T = 0u, stage = 0u, phase = 0u;
     LatentSeg seg;
-    // the stage's pair of chunks is free: all that read it has ended
-    auto wait_empty = [&](int32_t b) {
-      if (ok && T >= static_cast<uint32_t>(p.stages))
-        ok = __all_sync(0xFFFFFFFFu, bar_wait(empty + 8 * (stage * kLatPairs + b), phase ^ 1u, state));
+    // the stage is free: all that read it has ended
+    auto wait_empty = [&] {
+      if (ok && T >= static_cast<uint32_t>(p.stages)) ok = __all_sync(0xFFFFFFFFu, bar_wait(empty + 8 * stage, phase ^ 1u, state));
     };
     auto advance = [&] {
       ++T;
@@ -742,7 +778,7 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
       const int32_t p_hi = seg.p_first + static_cast<int32_t>(a.group.quot(static_cast<uint32_t>(seg.row0 + seg.nrows - 1)));
       // the page of key j of a tile (of its last key a row sees, for keys behind it)
       auto page_at = [&](int32_t j) { return __ldg(table + a.page.quot(static_cast<uint32_t>(min(j, p_hi)))); };
-      // by the first 64 loaders, a key each: where its row lies (-1: no row needs it), into sh_place; the others do nothing
+      // by the first loader warp, a key a lane: where its row lies (-1: no row needs it), into sh_place; the others do nothing
       auto place = [&](int32_t tile, int32_t id) {
         const int32_t j = tile * kLatKeys + static_cast<int32_t>(lt);
         const bool want = j <= p_hi, have = static_cast<uint32_t>(id) < static_cast<uint32_t>(a.num_pages);
@@ -769,26 +805,24 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
           if (whole) {
             const uint32_t key = static_cast<uint32_t>(tile * kLatKeys + static_cast<int32_t>(lane) * p.box);
             const int32_t in_page = static_cast<int32_t>(key - a.page.quot(key) * a.page.d);
-            for (int32_t c = 0; c < p.chunks; ++c) {
-              if ((c & 1) == 0) wait_empty(c >> 1);
-              if (!ok) break;
-              if (lt < 32u) {
-                const uint32_t bar = full + 8 * (stage * static_cast<uint32_t>(p.chunks) + c);
-                if (lane == 0u) {
-                  if (c == 0) sh_valid[stage] = ~0ull;
-                  bar_arrive_expect(bar, kLatChunk);
-                }
-                __syncwarp();
-                if (static_cast<int32_t>(lane) < boxes)
-                  tma_box(ring + stage * stage_bytes + c * kLatChunk + lane * box_bytes, &p.map, bar, 64 * c, in_page, 0, page);
+            wait_empty();
+            if (ok && lt < 32u) {
+              const uint32_t bar = full + 8 * stage;
+              if (lane == 0u) {
+                sh_valid[stage] = ~0u;
+                bar_arrive_expect(bar, stage_bytes);
               }
+              __syncwarp();
+              if (static_cast<int32_t>(lane) < boxes)
+                for (int32_t c = 0; c < p.chunks; ++c)
+                  tma_box(ring + stage * stage_bytes + c * kLatChunk + lane * box_bytes, &p.map, bar, 64 * c, in_page, 0, page);
             }
           } else {
-            for (int32_t b = 0; b < pairs; ++b) wait_empty(b);
+            wait_empty();
             if (lt < kLatKeys) {
               const bool have = place(tile, id) != 0xFFFFFFFFu;
               const uint32_t bits = __ballot_sync(0xFFFFFFFFu, have);
-              if (lane == 0u && ok) reinterpret_cast<uint32_t*>(sh_valid + stage)[lt >> 5] = bits;
+              if (lane == 0u && ok) sh_valid[stage] = bits;
             }
             sync_loaders();
             const uint32_t at = ring + stage * stage_bytes;
@@ -802,8 +836,7 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
             wait_all_async();
             fence_async_shared();
             sync_loaders();
-            if (lt == 0u && ok)
-              for (int32_t c = 0; c < p.chunks; ++c) bar_arrive(full + 8 * (stage * static_cast<uint32_t>(p.chunks) + c));
+            if (lt == 0u && ok) bar_arrive(full + 8 * stage);
           }
           if (ok) advance();
         }
@@ -836,7 +869,7 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
           }
         };
         auto put = [&](const uint4 (&v)[kPer], float scale, uint32_t bits) {
-          for (int32_t b = 0; b < pairs; ++b) wait_empty(b);
+          wait_empty();
           const uint32_t at = ring + stage * stage_bytes;
           if (ok) {
 #pragma unroll
@@ -859,13 +892,12 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
             }
             if (lt < kLatKeys) {
               sh_scale[stage * kLatKeys + lt] = scale;
-              if (lane == 0u) reinterpret_cast<uint32_t*>(sh_valid + stage)[lt >> 5] = bits;
+              if (lane == 0u) sh_valid[stage] = bits;
             }
           }
           fence_async_shared();
           sync_loaders();
-          if (lt == 0u && ok)
-            for (int32_t c = 0; c < p.chunks; ++c) bar_arrive(full + 8 * (stage * static_cast<uint32_t>(p.chunks) + c));
+          if (lt == 0u && ok) bar_arrive(full + 8 * stage);
           if (ok) advance();
         };
         if (seg.t0 < seg.t1) load(seg.t0, w[0], &sc[0], &have[0]);
@@ -1005,7 +1037,7 @@ __global__ void __launch_bounds__(32 * kLatJoinWarps) kv_attend_latent_join(cons
 // Host
 // ---------------------------------------------------------------------------
 
-constexpr int kLatMinSteps = 4;  // tiles of a share at least
+constexpr int kLatMinSteps = 8;  // tiles of a share at least
 
 template <int FMT, int NR, bool kBF16>
 kv_status launch_latent_tile(LatentTileParams p, void* work, int64_t work_bytes, int64_t max_keys, cudaStream_t stream) {
