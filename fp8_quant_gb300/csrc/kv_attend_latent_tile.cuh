@@ -19,7 +19,8 @@
 //              running maximum and sums in registers, P to shared memory. O^T is
 //              rescaled only when a row's maximum grew by 2^8 or more. They also
 //              bring the queries in and write the outputs.
-//   warp  4    issues the products: S of the next tile before P V of the last.
+//   warp  4    issues the products S, up to four tiles ahead of
+//   warp  6    P V (a product takes 31 clocks to issue and 25 to 48 to run: one warp for both was the bound).
 //   warp  5    cuts the work: finds the CTA's next items and hands them to the others.
 //   others     bring the tiles: 16-bit rows by TMA, a box for each 64 dims and
 //              run of keys within a page, where all 64 keys exist, else by cp.async; e4m3fn rows
@@ -50,6 +51,7 @@ constexpr int kLatKeys = 32;        // keys of a tile
 constexpr int kLatChunk = kLatKeys * 128;  // bytes of its keys x 64 dims of 16 bits
 constexpr int kLatMaxChunks = 9;    // row dims up to 576
 constexpr int kLatMaxStages = 8;
+constexpr int kLatScores = 4;       // tiles whose scores may be in TMEM
 
 struct LatentTileParams {
   LatentParams l;
@@ -72,7 +74,7 @@ struct LatentTileParams {
 template <int FMT>
 constexpr int kLatLoaders = FMT == KV_CACHE_SRC ? 4 : 8;
 template <int FMT>
-constexpr int kLatThreads = 32 * (6 + kLatLoaders<FMT>);
+constexpr int kLatThreads = 32 * (7 + kLatLoaders<FMT>);
 
 // A CTA's next piece of work.
 struct LatentSeg {
@@ -86,7 +88,7 @@ struct LatentSeg {
 template <int NR>
 struct LatentSmem {  // behind the stages
   static constexpr int kP = NR * 128;
-  static constexpr int kBars = 32;
+  static constexpr int kBars = 40;
   static constexpr int kSeg = 2;
   static __host__ __device__ constexpr int q_bytes(int chunks) { return chunks * NR * 128; }
   // offsets behind Q and P
@@ -99,7 +101,7 @@ struct LatentSmem {  // behind the stages
 };
 static_assert(sizeof(LatentSeg) <= 64, "segments");
 static_assert(LatentSmem<64>::total(kLatMaxChunks, 4) <= 227 * 1024, "four stages of the widest rows fit");
-static_assert(2 * kLatMaxStages + 13 <= LatentSmem<64>::kBars, "barriers");
+static_assert(2 * kLatMaxStages + 2 * kLatScores + 12 <= LatentSmem<64>::kBars, "barriers");
 
 // Rows of the sequence's queries in blocks of NR, and tiles of each (an upper bound, at least one).
 struct LatentGeom {
@@ -154,14 +156,27 @@ __device__ __forceinline__ void tc_ld_rows(float (&s)[16], uint32_t addr) {
   for (int i = 0; i < 16; ++i) s[i] = __uint_as_float(r[i]);
 }
 
-// bar_try without a pause.
-__device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile("{\n\t.reg .pred p;\n\t"
-               "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-               "selp.u32 %0, 1, 0, p;\n\t}"
-               : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-  return ok != 0u;
+// N products D (TMEM) = or += A B (shared memory), by a whole, converged warp as tc_mma_ss: the operands' descriptors
+// step by AS and BS (in 16 bytes), whose low words alone change.  One election for all, and no carries: a product then
+// takes 31 clocks to issue, 40 each on its own.
+template <int N, int AS, int BS>
+__device__ __forceinline__ void tc_mma_run(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+  static_assert(N == 2 || N == 4, "products");
+  const uint32_t al = static_cast<uint32_t>(a), ah = static_cast<uint32_t>(a >> 32), bl = static_cast<uint32_t>(b), bh = static_cast<uint32_t>(b >> 32);
+#define KV_FIRST "{\n\t.reg .pred e, p;\n\t.reg .b64 x, y;\n\t.reg .b32 u, v;\n\telect.sync _|e, 0xFFFFFFFF;\n\tsetp.ne.b32 p, %6, 0;\n\t" \
+  "mov.b64 x, {%1, %2};\n\tmov.b64 y, {%3, %4};\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %5, p;\n\t"
+#define KV_NEXT(i, j) "add.u32 u, %1, %" #i ";\n\tadd.u32 v, %3, %" #j ";\n\tmov.b64 x, {u, %2};\n\tmov.b64 y, {v, %4};\n\t" \
+  "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %5, 1;\n\t"
+  if constexpr (N == 4) {
+    asm volatile(KV_FIRST KV_NEXT(7, 8) KV_NEXT(9, 10) KV_NEXT(11, 12) "}"
+                 ::"r"(d), "r"(al), "r"(ah), "r"(bl), "r"(bh), "r"(idesc), "r"(acc ? 1u : 0u), "n"(AS), "n"(BS), "n"(2 * AS), "n"(2 * BS), "n"(3 * AS), "n"(3 * BS)
+                 : "memory");
+  } else {
+    asm volatile(KV_FIRST KV_NEXT(7, 8) "}"
+                 ::"r"(d), "r"(al), "r"(ah), "r"(bl), "r"(bh), "r"(idesc), "r"(acc ? 1u : 0u), "n"(AS), "n"(BS) : "memory");
+  }
+#undef KV_FIRST
+#undef KV_NEXT
 }
 
 __device__ __forceinline__ float lg2_fast(float x) {
@@ -194,8 +209,8 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
   const uint32_t small = p_at + S::kP;
   uint8_t* const small_ptr = smem_raw + (small - ring);
   const uint32_t full = small + S::kOffBars, empty = full + 8 * kLatMaxStages, q_full = empty + 8 * kLatMaxStages, s_full = q_full + 8,
-                 p_full = s_full + 16, pv_done = p_full + 16, seg_full = pv_done + 16, seg_empty = seg_full + 16, done = seg_empty + 16,
-                 load_bar = done + 8;
+                 s_free = s_full + 8 * kLatScores, p_full = s_free + 8 * kLatScores, pv_done = p_full + 16, seg_full = pv_done + 16, seg_empty = seg_full + 16, done = seg_empty + 16,
+                 load_bar = done + 16;
   LatentSeg* const segs = reinterpret_cast<LatentSeg*>(small_ptr + S::kOffSegs);
   float* const sh_alpha = reinterpret_cast<float*>(small_ptr + S::kOffAlpha);   // [2][NR]
   float* const sh_inv = reinterpret_cast<float*>(small_ptr + S::kOffInv);
@@ -219,14 +234,18 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
       bar_init(empty + 8 * i, 1);
     }
     bar_init(q_full, 128);
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kLatScores; ++i) {
       bar_init(s_full + 8 * i, 1);
+      bar_init(s_free + 8 * i, NR / 16);
+    }
+    for (int i = 0; i < 2; ++i) {
       bar_init(p_full + 8 * i, 128);
       bar_init(pv_done + 8 * i, 1);
       bar_init(seg_full + 8 * i, 1);
-      bar_init(seg_empty + 8 * i, 5 + kLoaders);
+      bar_init(seg_empty + 8 * i, 6 + kLoaders);
     }
     bar_init(done, 1);
+    bar_init(done + 8, 1);
     bar_init(load_bar, kLoaders);
     *state = WaitState{(ring & 1023u) != 0u ? 1 : 0, 0};
     *sh_bad = 0ull;
@@ -248,7 +267,7 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
     if (lane == 0u) bar_arrive(seg_empty + 8 * (k & 1u));
     return s->stop == 0;
   };
-  const uint32_t tm_s = tmem + 4 * NR;  // S, two buffers of kLatKeys columns, behind O^T
+  const uint32_t tm_s = tmem + 4 * NR;  // S, kLatScores buffers of kLatKeys columns, behind O^T
 
   if (warp < 4) {
     // ======================================================================================
@@ -334,13 +353,16 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
         if (rs[c] == 0.0f) rs[c] = __uint_as_float(1u);  // hidden scores (-inf) must stay -inf
       }
       for (int32_t j = seg.t0; j < seg.t1; ++j, ++T) {
-        ok = ok && __all_sync(0xFFFFFFFFu, bar_wait(s_full + 8 * (T & 1u), (T >> 1) & 1u, state) &&
-                                               bar_wait(full + 8 * stage, phase, state));
+        ok = ok && __all_sync(0xFFFFFFFFu, bar_wait(full + 8 * stage, phase, state));
+        const uint32_t valid = sh_valid[stage];
+        ok = ok && __all_sync(0xFFFFFFFFu, bar_wait(s_full + 8 * (T % kLatScores), (T / kLatScores) & 1u, state));
         tc_fence_after();
         float s[16], kf[8], alpha[2] = {1.0f, 1.0f};  // scores, their keys' scales, factors of the rows' sums
         bool grew = false;
         if (has_rows && ok) {
-          tc_ld_rows(s, tm_s + kLatKeys * (T & 1u) + lanes);
+          tc_ld_rows(s, tm_s + kLatKeys * (T % kLatScores) + lanes);
+          tc_fence_before();
+          if (lane == 0u) bar_arrive(s_free + 8 * (T % kLatScores));
           if constexpr (FMT != KV_CACHE_SRC) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -351,7 +373,6 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
 #pragma unroll
             for (int i = 0; i < 16; ++i) s[i] *= kf[2 * (i / 4) + (i & 1)] * rs[(i >> 1) & 1];
           }
-          const uint32_t valid = sh_valid[stage];
           if (j * kLatKeys + kLatKeys - 1 > p_lo || valid != ~0u) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
@@ -549,92 +570,96 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
       tc_fence_before();
       seg = next;
     }
-  } else if (warp == 4) {
+  } else if (warp == 4 || warp == 6) {
     // ======================================================================================
-    // the products
+    // the products: warp 4 S = Q K^T, warp 6 O^T += V^T P^T
     // ======================================================================================
-    const uint32_t qk_desc = (1u << 4) | (kBF16 ? 1u << 7 | 1u << 10 : 0u) | ((static_cast<uint32_t>(kLatKeys) >> 3) << 17) | ((64u >> 4) << 24);
-    const uint32_t pv_desc = (1u << 4) | (kBF16 ? 1u << 7 | 1u << 10 : 0u) | (1u << 15) | ((static_cast<uint32_t>(NR) >> 3) << 17) | ((128u >> 4) << 24);
     auto wait = [&](uint32_t bar, uint32_t parity) {
       if (ok) ok = __all_sync(0xFFFFFFFFu, bar_wait(bar, parity, state));
       tc_fence_after();
     };
-    // Descriptors and addresses have to stay in uniform registers: a reduction's result is in one, loops end by the
+    // Descriptors and addresses are to be in uniform registers: a reduction's result is in one, loops end by the
     // parameters alone, and products stand in straight lines. (Of the 36 + 8 products of a tile of 576 / 512 dims each takes
     // 25 to 48 clocks to run; with descriptors in any register 70 to 140 to issue.)
     auto same = [](uint32_t x) { return __reduce_or_sync(0xFFFFFFFFu, x); };
-    const uint32_t ring0 = same(ring), o_at = same(tmem), s_at = same(tm_s), free0 = same(empty);
-    const uint64_t q_desc = smem_desc(same(q_at), 16), p_desc = smem_desc(same(p_at), 16);
-    uint32_t k = 0u, T = 0u, items = 0u, stage = 0u, phase = 0u;
+    const uint32_t ring0 = same(ring);
+    uint32_t k = 0u, T = 0u, stage = 0u, phase = 0u;
     LatentSeg seg;
-    // O^T += V^T P^T over tile T - 1, in stage s
-    auto values = [&](uint32_t s, bool first) {
-      const uint32_t at = same(ring0 + s * stage_bytes), free_at = same(free0 + 8 * s), old = same(first ? 0u : 1u), odd = same((T - 1u) & 1u);
-      wait(p_full + 8 * odd, ((T - 1u) >> 1) & 1u);
-      const uint64_t v = smem_desc(at, kLatChunk), pd = p_desc + 4 * odd;
-      auto block = [&](int32_t b) {
+    auto advance = [&] {
+      ++T;
+      if (++stage == static_cast<uint32_t>(p.stages)) {
+        stage = 0u;
+        phase ^= 1u;
+      }
+    };
+    if (warp == 4) {
+      const uint32_t desc = (1u << 4) | (kBF16 ? 1u << 7 | 1u << 10 : 0u) | ((static_cast<uint32_t>(kLatKeys) >> 3) << 17) | ((64u >> 4) << 24);
+      const uint32_t s_at = same(tm_s);
+      const uint64_t q_desc = smem_desc(same(q_at), 16);
+      uint32_t items = 0u;
+      while (take(k++, &seg)) {
+        if (seg.t1 <= seg.t0) continue;
+        wait(q_full, items++ & 1u);
+        for (int32_t j = seg.t0; j < seg.t1; ++j) {
+          const uint32_t u = same(stage | (T % kLatScores) << 8), st = u & 255u, buf = u >> 8;
+          const uint64_t kd = smem_desc(ring0 + st * stage_bytes, 16);
+          const uint32_t d = s_at + kLatKeys * buf;
+          if (T >= kLatScores) wait(s_free + 8 * (T % kLatScores), (T / kLatScores - 1u) & 1u);
+          wait(full + 8 * stage, phase);
+          if (!ok) break;
+          auto chunk = [&](int32_t c) {
+            tc_mma_run<4, 2, 2>(d, q_desc + c * (NR * 128 >> 4), kd + c * (kLatChunk >> 4), desc, c > 0);
+          };
 #pragma unroll
-        for (int i = 0; i < kLatKeys / 16; ++i)
-          tc_mma_ss(o_at + b * NR, v + (b * (2 * kLatChunk >> 4) + i * (2048 >> 4)), pd + i * 2, pv_desc, i > 0 || old != 0u);
-      };
-      if (p.blocks == 4) {
-        block(0); block(1); block(2); block(3);
-      } else {
+          for (int c = 0; c < kLatMaxChunks; c += 3) {
+            if (p.ksteps >= 4 * c + 12) {
+              chunk(c); chunk(c + 1); chunk(c + 2);
+            } else {
 #pragma unroll 1
-        for (int32_t b = 0; b < p.blocks; ++b) block(b);
+              for (int32_t y = c; 4 * y + 4 <= p.ksteps; ++y) chunk(y);
+              if (p.ksteps >= 4 * c)
+#pragma unroll 1
+                for (int32_t i = p.ksteps & ~3; i < p.ksteps; ++i)
+                  tc_mma_ss(d, q_desc + ((i / 4) * (NR * 128 >> 4) + (i % 4) * 2), kd + ((i / 4) * (kLatChunk >> 4) + (i % 4) * 2), desc, i > 0);
+              break;
+            }
+          }
+          tc_commit(s_full + 8 * buf);
+          advance();
+        }
+        if (!ok) break;
       }
-      tc_commit(free_at);
-      tc_commit(pv_done + 8 * odd);
-    };
-    // Whether tile T - 1's weights are there before the next tile (its barrier `next`).
-    auto values_first = [&](uint32_t next, uint32_t parity) {
-      for (uint32_t i = 0; i < kSpin; ++i) {
-        if (__any_sync(0xFFFFFFFFu, bar_test(next, parity))) return false;
-        if (__any_sync(0xFFFFFFFFu, bar_test(p_full + 8 * ((T - 1u) & 1u), ((T - 1u) >> 1) & 1u))) return true;
-        if ((i & 1023u) == 1023u && state->ran_out()) break;
-      }
-      return true;  // (the wait to come runs out)
-    };
-    while (take(k++, &seg)) {
-      const int32_t n = static_cast<int32_t>(same(static_cast<uint32_t>(seg.t1 - seg.t0)));
-      if (n <= 0) continue;
-      wait(q_full, items++ & 1u);
-      uint32_t last = 0u;
-      bool valued = true;  // P V of the tile before has been issued
-      for (int32_t j = 0; j < n && ok; ++j) {
-        const uint32_t at = same(ring0 + stage * stage_bytes), d = same(s_at + kLatKeys * (T & 1u));
-        const uint64_t kd = smem_desc(at, 16);
-        wait(full + 8 * stage, phase);
-        auto step = [&](int k16, bool acc) {
-          tc_mma_ss(d, q_desc + ((k16 / 4) * (NR * 128 >> 4) + (k16 % 4) * 2), kd + ((k16 / 4) * (kLatChunk >> 4) + (k16 % 4) * 2), qk_desc, acc);
-        };
-#pragma unroll
-        for (int g = 0; g < kLatMaxChunks * 4; g += 12) {
-          if (p.ksteps >= g + 12) {
-#pragma unroll
-            for (int i = 0; i < 12; ++i) step(g + i, g + i > 0);
+    } else {
+      const uint32_t desc = (1u << 4) | (kBF16 ? 1u << 7 | 1u << 10 : 0u) | (1u << 15) | ((static_cast<uint32_t>(NR) >> 3) << 17) | ((128u >> 4) << 24);
+      const uint32_t o_at = same(tmem), free0 = same(empty);
+      const uint64_t p_desc = smem_desc(same(p_at), 16);
+      while (take(k++, &seg)) {
+        for (int32_t j = seg.t0; j < seg.t1; ++j) {
+          const uint32_t u = same(stage | (T & 1u) << 8 | (j > seg.t0 ? 512u : 0u)), st = u & 255u, odd = u >> 8 & 1u, old = u >> 9;
+          const uint64_t v = smem_desc(ring0 + st * stage_bytes, kLatChunk), pd = p_desc + 4 * odd;
+          wait(full + 8 * stage, phase);
+          wait(p_full + 8 * (T & 1u), (T >> 1) & 1u);
+          if (!ok) break;
+          auto block = [&](int32_t b) {
+            tc_mma_run<kLatKeys / 16, (2048 >> 4), 2>(o_at + b * NR, v + b * (2 * kLatChunk >> 4), pd, desc, old != 0u);
+          };
+          if (p.blocks == 4) {
+            block(0); block(1); block(2); block(3);
           } else {
 #pragma unroll 1
-            for (int32_t i = g; i < p.ksteps; ++i) step(i, i > 0);
+            for (int32_t b = 0; b < p.blocks; ++b) block(b);
           }
+          tc_commit(free0 + 8 * st);
+          tc_commit(pv_done + 8 * odd);
+          advance();
         }
-        tc_commit(s_full + 8 * (T & 1u));
-        if (!valued) values(last, j == 1);
-        last = stage;
-        ++T;
-        if (++stage == static_cast<uint32_t>(p.stages)) {
-          stage = 0u;
-          phase ^= 1u;
-        }
-        // P V of this tile, or S of the next before it: whichever can go first.
-        valued = j + 1 == n || values_first(full + 8 * stage, phase);
-        if (valued && ok) values(last, j == 0);
+        if (!ok) break;
       }
-      if (!ok) break;
     }
     if (!ok) {  // products still in flight read shared memory and write TMEM: let them end
-      tc_commit(done);
-      for (uint32_t i = 0; i < kSpin && !bar_try(done, 0); ++i) {}
+      const uint32_t bar = warp == 4 ? done : done + 8;
+      tc_commit(bar);
+      for (uint32_t i = 0; i < kSpin && !bar_try(bar, 0); ++i) {}
     }
     __syncwarp();
   } else if (warp == 5) {
@@ -751,7 +776,7 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
     // the tiles
     // ======================================================================================
     constexpr uint32_t kN = 32u * kLoaders;
-    const uint32_t lt = tid - 6u * 32u;  // of the loaders
+    const uint32_t lt = tid - 7u * 32u;  // of the loaders
     uint32_t k = 0u, T = 0u, stage = 0u, phase = 0u;
     LatentSeg seg;
     // the stage is free: all that read it has ended
