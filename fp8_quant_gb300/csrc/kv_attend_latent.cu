@@ -129,12 +129,18 @@ extern "C" kv_status kv_attend_latent(const void* q, void* out, float* lse, cons
     tp.blocks = (latent_dim + 127) / 128;
     const int64_t rows = (num_q_tokens + num_seqs - 1) / num_seqs * num_q_heads;
     const bool few = rows <= 32;
+    // more rows than a CTA takes: pairs of CTAs share their keys (16-bit rows)
+    tp.cluster = !fp8 && rows > 64 ? 2 : 1;
+    // TMA: eight keys of a page a box, with all their dims where these are whole chunks
+    if (page_size % 8 == 0) {
+      const int eb = fp8 ? 1 : 2;
+      if (row_dim % 64 == 0 && cache_map(&tp.map, cache, eb, a.bf16, 64, page_size, tp.chunks, num_pages, s->cache_slot, 64 * eb, s->cache_page, 64, 8,
+                                         tp.chunks, !fp8))
+        tp.tma = 2;
+      else if (!fp8 && cache_map(&tp.map, cache, 2, a.bf16, row_dim, page_size, 1, num_pages, s->cache_slot, 0, s->cache_page, 64, 8, 1, true))
+        tp.tma = 1;
+    }
     if (fp8) return latent_tile_e4m3(tp, few, work, work_bytes, a.max_len, stream);
-    // TMA: the longest runs of 8 to 32 keys that pages are cut into
-    int box = kLatKeys;
-    while (page_size % box != 0) box /= 2;
-    if (box >= 8 && cache_map(&tp.map, cache, 2, a.bf16, row_dim, page_size, 1, num_pages, s->cache_slot, 0, s->cache_page, 64, box, 1, true))
-      tp.box = box;
     return latent_tile_src(tp, few, work, work_bytes, a.max_len, stream);
   }
   return fp8 ? launch_rows_any<KV_CACHE_E4M3FN>(p, stream) : launch_rows_any<KV_CACHE_SRC>(p, stream);

@@ -19,15 +19,17 @@
 //              running maximum and sums in registers, P to shared memory. O^T is
 //              rescaled only when a row's maximum grew by 2^8 or more. They also
 //              bring the queries in and write the outputs.
-//   warp  4    issues the products S, up to four tiles ahead of
-//   warp  6    P V (a product takes 31 clocks to issue and 25 to 48 to run: one warp for both was the bound).
-//   warp  5    cuts the work: finds the CTA's next items and hands them to the others.
-//   others     bring the tiles: 16-bit rows by TMA, a box for each 64 dims and
-//              run of keys within a page, where all 64 keys exist, else by cp.async; e4m3fn rows
-//              through registers, a tile ahead, as fp16 (exact).
-//   A stage (tile) is waited for in chunks of 64 dims, so that S follows the copies,
-//   and given back by 128 dims, as P V goes over them: two stages of 576 dims and the
-//   queries fill the shared memory.
+//   warp  4    issues the products S, up to two tiles ahead of
+//   warp  5    P V. (A product takes 31 clocks to issue and 32 to 48 to run: one warp for both was the bound.)
+//   warp  6    cuts the work: finds the CTA's next items and hands them to the others.
+//   warp  7    brings the keys in units of 32: by TMA, a box for eight keys and all their dims, where all 32 exist, else by
+//              cp.async. e4m3fn rows come as they are, into a ring of their own, and become fp16 (exact) by
+//   warps 8-15 on their way into the ring of units.
+//   A unit is given back as soon as P V has gone over it. It lies as [8 keys][64 dims][key][128 bytes in the 128-byte
+//   swizzle], so that a tile is any two units that follow each other in the ring (two products of 32 keys where it wraps).
+//
+// Rows beyond NR (more queries, more heads) read the same keys: two CTAs then are a cluster, each brings half of
+// every unit and TMA writes it into both.
 //
 // Weights are rounded once to 16 bits, as the product's operand; their sums are
 // of the unrounded ones in fp32. An e4m3fn row's scale f multiplies its scores,
@@ -35,8 +37,8 @@
 // maximum of score + log2 f, so that p f, not p, begins at 2^7.
 //
 // Few long sequences are split over the CTAs by keys, in steps of a tile, counted
-// on the device: one share for each CTA and smaller ones for those that are done first;
-// parts are joined in the order of the keys by a second kernel.
+// on the device: one share for each CTA (or pair) and, without pairs, smaller ones for those that are done
+// first; parts are joined in the order of the keys by a second kernel.
 //
 // Every wait has a limit (kSpin); a CTA whose wait ran out records that in the
 // error record and in the workspace's head, lets its copies and products end and leaves.
@@ -47,92 +49,93 @@
 
 namespace kvimpl {
 
-constexpr int kLatKeys = 32;        // keys of a tile
-constexpr int kLatChunk = kLatKeys * 128;  // bytes of its keys x 64 dims of 16 bits
-constexpr int kLatMaxChunks = 9;    // row dims up to 576
-constexpr int kLatMaxStages = 8;
-constexpr int kLatScores = 4;       // tiles whose scores may be in TMEM
+constexpr int kLatKeys = 64;        // keys of a tile
+constexpr int kLatUnit = 32;        // and of a unit of the ring
+constexpr int kLatMaxChunks = 9;    // 64-dim chunks of a row: up to 576 dims
+constexpr int kLatMaxUnits = 8, kLatMaxRaws = 8;
+constexpr int kLatScores = 2;       // tiles whose scores may be in TMEM
 
 struct LatentTileParams {
   LatentParams l;
   CUtensorMap map;
-  int32_t box;       // keys of a TMA box; 0: no TMA
+  int32_t tma;       // 0: cp.async alone; 1: a box is 8 keys of a chunk; 2: of all chunks
+  int32_t cluster;   // CTAs that share their keys: 1 or 2
   int32_t page_stride, slot_stride;  // of the cache, bytes in 32 bits
   int32_t chunks;    // 64-dim chunks of a row, the last perhaps cut
   int32_t ksteps;    // 16-dim steps of a row
   int32_t blocks;    // 128-dim blocks of the values
-  int32_t stages;
-  int32_t split;     // 0: an item is one CTA's
+  int32_t units, raws;  // of the ring, and of that of e4m3fn rows
+  int32_t split;     // 0: an item is one CTA's (or pair's)
   int32_t min_steps, max_shares;
   int32_t part_rows;
   SplitWork* head;
   int64_t* meta;     // [num_seqs]: first step of each sequence
-  float *part_o, *part_ml;  // [2 * max_shares][part_rows] x 128 * blocks and x 2
+  float *part_o, *part_ml;  // [2 * max_shares][cluster][part_rows] x 128 * blocks and x 2
 };
 
-// Loader warps: e4m3fn rows are converted by them.
+constexpr int kLatConverters = 8;  // warps
 template <int FMT>
-constexpr int kLatLoaders = FMT == KV_CACHE_SRC ? 4 : 8;
-template <int FMT>
-constexpr int kLatThreads = 32 * (7 + kLatLoaders<FMT>);
+constexpr int kLatThreads = FMT == KV_CACHE_SRC ? 256 : 256 + 32 * kLatConverters;
 
 // A CTA's next piece of work.
 struct LatentSeg {
   int32_t b, q0, nq, p_first;  // sequence, its first query row and their number, position of the first
-  int32_t row0, nrows;         // rows of the item: (query, head) pairs of the sequence
+  int32_t row0, nrows, last;   // the CTA's rows of the item: (query, head) pairs of the sequence; the last, from row0 (at least 0)
+  int32_t p_hi;                // position of the item's last row
   int32_t t0, t1;              // tiles
   int32_t part;                // -1: the item is whole; else the part's place
   int32_t stop;
 };
 
-template <int NR>
-struct LatentSmem {  // behind the stages
+template <int FMT, int NR>
+struct LatentSmem {  // units, raw units, queries, weights, and
   static constexpr int kP = NR * 128;
-  static constexpr int kBars = 40;
-  static constexpr int kSeg = 2;
+  static constexpr int kBars = 2 * kLatMaxUnits + 2 * kLatMaxRaws + 2 * kLatScores + 9;
+  static __host__ __device__ constexpr int unit(int chunks) { return kLatUnit * 128 * chunks; }
+  static __host__ __device__ constexpr int raw(int chunks) { return kLatUnit * 64 * chunks; }
   static __host__ __device__ constexpr int q_bytes(int chunks) { return chunks * NR * 128; }
-  // offsets behind Q and P
-  static constexpr int kOffBars = 0, kOffSegs = kOffBars + kBars * 8, kOffAlpha = kOffSegs + kSeg * 64,
-                       kOffInv = kOffAlpha + 2 * NR * 4, kOffQf = kOffInv + NR * 4, kOffPlace = kOffQf + NR * 4,
-                       kOffMisc = kOffPlace + kLatKeys * 8, kOffValid = kOffMisc + 64, kOffScale = kOffValid + kLatMaxStages * 4;
-  static __host__ __device__ constexpr int total(int chunks, int stages) {
-    return stages * (chunks * kLatChunk + kLatKeys * 4) + q_bytes(chunks) + kP + kOffScale;
+  static constexpr int kOffBars = 0, kOffSegs = (kBars * 8 + 15) / 16 * 16, kOffAlpha = kOffSegs + 2 * 64, kOffInv = kOffAlpha + 2 * NR * 4,
+                       kOffQf = kOffInv + NR * 4, kOffMisc = kOffQf + NR * 4, kOffValid = kOffMisc + 64,
+                       kOffRawValid = kOffValid + kLatMaxUnits * 4, kOffScale = kOffRawValid + kLatMaxRaws * 4;
+  static __host__ __device__ constexpr int total(int chunks, int units, int raws) {
+    return units * (unit(chunks) + (FMT == KV_CACHE_SRC ? 0 : kLatUnit * 4)) + raws * (raw(chunks) + kLatUnit * 4) + q_bytes(chunks) + kP + kOffScale;
   }
 };
 static_assert(sizeof(LatentSeg) <= 64, "segments");
-static_assert(LatentSmem<64>::total(kLatMaxChunks, 4) <= 227 * 1024, "four stages of the widest rows fit");
-static_assert(2 * kLatMaxStages + 2 * kLatScores + 12 <= LatentSmem<64>::kBars, "barriers");
+static_assert(LatentSmem<KV_CACHE_SRC, 64>::total(kLatMaxChunks, 4, 0) <= 227 * 1024 &&
+                  LatentSmem<KV_CACHE_E4M3FN, 64>::total(kLatMaxChunks, 3, 2) <= 227 * 1024, "the widest rows fit");
 
-// Rows of the sequence's queries in blocks of NR, and tiles of each (an upper bound, at least one).
+// Rows of the sequence's queries in blocks of NR (of the pair: 2 NR), and tiles of each (an upper bound, at least one).
 struct LatentGeom {
   int32_t blocks, steps;
 };
 
 template <int NR>
-__device__ __forceinline__ LatentGeom latent_geom(const AttendParams& a, const AttendSeq& s) {
+__device__ __forceinline__ LatentGeom latent_geom(const LatentTileParams& p, const AttendSeq& s) {
   LatentGeom g;
-  g.blocks = static_cast<int32_t>((static_cast<uint32_t>(s.nq) * a.group.d + NR - 1) / NR);
+  const uint32_t rows = NR * static_cast<uint32_t>(p.cluster);
+  g.blocks = static_cast<int32_t>((static_cast<uint32_t>(s.nq) * p.l.a.group.d + rows - 1) / rows);
   g.steps = max((s.len + kLatKeys - 1) / kLatKeys, 1);
   return g;
 }
 
 template <int NR>
 __device__ __forceinline__ int64_t latent_units(const LatentTileParams& p, int32_t b, bool record) {
-  const LatentGeom g = latent_geom<NR>(p.l.a, attend_seq(p.l.a, b, record));
+  const LatentGeom g = latent_geom<NR>(p, attend_seq(p.l.a, b, record));
   return static_cast<int64_t>(g.blocks) * (p.split ? g.steps : 1);
 }
 
 // One share of 88 % of an equal part for each CTA, and the rest in shares of a quarter of what is left for each.
 constexpr int kLatFirst = 88;
 
-__device__ __forceinline__ int32_t latent_cut(int64_t total, int32_t ctas, int32_t max_shares, int32_t min_steps, ShareLevel (&level)[2],
-                                              int32_t* shares) {
+__device__ __forceinline__ int32_t latent_cut(int64_t total, int32_t ctas, bool pairs, int32_t max_shares, int32_t min_steps,
+                                              ShareLevel (&level)[2], int32_t* shares) {
   int64_t each = (total + ctas - 1) / ctas;
   if (each < min_steps) each = min_steps;
   const int64_t size = each * kLatFirst / 100, left = total - size * ctas;
   int64_t small = (left + 2 * ctas - 1) / (2 * ctas);
   if (small < min_steps) small = min_steps;
-  if (left <= 0 || each < 6 * min_steps || max_shares < ctas + (left + small - 1) / small) {
+  if (pairs || left <= 0 || each < 6 * min_steps || max_shares < ctas + (left + small - 1) / small) {
     level[0] = ShareLevel{0, static_cast<int32_t>(each), 0};
     *shares = static_cast<int32_t>((total + each - 1) / each);
     return 1;
@@ -143,40 +146,58 @@ __device__ __forceinline__ int32_t latent_cut(int64_t total, int32_t ctas, int32
   return 2;
 }
 
-// 16 lanes x 32 columns over the warp: thread (g, t) = (lane / 4, lane % 4) gets columns 8 i + 2 t, + 1 of
+// 16 lanes x 64 columns over the warp: thread (g, t) = (lane / 4, lane % 4) gets columns 8 i + 2 t, + 1 of
 // rows g (r[4 i], r[4 i + 1]) and g + 8 (r[4 i + 2], r[4 i + 3]).
-__device__ __forceinline__ void tc_ld_rows(float (&s)[16], uint32_t addr) {
-  uint32_t r[16];
-  asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 "
-               "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+__device__ __forceinline__ void tc_ld_rows(float (&s)[32], uint32_t addr) {
+  uint32_t r[32];
+#define KV_R4(i) "=r"(r[i]), "=r"(r[(i) + 1]), "=r"(r[(i) + 2]), "=r"(r[(i) + 3])
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+               "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
                "tcgen05.wait::ld.sync.aligned;"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-                 "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]) : "r"(addr) : "memory");
+               : KV_R4(0), KV_R4(4), KV_R4(8), KV_R4(12), KV_R4(16), KV_R4(20), KV_R4(24), KV_R4(28) : "r"(addr) : "memory");
+#undef KV_R4
 #pragma unroll
-  for (int i = 0; i < 16; ++i) s[i] = __uint_as_float(r[i]);
+  for (int i = 0; i < 32; ++i) s[i] = __uint_as_float(r[i]);
 }
 
-// N products D (TMEM) = or += A B (shared memory), by a whole, converged warp as tc_mma_ss: the operands' descriptors
-// step by AS and BS (in 16 bytes), whose low words alone change.  One election for all, and no carries: a product then
-// takes 31 clocks to issue, 40 each on its own.
-template <int N, int AS, int BS>
-__device__ __forceinline__ void tc_mma_run(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
-  static_assert(N == 2 || N == 4, "products");
-  const uint32_t al = static_cast<uint32_t>(a), ah = static_cast<uint32_t>(a >> 32), bl = static_cast<uint32_t>(b), bh = static_cast<uint32_t>(b >> 32);
+// smem_desc with groups of eight rows (or keys) `group` bytes apart.
+__device__ __forceinline__ uint64_t smem_desc_groups(uint32_t addr, uint32_t lead, uint32_t group) {
+  return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(lead >> 4) << 16) |
+         (static_cast<uint64_t>(group >> 4) << 32) | (uint64_t{1} << 46) | (uint64_t{2} << 61);
+}
+
+// Products D (TMEM) = or += A B (shared memory), by a whole, converged warp as tc_mma_ss: four whose operands' descriptors
+// step by 2 (32 bytes), or two whose steps are given (in 16 bytes). The descriptors' low words alone change. One election for
+// all, and no carries: a product then takes 31 clocks to issue, 40 each on its own.
 #define KV_FIRST "{\n\t.reg .pred e, p;\n\t.reg .b64 x, y;\n\t.reg .b32 u, v;\n\telect.sync _|e, 0xFFFFFFFF;\n\tsetp.ne.b32 p, %6, 0;\n\t" \
   "mov.b64 x, {%1, %2};\n\tmov.b64 y, {%3, %4};\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %5, p;\n\t"
-#define KV_NEXT(i, j) "add.u32 u, %1, %" #i ";\n\tadd.u32 v, %3, %" #j ";\n\tmov.b64 x, {u, %2};\n\tmov.b64 y, {v, %4};\n\t" \
+#define KV_NEXT(i, j) "add.u32 u, %1, " i ";\n\tadd.u32 v, %3, " j ";\n\tmov.b64 x, {u, %2};\n\tmov.b64 y, {v, %4};\n\t" \
   "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %5, 1;\n\t"
-  if constexpr (N == 4) {
-    asm volatile(KV_FIRST KV_NEXT(7, 8) KV_NEXT(9, 10) KV_NEXT(11, 12) "}"
-                 ::"r"(d), "r"(al), "r"(ah), "r"(bl), "r"(bh), "r"(idesc), "r"(acc ? 1u : 0u), "n"(AS), "n"(BS), "n"(2 * AS), "n"(2 * BS), "n"(3 * AS), "n"(3 * BS)
-                 : "memory");
-  } else {
-    asm volatile(KV_FIRST KV_NEXT(7, 8) "}"
-                 ::"r"(d), "r"(al), "r"(ah), "r"(bl), "r"(bh), "r"(idesc), "r"(acc ? 1u : 0u), "n"(AS), "n"(BS) : "memory");
-  }
+#define KV_OPERANDS "r"(d), "r"(static_cast<uint32_t>(a)), "r"(static_cast<uint32_t>(a >> 32)), "r"(static_cast<uint32_t>(b)), \
+  "r"(static_cast<uint32_t>(b >> 32)), "r"(idesc), "r"(acc ? 1u : 0u)
+__device__ __forceinline__ void tc_mma_chunk(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(KV_FIRST KV_NEXT("2", "2") KV_NEXT("4", "4") KV_NEXT("6", "6") "}" ::KV_OPERANDS : "memory");
+}
+__device__ __forceinline__ void tc_mma_two(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc, uint32_t a_step, uint32_t b_step) {
+  asm volatile(KV_FIRST KV_NEXT("%7", "%8") "}" ::KV_OPERANDS, "r"(a_step), "r"(b_step) : "memory");
+}
 #undef KV_FIRST
 #undef KV_NEXT
+#undef KV_OPERANDS
+
+// tma_box into the same place of both CTAs of a pair, and their barriers.
+__device__ __forceinline__ void tma_box_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t dim, int32_t key, int32_t head, int32_t page) {
+  asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%3, %4, %5, %6}], [%2], %7;"
+               ::"r"(dst), "l"(map), "r"(bar), "r"(dim), "r"(key), "r"(head), "r"(page), "h"(static_cast<uint16_t>(3)) : "memory");
+}
+// tc_commit to the same barrier of both CTAs of a pair.
+__device__ __forceinline__ void tc_commit_pair(uint32_t bar) {
+  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xFFFFFFFF;\n\t"
+               "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}"
+               ::"r"(bar), "h"(static_cast<uint16_t>(3)) : "memory");
+}
+__device__ __forceinline__ void sync_pair() {
+  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
 
 __device__ __forceinline__ float lg2_fast(float x) {
@@ -195,7 +216,7 @@ __device__ __forceinline__ bool any_of_softmax(bool x) {
 __device__ __forceinline__ void sync_softmax() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
 template <int FMT, int NR, bool kBF16>
 __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(const __grid_constant__ LatentTileParams p) {
-  using S = LatentSmem<NR>;
+  using S = LatentSmem<FMT, NR>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const LatentParams& lp = p.l;
   const AttendParams& a = lp.a;
@@ -203,25 +224,30 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
   // (no static shared memory: the dynamic part begins at a multiple of 1,024, which the swizzle wants)
   const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem_raw));
   const int32_t HQ = static_cast<int32_t>(a.group.d);
-  const uint32_t stage_bytes = static_cast<uint32_t>(p.chunks) * kLatChunk;
-  const uint32_t q_at = ring + static_cast<uint32_t>(p.stages) * stage_bytes;
+  const uint32_t units = static_cast<uint32_t>(p.units), raws = static_cast<uint32_t>(p.raws);
+  const uint32_t group_bytes = static_cast<uint32_t>(p.chunks) * 1024u, unit_bytes = 4u * group_bytes, raw_bytes = 2u * group_bytes;
+  const uint32_t raw_ring = ring + units * unit_bytes;
+  const uint32_t q_at = raw_ring + raws * raw_bytes;
   const uint32_t p_at = q_at + static_cast<uint32_t>(S::q_bytes(p.chunks));
   const uint32_t small = p_at + S::kP;
   uint8_t* const small_ptr = smem_raw + (small - ring);
-  const uint32_t full = small + S::kOffBars, empty = full + 8 * kLatMaxStages, q_full = empty + 8 * kLatMaxStages, s_full = q_full + 8,
-                 s_free = s_full + 8 * kLatScores, p_full = s_free + 8 * kLatScores, pv_done = p_full + 16, seg_full = pv_done + 16, seg_empty = seg_full + 16, done = seg_empty + 16,
-                 load_bar = done + 16;
+  const uint32_t full = small + S::kOffBars, empty = full + 8 * kLatMaxUnits, raw_full = empty + 8 * kLatMaxUnits,
+                 raw_empty = raw_full + 8 * kLatMaxRaws, q_full = raw_empty + 8 * kLatMaxRaws, s_full = q_full + 8,
+                 s_free = s_full + 8 * kLatScores, p_full = s_free + 8 * kLatScores, pv_done = p_full + 8, seg_full = pv_done + 8,
+                 seg_empty = seg_full + 16, done = seg_empty + 16;
   LatentSeg* const segs = reinterpret_cast<LatentSeg*>(small_ptr + S::kOffSegs);
   float* const sh_alpha = reinterpret_cast<float*>(small_ptr + S::kOffAlpha);   // [2][NR]
   float* const sh_inv = reinterpret_cast<float*>(small_ptr + S::kOffInv);
   float* const sh_qf = reinterpret_cast<float*>(small_ptr + S::kOffQf);
-  int64_t* const sh_place = reinterpret_cast<int64_t*>(small_ptr + S::kOffPlace);
-  float* const sh_scale = reinterpret_cast<float*>(small_ptr + S::kOffScale);   // [stages][kLatKeys]
-  uint32_t* const sh_valid = reinterpret_cast<uint32_t*>(small_ptr + S::kOffValid);  // of a stage's keys, a bit each
+  uint32_t* const sh_valid = reinterpret_cast<uint32_t*>(small_ptr + S::kOffValid);  // of a unit's keys, a bit each
+  uint32_t* const sh_raw_valid = reinterpret_cast<uint32_t*>(small_ptr + S::kOffRawValid);
+  float* const sh_scale = reinterpret_cast<float*>(small_ptr + S::kOffScale);        // [units][32], then [raws][32]
   WaitState* const state = reinterpret_cast<WaitState*>(small_ptr + S::kOffMisc);
   uint32_t* const sh_tmem = reinterpret_cast<uint32_t*>(small_ptr + S::kOffMisc + 16);
   unsigned long long* const sh_bad = reinterpret_cast<unsigned long long*>(small_ptr + S::kOffMisc + 24);
-  constexpr int kLoaders = kLatLoaders<FMT>;
+  constexpr int kFillers = FMT == KV_CACHE_SRC ? 1 : kLatConverters;  // that arrive for a full unit
+  const bool pair = p.cluster > 1;
+  const uint32_t rank = pair ? blockIdx.x & 1u : 0u;
 
   if (warp == 4) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
@@ -229,28 +255,31 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   if (tid == 0) {
-    for (int i = 0; i < p.stages; ++i) {
-      bar_init(full + 8 * i, 1);
-      bar_init(empty + 8 * i, 1);
+    for (uint32_t i = 0; i < units; ++i) {
+      bar_init(full + 8 * i, kFillers);
+      bar_init(empty + 8 * i, pair ? 2 : 1);
+    }
+    for (uint32_t i = 0; i < raws; ++i) {
+      bar_init(raw_full + 8 * i, 33);
+      bar_init(raw_empty + 8 * i, kLatConverters);
     }
     bar_init(q_full, 128);
     for (int i = 0; i < kLatScores; ++i) {
       bar_init(s_full + 8 * i, 1);
       bar_init(s_free + 8 * i, NR / 16);
     }
+    bar_init(p_full, 128);
+    bar_init(pv_done, 1);
     for (int i = 0; i < 2; ++i) {
-      bar_init(p_full + 8 * i, 128);
-      bar_init(pv_done + 8 * i, 1);
       bar_init(seg_full + 8 * i, 1);
-      bar_init(seg_empty + 8 * i, 6 + kLoaders);
+      bar_init(seg_empty + 8 * i, 7 + (FMT == KV_CACHE_SRC ? 0 : kLatConverters));
+      bar_init(done + 8 * i, 1);
     }
-    bar_init(done, 1);
-    bar_init(done + 8, 1);
-    bar_init(load_bar, kLoaders);
     *state = WaitState{(ring & 1023u) != 0u ? 1 : 0, 0};
     *sh_bad = 0ull;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  if (pair) sync_pair();  // the other CTA's barriers are there
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -268,6 +297,16 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
     return s->stop == 0;
   };
   const uint32_t tm_s = tmem + 4 * NR;  // S, kLatScores buffers of kLatKeys columns, behind O^T
+  // a warp's place in the ring of units
+  struct Place {
+    uint32_t unit, phase;
+  };
+  auto next_unit = [&](Place* w) {
+    if (++w->unit == units) {
+      w->unit = 0u;
+      w->phase ^= 1u;
+    }
+  };
 
   if (warp < 4) {
     // ======================================================================================
@@ -336,14 +375,14 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
       sync_softmax();  // sh_qf
     };
     uint32_t k = 0u, T = 0u;  // segments and tiles that went by
-    uint32_t stage = 0u, phase = 0u;
+    Place at{0u, 0u};
     LatentSeg seg, next;
     bool have = take(k++, &seg);
     const bool lost = any_of_softmax(!ok);
     if (!lost && have && seg.t1 > seg.t0) load_q(seg);
     while (!lost && have) {
-      const int32_t pos[2] = {seg.p_first + static_cast<int32_t>(a.group.quot(static_cast<uint32_t>(seg.row0 + min(r0, seg.nrows - 1)))),
-                              seg.p_first + static_cast<int32_t>(a.group.quot(static_cast<uint32_t>(seg.row0 + min(r0 + 8, seg.nrows - 1))))};
+      const int32_t pos[2] = {seg.p_first + static_cast<int32_t>(a.group.quot(static_cast<uint32_t>(seg.row0 + min(r0, seg.last)))),
+                              seg.p_first + static_cast<int32_t>(a.group.quot(static_cast<uint32_t>(seg.row0 + min(r0 + 8, seg.last))))};
       const int32_t p_lo = seg.p_first + static_cast<int32_t>(a.group.quot(static_cast<uint32_t>(seg.row0)));
       float rs[2], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
 #pragma unroll
@@ -353,48 +392,61 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
         if (rs[c] == 0.0f) rs[c] = __uint_as_float(1u);  // hidden scores (-inf) must stay -inf
       }
       for (int32_t j = seg.t0; j < seg.t1; ++j, ++T) {
-        ok = ok && __all_sync(0xFFFFFFFFu, bar_wait(full + 8 * stage, phase, state));
-        const uint32_t valid = sh_valid[stage];
-        ok = ok && __all_sync(0xFFFFFFFFu, bar_wait(s_full + 8 * (T % kLatScores), (T / kLatScores) & 1u, state));
+        // the units are long there; their keys' bits and scales are read while S is waited for
+        uint64_t valid;
+        uint32_t unit[2];
+        {
+          ok = ok && __all_sync(0xFFFFFFFFu, bar_wait(full + 8 * at.unit, at.phase, state));
+          unit[0] = at.unit;
+          next_unit(&at);
+          ok = ok && __all_sync(0xFFFFFFFFu, bar_wait(full + 8 * at.unit, at.phase, state));
+          unit[1] = at.unit;
+          next_unit(&at);
+          valid = sh_valid[unit[0]] | static_cast<uint64_t>(sh_valid[unit[1]]) << 32;
+        }
+        float s[32], kf[16], alpha[2] = {1.0f, 1.0f};  // scores, their keys' scales, factors of the rows' sums
+        if constexpr (FMT != KV_CACHE_SRC) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float2 f = *reinterpret_cast<const float2*>(sh_scale + unit[i / 4] * kLatUnit + 8 * (i & 3) + 2 * t);
+            kf[2 * i] = f.x;
+            kf[2 * i + 1] = f.y;
+          }
+        }
+        ok = ok && __all_sync(0xFFFFFFFFu, bar_wait(s_full + 8 * (T & 1u), (T >> 1) & 1u, state));
         tc_fence_after();
-        float s[16], kf[8], alpha[2] = {1.0f, 1.0f};  // scores, their keys' scales, factors of the rows' sums
         bool grew = false;
         if (has_rows && ok) {
-          tc_ld_rows(s, tm_s + kLatKeys * (T % kLatScores) + lanes);
+          tc_ld_rows(s, tm_s + kLatKeys * (T & 1u) + lanes);
           tc_fence_before();
-          if (lane == 0u) bar_arrive(s_free + 8 * (T % kLatScores));
+          if (lane == 0u) bar_arrive(s_free + 8 * (T & 1u));
           if constexpr (FMT != KV_CACHE_SRC) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float2 f = *reinterpret_cast<const float2*>(sh_scale + stage * kLatKeys + 8 * i + 2 * t);
-              kf[2 * i] = f.x;
-              kf[2 * i + 1] = f.y;
-            }
-#pragma unroll
-            for (int i = 0; i < 16; ++i) s[i] *= kf[2 * (i / 4) + (i & 1)] * rs[(i >> 1) & 1];
+            for (int i = 0; i < 32; ++i) s[i] *= kf[2 * (i / 4) + (i & 1)] * rs[(i >> 1) & 1];
           }
-          if (j * kLatKeys + kLatKeys - 1 > p_lo || valid != ~0u) {
+          if (j * kLatKeys + kLatKeys - 1 > p_lo || valid != ~0ull) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               const int32_t n = pos[c] - j * kLatKeys + 1;  // the first n keys
-              const uint32_t see = ((n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u) & valid) >> (2 * t);
+              const uint64_t see = (n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1ull) & valid;
+              const uint32_t lo = static_cast<uint32_t>(see) >> (2 * t), hi = static_cast<uint32_t>(see >> 32) >> (2 * t);
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
+              for (int i = 0; i < 8; ++i)
 #pragma unroll
                 for (int x = 0; x < 2; ++x)
-                  if ((see >> (8 * i + x) & 1u) == 0u) s[4 * i + 2 * c + x] = -INFINITY;
+                  if ((((i < 4 ? lo : hi) >> (8 * (i & 3) + x)) & 1u) == 0u) s[4 * i + 2 * c + x] = -INFINITY;
             }
           }
-          float lv[8];
+          float lv[16];
           if constexpr (FMT != KV_CACHE_SRC) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) lv[i] = fmaxf(lg2_fast(fabsf(kf[i])), -100.0f);
+            for (int i = 0; i < 16; ++i) lv[i] = fmaxf(lg2_fast(fabsf(kf[i])), -100.0f);
           }
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             float x[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 8; ++i)
 #pragma unroll
               for (int y = 0; y < 2; ++y) x[y] = fmaxf(x[y], FMT == KV_CACHE_SRC ? s[4 * i + 2 * c + y] : s[4 * i + 2 * c + y] + lv[2 * i + y]);
             float top = fmaxf(x[0], x[1]);
@@ -419,14 +471,14 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
           ok = false;
           break;
         }
-        uint32_t pw[8];
+        uint32_t pw[16];
         if (has_rows) {
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             const float ref = m[c] == -INFINITY ? 0.0f : m[c];
             float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 8; ++i) {
               float2 z = make_float2(s[4 * i + 2 * c], s[4 * i + 2 * c + 1]);
               if constexpr (FMT == KV_CACHE_SRC) z = fma2(z, rs[c], -ref); else z = add2(z, make_float2(-ref, -ref));
               float2 e = make_float2(exp2_fast(z.x), exp2_fast(z.y));
@@ -441,10 +493,9 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
             l[c] = __fmaf_rn(l[c], alpha[c], sum[0].x + sum[0].y);
           }
         }
-        if (T > 1u)  // P V of the last tile but one has read its P
-          ok = __all_sync(0xFFFFFFFFu, bar_wait(pv_done + 8 * (T & 1u), ((T >> 1) - 1u) & 1u, state));
-        if (rescale && ok) {  // and that of the last one has written O^T
-          ok = __all_sync(0xFFFFFFFFu, bar_wait(pv_done + 8 * ((T - 1u) & 1u), ((T - 1u) >> 1) & 1u, state));
+        if (T > 0u)  // P V of the last tile has read P and written O^T
+          ok = __all_sync(0xFFFFFFFFu, bar_wait(pv_done, (T - 1u) & 1u, state));
+        if (rescale && ok) {
           tc_fence_after();
           const float* f = sh_alpha + (T & 1u) * NR;
           for (int32_t b = 0; b < p.blocks; ++b)
@@ -463,17 +514,13 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
           for (int c = 0; c < 2; ++c) {
             const uint32_t r = static_cast<uint32_t>(r0 + 8 * c);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)  // tiles take turns in the halves of P's rows
-              asm volatile("st.shared.u32 [%0], %1;" ::"r"(p_at + r * 128u + (((i + 4u * (T & 1u)) ^ (r & 7u)) << 4) + 4u * t), "r"(pw[2 * i + c]) : "memory");
+            for (int i = 0; i < 8; ++i)
+              asm volatile("st.shared.u32 [%0], %1;" ::"r"(p_at + r * 128u + ((i ^ (r & 7u)) << 4) + 4u * t), "r"(pw[2 * i + c]) : "memory");
           }
         }
         fence_async_shared();
         tc_fence_before();
-        bar_arrive(p_full + 8 * (T & 1u));
-        if (++stage == static_cast<uint32_t>(p.stages)) {
-          stage = 0u;
-          phase ^= 1u;
-        }
+        bar_arrive(p_full);
       }
       if (any_of_softmax(!ok)) break;
       have = take(k++, &next);
@@ -488,7 +535,7 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
         if (has_rows && t == 0u) sh_inv[r0 + 8 * c] = l[c] < INFINITY ? __fdiv_rn(1.0f, l[c]) : NAN;
       }
       if (live) {
-        ok = __all_sync(0xFFFFFFFFu, bar_wait(pv_done + 8 * ((T - 1u) & 1u), ((T - 1u) >> 1) & 1u, state));
+        ok = __all_sync(0xFFFFFFFFu, bar_wait(pv_done, (T - 1u) & 1u, state));
         tc_fence_after();
       }
       if (any_of_softmax(!ok)) break;
@@ -570,99 +617,108 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
       tc_fence_before();
       seg = next;
     }
-  } else if (warp == 4 || warp == 6) {
+  } else if (warp == 4 || warp == 5) {
     // ======================================================================================
-    // the products: warp 4 S = Q K^T, warp 6 O^T += V^T P^T
+    // the products: warp 4 S = Q K^T, warp 5 O^T += V^T P^T
     // ======================================================================================
     auto wait = [&](uint32_t bar, uint32_t parity) {
       if (ok) ok = __all_sync(0xFFFFFFFFu, bar_wait(bar, parity, state));
       tc_fence_after();
     };
     // Descriptors and addresses are to be in uniform registers: a reduction's result is in one, loops end by the
-    // parameters alone, and products stand in straight lines. (Of the 36 + 8 products of a tile of 576 / 512 dims each takes
-    // 25 to 48 clocks to run; with descriptors in any register 70 to 140 to issue.)
+    // parameters alone, and products stand in straight lines. (With descriptors in any register a product took 70 to 140
+    // clocks to issue.)
     auto same = [](uint32_t x) { return __reduce_or_sync(0xFFFFFFFFu, x); };
     const uint32_t ring0 = same(ring);
-    uint32_t k = 0u, T = 0u, stage = 0u, phase = 0u;
+    constexpr uint32_t kType = (1u << 4) | (kBF16 ? 1u << 7 | 1u << 10 : 0u);
+    uint32_t k = 0u, T = 0u;
+    Place at{0u, 0u};
     LatentSeg seg;
-    auto advance = [&] {
-      ++T;
-      if (++stage == static_cast<uint32_t>(p.stages)) {
-        stage = 0u;
-        phase ^= 1u;
-      }
-    };
     if (warp == 4) {
-      const uint32_t desc = (1u << 4) | (kBF16 ? 1u << 7 | 1u << 10 : 0u) | ((static_cast<uint32_t>(kLatKeys) >> 3) << 17) | ((64u >> 4) << 24);
+      constexpr uint32_t kDesc = kType | ((64u >> 4) << 24);  // and N keys
       const uint32_t s_at = same(tm_s);
       const uint64_t q_desc = smem_desc(same(q_at), 16);
       uint32_t items = 0u;
+      // Q against the keys at `from`, N = 64 or 32 of them
+      auto scores = [&](uint32_t d, uint32_t from, uint32_t desc) {
+        const uint64_t kd = smem_desc_groups(from, 16, group_bytes);
+        auto chunk = [&](int32_t c) { tc_mma_chunk(d, q_desc + c * (NR * 128 >> 4), kd + c * (1024 >> 4), desc, c > 0); };
+#pragma unroll
+        for (int c = 0; c < kLatMaxChunks; c += 3) {
+          if (p.ksteps >= 4 * c + 12) {
+            chunk(c); chunk(c + 1); chunk(c + 2);
+          } else {
+#pragma unroll 1
+            for (int32_t y = c; 4 * y + 4 <= p.ksteps; ++y) chunk(y);
+#pragma unroll 1
+            for (int32_t i = p.ksteps & ~3; i < p.ksteps; ++i)
+              tc_mma_ss(d, q_desc + ((i / 4) * (NR * 128 >> 4) + (i % 4) * 2), kd + ((i / 4) * (1024 >> 4) + (i % 4) * 2), desc, i > 0);
+            break;
+          }
+        }
+      };
       while (take(k++, &seg)) {
         if (seg.t1 <= seg.t0) continue;
         wait(q_full, items++ & 1u);
-        for (int32_t j = seg.t0; j < seg.t1; ++j) {
-          const uint32_t u = same(stage | (T % kLatScores) << 8), st = u & 255u, buf = u >> 8;
-          const uint64_t kd = smem_desc(ring0 + st * stage_bytes, 16);
-          const uint32_t d = s_at + kLatKeys * buf;
-          if (T >= kLatScores) wait(s_free + 8 * (T % kLatScores), (T / kLatScores - 1u) & 1u);
-          wait(full + 8 * stage, phase);
+        for (int32_t j = seg.t0; j < seg.t1; ++j, ++T) {
+          if (T >= kLatScores) wait(s_free + 8 * (T & 1u), (T / kLatScores - 1u) & 1u);
+          const uint32_t u = same(at.unit | (T & 1u) << 8), u0 = u & 255u, buf = u >> 8, d = s_at + kLatKeys * buf;
+          wait(full + 8 * at.unit, at.phase);
+          next_unit(&at);
+          wait(full + 8 * at.unit, at.phase);
+          next_unit(&at);
           if (!ok) break;
-          auto chunk = [&](int32_t c) {
-            tc_mma_run<4, 2, 2>(d, q_desc + c * (NR * 128 >> 4), kd + c * (kLatChunk >> 4), desc, c > 0);
-          };
-#pragma unroll
-          for (int c = 0; c < kLatMaxChunks; c += 3) {
-            if (p.ksteps >= 4 * c + 12) {
-              chunk(c); chunk(c + 1); chunk(c + 2);
-            } else {
+          if (u0 + 1u < units) {
+            scores(d, ring0 + u0 * unit_bytes, kDesc | ((64u >> 3) << 17));
+          } else {  // the tile's second half is at the ring's begin
 #pragma unroll 1
-              for (int32_t y = c; 4 * y + 4 <= p.ksteps; ++y) chunk(y);
-              if (p.ksteps >= 4 * c)
-#pragma unroll 1
-                for (int32_t i = p.ksteps & ~3; i < p.ksteps; ++i)
-                  tc_mma_ss(d, q_desc + ((i / 4) * (NR * 128 >> 4) + (i % 4) * 2), kd + ((i / 4) * (kLatChunk >> 4) + (i % 4) * 2), desc, i > 0);
-              break;
-            }
+            for (uint32_t h = 0; h < 2u; ++h) scores(d + kLatUnit * h, h ? ring0 : ring0 + u0 * unit_bytes, kDesc | ((32u >> 3) << 17));
           }
           tc_commit(s_full + 8 * buf);
-          advance();
         }
         if (!ok) break;
       }
     } else {
-      const uint32_t desc = (1u << 4) | (kBF16 ? 1u << 7 | 1u << 10 : 0u) | (1u << 15) | ((static_cast<uint32_t>(NR) >> 3) << 17) | ((128u >> 4) << 24);
-      const uint32_t o_at = same(tmem), free0 = same(empty);
+      constexpr uint32_t kDesc = kType | (1u << 15) | ((static_cast<uint32_t>(NR) >> 3) << 17) | ((128u >> 4) << 24);
+      const uint32_t o_at = same(tmem), free0 = same(empty), step = same(group_bytes >> 3);  // 16 keys, in 16 bytes
       const uint64_t p_desc = smem_desc(same(p_at), 16);
       while (take(k++, &seg)) {
-        for (int32_t j = seg.t0; j < seg.t1; ++j) {
-          const uint32_t u = same(stage | (T & 1u) << 8 | (j > seg.t0 ? 512u : 0u)), st = u & 255u, odd = u >> 8 & 1u, old = u >> 9;
-          const uint64_t v = smem_desc(ring0 + st * stage_bytes, kLatChunk), pd = p_desc + 4 * odd;
-          wait(full + 8 * stage, phase);
-          wait(p_full + 8 * (T & 1u), (T >> 1) & 1u);
-          if (!ok) break;
-          auto block = [&](int32_t b) {
-            tc_mma_run<kLatKeys / 16, (2048 >> 4), 2>(o_at + b * NR, v + b * (2 * kLatChunk >> 4), pd, desc, old != 0u);
-          };
-          if (p.blocks == 4) {
-            block(0); block(1); block(2); block(3);
-          } else {
-#pragma unroll 1
-            for (int32_t b = 0; b < p.blocks; ++b) block(b);
+        for (int32_t j = seg.t0; j < seg.t1; ++j, ++T) {
+          Place two[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            two[h] = at;
+            wait(full + 8 * at.unit, at.phase);
+            next_unit(&at);
           }
-          tc_commit(free0 + 8 * st);
-          tc_commit(pv_done + 8 * odd);
-          advance();
+          const uint32_t u = same(two[0].unit | two[1].unit << 8 | (j > seg.t0 ? 1u << 16 : 0u));
+          wait(p_full, T & 1u);
+          if (!ok) break;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t un = (u >> (8 * h)) & 255u;
+            const uint64_t v = smem_desc_groups(ring0 + un * unit_bytes, 1024, group_bytes);
+            auto block = [&](int32_t b) { tc_mma_two(o_at + b * NR, v + b * (2048 >> 4), p_desc + 4 * h, kDesc, h > 0 || (u >> 16) != 0u, step, 2u); };
+            if (p.blocks == 4) {
+              block(0); block(1); block(2); block(3);
+            } else {
+#pragma unroll 1
+              for (int32_t b = 0; b < p.blocks; ++b) block(b);
+            }
+            if (pair) tc_commit_pair(free0 + 8 * un); else tc_commit(free0 + 8 * un);
+          }
+          tc_commit(pv_done);
         }
         if (!ok) break;
       }
     }
     if (!ok) {  // products still in flight read shared memory and write TMEM: let them end
-      const uint32_t bar = warp == 4 ? done : done + 8;
+      const uint32_t bar = done + 8 * (warp & 1u);
       tc_commit(bar);
       for (uint32_t i = 0; i < kSpin && !bar_try(bar, 0); ++i) {}
     }
     __syncwarp();
-  } else if (warp == 5) {
+  } else if (warp == 6) {
     // ======================================================================================
     // the work, item by item
     // ======================================================================================
@@ -682,9 +738,9 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
     }
     ShareLevel level[2] = {};
     int32_t shares = 0, levels = 1;
-    const int32_t ctas = static_cast<int32_t>(gridDim.x);
+    const int32_t ctas = static_cast<int32_t>(gridDim.x) / p.cluster, cta = static_cast<int32_t>(blockIdx.x) / p.cluster;
     if (p.split) {
-      levels = latent_cut(total, ctas, p.max_shares, p.min_steps, level, &shares);
+      levels = latent_cut(total, ctas, pair, p.max_shares, p.min_steps, level, &shares);
       if (blockIdx.x == 0 && lane == 0u) {
         p.head->level[0] = level[0];
         p.head->level[1] = level[1];
@@ -706,7 +762,7 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
       ++k;
     };
     int32_t round = 0;
-    int32_t share = static_cast<int32_t>(blockIdx.x);
+    int32_t share = cta;
     while (ok) {
       int64_t pos, end;
       if (p.split) {
@@ -715,7 +771,7 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
         pos = level[lv].start + static_cast<int64_t>(share - level[lv].first) * level[lv].size;
         end = min(lv + 1 < levels ? level[1].start : total, pos + level[lv].size);
       } else {  // items in turn, every second round the other way
-        pos = static_cast<int64_t>(round) * ctas + ((round & 1) ? ctas - 1 - static_cast<int32_t>(blockIdx.x) : static_cast<int32_t>(blockIdx.x));
+        pos = static_cast<int64_t>(round) * ctas + ((round & 1) ? ctas - 1 - cta : cta);
         end = pos + 1;
         ++round;
         if (pos >= total) {
@@ -743,7 +799,7 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
         LatentSeg s = {};
         s.b = cur_b + src;
         const AttendSeq seq = attend_seq(a, s.b, false);
-        const LatentGeom geom = latent_geom<NR>(a, seq);
+        const LatentGeom geom = latent_geom<NR>(p, seq);
         const int32_t unit = p.split ? geom.steps : 1;
         int32_t item = static_cast<int32_t>(local / unit);
         const int32_t s_in = static_cast<int32_t>(local - static_cast<int64_t>(item) * unit);
@@ -753,193 +809,186 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
         s.q0 = seq.q0;
         s.nq = seq.nq;
         s.p_first = seq.len - seq.nq;
-        s.row0 = item * NR;
-        s.nrows = min(NR, seq.nq * HQ - s.row0);
-        const int32_t p_hi = s.p_first + static_cast<int32_t>(a.group.quot(static_cast<uint32_t>(s.row0 + s.nrows - 1)));
-        const int32_t tiles = p_hi < 0 ? 0 : p_hi / kLatKeys + 1;
+        const int32_t rows = seq.nq * HQ, first = item * NR * p.cluster;
+        s.row0 = min(first + static_cast<int32_t>(rank) * NR, rows - 1);
+        s.nrows = max(min(NR, rows - (first + static_cast<int32_t>(rank) * NR)), 0);
+        s.last = max(s.nrows - 1, 0);
+        s.p_hi = s.p_first + static_cast<int32_t>(a.group.quot(static_cast<uint32_t>(min(rows, first + NR * p.cluster) - 1)));
+        const int32_t tiles = s.p_hi < 0 ? 0 : s.p_hi / kLatKeys + 1;
         s.t0 = p.split ? min(s_in, tiles) : 0;
         s.t1 = p.split ? min(s_out, tiles) : tiles;
-        s.part = s_out - s_in == unit ? -1 : 2 * share + (s_in == 0 ? 1 : 0);
+        s.part = s_out - s_in == unit ? -1 : (2 * share + (s_in == 0 ? 1 : 0)) * p.cluster + static_cast<int32_t>(rank);
         publish(s);
       }
       if (p.split) {
-        int32_t after = 0;
-        if (lane == 0u) after = static_cast<int32_t>(gridDim.x + atomicAdd(&p.head->next, 1u));
+        int32_t after = shares;  // a pair has one share
+        if (lane == 0u && !pair) after = static_cast<int32_t>(gridDim.x + atomicAdd(&p.head->next, 1u));
         share = __shfl_sync(0xFFFFFFFFu, after, 0);
       }
     }
     LatentSeg s = {};
     s.stop = 1;
     publish(s);
-  } else {
+  } else if (warp == 7) {
     // ======================================================================================
-    // the tiles
+    // the keys, a unit of 32 at a time
     // ======================================================================================
-    constexpr uint32_t kN = 32u * kLoaders;
-    const uint32_t lt = tid - 7u * 32u;  // of the loaders
-    uint32_t k = 0u, T = 0u, stage = 0u, phase = 0u;
+    uint32_t k = 0u, n = 0u;  // units that went by
+    Place at{0u, 0u};         // in the ring of units, or of raw ones
+    const uint32_t places = FMT == KV_CACHE_SRC ? units : raws;
+    const uint32_t full_at = FMT == KV_CACHE_SRC ? full : raw_full, empty_at = FMT == KV_CACHE_SRC ? empty : raw_empty;
+    const uint32_t pieces = static_cast<uint32_t>(a.head_dim) / (FMT == KV_CACHE_SRC ? 8u : 16u);  // 16-byte pieces of a row
     LatentSeg seg;
-    // the stage is free: all that read it has ended
-    auto wait_empty = [&] {
-      if (ok && T >= static_cast<uint32_t>(p.stages)) ok = __all_sync(0xFFFFFFFFu, bar_wait(empty + 8 * stage, phase ^ 1u, state));
-    };
-    auto advance = [&] {
-      ++T;
-      if (++stage == static_cast<uint32_t>(p.stages)) {
-        stage = 0u;
-        phase ^= 1u;
+    // 16-bit units that were copied by cp.async, and not yet handed over: the copies land while the next ones are issued
+    uint32_t pending[2] = {0u, 0u}, waiting = 0u;
+    auto hand_over = [&](bool all) {
+      if constexpr (FMT == KV_CACHE_SRC) {
+        while (waiting > (all ? 0u : 1u)) {
+          if (waiting == 2u) wait_async<1>(); else wait_async<0>();
+          fence_async_shared();
+          __syncwarp();
+          if (lane == 0u) bar_arrive(full + 8 * pending[0]);
+          pending[0] = pending[1];
+          --waiting;
+        }
       }
     };
-    // the loaders wait for one another, with the limit of all waits
-    uint32_t syncs = 0u;
-    auto sync_loaders = [&] {
-      __syncwarp();
-      if (lane == 0u) bar_arrive(load_bar);
-      ok = ok && __all_sync(0xFFFFFFFFu, bar_wait(load_bar, syncs++ & 1u, state));
-    };
-    const uint32_t per_row = static_cast<uint32_t>(a.head_dim) / (FMT == KV_CACHE_SRC ? 8u : 16u);  // 16-byte pieces
     while (take(k++, &seg)) {
       const int32_t* table = a.table + static_cast<int64_t>(seg.b) * a.table_stride;
-      const int32_t p_hi = seg.p_first + static_cast<int32_t>(a.group.quot(static_cast<uint32_t>(seg.row0 + seg.nrows - 1)));
-      // the page of key j of a tile (of its last key a row sees, for keys behind it)
-      auto page_at = [&](int32_t j) { return __ldg(table + a.page.quot(static_cast<uint32_t>(min(j, p_hi)))); };
-      // by the first loader warp, a key a lane: where its row lies (-1: no row needs it), into sh_place; the others do nothing
-      auto place = [&](int32_t tile, int32_t id) {
-        const int32_t j = tile * kLatKeys + static_cast<int32_t>(lt);
-        const bool want = j <= p_hi, have = static_cast<uint32_t>(id) < static_cast<uint32_t>(a.num_pages);
-        if (want && !have) record_oob(a.err, static_cast<uint64_t>(seg.b));
-        const uint32_t off = static_cast<uint32_t>(j) - a.page.quot(static_cast<uint32_t>(j)) * a.page.d;
-        sh_place[lt] = want && have ? wide(id, p.page_stride) + wide(off, p.slot_stride) : -1;
-        return want && have ? off : 0xFFFFFFFFu;
+      const int32_t n0 = 2 * seg.t0, n1 = 2 * seg.t1;
+      // lane = key: its page (of the last key that a row sees, for keys behind it), a unit ahead of its use
+      auto page_of = [&](int32_t unit) {
+        return __ldg(table + a.page.quot(static_cast<uint32_t>(min(unit * kLatUnit + static_cast<int32_t>(lane), seg.p_hi))));
       };
-      if constexpr (FMT == KV_CACHE_SRC) {
-        const int32_t boxes = p.box > 0 ? kLatKeys / p.box : 0;
-        const uint32_t box_bytes = static_cast<uint32_t>(p.box) * 128u;
-        // lane i: the page of the tile's i-th box; every loader warp knows whether all are there
-        auto box_page = [&](int32_t tile) -> int32_t {
-          if (tile >= seg.t1 || static_cast<int32_t>(lane) >= boxes) return 0;
-          return page_at(tile * kLatKeys + static_cast<int32_t>(lane) * p.box);
-        };
-        int32_t next_box = box_page(seg.t0), next_id = seg.t0 < seg.t1 && lt < kLatKeys ? page_at(seg.t0 * kLatKeys + static_cast<int32_t>(lt)) : 0;
-        for (int32_t tile = seg.t0; tile < seg.t1 && ok; ++tile) {
-          const int32_t page = next_box, id = next_id;
-          next_box = box_page(tile + 1);
-          if (lt < kLatKeys && tile + 1 < seg.t1) next_id = page_at((tile + 1) * kLatKeys + static_cast<int32_t>(lt));
-          const bool whole = boxes > 0 && tile * kLatKeys + kLatKeys - 1 <= p_hi &&
-                             __all_sync(0xFFFFFFFFu, static_cast<int32_t>(lane) >= boxes || (page >= 0 && page < a.num_pages));
-          if (whole) {
-            const uint32_t key = static_cast<uint32_t>(tile * kLatKeys + static_cast<int32_t>(lane) * p.box);
-            const int32_t in_page = static_cast<int32_t>(key - a.page.quot(key) * a.page.d);
-            wait_empty();
-            if (ok && lt < 32u) {
-              const uint32_t bar = full + 8 * stage;
-              if (lane == 0u) {
-                sh_valid[stage] = ~0u;
-                bar_arrive_expect(bar, stage_bytes);
-              }
-              __syncwarp();
-              if (static_cast<int32_t>(lane) < boxes)
-                for (int32_t c = 0; c < p.chunks; ++c)
-                  tma_box(ring + stage * stage_bytes + c * kLatChunk + lane * box_bytes, &p.map, bar, 64 * c, in_page, 0, page);
-            }
-          } else {
-            wait_empty();
-            if (lt < kLatKeys) {
-              const bool have = place(tile, id) != 0xFFFFFFFFu;
-              const uint32_t bits = __ballot_sync(0xFFFFFFFFu, have);
-              if (lane == 0u && ok) sh_valid[stage] = bits;
-            }
-            sync_loaders();
-            const uint32_t at = ring + stage * stage_bytes;
-            if (ok)
-              for (uint32_t i = lt; i < kLatKeys * per_row; i += kN) {
-                const uint32_t key = i / per_row, piece = i - key * per_row;
-                const int64_t off = sh_place[key];
-                copy_async<16>(at + (piece >> 3) * kLatChunk + key * 128u + (((piece & 7u) ^ (key & 7u)) << 4),
-                               a.k + (off < 0 ? 0 : off + 16 * piece), off < 0 ? 0u : 16u);
-              }
-            wait_all_async();
-            fence_async_shared();
-            sync_loaders();
-            if (lt == 0u && ok) bar_arrive(full + 8 * stage);
-          }
-          if (ok) advance();
+      int32_t next_id = n0 < n1 ? page_of(n0) : 0;
+      for (int32_t unit = n0; unit < n1 && ok; ++unit, ++n) {
+        const int32_t id = next_id, key = unit * kLatUnit + static_cast<int32_t>(lane);
+        if (unit + 1 < n1) next_id = page_of(unit + 1);
+        const bool want = key <= seg.p_hi, have = static_cast<uint32_t>(id) < static_cast<uint32_t>(a.num_pages);
+        if (want && !have && rank == 0u) record_oob(a.err, static_cast<uint64_t>(seg.b));
+        const uint32_t bits = __ballot_sync(0xFFFFFFFFu, want && have);
+        const uint32_t off = static_cast<uint32_t>(key) - a.page.quot(static_cast<uint32_t>(key)) * a.page.d;
+        if (n >= places) {
+          if (waiting > 0u && !__all_sync(0xFFFFFFFFu, bar_try(empty_at + 8 * at.unit, at.phase ^ 1u))) hand_over(true);
+          ok = __all_sync(0xFFFFFFFFu, bar_wait(empty_at + 8 * at.unit, at.phase ^ 1u, state));
+          if (!ok) break;
+          if constexpr (FMT != KV_CACHE_SRC) fence_async_shared();  // generic loads, and then boxes
         }
-      } else {
-        constexpr int kPer = (kLatKeys * kLatMaxChunks * 4 + static_cast<int>(kN) - 1) / static_cast<int>(kN);  // pieces of a thread
-        const uint32_t pieces = kLatKeys * per_row;
-        uint4 w[2][kPer];
-        float sc[2] = {0.0f, 0.0f};
-        uint32_t have[2] = {0u, 0u};
-        int32_t next_id = seg.t0 < seg.t1 && lt < kLatKeys ? page_at(seg.t0 * kLatKeys + static_cast<int32_t>(lt)) : 0;
-        auto load = [&](int32_t tile, uint4 (&v)[kPer], float* scale, uint32_t* bits) {
-          sync_loaders();  // sh_place has been read
-          if (lt < kLatKeys) {
-            const int32_t id = next_id;
-            if (tile + 1 < seg.t1) next_id = page_at((tile + 1) * kLatKeys + static_cast<int32_t>(lt));
-            const uint32_t off = place(tile, id);
-            *scale = 0.0f;
-            if (off != 0xFFFFFFFFu) *scale = row_scale(lp, id, off);
-            *bits = __ballot_sync(0xFFFFFFFFu, off != 0xFFFFFFFFu);
-          }
-          sync_loaders();
-#pragma unroll
-          for (int i = 0; i < kPer; ++i) {
-            const uint32_t n = lt + i * kN, key = n / per_row, piece = n - key * per_row;
-            v[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (n < pieces) {
-              const int64_t off = sh_place[key];
-              if (off >= 0) v[i] = __ldg(reinterpret_cast<const uint4*>(a.k + off + 16 * piece));
+        const uint32_t bar = full_at + 8 * at.unit;
+        const uint32_t dst = FMT == KV_CACHE_SRC ? ring + at.unit * unit_bytes : raw_ring + at.unit * raw_bytes;
+        const uint32_t part = FMT == KV_CACHE_SRC ? group_bytes : group_bytes / 2u;  // of eight keys
+        if (lane == 0u) (FMT == KV_CACHE_SRC ? sh_valid : sh_raw_valid)[at.unit] = bits;
+        if constexpr (FMT != KV_CACHE_SRC) {
+          const bool live = want && have;
+          copy_async<4>(static_cast<uint32_t>(__cvta_generic_to_shared(sh_scale + (units + at.unit) * kLatUnit + lane)),
+                        reinterpret_cast<const uint8_t*>(live ? lp.scales + (static_cast<int64_t>(id) * a.page.d + off) * lp.scale_slot : lp.scales),
+                        live ? 4u : 0u);
+        }
+        if (p.tma && bits == ~0u) {
+          hand_over(true);
+          // lane g: the eight keys from 8 g on (which share a page); of a pair's CTAs each brings two of the four
+          const int32_t page = __shfl_sync(0xFFFFFFFFu, id, 8 * (lane & 3u)), in_page = static_cast<int32_t>(__shfl_sync(0xFFFFFFFFu, off, 8 * (lane & 3u)));
+          if (lane == 0u) bar_arrive_expect(bar, 4u * part);
+          __syncwarp();
+          if (lane < 4u && (!pair || (lane >> 1) == rank)) {
+            const uint32_t to = dst + lane * part, span = part / static_cast<uint32_t>(p.chunks);
+            const int32_t boxes = p.tma == 2 ? 1 : p.chunks;
+            for (int32_t c = 0; c < boxes; ++c) {
+              if (pair) tma_box_pair(to + c * span, &p.map, bar, 64 * c, in_page, 0, page);
+              else tma_box(to + c * span, &p.map, bar, 64 * c, in_page, 0, page);
             }
           }
-        };
-        auto put = [&](const uint4 (&v)[kPer], float scale, uint32_t bits) {
-          wait_empty();
-          const uint32_t at = ring + stage * stage_bytes;
-          if (ok) {
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-              const uint32_t n = lt + i * kN, key = n / per_row, piece = n - key * per_row;
-              if (n < pieces) {
-                const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-                uint32_t f[8];
-#pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                  f[2 * y] = f16x2_from_e4m3x2(x[y]);
-                  f[2 * y + 1] = f16x2_from_e4m3x2(x[y] >> 16);
-                }
-                // pieces of two neighbouring chunks take turns, so that eight lanes meet all banks
-                const uint32_t row = at + (piece >> 2) * kLatChunk + key * 128u, first = piece >> 2 & 1u;
-                const uint32_t at0 = row + (((2u * (piece & 3u) + first) ^ (key & 7u)) << 4), at1 = row + (((2u * (piece & 3u) + 1u - first) ^ (key & 7u)) << 4);
-                st_shared16(at0, first ? f[4] : f[0], first ? f[5] : f[1], first ? f[6] : f[2], first ? f[7] : f[3]);
-                st_shared16(at1, first ? f[0] : f[4], first ? f[1] : f[5], first ? f[2] : f[6], first ? f[3] : f[7]);
-              }
-            }
-            if (lt < kLatKeys) {
-              sh_scale[stage * kLatKeys + lt] = scale;
-              if (lane == 0u) sh_valid[stage] = bits;
-            }
+          if constexpr (FMT != KV_CACHE_SRC) bar_arrive_copies(bar);  // the scales
+        } else {
+          const int64_t row = want && have ? wide(id, p.page_stride) + wide(off, p.slot_stride) : -1;
+          // pieces in turn, so that lanes copy neighbouring ones
+          for (uint32_t i0 = 0; i0 < kLatUnit * pieces; i0 += 32u) {
+            const uint32_t i = i0 + lane, kk = i / pieces, piece = i - kk * pieces;
+            const int64_t r = __shfl_sync(0xFFFFFFFFu, row, kk);
+            const uint32_t base = dst + (kk >> 3) * part;
+            const uint32_t to = FMT == KV_CACHE_SRC ? base + (piece >> 3) * 1024u + (kk & 7u) * 128u + (((piece & 7u) ^ (kk & 7u)) << 4)
+                                                    : base + (piece >> 2) * 512u + (kk & 7u) * 64u + ((piece & 3u) << 4);
+            copy_async<16>(to, a.k + (r < 0 ? 0 : r + 16 * piece), r < 0 ? 0u : 16u);
           }
-          fence_async_shared();
-          sync_loaders();
-          if (lt == 0u && ok) bar_arrive(full + 8 * stage);
-          if (ok) advance();
-        };
-        if (seg.t0 < seg.t1) load(seg.t0, w[0], &sc[0], &have[0]);
-        for (int32_t tile = seg.t0; tile < seg.t1 && ok; tile += 2) {
-          if (tile + 1 < seg.t1) load(tile + 1, w[1], &sc[1], &have[1]);
-          put(w[0], sc[0], have[0]);
-          if (tile + 1 < seg.t1) {
-            if (tile + 2 < seg.t1) load(tile + 2, w[0], &sc[0], &have[0]);
-            put(w[1], sc[1], have[1]);
+          if constexpr (FMT == KV_CACHE_SRC) {
+            commit_async();
+            pending[waiting++] = at.unit;
+            hand_over(false);
+          } else {
+            bar_arrive_copies(bar);
+            if (lane == 0u) bar_arrive(bar);
           }
+        }
+        if (++at.unit == places) {
+          at.unit = 0u;
+          at.phase ^= 1u;
         }
       }
+      hand_over(true);
       if (!ok) break;
     }
-    if (!ok) {  // copies in flight write shared memory: let them land before the CTA leaves it
-      wait_all_async();
+    wait_all_async();
+    if (!ok)  // boxes in flight write shared memory: let them land before the CTA leaves it
       for (int i = 0; i < 1000; ++i) __nanosleep(1000);
+  } else if constexpr (FMT != KV_CACHE_SRC) {
+    // ======================================================================================
+    // e4m3fn rows to fp16: a warp takes eight keys of a chunk at a time, 16 codes a lane
+    // ======================================================================================
+    constexpr int kPer = (4 * kLatMaxChunks + kLatConverters - 1) / kLatConverters;
+    const uint32_t w = warp - 8u, jobs = 4u * static_cast<uint32_t>(p.chunks);
+    const uint32_t row = lane >> 2, q = lane & 3u;
+    uint32_t k = 0u, n = 0u;
+    Place at{0u, 0u}, from{0u, 0u};
+    LatentSeg seg;
+    while (take(k++, &seg)) {
+      for (int32_t unit = 2 * seg.t0; unit < 2 * seg.t1; ++unit, ++n) {
+        ok = __all_sync(0xFFFFFFFFu, bar_wait(raw_full + 8 * from.unit, from.phase, state));
+        if (!ok) break;
+        uint4 v[kPer];
+        const uint32_t src = raw_ring + from.unit * raw_bytes;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+          if (w + kLatConverters * i < jobs) v[i] = ld_shared16(src + (w + kLatConverters * i) * 512u + lane * 16u);
+        float scale = 0.0f;
+        uint32_t bits = 0u;
+        if (w == 0u) {
+          scale = sh_scale[(units + from.unit) * kLatUnit + lane];
+          bits = sh_raw_valid[from.unit];
+        }
+        __syncwarp();
+        if (lane == 0u) bar_arrive(raw_empty + 8 * from.unit);
+        if (++from.unit == raws) {
+          from.unit = 0u;
+          from.phase ^= 1u;
+        }
+        if (n >= units) ok = __all_sync(0xFFFFFFFFu, bar_wait(empty + 8 * at.unit, at.phase ^ 1u, state));
+        if (!ok) break;
+        const uint32_t dst = ring + at.unit * unit_bytes;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          if (w + kLatConverters * i < jobs) {
+            const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+            uint32_t f[8];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              f[2 * y] = f16x2_from_e4m3x2(x[y]);
+              f[2 * y + 1] = f16x2_from_e4m3x2(x[y] >> 16);
+            }
+            const uint32_t to = dst + (w + kLatConverters * i) * 1024u + row * 128u;
+            st_shared16(to + (((2u * q) ^ row) << 4), f[0], f[1], f[2], f[3]);
+            st_shared16(to + (((2u * q + 1u) ^ row) << 4), f[4], f[5], f[6], f[7]);
+          }
+        }
+        if (w == 0u) {
+          sh_scale[at.unit * kLatUnit + lane] = scale;
+          if (lane == 0u) sh_valid[at.unit] = bits;
+        }
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0u) bar_arrive(full + 8 * at.unit);
+        next_unit(&at);
+      }
+      if (!ok) break;
     }
   }
   tc_fence_before();
@@ -952,6 +1001,7 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   }
+  if (pair) sync_pair();  // the other CTA's boxes and arrivals come here
 }
 
 constexpr int kLatJoinWarps = 16;
@@ -972,7 +1022,7 @@ __global__ void __launch_bounds__(32 * kLatJoinWarps) kv_attend_latent_join(cons
   const int32_t tok = static_cast<int32_t>(row_of / a.q_heads), h = static_cast<int32_t>(row_of - static_cast<int64_t>(tok) * a.q_heads);
   grid_handover();
   if (blockIdx.x == 0 && threadIdx.x == 0) p.head->next = 0u;
-  int32_t b = tok, c0 = 0, c1 = 0, r = 0, pos = 0;
+  int32_t b = tok, c0 = 0, c1 = 0, r = 0, rank = 0, pos = 0;
   bool joined = false, lost = false;
   if (tok < a.num_q) {
     if (a.q_start) {
@@ -985,9 +1035,10 @@ __global__ void __launch_bounds__(32 * kLatJoinWarps) kv_attend_latent_join(cons
     }
     const AttendSeq s = attend_seq(a, b, false);
     if (tok >= s.q0 && tok < s.q0 + s.nq) {
-      const LatentGeom geom = latent_geom<NR>(a, s);
-      const int32_t row = (tok - s.q0) * a.q_heads + h, rb = row / NR;
-      r = row - rb * NR;
+      const LatentGeom geom = latent_geom<NR>(p, s);
+      const int32_t row = (tok - s.q0) * a.q_heads + h, rb = row / (NR * p.cluster);
+      rank = row / NR - rb * p.cluster;
+      r = row % NR;
       pos = s.len - s.nq + (tok - s.q0);
       const int64_t s0 = p.meta[b] + static_cast<int64_t>(rb) * geom.steps;
       c0 = share_of(p.head, s0);
@@ -1019,7 +1070,7 @@ __global__ void __launch_bounds__(32 * kLatJoinWarps) kv_attend_latent_join(cons
         ml[x] = make_float2(-INFINITY, 0.0f);
         v[x] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (cc <= c1) {
-          const int64_t at = static_cast<int64_t>(2 * cc + (cc == c0 ? 1 : 0)) * p.part_rows + r;
+          const int64_t at = (static_cast<int64_t>(2 * cc + (cc == c0 ? 1 : 0)) * p.cluster + rank) * p.part_rows + r;
           ml[x] = __ldcg(reinterpret_cast<const float2*>(p.part_ml + at * 2));
           v[x] = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * width + 128 * block) + lane);
         }
@@ -1062,11 +1113,37 @@ __global__ void __launch_bounds__(32 * kLatJoinWarps) kv_attend_latent_join(cons
 // Host
 // ---------------------------------------------------------------------------
 
-constexpr int kLatMinSteps = 8;  // tiles of a share at least
+constexpr int kLatMinSteps = 4;  // tiles of a share at least
+
+// Pairs of CTAs of a kernel that can be resident at once, per device.
+inline kv_status pairs_resident(const void* kernel, int threads, int smem, std::atomic<int>* known, int* out) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e);
+  std::atomic<int>* at = dev >= 0 && dev < kMaxDevices ? known + dev : nullptr;
+  int n = at ? at->load(std::memory_order_relaxed) : 0;
+  if (n == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+    if (e != cudaSuccess) return cuda_fail(e);
+    if (at) at->store(n, std::memory_order_relaxed);
+  }
+  *out = n;
+  return KV_OK;
+}
 
 template <int FMT, int NR, bool kBF16>
 kv_status launch_latent_tile(LatentTileParams p, void* work, int64_t work_bytes, int64_t max_keys, cudaStream_t stream) {
-  using S = LatentSmem<NR>;
+  using S = LatentSmem<FMT, NR>;
   const AttendParams& a = p.l.a;
   auto* kernel = kv_attend_latent_tile<FMT, NR, kBF16>;
   constexpr int kMost = 227 * 1024;
@@ -1076,33 +1153,68 @@ kv_status launch_latent_tile(LatentTileParams p, void* work, int64_t work_bytes,
   int sms = 0;
   st = current_sm_count(&sms);
   if (st != KV_OK) return st;
-  p.stages = 2;
-  while (p.stages < kLatMaxStages && S::total(p.chunks, p.stages + 1) <= kMost) ++p.stages;
-  const int64_t items = static_cast<int64_t>(a.num_q) * a.group.d / NR + a.num_seqs;  // at most
+  p.units = 3;
+  if (FMT == KV_CACHE_SRC) {
+    while (p.units < kLatMaxUnits && S::total(p.chunks, p.units + 1, 0) <= kMost) ++p.units;
+  } else {
+    p.raws = 2;
+    if (S::total(p.chunks, 4, 4) <= kMost) p.units = 4;
+    while (p.raws < kLatMaxRaws && S::total(p.chunks, p.units, p.raws + 1) <= kMost) ++p.raws;
+  }
+  const int smem = S::total(p.chunks, p.units, p.raws);
+  int64_t ctas = sms;  // or pairs
+  if (p.cluster > 1) {
+    static std::atomic<int> known[kMaxDevices];
+    int pairs = 0;
+    st = pairs_resident(reinterpret_cast<const void*>(kernel), kLatThreads<FMT>, kMost, known, &pairs);
+    if (st != KV_OK) return st;
+    ctas = pairs;
+    if (pairs < 1) {
+      p.cluster = 1;
+      ctas = sms;
+    }
+  }
+  const int64_t items = static_cast<int64_t>(a.num_q) * a.group.d / (NR * p.cluster) + a.num_seqs;  // at most
   const int64_t meta = (static_cast<int64_t>(a.num_seqs) + 31) / 32 * 256;
   p.part_rows = a.q_start || static_cast<int32_t>(a.group.d) > NR ? NR : static_cast<int32_t>(a.group.d);
-  const int64_t slot = static_cast<int64_t>(p.part_rows) * (128 * p.blocks + 2) * 4;
+  const int64_t slot = static_cast<int64_t>(p.cluster) * p.part_rows * (128 * p.blocks + 2) * 4;
   int64_t fit = work && work_bytes > kSplitHead + meta ? (work_bytes - kSplitHead - meta) / (2 * slot) : 0;
-  if (fit > 8 * sms) fit = 8 * sms;
+  if (fit > 8 * ctas) fit = 8 * ctas;
   p.min_steps = kLatMinSteps;
-  p.split = items < 4 * sms && max_keys > kLatMinSteps * kLatKeys && 2 * fit >= sms;
-  int64_t grid = items < sms ? items : sms;
+  p.split = items < 4 * ctas && max_keys > kLatMinSteps * kLatKeys && 2 * fit >= ctas;
+  int64_t grid = items < ctas ? items : ctas;
   if (p.split) {
-    grid = fit < sms ? fit : sms;
+    grid = fit < ctas ? fit : ctas;
     p.max_shares = static_cast<int32_t>(fit);
     p.head = static_cast<SplitWork*>(work);
     p.meta = reinterpret_cast<int64_t*>(static_cast<uint8_t*>(work) + kSplitHead);
     p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(work) + kSplitHead + meta);
-    p.part_ml = p.part_o + 2 * fit * p.part_rows * 128 * p.blocks;
+    p.part_ml = p.part_o + 2 * fit * p.cluster * p.part_rows * 128 * p.blocks;
   }
-  st = launch_chained(kernel, grid, kLatThreads<FMT>, S::total(p.chunks, p.stages), stream, p);
-  if (st != KV_OK || !p.split) return st;
+  {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid * p.cluster));
+    cfg.blockDim = dim3(kLatThreads<FMT>);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(p.cluster);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.cluster > 1 ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
+    if (e != cudaSuccess) return cuda_fail(e);
+  }
+  if (!p.split) return KV_OK;
   // the fewer the rows, the more parts has each and the more warps take it
-  const int64_t units = static_cast<int64_t>(a.num_q) * a.q_heads * p.blocks;
+  const int64_t rows = static_cast<int64_t>(a.num_q) * a.q_heads * p.blocks;
   int32_t wpr = 1;
-  while (wpr < kLatJoinWarps && units * wpr < 16ll * sms) wpr *= 2;
+  while (wpr < kLatJoinWarps && rows * wpr < 16ll * sms) wpr *= 2;
   const int64_t per = kLatJoinWarps / wpr;
-  return launch_chained(kv_attend_latent_join<FMT, NR>, (units + per - 1) / per, 32 * kLatJoinWarps, 0, stream, p, wpr);
+  return launch_chained(kv_attend_latent_join<FMT, NR>, (rows + per - 1) / per, 32 * kLatJoinWarps, 0, stream, p, wpr);
 }
 
 // The instantiations: 16-bit rows, and e4m3fn ones.
