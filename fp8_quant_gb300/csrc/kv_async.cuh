@@ -85,4 +85,10 @@ bool cache_map(CUtensorMap* map, const void* cache, int elem_bytes, bool bf16, i
                int64_t pages, int64_t slot_stride, int64_t head_stride, int64_t page_stride, int width, int keys, int box_heads,
                bool swizzle);
 
+// The tensor map of a cache of latent rows: (dim of a chunk or of the row, key of a group of eight, chunk, group of its page,
+// page), boxes of `groups` groups whose keys lie as [group][chunk][key][64 elements]. With box_chunks 1 dims are the row's, so
+// that those behind it are zeros. False where there is none (strides are positive multiples of 16 bytes below 2^40).
+bool latent_map(CUtensorMap* map, const void* cache, int elem_bytes, bool bf16, int64_t row, int64_t page_size, int64_t pages,
+                int64_t slot_stride, int64_t page_stride, int chunks, int box_chunks, int groups, bool swizzle);
+
 }  // namespace kvimpl

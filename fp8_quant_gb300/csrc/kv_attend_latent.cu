@@ -131,14 +131,15 @@ extern "C" kv_status kv_attend_latent(const void* q, void* out, float* lse, cons
     const bool few = rows <= 32;
     // more rows than a CTA takes: pairs of CTAs share their keys (16-bit rows)
     tp.cluster = !fp8 && rows > 64 ? 2 : 1;
-    // TMA: eight keys of a page a box, with all their dims where these are whole chunks
-    if (page_size % 8 == 0) {
-      const int eb = fp8 ? 1 : 2;
-      if (row_dim % 64 == 0 && cache_map(&tp.map, cache, eb, a.bf16, 64, page_size, tp.chunks, num_pages, s->cache_slot, 64 * eb, s->cache_page, 64, 8,
-                                         tp.chunks, !fp8))
-        tp.tma = 2;
-      else if (!fp8 && cache_map(&tp.map, cache, 2, a.bf16, row_dim, page_size, 1, num_pages, s->cache_slot, 0, s->cache_page, 64, 8, 1, true))
-        tp.tma = 1;
+    // TMA: runs of 8, 16 or 32 keys of a page a box (a pair's CTA brings 16), with all their dims where these are whole chunks
+    int groups = tp.cluster > 1 ? 2 : 4;
+    while (groups > 0 && page_size % (8 * groups) != 0) groups /= 2;
+    const bool whole = row_dim % 64 == 0;
+    if (groups > 0 && (whole || !fp8) &&
+        latent_map(&tp.map, cache, fp8 ? 1 : 2, a.bf16, row_dim, page_size, num_pages, s->cache_slot, s->cache_page, tp.chunks,
+                   whole ? tp.chunks : 1, whole ? groups : 1, !fp8)) {
+      tp.box = whole ? groups : 1;
+      tp.box_chunks = whole ? tp.chunks : 1;
     }
     if (fp8) return latent_tile_e4m3(tp, few, work, work_bytes, a.max_len, stream);
     return latent_tile_src(tp, few, work, work_bytes, a.max_len, stream);

@@ -37,8 +37,7 @@
 // maximum of score + log2 f, so that p f, not p, begins at 2^7.
 //
 // Few long sequences are split over the CTAs by keys, in steps of a tile, counted
-// on the device: one share for each CTA (or pair) and, without pairs, smaller ones for those that are done
-// first; parts are joined in the order of the keys by a second kernel.
+// on the device, a share for each CTA (or pair); parts are joined in the order of the keys by a second kernel.
 //
 // Every wait has a limit (kSpin); a CTA whose wait ran out records that in the
 // error record and in the workspace's head, lets its copies and products end and leaves.
@@ -58,7 +57,8 @@ constexpr int kLatScores = 2;       // tiles whose scores may be in TMEM
 struct LatentTileParams {
   LatentParams l;
   CUtensorMap map;
-  int32_t tma;       // 0: cp.async alone; 1: a box is 8 keys of a chunk; 2: of all chunks
+  int32_t box;       // groups of eight keys in a TMA box: 1, 2 or 4; 0: cp.async alone
+  int32_t box_chunks;  // chunks of one: 1 or all
   int32_t cluster;   // CTAs that share their keys: 1 or 2
   int32_t page_stride, slot_stride;  // of the cache, bytes in 32 bits
   int32_t chunks;    // 64-dim chunks of a row, the last perhaps cut
@@ -66,11 +66,11 @@ struct LatentTileParams {
   int32_t blocks;    // 128-dim blocks of the values
   int32_t units, raws;  // of the ring, and of that of e4m3fn rows
   int32_t split;     // 0: an item is one CTA's (or pair's)
-  int32_t min_steps, max_shares;
+  int32_t min_steps;
   int32_t part_rows;
   SplitWork* head;
   int64_t* meta;     // [num_seqs]: first step of each sequence
-  float *part_o, *part_ml;  // [2 * max_shares][cluster][part_rows] x 128 * blocks and x 2
+  float *part_o, *part_ml;  // [2 * shares][cluster][part_rows] x 128 * blocks and x 2
 };
 
 constexpr int kLatConverters = 8;  // warps
@@ -125,25 +125,13 @@ __device__ __forceinline__ int64_t latent_units(const LatentTileParams& p, int32
   return static_cast<int64_t>(g.blocks) * (p.split ? g.steps : 1);
 }
 
-// One share of 88 % of an equal part for each CTA, and the rest in shares of a quarter of what is left for each.
-constexpr int kLatFirst = 88;
-
-__device__ __forceinline__ int32_t latent_cut(int64_t total, int32_t ctas, bool pairs, int32_t max_shares, int32_t min_steps,
-                                              ShareLevel (&level)[2], int32_t* shares) {
+// A share for each CTA (or pair), all of a size. (Smaller shares behind them, for those that are done first, cost more in
+// queries brought in and parts written than they balance.)
+__device__ __forceinline__ ShareLevel latent_cut(int64_t total, int32_t ctas, int32_t min_steps, int32_t* shares) {
   int64_t each = (total + ctas - 1) / ctas;
   if (each < min_steps) each = min_steps;
-  const int64_t size = each * kLatFirst / 100, left = total - size * ctas;
-  int64_t small = (left + 2 * ctas - 1) / (2 * ctas);
-  if (small < min_steps) small = min_steps;
-  if (pairs || left <= 0 || each < 6 * min_steps || max_shares < ctas + (left + small - 1) / small) {
-    level[0] = ShareLevel{0, static_cast<int32_t>(each), 0};
-    *shares = static_cast<int32_t>((total + each - 1) / each);
-    return 1;
-  }
-  level[0] = ShareLevel{0, static_cast<int32_t>(size), 0};
-  level[1] = ShareLevel{size * ctas, static_cast<int32_t>(small), ctas};
-  *shares = ctas + static_cast<int32_t>((left + small - 1) / small);
-  return 2;
+  *shares = static_cast<int32_t>((total + each - 1) / each);
+  return ShareLevel{0, static_cast<int32_t>(each), 0};
 }
 
 // 16 lanes x 64 columns over the warp: thread (g, t) = (lane / 4, lane % 4) gets columns 8 i + 2 t, + 1 of
@@ -185,10 +173,18 @@ __device__ __forceinline__ void tc_mma_two(uint32_t d, uint64_t a, uint64_t b, u
 #undef KV_NEXT
 #undef KV_OPERANDS
 
-// tma_box into the same place of both CTAs of a pair, and their barriers.
-__device__ __forceinline__ void tma_box_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t dim, int32_t key, int32_t head, int32_t page) {
-  asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%3, %4, %5, %6}], [%2], %7;"
-               ::"r"(dst), "l"(map), "r"(bar), "r"(dim), "r"(key), "r"(head), "r"(page), "h"(static_cast<uint16_t>(3)) : "memory");
+// A box of a cache of latent rows (latent_map), by one lane of a converged warp; into the same place of both CTAs of a
+// pair, and their barriers.
+__device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t dim, int32_t group, int32_t page, bool pair) {
+  if (pair) {
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xFFFFFFFF;\n\t"
+                 "@e cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%3, %6, %6, %4, %5}], [%2], %7;\n\t}"
+                 ::"r"(dst), "l"(map), "r"(bar), "r"(dim), "r"(group), "r"(page), "r"(0), "h"(static_cast<uint16_t>(3)) : "memory");
+  } else {
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xFFFFFFFF;\n\t"
+                 "@e cp.async.bulk.tensor.5d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %6, %6, %4, %5}], [%2];\n\t}"
+                 ::"r"(dst), "l"(map), "r"(bar), "r"(dim), "r"(group), "r"(page), "r"(0) : "memory");
+  }
 }
 // tc_commit to the same barrier of both CTAs of a pair.
 __device__ __forceinline__ void tc_commit_pair(uint32_t bar) {
@@ -318,10 +314,10 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
     const uint32_t lanes = warp << 21;
     const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;  // the maximum is taken before the scale
     constexpr float kSmall = kBF16 ? 0.0f : 7.0f;
-    // Queries into shared memory: a warp has NR / 4 rows, four at a time. (All products that read the
+    // Queries into shared memory: a warp has NR / 4 rows, some at a time. (All products that read the
     // last ones have ended, as their scores were waited for.)
     auto load_q = [&](const LatentSeg& s) {
-      constexpr int kRows = NR / 4, kAt = 4, kPer = (kLatMaxChunks * 8 + 31) / 32;
+      constexpr int kRows = NR / 4, kAt = FMT == KV_CACHE_SRC ? 8 : 4, kPer = (kLatMaxChunks * 8 + 31) / 32;
       const uint32_t pieces = static_cast<uint32_t>(a.head_dim) / 8u;
       for (int i0 = 0; i0 < kRows; i0 += kAt) {
         uint4 w[kAt][kPer];
@@ -736,15 +732,14 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
       if (p.split && blockIdx.x == 0 && b < a.num_seqs) p.meta[b] = total + incl - u;
       total += __shfl_sync(0xFFFFFFFFu, incl, 31);
     }
-    ShareLevel level[2] = {};
-    int32_t shares = 0, levels = 1;
+    ShareLevel level = {};
+    int32_t shares = 0;
     const int32_t ctas = static_cast<int32_t>(gridDim.x) / p.cluster, cta = static_cast<int32_t>(blockIdx.x) / p.cluster;
     if (p.split) {
-      levels = latent_cut(total, ctas, pair, p.max_shares, p.min_steps, level, &shares);
+      level = latent_cut(total, ctas, p.min_steps, &shares);
       if (blockIdx.x == 0 && lane == 0u) {
-        p.head->level[0] = level[0];
-        p.head->level[1] = level[1];
-        p.head->levels = levels;
+        p.head->level[0] = level;
+        p.head->levels = 1;
       }
     }
     // the cursor: sequences cur_b .. cur_b + 31, whose first unit is cur_at; a lane has its sequence's units
@@ -767,9 +762,8 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
       int64_t pos, end;
       if (p.split) {
         if (share >= shares) break;
-        const int32_t lv = levels > 1 && share >= level[1].first ? 1 : 0;
-        pos = level[lv].start + static_cast<int64_t>(share - level[lv].first) * level[lv].size;
-        end = min(lv + 1 < levels ? level[1].start : total, pos + level[lv].size);
+        pos = static_cast<int64_t>(share) * level.size;
+        end = min(total, pos + level.size);
       } else {  // items in turn, every second round the other way
         pos = static_cast<int64_t>(round) * ctas + ((round & 1) ? ctas - 1 - cta : cta);
         end = pos + 1;
@@ -820,11 +814,7 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
         s.part = s_out - s_in == unit ? -1 : (2 * share + (s_in == 0 ? 1 : 0)) * p.cluster + static_cast<int32_t>(rank);
         publish(s);
       }
-      if (p.split) {
-        int32_t after = shares;  // a pair has one share
-        if (lane == 0u && !pair) after = static_cast<int32_t>(gridDim.x + atomicAdd(&p.head->next, 1u));
-        share = __shfl_sync(0xFFFFFFFFu, after, 0);
-      }
+      share += ctas;
     }
     LatentSeg s = {};
     s.stop = 1;
@@ -833,6 +823,7 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
     // ======================================================================================
     // the keys, a unit of 32 at a time
     // ======================================================================================
+    auto same = [](uint32_t x) { return __reduce_or_sync(0xFFFFFFFFu, x); };  // in a uniform register
     uint32_t k = 0u, n = 0u;  // units that went by
     Place at{0u, 0u};         // in the ring of units, or of raw ones
     const uint32_t places = FMT == KV_CACHE_SRC ? units : raws;
@@ -884,19 +875,17 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
                         reinterpret_cast<const uint8_t*>(live ? lp.scales + (static_cast<int64_t>(id) * a.page.d + off) * lp.scale_slot : lp.scales),
                         live ? 4u : 0u);
         }
-        if (p.tma && bits == ~0u) {
+        if (p.box > 0 && bits == ~0u) {
           hand_over(true);
-          // lane g: the eight keys from 8 g on (which share a page); of a pair's CTAs each brings two of the four
-          const int32_t page = __shfl_sync(0xFFFFFFFFu, id, 8 * (lane & 3u)), in_page = static_cast<int32_t>(__shfl_sync(0xFFFFFFFFu, off, 8 * (lane & 3u)));
+          // boxes of `box` groups of eight keys, which share a page; of a pair's CTAs each brings half of the unit
           if (lane == 0u) bar_arrive_expect(bar, 4u * part);
           __syncwarp();
-          if (lane < 4u && (!pair || (lane >> 1) == rank)) {
-            const uint32_t to = dst + lane * part, span = part / static_cast<uint32_t>(p.chunks);
-            const int32_t boxes = p.tma == 2 ? 1 : p.chunks;
-            for (int32_t c = 0; c < boxes; ++c) {
-              if (pair) tma_box_pair(to + c * span, &p.map, bar, 64 * c, in_page, 0, page);
-              else tma_box(to + c * span, &p.map, bar, 64 * c, in_page, 0, page);
-            }
+          const int32_t g0 = pair ? 2 * static_cast<int32_t>(rank) : 0, g1 = pair ? g0 + 2 : 4;
+          for (int32_t g = g0; g < g1; g += p.box) {
+            const int32_t page = static_cast<int32_t>(same(static_cast<uint32_t>(__shfl_sync(0xFFFFFFFFu, id, 8 * g))));
+            const int32_t in_page = static_cast<int32_t>(same(__shfl_sync(0xFFFFFFFFu, off, 8 * g)) >> 3);
+            for (int32_t c = 0; c < p.chunks; c += p.box_chunks)
+              tma_rows(dst + g * part + c * (part / static_cast<uint32_t>(p.chunks)), &p.map, bar, 64 * c, in_page, page, pair);
           }
           if constexpr (FMT != KV_CACHE_SRC) bar_arrive_copies(bar);  // the scales
         } else {
@@ -1021,7 +1010,6 @@ __global__ void __launch_bounds__(32 * kLatJoinWarps) kv_attend_latent_join(cons
   const int32_t block = static_cast<int32_t>(unit - row_of * p.blocks);
   const int32_t tok = static_cast<int32_t>(row_of / a.q_heads), h = static_cast<int32_t>(row_of - static_cast<int64_t>(tok) * a.q_heads);
   grid_handover();
-  if (blockIdx.x == 0 && threadIdx.x == 0) p.head->next = 0u;
   int32_t b = tok, c0 = 0, c1 = 0, r = 0, rank = 0, pos = 0;
   bool joined = false, lost = false;
   if (tok < a.num_q) {
@@ -1113,7 +1101,7 @@ __global__ void __launch_bounds__(32 * kLatJoinWarps) kv_attend_latent_join(cons
 // Host
 // ---------------------------------------------------------------------------
 
-constexpr int kLatMinSteps = 4;  // tiles of a share at least
+constexpr int kLatMinSteps = 1;  // tiles of a share at least
 
 // Pairs of CTAs of a kernel that can be resident at once, per device.
 inline kv_status pairs_resident(const void* kernel, int threads, int smem, std::atomic<int>* known, int* out) {
@@ -1179,13 +1167,12 @@ kv_status launch_latent_tile(LatentTileParams p, void* work, int64_t work_bytes,
   p.part_rows = a.q_start || static_cast<int32_t>(a.group.d) > NR ? NR : static_cast<int32_t>(a.group.d);
   const int64_t slot = static_cast<int64_t>(p.cluster) * p.part_rows * (128 * p.blocks + 2) * 4;
   int64_t fit = work && work_bytes > kSplitHead + meta ? (work_bytes - kSplitHead - meta) / (2 * slot) : 0;
-  if (fit > 8 * ctas) fit = 8 * ctas;
+  if (fit > ctas) fit = ctas;
   p.min_steps = kLatMinSteps;
-  p.split = items < 4 * ctas && max_keys > kLatMinSteps * kLatKeys && 2 * fit >= ctas;
+  p.split = items < 4 * ctas && max_keys > 4 * kLatKeys && 2 * fit >= ctas;
   int64_t grid = items < ctas ? items : ctas;
   if (p.split) {
     grid = fit < ctas ? fit : ctas;
-    p.max_shares = static_cast<int32_t>(fit);
     p.head = static_cast<SplitWork*>(work);
     p.meta = reinterpret_cast<int64_t*>(static_cast<uint8_t*>(work) + kSplitHead);
     p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(work) + kSplitHead + meta);
