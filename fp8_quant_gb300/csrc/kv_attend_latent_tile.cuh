@@ -6,8 +6,8 @@
 // bytes, from about four queries on by the products.
 //
 // A CTA takes up to NR = 64 or 32 query rows, a row being a (query, head)
-// pair, and goes over tiles of 64 keys:
-//   S [rows][keys] = Q K^T       M = 64 (Q, shared memory), N = 64 keys, all D dims;
+// pair, and goes over tiles of 32 keys:
+//   S [rows][keys] = Q K^T       M = 64 (Q, shared memory), N = 32 keys, or 64 of two tiles, all D dims;
 //   O^T [dims][rows] += V^T P^T  M = 128 dims, N = NR rows: the tile's first L
 //                                dims as they lie (dims contiguous), P in
 //                                shared memory.
@@ -15,18 +15,20 @@
 // rows as M it would be all of it), a key tile is brought in once for both
 // products, and the rows that do not fill M = 128 cost nothing.
 //
-//   warps 0-3  the softmax: S by 16x256b loads (a thread has 16 keys of two rows),
+//   warps 0-3  the softmax: S by 16x256b loads (a thread has 8 keys of two rows),
 //              running maximum and sums in registers, P to shared memory. O^T is
 //              rescaled only when a row's maximum grew by 2^8 or more. They also
 //              bring the queries in and write the outputs.
-//   warp  4    issues the products S, up to two tiles ahead of
+//   warp  4    issues the products S, up to four tiles ahead of
 //   warp  5    P V. (A product takes 31 clocks to issue and 32 to 48 to run: one warp for both was the bound.)
 //   warp  6    cuts the work: finds the CTA's next items and hands them to the others.
-//   warp  7    brings the keys in units of 32: by TMA, a box for eight keys and all their dims, where all 32 exist, else by
-//              cp.async. e4m3fn rows come as they are, into a ring of their own, and become fp16 (exact) by
+//   warp  7    brings the keys, a tile a unit of the ring: by TMA, a box for all of it where its 32 keys exist and share a
+//              page, else by cp.async. e4m3fn rows come as they are, into a ring of their own, and become fp16 (exact) by
 //   warps 8-15 on their way into the ring of units.
-//   A unit is given back as soon as P V has gone over it. It lies as [8 keys][64 dims][key][128 bytes in the 128-byte
-//   swizzle], so that a tile is any two units that follow each other in the ring (two products of 32 keys where it wraps).
+//   A unit lies as [8 keys][64 dims][key][128 bytes in the 128-byte swizzle], so that two that follow each other in the ring
+//   are 64 keys of one product. It is given back when P V has gone over it. Tiles are small because that time is what the
+//   ring has to cover beside the memory's latency: tiles of 64 keys held it twice as long (decode, 64 sequences of 4,000 -
+//   16,384 keys: 171 us).
 //
 // Rows beyond NR (more queries, more heads) read the same keys: two CTAs then are a cluster, each brings half of
 // every unit and TMA writes it into both.
@@ -48,11 +50,10 @@
 
 namespace kvimpl {
 
-constexpr int kLatKeys = 64;        // keys of a tile
-constexpr int kLatUnit = 32;        // and of a unit of the ring
+constexpr int kLatKeys = 32;        // keys of a tile, which is a unit of the ring
 constexpr int kLatMaxChunks = 9;    // 64-dim chunks of a row: up to 576 dims
 constexpr int kLatMaxUnits = 8, kLatMaxRaws = 8;
-constexpr int kLatScores = 2;       // tiles whose scores may be in TMEM
+constexpr int kLatScores = 4;       // tiles whose scores may be in TMEM
 
 struct LatentTileParams {
   LatentParams l;
@@ -90,15 +91,15 @@ struct LatentSeg {
 template <int FMT, int NR>
 struct LatentSmem {  // units, raw units, queries, weights, and
   static constexpr int kP = NR * 128;
-  static constexpr int kBars = 2 * kLatMaxUnits + 2 * kLatMaxRaws + 2 * kLatScores + 9;
-  static __host__ __device__ constexpr int unit(int chunks) { return kLatUnit * 128 * chunks; }
-  static __host__ __device__ constexpr int raw(int chunks) { return kLatUnit * 64 * chunks; }
+  static constexpr int kBars = 2 * kLatMaxUnits + 2 * kLatMaxRaws + 2 * kLatScores + 11;
+  static __host__ __device__ constexpr int unit(int chunks) { return kLatKeys * 128 * chunks; }
+  static __host__ __device__ constexpr int raw(int chunks) { return kLatKeys * 64 * chunks; }
   static __host__ __device__ constexpr int q_bytes(int chunks) { return chunks * NR * 128; }
   static constexpr int kOffBars = 0, kOffSegs = (kBars * 8 + 15) / 16 * 16, kOffAlpha = kOffSegs + 2 * 64, kOffInv = kOffAlpha + 2 * NR * 4,
                        kOffQf = kOffInv + NR * 4, kOffMisc = kOffQf + NR * 4, kOffValid = kOffMisc + 64,
                        kOffRawValid = kOffValid + kLatMaxUnits * 4, kOffScale = kOffRawValid + kLatMaxRaws * 4;
   static __host__ __device__ constexpr int total(int chunks, int units, int raws) {
-    return units * (unit(chunks) + (FMT == KV_CACHE_SRC ? 0 : kLatUnit * 4)) + raws * (raw(chunks) + kLatUnit * 4) + q_bytes(chunks) + kP + kOffScale;
+    return units * (unit(chunks) + (FMT == KV_CACHE_SRC ? 0 : kLatKeys * 4)) + raws * (raw(chunks) + kLatKeys * 4) + q_bytes(chunks) + kP + kOffScale;
   }
 };
 static_assert(sizeof(LatentSeg) <= 64, "segments");
@@ -134,18 +135,17 @@ __device__ __forceinline__ ShareLevel latent_cut(int64_t total, int32_t ctas, in
   return ShareLevel{0, static_cast<int32_t>(each), 0};
 }
 
-// 16 lanes x 64 columns over the warp: thread (g, t) = (lane / 4, lane % 4) gets columns 8 i + 2 t, + 1 of
+// 16 lanes x 32 columns over the warp: thread (g, t) = (lane / 4, lane % 4) gets columns 8 i + 2 t, + 1 of
 // rows g (r[4 i], r[4 i + 1]) and g + 8 (r[4 i + 2], r[4 i + 3]).
-__device__ __forceinline__ void tc_ld_rows(float (&s)[32], uint32_t addr) {
-  uint32_t r[32];
-#define KV_R4(i) "=r"(r[i]), "=r"(r[(i) + 1]), "=r"(r[(i) + 2]), "=r"(r[(i) + 3])
-  asm volatile("tcgen05.ld.sync.aligned.16x256b.x8.b32 "
-               "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+__device__ __forceinline__ void tc_ld_rows(float (&s)[16], uint32_t addr) {
+  uint32_t r[16];
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+               "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
                "tcgen05.wait::ld.sync.aligned;"
-               : KV_R4(0), KV_R4(4), KV_R4(8), KV_R4(12), KV_R4(16), KV_R4(20), KV_R4(24), KV_R4(28) : "r"(addr) : "memory");
-#undef KV_R4
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+                 "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]) : "r"(addr) : "memory");
 #pragma unroll
-  for (int i = 0; i < 32; ++i) s[i] = __uint_as_float(r[i]);
+  for (int i = 0; i < 16; ++i) s[i] = __uint_as_float(r[i]);
 }
 
 // smem_desc with groups of eight rows (or keys) `group` bytes apart.
@@ -196,6 +196,16 @@ __device__ __forceinline__ void sync_pair() {
   asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
 
+// bar_try without a pause.
+__device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\t"
+               "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+               "selp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  return ok != 0u;
+}
+
 __device__ __forceinline__ float lg2_fast(float x) {
   float r;
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -229,7 +239,7 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
   uint8_t* const small_ptr = smem_raw + (small - ring);
   const uint32_t full = small + S::kOffBars, empty = full + 8 * kLatMaxUnits, raw_full = empty + 8 * kLatMaxUnits,
                  raw_empty = raw_full + 8 * kLatMaxRaws, q_full = raw_empty + 8 * kLatMaxRaws, s_full = q_full + 8,
-                 s_free = s_full + 8 * kLatScores, p_full = s_free + 8 * kLatScores, pv_done = p_full + 8, seg_full = pv_done + 8,
+                 s_free = s_full + 8 * kLatScores, p_full = s_free + 8 * kLatScores, pv_done = p_full + 16, seg_full = pv_done + 16,
                  seg_empty = seg_full + 16, done = seg_empty + 16;
   LatentSeg* const segs = reinterpret_cast<LatentSeg*>(small_ptr + S::kOffSegs);
   float* const sh_alpha = reinterpret_cast<float*>(small_ptr + S::kOffAlpha);   // [2][NR]
@@ -259,14 +269,14 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
       bar_init(raw_full + 8 * i, 33);
       bar_init(raw_empty + 8 * i, kLatConverters);
     }
-    bar_init(q_full, 128);
+    bar_init(q_full, 4);
     for (int i = 0; i < kLatScores; ++i) {
       bar_init(s_full + 8 * i, 1);
       bar_init(s_free + 8 * i, NR / 16);
     }
-    bar_init(p_full, 128);
-    bar_init(pv_done, 1);
     for (int i = 0; i < 2; ++i) {
+      bar_init(p_full + 8 * i, 4);
+      bar_init(pv_done + 8 * i, 1);
       bar_init(seg_full + 8 * i, 1);
       bar_init(seg_empty + 8 * i, 7 + (FMT == KV_CACHE_SRC ? 0 : kLatConverters));
       bar_init(done + 8 * i, 1);
@@ -367,7 +377,8 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
         }
       }
       fence_async_shared();
-      bar_arrive(q_full);
+      __syncwarp();
+      if (lane == 0u) bar_arrive(q_full);
       sync_softmax();  // sh_qf
     };
     uint32_t k = 0u, T = 0u;  // segments and tiles that went by
@@ -388,71 +399,71 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
         if (rs[c] == 0.0f) rs[c] = __uint_as_float(1u);  // hidden scores (-inf) must stay -inf
       }
       for (int32_t j = seg.t0; j < seg.t1; ++j, ++T) {
-        // the units are long there; their keys' bits and scales are read while S is waited for
-        uint64_t valid;
-        uint32_t unit[2];
-        {
-          ok = ok && __all_sync(0xFFFFFFFFu, bar_wait(full + 8 * at.unit, at.phase, state));
-          unit[0] = at.unit;
-          next_unit(&at);
-          ok = ok && __all_sync(0xFFFFFFFFu, bar_wait(full + 8 * at.unit, at.phase, state));
-          unit[1] = at.unit;
-          next_unit(&at);
-          valid = sh_valid[unit[0]] | static_cast<uint64_t>(sh_valid[unit[1]]) << 32;
-        }
-        float s[32], kf[16], alpha[2] = {1.0f, 1.0f};  // scores, their keys' scales, factors of the rows' sums
+        // the unit is long there; its keys' bits and scales are read while S is waited for. (Threads that gave up a wait go
+        // on to the barrier below, where all leave together.)
+        ok = bar_wait(full + 8 * at.unit, at.phase, state) && ok;
+        const uint32_t valid = sh_valid[at.unit];
+        float s[16], kf[8], alpha[2] = {1.0f, 1.0f};  // scores, their keys' scales, factors of the rows' sums
         if constexpr (FMT != KV_CACHE_SRC) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float2 f = *reinterpret_cast<const float2*>(sh_scale + unit[i / 4] * kLatUnit + 8 * (i & 3) + 2 * t);
+          for (int i = 0; i < 4; ++i) {
+            const float2 f = *reinterpret_cast<const float2*>(sh_scale + at.unit * kLatKeys + 8 * i + 2 * t);
             kf[2 * i] = f.x;
             kf[2 * i + 1] = f.y;
           }
         }
-        ok = ok && __all_sync(0xFFFFFFFFu, bar_wait(s_full + 8 * (T & 1u), (T >> 1) & 1u, state));
+        next_unit(&at);
+        ok = bar_wait(s_full + 8 * (T % kLatScores), (T / kLatScores) & 1u, state) && ok;
+        __syncwarp();
         tc_fence_after();
         bool grew = false;
-        if (has_rows && ok) {
-          tc_ld_rows(s, tm_s + kLatKeys * (T & 1u) + lanes);
+        if (has_rows) {
+          tc_ld_rows(s, tm_s + kLatKeys * (T % kLatScores) + lanes);
           tc_fence_before();
-          if (lane == 0u) bar_arrive(s_free + 8 * (T & 1u));
+          __syncwarp();
+          if (lane == 0u) bar_arrive(s_free + 8 * (T % kLatScores));
           if constexpr (FMT != KV_CACHE_SRC) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) s[i] *= kf[2 * (i / 4) + (i & 1)] * rs[(i >> 1) & 1];
+            for (int i = 0; i < 16; ++i) s[i] *= kf[2 * (i / 4) + (i & 1)] * rs[(i >> 1) & 1];
           }
-          if (j * kLatKeys + kLatKeys - 1 > p_lo || valid != ~0ull) {
+          if (j * kLatKeys + kLatKeys - 1 > p_lo || valid != ~0u) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               const int32_t n = pos[c] - j * kLatKeys + 1;  // the first n keys
-              const uint64_t see = (n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1ull) & valid;
-              const uint32_t lo = static_cast<uint32_t>(see) >> (2 * t), hi = static_cast<uint32_t>(see >> 32) >> (2 * t);
+              const uint32_t see = ((n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u) & valid) >> (2 * t);
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
+              for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int x = 0; x < 2; ++x)
-                  if ((((i < 4 ? lo : hi) >> (8 * (i & 3) + x)) & 1u) == 0u) s[4 * i + 2 * c + x] = -INFINITY;
+                  if ((see >> (8 * i + x) & 1u) == 0u) s[4 * i + 2 * c + x] = -INFINITY;
             }
           }
-          float lv[16];
+          float lv[8];
           if constexpr (FMT != KV_CACHE_SRC) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) lv[i] = fmaxf(lg2_fast(fabsf(kf[i])), -100.0f);
+            for (int i = 0; i < 8; ++i) lv[i] = fmaxf(lg2_fast(fabsf(kf[i])), -100.0f);
           }
+          float top[2];
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             float x[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
               for (int y = 0; y < 2; ++y) x[y] = fmaxf(x[y], FMT == KV_CACHE_SRC ? s[4 * i + 2 * c + y] : s[4 * i + 2 * c + y] + lv[2 * i + y]);
-            float top = fmaxf(x[0], x[1]);
-            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-            top = FMT == KV_CACHE_SRC ? __fmaf_rn(top, rs[c], -kSmall) : top - kSmall;
+            top[c] = fmaxf(x[0], x[1]);
+          }
+#pragma unroll
+          for (int o = 1; o < 4; o <<= 1)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) top[c] = fmaxf(top[c], __shfl_xor_sync(0xFFFFFFFFu, top[c], o));
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            top[c] = FMT == KV_CACHE_SRC ? __fmaf_rn(top[c], rs[c], -kSmall) : top[c] - kSmall;
             // a maximum that grew little is kept (the weights stay below 2^(kSmall + 8))
-            if (top > m[c] + 8.0f || (m[c] == -INFINITY && top > m[c])) {
-              alpha[c] = exp2_fast(m[c] - top);
-              m[c] = top;
+            if (top[c] > m[c] + 8.0f || (m[c] == -INFINITY && top[c] > m[c])) {
+              alpha[c] = exp2_fast(m[c] - top[c]);
+              m[c] = top[c];
               grew = true;
             }
           }
@@ -467,14 +478,14 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
           ok = false;
           break;
         }
-        uint32_t pw[16];
+        uint32_t pw[8];
         if (has_rows) {
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             const float ref = m[c] == -INFINITY ? 0.0f : m[c];
             float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < 4; ++i) {
               float2 z = make_float2(s[4 * i + 2 * c], s[4 * i + 2 * c + 1]);
               if constexpr (FMT == KV_CACHE_SRC) z = fma2(z, rs[c], -ref); else z = add2(z, make_float2(-ref, -ref));
               float2 e = make_float2(exp2_fast(z.x), exp2_fast(z.y));
@@ -489,9 +500,11 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
             l[c] = __fmaf_rn(l[c], alpha[c], sum[0].x + sum[0].y);
           }
         }
-        if (T > 0u)  // P V of the last tile has read P and written O^T
-          ok = __all_sync(0xFFFFFFFFu, bar_wait(pv_done, (T - 1u) & 1u, state));
-        if (rescale && ok) {
+        // tiles take turns in the halves of P's rows: P V of the last but one has read its
+        if (T > 1u) ok = bar_wait(pv_done + 8 * (T & 1u), ((T >> 1) - 1u) & 1u, state) && ok;
+        if (rescale) {  // and that of the last one has written O^T
+          ok = bar_wait(pv_done + 8 * ((T - 1u) & 1u), ((T - 1u) >> 1) & 1u, state) && ok;
+          __syncwarp();
           tc_fence_after();
           const float* f = sh_alpha + (T & 1u) * NR;
           for (int32_t b = 0; b < p.blocks; ++b)
@@ -505,18 +518,19 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
             }
           tc_wait_st();
         }
-        if (has_rows && ok) {
+        if (has_rows) {
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             const uint32_t r = static_cast<uint32_t>(r0 + 8 * c);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              asm volatile("st.shared.u32 [%0], %1;" ::"r"(p_at + r * 128u + ((i ^ (r & 7u)) << 4) + 4u * t), "r"(pw[2 * i + c]) : "memory");
+            for (int i = 0; i < 4; ++i)
+              asm volatile("st.shared.u32 [%0], %1;" ::"r"(p_at + r * 128u + (((i + 4u * (T & 1u)) ^ (r & 7u)) << 4) + 4u * t), "r"(pw[2 * i + c]) : "memory");
           }
         }
         fence_async_shared();
         tc_fence_before();
-        bar_arrive(p_full);
+        __syncwarp();
+        if (lane == 0u) bar_arrive(p_full + 8 * (T & 1u));
       }
       if (any_of_softmax(!ok)) break;
       have = take(k++, &next);
@@ -531,7 +545,8 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
         if (has_rows && t == 0u) sh_inv[r0 + 8 * c] = l[c] < INFINITY ? __fdiv_rn(1.0f, l[c]) : NAN;
       }
       if (live) {
-        ok = __all_sync(0xFFFFFFFFu, bar_wait(pv_done, (T - 1u) & 1u, state));
+        ok = bar_wait(pv_done + 8 * ((T - 1u) & 1u), ((T - 1u) >> 1) & 1u, state) && ok;
+        __syncwarp();
         tc_fence_after();
       }
       if (any_of_softmax(!ok)) break;
@@ -635,7 +650,7 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
       const uint32_t s_at = same(tm_s);
       const uint64_t q_desc = smem_desc(same(q_at), 16);
       uint32_t items = 0u;
-      // Q against the keys at `from`, N = 64 or 32 of them
+      // Q against the keys at `from`, 64 or 32 of them
       auto scores = [&](uint32_t d, uint32_t from, uint32_t desc) {
         const uint64_t kd = smem_desc_groups(from, 16, group_bytes);
         auto chunk = [&](int32_t c) { tc_mma_chunk(d, q_desc + c * (NR * 128 >> 4), kd + c * (1024 >> 4), desc, c > 0); };
@@ -656,21 +671,32 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
       while (take(k++, &seg)) {
         if (seg.t1 <= seg.t0) continue;
         wait(q_full, items++ & 1u);
-        for (int32_t j = seg.t0; j < seg.t1; ++j, ++T) {
-          if (T >= kLatScores) wait(s_free + 8 * (T & 1u), (T / kLatScores - 1u) & 1u);
-          const uint32_t u = same(at.unit | (T & 1u) << 8), u0 = u & 255u, buf = u >> 8, d = s_at + kLatKeys * buf;
+        for (int32_t j = seg.t0; j < seg.t1;) {
+          if (T >= kLatScores) wait(s_free + 8 * (T % kLatScores), (T / kLatScores - 1u) & 1u);
           wait(full + 8 * at.unit, at.phase);
-          next_unit(&at);
-          wait(full + 8 * at.unit, at.phase);
-          next_unit(&at);
+          // a second tile with the first, where it is there: 64 keys cost 32 clocks a product, 32 keys 25
+          const uint32_t T1 = T + 1u;
+          const bool two = j + 1 < seg.t1 && at.unit + 1u < units && T1 % kLatScores != 0u &&
+                           __all_sync(0xFFFFFFFFu, bar_test(full + 8 * (at.unit + 1u), at.phase) &&
+                                                       (T1 < kLatScores || bar_test(s_free + 8 * (T1 % kLatScores), (T1 / kLatScores - 1u) & 1u)));
+          const uint32_t u = same(at.unit | (T % kLatScores) << 8 | (two ? 1u << 16 : 0u)), buf = (u >> 8) & 255u;
           if (!ok) break;
-          if (u0 + 1u < units) {
-            scores(d, ring0 + u0 * unit_bytes, kDesc | ((64u >> 3) << 17));
-          } else {  // the tile's second half is at the ring's begin
-#pragma unroll 1
-            for (uint32_t h = 0; h < 2u; ++h) scores(d + kLatUnit * h, h ? ring0 : ring0 + u0 * unit_bytes, kDesc | ((32u >> 3) << 17));
+          const uint32_t d = s_at + kLatKeys * buf, from = ring0 + (u & 255u) * unit_bytes;
+          if ((u >> 16) != 0u) {
+            tc_fence_after();
+            scores(d, from, kDesc | ((64u >> 3) << 17));
+            tc_commit(s_full + 8 * buf);
+            tc_commit(s_full + 8 * buf + 8);
+            next_unit(&at);
+            ++T;
+            ++j;
+          } else {
+            scores(d, from, kDesc | ((32u >> 3) << 17));
+            tc_commit(s_full + 8 * buf);
           }
-          tc_commit(s_full + 8 * buf);
+          next_unit(&at);
+          ++T;
+          ++j;
         }
         if (!ok) break;
       }
@@ -680,30 +706,21 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
       const uint64_t p_desc = smem_desc(same(p_at), 16);
       while (take(k++, &seg)) {
         for (int32_t j = seg.t0; j < seg.t1; ++j, ++T) {
-          Place two[2];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            two[h] = at;
-            wait(full + 8 * at.unit, at.phase);
-            next_unit(&at);
-          }
-          const uint32_t u = same(two[0].unit | two[1].unit << 8 | (j > seg.t0 ? 1u << 16 : 0u));
-          wait(p_full, T & 1u);
+          const uint32_t u = same(at.unit | (T & 1u) << 8 | (j > seg.t0 ? 1u << 16 : 0u)), un = u & 255u, odd = (u >> 8) & 1u;
+          wait(full + 8 * at.unit, at.phase);
+          wait(p_full + 8 * (T & 1u), (T >> 1) & 1u);
           if (!ok) break;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t un = (u >> (8 * h)) & 255u;
-            const uint64_t v = smem_desc_groups(ring0 + un * unit_bytes, 1024, group_bytes);
-            auto block = [&](int32_t b) { tc_mma_two(o_at + b * NR, v + b * (2048 >> 4), p_desc + 4 * h, kDesc, h > 0 || (u >> 16) != 0u, step, 2u); };
-            if (p.blocks == 4) {
-              block(0); block(1); block(2); block(3);
-            } else {
+          const uint64_t v = smem_desc_groups(ring0 + un * unit_bytes, 1024, group_bytes), pd = p_desc + 4 * odd;
+          auto block = [&](int32_t b) { tc_mma_two(o_at + b * NR, v + b * (2048 >> 4), pd, kDesc, (u >> 16) != 0u, step, 2u); };
+          if (p.blocks == 4) {
+            block(0); block(1); block(2); block(3);
+          } else {
 #pragma unroll 1
-              for (int32_t b = 0; b < p.blocks; ++b) block(b);
-            }
-            if (pair) tc_commit_pair(free0 + 8 * un); else tc_commit(free0 + 8 * un);
+            for (int32_t b = 0; b < p.blocks; ++b) block(b);
           }
-          tc_commit(pv_done);
+          if (pair) tc_commit_pair(free0 + 8 * un); else tc_commit(free0 + 8 * un);
+          tc_commit(pv_done + 8 * odd);
+          next_unit(&at);
         }
         if (!ok) break;
       }
@@ -846,14 +863,14 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
     };
     while (take(k++, &seg)) {
       const int32_t* table = a.table + static_cast<int64_t>(seg.b) * a.table_stride;
-      const int32_t n0 = 2 * seg.t0, n1 = 2 * seg.t1;
+      const int32_t n0 = seg.t0, n1 = seg.t1;
       // lane = key: its page (of the last key that a row sees, for keys behind it), a unit ahead of its use
       auto page_of = [&](int32_t unit) {
-        return __ldg(table + a.page.quot(static_cast<uint32_t>(min(unit * kLatUnit + static_cast<int32_t>(lane), seg.p_hi))));
+        return __ldg(table + a.page.quot(static_cast<uint32_t>(min(unit * kLatKeys + static_cast<int32_t>(lane), seg.p_hi))));
       };
       int32_t next_id = n0 < n1 ? page_of(n0) : 0;
       for (int32_t unit = n0; unit < n1 && ok; ++unit, ++n) {
-        const int32_t id = next_id, key = unit * kLatUnit + static_cast<int32_t>(lane);
+        const int32_t id = next_id, key = unit * kLatKeys + static_cast<int32_t>(lane);
         if (unit + 1 < n1) next_id = page_of(unit + 1);
         const bool want = key <= seg.p_hi, have = static_cast<uint32_t>(id) < static_cast<uint32_t>(a.num_pages);
         if (want && !have && rank == 0u) record_oob(a.err, static_cast<uint64_t>(seg.b));
@@ -871,7 +888,7 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
         if (lane == 0u) (FMT == KV_CACHE_SRC ? sh_valid : sh_raw_valid)[at.unit] = bits;
         if constexpr (FMT != KV_CACHE_SRC) {
           const bool live = want && have;
-          copy_async<4>(static_cast<uint32_t>(__cvta_generic_to_shared(sh_scale + (units + at.unit) * kLatUnit + lane)),
+          copy_async<4>(static_cast<uint32_t>(__cvta_generic_to_shared(sh_scale + (units + at.unit) * kLatKeys + lane)),
                         reinterpret_cast<const uint8_t*>(live ? lp.scales + (static_cast<int64_t>(id) * a.page.d + off) * lp.scale_slot : lp.scales),
                         live ? 4u : 0u);
         }
@@ -891,7 +908,7 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
         } else {
           const int64_t row = want && have ? wide(id, p.page_stride) + wide(off, p.slot_stride) : -1;
           // pieces in turn, so that lanes copy neighbouring ones
-          for (uint32_t i0 = 0; i0 < kLatUnit * pieces; i0 += 32u) {
+          for (uint32_t i0 = 0; i0 < kLatKeys * pieces; i0 += 32u) {
             const uint32_t i = i0 + lane, kk = i / pieces, piece = i - kk * pieces;
             const int64_t r = __shfl_sync(0xFFFFFFFFu, row, kk);
             const uint32_t base = dst + (kk >> 3) * part;
@@ -930,7 +947,7 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
     Place at{0u, 0u}, from{0u, 0u};
     LatentSeg seg;
     while (take(k++, &seg)) {
-      for (int32_t unit = 2 * seg.t0; unit < 2 * seg.t1; ++unit, ++n) {
+      for (int32_t unit = seg.t0; unit < seg.t1; ++unit, ++n) {
         ok = __all_sync(0xFFFFFFFFu, bar_wait(raw_full + 8 * from.unit, from.phase, state));
         if (!ok) break;
         uint4 v[kPer];
@@ -941,7 +958,7 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
         float scale = 0.0f;
         uint32_t bits = 0u;
         if (w == 0u) {
-          scale = sh_scale[(units + from.unit) * kLatUnit + lane];
+          scale = sh_scale[(units + from.unit) * kLatKeys + lane];
           bits = sh_raw_valid[from.unit];
         }
         __syncwarp();
@@ -969,7 +986,7 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
           }
         }
         if (w == 0u) {
-          sh_scale[at.unit * kLatUnit + lane] = scale;
+          sh_scale[at.unit * kLatKeys + lane] = scale;
           if (lane == 0u) sh_valid[at.unit] = bits;
         }
         fence_async_shared();
@@ -1101,7 +1118,7 @@ __global__ void __launch_bounds__(32 * kLatJoinWarps) kv_attend_latent_join(cons
 // Host
 // ---------------------------------------------------------------------------
 
-constexpr int kLatMinSteps = 1;  // tiles of a share at least
+constexpr int kLatMinSteps = 2;  // tiles of a share at least
 
 // Pairs of CTAs of a kernel that can be resident at once, per device.
 inline kv_status pairs_resident(const void* kernel, int threads, int smem, std::atomic<int>* known, int* out) {
@@ -1169,7 +1186,7 @@ kv_status launch_latent_tile(LatentTileParams p, void* work, int64_t work_bytes,
   int64_t fit = work && work_bytes > kSplitHead + meta ? (work_bytes - kSplitHead - meta) / (2 * slot) : 0;
   if (fit > ctas) fit = ctas;
   p.min_steps = kLatMinSteps;
-  p.split = items < 4 * ctas && max_keys > 4 * kLatKeys && 2 * fit >= ctas;
+  p.split = items < 4 * ctas && max_keys > 8 * kLatKeys && 2 * fit >= ctas;
   int64_t grid = items < ctas ? items : ctas;
   if (p.split) {
     grid = fit < ctas ? fit : ctas;
