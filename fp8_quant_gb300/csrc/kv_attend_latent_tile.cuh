@@ -7,7 +7,7 @@
 //
 // A CTA takes up to NR = 64 or 32 query rows, a row being a (query, head)
 // pair, and goes over tiles of 32 keys:
-//   S [rows][keys] = Q K^T       M = 64 (Q, shared memory), N = 32 keys, or 64 of two tiles, all D dims;
+//   S [rows][keys] = Q K^T       M = 64 (Q, shared memory), N = 32 keys, all D dims;
 //   O^T [dims][rows] += V^T P^T  M = 128 dims, N = NR rows: the tile's first L
 //                                dims as they lie (dims contiguous), P in
 //                                shared memory.
@@ -19,14 +19,14 @@
 //              running maximum and sums in registers, P to shared memory. O^T is
 //              rescaled only when a row's maximum grew by 2^8 or more. They also
 //              bring the queries in and write the outputs.
-//   warp  4    issues the products S, up to four tiles ahead of
-//   warp  5    P V. (A product takes 31 clocks to issue and 32 to 48 to run: one warp for both was the bound.)
+//   warps 4, 8 issue the products S, of every other tile each, up to four tiles ahead of
+//   warp  5    P V. (A product takes 31 clocks to issue and 25 to 48 to run: one warp for all, or for S, was the bound.)
 //   warp  6    cuts the work: finds the CTA's next items and hands them to the others.
 //   warp  7    brings the keys, a tile a unit of the ring: by TMA, a box for all of it where its 32 keys exist and share a
 //              page, else by cp.async. e4m3fn rows come as they are, into a ring of their own, and become fp16 (exact) by
-//   warps 8-15 on their way into the ring of units.
-//   A unit lies as [8 keys][64 dims][key][128 bytes in the 128-byte swizzle], so that two that follow each other in the ring
-//   are 64 keys of one product. It is given back when P V has gone over it. Tiles are small because that time is what the
+//   warps 9-15 on their way into the ring of units.
+//   A unit lies as [8 keys][64 dims][key][128 bytes in the 128-byte swizzle], as a box of the cache's eights of keys does.
+//   It is given back when P V has gone over it. Tiles are small because that time is what the
 //   ring has to cover beside the memory's latency: tiles of 64 keys held it twice as long (decode, 64 sequences of 4,000 -
 //   16,384 keys: 171 us).
 //
@@ -74,9 +74,9 @@ struct LatentTileParams {
   float *part_o, *part_ml;  // [2 * shares][cluster][part_rows] x 128 * blocks and x 2
 };
 
-constexpr int kLatConverters = 8;  // warps
+constexpr int kLatConverters = 7;  // warps
 template <int FMT>
-constexpr int kLatThreads = FMT == KV_CACHE_SRC ? 256 : 256 + 32 * kLatConverters;
+constexpr int kLatThreads = 288 + (FMT == KV_CACHE_SRC ? 0 : 32 * kLatConverters);
 
 // A CTA's next piece of work.
 struct LatentSeg {
@@ -91,7 +91,7 @@ struct LatentSeg {
 template <int FMT, int NR>
 struct LatentSmem {  // units, raw units, queries, weights, and
   static constexpr int kP = NR * 128;
-  static constexpr int kBars = 2 * kLatMaxUnits + 2 * kLatMaxRaws + 2 * kLatScores + 11;
+  static constexpr int kBars = 2 * kLatMaxUnits + 2 * kLatMaxRaws + 2 * kLatScores + 12;
   static __host__ __device__ constexpr int unit(int chunks) { return kLatKeys * 128 * chunks; }
   static __host__ __device__ constexpr int raw(int chunks) { return kLatKeys * 64 * chunks; }
   static __host__ __device__ constexpr int q_bytes(int chunks) { return chunks * NR * 128; }
@@ -196,16 +196,6 @@ __device__ __forceinline__ void sync_pair() {
   asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
 
-// bar_try without a pause.
-__device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile("{\n\t.reg .pred p;\n\t"
-               "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-               "selp.u32 %0, 1, 0, p;\n\t}"
-               : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-  return ok != 0u;
-}
-
 __device__ __forceinline__ float lg2_fast(float x) {
   float r;
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -278,9 +268,9 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
       bar_init(p_full + 8 * i, 4);
       bar_init(pv_done + 8 * i, 1);
       bar_init(seg_full + 8 * i, 1);
-      bar_init(seg_empty + 8 * i, 7 + (FMT == KV_CACHE_SRC ? 0 : kLatConverters));
-      bar_init(done + 8 * i, 1);
+      bar_init(seg_empty + 8 * i, 8 + (FMT == KV_CACHE_SRC ? 0 : kLatConverters));
     }
+    for (int i = 0; i < 3; ++i) bar_init(done + 8 * i, 1);
     *state = WaitState{(ring & 1023u) != 0u ? 1 : 0, 0};
     *sh_bad = 0ull;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -628,9 +618,9 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
       tc_fence_before();
       seg = next;
     }
-  } else if (warp == 4 || warp == 5) {
+  } else if (warp == 4 || warp == 5 || warp == 8) {
     // ======================================================================================
-    // the products: warp 4 S = Q K^T, warp 5 O^T += V^T P^T
+    // the products: warps 4 and 8 S = Q K^T, of every other tile each, warp 5 O^T += V^T P^T
     // ======================================================================================
     auto wait = [&](uint32_t bar, uint32_t parity) {
       if (ok) ok = __all_sync(0xFFFFFFFFu, bar_wait(bar, parity, state));
@@ -645,58 +635,39 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
     uint32_t k = 0u, T = 0u;
     Place at{0u, 0u};
     LatentSeg seg;
-    if (warp == 4) {
-      constexpr uint32_t kDesc = kType | ((64u >> 4) << 24);  // and N keys
+    if (warp != 5) {
+      constexpr uint32_t kDesc = kType | ((static_cast<uint32_t>(kLatKeys) >> 3) << 17) | ((64u >> 4) << 24);
+      const uint32_t turn = warp >> 3;  // tiles with this parity are the warp's
       const uint32_t s_at = same(tm_s);
       const uint64_t q_desc = smem_desc(same(q_at), 16);
       uint32_t items = 0u;
-      // Q against the keys at `from`, 64 or 32 of them
-      auto scores = [&](uint32_t d, uint32_t from, uint32_t desc) {
-        const uint64_t kd = smem_desc_groups(from, 16, group_bytes);
-        auto chunk = [&](int32_t c) { tc_mma_chunk(d, q_desc + c * (NR * 128 >> 4), kd + c * (1024 >> 4), desc, c > 0); };
-#pragma unroll
-        for (int c = 0; c < kLatMaxChunks; c += 3) {
-          if (p.ksteps >= 4 * c + 12) {
-            chunk(c); chunk(c + 1); chunk(c + 2);
-          } else {
-#pragma unroll 1
-            for (int32_t y = c; 4 * y + 4 <= p.ksteps; ++y) chunk(y);
-#pragma unroll 1
-            for (int32_t i = p.ksteps & ~3; i < p.ksteps; ++i)
-              tc_mma_ss(d, q_desc + ((i / 4) * (NR * 128 >> 4) + (i % 4) * 2), kd + ((i / 4) * (1024 >> 4) + (i % 4) * 2), desc, i > 0);
-            break;
-          }
-        }
-      };
       while (take(k++, &seg)) {
         if (seg.t1 <= seg.t0) continue;
         wait(q_full, items++ & 1u);
-        for (int32_t j = seg.t0; j < seg.t1;) {
-          if (T >= kLatScores) wait(s_free + 8 * (T % kLatScores), (T / kLatScores - 1u) & 1u);
-          wait(full + 8 * at.unit, at.phase);
-          // a second tile with the first, where it is there: 64 keys cost 32 clocks a product, 32 keys 25
-          const uint32_t T1 = T + 1u;
-          const bool two = j + 1 < seg.t1 && at.unit + 1u < units && T1 % kLatScores != 0u &&
-                           __all_sync(0xFFFFFFFFu, bar_test(full + 8 * (at.unit + 1u), at.phase) &&
-                                                       (T1 < kLatScores || bar_test(s_free + 8 * (T1 % kLatScores), (T1 / kLatScores - 1u) & 1u)));
-          const uint32_t u = same(at.unit | (T % kLatScores) << 8 | (two ? 1u << 16 : 0u)), buf = (u >> 8) & 255u;
-          if (!ok) break;
-          const uint32_t d = s_at + kLatKeys * buf, from = ring0 + (u & 255u) * unit_bytes;
-          if ((u >> 16) != 0u) {
-            tc_fence_after();
-            scores(d, from, kDesc | ((64u >> 3) << 17));
-            tc_commit(s_full + 8 * buf);
-            tc_commit(s_full + 8 * buf + 8);
-            next_unit(&at);
-            ++T;
-            ++j;
-          } else {
-            scores(d, from, kDesc | ((32u >> 3) << 17));
+        for (int32_t j = seg.t0; j < seg.t1; ++j, ++T) {
+          if ((T & 1u) == turn) {
+            const uint32_t u = same(at.unit | (T % kLatScores) << 8), un = u & 255u, buf = u >> 8, d = s_at + kLatKeys * buf;
+            const uint64_t kd = smem_desc_groups(ring0 + un * unit_bytes, 16, group_bytes);
+            if (T >= kLatScores) wait(s_free + 8 * (T % kLatScores), (T / kLatScores - 1u) & 1u);
+            wait(full + 8 * at.unit, at.phase);
+            if (!ok) break;
+            auto chunk = [&](int32_t c) { tc_mma_chunk(d, q_desc + c * (NR * 128 >> 4), kd + c * (1024 >> 4), kDesc, c > 0); };
+#pragma unroll
+            for (int c = 0; c < kLatMaxChunks; c += 3) {
+              if (p.ksteps >= 4 * c + 12) {
+                chunk(c); chunk(c + 1); chunk(c + 2);
+              } else {
+#pragma unroll 1
+                for (int32_t y = c; 4 * y + 4 <= p.ksteps; ++y) chunk(y);
+#pragma unroll 1
+                for (int32_t i = p.ksteps & ~3; i < p.ksteps; ++i)
+                  tc_mma_ss(d, q_desc + ((i / 4) * (NR * 128 >> 4) + (i % 4) * 2), kd + ((i / 4) * (1024 >> 4) + (i % 4) * 2), kDesc, i > 0);
+                break;
+              }
+            }
             tc_commit(s_full + 8 * buf);
           }
           next_unit(&at);
-          ++T;
-          ++j;
         }
         if (!ok) break;
       }
@@ -726,7 +697,7 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
       }
     }
     if (!ok) {  // products still in flight read shared memory and write TMEM: let them end
-      const uint32_t bar = done + 8 * (warp & 1u);
+      const uint32_t bar = done + 8 * (warp == 8 ? 2u : warp - 4u);
       tc_commit(bar);
       for (uint32_t i = 0; i < kSpin && !bar_try(bar, 0); ++i) {}
     }
@@ -941,7 +912,7 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
     // e4m3fn rows to fp16: a warp takes eight keys of a chunk at a time, 16 codes a lane
     // ======================================================================================
     constexpr int kPer = (4 * kLatMaxChunks + kLatConverters - 1) / kLatConverters;
-    const uint32_t w = warp - 8u, jobs = 4u * static_cast<uint32_t>(p.chunks);
+    const uint32_t w = warp - 9u, jobs = 4u * static_cast<uint32_t>(p.chunks);
     const uint32_t row = lane >> 2, q = lane & 3u;
     uint32_t k = 0u, n = 0u;
     Place at{0u, 0u}, from{0u, 0u};
