@@ -95,7 +95,7 @@ struct LatentSmem {  // units, raw units, queries, weights, and
   static __host__ __device__ constexpr int unit(int chunks) { return kLatKeys * 128 * chunks; }
   static __host__ __device__ constexpr int raw(int chunks) { return kLatKeys * 64 * chunks; }
   static __host__ __device__ constexpr int q_bytes(int chunks) { return chunks * NR * 128; }
-  static constexpr int kOffBars = 0, kOffSegs = (kBars * 8 + 15) / 16 * 16, kOffAlpha = kOffSegs + 2 * 64, kOffInv = kOffAlpha + 2 * NR * 4,
+  static constexpr int kOffBars = 0, kOffSegs = (kBars * 8 + 15) / 16 * 16, kOffAlpha = kOffSegs + 2 * 64, kOffInv = kOffAlpha + NR * 4,
                        kOffQf = kOffInv + NR * 4, kOffMisc = kOffQf + NR * 4, kOffValid = kOffMisc + 64,
                        kOffRawValid = kOffValid + kLatMaxUnits * 4, kOffScale = kOffRawValid + kLatMaxRaws * 4;
   static __host__ __device__ constexpr int total(int chunks, int units, int raws) {
@@ -103,6 +103,7 @@ struct LatentSmem {  // units, raw units, queries, weights, and
   }
 };
 static_assert(sizeof(LatentSeg) <= 64, "segments");
+static_assert(kLatThreads<KV_CACHE_E4M3FN> == 512, "176 + 3 x 112 registers of four warpgroups are the launch's 512 x 128");
 static_assert(LatentSmem<KV_CACHE_SRC, 64>::total(kLatMaxChunks, 4, 0) <= 227 * 1024 &&
                   LatentSmem<KV_CACHE_E4M3FN, 64>::total(kLatMaxChunks, 3, 2) <= 227 * 1024, "the widest rows fit");
 
@@ -232,7 +233,7 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
                  s_free = s_full + 8 * kLatScores, p_full = s_free + 8 * kLatScores, pv_done = p_full + 16, seg_full = pv_done + 16,
                  seg_empty = seg_full + 16, done = seg_empty + 16;
   LatentSeg* const segs = reinterpret_cast<LatentSeg*>(small_ptr + S::kOffSegs);
-  float* const sh_alpha = reinterpret_cast<float*>(small_ptr + S::kOffAlpha);   // [2][NR]
+  float* const sh_alpha = reinterpret_cast<float*>(small_ptr + S::kOffAlpha);   // [NR]
   float* const sh_inv = reinterpret_cast<float*>(small_ptr + S::kOffInv);
   float* const sh_qf = reinterpret_cast<float*>(small_ptr + S::kOffQf);
   uint32_t* const sh_valid = reinterpret_cast<uint32_t*>(small_ptr + S::kOffValid);  // of a unit's keys, a bit each
@@ -304,6 +305,10 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
     }
   };
 
+  if constexpr (FMT != KV_CACHE_SRC) {  // 512 threads of 128 registers: the softmax takes more, the others leave them
+    if (warp < 4) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
+  }
   if (warp < 4) {
     // ======================================================================================
     // the softmax
@@ -457,16 +462,18 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
               grew = true;
             }
           }
-          if (t == 0u) {
-            sh_alpha[(T & 1u) * NR + r0] = alpha[0];
-            sh_alpha[(T & 1u) * NR + r0 + 8] = alpha[1];
-          }
         }
         // O^T is all warps': whether any row of the CTA grew
         const bool rescale = any_of_softmax((grew && j > seg.t0) || !ok);
-        if (rescale && any_of_softmax(!ok)) {  // (a warp that gave up still comes here: all leave together)
-          ok = false;
-          break;
+        if (rescale) {
+          if (has_rows && t == 0u) {
+            sh_alpha[r0] = alpha[0];
+            sh_alpha[r0 + 8] = alpha[1];
+          }
+          if (any_of_softmax(!ok)) {  // (a warp that gave up still comes here: all leave together)
+            ok = false;
+            break;
+          }
         }
         uint32_t pw[8];
         if (has_rows) {
@@ -496,14 +503,13 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
           ok = bar_wait(pv_done + 8 * ((T - 1u) & 1u), ((T - 1u) >> 1) & 1u, state) && ok;
           __syncwarp();
           tc_fence_after();
-          const float* f = sh_alpha + (T & 1u) * NR;
           for (int32_t b = 0; b < p.blocks; ++b)
 #pragma unroll 1
             for (int c = 0; c < NR / 16; ++c) {
               uint32_t w[16];
               tc_ld16(w, tmem + lanes + b * NR + 16 * c);
 #pragma unroll
-              for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * f[16 * c + i]);
+              for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * sh_alpha[16 * c + i]);
               tc_st16(tmem + lanes + b * NR + 16 * c, w);
             }
           tc_wait_st();
@@ -843,41 +849,51 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
       for (int32_t unit = n0; unit < n1 && ok; ++unit, ++n) {
         const int32_t id = next_id, key = unit * kLatKeys + static_cast<int32_t>(lane);
         if (unit + 1 < n1) next_id = page_of(unit + 1);
-        const bool want = key <= seg.p_hi, have = static_cast<uint32_t>(id) < static_cast<uint32_t>(a.num_pages);
+        const bool want = key <= seg.p_hi, have = static_cast<uint32_t>(id) < static_cast<uint32_t>(a.num_pages), live = want && have;
         if (want && !have && rank == 0u) record_oob(a.err, static_cast<uint64_t>(seg.b));
-        const uint32_t bits = __ballot_sync(0xFFFFFFFFu, want && have);
+        const uint32_t bits = __ballot_sync(0xFFFFFFFFu, live);
         const uint32_t off = static_cast<uint32_t>(key) - a.page.quot(static_cast<uint32_t>(key)) * a.page.d;
+        // boxes of `box` groups of eight keys, which share a page; of a pair's CTAs each brings half of the unit
+        const bool boxes = p.box > 0 && bits == ~0u;
+        const int32_t g0 = pair ? 2 * static_cast<int32_t>(rank) : 0;
+        const int32_t page0 = static_cast<int32_t>(same(static_cast<uint32_t>(__shfl_sync(0xFFFFFFFFu, id, 8 * g0))));
+        const int32_t in0 = static_cast<int32_t>(same(__shfl_sync(0xFFFFFFFFu, off, 8 * g0)) >> 3);
+        const uint32_t bar = same(full_at + 8 * at.unit), part = FMT == KV_CACHE_SRC ? group_bytes : group_bytes / 2u;  // of eight keys
+        const uint32_t dst = same(FMT == KV_CACHE_SRC ? ring + at.unit * unit_bytes : raw_ring + at.unit * raw_bytes);
+        // (nothing that can be known before stands between a free unit and its boxes)
         if (n >= places) {
           if (waiting > 0u && !__all_sync(0xFFFFFFFFu, bar_try(empty_at + 8 * at.unit, at.phase ^ 1u))) hand_over(true);
           ok = __all_sync(0xFFFFFFFFu, bar_wait(empty_at + 8 * at.unit, at.phase ^ 1u, state));
           if (!ok) break;
           if constexpr (FMT != KV_CACHE_SRC) fence_async_shared();  // generic loads, and then boxes
         }
-        const uint32_t bar = full_at + 8 * at.unit;
-        const uint32_t dst = FMT == KV_CACHE_SRC ? ring + at.unit * unit_bytes : raw_ring + at.unit * raw_bytes;
-        const uint32_t part = FMT == KV_CACHE_SRC ? group_bytes : group_bytes / 2u;  // of eight keys
-        if (lane == 0u) (FMT == KV_CACHE_SRC ? sh_valid : sh_raw_valid)[at.unit] = bits;
-        if constexpr (FMT != KV_CACHE_SRC) {
-          const bool live = want && have;
+        if (boxes) {
+          if constexpr (FMT == KV_CACHE_SRC) {
+            if (waiting > 0u) hand_over(true);
+          }
+          if (p.box == (pair ? 2 : 4) && p.box_chunks == p.chunks) {
+            tma_rows(dst + g0 * part, &p.map, bar, 0, in0, page0, pair);
+          } else {
+            for (int32_t g = g0; g < (pair ? g0 + 2 : 4); g += p.box) {
+              const int32_t page = static_cast<int32_t>(same(static_cast<uint32_t>(__shfl_sync(0xFFFFFFFFu, id, 8 * g))));
+              const int32_t in_page = static_cast<int32_t>(same(__shfl_sync(0xFFFFFFFFu, off, 8 * g)) >> 3);
+              for (int32_t c = 0; c < p.chunks; c += p.box_chunks)
+                tma_rows(dst + g * part + c * (part / static_cast<uint32_t>(p.chunks)), &p.map, bar, 64 * c, in_page, page, pair);
+            }
+          }
+          if (lane == 0u) {
+            (FMT == KV_CACHE_SRC ? sh_valid : sh_raw_valid)[at.unit] = bits;
+            bar_arrive_expect(bar, 4u * part);  // (boxes that land before are counted already)
+          }
+        } else if (lane == 0u) {
+          (FMT == KV_CACHE_SRC ? sh_valid : sh_raw_valid)[at.unit] = bits;
+        }
+        if constexpr (FMT != KV_CACHE_SRC)
           copy_async<4>(static_cast<uint32_t>(__cvta_generic_to_shared(sh_scale + (units + at.unit) * kLatKeys + lane)),
                         reinterpret_cast<const uint8_t*>(live ? lp.scales + (static_cast<int64_t>(id) * a.page.d + off) * lp.scale_slot : lp.scales),
                         live ? 4u : 0u);
-        }
-        if (p.box > 0 && bits == ~0u) {
-          hand_over(true);
-          // boxes of `box` groups of eight keys, which share a page; of a pair's CTAs each brings half of the unit
-          if (lane == 0u) bar_arrive_expect(bar, 4u * part);
-          __syncwarp();
-          const int32_t g0 = pair ? 2 * static_cast<int32_t>(rank) : 0, g1 = pair ? g0 + 2 : 4;
-          for (int32_t g = g0; g < g1; g += p.box) {
-            const int32_t page = static_cast<int32_t>(same(static_cast<uint32_t>(__shfl_sync(0xFFFFFFFFu, id, 8 * g))));
-            const int32_t in_page = static_cast<int32_t>(same(__shfl_sync(0xFFFFFFFFu, off, 8 * g)) >> 3);
-            for (int32_t c = 0; c < p.chunks; c += p.box_chunks)
-              tma_rows(dst + g * part + c * (part / static_cast<uint32_t>(p.chunks)), &p.map, bar, 64 * c, in_page, page, pair);
-          }
-          if constexpr (FMT != KV_CACHE_SRC) bar_arrive_copies(bar);  // the scales
-        } else {
-          const int64_t row = want && have ? wide(id, p.page_stride) + wide(off, p.slot_stride) : -1;
+        if (!boxes) {
+          const int64_t row = live ? wide(id, p.page_stride) + wide(off, p.slot_stride) : -1;
           // pieces in turn, so that lanes copy neighbouring ones
           for (uint32_t i0 = 0; i0 < kLatKeys * pieces; i0 += 32u) {
             const uint32_t i = i0 + lane, kk = i / pieces, piece = i - kk * pieces;
@@ -887,14 +903,16 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
                                                     : base + (piece >> 2) * 512u + (kk & 7u) * 64u + ((piece & 3u) << 4);
             copy_async<16>(to, a.k + (r < 0 ? 0 : r + 16 * piece), r < 0 ? 0u : 16u);
           }
-          if constexpr (FMT == KV_CACHE_SRC) {
+        }
+        if constexpr (FMT == KV_CACHE_SRC) {
+          if (!boxes) {
             commit_async();
             pending[waiting++] = at.unit;
             hand_over(false);
-          } else {
-            bar_arrive_copies(bar);
-            if (lane == 0u) bar_arrive(bar);
           }
+        } else {
+          bar_arrive_copies(bar);  // the scales, and rows
+          if (!boxes && lane == 0u) bar_arrive(bar);
         }
         if (++at.unit == places) {
           at.unit = 0u;
