@@ -7,7 +7,7 @@
 //
 // A CTA takes up to NR = 64 or 32 query rows, a row being a (query, head)
 // pair, and goes over tiles of 32 keys:
-//   S [rows][keys] = Q K^T       M = 64 (Q, shared memory), N = 32 keys, all D dims;
+//   S [rows][keys] = Q K^T       M = 64 (Q: 384 dims in TMEM, all for 32 rows, the others in shared memory), N = 32 keys;
 //   O^T [dims][rows] += V^T P^T  M = 128 dims, N = NR rows: the tile's first L
 //                                dims as they lie (dims contiguous), P in
 //                                shared memory.
@@ -53,7 +53,7 @@ namespace kvimpl {
 constexpr int kLatKeys = 32;        // keys of a tile, which is a unit of the ring
 constexpr int kLatMaxChunks = 9;    // 64-dim chunks of a row: up to 576 dims
 constexpr int kLatMaxUnits = 8, kLatMaxRaws = 8;
-constexpr int kLatScores = 4;       // tiles whose scores may be in TMEM
+constexpr int kLatScores = 2;       // tiles whose scores may be in TMEM
 
 struct LatentTileParams {
   LatentParams l;
@@ -94,7 +94,9 @@ struct LatentSmem {  // units, raw units, queries, weights, and
   static constexpr int kBars = 2 * kLatMaxUnits + 2 * kLatMaxRaws + 2 * kLatScores + 12;
   static __host__ __device__ constexpr int unit(int chunks) { return kLatKeys * 128 * chunks; }
   static __host__ __device__ constexpr int raw(int chunks) { return kLatKeys * 64 * chunks; }
-  static __host__ __device__ constexpr int q_bytes(int chunks) { return chunks * NR * 128; }
+  // chunks of the queries that are in TMEM, beside O^T and the scores; the others are in shared memory
+  static constexpr int kInTmem = NR == 64 ? 6 : 9;
+  static __host__ __device__ constexpr int q_bytes(int chunks) { return chunks > kInTmem ? (chunks - kInTmem) * NR * 128 : 0; }
   static constexpr int kOffBars = 0, kOffSegs = (kBars * 8 + 15) / 16 * 16, kOffAlpha = kOffSegs + 2 * 64, kOffInv = kOffAlpha + NR * 4,
                        kOffQf = kOffInv + NR * 4, kOffMisc = kOffQf + NR * 4, kOffValid = kOffMisc + 64,
                        kOffRawValid = kOffValid + kLatMaxUnits * 4, kOffScale = kOffRawValid + kLatMaxRaws * 4;
@@ -104,8 +106,10 @@ struct LatentSmem {  // units, raw units, queries, weights, and
 };
 static_assert(sizeof(LatentSeg) <= 64, "segments");
 static_assert(kLatThreads<KV_CACHE_E4M3FN> == 512, "176 + 3 x 112 registers of four warpgroups are the launch's 512 x 128");
-static_assert(LatentSmem<KV_CACHE_SRC, 64>::total(kLatMaxChunks, 4, 0) <= 227 * 1024 &&
-                  LatentSmem<KV_CACHE_E4M3FN, 64>::total(kLatMaxChunks, 3, 2) <= 227 * 1024, "the widest rows fit");
+static_assert(LatentSmem<KV_CACHE_SRC, 64>::total(kLatMaxChunks, 5, 0) <= 227 * 1024 &&
+                  LatentSmem<KV_CACHE_E4M3FN, 64>::total(kLatMaxChunks, 3, 4) <= 227 * 1024, "the widest rows fit");
+static_assert(4 * 64 + kLatScores * kLatKeys + 32 * LatentSmem<KV_CACHE_SRC, 64>::kInTmem <= 512 &&
+                  4 * 32 + kLatScores * kLatKeys + 32 * LatentSmem<KV_CACHE_SRC, 32>::kInTmem <= 512, "TMEM");
 
 // Rows of the sequence's queries in blocks of NR (of the pair: 2 NR), and tiles of each (an upper bound, at least one).
 struct LatentGeom {
@@ -149,6 +153,13 @@ __device__ __forceinline__ void tc_ld_rows(float (&s)[16], uint32_t addr) {
   for (int i = 0; i < 16; ++i) s[i] = __uint_as_float(r[i]);
 }
 
+// The same, stored.
+__device__ __forceinline__ void tc_st_rows(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile("tcgen05.st.sync.aligned.16x256b.x4.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};"
+               ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+               "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr) : "memory");
+}
+
 // smem_desc with groups of eight rows (or keys) `group` bytes apart.
 __device__ __forceinline__ uint64_t smem_desc_groups(uint32_t addr, uint32_t lead, uint32_t group) {
   return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(lead >> 4) << 16) |
@@ -173,6 +184,15 @@ __device__ __forceinline__ void tc_mma_two(uint32_t d, uint64_t a, uint64_t b, u
 #undef KV_FIRST
 #undef KV_NEXT
 #undef KV_OPERANDS
+// A in TMEM: its 64 dims are 32 columns.
+__device__ __forceinline__ void tc_mma_chunk_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+#define KV_NEXT(i, j) "add.u32 u, %1, " i ";\n\tadd.u32 v, %2, " j ";\n\tmov.b64 y, {v, %3};\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [u], y, %4, 1;\n\t"
+  asm volatile("{\n\t.reg .pred e, p;\n\t.reg .b64 y;\n\t.reg .b32 u, v;\n\telect.sync _|e, 0xFFFFFFFF;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+               "mov.b64 y, {%2, %3};\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t"
+               KV_NEXT("8", "2") KV_NEXT("16", "4") KV_NEXT("24", "6") "}"
+               ::"r"(d), "r"(a), "r"(static_cast<uint32_t>(b)), "r"(static_cast<uint32_t>(b >> 32)), "r"(idesc), "r"(acc ? 1u : 0u) : "memory");
+#undef KV_NEXT
+}
 
 // A box of a cache of latent rows (latent_map), by one lane of a converged warp; into the same place of both CTAs of a
 // pair, and their barriers.
@@ -293,7 +313,8 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
     if (lane == 0u) bar_arrive(seg_empty + 8 * (k & 1u));
     return s->stop == 0;
   };
-  const uint32_t tm_s = tmem + 4 * NR;  // S, kLatScores buffers of kLatKeys columns, behind O^T
+  const uint32_t tm_s = tmem + 4 * NR;  // S, kLatScores buffers of kLatKeys columns, behind O^T; then Q
+  const uint32_t tm_q = tm_s + kLatScores * kLatKeys;
   // a warp's place in the ring of units
   struct Place {
     uint32_t unit, phase;
@@ -319,62 +340,105 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
     const uint32_t lanes = warp << 21;
     const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;  // the maximum is taken before the scale
     constexpr float kSmall = kBF16 ? 0.0f : 7.0f;
-    // Queries into shared memory: a warp has NR / 4 rows, some at a time. (All products that read the
-    // last ones have ended, as their scores were waited for.)
+    // The queries. (All products that read the last ones have ended, as their scores were waited for.) A power of two brings
+    // bf16 ones over e4m3fn rows into fp16's range: the row's largest element to 2^13 .. 2^14.
+    auto row_of = [&](const LatentSeg& s, int32_t r) {
+      const int32_t x = s.row0 + min(r, s.last), qi = static_cast<int32_t>(a.group.quot(static_cast<uint32_t>(x)));
+      return a.q + static_cast<int64_t>(s.q0 + qi) * a.q_token + static_cast<int64_t>(x - qi * HQ) * a.q_head;
+    };
     auto load_q = [&](const LatentSeg& s) {
-      constexpr int kRows = NR / 4, kAt = FMT == KV_CACHE_SRC ? 8 : 4, kPer = (kLatMaxChunks * 8 + 31) / 32;
-      const uint32_t pieces = static_cast<uint32_t>(a.head_dim) / 8u;
-      for (int i0 = 0; i0 < kRows; i0 += kAt) {
-        uint4 w[kAt][kPer];
+      constexpr int kIn = S::kInTmem, kAt = 3;  // chunks in TMEM; chunks in flight
+      const bool shift = FMT != KV_CACHE_SRC && a.bf16;
+      auto shifted = [](uint32_t z, float f) {
+        const float2 v = widen2<true>(z);
+        return pack2(v.x * f, v.y * f, false);
+      };
+      if (has_rows) {
+        // thread (g, t): dims 16 i + 4 t .. + 3 of each chunk of rows g and g + 8
+        const uint8_t* src[2] = {row_of(s, r0) + 8 * t, row_of(s, r0 + 8) + 8 * t};
+        const bool live[2] = {r0 < s.nrows, r0 + 8 < s.nrows};
+        auto piece = [&](int c, int chunk, int i) {
+          uint2 w = make_uint2(0u, 0u);
+          if (live[c] && 4 * chunk + i < p.ksteps) w = __ldg(reinterpret_cast<const uint2*>(src[c] + 128 * chunk + 32 * i));
+          return w;
+        };
+        float f[2] = {1.0f, 1.0f};
+        if (shift) {
 #pragma unroll
-        for (int y = 0; y < kAt; ++y) {
-          const int32_t r = static_cast<int32_t>(warp) * kRows + i0 + y;
-          const bool live = r < s.nrows;
-          const int32_t qi = static_cast<int32_t>(a.group.quot(static_cast<uint32_t>(s.row0 + (live ? r : 0))));
-          const int32_t h = s.row0 + (live ? r : 0) - qi * HQ;
-          const uint8_t* src = a.q + static_cast<int64_t>(s.q0 + qi) * a.q_token + static_cast<int64_t>(h) * a.q_head;
+          for (int c = 0; c < 2; ++c) {
+            uint32_t m = 0u;
+#pragma unroll 3
+            for (int32_t chunk = 0; chunk < p.chunks; ++chunk)
 #pragma unroll
-          for (int x = 0; x < kPer; ++x) {
-            const uint32_t piece = lane + 32u * x;
-            w[y][x] = make_uint4(0u, 0u, 0u, 0u);
-            if (live && piece < pieces) w[y][x] = __ldg(reinterpret_cast<const uint4*>(src + 16u * piece));
+              for (int i = 0; i < 4; ++i) {
+                const uint2 w = piece(c, chunk, i);
+                m = absmax_pair<true>(absmax_pair<true>(m, w.x), w.y);
+              }
+            uint32_t e = __float_as_uint(absmax_pair_value<true>(m));
+            e = max(e, __shfl_xor_sync(0xFFFFFFFFu, e, 1));
+            e = max(e, __shfl_xor_sync(0xFFFFFFFFu, e, 2)) >> 23;
+            f[c] = __uint_as_float(min(254u, 267u - e) << 23);
           }
         }
-#pragma unroll
-        for (int y = 0; y < kAt; ++y) {
-          const uint32_t r = warp * kRows + i0 + y;
-          if constexpr (FMT != KV_CACHE_SRC) {
-            float f = 1.0f;
-            if (a.bf16) {  // into fp16's range: the row's largest element to 2^13 .. 2^14
-              uint32_t m = 0u;
-#pragma unroll
-              for (int x = 0; x < kPer; ++x)
-                m = absmax_pair<true>(absmax_pair<true>(absmax_pair<true>(absmax_pair<true>(m, w[y][x].x), w[y][x].y), w[y][x].z), w[y][x].w);
-              const uint32_t e = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(absmax_pair_value<true>(m))) >> 23;
-              f = __uint_as_float(min(254u, 267u - e) << 23);
-              auto shift = [&](uint32_t z) {
-                const float2 v = widen2<true>(z);
-                return pack2(v.x * f, v.y * f, false);
-              };
-#pragma unroll
-              for (int x = 0; x < kPer; ++x)
-                w[y][x] = make_uint4(shift(w[y][x].x), shift(w[y][x].y), shift(w[y][x].z), shift(w[y][x].w));
-            }
-            if (lane == 0u) sh_qf[r] = __fdiv_rn(1.0f, f);
-          }
-#pragma unroll
-          for (int x = 0; x < kPer; ++x) {
-            const uint32_t piece = lane + 32u * x;
-            if (piece < pieces)
-              st_shared16(q_at + (piece >> 3) * (NR * 128u) + r * 128u + (((piece & 7u) ^ (r & 7u)) << 4), w[y][x].x ^ flip,
-                          w[y][x].y ^ flip, w[y][x].z ^ flip, w[y][x].w ^ flip);
+        if constexpr (FMT != KV_CACHE_SRC) {
+          if (t == 0u) {
+            sh_qf[r0] = f[0];
+            sh_qf[r0 + 8] = f[1];
           }
         }
+#pragma unroll 1
+        for (int32_t c0 = 0; c0 < min(kIn, p.chunks); c0 += kAt) {
+          uint2 w[kAt][2][4];
+#pragma unroll
+          for (int y = 0; y < kAt; ++y)
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) w[y][c][i] = piece(c, c0 + y, i);
+#pragma unroll
+          for (int y = 0; y < kAt; ++y) {
+            if (c0 + y >= kIn) break;
+            uint32_t r[16];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                const uint2 z = w[y][c][i];
+                r[4 * i + 2 * c] = (shift ? shifted(z.x, f[c]) : z.x) ^ flip;
+                r[4 * i + 2 * c + 1] = (shift ? shifted(z.y, f[c]) : z.y) ^ flip;
+              }
+            tc_st_rows(tm_q + 32 * (c0 + y) + lanes, r);
+          }
+        }
+        tc_wait_st();
       }
-      fence_async_shared();
+      if (kIn < kLatMaxChunks && p.chunks > kIn) {  // the last chunks to shared memory: a warp has NR / 4 rows, 16 bytes a lane
+        constexpr int kRows = NR / 4;
+        if (shift) sync_softmax();  // sh_qf
+        const uint32_t rest = static_cast<uint32_t>(a.head_dim) / 8u - 8u * kIn;  // pieces, at most 24
+        uint4 w[kRows];
+#pragma unroll
+        for (int y = 0; y < kRows; ++y) {
+          const int32_t r = static_cast<int32_t>(warp) * kRows + y;
+          w[y] = make_uint4(0u, 0u, 0u, 0u);
+          if (r < s.nrows && lane < rest) w[y] = __ldg(reinterpret_cast<const uint4*>(row_of(s, r) + 128 * kIn + 16u * lane));
+        }
+#pragma unroll
+        for (int y = 0; y < kRows; ++y) {
+          const uint32_t r = warp * kRows + y;
+          if (shift) {
+            const float f = sh_qf[r];
+            w[y] = make_uint4(shifted(w[y].x, f), shifted(w[y].y, f), shifted(w[y].z, f), shifted(w[y].w, f));
+          }
+          if (lane < rest)
+            st_shared16(q_at + (lane >> 3) * (NR * 128u) + r * 128u + (((lane & 7u) ^ (r & 7u)) << 4), w[y].x ^ flip, w[y].y ^ flip, w[y].z ^ flip,
+                        w[y].w ^ flip);
+        }
+        fence_async_shared();
+      }
+      tc_fence_before();
       __syncwarp();
       if (lane == 0u) bar_arrive(q_full);
-      sync_softmax();  // sh_qf
     };
     uint32_t k = 0u, T = 0u;  // segments and tiles that went by
     Place at{0u, 0u};
@@ -390,7 +454,7 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         rs[c] = fabsf(a.scale_log2);
-        if constexpr (FMT != KV_CACHE_SRC) rs[c] *= has_rows ? sh_qf[r0 + 8 * c] : 1.0f;
+        if constexpr (FMT != KV_CACHE_SRC) rs[c] *= has_rows ? __fdiv_rn(1.0f, sh_qf[r0 + 8 * c]) : 1.0f;
         if (rs[c] == 0.0f) rs[c] = __uint_as_float(1u);  // hidden scores (-inf) must stay -inf
       }
       for (int32_t j = seg.t0; j < seg.t1; ++j, ++T) {
@@ -644,8 +708,8 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
     if (warp != 5) {
       constexpr uint32_t kDesc = kType | ((static_cast<uint32_t>(kLatKeys) >> 3) << 17) | ((64u >> 4) << 24);
       const uint32_t turn = warp >> 3;  // tiles with this parity are the warp's
-      const uint32_t s_at = same(tm_s);
-      const uint64_t q_desc = smem_desc(same(q_at), 16);
+      const uint32_t s_at = same(tm_s), q_col = same(tm_q);
+      const uint64_t q_desc = smem_desc(same(q_at), 16);  // of the chunks that are not in TMEM
       uint32_t items = 0u;
       while (take(k++, &seg)) {
         if (seg.t1 <= seg.t0) continue;
@@ -657,7 +721,10 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
             if (T >= kLatScores) wait(s_free + 8 * (T % kLatScores), (T / kLatScores - 1u) & 1u);
             wait(full + 8 * at.unit, at.phase);
             if (!ok) break;
-            auto chunk = [&](int32_t c) { tc_mma_chunk(d, q_desc + c * (NR * 128 >> 4), kd + c * (1024 >> 4), kDesc, c > 0); };
+            auto chunk = [&](int32_t c) {
+              if (c < S::kInTmem) tc_mma_chunk_ts(d, q_col + 32 * c, kd + c * (1024 >> 4), kDesc, c > 0);
+              else tc_mma_chunk(d, q_desc + (c - S::kInTmem) * (NR * 128 >> 4), kd + c * (1024 >> 4), kDesc, c > 0);
+            };
 #pragma unroll
             for (int c = 0; c < kLatMaxChunks; c += 3) {
               if (p.ksteps >= 4 * c + 12) {
@@ -666,8 +733,11 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
 #pragma unroll 1
                 for (int32_t y = c; 4 * y + 4 <= p.ksteps; ++y) chunk(y);
 #pragma unroll 1
-                for (int32_t i = p.ksteps & ~3; i < p.ksteps; ++i)
-                  tc_mma_ss(d, q_desc + ((i / 4) * (NR * 128 >> 4) + (i % 4) * 2), kd + ((i / 4) * (1024 >> 4) + (i % 4) * 2), kDesc, i > 0);
+                for (int32_t i = p.ksteps & ~3; i < p.ksteps; ++i) {
+                  const uint64_t b = kd + ((i / 4) * (1024 >> 4) + (i % 4) * 2);
+                  if (i < 4 * S::kInTmem) tc_mma_ts(d, q_col + 8 * i, b, kDesc, i > 0);
+                  else tc_mma_ss(d, q_desc + ((i / 4 - S::kInTmem) * (NR * 128 >> 4) + (i % 4) * 2), b, kDesc, true);
+                }
                 break;
               }
             }
