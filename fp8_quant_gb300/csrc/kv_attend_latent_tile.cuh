@@ -45,6 +45,8 @@
 // error record and in the workspace's head, lets its copies and products end and leaves.
 #pragma once
 
+#include <type_traits>
+
 #include "kv_attend_latent.cuh"
 #include "kv_attend_tile.cuh"
 
@@ -53,7 +55,7 @@ namespace kvimpl {
 constexpr int kLatKeys = 32;        // keys of a tile, which is a unit of the ring
 constexpr int kLatMaxChunks = 9;    // 64-dim chunks of a row: up to 576 dims
 constexpr int kLatMaxUnits = 8, kLatMaxRaws = 8;
-constexpr int kLatScores = 2;       // tiles whose scores may be in TMEM
+constexpr int kLatScores = 3;       // tiles whose scores may be in TMEM
 
 struct LatentTileParams {
   LatentParams l;
@@ -95,7 +97,7 @@ struct LatentSmem {  // units, raw units, queries, weights, and
   static __host__ __device__ constexpr int unit(int chunks) { return kLatKeys * 128 * chunks; }
   static __host__ __device__ constexpr int raw(int chunks) { return kLatKeys * 64 * chunks; }
   // chunks of the queries that are in TMEM, beside O^T and the scores; the others are in shared memory
-  static constexpr int kInTmem = NR == 64 ? 6 : 9;
+  static constexpr int kInTmem = NR == 64 ? 5 : 9;
   static __host__ __device__ constexpr int q_bytes(int chunks) { return chunks > kInTmem ? (chunks - kInTmem) * NR * 128 : 0; }
   static constexpr int kOffBars = 0, kOffSegs = (kBars * 8 + 15) / 16 * 16, kOffAlpha = kOffSegs + 2 * 64, kOffInv = kOffAlpha + NR * 4,
                        kOffQf = kOffInv + NR * 4, kOffMisc = kOffQf + NR * 4, kOffValid = kOffMisc + 64,
@@ -441,7 +443,7 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
       if (lane == 0u) bar_arrive(q_full);
     };
     uint32_t k = 0u, T = 0u;  // segments and tiles that went by
-    Place at{0u, 0u};
+    Place at{0u, 0u}, buf{0u, 0u};  // of units, and of scores
     LatentSeg seg, next;
     bool have = take(k++, &seg);
     const bool lost = any_of_softmax(!ok);
@@ -457,60 +459,79 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
         if constexpr (FMT != KV_CACHE_SRC) rs[c] *= has_rows ? __fdiv_rn(1.0f, sh_qf[r0 + 8 * c]) : 1.0f;
         if (rs[c] == 0.0f) rs[c] = __uint_as_float(1u);  // hidden scores (-inf) must stay -inf
       }
-      for (int32_t j = seg.t0; j < seg.t1; ++j, ++T) {
-        // the unit is long there; its keys' bits and scales are read while S is waited for. (Threads that gave up a wait go
-        // on to the barrier below, where all leave together.)
-        ok = bar_wait(full + 8 * at.unit, at.phase, state) && ok;
-        const uint32_t valid = sh_valid[at.unit];
-        float s[16], kf[8], alpha[2] = {1.0f, 1.0f};  // scores, their keys' scales, factors of the rows' sums
-        if constexpr (FMT != KV_CACHE_SRC) {
+      // N tiles from j on; false: a wait ran out, and all leave together
+      auto tiles = [&](auto count, int32_t j) {
+        constexpr int N = decltype(count)::value;
+        // The units are long there; their keys' bits and scales are read while S is waited for. (Threads that gave up a wait
+        // go on to the barrier below.)
+        uint32_t valid[N];
+        float s[N][16], kf[N][8], alpha[2] = {1.0f, 1.0f};  // scores, their keys' scales, factors of the rows' sums
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 f = *reinterpret_cast<const float2*>(sh_scale + at.unit * kLatKeys + 8 * i + 2 * t);
-            kf[2 * i] = f.x;
-            kf[2 * i + 1] = f.y;
-          }
-        }
-        next_unit(&at);
-        ok = bar_wait(s_full + 8 * (T % kLatScores), (T / kLatScores) & 1u, state) && ok;
-        __syncwarp();
-        tc_fence_after();
-        bool grew = false;
-        if (has_rows) {
-          tc_ld_rows(s, tm_s + kLatKeys * (T % kLatScores) + lanes);
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0u) bar_arrive(s_free + 8 * (T % kLatScores));
+        for (int x = 0; x < N; ++x) {
+          ok = bar_wait(full + 8 * at.unit, at.phase, state) && ok;
+          valid[x] = sh_valid[at.unit];
           if constexpr (FMT != KV_CACHE_SRC) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) s[i] *= kf[2 * (i / 4) + (i & 1)] * rs[(i >> 1) & 1];
+            for (int i = 0; i < 4; ++i) {
+              const float2 f = *reinterpret_cast<const float2*>(sh_scale + at.unit * kLatKeys + 8 * i + 2 * t);
+              kf[x][2 * i] = f.x;
+              kf[x][2 * i + 1] = f.y;
+            }
           }
-          if (j * kLatKeys + kLatKeys - 1 > p_lo || valid != ~0u) {
+          next_unit(&at);
+        }
+        bool grew = false;
+#pragma unroll
+        for (int x = 0; x < N; ++x) {
+          ok = bar_wait(s_full + 8 * buf.unit, buf.phase, state) && ok;
+          __syncwarp();
+          tc_fence_after();
+          if (has_rows) {
+            tc_ld_rows(s[x], tm_s + kLatKeys * buf.unit + lanes);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0u) bar_arrive(s_free + 8 * buf.unit);
+          }
+          if (++buf.unit == kLatScores) {
+            buf.unit = 0u;
+            buf.phase ^= 1u;
+          }
+        }
+        if (has_rows) {
+          float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+          for (int x = 0; x < N; ++x) {
+            if constexpr (FMT != KV_CACHE_SRC) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) s[x][i] *= kf[x][2 * (i / 4) + (i & 1)] * rs[(i >> 1) & 1];
+            }
+            if ((j + x) * kLatKeys + kLatKeys - 1 > p_lo || valid[x] != ~0u) {
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                const int32_t n = pos[c] - (j + x) * kLatKeys + 1;  // the first n keys
+                const uint32_t see = ((n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u) & valid[x]) >> (2 * t);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                  for (int y = 0; y < 2; ++y)
+                    if ((see >> (8 * i + y) & 1u) == 0u) s[x][4 * i + 2 * c + y] = -INFINITY;
+              }
+            }
+            float lv[8];
+            if constexpr (FMT != KV_CACHE_SRC) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) lv[i] = fmaxf(lg2_fast(fabsf(kf[x][i])), -100.0f);
+            }
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              const int32_t n = pos[c] - j * kLatKeys + 1;  // the first n keys
-              const uint32_t see = ((n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u) & valid) >> (2 * t);
+              float z[2] = {-INFINITY, -INFINITY};
 #pragma unroll
               for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int x = 0; x < 2; ++x)
-                  if ((see >> (8 * i + x) & 1u) == 0u) s[4 * i + 2 * c + x] = -INFINITY;
+                for (int y = 0; y < 2; ++y)
+                  z[y] = fmaxf(z[y], FMT == KV_CACHE_SRC ? s[x][4 * i + 2 * c + y] : s[x][4 * i + 2 * c + y] + lv[2 * i + y]);
+              top[c] = fmaxf(top[c], fmaxf(z[0], z[1]));
             }
-          }
-          float lv[8];
-          if constexpr (FMT != KV_CACHE_SRC) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) lv[i] = fmaxf(lg2_fast(fabsf(kf[i])), -100.0f);
-          }
-          float top[2];
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float x[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-              for (int y = 0; y < 2; ++y) x[y] = fmaxf(x[y], FMT == KV_CACHE_SRC ? s[4 * i + 2 * c + y] : s[4 * i + 2 * c + y] + lv[2 * i + y]);
-            top[c] = fmaxf(x[0], x[1]);
           }
 #pragma unroll
           for (int o = 1; o < 4; o <<= 1)
@@ -534,35 +555,36 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
             sh_alpha[r0] = alpha[0];
             sh_alpha[r0 + 8] = alpha[1];
           }
-          if (any_of_softmax(!ok)) {  // (a warp that gave up still comes here: all leave together)
-            ok = false;
-            break;
-          }
+          if (any_of_softmax(!ok)) return false;
         }
-        uint32_t pw[8];
+        uint32_t pw[N][8];
         if (has_rows) {
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             const float ref = m[c] == -INFINITY ? 0.0f : m[c];
             float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              float2 z = make_float2(s[4 * i + 2 * c], s[4 * i + 2 * c + 1]);
-              if constexpr (FMT == KV_CACHE_SRC) z = fma2(z, rs[c], -ref); else z = add2(z, make_float2(-ref, -ref));
-              float2 e = make_float2(exp2_fast(z.x), exp2_fast(z.y));
-              sum[i & 1] = add2(sum[i & 1], e);
-              if constexpr (FMT != KV_CACHE_SRC) {
-                e.x *= kf[2 * i];
-                e.y *= kf[2 * i + 1];
+            for (int x = 0; x < N; ++x)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                float2 z = make_float2(s[x][4 * i + 2 * c], s[x][4 * i + 2 * c + 1]);
+                if constexpr (FMT == KV_CACHE_SRC) z = fma2(z, rs[c], -ref); else z = add2(z, make_float2(-ref, -ref));
+                float2 e = make_float2(exp2_fast(z.x), exp2_fast(z.y));
+                sum[i & 1] = add2(sum[i & 1], e);
+                if constexpr (FMT != KV_CACHE_SRC) {
+                  e.x *= kf[x][2 * i];
+                  e.y *= kf[x][2 * i + 1];
+                }
+                pw[x][2 * i + c] = pack2(e.x, e.y, kBF16);
               }
-              pw[2 * i + c] = pack2(e.x, e.y, kBF16);
-            }
             sum[0] = add2(sum[0], sum[1]);
             l[c] = __fmaf_rn(l[c], alpha[c], sum[0].x + sum[0].y);
           }
         }
         // tiles take turns in the halves of P's rows: P V of the last but one has read its
-        if (T > 1u) ok = bar_wait(pv_done + 8 * (T & 1u), ((T >> 1) - 1u) & 1u, state) && ok;
+#pragma unroll
+        for (int x = 0; x < N; ++x)
+          if (T + x > 1u) ok = bar_wait(pv_done + 8 * ((T + x) & 1u), (((T + x) >> 1) - 1u) & 1u, state) && ok;
         if (rescale) {  // and that of the last one has written O^T
           ok = bar_wait(pv_done + 8 * ((T - 1u) & 1u), ((T - 1u) >> 1) & 1u, state) && ok;
           __syncwarp();
@@ -580,18 +602,35 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
         }
         if (has_rows) {
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const uint32_t r = static_cast<uint32_t>(r0 + 8 * c);
+          for (int x = 0; x < N; ++x)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              asm volatile("st.shared.u32 [%0], %1;" ::"r"(p_at + r * 128u + (((i + 4u * (T & 1u)) ^ (r & 7u)) << 4) + 4u * t), "r"(pw[2 * i + c]) : "memory");
-          }
+            for (int c = 0; c < 2; ++c) {
+              const uint32_t r = static_cast<uint32_t>(r0 + 8 * c);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                asm volatile("st.shared.u32 [%0], %1;" ::"r"(p_at + r * 128u + (((i + 4u * ((T + x) & 1u)) ^ (r & 7u)) << 4) + 4u * t), "r"(pw[x][2 * i + c]) : "memory");
+            }
         }
         fence_async_shared();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0u) bar_arrive(p_full + 8 * (T & 1u));
+        if (lane < static_cast<uint32_t>(N)) bar_arrive(p_full + 8 * ((T + lane) & 1u));
+        T += N;
+        return true;
+      };
+      // With 64 rows the products are the longer and two tiles go together (what a step costs whatever its keys is a third of
+      // it); with 32 the memory is, and a tile does not wait for the next.
+      bool left = false;
+      for (int32_t j = seg.t0; j < seg.t1 && !left;) {
+        if (NR == 64 && j + 1 < seg.t1) {
+          left = !tiles(std::integral_constant<int, NR / 32>(), j);
+          j += 2;
+        } else {
+          left = !tiles(std::integral_constant<int, 1>(), j);
+          ++j;
+        }
       }
+      if (left) break;
       if (any_of_softmax(!ok)) break;
       have = take(k++, &next);
       if (any_of_softmax(!ok)) break;
@@ -612,31 +651,48 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
       if (any_of_softmax(!ok)) break;
       const int32_t L = lp.latent;
       if (seg.part < 0) {
+        // 32 dims of some rows at a time through shared memory (P's, which all products have read), so that four lanes write 64
+        // bytes of a row
+        constexpr int kOut = NR / 2;  // rows
+        const uint32_t stage = p_at + warp * (kOut * 64u);
         unsigned long long bad = 0ull;
         for (int32_t b = 0; b < p.blocks; ++b) {
-          const int32_t d = 128 * b + static_cast<int32_t>(tid);
-          for (int32_t c = 0; 16 * c < seg.nrows; ++c) {
-            uint32_t w[16];
-            if (live) {
-              tc_ld16(w, tmem + lanes + b * NR + 16 * c);
-            } else {
+          const int32_t d0 = 128 * b + 32 * static_cast<int32_t>(warp);
+          const bool mine = d0 + static_cast<int32_t>(lane) < L;
+          for (int32_t r1 = 0; r1 < seg.nrows; r1 += kOut) {
 #pragma unroll
-              for (int i = 0; i < 16; ++i) w[i] = 0u;
-            }
+            for (int c = 0; c < kOut / 16; ++c) {
+              uint32_t w[16];
+              if (live) {
+                tc_ld16(w, tmem + lanes + b * NR + r1 + 16 * c);
+              } else {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int32_t r = 16 * c + i;
-              if (r >= seg.nrows) break;
-              const int32_t qi = static_cast<int32_t>(a.group.quot(static_cast<uint32_t>(seg.row0 + r))), h = seg.row0 + r - qi * HQ;
-              uint16_t* out = reinterpret_cast<uint16_t*>(a.out + static_cast<int64_t>(seg.q0 + qi) * a.o_token + static_cast<int64_t>(h) * a.o_head);
-              const float v = live ? __uint_as_float(w[i]) * sh_inv[r] : 0.0f;
-              if (d < L) {
-                if (!(fabsf(v) < INFINITY)) bad |= 1ull << r;
-                out[d] = round16(v, a.bf16);
+                for (int i = 0; i < 16; ++i) w[i] = 0u;
+              }
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const float v = live ? __uint_as_float(w[i]) * sh_inv[r1 + 16 * c + i] : 0.0f;
+                if (mine && !(fabsf(v) < INFINITY)) bad |= 1ull << (r1 + 16 * c + i);
+                asm volatile("st.shared.u16 [%0], %1;" ::"r"(stage + (16 * c + i) * 64u + 2u * lane), "h"(round16(v, a.bf16)) : "memory");
               }
             }
+            __syncwarp();
+            if (d0 + 8 * static_cast<int32_t>(lane & 3u) < L) {
+#pragma unroll
+              for (int y = 0; y < kOut / 8; ++y) {
+                const int32_t r = r1 + 8 * y + static_cast<int32_t>(lane >> 2);
+                if (r < seg.nrows) {
+                  const int32_t qi = static_cast<int32_t>(a.group.quot(static_cast<uint32_t>(seg.row0 + r))), h = seg.row0 + r - qi * HQ;
+                  *reinterpret_cast<uint4*>(a.out + static_cast<int64_t>(seg.q0 + qi) * a.o_token + static_cast<int64_t>(h) * a.o_head + 2 * d0 +
+                                            16 * (lane & 3u)) = ld_shared16(stage + (8 * y + (lane >> 2)) * 64u + 16u * (lane & 3u));
+                }
+              }
+            }
+            __syncwarp();
           }
         }
+        // (rows behind the last have no sums)
+        if (seg.nrows < 64) bad &= (1ull << seg.nrows) - 1ull;
         const uint32_t lo = __reduce_or_sync(0xFFFFFFFFu, static_cast<uint32_t>(bad)), hi = __reduce_or_sync(0xFFFFFFFFu, static_cast<uint32_t>(bad >> 32));
         if (lane == 0u && (lo | hi) != 0u) atomicOr(sh_bad, static_cast<unsigned long long>(hi) << 32 | lo);
         sync_softmax();
