@@ -465,7 +465,8 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
         // The units are long there; their keys' bits and scales are read while S is waited for. (Threads that gave up a wait
         // go on to the barrier below.)
         uint32_t valid[N];
-        float s[N][16], kf[N][8], alpha[2] = {1.0f, 1.0f};  // scores, their keys' scales, factors of the rows' sums
+        [[maybe_unused]] float kf[N][8];
+        float s[N][16], alpha[2] = {1.0f, 1.0f};  // scores, their keys' scales, factors of the rows' sums
 #pragma unroll
         for (int x = 0; x < N; ++x) {
           ok = bar_wait(full + 8 * at.unit, at.phase, state) && ok;
@@ -967,14 +968,26 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
     while (take(k++, &seg)) {
       const int32_t* table = a.table + static_cast<int64_t>(seg.b) * a.table_stride;
       const int32_t n0 = seg.t0, n1 = seg.t1;
-      // lane = key: its page (of the last key that a row sees, for keys behind it), a unit ahead of its use
-      auto page_of = [&](int32_t unit) {
-        return __ldg(table + a.page.quot(static_cast<uint32_t>(min(unit * kLatKeys + static_cast<int32_t>(lane), seg.p_hi))));
-      };
-      int32_t next_id = n0 < n1 ? page_of(n0) : 0;
+      // 32 entries of the table, a lane each, from entry e0 on, and where the next 32 are needed them
+      const int32_t e_last = static_cast<int32_t>(a.page.quot(static_cast<uint32_t>(max(seg.p_hi, 0))));
+      auto entries = [&](int32_t e) { return __ldg(table + min(e + static_cast<int32_t>(lane), e_last)); };
+      int32_t e0 = static_cast<int32_t>(a.page.quot(static_cast<uint32_t>(n0 * kLatKeys))), ids = 0, ahead = 0;
+      if (n0 < n1) {
+        ids = entries(e0);
+        ahead = entries(e0 + 32);
+      }
       for (int32_t unit = n0; unit < n1 && ok; ++unit, ++n) {
-        const int32_t id = next_id, key = unit * kLatKeys + static_cast<int32_t>(lane);
-        if (unit + 1 < n1) next_id = page_of(unit + 1);
+        const int32_t key = unit * kLatKeys + static_cast<int32_t>(lane);
+        // lane = key: its page (of the last key that a row sees, for keys behind it)
+        const int32_t e = static_cast<int32_t>(a.page.quot(static_cast<uint32_t>(min(key, seg.p_hi))));
+        int32_t id = __shfl_sync(0xFFFFFFFFu, ids, e - e0);
+        if (__shfl_sync(0xFFFFFFFFu, e, 31) >= e0 + 32) {  // (at most 32 entries a unit: these and the next)
+          const int32_t other = __shfl_sync(0xFFFFFFFFu, ahead, e - e0 - 32);
+          if (e >= e0 + 32) id = other;
+          e0 += 32;
+          ids = ahead;
+          ahead = entries(e0 + 32);
+        }
         const bool want = key <= seg.p_hi, have = static_cast<uint32_t>(id) < static_cast<uint32_t>(a.num_pages), live = want && have;
         if (want && !have && rank == 0u) record_oob(a.err, static_cast<uint64_t>(seg.b));
         const uint32_t bits = __ballot_sync(0xFFFFFFFFu, live);
