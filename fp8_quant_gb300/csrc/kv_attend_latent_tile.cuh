@@ -93,7 +93,7 @@ struct LatentSeg {
 template <int FMT, int NR>
 struct LatentSmem {  // units, raw units, queries, weights, and
   static constexpr int kP = NR * 128;
-  static constexpr int kBars = 2 * kLatMaxUnits + 2 * kLatMaxRaws + 2 * kLatScores + 12;
+  static constexpr int kBars = 2 * kLatMaxUnits + 2 * kLatMaxRaws + 2 * kLatScores + 15;
   static __host__ __device__ constexpr int unit(int chunks) { return kLatKeys * 128 * chunks; }
   static __host__ __device__ constexpr int raw(int chunks) { return kLatKeys * 64 * chunks; }
   // chunks of the queries that are in TMEM, beside O^T and the scores; the others are in shared memory
@@ -103,7 +103,7 @@ struct LatentSmem {  // units, raw units, queries, weights, and
                        kOffQf = kOffInv + NR * 4, kOffMisc = kOffQf + NR * 4, kOffValid = kOffMisc + 64,
                        kOffRawValid = kOffValid + kLatMaxUnits * 4, kOffScale = kOffRawValid + kLatMaxRaws * 4;
   static __host__ __device__ constexpr int total(int chunks, int units, int raws) {
-    return units * (unit(chunks) + (FMT == KV_CACHE_SRC ? 0 : kLatKeys * 4)) + raws * (raw(chunks) + kLatKeys * 4) + q_bytes(chunks) + kP + kOffScale;
+    return units * (unit(chunks) + (FMT == KV_CACHE_SRC ? 0 : 2 * kLatKeys * 4)) + raws * (raw(chunks) + kLatKeys * 4) + q_bytes(chunks) + kP + kOffScale;
   }
 };
 static_assert(sizeof(LatentSeg) <= 64, "segments");
@@ -135,10 +135,13 @@ __device__ __forceinline__ int64_t latent_units(const LatentTileParams& p, int32
 
 // A share for each CTA (or pair), all of a size. (Smaller shares behind them, for those that are done first, cost more in
 // queries brought in and parts written than they balance.)
+__device__ __forceinline__ int64_t quotient(int64_t x, int64_t d) {  // of non-negative numbers; most are short
+  return ((x | d) >> 32) == 0 ? static_cast<int64_t>(static_cast<uint32_t>(x) / static_cast<uint32_t>(d)) : x / d;
+}
 __device__ __forceinline__ ShareLevel latent_cut(int64_t total, int32_t ctas, int32_t min_steps, int32_t* shares) {
-  int64_t each = (total + ctas - 1) / ctas;
+  int64_t each = quotient(total + ctas - 1, ctas);
   if (each < min_steps) each = min_steps;
-  *shares = static_cast<int32_t>((total + each - 1) / each);
+  *shares = static_cast<int32_t>(quotient(total + each - 1, each));
   return ShareLevel{0, static_cast<int32_t>(each), 0};
 }
 
@@ -251,7 +254,7 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
   const uint32_t small = p_at + S::kP;
   uint8_t* const small_ptr = smem_raw + (small - ring);
   const uint32_t full = small + S::kOffBars, empty = full + 8 * kLatMaxUnits, raw_full = empty + 8 * kLatMaxUnits,
-                 raw_empty = raw_full + 8 * kLatMaxRaws, q_full = raw_empty + 8 * kLatMaxRaws, s_full = q_full + 8,
+                 raw_empty = raw_full + 8 * kLatMaxRaws, q_full = raw_empty + 8 * kLatMaxRaws, s_full = q_full + 32,
                  s_free = s_full + 8 * kLatScores, p_full = s_free + 8 * kLatScores, pv_done = p_full + 16, seg_full = pv_done + 16,
                  seg_empty = seg_full + 16, done = seg_empty + 16;
   LatentSeg* const segs = reinterpret_cast<LatentSeg*>(small_ptr + S::kOffSegs);
@@ -261,6 +264,7 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
   uint32_t* const sh_valid = reinterpret_cast<uint32_t*>(small_ptr + S::kOffValid);  // of a unit's keys, a bit each
   uint32_t* const sh_raw_valid = reinterpret_cast<uint32_t*>(small_ptr + S::kOffRawValid);
   float* const sh_scale = reinterpret_cast<float*>(small_ptr + S::kOffScale);        // [units][32], then [raws][32]
+  float* const sh_log = sh_scale + (units + raws) * kLatKeys;                        // [units][32]: of the scales
   WaitState* const state = reinterpret_cast<WaitState*>(small_ptr + S::kOffMisc);
   uint32_t* const sh_tmem = reinterpret_cast<uint32_t*>(small_ptr + S::kOffMisc + 16);
   unsigned long long* const sh_bad = reinterpret_cast<unsigned long long*>(small_ptr + S::kOffMisc + 24);
@@ -282,10 +286,10 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
       bar_init(raw_full + 8 * i, 33);
       bar_init(raw_empty + 8 * i, kLatConverters);
     }
-    bar_init(q_full, 4);
+    for (int i = 0; i < 4; ++i) bar_init(q_full + 8 * i, 4);
     for (int i = 0; i < kLatScores; ++i) {
       bar_init(s_full + 8 * i, 1);
-      bar_init(s_free + 8 * i, NR / 16);
+      bar_init(s_free + 8 * i, 4);
     }
     for (int i = 0; i < 2; ++i) {
       bar_init(p_full + 8 * i, 4);
@@ -348,8 +352,9 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
       const int32_t x = s.row0 + min(r, s.last), qi = static_cast<int32_t>(a.group.quot(static_cast<uint32_t>(x)));
       return a.q + static_cast<int64_t>(s.q0 + qi) * a.q_token + static_cast<int64_t>(x - qi * HQ) * a.q_head;
     };
+    uint32_t items = 0u;  // that have tiles
     auto load_q = [&](const LatentSeg& s) {
-      constexpr int kIn = S::kInTmem, kAt = 3;  // chunks in TMEM; chunks in flight
+      constexpr int kIn = S::kInTmem, kAt = FMT == KV_CACHE_SRC && NR == 32 ? 3 : 1;  // chunks in TMEM; chunks in flight
       const bool shift = FMT != KV_CACHE_SRC && a.bf16;
       auto shifted = [](uint32_t z, float f) {
         const float2 v = widen2<true>(z);
@@ -440,7 +445,7 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0u) bar_arrive(q_full);
+      if (lane == 0u) bar_arrive(q_full + 8 * (items++ & 3u));
     };
     uint32_t k = 0u, T = 0u;  // segments and tiles that went by
     Place at{0u, 0u}, buf{0u, 0u};  // of units, and of scores
@@ -465,8 +470,8 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
         // The units are long there; their keys' bits and scales are read while S is waited for. (Threads that gave up a wait
         // go on to the barrier below.)
         uint32_t valid[N];
-        [[maybe_unused]] float kf[N][8];
-        float s[N][16], alpha[2] = {1.0f, 1.0f};  // scores, their keys' scales, factors of the rows' sums
+        [[maybe_unused]] float kf[N][8], lv[N][8];  // the keys' scales, and their binary logarithms
+        float s[N][16], alpha[2] = {1.0f, 1.0f};  // scores, factors of the rows' sums
 #pragma unroll
         for (int x = 0; x < N; ++x) {
           ok = bar_wait(full + 8 * at.unit, at.phase, state) && ok;
@@ -477,6 +482,9 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
               const float2 f = *reinterpret_cast<const float2*>(sh_scale + at.unit * kLatKeys + 8 * i + 2 * t);
               kf[x][2 * i] = f.x;
               kf[x][2 * i + 1] = f.y;
+              const float2 v = *reinterpret_cast<const float2*>(sh_log + at.unit * kLatKeys + 8 * i + 2 * t);
+              lv[x][2 * i] = v.x;
+              lv[x][2 * i + 1] = v.y;
             }
           }
           next_unit(&at);
@@ -491,8 +499,9 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
             tc_ld_rows(s[x], tm_s + kLatKeys * buf.unit + lanes);
             tc_fence_before();
             __syncwarp();
-            if (lane == 0u) bar_arrive(s_free + 8 * buf.unit);
           }
+          // (by warps without rows too: one that is late with an item's outputs must not miss a phase of s_full)
+          if (lane == 0u) bar_arrive(s_free + 8 * buf.unit);
           if (++buf.unit == kLatScores) {
             buf.unit = 0u;
             buf.phase ^= 1u;
@@ -504,7 +513,7 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
           for (int x = 0; x < N; ++x) {
             if constexpr (FMT != KV_CACHE_SRC) {
 #pragma unroll
-              for (int i = 0; i < 16; ++i) s[x][i] *= kf[x][2 * (i / 4) + (i & 1)] * rs[(i >> 1) & 1];
+              for (int i = 0; i < 16; ++i) s[x][i] *= kf[x][2 * (i / 4) + (i & 1)];
             }
             if ((j + x) * kLatKeys + kLatKeys - 1 > p_lo || valid[x] != ~0u) {
 #pragma unroll
@@ -518,11 +527,6 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
                     if ((see >> (8 * i + y) & 1u) == 0u) s[x][4 * i + 2 * c + y] = -INFINITY;
               }
             }
-            float lv[8];
-            if constexpr (FMT != KV_CACHE_SRC) {
-#pragma unroll
-              for (int i = 0; i < 8; ++i) lv[i] = fmaxf(lg2_fast(fabsf(kf[x][i])), -100.0f);
-            }
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               float z[2] = {-INFINITY, -INFINITY};
@@ -530,7 +534,7 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
               for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int y = 0; y < 2; ++y)
-                  z[y] = fmaxf(z[y], FMT == KV_CACHE_SRC ? s[x][4 * i + 2 * c + y] : s[x][4 * i + 2 * c + y] + lv[2 * i + y]);
+                  z[y] = fmaxf(z[y], FMT == KV_CACHE_SRC ? s[x][4 * i + 2 * c + y] : __fmaf_rn(s[x][4 * i + 2 * c + y], rs[c], lv[x][2 * i + y]));
               top[c] = fmaxf(top[c], fmaxf(z[0], z[1]));
             }
           }
@@ -569,7 +573,7 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 float2 z = make_float2(s[x][4 * i + 2 * c], s[x][4 * i + 2 * c + 1]);
-                if constexpr (FMT == KV_CACHE_SRC) z = fma2(z, rs[c], -ref); else z = add2(z, make_float2(-ref, -ref));
+                z = fma2(z, rs[c], -ref);
                 float2 e = make_float2(exp2_fast(z.x), exp2_fast(z.y));
                 sum[i & 1] = add2(sum[i & 1], e);
                 if constexpr (FMT != KV_CACHE_SRC) {
@@ -623,7 +627,7 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
       // it); with 32 the memory is, and a tile does not wait for the next.
       bool left = false;
       for (int32_t j = seg.t0; j < seg.t1 && !left;) {
-        if (NR == 64 && j + 1 < seg.t1) {
+        if (NR == 64 && (FMT != KV_CACHE_SRC || seg.nq * HQ > 4 * NR) && j + 1 < seg.t1) {
           left = !tiles(std::integral_constant<int, NR / 32>(), j);
           j += 2;
         } else {
@@ -723,19 +727,23 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
       } else {
         const int64_t at = static_cast<int64_t>(seg.part) * p.part_rows;
         const int32_t width = 128 * p.blocks;
-        for (int32_t b = 0; b < p.blocks; ++b)
-          for (int32_t c = 0; 16 * c < seg.nrows; ++c) {
-            uint32_t w[16];
+        for (int32_t c = 0; 32 * c < seg.nrows; ++c) {
+          float* const to = p.part_o + (at + 32 * c) * width + tid;
+          for (int32_t b = 0; b < p.blocks; ++b) {
+            uint32_t w[32];
             if (live) {
-              tc_ld16(w, tmem + lanes + b * NR + 16 * c);
+              tc_ld32(w, tmem + lanes + b * NR + 32 * c);
             } else {
 #pragma unroll
-              for (int i = 0; i < 16; ++i) w[i] = 0u;
+              for (int i = 0; i < 32; ++i) w[i] = 0u;
             }
+            float* row = to + 128 * b;
+            const int32_t rows = seg.nrows - 32 * c;
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (16 * c + i < seg.nrows) p.part_o[(at + 16 * c + i) * width + 128 * b + tid] = __uint_as_float(w[i]);
+            for (int i = 0; i < 32; ++i, row += width)
+              if (i < rows) *row = __uint_as_float(w[i]);
           }
+        }
         if (has_rows && t == 0u) {
 #pragma unroll
           for (int c = 0; c < 2; ++c)
@@ -770,7 +778,10 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
       uint32_t items = 0u;
       while (take(k++, &seg)) {
         if (seg.t1 <= seg.t0) continue;
-        wait(q_full, items++ & 1u);
+        // (four barriers in turn: a warp without a tile of an item can be late, but not by more items than the queue of
+        // segments holds, so that no phase passes it by)
+        wait(q_full + 8 * (items & 3u), (items >> 2) & 1u);
+        ++items;
         for (int32_t j = seg.t0; j < seg.t1; ++j, ++T) {
           if ((T & 1u) == turn) {
             const uint32_t u = same(at.unit | (T % kLatScores) << 8), un = u & 255u, buf = u >> 8, d = s_at + kLatKeys * buf;
@@ -916,7 +927,7 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
         const AttendSeq seq = attend_seq(a, s.b, false);
         const LatentGeom geom = latent_geom<NR>(p, seq);
         const int32_t unit = p.split ? geom.steps : 1;
-        int32_t item = static_cast<int32_t>(local / unit);
+        int32_t item = static_cast<int32_t>(quotient(local, unit));
         const int32_t s_in = static_cast<int32_t>(local - static_cast<int64_t>(item) * unit);
         const int32_t s_out = static_cast<int32_t>(min(static_cast<int64_t>(unit), s_in + (end - pos)));
         pos += s_out - s_in;
@@ -934,6 +945,14 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
         s.t1 = p.split ? min(s_out, tiles) : tiles;
         s.part = s_out - s_in == unit ? -1 : (2 * share + (s_in == 0 ? 1 : 0)) * p.cluster + static_cast<int32_t>(rank);
         publish(s);
+        if (NR == 32 && s.t1 > s.t0) {  // its queries into L2: they are wanted when the item before ends
+          const int32_t lines = (a.head_dim * 2 + 127) / 128;
+          for (int32_t i = static_cast<int32_t>(lane); i < s.nrows * lines; i += 32) {
+            const int32_t r = i / lines, qi = static_cast<int32_t>(a.group.quot(static_cast<uint32_t>(s.row0 + r)));
+            prefetch_l2_line(a.q + static_cast<int64_t>(s.q0 + qi) * a.q_token + static_cast<int64_t>(s.row0 + r - qi * HQ) * a.q_head +
+                             min(128 * (i - r * lines), a.head_dim * 2 - 1));
+          }
+        }
       }
       share += ctas;
     }
@@ -944,7 +963,6 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
     // ======================================================================================
     // the keys, a unit of 32 at a time
     // ======================================================================================
-    auto same = [](uint32_t x) { return __reduce_or_sync(0xFFFFFFFFu, x); };  // in a uniform register
     uint32_t k = 0u, n = 0u;  // units that went by
     Place at{0u, 0u};         // in the ring of units, or of raw ones
     const uint32_t places = FMT == KV_CACHE_SRC ? units : raws;
@@ -995,10 +1013,9 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
         // boxes of `box` groups of eight keys, which share a page; of a pair's CTAs each brings half of the unit
         const bool boxes = p.box > 0 && bits == ~0u;
         const int32_t g0 = pair ? 2 * static_cast<int32_t>(rank) : 0;
-        const int32_t page0 = static_cast<int32_t>(same(static_cast<uint32_t>(__shfl_sync(0xFFFFFFFFu, id, 8 * g0))));
-        const int32_t in0 = static_cast<int32_t>(same(__shfl_sync(0xFFFFFFFFu, off, 8 * g0)) >> 3);
-        const uint32_t bar = same(full_at + 8 * at.unit), part = FMT == KV_CACHE_SRC ? group_bytes : group_bytes / 2u;  // of eight keys
-        const uint32_t dst = same(FMT == KV_CACHE_SRC ? ring + at.unit * unit_bytes : raw_ring + at.unit * raw_bytes);
+        const int32_t page0 = __shfl_sync(0xFFFFFFFFu, id, 8 * g0), in0 = static_cast<int32_t>(__shfl_sync(0xFFFFFFFFu, off, 8 * g0) >> 3);
+        const uint32_t bar = full_at + 8 * at.unit, part = FMT == KV_CACHE_SRC ? group_bytes : group_bytes / 2u;  // of eight keys
+        const uint32_t dst = FMT == KV_CACHE_SRC ? ring + at.unit * unit_bytes : raw_ring + at.unit * raw_bytes;
         // (nothing that can be known before stands between a free unit and its boxes)
         if (n >= places) {
           if (waiting > 0u && !__all_sync(0xFFFFFFFFu, bar_try(empty_at + 8 * at.unit, at.phase ^ 1u))) hand_over(true);
@@ -1014,8 +1031,7 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
             tma_rows(dst + g0 * part, &p.map, bar, 0, in0, page0, pair);
           } else {
             for (int32_t g = g0; g < (pair ? g0 + 2 : 4); g += p.box) {
-              const int32_t page = static_cast<int32_t>(same(static_cast<uint32_t>(__shfl_sync(0xFFFFFFFFu, id, 8 * g))));
-              const int32_t in_page = static_cast<int32_t>(same(__shfl_sync(0xFFFFFFFFu, off, 8 * g)) >> 3);
+              const int32_t page = __shfl_sync(0xFFFFFFFFu, id, 8 * g), in_page = static_cast<int32_t>(__shfl_sync(0xFFFFFFFFu, off, 8 * g) >> 3);
               for (int32_t c = 0; c < p.chunks; c += p.box_chunks)
                 tma_rows(dst + g * part + c * (part / static_cast<uint32_t>(p.chunks)), &p.map, bar, 64 * c, in_page, page, pair);
             }
@@ -1115,6 +1131,7 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
         }
         if (w == 0u) {
           sh_scale[at.unit * kLatKeys + lane] = scale;
+          sh_log[at.unit * kLatKeys + lane] = fmaxf(lg2_fast(fabsf(scale)), -100.0f);
           if (lane == 0u) sh_valid[at.unit] = bits;
         }
         fence_async_shared();

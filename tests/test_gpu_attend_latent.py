@@ -313,3 +313,20 @@ def test_an_append_and_the_attention_that_reads_it(fmt):
     # keys and as values
     assert off.item() <= (2.0 ** -6 if fmt is None else 2.0 ** -3)
     assert kv.kv_error_poll(layer.err)[1] == 0
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("HQ", [16, 32, 64])
+def test_many_short_items_a_share(HQ, fmt):
+    """Shares that hold the end of one sequence, whole ones of a tile, and the beginning of another; call after call. A warp
+    that is late with an item's outputs must find the next items' scores."""
+    rng = np.random.default_rng(5)
+    lens = [int(n) for pair in zip(rng.integers(900, 2500, 20), rng.integers(0, 70, 20)) for n in pair]
+    p = LatentProblem(lens, [1] * len(lens), HQ, 512, 64, fmt=fmt, seed=40, page=64)
+    d = p.tensors("cuda")
+    work = torch.zeros(1 << 25, dtype=torch.uint8, device="cuda")
+    first = p.attend(d, work=work, q_start=None)
+    p.check(first)
+    for _ in range(50):
+        outs = [p.attend(d, work=work, q_start=None) for _ in range(4)]
+        assert all(torch.equal(first, o) for o in outs)
