@@ -100,7 +100,7 @@ struct LatentSmem {  // units, raw units, queries, weights, and
   static constexpr int kInTmem = NR == 64 ? 5 : 9;
   static __host__ __device__ constexpr int q_bytes(int chunks) { return chunks > kInTmem ? (chunks - kInTmem) * NR * 128 : 0; }
   static constexpr int kOffBars = 0, kOffSegs = (kBars * 8 + 15) / 16 * 16, kOffAlpha = kOffSegs + 2 * 64, kOffInv = kOffAlpha + NR * 4,
-                       kOffQf = kOffInv + NR * 4, kOffMisc = kOffQf + NR * 4, kOffValid = kOffMisc + 64,
+                       kOffQf = kOffInv + NR * 4, kOffTop = kOffQf + NR * 4, kOffMisc = kOffTop + 64 * 4, kOffValid = kOffMisc + 64,
                        kOffRawValid = kOffValid + kLatMaxUnits * 4, kOffScale = kOffRawValid + kLatMaxRaws * 4;
   static __host__ __device__ constexpr int total(int chunks, int units, int raws) {
     return units * (unit(chunks) + (FMT == KV_CACHE_SRC ? 0 : 2 * kLatKeys * 4)) + raws * (raw(chunks) + kLatKeys * 4) + q_bytes(chunks) + kP + kOffScale;
@@ -145,7 +145,7 @@ __device__ __forceinline__ ShareLevel latent_cut(int64_t total, int32_t ctas, in
   return ShareLevel{0, static_cast<int32_t>(each), 0};
 }
 
-// 16 lanes x 32 columns over the warp: thread (g, t) = (lane / 4, lane % 4) gets columns 8 i + 2 t, + 1 of
+// 16 lanes x 32 (or 16) columns over the warp: thread (g, t) = (lane / 4, lane % 4) gets columns 8 i + 2 t, + 1 of
 // rows g (r[4 i], r[4 i + 1]) and g + 8 (r[4 i + 2], r[4 i + 3]).
 __device__ __forceinline__ void tc_ld_rows(float (&s)[16], uint32_t addr) {
   uint32_t r[16];
@@ -156,6 +156,13 @@ __device__ __forceinline__ void tc_ld_rows(float (&s)[16], uint32_t addr) {
                  "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]) : "r"(addr) : "memory");
 #pragma unroll
   for (int i = 0; i < 16; ++i) s[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tc_ld_rows(float (&s)[8], uint32_t addr) {
+  uint32_t r[8];
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\ttcgen05.wait::ld.sync.aligned;"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]) : "r"(addr) : "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s[i] = __uint_as_float(r[i]);
 }
 
 // The same, stored.
@@ -261,6 +268,7 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
   float* const sh_alpha = reinterpret_cast<float*>(small_ptr + S::kOffAlpha);   // [NR]
   float* const sh_inv = reinterpret_cast<float*>(small_ptr + S::kOffInv);
   float* const sh_qf = reinterpret_cast<float*>(small_ptr + S::kOffQf);
+  float* const sh_top = reinterpret_cast<float*>(small_ptr + S::kOffTop);       // [64 / NR][NR]
   uint32_t* const sh_valid = reinterpret_cast<uint32_t*>(small_ptr + S::kOffValid);  // of a unit's keys, a bit each
   uint32_t* const sh_raw_valid = reinterpret_cast<uint32_t*>(small_ptr + S::kOffRawValid);
   float* const sh_scale = reinterpret_cast<float*>(small_ptr + S::kOffScale);        // [units][32], then [raws][32]
@@ -341,8 +349,12 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
     // the softmax
     // ======================================================================================
     const uint32_t g = lane >> 2, t = lane & 3u;
-    const bool has_rows = warp < NR / 16;
-    const int32_t r0 = static_cast<int32_t>(16u * warp + g);  // and r0 + 8
+    // With 32 rows the other half of the 64 that a product has anyway are the same ones again: warps 2 and 3 take the last 16
+    // keys of each tile.
+    constexpr int kHalves = 64 / NR, kCols = kLatKeys / kHalves;  // keys of a warp
+    const uint32_t half = NR == 64 ? 0u : warp >> 1;
+    const int32_t r0 = static_cast<int32_t>(16u * (warp & (NR / 16 - 1u)) + g);  // and r0 + 8
+    const bool first = t == 0u && half == 0u;  // that writes what a row has once
     const uint32_t lanes = warp << 21;
     const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;  // the maximum is taken before the scale
     constexpr float kSmall = kBF16 ? 0.0f : 7.0f;
@@ -360,65 +372,63 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
         const float2 v = widen2<true>(z);
         return pack2(v.x * f, v.y * f, false);
       };
-      if (has_rows) {
-        // thread (g, t): dims 16 i + 4 t .. + 3 of each chunk of rows g and g + 8
-        const uint8_t* src[2] = {row_of(s, r0) + 8 * t, row_of(s, r0 + 8) + 8 * t};
-        const bool live[2] = {r0 < s.nrows, r0 + 8 < s.nrows};
-        auto piece = [&](int c, int chunk, int i) {
-          uint2 w = make_uint2(0u, 0u);
-          if (live[c] && 4 * chunk + i < p.ksteps) w = __ldg(reinterpret_cast<const uint2*>(src[c] + 128 * chunk + 32 * i));
-          return w;
-        };
-        float f[2] = {1.0f, 1.0f};
-        if (shift) {
+      // thread (g, t): dims 16 i + 4 t .. + 3 of each chunk of rows g and g + 8
+      const uint8_t* src[2] = {row_of(s, r0) + 8 * t, row_of(s, r0 + 8) + 8 * t};
+      const bool live[2] = {r0 < s.nrows, r0 + 8 < s.nrows};
+      auto piece = [&](int c, int chunk, int i) {
+        uint2 w = make_uint2(0u, 0u);
+        if (live[c] && 4 * chunk + i < p.ksteps) w = __ldg(reinterpret_cast<const uint2*>(src[c] + 128 * chunk + 32 * i));
+        return w;
+      };
+      float f[2] = {1.0f, 1.0f};
+      if (shift) {
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t m = 0u;
+        for (int c = 0; c < 2; ++c) {
+          uint32_t m = 0u;
 #pragma unroll 3
-            for (int32_t chunk = 0; chunk < p.chunks; ++chunk)
+          for (int32_t chunk = 0; chunk < p.chunks; ++chunk)
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const uint2 w = piece(c, chunk, i);
-                m = absmax_pair<true>(absmax_pair<true>(m, w.x), w.y);
-              }
-            uint32_t e = __float_as_uint(absmax_pair_value<true>(m));
-            e = max(e, __shfl_xor_sync(0xFFFFFFFFu, e, 1));
-            e = max(e, __shfl_xor_sync(0xFFFFFFFFu, e, 2)) >> 23;
-            f[c] = __uint_as_float(min(254u, 267u - e) << 23);
-          }
+            for (int i = 0; i < 4; ++i) {
+              const uint2 w = piece(c, chunk, i);
+              m = absmax_pair<true>(absmax_pair<true>(m, w.x), w.y);
+            }
+          uint32_t e = __float_as_uint(absmax_pair_value<true>(m));
+          e = max(e, __shfl_xor_sync(0xFFFFFFFFu, e, 1));
+          e = max(e, __shfl_xor_sync(0xFFFFFFFFu, e, 2)) >> 23;
+          f[c] = __uint_as_float(min(254u, 267u - e) << 23);
         }
-        if constexpr (FMT != KV_CACHE_SRC) {
-          if (t == 0u) {
-            sh_qf[r0] = f[0];
-            sh_qf[r0 + 8] = f[1];
-          }
-        }
-#pragma unroll 1
-        for (int32_t c0 = 0; c0 < min(kIn, p.chunks); c0 += kAt) {
-          uint2 w[kAt][2][4];
-#pragma unroll
-          for (int y = 0; y < kAt; ++y)
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) w[y][c][i] = piece(c, c0 + y, i);
-#pragma unroll
-          for (int y = 0; y < kAt; ++y) {
-            if (c0 + y >= kIn) break;
-            uint32_t r[16];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                const uint2 z = w[y][c][i];
-                r[4 * i + 2 * c] = (shift ? shifted(z.x, f[c]) : z.x) ^ flip;
-                r[4 * i + 2 * c + 1] = (shift ? shifted(z.y, f[c]) : z.y) ^ flip;
-              }
-            tc_st_rows(tm_q + 32 * (c0 + y) + lanes, r);
-          }
-        }
-        tc_wait_st();
       }
+      if constexpr (FMT != KV_CACHE_SRC) {
+        if (t == 0u) {
+          sh_qf[r0] = f[0];
+          sh_qf[r0 + 8] = f[1];
+        }
+      }
+#pragma unroll 1
+      for (int32_t c0 = 0; c0 < min(kIn, p.chunks); c0 += kAt) {
+        uint2 w[kAt][2][4];
+#pragma unroll
+        for (int y = 0; y < kAt; ++y)
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[y][c][i] = piece(c, c0 + y, i);
+#pragma unroll
+        for (int y = 0; y < kAt; ++y) {
+          if (c0 + y >= kIn) break;
+          uint32_t r[16];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const uint2 z = w[y][c][i];
+              r[4 * i + 2 * c] = (shift ? shifted(z.x, f[c]) : z.x) ^ flip;
+              r[4 * i + 2 * c + 1] = (shift ? shifted(z.y, f[c]) : z.y) ^ flip;
+            }
+          tc_st_rows(tm_q + 32 * (c0 + y) + lanes, r);
+        }
+      }
+      tc_wait_st();
       if (kIn < kLatMaxChunks && p.chunks > kIn) {  // the last chunks to shared memory: a warp has NR / 4 rows, 16 bytes a lane
         constexpr int kRows = NR / 4;
         if (shift) sync_softmax();  // sh_qf
@@ -461,7 +471,7 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         rs[c] = fabsf(a.scale_log2);
-        if constexpr (FMT != KV_CACHE_SRC) rs[c] *= has_rows ? __fdiv_rn(1.0f, sh_qf[r0 + 8 * c]) : 1.0f;
+        if constexpr (FMT != KV_CACHE_SRC) rs[c] *= __fdiv_rn(1.0f, sh_qf[r0 + 8 * c]);
         if (rs[c] == 0.0f) rs[c] = __uint_as_float(1u);  // hidden scores (-inf) must stay -inf
       }
       // N tiles from j on; false: a wait ran out, and all leave together
@@ -470,121 +480,122 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
         // The units are long there; their keys' bits and scales are read while S is waited for. (Threads that gave up a wait
         // go on to the barrier below.)
         uint32_t valid[N];
-        [[maybe_unused]] float kf[N][8], lv[N][8];  // the keys' scales, and their binary logarithms
-        float s[N][16], alpha[2] = {1.0f, 1.0f};  // scores, factors of the rows' sums
+        [[maybe_unused]] float kf[N][kCols / 4], lv[N][kCols / 4];  // the keys' scales, and their binary logarithms
+        float s[N][kCols / 2], alpha[2] = {1.0f, 1.0f};             // scores, factors of the rows' sums
 #pragma unroll
         for (int x = 0; x < N; ++x) {
           ok = bar_wait(full + 8 * at.unit, at.phase, state) && ok;
-          valid[x] = sh_valid[at.unit];
+          valid[x] = sh_valid[at.unit] >> (kCols * half);
           if constexpr (FMT != KV_CACHE_SRC) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float2 f = *reinterpret_cast<const float2*>(sh_scale + at.unit * kLatKeys + 8 * i + 2 * t);
+            for (int i = 0; i < kCols / 8; ++i) {
+              const uint32_t key = at.unit * kLatKeys + kCols * half + 8 * i + 2 * t;
+              const float2 f = *reinterpret_cast<const float2*>(sh_scale + key), v = *reinterpret_cast<const float2*>(sh_log + key);
               kf[x][2 * i] = f.x;
               kf[x][2 * i + 1] = f.y;
-              const float2 v = *reinterpret_cast<const float2*>(sh_log + at.unit * kLatKeys + 8 * i + 2 * t);
               lv[x][2 * i] = v.x;
               lv[x][2 * i + 1] = v.y;
             }
           }
           next_unit(&at);
         }
-        bool grew = false;
 #pragma unroll
         for (int x = 0; x < N; ++x) {
           ok = bar_wait(s_full + 8 * buf.unit, buf.phase, state) && ok;
           __syncwarp();
           tc_fence_after();
-          if (has_rows) {
-            tc_ld_rows(s[x], tm_s + kLatKeys * buf.unit + lanes);
-            tc_fence_before();
-            __syncwarp();
-          }
-          // (by warps without rows too: one that is late with an item's outputs must not miss a phase of s_full)
+          tc_ld_rows(s[x], tm_s + kLatKeys * buf.unit + kCols * half + lanes);
+          tc_fence_before();
+          __syncwarp();
           if (lane == 0u) bar_arrive(s_free + 8 * buf.unit);
           if (++buf.unit == kLatScores) {
             buf.unit = 0u;
             buf.phase ^= 1u;
           }
         }
-        if (has_rows) {
-          float top[2] = {-INFINITY, -INFINITY};
+        float top[2] = {-INFINITY, -INFINITY};  // of the thread's own
 #pragma unroll
-          for (int x = 0; x < N; ++x) {
-            if constexpr (FMT != KV_CACHE_SRC) {
+        for (int x = 0; x < N; ++x) {
+          if constexpr (FMT != KV_CACHE_SRC) {
 #pragma unroll
-              for (int i = 0; i < 16; ++i) s[x][i] *= kf[x][2 * (i / 4) + (i & 1)];
-            }
-            if ((j + x) * kLatKeys + kLatKeys - 1 > p_lo || valid[x] != ~0u) {
-#pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                const int32_t n = pos[c] - (j + x) * kLatKeys + 1;  // the first n keys
-                const uint32_t see = ((n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u) & valid[x]) >> (2 * t);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                  for (int y = 0; y < 2; ++y)
-                    if ((see >> (8 * i + y) & 1u) == 0u) s[x][4 * i + 2 * c + y] = -INFINITY;
-              }
-            }
+            for (int i = 0; i < kCols / 2; ++i) s[x][i] *= kf[x][2 * (i / 4) + (i & 1)];
+          }
+          if ((j + x) * kLatKeys + kLatKeys - 1 > p_lo || valid[x] != ~0u >> (32 - kCols)) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              float z[2] = {-INFINITY, -INFINITY};
+              const int32_t n = pos[c] - ((j + x) * kLatKeys + kCols * static_cast<int32_t>(half)) + 1;  // the first n keys
+              const uint32_t see = ((n >= kCols ? ~0u : n <= 0 ? 0u : (1u << n) - 1u) & valid[x]) >> (2 * t);
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
+              for (int i = 0; i < kCols / 8; ++i)
 #pragma unroll
                 for (int y = 0; y < 2; ++y)
-                  z[y] = fmaxf(z[y], FMT == KV_CACHE_SRC ? s[x][4 * i + 2 * c + y] : __fmaf_rn(s[x][4 * i + 2 * c + y], rs[c], lv[x][2 * i + y]));
-              top[c] = fmaxf(top[c], fmaxf(z[0], z[1]));
+                  if ((see >> (8 * i + y) & 1u) == 0u) s[x][4 * i + 2 * c + y] = -INFINITY;
             }
           }
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float z[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int i = 0; i < kCols / 8; ++i)
+#pragma unroll
+              for (int y = 0; y < 2; ++y)
+                z[y] = fmaxf(z[y], FMT == KV_CACHE_SRC ? s[x][4 * i + 2 * c + y] : __fmaf_rn(s[x][4 * i + 2 * c + y], rs[c], lv[x][2 * i + y]));
+            top[c] = fmaxf(top[c], fmaxf(z[0], z[1]));
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) top[c] = FMT == KV_CACHE_SRC ? __fmaf_rn(top[c], rs[c], -kSmall) : top[c] - kSmall;
+        // A maximum that grew little is kept (the weights stay below 2^(kSmall + 8)), so that a tile seldom asks for the
+        // others' scores: the rows' new maxima, and O^T, which is all warps', are brought up to date when some row grew.
+        auto grows = [&](int c) { return top[c] > m[c] + 8.0f || (m[c] == -INFINITY && top[c] > m[c]); };
+        const bool renew = any_of_softmax(grows(0) || grows(1) || !ok), rescale = renew && j > seg.t0;
+        if (renew) {
 #pragma unroll
           for (int o = 1; o < 4; o <<= 1)
 #pragma unroll
             for (int c = 0; c < 2; ++c) top[c] = fmaxf(top[c], __shfl_xor_sync(0xFFFFFFFFu, top[c], o));
+          if constexpr (kHalves > 1) {
+            if (t == 0u) {
+              sh_top[NR * half + r0] = top[0];
+              sh_top[NR * half + r0 + 8] = top[1];
+            }
+            sync_softmax();
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            top[c] = FMT == KV_CACHE_SRC ? __fmaf_rn(top[c], rs[c], -kSmall) : top[c] - kSmall;
-            // a maximum that grew little is kept (the weights stay below 2^(kSmall + 8))
-            if (top[c] > m[c] + 8.0f || (m[c] == -INFINITY && top[c] > m[c])) {
+            for (int c = 0; c < 2; ++c) top[c] = fmaxf(top[c], sh_top[NR * (half ^ 1u) + r0 + 8 * c]);
+          }
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            if (grows(c)) {
               alpha[c] = exp2_fast(m[c] - top[c]);
               m[c] = top[c];
-              grew = true;
             }
-          }
-        }
-        // O^T is all warps': whether any row of the CTA grew
-        const bool rescale = any_of_softmax((grew && j > seg.t0) || !ok);
-        if (rescale) {
-          if (has_rows && t == 0u) {
+          if (first) {
             sh_alpha[r0] = alpha[0];
             sh_alpha[r0 + 8] = alpha[1];
           }
           if (any_of_softmax(!ok)) return false;
         }
-        uint32_t pw[N][8];
-        if (has_rows) {
+        uint32_t pw[N][kCols / 4];
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const float ref = m[c] == -INFINITY ? 0.0f : m[c];
-            float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+        for (int c = 0; c < 2; ++c) {
+          const float ref = m[c] == -INFINITY ? 0.0f : m[c];
+          float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-            for (int x = 0; x < N; ++x)
+          for (int x = 0; x < N; ++x)
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                float2 z = make_float2(s[x][4 * i + 2 * c], s[x][4 * i + 2 * c + 1]);
-                z = fma2(z, rs[c], -ref);
-                float2 e = make_float2(exp2_fast(z.x), exp2_fast(z.y));
-                sum[i & 1] = add2(sum[i & 1], e);
-                if constexpr (FMT != KV_CACHE_SRC) {
-                  e.x *= kf[x][2 * i];
-                  e.y *= kf[x][2 * i + 1];
-                }
-                pw[x][2 * i + c] = pack2(e.x, e.y, kBF16);
+            for (int i = 0; i < kCols / 8; ++i) {
+              float2 z = make_float2(s[x][4 * i + 2 * c], s[x][4 * i + 2 * c + 1]);
+              z = fma2(z, rs[c], -ref);
+              float2 e = make_float2(exp2_fast(z.x), exp2_fast(z.y));
+              sum[i & 1] = add2(sum[i & 1], e);
+              if constexpr (FMT != KV_CACHE_SRC) {
+                e.x *= kf[x][2 * i];
+                e.y *= kf[x][2 * i + 1];
               }
-            sum[0] = add2(sum[0], sum[1]);
-            l[c] = __fmaf_rn(l[c], alpha[c], sum[0].x + sum[0].y);
-          }
+              pw[x][2 * i + c] = pack2(e.x, e.y, kBF16);
+            }
+          sum[0] = add2(sum[0], sum[1]);
+          l[c] = __fmaf_rn(l[c], alpha[c], sum[0].x + sum[0].y);
         }
         // tiles take turns in the halves of P's rows: P V of the last but one has read its
 #pragma unroll
@@ -605,17 +616,16 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
             }
           tc_wait_st();
         }
-        if (has_rows) {
 #pragma unroll
-          for (int x = 0; x < N; ++x)
+        for (int x = 0; x < N; ++x)
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const uint32_t r = static_cast<uint32_t>(r0 + 8 * c);
+          for (int c = 0; c < 2; ++c) {
+            const uint32_t r = static_cast<uint32_t>(r0 + 8 * c);
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                asm volatile("st.shared.u32 [%0], %1;" ::"r"(p_at + r * 128u + (((i + 4u * ((T + x) & 1u)) ^ (r & 7u)) << 4) + 4u * t), "r"(pw[x][2 * i + c]) : "memory");
-            }
-        }
+            for (int i = 0; i < kCols / 8; ++i)
+              asm volatile("st.shared.u32 [%0], %1;" ::"r"(p_at + r * 128u + (((i + kCols / 8 * half + 4u * ((T + x) & 1u)) ^ (r & 7u)) << 4) + 4u * t),
+                           "r"(pw[x][2 * i + c]) : "memory");
+          }
         fence_async_shared();
         tc_fence_before();
         __syncwarp();
@@ -646,7 +656,20 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
       for (int c = 0; c < 2; ++c) {
         l[c] += __shfl_xor_sync(0xFFFFFFFFu, l[c], 1);
         l[c] += __shfl_xor_sync(0xFFFFFFFFu, l[c], 2);
-        if (has_rows && t == 0u) sh_inv[r0 + 8 * c] = l[c] < INFINITY ? __fdiv_rn(1.0f, l[c]) : NAN;
+      }
+      if constexpr (kHalves > 1) {
+        if (t == 0u && half != 0u) {
+          sh_top[r0] = l[0];
+          sh_top[r0 + 8] = l[1];
+        }
+        sync_softmax();
+      }
+      if (first) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          if constexpr (kHalves > 1) l[c] += sh_top[r0 + 8 * c];
+          sh_inv[r0 + 8 * c] = l[c] < INFINITY ? __fdiv_rn(1.0f, l[c]) : NAN;
+        }
       }
       if (live) {
         ok = bar_wait(pv_done + 8 * ((T - 1u) & 1u), ((T - 1u) >> 1) & 1u, state) && ok;
@@ -702,7 +725,7 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
         if (lane == 0u && (lo | hi) != 0u) atomicOr(sh_bad, static_cast<unsigned long long>(hi) << 32 | lo);
         sync_softmax();
         unsigned long long again = *const_cast<volatile unsigned long long*>(sh_bad);
-        if (a.lse && has_rows && t == 0u) {
+        if (a.lse && first) {
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             const int32_t r = r0 + 8 * c;
@@ -744,7 +767,7 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
               if (i < rows) *row = __uint_as_float(w[i]);
           }
         }
-        if (has_rows && t == 0u) {
+        if (first) {
 #pragma unroll
           for (int c = 0; c < 2; ++c)
             if (r0 + 8 * c < seg.nrows) *reinterpret_cast<float2*>(p.part_ml + (at + r0 + 8 * c) * 2) = make_float2(m[c], l[c]);
@@ -1309,6 +1332,8 @@ kv_status launch_latent_tile(LatentTileParams p, void* work, int64_t work_bytes,
   } else {
     p.raws = 2;
     if (S::total(p.chunks, 4, 4) <= kMost) p.units = 4;
+    while (p.raws < 4 && S::total(p.chunks, p.units, p.raws + 1) <= kMost) ++p.raws;
+    while (p.units < kLatMaxUnits && S::total(p.chunks, p.units + 1, p.raws) <= kMost) ++p.units;
     while (p.raws < kLatMaxRaws && S::total(p.chunks, p.units, p.raws + 1) <= kMost) ++p.raws;
   }
   const int smem = S::total(p.chunks, p.units, p.raws);

@@ -158,7 +158,7 @@ __device__ __forceinline__ uint2 codes8(const float* x, float f) {
 
 // CH: chunks of 256 latent dims; U: passes of query items a warp.
 template <int FMT, bool kInter, int CH, int U>
-__global__ void __launch_bounds__(kThreads) kv_latent_rows(const __grid_constant__ LatentStoreParams p) {
+__global__ void __launch_bounds__(kThreads, 4) kv_latent_rows(const __grid_constant__ LatentStoreParams p) {
   const uint32_t lane = threadIdx.x & 31u;
   const uint64_t nwarps = static_cast<uint64_t>(gridDim.x) * warps_per_cta();
   const uint32_t half = p.rotary / 2;
