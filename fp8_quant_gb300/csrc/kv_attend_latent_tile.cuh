@@ -816,21 +816,35 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
               if (c < S::kInTmem) tc_mma_chunk_ts(d, q_col + 32 * c, kd + c * (1024 >> 4), kDesc, c > 0);
               else tc_mma_chunk(d, q_desc + (c - S::kInTmem) * (NR * 128 >> 4), kd + c * (1024 >> 4), kDesc, c > 0);
             };
-#pragma unroll
-            for (int c = 0; c < kLatMaxChunks; c += 3) {
-              if (p.ksteps >= 4 * c + 12) {
-                chunk(c); chunk(c + 1); chunk(c + 2);
-              } else {
+            auto rest = [&] {
 #pragma unroll 1
-                for (int32_t y = c; 4 * y + 4 <= p.ksteps; ++y) chunk(y);
-#pragma unroll 1
-                for (int32_t i = p.ksteps & ~3; i < p.ksteps; ++i) {
-                  const uint64_t b = kd + ((i / 4) * (1024 >> 4) + (i % 4) * 2);
-                  if (i < 4 * S::kInTmem) tc_mma_ts(d, q_col + 8 * i, b, kDesc, i > 0);
-                  else tc_mma_ss(d, q_desc + ((i / 4 - S::kInTmem) * (NR * 128 >> 4) + (i % 4) * 2), b, kDesc, true);
-                }
-                break;
+              for (int32_t i = p.ksteps & ~3; i < p.ksteps; ++i) {
+                const uint64_t b = kd + ((i / 4) * (1024 >> 4) + (i % 4) * 2);
+                if (i < 4 * S::kInTmem) tc_mma_ts(d, q_col + 8 * i, b, kDesc, i > 0);
+                else tc_mma_ss(d, q_desc + ((i / 4 - S::kInTmem) * (NR * 128 >> 4) + (i % 4) * 2), b, kDesc, true);
               }
+            };
+            if constexpr (FMT == KV_CACHE_SRC) {
+#pragma unroll
+              for (int c = 0; c < kLatMaxChunks; c += 3) {
+                if (p.ksteps >= 4 * c + 12) {
+                  chunk(c); chunk(c + 1); chunk(c + 2);
+                } else {
+#pragma unroll 1
+                  for (int32_t y = c; 4 * y + 4 <= p.ksteps; ++y) chunk(y);
+                  rest();
+                  break;
+                }
+              }
+            } else {  // loops: beside the converters' code straight lines do not stay in the instruction cache
+              const int32_t whole = p.ksteps >> 2, ts = min(whole, S::kInTmem);
+#pragma unroll 1
+              for (int32_t c = 0; c < ts; ++c) tc_mma_chunk_ts(d, q_col + 32 * c, kd + c * (1024 >> 4), kDesc, c > 0);
+              if constexpr (S::kInTmem < kLatMaxChunks) {
+#pragma unroll 1
+                for (int32_t c = S::kInTmem; c < whole; ++c) chunk(c);
+              }
+              rest();
             }
             tc_commit(s_full + 8 * buf);
           }
@@ -850,7 +864,7 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
           if (!ok) break;
           const uint64_t v = smem_desc_groups(ring0 + un * unit_bytes, 1024, group_bytes), pd = p_desc + 4 * odd;
           auto block = [&](int32_t b) { tc_mma_two(o_at + b * NR, v + b * (2048 >> 4), pd, kDesc, (u >> 16) != 0u, step, 2u); };
-          if (p.blocks == 4) {
+          if (FMT == KV_CACHE_SRC && p.blocks == 4) {
             block(0); block(1); block(2); block(3);
           } else {
 #pragma unroll 1
@@ -1107,7 +1121,6 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
     // ======================================================================================
     // e4m3fn rows to fp16: a warp takes eight keys of a chunk at a time, 16 codes a lane
     // ======================================================================================
-    constexpr int kPer = (4 * kLatMaxChunks + kLatConverters - 1) / kLatConverters;
     const uint32_t w = warp - 9u, jobs = 4u * static_cast<uint32_t>(p.chunks);
     const uint32_t row = lane >> 2, q = lane & 3u;
     uint32_t k = 0u, n = 0u;
@@ -1117,40 +1130,43 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
       for (int32_t unit = seg.t0; unit < seg.t1; ++unit, ++n) {
         ok = __all_sync(0xFFFFFFFFu, bar_wait(raw_full + 8 * from.unit, from.phase, state));
         if (!ok) break;
-        uint4 v[kPer];
         const uint32_t src = raw_ring + from.unit * raw_bytes;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-          if (w + kLatConverters * i < jobs) v[i] = ld_shared16(src + (w + kLatConverters * i) * 512u + lane * 16u);
         float scale = 0.0f;
         uint32_t bits = 0u;
         if (w == 0u) {
           scale = sh_scale[(units + from.unit) * kLatKeys + lane];
           bits = sh_raw_valid[from.unit];
         }
+        if (n >= units) ok = __all_sync(0xFFFFFFFFu, bar_wait(empty + 8 * at.unit, at.phase ^ 1u, state));
+        if (!ok) break;
+        const uint32_t dst = ring + at.unit * unit_bytes;
+#pragma unroll 1
+        for (uint32_t i0 = w; i0 < jobs; i0 += 2u * kLatConverters) {
+          uint4 v[2];
+#pragma unroll
+          for (uint32_t i = 0; i < 2u; ++i)
+            if (i0 + kLatConverters * i < jobs) v[i] = ld_shared16(src + (i0 + kLatConverters * i) * 512u + lane * 16u);
+#pragma unroll
+          for (uint32_t i = 0; i < 2u; ++i) {
+            if (i0 + kLatConverters * i < jobs) {
+              const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+              uint32_t f[8];
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                f[2 * y] = f16x2_from_e4m3x2(x[y]);
+                f[2 * y + 1] = f16x2_from_e4m3x2(x[y] >> 16);
+              }
+              const uint32_t to = dst + (i0 + kLatConverters * i) * 1024u + row * 128u;
+              st_shared16(to + (((2u * q) ^ row) << 4), f[0], f[1], f[2], f[3]);
+              st_shared16(to + (((2u * q + 1u) ^ row) << 4), f[4], f[5], f[6], f[7]);
+            }
+          }
+        }
         __syncwarp();
         if (lane == 0u) bar_arrive(raw_empty + 8 * from.unit);
         if (++from.unit == raws) {
           from.unit = 0u;
           from.phase ^= 1u;
-        }
-        if (n >= units) ok = __all_sync(0xFFFFFFFFu, bar_wait(empty + 8 * at.unit, at.phase ^ 1u, state));
-        if (!ok) break;
-        const uint32_t dst = ring + at.unit * unit_bytes;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          if (w + kLatConverters * i < jobs) {
-            const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-            uint32_t f[8];
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              f[2 * y] = f16x2_from_e4m3x2(x[y]);
-              f[2 * y + 1] = f16x2_from_e4m3x2(x[y] >> 16);
-            }
-            const uint32_t to = dst + (w + kLatConverters * i) * 1024u + row * 128u;
-            st_shared16(to + (((2u * q) ^ row) << 4), f[0], f[1], f[2], f[3]);
-            st_shared16(to + (((2u * q + 1u) ^ row) << 4), f[4], f[5], f[6], f[7]);
-          }
         }
         if (w == 0u) {
           sh_scale[at.unit * kLatKeys + lane] = scale;
