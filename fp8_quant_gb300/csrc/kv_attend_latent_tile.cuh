@@ -243,6 +243,12 @@ __device__ __forceinline__ bool any_of_softmax(bool x) {
   return r != 0u;
 }
 __device__ __forceinline__ void sync_softmax() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
+// A row that overflowed, in full precision; a call, as it is seldom and the loops want the instruction cache.
+template <int FMT>
+__device__ __noinline__ void latent_row_again(const LatentParams& lp, int32_t b, int32_t pos, int32_t t, int32_t h, int32_t L) {
+  attend_latent_row<FMT, 18>(lp, b, pos, t, h, 0, L);
+}
+
 template <int FMT, int NR, bool kBF16>
 __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(const __grid_constant__ LatentTileParams p) {
   using S = LatentSmem<FMT, NR>;
@@ -741,7 +747,7 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
           for (int32_t r = static_cast<int32_t>(warp); r < seg.nrows; r += 4) {
             if ((again >> r & 1ull) == 0ull) continue;
             const int32_t qi = static_cast<int32_t>(a.group.quot(static_cast<uint32_t>(seg.row0 + r))), h = seg.row0 + r - qi * HQ;
-            attend_latent_row<FMT, 18>(lp, seg.b, seg.p_first + qi, seg.q0 + qi, h, 0, L);
+            latent_row_again<FMT>(lp, seg.b, seg.p_first + qi, seg.q0 + qi, h, L);
           }
           if (lane == 0u) state->hold(-1);
           sync_softmax();
