@@ -74,7 +74,7 @@ extern "C" kv_status kv_attend_latent(const void* q, void* out, float* lse, cons
   const uint64_t q_bits = u64(q) | u64(out) | u64(s->q_token) | u64(s->q_head) | u64(s->o_token) | u64(s->o_head);
   const uint64_t c_bits = u64(cache) | u64(s->cache_page) | u64(s->cache_slot);
   if ((q_bits & 1u) != 0 || (!fp8 && (c_bits & 1u) != 0)) return KV_ERR_UNSUPPORTED;
-  if (row_dim > kMaxRow || num_q_tokens >= (1 << 30) || num_q_tokens * num_q_heads >= INT_MAX || page_size >= INT_MAX ||
+  if (row_dim > kMaxRow || num_q_tokens >= (1 << 30) || num_q_tokens * num_q_heads >= INT_MAX - 1024 || page_size >= INT_MAX ||
       num_pages >= INT_MAX)
     return KV_ERR_UNSUPPORTED;
   {

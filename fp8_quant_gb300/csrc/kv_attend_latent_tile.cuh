@@ -324,6 +324,14 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
   bool ok = !state->ran_out();
   grid_handover();
 
+  // Tries are not counted while a warp is at work that may take any time: in its CTA, and in the pair's other one, which
+  // waits for its units.
+  auto hold = [&](int more) {
+    state->hold(more);
+    if (pair)
+      asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\tred.relaxed.cluster.shared::cluster.add.u32 [a], %2;\n\t}"
+                   ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(&state->held))), "r"(rank ^ 1u), "r"(more) : "memory");
+  };
   // A consumer's next segment; false after a wait that ran out. (By a whole warp.)
   auto take = [&](uint32_t k, LatentSeg* s) {
     ok = ok && __all_sync(0xFFFFFFFFu, bar_wait(seg_full + 8 * (k & 1u), (k >> 1) & 1u, state));
@@ -742,14 +750,14 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
           }
         }
         if (again != 0ull) {
-          if (lane == 0u) state->hold(1);
+          if (lane == 0u) hold(1);
           __syncwarp();
           for (int32_t r = static_cast<int32_t>(warp); r < seg.nrows; r += 4) {
             if ((again >> r & 1ull) == 0ull) continue;
             const int32_t qi = static_cast<int32_t>(a.group.quot(static_cast<uint32_t>(seg.row0 + r))), h = seg.row0 + r - qi * HQ;
             latent_row_again<FMT>(lp, seg.b, seg.p_first + qi, seg.q0 + qi, h, L);
           }
-          if (lane == 0u) state->hold(-1);
+          if (lane == 0u) hold(-1);
           sync_softmax();
           if (tid == 0u) *sh_bad = 0ull;
         }

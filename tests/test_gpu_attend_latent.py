@@ -330,3 +330,91 @@ def test_many_short_items_a_share(HQ, fmt):
     for _ in range(50):
         outs = [p.attend(d, work=work, q_start=None) for _ in range(4)]
         assert all(torch.equal(first, o) for o in outs)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("nqs", [[1, 1], [20, 20]])
+def test_a_split_call_that_lost_a_part_gives_nan(nqs, fmt):
+    """The mark that a CTA leaves in the workspace's head, set beforehand: no row is made of parts that may be missing."""
+    import fp8_quant_gb300 as kv
+    p = LatentProblem([3000, 700], nqs, 8, 512, 64, fmt=fmt, seed=41)
+    d = p.tensors("cuda")
+    work = torch.zeros(kv.ATTEND_WORK_BYTES, dtype=torch.uint8, device="cuda")
+    lse = torch.zeros(sum(nqs), 8, device="cuda")
+    p.check(p.attend(d, work=work, lse=lse), lse)
+    work.view(torch.int32)[1] = 1
+    assert p.attend(d, work=work, lse=lse).isnan().all() and lse.isnan().all()
+    work[:kv.ATTEND_HEAD_BYTES] = 0
+    p.check(p.attend(d, work=work, lse=lse), lse)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("long", [90_000, 160_000])
+def test_no_wait_runs_out_while_rows_are_done_again(long, fmt):
+    """A NaN that one sequence's last token sees has its 64 rows done key by key, for seconds: longer than any wait may last.
+    The CTA's next item waits all that time, and so does the other CTA of a pair, whose rows are the token's before.
+    (Items enough that none is split.)"""
+    import fp8_quant_gb300 as kv
+    B = 700
+    lens = [64] * B
+    lens[150] = long
+    p = LatentProblem(lens, [2] * B, 64, 128, 64, fmt=fmt, seed=42, page=64)
+    at = p.table[150, (long - 1) // 64], (long - 1) % 64
+    p.value[at[0], at[1], :] = np.nan
+    p.cache[at[0], at[1], :] = 0x7F if fmt else NAN16[p.dtype]
+    d = p.tensors("cuda")
+    err = kv.error_record()
+    start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    out = p.attend(d, err=err)
+    start.record()
+    out = p.attend(d, out=out, err=err)
+    end.record()
+    assert kv.kv_error_poll(err) == (kv.KVStatus.OK, 0, -1)
+    assert bool(out[301].isnan().all()) and not bool(out[:301].isnan().any()) and not bool(out[302:].isnan().any())
+    if long > 100_000 and fmt is None:
+        assert start.elapsed_time(end) > 2300      # it did take longer than a wait may
+
+
+def _refused(call, args, name):
+    import fp8_quant_gb300 as kv
+    call(**args)
+    torch.cuda.synchronize()
+    with pytest.raises((kv.KVError, TypeError, ValueError)) as e:
+        call(**dict(args, **{name: args[name].cpu()}))
+    assert getattr(e.value, "status", kv.KVStatus.ERR_INVALID_ARG) == kv.KVStatus.ERR_INVALID_ARG
+    call(**args)
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("name", ["q", "cache", "page_table", "seq_lens", "q_start", "scales", "out", "lse", "work", "err"])
+def test_host_memory_is_refused(name):
+    """Pageable host memory, before anything is launched."""
+    import fp8_quant_gb300 as kv
+    p = LatentProblem([40, 3], [2, 1], 4, 64, 64, fmt="e4m3fn", seed=43)
+    d = p.tensors("cuda")
+    a = dict(q=d["q"], cache=d["cache"], page_table=d["table"], seq_lens=d["lens"], q_start=d["q_start"], scales=d["scales"], fmt="e4m3fn",
+             out=torch.empty(3, 4, 64, dtype=d["q"].dtype, device="cuda"), lse=torch.empty(3, 4, device="cuda"), latent_dim=64,
+             work=torch.zeros(1 << 20, dtype=torch.uint8, device="cuda"), err=kv.error_record())
+    _refused(kv.kv_attend_latent, a, name)
+
+
+def test_two_graphs_with_one_workspace():
+    ps = [LatentProblem([4000, 200], [1, 1], 32, 512, 64, seed=s) for s in (44, 45)]
+    ds = [p.tensors("cuda") for p in ps]
+    work = torch.zeros(1 << 24, dtype=torch.uint8, device="cuda")
+    outs = [torch.empty((2, 32, 512), dtype=torch.bfloat16, device="cuda") for _ in ps]
+    graphs = []
+    for p, d, o in zip(ps, ds, outs):
+        p.attend(d, out=o, work=work)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            p.attend(d, out=o, work=work)
+        graphs.append(g)
+    for _ in range(3):
+        for g, o in zip(graphs, outs):
+            o.zero_()
+            g.replay()
+    torch.cuda.synchronize()
+    for p, o in zip(ps, outs):
+        p.check(o)
