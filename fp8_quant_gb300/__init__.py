@@ -1152,9 +1152,10 @@ def _latent_cache(cache, page_size, fmt, dtype):
         raise ValueError(f"fmt must be one of {list(LATENT_FORMATS)}")
     if fmt is None and cache.dtype is not dtype:
         raise TypeError("without a format the cache has the rows' dtype")
-    D = cache.shape[-1] if cache.dim() else 0
+    shape = cache.shape
+    D = shape[-1] if len(shape) else 0
     page, slot, _, dim, slots, H = _cache_strides(cache, page_size, D, 1 if fmt else 2, "cache")
-    if H != 1 or (dim != cache.element_size() and D > 1):
+    if H != 1 or (D > 1 and dim != (1 if fmt else 2)):
         raise ValueError("a latent cache has one head, with contiguous dims")
     return page, slot, slots, D
 
@@ -1168,7 +1169,7 @@ def _latent_scales(scales, fmt, slots):
     import torch
     if scales is None or scales.dtype is not torch.float32:
         raise TypeError("an e4m3fn cache needs fp32 scales")
-    if tuple(scales.shape) not in ((slots,), (slots, 1)):
+    if scales.shape not in ((slots,), (slots, 1)):
         raise ValueError("scales must be [slots] or [slots, 1]")
     return scales.data_ptr(), scales.stride(0) if slots > 1 else 1
 
@@ -1195,17 +1196,20 @@ def kv_store_latent(c, r, cache, indices, positions=None, cos_sin=None, *, weigh
     import torch
     dtype = c.dtype
     bf16 = _is_bf16(dtype)
-    if c.dim() != 2 or (c.shape[1] > 1 and c.stride(1) != 1):
+    shape, st = c.shape, c.stride()
+    if len(shape) != 2 or (shape[1] > 1 and st[1] != 1):
         raise ValueError("c must be [T, L] with contiguous dims")
-    T, L = c.shape
+    T, L = shape
+    c_token, r_token = st[0] * 2, 0
     if r is None:
         R = 0
         if q is not None or positions is not None or cos_sin is not None:
             raise ValueError("positions, cos_sin and q belong to rotary dims (r)")
     else:
-        if r.dim() != 2 or r.shape[0] != T or r.dtype is not dtype or (r.shape[1] > 1 and r.stride(1) != 1):
+        shape, st = r.shape, r.stride()
+        if len(shape) != 2 or shape[0] != T or r.dtype is not dtype or (shape[1] > 1 and st[1] != 1):
             raise ValueError("r must be [T, R] of c's dtype with contiguous dims")
-        R = r.shape[1]
+        R, r_token = shape[1], st[0] * 2
         if positions is None or cos_sin is None:
             raise ValueError("rotary dims need positions and cos_sin")
     page, slot, slots, D = _latent_cache(cache, page_size, fmt, dtype)
@@ -1214,7 +1218,7 @@ def kv_store_latent(c, r, cache, indices, positions=None, cos_sin=None, *, weigh
     if indices.shape != (T,):
         raise ValueError("indices must hold one entry per row")
     idt, istride = _index_args(indices)
-    if weight is not None and (weight.dtype is not dtype or tuple(weight.shape) != (L,) or not weight.is_contiguous()):
+    if weight is not None and (weight.dtype is not dtype or weight.shape != (L,) or not weight.is_contiguous()):
         raise ValueError("weight must be a contiguous [L] of c's dtype")
     sc, sc_slot = _latent_scales(scales, fmt, slots)
     device = cache.device
@@ -1229,16 +1233,17 @@ def kv_store_latent(c, r, cache, indices, positions=None, cos_sin=None, *, weigh
             raise TypeError("cos_sin must be fp32 [max_position, R] with contiguous rows")
         qa = (None, None, 0, 0, 0, 0, 0)
         if q is not None:
-            if q.dim() != 3 or q.shape[0] != T or q.shape[2] != R or q.dtype is not dtype or (R > 1 and q.stride(2) != 1):
+            shape, st = q.shape, q.stride()
+            if len(shape) != 3 or shape[0] != T or shape[2] != R or q.dtype is not dtype or (R > 1 and st[2] != 1):
                 raise ValueError("q must be [T, HQ, R] of c's dtype with contiguous dims")
             if q_out is None:
                 with _on_stream(stream, device):  # (q itself may be page-locked host memory)
-                    q_out = torch.empty(q.shape, dtype=dtype, device=device)
-            if q_out.shape != q.shape or q_out.dtype is not dtype or (R > 1 and q_out.stride(2) != 1):
+                    q_out = torch.empty(shape, dtype=dtype, device=device)
+            so = st if q_out is q else q_out.stride()
+            if q_out.shape != shape or q_out.dtype is not dtype or (R > 1 and so[2] != 1):
                 raise ValueError("q_out must be like q, with contiguous dims")
-            if q.shape[1]:
-                qa = (q.data_ptr(), q_out.data_ptr(), q.shape[1], q.stride(0) * 2, q.stride(1) * 2,
-                      q_out.stride(0) * 2, q_out.stride(1) * 2)
+            if shape[1]:
+                qa = (q.data_ptr(), q_out.data_ptr(), shape[1], st[0] * 2, st[1] * 2, so[0] * 2, so[1] * 2)
         rope = (cos_sin.data_ptr(), tstride if rows > 1 else rot, rows, positions.data_ptr(), pdt, pstride, rot,
                 1 if interleaved else 0, *qa)
     if q is None and q_out is not None:
@@ -1246,7 +1251,7 @@ def kv_store_latent(c, r, cache, indices, positions=None, cos_sin=None, *, weigh
     rec = err if err is not None else _default_record(device)
     rc = raw.kv_store_latent(
         c.data_ptr(), r.data_ptr() if R else None, cache.data_ptr(), indices.data_ptr(), idt, istride, T, L, R, bf16,
-        (c.stride(0) * 2, r.stride(0) * 2 if R else 0, page, slot, sc_slot), page_size,
+        (c_token, r_token if R else 0, page, slot, sc_slot), page_size,
         slots if size_limit is None else size_limit, None if weight is None else weight.data_ptr(), eps, rope,
         LATENT_FORMATS[fmt], sc, rec.data_ptr(), _stream_handle(stream, device))
     if rc:
@@ -1258,20 +1263,21 @@ def kv_gather_latent(cache, out, indices, *, page_size: int = 1, fmt: Optional[s
                      size_limit: Optional[int] = None, err=None, stream=None) -> None:
     """Rows of a cache of latent rows (see :func:`kv_store_latent`) back: row t of ``out`` [T, L + R],
     bf16 or fp16, takes the row of ``indices[t]``, dequantised for "e4m3fn"."""
-    if out.dim() != 2 or (out.shape[1] > 1 and out.stride(1) != 1):
+    shape, st = out.shape, out.stride()
+    if len(shape) != 2 or (shape[1] > 1 and st[1] != 1):
         raise ValueError("out must be [T, L + R] with contiguous dims")
     bf16 = _is_bf16(out.dtype)
     page, slot, slots, D = _latent_cache(cache, page_size, fmt, out.dtype)
-    if out.shape[1] != D:
-        raise ValueError(f"cache rows of {D} dims, output rows of {out.shape[1]}")
+    if shape[1] != D:
+        raise ValueError(f"cache rows of {D} dims, output rows of {shape[1]}")
     idt, istride = _index_args(indices)
     n = indices.shape[0]
-    if n > out.shape[0]:
+    if n > shape[0]:
         raise ValueError("fewer output rows than indices")
     sc, sc_slot = _latent_scales(scales, fmt, slots)
     rec = err if err is not None else _default_record(cache.device)
     rc = raw.kv_gather_latent(cache.data_ptr(), sc, out.data_ptr(), indices.data_ptr(), idt, istride, n, D, bf16,
-                              (out.stride(0) * 2, 0, page, slot, sc_slot), page_size,
+                              (st[0] * 2, 0, page, slot, sc_slot), page_size,
                               slots if size_limit is None else size_limit, LATENT_FORMATS[fmt], rec.data_ptr(),
                               _stream_handle(stream, cache.device))
     if rc:
@@ -1292,9 +1298,10 @@ def kv_attend_latent(q, cache, page_table, seq_lens, *, latent_dim: int, q_start
     import torch
     dtype = q.dtype
     bf16 = _is_bf16(dtype)
-    if q.dim() != 3 or (q.shape[2] > 1 and q.stride(2) != 1):
+    shape, sq = q.shape, q.stride()
+    if len(shape) != 3 or (shape[2] > 1 and sq[2] != 1):
         raise ValueError("q must be [tokens, HQ, D] with contiguous dims")
-    T, HQ, D = q.shape
+    T, HQ, D = shape
     if page_size is None:
         if cache.dim() != 4:
             raise ValueError("page_size is needed with [slots, 1, D] caches")
@@ -1319,7 +1326,8 @@ def kv_attend_latent(q, cache, page_table, seq_lens, *, latent_dim: int, q_start
     if out is None:
         with _on_stream(stream, device):
             out = torch.empty(shape, dtype=dtype, device=device)
-    if tuple(out.shape) != shape or out.dtype is not dtype or (latent_dim > 1 and out.stride(2) != 1):
+    so = out.stride()
+    if out.shape != shape or out.dtype is not dtype or (latent_dim > 1 and so[2] != 1):
         raise ValueError("out must be [tokens, HQ, latent_dim] of q's dtype, with contiguous dims")
     if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (T, HQ) or not lse.is_contiguous()):
         raise ValueError("lse must be a contiguous fp32 [tokens, HQ]")
@@ -1334,7 +1342,7 @@ def kv_attend_latent(q, cache, page_table, seq_lens, *, latent_dim: int, q_start
         q.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(), cache.data_ptr(), sc,
         page_table.data_ptr(), tst[0] if B > 1 else width, width, seq_lens.data_ptr(),
         None if q_start is None else q_start.data_ptr(), B, T, HQ, D, latent_dim, bf16,
-        (q.stride(0) * 2, q.stride(1) * 2, out.stride(0) * 2, out.stride(1) * 2, page, slot, sc_slot), page_size,
+        (sq[0] * 2, sq[1] * 2, so[0] * 2, so[1] * 2, page, slot, sc_slot), page_size,
         slots // page_size, LATENT_FORMATS[fmt], 1.0 / math.sqrt(D) if sm_scale is None else sm_scale, work.data_ptr(),
         work.numel() * work.element_size(), rec.data_ptr(), _stream_handle(stream, device))
     if rc:

@@ -7,7 +7,7 @@
 //
 // A CTA takes up to NR = 64 or 32 query rows, a row being a (query, head)
 // pair, and goes over tiles of 32 keys:
-//   S [rows][keys] = Q K^T       M = 64 (Q: 384 dims in TMEM, all for 32 rows, the others in shared memory), N = 32 keys;
+//   S [rows][keys] = Q K^T       M = 64 (Q: 320 dims in TMEM, with 32 rows all, the others in shared memory), N = 32 keys;
 //   O^T [dims][rows] += V^T P^T  M = 128 dims, N = NR rows: the tile's first L
 //                                dims as they lie (dims contiguous), P in
 //                                shared memory.
@@ -16,19 +16,27 @@
 // products, and the rows that do not fill M = 128 cost nothing.
 //
 //   warps 0-3  the softmax: S by 16x256b loads (a thread has 8 keys of two rows),
-//              running maximum and sums in registers, P to shared memory. O^T is
-//              rescaled only when a row's maximum grew by 2^8 or more. They also
-//              bring the queries in and write the outputs.
-//   warps 4, 8 issue the products S, of every other tile each, up to four tiles ahead of
-//   warp  5    P V. (A product takes 31 clocks to issue and 25 to 48 to run: one warp for all, or for S, was the bound.)
+//              running maximum and sums in registers, P to shared memory. A tile's scores are only compared with the
+//              running maxima; these, and O^T, are brought up to date when some row's grew by 2^8 or more (the reduction
+//              over a row's threads in every tile: 32 heads over e4m3fn 188 us, 172 without). With 32 rows the 64 of a
+//              product hold them twice, and warps 2 and 3 take half of the keys. They also bring the queries in and
+//              write the outputs.
+//   warps 4, 8 issue the products S, of every other tile each, up to three tiles ahead of
+//   warp  5    P V. (A product takes 31 clocks to issue and 25 to 48 to run: with one warp for all of them decode below
+//              took 223 us, with one for S 151.)
 //   warp  6    cuts the work: finds the CTA's next items and hands them to the others.
 //   warp  7    brings the keys, a tile a unit of the ring: by TMA, a box for all of it where its 32 keys exist and share a
 //              page, else by cp.async. e4m3fn rows come as they are, into a ring of their own, and become fp16 (exact) by
 //   warps 9-15 on their way into the ring of units.
 //   A unit lies as [8 keys][64 dims][key][128 bytes in the 128-byte swizzle], as a box of the cache's eights of keys does.
 //   It is given back when P V has gone over it. Tiles are small because that time is what the
-//   ring has to cover beside the memory's latency: tiles of 64 keys held it twice as long (decode, 64 sequences of 4,000 -
-//   16,384 keys: 171 us).
+//   ring has to cover beside the memory's latency: tiles of 64 keys held it twice as long (171 us where 32 took 151), and
+//   so did products S over two tiles at once, which run 36 % faster a key (chunks 1,113 us, 939 without).
+//
+// Measured (one GB300): 64 sequences of 4,000 - 16,384 bf16 keys, 32 heads, one token each (decode) 139 us, 83 % of the
+// copy rate for its bytes; chunks of 700 - 1,023 tokens over 5,000 - 8,190 keys 918 us, 840 TFLOP/s: the products' own
+// time, 36 x 25 + 8 x 48 clocks a tile, is 84 % of it; 32 sequences of 16,000 - 32,768 e4m3fn keys 166 us: products and
+// conversions share the 128 bytes a clock of shared memory (S 288, P V 320, conversions 576 of 1,790 clocks a tile).
 //
 // Rows beyond NR (more queries, more heads) read the same keys: two CTAs then are a cluster, each brings half of
 // every unit and TMA writes it into both.
@@ -56,6 +64,7 @@ constexpr int kLatKeys = 32;        // keys of a tile, which is a unit of the ri
 constexpr int kLatMaxChunks = 9;    // 64-dim chunks of a row: up to 576 dims
 constexpr int kLatMaxUnits = 8, kLatMaxRaws = 8;
 constexpr int kLatScores = 3;       // tiles whose scores may be in TMEM
+constexpr int kLatMinSteps = 2;     // tiles of a share at least
 
 struct LatentTileParams {
   LatentParams l;
@@ -69,7 +78,6 @@ struct LatentTileParams {
   int32_t blocks;    // 128-dim blocks of the values
   int32_t units, raws;  // of the ring, and of that of e4m3fn rows
   int32_t split;     // 0: an item is one CTA's (or pair's)
-  int32_t min_steps;
   int32_t part_rows;
   SplitWork* head;
   int64_t* meta;     // [num_seqs]: first step of each sequence
@@ -133,14 +141,16 @@ __device__ __forceinline__ int64_t latent_units(const LatentTileParams& p, int32
   return static_cast<int64_t>(g.blocks) * (p.split ? g.steps : 1);
 }
 
-// A share for each CTA (or pair), all of a size. (Smaller shares behind them, for those that are done first, cost more in
-// queries brought in and parts written than they balance.)
-__device__ __forceinline__ int64_t quotient(int64_t x, int64_t d) {  // of non-negative numbers; most are short
+// Of non-negative numbers, most of them short.
+__device__ __forceinline__ int64_t quotient(int64_t x, int64_t d) {
   return ((x | d) >> 32) == 0 ? static_cast<int64_t>(static_cast<uint32_t>(x) / static_cast<uint32_t>(d)) : x / d;
 }
-__device__ __forceinline__ ShareLevel latent_cut(int64_t total, int32_t ctas, int32_t min_steps, int32_t* shares) {
+
+// A share for each CTA (or pair), all of a size. (Smaller shares behind them, for those that are done first, cost more in
+// queries brought in and parts written than they balance.)
+__device__ __forceinline__ ShareLevel latent_cut(int64_t total, int32_t ctas, int32_t* shares) {
   int64_t each = quotient(total + ctas - 1, ctas);
-  if (each < min_steps) each = min_steps;
+  if (each < kLatMinSteps) each = kLatMinSteps;
   *shares = static_cast<int32_t>(quotient(total + each - 1, each));
   return ShareLevel{0, static_cast<int32_t>(each), 0};
 }
@@ -380,7 +390,9 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
     };
     uint32_t items = 0u;  // that have tiles
     auto load_q = [&](const LatentSeg& s) {
-      constexpr int kIn = S::kInTmem, kAt = FMT == KV_CACHE_SRC && NR == 32 ? 3 : 1;  // chunks in TMEM; chunks in flight
+      // chunks in TMEM; chunks in flight (decode 150 us with one, 143 with three, 147 with nine; over e4m3fn 194 with one, 204
+      // with three)
+      constexpr int kIn = S::kInTmem, kAt = FMT == KV_CACHE_SRC && NR == 32 ? 3 : 1;
       const bool shift = FMT != KV_CACHE_SRC && a.bf16;
       auto shifted = [](uint32_t z, float f) {
         const float2 v = widen2<true>(z);
@@ -647,8 +659,10 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
         T += N;
         return true;
       };
-      // With 64 rows the products are the longer and two tiles go together (what a step costs whatever its keys is a third of
-      // it); with 32 the memory is, and a tile does not wait for the next.
+      // Where the products are the longer two tiles go together, as what a step costs whatever its keys is a third of it: 64
+      // rows over e4m3fn keys (24 heads, 200 - 777 tokens 651 us, 780 with one), or of sequences with so many rows that a
+      // unit serves several CTAs (chunks 929 and 1,013 us). Else a tile does not wait for the next: 48 heads, 2 - 5 tokens
+      // 190 us with two and 167 with one, 32 heads, one token over e4m3fn 243 and 187.
       bool left = false;
       for (int32_t j = seg.t0; j < seg.t1 && !left;) {
         if (NR == 64 && (FMT != KV_CACHE_SRC || seg.nq * HQ > 4 * NR) && j + 1 < seg.t1) {
@@ -850,7 +864,7 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
                   break;
                 }
               }
-            } else {  // loops: beside the converters' code straight lines do not stay in the instruction cache
+            } else {  // loops: beside the converters' code straight lines do not stay in the instruction cache (638 us, 521)
               const int32_t whole = p.ksteps >> 2, ts = min(whole, S::kInTmem);
 #pragma unroll 1
               for (int32_t c = 0; c < ts; ++c) tc_mma_chunk_ts(d, q_col + 32 * c, kd + c * (1024 >> 4), kDesc, c > 0);
@@ -919,7 +933,7 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
     int32_t shares = 0;
     const int32_t ctas = static_cast<int32_t>(gridDim.x) / p.cluster, cta = static_cast<int32_t>(blockIdx.x) / p.cluster;
     if (p.split) {
-      level = latent_cut(total, ctas, p.min_steps, &shares);
+      level = latent_cut(total, ctas, &shares);
       if (blockIdx.x == 0 && lane == 0u) {
         p.head->level[0] = level;
         p.head->levels = 1;
@@ -996,7 +1010,9 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
         s.t1 = p.split ? min(s_out, tiles) : tiles;
         s.part = s_out - s_in == unit ? -1 : (2 * share + (s_in == 0 ? 1 : 0)) * p.cluster + static_cast<int32_t>(rank);
         publish(s);
-        if (NR == 32 && s.t1 > s.t0) {  // its queries into L2: they are wanted when the item before ends
+        // its queries into L2: they are wanted when the item before ends (32 heads over e4m3fn 212 us without, 204 with; with
+        // 64 rows an item has many tiles, and the code alone costs what it brings: chunks 930 us without, 1,006 with)
+        if (NR == 32 && s.t1 > s.t0) {
           const int32_t lines = (a.head_dim * 2 + 127) / 128;
           for (int32_t i = static_cast<int32_t>(lane); i < s.nrows * lines; i += 32) {
             const int32_t r = i / lines, qi = static_cast<int32_t>(a.group.quot(static_cast<uint32_t>(s.row0 + r)));
@@ -1316,8 +1332,6 @@ __global__ void __launch_bounds__(32 * kLatJoinWarps) kv_attend_latent_join(cons
 // Host
 // ---------------------------------------------------------------------------
 
-constexpr int kLatMinSteps = 2;  // tiles of a share at least
-
 // Pairs of CTAs of a kernel that can be resident at once, per device.
 inline kv_status pairs_resident(const void* kernel, int threads, int smem, std::atomic<int>* known, int* out) {
   int dev = 0;
@@ -1385,7 +1399,6 @@ kv_status launch_latent_tile(LatentTileParams p, void* work, int64_t work_bytes,
   const int64_t slot = static_cast<int64_t>(p.cluster) * p.part_rows * (128 * p.blocks + 2) * 4;
   int64_t fit = work && work_bytes > kSplitHead + meta ? (work_bytes - kSplitHead - meta) / (2 * slot) : 0;
   if (fit > ctas) fit = ctas;
-  p.min_steps = kLatMinSteps;
   p.split = items < 4 * ctas && max_keys > 8 * kLatKeys && 2 * fit >= ctas;
   int64_t grid = items < ctas ? items : ctas;
   if (p.split) {
