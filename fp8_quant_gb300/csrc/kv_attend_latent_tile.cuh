@@ -33,9 +33,9 @@
 //   ring has to cover beside the memory's latency: tiles of 64 keys held it twice as long (171 us where 32 took 151), and
 //   so did products S over two tiles at once, which run 36 % faster a key (chunks 1,113 us, 939 without).
 //
-// Measured (one GB300): 64 sequences of 4,000 - 16,384 bf16 keys, 32 heads, one token each (decode) 139 us, 83 % of the
-// copy rate for its bytes; chunks of 700 - 1,023 tokens over 5,000 - 8,190 keys 918 us, 840 TFLOP/s: the products' own
-// time, 36 x 25 + 8 x 48 clocks a tile, is 84 % of it; 32 sequences of 16,000 - 32,768 e4m3fn keys 166 us: products and
+// Measured (one GB300): 64 sequences of 4,000 - 16,384 bf16 keys, 32 heads, one token each (decode) 137 us, 82 % of the
+// copy rate for its bytes; chunks of 700 - 1,023 tokens over 5,000 - 8,190 keys 912 us, 848 TFLOP/s: the products' own
+// time, 36 x 25 + 8 x 48 clocks a tile, is 84 % of it; 32 sequences of 16,000 - 32,768 e4m3fn keys 160 us: products and
 // conversions share the 128 bytes a clock of shared memory (S 288, P V 320, conversions 576 of 1,790 clocks a tile).
 //
 // Rows beyond NR (more queries, more heads) read the same keys: two CTAs then are a cluster, each brings half of
@@ -64,7 +64,11 @@ constexpr int kLatKeys = 32;        // keys of a tile, which is a unit of the ri
 constexpr int kLatMaxChunks = 9;    // 64-dim chunks of a row: up to 576 dims
 constexpr int kLatMaxUnits = 8, kLatMaxRaws = 8;
 constexpr int kLatScores = 3;       // tiles whose scores may be in TMEM
-constexpr int kLatMinSteps = 2;     // tiles of a share at least
+constexpr int kLatMinSteps = 2;     // steps of a share at least
+// Steps that an item counts beside its tiles where items are split: what its queries, first scores and outputs take. (24 heads,
+// 200 - 777 tokens over e4m3fn keys 514 us with none, 501 with 4, 475 with 8 and with 12; 32 heads, one token 166, 164, 161, 159;
+// over 16-bit keys no difference.)
+constexpr int kLatItemSteps = 8;
 
 struct LatentTileParams {
   LatentParams l;
@@ -121,7 +125,8 @@ static_assert(LatentSmem<KV_CACHE_SRC, 64>::total(kLatMaxChunks, 5, 0) <= 227 * 
 static_assert(4 * 64 + kLatScores * kLatKeys + 32 * LatentSmem<KV_CACHE_SRC, 64>::kInTmem <= 512 &&
                   4 * 32 + kLatScores * kLatKeys + 32 * LatentSmem<KV_CACHE_SRC, 32>::kInTmem <= 512, "TMEM");
 
-// Rows of the sequence's queries in blocks of NR (of the pair: 2 NR), and tiles of each (an upper bound, at least one).
+// Rows of the sequence's queries in blocks of NR (of the pair: 2 NR), and steps of each: kLatItemSteps, and its tiles (an
+// upper bound, at least one).
 struct LatentGeom {
   int32_t blocks, steps;
 };
@@ -131,7 +136,7 @@ __device__ __forceinline__ LatentGeom latent_geom(const LatentTileParams& p, con
   LatentGeom g;
   const uint32_t rows = NR * static_cast<uint32_t>(p.cluster);
   g.blocks = static_cast<int32_t>((static_cast<uint32_t>(s.nq) * p.l.a.group.d + rows - 1) / rows);
-  g.steps = max((s.len + kLatKeys - 1) / kLatKeys, 1);
+  g.steps = max((s.len + kLatKeys - 1) / kLatKeys, 1) + kLatItemSteps;
   return g;
 }
 
@@ -1006,8 +1011,8 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
         s.last = max(s.nrows - 1, 0);
         s.p_hi = s.p_first + static_cast<int32_t>(a.group.quot(static_cast<uint32_t>(min(rows, first + NR * p.cluster) - 1)));
         const int32_t tiles = s.p_hi < 0 ? 0 : s.p_hi / kLatKeys + 1;
-        s.t0 = p.split ? min(s_in, tiles) : 0;
-        s.t1 = p.split ? min(s_out, tiles) : tiles;
+        s.t0 = p.split ? min(max(s_in - kLatItemSteps, 0), tiles) : 0;
+        s.t1 = p.split ? min(max(s_out - kLatItemSteps, 0), tiles) : tiles;
         s.part = s_out - s_in == unit ? -1 : (2 * share + (s_in == 0 ? 1 : 0)) * p.cluster + static_cast<int32_t>(rank);
         publish(s);
         // its queries into L2: they are wanted when the item before ends (32 heads over e4m3fn 212 us without, 204 with; with
