@@ -129,10 +129,8 @@ extern "C" kv_status kv_attend_latent(const void* q, void* out, float* lse, cons
     tp.blocks = (latent_dim + 127) / 128;
     const int64_t rows = (num_q_tokens + num_seqs - 1) / num_seqs * num_q_heads;
     const bool few = rows <= 32;
-    // more rows than a CTA takes: pairs of CTAs share their keys (16-bit rows)
-    tp.cluster = !fp8 && rows > 64 ? 2 : 1;
-    // TMA: runs of 8, 16 or 32 keys of a page a box (a pair's CTA brings 16), with all their dims where these are whole chunks
-    int groups = tp.cluster > 1 ? 2 : 4;
+    // TMA: runs of 8, 16 or 32 keys of a page a box, with all their dims where these are whole chunks
+    int groups = 4;
     while (groups > 0 && page_size % (8 * groups) != 0) groups /= 2;
     const bool whole = row_dim % 64 == 0;
     if (groups > 0 && (whole || !fp8) &&

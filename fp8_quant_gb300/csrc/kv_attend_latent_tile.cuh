@@ -38,8 +38,7 @@
 // time, 36 x 25 + 8 x 48 clocks a tile, is 84 % of it; 32 sequences of 16,000 - 32,768 e4m3fn keys 160 us: products and
 // conversions share the 128 bytes a clock of shared memory (S 288, P V 320, conversions 576 of 1,790 clocks a tile).
 //
-// Rows beyond NR (more queries, more heads) read the same keys: two CTAs then are a cluster, each brings half of
-// every unit and TMA writes it into both.
+// Rows beyond NR (more queries, more heads) are further items, which read the same keys: mostly from L2.
 //
 // Weights are rounded once to 16 bits, as the product's operand; their sums are
 // of the unrounded ones in fp32. An e4m3fn row's scale f multiplies its scores,
@@ -47,7 +46,7 @@
 // maximum of score + log2 f, so that p f, not p, begins at 2^7.
 //
 // Few long sequences are split over the CTAs by keys, in steps of a tile, counted
-// on the device, a share for each CTA (or pair); parts are joined in the order of the keys by a second kernel.
+// on the device, a share for each CTA; parts are joined in the order of the keys by a second kernel.
 //
 // Every wait has a limit (kSpin); a CTA whose wait ran out records that in the
 // error record and in the workspace's head, lets its copies and products end and leaves.
@@ -75,17 +74,16 @@ struct LatentTileParams {
   CUtensorMap map;
   int32_t box;       // groups of eight keys in a TMA box: 1, 2 or 4; 0: cp.async alone
   int32_t box_chunks;  // chunks of one: 1 or all
-  int32_t cluster;   // CTAs that share their keys: 1 or 2
   int32_t page_stride, slot_stride;  // of the cache, bytes in 32 bits
   int32_t chunks;    // 64-dim chunks of a row, the last perhaps cut
   int32_t ksteps;    // 16-dim steps of a row
   int32_t blocks;    // 128-dim blocks of the values
   int32_t units, raws;  // of the ring, and of that of e4m3fn rows
-  int32_t split;     // 0: an item is one CTA's (or pair's)
+  int32_t split;     // 0: an item is one CTA's
   int32_t part_rows;
   SplitWork* head;
   int64_t* meta;     // [num_seqs]: first step of each sequence
-  float *part_o, *part_ml;  // [2 * shares][cluster][part_rows] x 128 * blocks and x 2
+  float *part_o, *part_ml;  // [2 * shares][part_rows] x 128 * blocks and x 2
 };
 
 constexpr int kLatConverters = 7;  // warps
@@ -95,7 +93,7 @@ constexpr int kLatThreads = 288 + (FMT == KV_CACHE_SRC ? 0 : 32 * kLatConverters
 // A CTA's next piece of work.
 struct LatentSeg {
   int32_t b, q0, nq, p_first;  // sequence, its first query row and their number, position of the first
-  int32_t row0, nrows, last;   // the CTA's rows of the item: (query, head) pairs of the sequence; the last, from row0 (at least 0)
+  int32_t row0, nrows, last;   // its rows: (query, head) pairs of the sequence; the last, from row0
   int32_t p_hi;                // position of the item's last row
   int32_t t0, t1;              // tiles
   int32_t part;                // -1: the item is whole; else the part's place
@@ -125,8 +123,8 @@ static_assert(LatentSmem<KV_CACHE_SRC, 64>::total(kLatMaxChunks, 5, 0) <= 227 * 
 static_assert(4 * 64 + kLatScores * kLatKeys + 32 * LatentSmem<KV_CACHE_SRC, 64>::kInTmem <= 512 &&
                   4 * 32 + kLatScores * kLatKeys + 32 * LatentSmem<KV_CACHE_SRC, 32>::kInTmem <= 512, "TMEM");
 
-// Rows of the sequence's queries in blocks of NR (of the pair: 2 NR), and steps of each: kLatItemSteps, and its tiles (an
-// upper bound, at least one).
+// Rows of the sequence's queries in blocks of NR, and steps of each: kLatItemSteps, and its tiles (an upper bound, at
+// least one).
 struct LatentGeom {
   int32_t blocks, steps;
 };
@@ -134,8 +132,7 @@ struct LatentGeom {
 template <int NR>
 __device__ __forceinline__ LatentGeom latent_geom(const LatentTileParams& p, const AttendSeq& s) {
   LatentGeom g;
-  const uint32_t rows = NR * static_cast<uint32_t>(p.cluster);
-  g.blocks = static_cast<int32_t>((static_cast<uint32_t>(s.nq) * p.l.a.group.d + rows - 1) / rows);
+  g.blocks = static_cast<int32_t>((static_cast<uint32_t>(s.nq) * p.l.a.group.d + NR - 1) / NR);
   g.steps = max((s.len + kLatKeys - 1) / kLatKeys, 1) + kLatItemSteps;
   return g;
 }
@@ -151,7 +148,7 @@ __device__ __forceinline__ int64_t quotient(int64_t x, int64_t d) {
   return ((x | d) >> 32) == 0 ? static_cast<int64_t>(static_cast<uint32_t>(x) / static_cast<uint32_t>(d)) : x / d;
 }
 
-// A share for each CTA (or pair), all of a size. (Smaller shares behind them, for those that are done first, cost more in
+// A share for each CTA, all of a size. (Smaller shares behind them, for those that are done first, cost more in
 // queries brought in and parts written than they balance.)
 __device__ __forceinline__ ShareLevel latent_cut(int64_t total, int32_t ctas, int32_t* shares) {
   int64_t each = quotient(total + ctas - 1, ctas);
@@ -221,27 +218,11 @@ __device__ __forceinline__ void tc_mma_chunk_ts(uint32_t d, uint32_t a, uint64_t
 #undef KV_NEXT
 }
 
-// A box of a cache of latent rows (latent_map), by one lane of a converged warp; into the same place of both CTAs of a
-// pair, and their barriers.
-__device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t dim, int32_t group, int32_t page, bool pair) {
-  if (pair) {
-    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xFFFFFFFF;\n\t"
-                 "@e cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%3, %6, %6, %4, %5}], [%2], %7;\n\t}"
-                 ::"r"(dst), "l"(map), "r"(bar), "r"(dim), "r"(group), "r"(page), "r"(0), "h"(static_cast<uint16_t>(3)) : "memory");
-  } else {
-    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xFFFFFFFF;\n\t"
-                 "@e cp.async.bulk.tensor.5d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %6, %6, %4, %5}], [%2];\n\t}"
-                 ::"r"(dst), "l"(map), "r"(bar), "r"(dim), "r"(group), "r"(page), "r"(0) : "memory");
-  }
-}
-// tc_commit to the same barrier of both CTAs of a pair.
-__device__ __forceinline__ void tc_commit_pair(uint32_t bar) {
+// A box of a cache of latent rows (latent_map), by one lane of a converged warp.
+__device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t dim, int32_t group, int32_t page) {
   asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xFFFFFFFF;\n\t"
-               "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}"
-               ::"r"(bar), "h"(static_cast<uint16_t>(3)) : "memory");
-}
-__device__ __forceinline__ void sync_pair() {
-  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+               "@e cp.async.bulk.tensor.5d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %6, %6, %4, %5}], [%2];\n\t}"
+               ::"r"(dst), "l"(map), "r"(bar), "r"(dim), "r"(group), "r"(page), "r"(0) : "memory");
 }
 
 __device__ __forceinline__ float lg2_fast(float x) {
@@ -298,8 +279,6 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
   uint32_t* const sh_tmem = reinterpret_cast<uint32_t*>(small_ptr + S::kOffMisc + 16);
   unsigned long long* const sh_bad = reinterpret_cast<unsigned long long*>(small_ptr + S::kOffMisc + 24);
   constexpr int kFillers = FMT == KV_CACHE_SRC ? 1 : kLatConverters;  // that arrive for a full unit
-  const bool pair = p.cluster > 1;
-  const uint32_t rank = pair ? blockIdx.x & 1u : 0u;
 
   if (warp == 4) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
@@ -309,7 +288,7 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
   if (tid == 0) {
     for (uint32_t i = 0; i < units; ++i) {
       bar_init(full + 8 * i, kFillers);
-      bar_init(empty + 8 * i, pair ? 2 : 1);
+      bar_init(empty + 8 * i, 1);
     }
     for (uint32_t i = 0; i < raws; ++i) {
       bar_init(raw_full + 8 * i, 33);
@@ -331,7 +310,6 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
     *sh_bad = 0ull;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (pair) sync_pair();  // the other CTA's barriers are there
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -339,14 +317,6 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
   bool ok = !state->ran_out();
   grid_handover();
 
-  // Tries are not counted while a warp is at work that may take any time: in its CTA, and in the pair's other one, which
-  // waits for its units.
-  auto hold = [&](int more) {
-    state->hold(more);
-    if (pair)
-      asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\tred.relaxed.cluster.shared::cluster.add.u32 [a], %2;\n\t}"
-                   ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(&state->held))), "r"(rank ^ 1u), "r"(more) : "memory");
-  };
   // A consumer's next segment; false after a wait that ran out. (By a whole warp.)
   auto take = [&](uint32_t k, LatentSeg* s) {
     ok = ok && __all_sync(0xFFFFFFFFu, bar_wait(seg_full + 8 * (k & 1u), (k >> 1) & 1u, state));
@@ -769,14 +739,14 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
           }
         }
         if (again != 0ull) {
-          if (lane == 0u) hold(1);
+          if (lane == 0u) state->hold(1);
           __syncwarp();
           for (int32_t r = static_cast<int32_t>(warp); r < seg.nrows; r += 4) {
             if ((again >> r & 1ull) == 0ull) continue;
             const int32_t qi = static_cast<int32_t>(a.group.quot(static_cast<uint32_t>(seg.row0 + r))), h = seg.row0 + r - qi * HQ;
             latent_row_again<FMT>(lp, seg.b, seg.p_first + qi, seg.q0 + qi, h, L);
           }
-          if (lane == 0u) hold(-1);
+          if (lane == 0u) state->hold(-1);
           sync_softmax();
           if (tid == 0u) *sh_bad = 0ull;
         }
@@ -903,7 +873,7 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
 #pragma unroll 1
             for (int32_t b = 0; b < p.blocks; ++b) block(b);
           }
-          if (pair) tc_commit_pair(free0 + 8 * un); else tc_commit(free0 + 8 * un);
+          tc_commit(free0 + 8 * un);
           tc_commit(pv_done + 8 * odd);
           next_unit(&at);
         }
@@ -936,7 +906,7 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
     }
     ShareLevel level = {};
     int32_t shares = 0;
-    const int32_t ctas = static_cast<int32_t>(gridDim.x) / p.cluster, cta = static_cast<int32_t>(blockIdx.x) / p.cluster;
+    const int32_t ctas = static_cast<int32_t>(gridDim.x), cta = static_cast<int32_t>(blockIdx.x);
     if (p.split) {
       level = latent_cut(total, ctas, &shares);
       if (blockIdx.x == 0 && lane == 0u) {
@@ -1005,15 +975,15 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
         s.q0 = seq.q0;
         s.nq = seq.nq;
         s.p_first = seq.len - seq.nq;
-        const int32_t rows = seq.nq * HQ, first = item * NR * p.cluster;
-        s.row0 = min(first + static_cast<int32_t>(rank) * NR, rows - 1);
-        s.nrows = max(min(NR, rows - (first + static_cast<int32_t>(rank) * NR)), 0);
-        s.last = max(s.nrows - 1, 0);
-        s.p_hi = s.p_first + static_cast<int32_t>(a.group.quot(static_cast<uint32_t>(min(rows, first + NR * p.cluster) - 1)));
+        const int32_t rows = seq.nq * HQ, first = item * NR;
+        s.row0 = first;
+        s.nrows = min(NR, rows - first);
+        s.last = s.nrows - 1;
+        s.p_hi = s.p_first + static_cast<int32_t>(a.group.quot(static_cast<uint32_t>(first + s.last)));
         const int32_t tiles = s.p_hi < 0 ? 0 : s.p_hi / kLatKeys + 1;
         s.t0 = p.split ? min(max(s_in - kLatItemSteps, 0), tiles) : 0;
         s.t1 = p.split ? min(max(s_out - kLatItemSteps, 0), tiles) : tiles;
-        s.part = s_out - s_in == unit ? -1 : (2 * share + (s_in == 0 ? 1 : 0)) * p.cluster + static_cast<int32_t>(rank);
+        s.part = s_out - s_in == unit ? -1 : 2 * share + (s_in == 0 ? 1 : 0);
         publish(s);
         // its queries into L2: they are wanted when the item before ends (32 heads over e4m3fn 212 us without, 204 with; with
         // 64 rows an item has many tiles, and the code alone costs what it brings: chunks 930 us without, 1,006 with)
@@ -1079,13 +1049,12 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
           ahead = entries(e0 + 32);
         }
         const bool want = key <= seg.p_hi, have = static_cast<uint32_t>(id) < static_cast<uint32_t>(a.num_pages), live = want && have;
-        if (want && !have && rank == 0u) record_oob(a.err, static_cast<uint64_t>(seg.b));
+        if (want && !have) record_oob(a.err, static_cast<uint64_t>(seg.b));
         const uint32_t bits = __ballot_sync(0xFFFFFFFFu, live);
         const uint32_t off = static_cast<uint32_t>(key) - a.page.quot(static_cast<uint32_t>(key)) * a.page.d;
-        // boxes of `box` groups of eight keys, which share a page; of a pair's CTAs each brings half of the unit
+        // boxes of `box` groups of eight keys, which share a page
         const bool boxes = p.box > 0 && bits == ~0u;
-        const int32_t g0 = pair ? 2 * static_cast<int32_t>(rank) : 0;
-        const int32_t page0 = __shfl_sync(0xFFFFFFFFu, id, 8 * g0), in0 = static_cast<int32_t>(__shfl_sync(0xFFFFFFFFu, off, 8 * g0) >> 3);
+        const int32_t page0 = __shfl_sync(0xFFFFFFFFu, id, 0), in0 = static_cast<int32_t>(__shfl_sync(0xFFFFFFFFu, off, 0) >> 3);
         const uint32_t bar = full_at + 8 * at.unit, part = FMT == KV_CACHE_SRC ? group_bytes : group_bytes / 2u;  // of eight keys
         const uint32_t dst = FMT == KV_CACHE_SRC ? ring + at.unit * unit_bytes : raw_ring + at.unit * raw_bytes;
         // (nothing that can be known before stands between a free unit and its boxes)
@@ -1099,13 +1068,13 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
           if constexpr (FMT == KV_CACHE_SRC) {
             if (waiting > 0u) hand_over(true);
           }
-          if (p.box == (pair ? 2 : 4) && p.box_chunks == p.chunks) {
-            tma_rows(dst + g0 * part, &p.map, bar, 0, in0, page0, pair);
+          if (p.box == 4 && p.box_chunks == p.chunks) {
+            tma_rows(dst, &p.map, bar, 0, in0, page0);
           } else {
-            for (int32_t g = g0; g < (pair ? g0 + 2 : 4); g += p.box) {
+            for (int32_t g = 0; g < 4; g += p.box) {
               const int32_t page = __shfl_sync(0xFFFFFFFFu, id, 8 * g), in_page = static_cast<int32_t>(__shfl_sync(0xFFFFFFFFu, off, 8 * g) >> 3);
               for (int32_t c = 0; c < p.chunks; c += p.box_chunks)
-                tma_rows(dst + g * part + c * (part / static_cast<uint32_t>(p.chunks)), &p.map, bar, 64 * c, in_page, page, pair);
+                tma_rows(dst + g * part + c * (part / static_cast<uint32_t>(p.chunks)), &p.map, bar, 64 * c, in_page, page);
             }
           }
           if (lane == 0u) {
@@ -1226,7 +1195,6 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   }
-  if (pair) sync_pair();  // the other CTA's boxes and arrivals come here
 }
 
 constexpr int kLatJoinWarps = 16;
@@ -1246,7 +1214,7 @@ __global__ void __launch_bounds__(32 * kLatJoinWarps) kv_attend_latent_join(cons
   const int32_t block = static_cast<int32_t>(unit - row_of * p.blocks);
   const int32_t tok = static_cast<int32_t>(row_of / a.q_heads), h = static_cast<int32_t>(row_of - static_cast<int64_t>(tok) * a.q_heads);
   grid_handover();
-  int32_t b = tok, c0 = 0, c1 = 0, r = 0, rank = 0, pos = 0;
+  int32_t b = tok, c0 = 0, c1 = 0, r = 0, pos = 0;
   bool joined = false, lost = false;
   if (tok < a.num_q) {
     if (a.q_start) {
@@ -1260,8 +1228,7 @@ __global__ void __launch_bounds__(32 * kLatJoinWarps) kv_attend_latent_join(cons
     const AttendSeq s = attend_seq(a, b, false);
     if (tok >= s.q0 && tok < s.q0 + s.nq) {
       const LatentGeom geom = latent_geom<NR>(p, s);
-      const int32_t row = (tok - s.q0) * a.q_heads + h, rb = row / (NR * p.cluster);
-      rank = row / NR - rb * p.cluster;
+      const int32_t row = (tok - s.q0) * a.q_heads + h, rb = row / NR;
       r = row % NR;
       pos = s.len - s.nq + (tok - s.q0);
       const int64_t s0 = p.meta[b] + static_cast<int64_t>(rb) * geom.steps;
@@ -1294,7 +1261,7 @@ __global__ void __launch_bounds__(32 * kLatJoinWarps) kv_attend_latent_join(cons
         ml[x] = make_float2(-INFINITY, 0.0f);
         v[x] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (cc <= c1) {
-          const int64_t at = (static_cast<int64_t>(2 * cc + (cc == c0 ? 1 : 0)) * p.cluster + rank) * p.part_rows + r;
+          const int64_t at = static_cast<int64_t>(2 * cc + (cc == c0 ? 1 : 0)) * p.part_rows + r;
           ml[x] = __ldcg(reinterpret_cast<const float2*>(p.part_ml + at * 2));
           v[x] = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * width + 128 * block) + lane);
         }
@@ -1337,32 +1304,6 @@ __global__ void __launch_bounds__(32 * kLatJoinWarps) kv_attend_latent_join(cons
 // Host
 // ---------------------------------------------------------------------------
 
-// Pairs of CTAs of a kernel that can be resident at once, per device.
-inline kv_status pairs_resident(const void* kernel, int threads, int smem, std::atomic<int>* known, int* out) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return cuda_fail(e);
-  std::atomic<int>* at = dev >= 0 && dev < kMaxDevices ? known + dev : nullptr;
-  int n = at ? at->load(std::memory_order_relaxed) : 0;
-  if (n == 0) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2);
-    cfg.blockDim = dim3(static_cast<unsigned>(threads));
-    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
-    if (e != cudaSuccess) return cuda_fail(e);
-    if (at) at->store(n, std::memory_order_relaxed);
-  }
-  *out = n;
-  return KV_OK;
-}
-
 template <int FMT, int NR, bool kBF16>
 kv_status launch_latent_tile(LatentTileParams p, void* work, int64_t work_bytes, int64_t max_keys, cudaStream_t stream) {
   using S = LatentSmem<FMT, NR>;
@@ -1386,22 +1327,11 @@ kv_status launch_latent_tile(LatentTileParams p, void* work, int64_t work_bytes,
     while (p.raws < kLatMaxRaws && S::total(p.chunks, p.units, p.raws + 1) <= kMost) ++p.raws;
   }
   const int smem = S::total(p.chunks, p.units, p.raws);
-  int64_t ctas = sms;  // or pairs
-  if (p.cluster > 1) {
-    static std::atomic<int> known[kMaxDevices];
-    int pairs = 0;
-    st = pairs_resident(reinterpret_cast<const void*>(kernel), kLatThreads<FMT>, kMost, known, &pairs);
-    if (st != KV_OK) return st;
-    ctas = pairs;
-    if (pairs < 1) {
-      p.cluster = 1;
-      ctas = sms;
-    }
-  }
-  const int64_t items = static_cast<int64_t>(a.num_q) * a.group.d / (NR * p.cluster) + a.num_seqs;  // at most
+  const int64_t ctas = sms;
+  const int64_t items = static_cast<int64_t>(a.num_q) * a.group.d / NR + a.num_seqs;  // at most
   const int64_t meta = (static_cast<int64_t>(a.num_seqs) + 31) / 32 * 256;
   p.part_rows = a.q_start || static_cast<int32_t>(a.group.d) > NR ? NR : static_cast<int32_t>(a.group.d);
-  const int64_t slot = static_cast<int64_t>(p.cluster) * p.part_rows * (128 * p.blocks + 2) * 4;
+  const int64_t slot = static_cast<int64_t>(p.part_rows) * (128 * p.blocks + 2) * 4;
   int64_t fit = work && work_bytes > kSplitHead + meta ? (work_bytes - kSplitHead - meta) / (2 * slot) : 0;
   if (fit > ctas) fit = ctas;
   p.split = items < 4 * ctas && max_keys > 8 * kLatKeys && 2 * fit >= ctas;
@@ -1411,26 +1341,10 @@ kv_status launch_latent_tile(LatentTileParams p, void* work, int64_t work_bytes,
     p.head = static_cast<SplitWork*>(work);
     p.meta = reinterpret_cast<int64_t*>(static_cast<uint8_t*>(work) + kSplitHead);
     p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(work) + kSplitHead + meta);
-    p.part_ml = p.part_o + 2 * fit * p.cluster * p.part_rows * 128 * p.blocks;
+    p.part_ml = p.part_o + 2 * fit * p.part_rows * 128 * p.blocks;
   }
-  {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(grid * p.cluster));
-    cfg.blockDim = dim3(kLatThreads<FMT>);
-    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = static_cast<unsigned>(p.cluster);
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = p.cluster > 1 ? 2 : 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
-    if (e != cudaSuccess) return cuda_fail(e);
-  }
-  if (!p.split) return KV_OK;
+  st = launch_chained(kernel, grid, kLatThreads<FMT>, smem, stream, p);
+  if (st != KV_OK || !p.split) return st;
   // the fewer the rows, the more parts has each and the more warps take it
   const int64_t rows = static_cast<int64_t>(a.num_q) * a.q_heads * p.blocks;
   int32_t wpr = 1;
