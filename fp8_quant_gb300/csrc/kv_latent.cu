@@ -89,9 +89,21 @@ __device__ __forceinline__ float2 turn(float a, float b, float c, float s) {
   return make_float2(__fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s)), __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s)));
 }
 
-// The row's factor and scale for codes.
-__device__ __forceinline__ float2 code_factors(float amax) {
-  return amax > 0.0f ? make_float2(__fdiv_rn(448.0f, amax), __fdiv_rn(amax, 448.0f)) : make_float2(1.0f, 1.0f);
+// The row's factor and scale for codes. 448 / amax is beyond fp32 for rows below 2^-119 (and their zeros would become NaN):
+// their elements are first taken `up` by 2^64, which rounds nothing and leaves the codes what they are.
+constexpr float kUp = 0x1p64f;
+struct CodeFactors {
+  float up, factor, scale;
+};
+
+__device__ __forceinline__ CodeFactors code_factors(float amax) {
+  CodeFactors f{1.0f, 1.0f, 1.0f};
+  if (amax > 0.0f) {
+    if (amax < 0x1p-100f) f.up = kUp;
+    f.factor = __fdiv_rn(448.0f, __fmul_rn(amax, f.up));
+    f.scale = __fdiv_rn(amax, 448.0f);
+  }
+  return f;
 }
 
 __device__ __forceinline__ float warp_sum(float x) {
@@ -273,15 +285,25 @@ __global__ void __launch_bounds__(kThreads, 4) kv_latent_rows(const __grid_const
 #pragma unroll
           for (int j = 0; j < 16; ++j) amax = fmaxf(amax, fabsf(y[j]));
         }
-        const float2 f = code_factors(warp_absmax(amax));
+        const CodeFactors f = code_factors(warp_absmax(amax));
+        if (f.up != 1.0f) {  // (the whole warp)
+#pragma unroll
+          for (int i = 0; i < CH; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[i][j] = __fmul_rn(x[i][j], kUp);
+          if (rot) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) y[j] = __fmul_rn(y[j], kUp);
+          }
+        }
 #pragma unroll
         for (int i = 0; i < CH; ++i)
-          if (8u * (lane + 32u * i) < p.latent) *reinterpret_cast<uint2*>(dst + 8u * (lane + 32u * i)) = codes8(x[i], f.x);
+          if (8u * (lane + 32u * i) < p.latent) *reinterpret_cast<uint2*>(dst + 8u * (lane + 32u * i)) = codes8(x[i], f.factor);
         if (rot) {
-          *reinterpret_cast<uint2*>(rdst + piece_a<kInter>(lane, 1)) = codes8(y, f.x);
-          *reinterpret_cast<uint2*>(rdst + piece_b<kInter>(lane, 1, half)) = codes8(y + 8, f.x);
+          *reinterpret_cast<uint2*>(rdst + piece_a<kInter>(lane, 1)) = codes8(y, f.factor);
+          *reinterpret_cast<uint2*>(rdst + piece_b<kInter>(lane, 1, half)) = codes8(y + 8, f.factor);
         }
-        if (lane == 0u) p.scales[at.slot * p.scale_slot] = f.y;
+        if (lane == 0u) p.scales[at.slot * p.scale_slot] = f.scale;
       }
     }
     if (FMT == KV_CACHE_SRC && rot) {
@@ -359,8 +381,8 @@ __global__ void __launch_bounds__(kThreads) kv_latent_any(const __grid_constant_
         amax = fmaxf(amax, fmaxf(fabsf(y.x), fabsf(y.y)));
       }
       for (uint32_t d = p.rotary + lane; d < p.rope; d += 32u) amax = fmaxf(amax, fabsf(widen16(raw(d), p.bf16)));
-      const float2 f = code_factors(warp_absmax(amax));
-      auto code = [&](float x) { return static_cast<uint8_t>(e4m3x2(__fmul_rn(x, f.x), 0.0f)); };
+      const CodeFactors f = code_factors(warp_absmax(amax));
+      auto code = [&](float x) { return static_cast<uint8_t>(e4m3x2(__fmul_rn(__fmul_rn(x, f.up), f.factor), 0.0f)); };
       for (uint32_t d = lane; d < p.latent; d += 32u) dst[d] = code(latent(d));
       dst += p.latent;
       for (uint32_t i = lane; i < half; i += 32u) {
@@ -369,7 +391,7 @@ __global__ void __launch_bounds__(kThreads) kv_latent_any(const __grid_constant_
         dst[d1] = code(y.y);
       }
       for (uint32_t d = p.rotary + lane; d < p.rope; d += 32u) dst[d] = code(widen16(raw(d), p.bf16));
-      if (lane == 0u) p.scales[at.slot * p.scale_slot] = f.y;
+      if (lane == 0u) p.scales[at.slot * p.scale_slot] = f.scale;
     }
   }
 }

@@ -630,8 +630,10 @@ typedef struct kv_latent_strides {
  *   KV_CACHE_SRC     every element of [n | r'] rounded once to the source type
  *                    (elements that neither step touches keep their bytes);
  *   KV_CACHE_E4M3FN  m = max |[n | r']| (NaN ignored), scale = fl(m / 448),
- *                    codes e4m3fn(fl(x * fl(448 / m))), saturating; scale and
- *                    factor are 1 where m is 0.
+ *                    codes e4m3fn(fl(x * fl(448 / m))), saturating, where the
+ *                    factor may pass fp32's largest number (rows of m below
+ *                    2^-119 have the codes of rows 2^64 times as large, and
+ *                    subnormal scales); scale and factor are 1 where m is 0.
  * All in fp32; the mean is a sum of fp32 squares (its relative error is below
  * 2^-18 for up to 1,024 dims).
  * rope->q (optional): rotary dims of the queries, [num_tokens, num_q_heads,
