@@ -157,6 +157,14 @@ __device__ __forceinline__ ShareLevel latent_cut(int64_t total, int32_t ctas, in
   return ShareLevel{0, static_cast<int32_t>(each), 0};
 }
 
+// The bits of a warp's own keys, kCols of a unit's 32.
+template <int kCols>
+__host__ __device__ constexpr uint32_t own_keys(uint32_t valid, uint32_t half) {
+  return valid >> (kCols * half) & (~0u >> (32 - kCols));
+}
+static_assert(own_keys<32>(~0u, 0) == ~0u && own_keys<16>(~0u, 0) == 0xFFFFu && own_keys<16>(~0u, 1) == 0xFFFFu &&
+                  own_keys<16>(0xABCD1234u, 0) == 0x1234u && own_keys<16>(0xABCD1234u, 1) == 0xABCDu, "the warp's own, and no others");
+
 // 16 lanes x 32 (or 16) columns over the warp: thread (g, t) = (lane / 4, lane % 4) gets columns 8 i + 2 t, + 1 of
 // rows g (r[4 i], r[4 i + 1]) and g + 8 (r[4 i + 2], r[4 i + 3]).
 __device__ __forceinline__ void tc_ld_rows(float (&s)[16], uint32_t addr) {
@@ -486,7 +494,7 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
 #pragma unroll
         for (int x = 0; x < N; ++x) {
           ok = bar_wait(full + 8 * at.unit, at.phase, state) && ok;
-          valid[x] = sh_valid[at.unit] >> (kCols * half);
+          valid[x] = own_keys<kCols>(sh_valid[at.unit], half);
           if constexpr (FMT != KV_CACHE_SRC) {
 #pragma unroll
             for (int i = 0; i < kCols / 8; ++i) {
