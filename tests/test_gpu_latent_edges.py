@@ -1,10 +1,10 @@
-"""The cache of latent rows at the ends of the number range."""
+"""The cache of latent rows at the ends of the number range, and what a query makes of an infinite row that it sees."""
 
 import numpy as np
 import pytest
 
 from attncheck import E4M3_ALL, bits_to_f32, e4m3_codes
-from latentcheck import StoreProblem, to_bits
+from latentcheck import LatentProblem, StoreProblem, to_bits
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -111,3 +111,41 @@ def test_attention_over_rows_of_tiny_values():
     assert np.isfinite(want).all() and np.isfinite(got).all()
     # the output's rounding, the weights', and the scores' (fp32 sums of 320 products, queries at 2^-25 of their largest)
     assert (np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -7 * np.abs(rows).max()).all()
+
+
+@pytest.mark.parametrize("fmt,what", [(None, np.inf), (None, -np.inf), ("e4m3fn", np.inf)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("batch", [([90, 4, 333, 64], [4, 4, 2, 3]), ([300, 129, 1000], [65, 128, 311]), ([1, 40, 700], [1, 1, 1])])
+def test_what_an_infinite_row_gives(batch, dtype, fmt, what):
+    """An infinite value (or scale) at each sequence's last key. Its last query has a score of infinity, and is NaN throughout, or of
+    minus infinity, and then a weight of 0, which times the infinite value is NaN in that dim and nothing in the others; earlier
+    queries do not see it."""
+    lens, nqs = batch
+    p = LatentProblem(lens, nqs, 4, 256, 64, dtype=dtype, fmt=fmt, seed=64)
+    for b, n in enumerate(lens):
+        at = p.table[b, (n - 1) // p.page], (n - 1) % p.page
+        if fmt is None:
+            p.cache[at][3] = ((0x7F80 if dtype == "bf16" else 0x7C00) | (0x8000 if what < 0 else 0))
+            p.value[at][3] = what
+        else:
+            p.scales[at] = what
+            with np.errstate(invalid="ignore"):
+                p.value[at] = E4M3_ALL[p.cache[at]] * what
+    d = p.tensors("cuda")
+    lse = torch.zeros((sum(nqs), 4), device="cuda")
+    out = p.attend(d, lse=lse)
+    got = out.float().cpu().numpy()
+    last = p.q_start[1:] - 1
+    rest = np.setdiff1d(np.arange(sum(nqs)), last)
+    assert np.isfinite(got[rest]).all()
+    if fmt is None:
+        assert np.isnan(got[last][..., 3]).all()
+        q3 = bits_to_f32(p.q, dtype)[last][..., 3] * what
+        alone = np.array(lens) == 1      # nothing but a score of -infinity: 0 / 0
+        whole = (q3 > 0) | alone[:, None]
+        assert np.isnan(got[last])[whole].all()
+        assert (np.isnan(got[last])[~whole].sum(-1) == 1).all()
+    else:
+        assert np.isnan(got[last]).all()
+    if 1 not in lens:
+        p.check(out, lse)
