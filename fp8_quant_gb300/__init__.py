@@ -1293,7 +1293,9 @@ def kv_attend_latent(q, cache, page_table, seq_lens, *, latent_dim: int, q_start
     Every head reads the same rows, whose first ``latent_dim`` dims are the values. ``cache``, ``fmt``
     and ``scales`` as in :func:`kv_store_latent` (``page_size`` is needed with a [slots, 1, D] cache);
     ``page_table``, ``seq_lens``, ``q_start``, ``lse``, ``work`` and ``err`` as in :func:`kv_attend`.
-    ``sm_scale``: of the scores (1 / sqrt(D) if None).
+    ``sm_scale``: of the scores. Queries into which the keys' up-projection was multiplied still have their
+    own head's products as scores: give 1 / sqrt(the dims, rotary ones included, of that head's queries and keys
+    before it, 192 for 128 + 64). None is 1 / sqrt(D), which is right only where a head's queries are D dims of its own.
     """
     import torch
     dtype = q.dtype

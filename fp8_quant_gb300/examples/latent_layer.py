@@ -5,7 +5,8 @@ generates tokens with the whole step (append, attention, the lengths) in one CUD
 time and how far the last outputs are from the attention of the unquantised rows in 64 bits.
 
 A token's projections give its latent and rotary dims, [L + R], and its queries [HQ, L + R], the first L of which
-already carry the keys' up-projection; the outputs [HQ, L] go to the values' up-projection.
+already carry the keys' up-projection; the outputs [HQ, L] go to the values' up-projection. The scores are those of the
+heads as they were before that, of `head_dim` dims, and so is their scale.
 """
 
 from __future__ import annotations
@@ -22,15 +23,16 @@ EPS = 1e-6
 
 
 class LatentLayer:
-    """The cache of one layer and its two passes. ``fmt`` as in :func:`kv.kv_store_latent`.
+    """The cache of one layer and its two passes. ``fmt`` as in :func:`kv.kv_store_latent`. ``head_dim``: dims of a head's
+    queries and keys before the keys' up-projection went into the queries, rotary ones included.
 
     One stream at a time: the workspace and the error record belong to the layer.
     """
 
-    def __init__(self, heads, latent, rotary, *, pages, page_size, max_position, weight=None, fmt=None, dtype=torch.bfloat16,
-                 sm_scale=None, device="cuda"):
+    def __init__(self, heads, latent, rotary, *, head_dim, pages, page_size, max_position, weight=None, fmt=None,
+                 dtype=torch.bfloat16, device="cuda"):
         self.HQ, self.L, self.R, self.page_size, self.fmt, self.dtype = heads, latent, rotary, page_size, fmt, dtype
-        self.weight, self.sm_scale = weight, 1.0 / math.sqrt(latent + rotary) if sm_scale is None else sm_scale
+        self.weight, self.sm_scale = weight, 1.0 / math.sqrt(head_dim)
         device = torch.device(device, torch.cuda.current_device())
         self.cache = torch.zeros((pages, page_size, 1, latent + rotary), dtype=torch.uint8 if fmt else dtype, device=device)
         self.scales = torch.zeros((pages * page_size, 1), device=device) if fmt else None
@@ -126,15 +128,15 @@ def plain_attention(layer, inputs):
     return (q @ keys.T * layer.sm_scale).softmax(-1) @ keys[:, :L]
 
 
-def generate(prompts=(1, 77, 300, 1023), steps=8, heads=32, latent=512, rotary=64, page_size=16, fmt=None, dtype=torch.bfloat16,
-             graph=True, seed=1):
+def generate(prompts=(1, 77, 300, 1023), steps=8, heads=32, latent=512, rotary=64, head_dim=128 + 64, page_size=16, fmt=None,
+             dtype=torch.bfloat16, graph=True, seed=1):
     """Prompts, then `steps` tokens each. Returns the layer, all outputs and the inputs per sequence. The projections'
     outputs are random, so the steps do not depend on one another's results."""
     g = torch.Generator(device="cuda").manual_seed(seed)
     ends = [n + steps for n in prompts]
     weight = (1 + 0.2 * torch.randn(latent, generator=g, device="cuda")).to(dtype)
-    layer = LatentLayer(heads, latent, rotary, pages=sum(-(-n // page_size) for n in ends) + 1, page_size=page_size,
-                        max_position=max(ends), weight=weight, fmt=fmt, dtype=dtype)
+    layer = LatentLayer(heads, latent, rotary, head_dim=head_dim, pages=sum(-(-n // page_size) for n in ends) + 1,
+                        page_size=page_size, max_position=max(ends), weight=weight, fmt=fmt, dtype=dtype)
     D = latent + rotary
     inputs = [(torch.randn(n, D, generator=g, device="cuda").to(dtype), torch.randn(n, heads, D, generator=g, device="cuda").to(dtype))
               for n in ends]

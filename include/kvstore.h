@@ -702,6 +702,9 @@ typedef struct kv_attend_latent_strides {
  *                up to 576) and 8 (latent_dim, up to 512) with 16-byte aligned
  *                bases and strides take the tensor-core kernel; the rest a general one.
  *   format       KV_CACHE_SRC or KV_CACHE_E4M3FN (with scales).
+ *   sm_scale     of the scores.  Where the keys' up-projection was multiplied into the
+ *                queries, the scores are still the products of the head before that: the
+ *                scale is 1 / sqrt(its dims, rotary ones included), not 1 / sqrt(row_dim).
  *   work         as in kv_attend (KV_ATTEND_WORK_BYTES is always enough).
  * Page tables, lengths, q_start, waits, errors, determinism and the workspace's
  * head are as in kv_attend.
