@@ -993,9 +993,9 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
         s.t1 = p.split ? min(max(s_out - kLatItemSteps, 0), tiles) : tiles;
         s.part = s_out - s_in == unit ? -1 : 2 * share + (s_in == 0 ? 1 : 0);
         publish(s);
-        // its queries into L2: they are wanted when the item before ends (32 heads over e4m3fn 212 us without, 204 with; with
-        // 64 rows an item has many tiles, and the code alone costs what it brings: chunks 930 us without, 1,006 with)
-        if (NR == 32 && s.t1 > s.t0) {
+        // its queries into L2: they are wanted when the item before ends (32 heads, one token 138.8 us without, 136.5 with; over
+        // e4m3fn 157.5 and 154.3; chunks 925 and 927, but 966 where the compiler leaves it out of the 64-row form)
+        if (s.t1 > s.t0) {
           const int32_t lines = (a.head_dim * 2 + 127) / 128;
           for (int32_t i = static_cast<int32_t>(lane); i < s.nrows * lines; i += 32) {
             const int32_t r = i / lines, qi = static_cast<int32_t>(a.group.quot(static_cast<uint32_t>(s.row0 + r)));
