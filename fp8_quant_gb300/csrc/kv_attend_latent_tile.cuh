@@ -18,29 +18,30 @@
 //   warps 0-3  the softmax: S by 16x256b loads (a thread has 8 keys of two rows),
 //              running maximum and sums in registers, P to shared memory. A tile's scores are only compared with the
 //              running maxima; these, and O^T, are brought up to date when some row's grew by 2^8 or more (the reduction
-//              over a row's threads in every tile: 32 heads over e4m3fn 188 us, 172 without). With 32 rows the 64 of a
+//              over a row's threads in every tile: 32 heads over e4m3fn 172 us, 154 without). With 32 rows the 64 of a
 //              product hold them twice, and warps 2 and 3 take half of the keys. They also bring the queries in and
 //              write the outputs.
 //   warps 4, 8 issue the products S, of every other tile each, up to three tiles ahead of
-//   warp  5    P V. (A product takes 31 clocks to issue and 25 to 48 to run: with one warp for all of them decode below
-//              took 223 us, with one for S 151.)
+//   warp  5    P V. (A product takes 31 clocks to issue and 25 to 48 to run: with one warp for S decode below takes
+//              152 us, where two take 137; over e4m3fn 209 and 154; chunks 1,229 and 927.)
 //   warp  6    cuts the work: finds the CTA's next items and hands them to the others.
 //   warp  7    brings the keys, a tile a unit of the ring: by TMA, a box for all of it where its 32 keys exist and share a
 //              page, else by cp.async. e4m3fn rows come as they are, into a ring of their own, and become fp16 (exact) by
 //   warps 9-15 on their way into the ring of units.
 //   A unit lies as [8 keys][64 dims][key][128 bytes in the 128-byte swizzle], as a box of the cache's eights of keys does.
 //   It is given back when P V has gone over it. Tiles are small because that time is what the
-//   ring has to cover beside the memory's latency: tiles of 64 keys held it twice as long (171 us where 32 took 151), and
-//   so did products S over two tiles at once, which run 36 % faster a key (chunks 1,113 us, 939 without).
+//   ring has to cover beside the memory's latency: tiles of 64 keys hold it twice as long (decode 13 % slower when both
+//   forms were there), and so do products S over two tiles at once, which run 36 % faster a key (chunks 19 % slower).
 //
-// Measured (one GB300): 64 sequences of 4,000 - 16,384 bf16 keys, 32 heads, one token each (decode) 137 us, 82 % of the
-// copy rate for its bytes; chunks of 700 - 1,023 tokens over 5,000 - 8,190 keys 912 us, 848 TFLOP/s: the products' own
-// time, 36 x 25 + 8 x 48 clocks a tile, is 84 % of it; 32 sequences of 16,000 - 32,768 e4m3fn keys 160 us: products and
-// conversions share the 128 bytes a clock of shared memory (S 288, P V 320, conversions 576 of 1,790 clocks a tile).
+// Measured (one GB300): 64 sequences of 4,000 - 16,384 bf16 keys, 32 heads, one token each (decode) 136 us, 83 % of the
+// copy rate for its bytes; chunks of 700 - 1,023 tokens over 5,000 - 8,190 keys 915 - 927 us, 846 - 834 TFLOP/s: the products' own
+// time, 36 x 25 + 8 x 48 clocks a tile, is 83 % of it; 32 sequences of 16,000 - 32,768 e4m3fn keys 154 us: products and
+// conversions share the 128 bytes a clock of shared memory (S 288, P V 320, conversions 576 of 1,730 clocks a tile).
 //
 // Rows beyond NR (more queries, more heads) are further items, which read the same keys: mostly from L2.
 //
-// Weights are rounded once to 16 bits, as the product's operand; their sums are
+// Weights are rounded once to 16 bits, as the product's operand (a second term, as kv_attend's split kernels keep for 16-bit
+// caches, would be P V a second time; up to 2^-9 or 2^-12 of sum p |k| / sum p, as the header says); their sums are
 // of the unrounded ones in fp32. An e4m3fn row's scale f multiplies its scores,
 // and its weights p before they are rounded: the running reference is the
 // maximum of score + log2 f, so that p f, not p, begins at 2^7.
@@ -65,8 +66,8 @@ constexpr int kLatMaxUnits = 8, kLatMaxRaws = 8;
 constexpr int kLatScores = 3;       // tiles whose scores may be in TMEM
 constexpr int kLatMinSteps = 2;     // steps of a share at least
 // Steps that an item counts beside its tiles where items are split: what its queries, first scores and outputs take. (24 heads,
-// 200 - 777 tokens over e4m3fn keys 514 us with none, 501 with 4, 475 with 8 and with 12; 32 heads, one token 166, 164, 161, 159;
-// over 16-bit keys no difference.)
+// 200 - 777 tokens over e4m3fn keys 469 us with none, 453 with 4, 435 with 8, 433 with 12; 32 heads, one token 158, 156.5, 154,
+// 152; over 16-bit keys 140, 137.5, 136.5, 135.5.)
 constexpr int kLatItemSteps = 8;
 
 struct LatentTileParams {
@@ -373,8 +374,8 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
     };
     uint32_t items = 0u;  // that have tiles
     auto load_q = [&](const LatentSeg& s) {
-      // chunks in TMEM; chunks in flight (decode 150 us with one, 143 with three, 147 with nine; over e4m3fn 194 with one, 204
-      // with three)
+      // chunks in TMEM; chunks in flight (decode 145 us with one, 136.5 with three, 142.5 with nine; over e4m3fn 154 with one
+      // or three)
       constexpr int kIn = S::kInTmem, kAt = FMT == KV_CACHE_SRC && NR == 32 ? 3 : 1;
       const bool shift = FMT != KV_CACHE_SRC && a.bf16;
       auto shifted = [](uint32_t z, float f) {
@@ -441,7 +442,7 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
       if (kIn < kLatMaxChunks && p.chunks > kIn) {  // the last chunks to shared memory: a warp has NR / 4 rows, 16 bytes a lane
         constexpr int kRows = NR / 4;
         if (shift) sync_softmax();  // sh_qf
-        const uint32_t rest = static_cast<uint32_t>(a.head_dim) / 8u - 8u * kIn;  // pieces, at most 24
+        const uint32_t rest = static_cast<uint32_t>(a.head_dim) / 8u - 8u * kIn;  // pieces, at most 32
         uint4 w[kRows];
 #pragma unroll
         for (int y = 0; y < kRows; ++y) {
@@ -643,9 +644,9 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
         return true;
       };
       // Where the products are the longer two tiles go together, as what a step costs whatever its keys is a third of it: 64
-      // rows over e4m3fn keys (24 heads, 200 - 777 tokens 651 us, 780 with one), or of sequences with so many rows that a
-      // unit serves several CTAs (chunks 929 and 1,013 us). Else a tile does not wait for the next: 48 heads, 2 - 5 tokens
-      // 190 us with two and 167 with one, 32 heads, one token over e4m3fn 243 and 187.
+      // rows over e4m3fn keys (24 heads, 200 - 777 tokens 435 us, 500 with one; but 48 heads, 2 - 5 tokens 236 and 187), or of
+      // sequences with so many rows that their keys come from L2 (chunks 927 and 964 us). Else a tile does not wait for the
+      // next: 48 heads, 2 - 5 tokens over 16-bit keys 164 us with two and 153 with one, 128 heads, one token 98 and 92.
       bool left = false;
       for (int32_t j = seg.t0; j < seg.t1 && !left;) {
         if (NR == 64 && (FMT != KV_CACHE_SRC || seg.nq * HQ > 4 * NR) && j + 1 < seg.t1) {
@@ -847,7 +848,7 @@ __global__ void __launch_bounds__(kLatThreads<FMT>, 1) kv_attend_latent_tile(con
                   break;
                 }
               }
-            } else {  // loops: beside the converters' code straight lines do not stay in the instruction cache (638 us, 521)
+            } else {  // loops: beside the converters' code straight lines do not stay in the instruction cache (chunks 516 us, 435 with loops)
               const int32_t whole = p.ksteps >> 2, ts = min(whole, S::kInTmem);
 #pragma unroll 1
               for (int32_t c = 0; c < ts; ++c) tc_mma_chunk_ts(d, q_col + 32 * c, kd + c * (1024 >> 4), kDesc, c > 0);

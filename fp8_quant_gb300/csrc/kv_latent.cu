@@ -14,10 +14,14 @@
 //                    pieces of 8 dims.  Further warps take the queries' items, up to
 //                    four passes' loads in flight, their eight cosines and
 //                    sines loaded once.  No row load waits for the slot or the position.
-//                    At most 64 registers: a prefill of 32,768 fp16 rows of 512 + 64 dims with
-//                    32 heads' queries 71 us (5.0 TB/s, 74 % of the copy rate; 80 us with 93
-//                    registers, 89 with 51, which spill).  Pieces of 128 bytes in rows of
-//                    1,152 and the loads' latency bound it.
+//                    At most 64 registers, so that an SM has four CTAs, although the forms
+//                    with four passes, and those of more than 512 latent dims, then spill
+//                    (172 bytes stored and 152 loaded in the one measured here): a prefill of
+//                    32,768 fp16 rows of 512 + 64 dims with 32 heads' queries 71 us (5.0
+//                    TB/s, 74 % of the copy rate), 74 with 80 registers and 40 bytes
+//                    spilled, 89 with 98 and none, 90 with 48; into an e4m3fn cache 73, 75,
+//                    79 and 91.  Pieces of 128 bytes in rows of 1,152, the loads' latency
+//                    and the spills bound it.
 //  * kv_latent_any   any layout: a warp per (token, row or query head), elements
 //                    one by one, the row gone through once for each sum it needs.
 //  * kv_latent_gather  an item is 32 or 16 bytes of a 16-bit row, or 16 codes; a
