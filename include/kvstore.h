@@ -700,7 +700,8 @@ typedef struct kv_attend_latent_strides {
  *   out          [num_q_tokens, num_q_heads, latent_dim]; must not overlap q or the cache.
  *   row_dim      1 .. 1024; latent_dim 1 .. row_dim.  Multiples of 16 (row_dim,
  *                up to 576) and 8 (latent_dim, up to 512) with 16-byte aligned
- *                bases and strides take the tensor-core kernel; the rest a general one.
+ *                bases and strides, and page and slot strides below 2^31 bytes, take
+ *                the tensor-core kernel; the rest a general one.
  *   format       KV_CACHE_SRC or KV_CACHE_E4M3FN (with scales).
  *   sm_scale     of the scores.  Where the keys' up-projection was multiplied into the
  *                queries, the scores are still the products of the head before that: the
